@@ -23,6 +23,12 @@
  *                           tq4_decompress).
  *   tq_write_kv_prod,       product-quantised ("QJL residual") key rows and the decode
  *   tq_paged_decode_prod    over them ("vLLM Reference Audit", MSE and QJL codecs).
+ *   tq_plan_step            a step's block tables, slot map and row list from request
+ *                           lengths, on the device ("vLLM Usage", Slot Mapping).
+ *   tq_paged_tree           attention of drafted tokens (a tree per sequence) over the pages;
+ *   tq_commit_tree          the accepted ones' rows moved behind their context.
+ *   tq_paged_prefill_biased prefill / decode with capped scores, a distance bias, a sliding
+ *                           window, a bidirectional prefix, packed documents.
  *   tq_write_kv_recipe,     the recipe cache modes turboquant25 / turboquant35: grouped
  *   tq_paged_decode_recipe  product-quantised K and V rows ("vLLM Usage", Cache Dtypes;
  *                           "Architecture", vLLM Runtime Mapping), with the metadata
@@ -68,9 +74,10 @@ typedef enum tq_status {
   TQ_ERR_SLOT_OUT_OF_RANGE = 3,  /* a write slot >= num_blocks * block_size */
   TQ_ERR_BLOCK_OUT_OF_RANGE = 4, /* a block-table entry read by decode lies outside [0, num_blocks) */
   TQ_ERR_CUDA = 5,               /* a CUDA runtime call failed (message in tq_last_error) */
-  TQ_ERR_TIMEOUT = 6             /* a device-side wait gave up after its iteration limit; the
+  TQ_ERR_TIMEOUT = 6,            /* a device-side wait gave up after its iteration limit; the
                                     output of that call is incomplete (an internal error: no
                                     valid input produces it) */
+  TQ_ERR_OUT_OF_BLOCKS = 7       /* tq_plan_step: the step needs more blocks than are free */
 } tq_status;
 
 typedef enum tq_dtype { TQ_F32 = 0, TQ_F16 = 1, TQ_BF16 = 2 } tq_dtype;
@@ -436,6 +443,131 @@ tq_status tq_paged_decode_recipe(const void* q, tq_dtype q_dtype, int batch, int
                                  const float* mse_high, const float* mse_low, const float* qjl_matrix, float scale,
                                  void* out, tq_dtype out_dtype, void* workspace, size_t workspace_bytes,
                                  int32_t* status_dev, void* stream);
+
+/* ------------------------------------------------------- steps of a serving engine
+ *
+ * The pages fix how a token is addressed ("vLLM Usage", Slot Mapping; "Architecture",
+ * PackedPageCache) and leave who fills the tables to the host framework.  The calls below do
+ * it on the device, for an engine that drafts several tokens a step: tq_plan_step lays out a
+ * step's rows, tq_write_kv (or _prod, _recipe) writes them, tq_paged_tree verifies drafted
+ * tokens, tq_commit_tree keeps the accepted ones. */
+
+/* Plans one step: appends new_lens[s] tokens to every sequence, taking new blocks from a ring
+ * of free ones, and returns the blocks of finished sequences to it.
+ *
+ *   seq_lens     device int32[num_seqs], tokens already cached.
+ *   new_lens     device int32[num_seqs], tokens this step adds (0 allowed); negative: the
+ *                sequence is finished, its blocks go back to the ring and its length to 0.
+ *   seq_blocks   device int32[num_seqs], table entries in use (may exceed
+ *                ceil(seq_lens / block_size): blocks reserved by an earlier step).
+ *   block_table  device int32[num_seqs][max_blocks_per_seq]; new entries are written, the
+ *                others stay.
+ *   free_blocks  device int32[num_blocks], a ring of free block ids: free_state = {head,
+ *                count}, entry i of the queue at (head + i) % num_blocks.  New blocks come
+ *                from the head in sequence order; returned blocks go to the tail in sequence
+ *                and table order (free for the next step, not for this one).
+ *   max_rows     rows of the outputs; rows behind the last one get slot -1 (tq_write_kv
+ *                skips it), q_seq -1 (a padding row of tq_paged_tree and
+ *                tq_paged_prefill_biased) and q_len 0.
+ *   slots        device int64[max_rows], flat slot of every new token, sequence by sequence.
+ *   q_seq, q_len device int32[max_rows], the row's sequence and its position + 1.
+ *   row_start    device int32[num_seqs + 1], first row of every sequence, then the total.
+ *   seq_lens_out, seq_blocks_out, free_state_out  the state after the step; each may be the
+ *                input itself.  No other two buffers may overlap.
+ *   status_dev   device int32 or NULL: 0; TQ_ERR_OUT_OF_BLOCKS when the ring holds too few
+ *                blocks; TQ_ERR_INVALID_ARG when a length is negative or beyond its blocks, a
+ *                sequence would pass max_blocks_per_seq, the rows pass max_rows, or free_state
+ *                is inconsistent.  In these cases nothing is planned: the state comes out as it
+ *                was, every row is a padding row.  TQ_ERR_BLOCK_OUT_OF_RANGE when a block id
+ *                taken from the table or the ring lies outside [0, num_blocks): that token's
+ *                slot is -1.
+ *
+ * One launch, graph-capturable.  Host-detected errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_plan_step(const int32_t* seq_lens, const int32_t* new_lens, const int32_t* seq_blocks, int num_seqs,
+                       int32_t* block_table, int max_blocks_per_seq, int32_t* free_blocks, const int32_t* free_state,
+                       int64_t num_blocks, int block_size, int64_t max_rows, int64_t* slots, int32_t* q_seq,
+                       int32_t* q_len, int32_t* row_start, int32_t* seq_lens_out, int32_t* seq_blocks_out,
+                       int32_t* free_state_out, int32_t* status_dev, void* stream);
+
+/* Keeps the accepted tokens of a verified tree: for every sequence s and j < path_lens[s], the
+ * K and V rows (all heads) of token ctx_lens[s] + path[s][j] move to token ctx_lens[s] + j, and
+ * seq_lens_out[s] = ctx_lens[s] + path_lens[s].  Rows are moved as bytes, so the pages may hold
+ * MSE, product-quantised or recipe rows.
+ *
+ *   k_pages, v_pages  device, uint8[num_blocks][block_size][num_kv_heads][row_bytes], 16-byte
+ *                     aligned; either may be NULL.
+ *   path              device int32[num_seqs][max_path]: accepted nodes, strictly ascending in
+ *                     the first path_lens[s] entries.
+ *   seq_lens_out      device int32[num_seqs]; may be ctx_lens.
+ *   status_dev        device int32 or NULL: 0; TQ_ERR_INVALID_ARG for a sequence whose path is
+ *                     not ascending, or whose lengths leave the table or max_path (nothing of
+ *                     it moves, its length stays ctx_lens[s]); TQ_ERR_BLOCK_OUT_OF_RANGE for a
+ *                     block id outside [0, num_blocks) (that row does not move).
+ *
+ * Two sequences must not share a block that a moved row lies in.  Asynchronous,
+ * graph-capturable; host-detected errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (a token's
+ * rows above 16 MiB), TQ_ERR_CUDA. */
+tq_status tq_commit_tree(uint8_t* k_pages, int64_t k_row_bytes, uint8_t* v_pages, int64_t v_row_bytes,
+                         int64_t num_blocks, int block_size, int num_kv_heads, const int32_t* block_table,
+                         int num_seqs, int max_blocks_per_seq, const int32_t* ctx_lens, const int32_t* path,
+                         const int32_t* path_lens, int max_path, int32_t* seq_lens_out, int32_t* status_dev,
+                         void* stream);
+
+/* Workspace bytes of tq_paged_tree and of tq_paged_prefill_biased on the current device, for
+ * any table, widths and dtypes; 0 when the arguments are invalid. */
+size_t tq_paged_tree_workspace(int num_q_rows, int num_q_heads, int num_kv_heads, int head_dim);
+
+/* Attention of drafted tokens over the packed cache.  The cache holds each sequence's context
+ * (ctx_lens[s] tokens) and, at the tokens behind it, its drafted tokens (written by
+ * tq_write_kv): node j at token ctx_lens[s] + j.  Query row i belongs to sequence q_seq[i] and
+ * sees the whole context and every node j whose bit is set in its mask: bit j % 32 of
+ * tree_mask[i][j / 32] (for a tree: its ancestors and itself; any set of bits is allowed).
+ *
+ *   q          device, q_dtype[num_q_rows][num_q_heads][head_dim]
+ *   q_seq      device int32[num_q_rows]; -1: a padding row (its output is zero)
+ *   ctx_lens   device int32[num_seqs]
+ *   tree_mask  device uint32[num_q_rows][mask_words], mask_words 1 .. 1024
+ *   softcap    0, or c > 0: scores s become c tanh(s / c) before the softmax
+ *   workspace  device, >= tq_paged_tree_workspace(...) bytes, 256-byte aligned
+ *   status_dev device int32 or NULL: TQ_ERR_INVALID_ARG when a q_seq lies outside
+ *              [-1, num_seqs) (zero row), or a context or node lies beyond the table row
+ *              (clamped); TQ_ERR_BLOCK_OUT_OF_RANGE when a block id read lies outside
+ *              [0, num_blocks) (its tokens are left out).
+ * A row that sees nothing is zero.  Rows of one sequence should be neighbours: they share
+ * every dequantised tile.  The other arguments are tq_paged_prefill's.  fp32 outputs are
+ * computed in fp32 throughout; fp16 and bf16 outputs from fp16 products with fp32 sums.
+ * Asynchronous, graph-capturable (one workspace per call in flight); host-detected errors:
+ * TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA. */
+tq_status tq_paged_tree(const void* q, tq_dtype q_dtype, int num_q_rows, int num_q_heads, int num_kv_heads,
+                        int head_dim, const uint8_t* k_pages, int k_bits, const uint8_t* v_pages, int v_bits,
+                        int64_t num_blocks, int block_size, const int32_t* block_table, int num_seqs,
+                        int max_blocks_per_seq, const int32_t* q_seq, const int32_t* ctx_lens,
+                        const uint32_t* tree_mask, int mask_words, const float* signs, const float* k_centroids,
+                        const float* v_centroids, float scale, float softcap, void* out, tq_dtype out_dtype,
+                        void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/* Mixed prefill / decode with modified scores and visible sets: tq_paged_prefill's rows (row i
+ * at position q_len[i] - 1 of sequence q_seq[i]; -1: padding, zero output), with
+ *   x_t = f(scale <q, k_t>) - slope |q_len[i] - 1 - t|,  f(s) = softcap tanh(s / softcap)
+ * over the tokens t >= doc_starts[i] with t < prefix_lens[s] or q_len[i] - window <= t < q_len[i].
+ *
+ *   prefix_lens   device int32[num_seqs] or NULL: tokens every row of the sequence sees, also
+ *                 those behind its own position and outside its window
+ *   doc_starts    device int32[num_q_rows] or NULL: first token of the row's document
+ *   window        0: none
+ *   alibi_slopes  device float[num_q_heads] or NULL
+ *   softcap       0: none
+ * Workspace, status word (also TQ_ERR_INVALID_ARG for a q_len or prefix_lens beyond the table
+ * row, clamped) and errors as tq_paged_tree; tiles that no row sees are not read.  A row whose
+ * set is empty is zero.  Without modifiers the result is tq_paged_prefill's. */
+tq_status tq_paged_prefill_biased(const void* q, tq_dtype q_dtype, int num_q_rows, int num_q_heads, int num_kv_heads,
+                                  int head_dim, const uint8_t* k_pages, int k_bits, const uint8_t* v_pages, int v_bits,
+                                  int64_t num_blocks, int block_size, const int32_t* block_table, int num_seqs,
+                                  int max_blocks_per_seq, const int32_t* q_seq, const int32_t* q_len,
+                                  const int32_t* prefix_lens, const int32_t* doc_starts, int window,
+                                  const float* alibi_slopes, const float* signs, const float* k_centroids,
+                                  const float* v_centroids, float scale, float softcap, void* out, tq_dtype out_dtype,
+                                  void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream);
 
 #ifdef __cplusplus
 }

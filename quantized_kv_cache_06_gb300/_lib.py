@@ -7,9 +7,11 @@ functions raise: there is no fallback path.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -22,6 +24,7 @@ TQ_ERR_SLOT_OUT_OF_RANGE = 3
 TQ_ERR_BLOCK_OUT_OF_RANGE = 4
 TQ_ERR_CUDA = 5
 TQ_ERR_TIMEOUT = 6
+TQ_ERR_OUT_OF_BLOCKS = 7
 
 STATUS_NAMES = {
     TQ_OK: "TQ_OK",
@@ -31,6 +34,7 @@ STATUS_NAMES = {
     TQ_ERR_BLOCK_OUT_OF_RANGE: "TQ_ERR_BLOCK_OUT_OF_RANGE",
     TQ_ERR_CUDA: "TQ_ERR_CUDA",
     TQ_ERR_TIMEOUT: "TQ_ERR_TIMEOUT",
+    TQ_ERR_OUT_OF_BLOCKS: "TQ_ERR_OUT_OF_BLOCKS",
 }
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -87,6 +91,17 @@ SIGNATURES = {
     "tq_paged_decode_recipe": (_c_int, [_c_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_p, _c_p, _c_int, _c_i64,
                                         _c_int, _c_p, _c_int, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_f, _c_p, _c_int,
                                         _c_p, _c_sz, _c_p, _c_p]),
+    "tq_plan_step": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_p, _c_int, _c_p, _c_p, _c_i64, _c_int, _c_i64, _c_p, _c_p,
+                              _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "tq_commit_tree": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_int, _c_int, _c_p, _c_int, _c_int, _c_p, _c_p,
+                                _c_p, _c_int, _c_p, _c_p, _c_p]),
+    "tq_paged_tree_workspace": (_c_sz, [_c_int, _c_int, _c_int, _c_int]),
+    "tq_paged_tree": (_c_int, [_c_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_p, _c_int, _c_p, _c_int, _c_i64,
+                               _c_int, _c_p, _c_int, _c_int, _c_p, _c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_f, _c_f,
+                               _c_p, _c_int, _c_p, _c_sz, _c_p, _c_p]),
+    "tq_paged_prefill_biased": (_c_int, [_c_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_p, _c_int, _c_p, _c_int,
+                                         _c_i64, _c_int, _c_p, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p, _c_int, _c_p,
+                                         _c_p, _c_p, _c_p, _c_f, _c_f, _c_p, _c_int, _c_p, _c_sz, _c_p, _c_p]),
 }
 
 _lib = None
@@ -694,3 +709,227 @@ def tq_paged_decode_recipe(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     if check and status is not None:
         raise_for_device_status(status)
     return out
+
+
+# ---------------------------------------------------------------- serving steps
+
+class StepPlan(NamedTuple):
+    """Outputs of tq_plan_step: the rows of the step and the state after it."""
+    slots: torch.Tensor       # int64 [max_rows]
+    q_seq: torch.Tensor       # int32 [max_rows]
+    q_len: torch.Tensor       # int32 [max_rows]
+    row_start: torch.Tensor   # int32 [S + 1]
+    seq_lens: torch.Tensor    # int32 [S]
+    seq_blocks: torch.Tensor  # int32 [S]
+    free_state: torch.Tensor  # int32 [2]
+
+
+def _need_like(name: str, dev: torch.device, **want) -> None:
+    """Every named (tensor, dtype, shape) is a contiguous tensor of that dtype and shape on `dev`."""
+    index = dev.index
+    for what, (t, dtype, shape) in want.items():
+        if t.get_device() != index or dev.type != "cuda":
+            raise ValueError(f"{name}: all tensors must be on the same CUDA device ({what} is on {t.device})")
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: {what} must be a contiguous {dtype} {list(shape)}, got {t.dtype} "
+                             f"{list(t.shape)}")
+
+
+def _call(dev: torch.device, fn, *args) -> None:
+    """One library call on the current stream of `dev`, with that device current."""
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != TQ_OK:
+        _check(status)
+
+
+def tq_plan_step(seq_lens: torch.Tensor, new_lens: torch.Tensor, seq_blocks: torch.Tensor, block_table: torch.Tensor,
+                 free_blocks: torch.Tensor, free_state: torch.Tensor, block_size: int, max_rows: int,
+                 out: StepPlan | None = None, status: torch.Tensor | None = None, check: bool = False) -> StepPlan:
+    """Plans a step on the device: appends new_lens[s] tokens to each sequence (negative:
+    finished, its blocks are returned), taking new blocks from the ring free_blocks[NB] whose
+    {head, count} is free_state[2].  block_table[S, W] and free_blocks are updated in place; the
+    state after the step is in the result, whose seq_lens / seq_blocks / free_state may be the
+    inputs themselves (pass them in `out`).  With check=True the call synchronises and raises
+    TQError(TQ_ERR_OUT_OF_BLOCKS / TQ_ERR_INVALID_ARG), with nothing planned."""
+    name = "tq_plan_step"
+    dev, i32 = seq_lens.device, torch.int32
+    if block_table.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError(f"{name}: block_table [S, W] and free_blocks [NB] expected")
+    s, w = block_table.shape
+    max_rows = int(max_rows)
+    if max_rows < 0:
+        raise ValueError(f"{name}: max_rows {max_rows} < 0")
+    if out is None:
+        if dev.type != "cuda":
+            raise ValueError(f"{name}: all tensors must be on the same CUDA device (seq_lens is on {dev})")
+        rows = torch.empty(4, max_rows, dtype=i32, device=dev)  # slots, q_seq, q_len
+        ints = torch.empty(3 * s + 3, dtype=i32, device=dev)
+        out = StepPlan(rows[:2].view(-1).view(torch.int64), rows[2], rows[3], ints[:s + 1], ints[s + 1:2 * s + 1],
+                       ints[2 * s + 1:3 * s + 1], ints[3 * s + 1:])
+    _need_like(name, dev, seq_lens=(seq_lens, i32, (s,)), new_lens=(new_lens, i32, (s,)),
+               seq_blocks=(seq_blocks, i32, (s,)), block_table=(block_table, i32, (s, w)),
+               free_blocks=(free_blocks, i32, (free_blocks.numel(),)), free_state=(free_state, i32, (2,)),
+               slots=(out.slots, torch.int64, (max_rows,)), q_seq=(out.q_seq, i32, (max_rows,)),
+               q_len=(out.q_len, i32, (max_rows,)), row_start=(out.row_start, i32, (s + 1,)),
+               seq_lens_out=(out.seq_lens, i32, (s,)), seq_blocks_out=(out.seq_blocks, i32, (s,)),
+               free_state_out=(out.free_state, i32, (2,)))
+    _need_status(name, status, dev)
+    if status is None and check:
+        status = _status_buffer(dev)
+    _call(dev, lib().tq_plan_step, seq_lens.data_ptr(), new_lens.data_ptr(), seq_blocks.data_ptr(), s,
+          block_table.data_ptr(), w, free_blocks.data_ptr(), free_state.data_ptr(), free_blocks.numel(),
+          int(block_size), max_rows, out.slots.data_ptr(), out.q_seq.data_ptr(), out.q_len.data_ptr(),
+          out.row_start.data_ptr(), out.seq_lens.data_ptr(), out.seq_blocks.data_ptr(), out.free_state.data_ptr(),
+          _ptr(status))
+    if check:
+        raise_for_device_status(status)
+    return out
+
+
+def tq_commit_tree(k_pages: torch.Tensor | None, v_pages: torch.Tensor | None, block_table: torch.Tensor,
+                   ctx_lens: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
+                   seq_lens: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                   check: bool = False) -> torch.Tensor:
+    """Moves the accepted rows of a verified tree: token ctx + path[s, j] to token ctx + j for
+    j < path_lens[s] (path[S, P] strictly ascending), in both page tensors [NB, bs, H, RB].
+    Returns the new lengths ctx + path_lens (written to `seq_lens`, which may be ctx_lens)."""
+    name = "tq_commit_tree"
+    pages = k_pages if k_pages is not None else v_pages
+    if pages is None or pages.dim() != 4 or block_table.dim() != 2 or path.dim() != 2:
+        raise ValueError(f"{name}: pages [NB, bs, H, RB], block_table [S, W] and path [S, P] expected")
+    nb, bs, h, _ = pages.shape
+    s, w = block_table.shape
+    dev, i32 = pages.device, torch.int32
+    if seq_lens is None:
+        seq_lens = torch.empty(s, dtype=i32, device=dev)
+    rb = [0, 0]
+    for i, (what, t) in enumerate((("k_pages", k_pages), ("v_pages", v_pages))):
+        if t is not None:
+            rb[i] = t.shape[-1]
+            _need_like(name, dev, **{what: (t, torch.uint8, (nb, bs, h, rb[i]))})
+    _need_like(name, dev, block_table=(block_table, i32, (s, w)), ctx_lens=(ctx_lens, i32, (s,)),
+               path=(path, i32, (s, path.shape[1])), path_lens=(path_lens, i32, (s,)), seq_lens=(seq_lens, i32, (s,)))
+    _need_status(name, status, dev)
+    if status is None and check:
+        status = _status_buffer(dev)
+    _call(dev, lib().tq_commit_tree, _ptr(k_pages), rb[0], _ptr(v_pages), rb[1], nb, bs, h, block_table.data_ptr(), s,
+          w, ctx_lens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), path.shape[1], seq_lens.data_ptr(),
+          _ptr(status))
+    if check:
+        raise_for_device_status(status)
+    return seq_lens
+
+
+_TREE_WORKSPACE: dict = {}
+
+
+def tq_paged_tree_workspace(num_q_rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of tq_paged_tree and tq_paged_prefill_biased on the current device."""
+    key = (torch.cuda.current_device(), num_q_rows, num_q_heads, num_kv_heads, head_dim)
+    need = _TREE_WORKSPACE.get(key)
+    if need is None:
+        need = int(lib().tq_paged_tree_workspace(num_q_rows, num_q_heads, num_kv_heads, head_dim))
+        if len(_TREE_WORKSPACE) > 4096:
+            _TREE_WORKSPACE.clear()
+        _TREE_WORKSPACE[key] = need
+    return need
+
+
+def _attn_call(name: str, q, q_seq, k_pages, v_pages, block_table, signs, k_centroids, v_centroids, out, out_dtype,
+               workspace, status, check, more, middle, tail, fn):
+    """Checks shared by tq_paged_tree and tq_paged_prefill_biased, and the call: `more` their
+    own tensors for _need_like (given the sizes), `middle` and `tail` their arguments."""
+    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError(f"{name}: q [T, Hq, D], pages [NB, bs, H, RB], block_table [S, W] expected")
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"{name}: q f32/f16/bf16 expected")
+    t, hq, d = q.shape
+    nb, bs, h, rbk = k_pages.shape
+    rbv = v_pages.shape[3]
+    s, w = block_table.shape
+    dev, i32 = q.device, torch.int32
+    kb, vb = _bits_from_centroids(k_centroids), _bits_from_centroids(v_centroids)
+    if rbk != tq_row_bytes(d, kb) or rbv != tq_row_bytes(d, vb):
+        raise ValueError(f"{name}: page rows of {rbk} / {rbv} bytes do not match head_dim {d} at {kb} / {vb} bits")
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=out_dtype or q.dtype, device=dev)
+    elif out.dtype not in _DTYPES:
+        raise ValueError(f"{name}: out must be f32/f16/bf16, got {out.dtype}")
+    _need_like(name, dev, q=(q, q.dtype, (t, hq, d)), k_pages=(k_pages, torch.uint8, (nb, bs, h, rbk)),
+               v_pages=(v_pages, torch.uint8, (nb, bs, h, rbv)), block_table=(block_table, i32, (s, w)),
+               q_seq=(q_seq, i32, (t,)), signs=(signs, torch.float32, (d,)),
+               k_centroids=(k_centroids, torch.float32, (1 << kb,)),
+               v_centroids=(v_centroids, torch.float32, (1 << vb,)), out=(out, out.dtype, (t, hq, d)),
+               **more(t, hq, s, i32))
+    _need_status(name, status, dev)
+    with torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else _NO_SWITCH:
+        need = tq_paged_tree_workspace(t, hq, h, d)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        elif workspace.get_device() != dev.index or not workspace.is_contiguous():
+            raise ValueError(f"{name}: workspace must be contiguous on {dev}")
+        if status is None and check:
+            status = _status_buffer(dev)
+        code = fn(q.data_ptr(), _DTYPES[q.dtype], t, hq, h, d, k_pages.data_ptr(), kb, v_pages.data_ptr(), vb, nb, bs,
+                  block_table.data_ptr(), s, w, q_seq.data_ptr(), *middle, signs.data_ptr(), k_centroids.data_ptr(),
+                  v_centroids.data_ptr(), *tail, out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(),
+                  workspace.numel() * workspace.element_size(), _ptr(status),
+                  torch.cuda.current_stream(dev).cuda_stream)
+    if code != TQ_OK:
+        _check(code)
+    if check:
+        raise_for_device_status(status)
+    return out
+
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def tq_paged_tree(q: torch.Tensor, q_seq: torch.Tensor, ctx_lens: torch.Tensor, tree_mask: torch.Tensor,
+                  k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, signs: torch.Tensor,
+                  k_centroids: torch.Tensor, v_centroids: torch.Tensor, scale: float | None = None,
+                  softcap: float = 0.0, out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                  workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                  check: bool = False) -> torch.Tensor:
+    """Attention of drafted tokens: row i of q[T, Hq, D] sees the first ctx_lens[q_seq[i]]
+    tokens of its sequence and, behind them, token ctx + j for every set bit j of its mask
+    (bit j % 32 of tree_mask[i, j // 32], int32 [T, words]).  q_seq -1 is a padding row."""
+    if tree_mask.dim() != 2:
+        raise ValueError("tq_paged_tree: tree_mask [T, words] expected")
+    words = tree_mask.shape[1]
+    return _attn_call("tq_paged_tree", q, q_seq, k_pages, v_pages, block_table, signs, k_centroids, v_centroids, out,
+                      out_dtype, workspace, status, check,
+                      lambda t, hq, s, i32: dict(ctx_lens=(ctx_lens, i32, (s,)), tree_mask=(tree_mask, i32, (t, words))),
+                      (ctx_lens.data_ptr(), tree_mask.data_ptr(), words), (float(scale or 0.0), float(softcap)),
+                      lib().tq_paged_tree)
+
+
+def tq_paged_prefill_biased(q: torch.Tensor, q_seq: torch.Tensor, q_len: torch.Tensor, k_pages: torch.Tensor,
+                            v_pages: torch.Tensor, block_table: torch.Tensor, signs: torch.Tensor,
+                            k_centroids: torch.Tensor, v_centroids: torch.Tensor, scale: float | None = None,
+                            softcap: float = 0.0, window: int = 0, alibi_slopes: torch.Tensor | None = None,
+                            prefix_lens: torch.Tensor | None = None, doc_starts: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                            workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                            check: bool = False) -> torch.Tensor:
+    """tq_paged_prefill with modified scores and visible sets: scores capped at `softcap` by a
+    tanh, minus alibi_slopes[Hq] times the distance; row i sees tokens t >= doc_starts[i] with
+    t < prefix_lens[q_seq[i]] or q_len[i] - window <= t < q_len[i] (window 0: all before it)."""
+    def more(t, hq, s, i32):
+        want = dict(q_len=(q_len, i32, (t,)))
+        if alibi_slopes is not None:
+            want["alibi_slopes"] = (alibi_slopes, torch.float32, (hq,))
+        if prefix_lens is not None:
+            want["prefix_lens"] = (prefix_lens, i32, (s,))
+        if doc_starts is not None:
+            want["doc_starts"] = (doc_starts, i32, (t,))
+        return want
+
+    return _attn_call("tq_paged_prefill_biased", q, q_seq, k_pages, v_pages, block_table, signs, k_centroids,
+                      v_centroids, out, out_dtype, workspace, status, check, more,
+                      (q_len.data_ptr(), _ptr(prefix_lens), _ptr(doc_starts), int(window), _ptr(alibi_slopes)),
+                      (float(scale or 0.0), float(softcap)), lib().tq_paged_prefill_biased)

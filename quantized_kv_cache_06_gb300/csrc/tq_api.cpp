@@ -19,9 +19,11 @@
 #include <vector>
 
 #include "tq.h"
+#include "tq_attn.h"
 #include "tq_internal.h"
 #include "tq_qjl.h"
 #include "tq_recipe.h"
+#include "tq_step.h"
 
 namespace {
 
@@ -321,6 +323,71 @@ tq_status decode_impl(const char* name, const void* q, tq_dtype q_dtype, int bat
     return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be >= %zu bytes and 16-byte aligned (got %zu)", name,
                 plan.workspace_bytes, workspace_bytes);
   return check_cuda(tq::launch_decode(a, plan, static_cast<cudaStream_t>(stream)), name);
+}
+
+
+tq::AttnArgs make_attn_args(int num_q_rows, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                            int block_size) {
+  tq::AttnArgs a{};
+  a.num_rows = num_q_rows;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.v_alpha = a.k_alpha = 1.0f;
+  return a;
+}
+
+// The bits and dtypes decide between the kernels, and the workspace queries do not take them:
+// the largest plan over them.
+size_t attn_workspace_any(tq::AttnArgs a, int sms) {
+  size_t need = 0;
+  for (int t : {TQ_F32, TQ_F16, TQ_BF16}) {
+    a.out_dtype = t;
+    for (int bits = 2; bits <= 5; ++bits) {
+      a.k_bits = a.v_bits = bits;
+      need = std::max(need, tq::plan_attn(a, sms).workspace_bytes);
+    }
+  }
+  return need;
+}
+
+// Checks shared by tq_paged_tree and tq_paged_prefill_biased, then the launch.
+tq_status attn_impl(const char* name, tq::AttnArgs a, size_t workspace_bytes, const void* row_lens, void* stream) {
+  tq_status st = decode_shape_check(a.num_rows, a.num_q_heads, a.num_kv_heads, a.head_dim, a.max_blocks_per_seq,
+                                    a.block_size);
+  if (st != TQ_OK) return st;
+  if (!bits_ok(a.k_bits) || !bits_ok(a.v_bits))
+    return fail(TQ_ERR_UNSUPPORTED, "k_bits %d / v_bits %d: must be 2, 3, 4 or 5", a.k_bits, a.v_bits);
+  if (!dtype_ok(a.q_dtype) || !dtype_ok(a.out_dtype)) return fail(TQ_ERR_INVALID_ARG, "%s: unknown dtype", name);
+  if (a.num_blocks < 0 || a.num_seqs < 0) return fail(TQ_ERR_INVALID_ARG, "%s: num_blocks or num_seqs < 0", name);
+  if (!(a.softcap >= 0.f) || std::isinf(a.softcap))
+    return fail(TQ_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0 (0: none)", name);
+  const int64_t cap = (int64_t)a.max_blocks_per_seq * a.block_size;
+  if (cap > 0x7fffff00LL)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: a table row of %lld tokens (at most 2^31 - 256)", name, (long long)cap);
+  if ((double)a.num_rows * (double)(cap / tq::kAttnTile + 2) > 2147483647.0)
+    return fail(TQ_ERR_UNSUPPORTED, "%s: %d rows of up to %lld tokens: pass fewer rows a call", name, a.num_rows,
+                (long long)cap);
+  if (a.num_rows > 0 && (!a.q || !a.k_pages || !a.v_pages || !a.q_seq || !row_lens || !a.signs || !a.k_centroids ||
+                         !a.v_centroids || !a.out || (a.max_blocks_per_seq > 0 && a.num_seqs > 0 && !a.block_table)))
+    return fail(TQ_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (a.num_rows > 0 &&
+      (!aligned(a.q, dtype_size(a.q_dtype)) || !aligned(a.out, dtype_size(a.out_dtype)) || !aligned(a.k_pages, 16) ||
+       !aligned(a.v_pages, 16) || !aligned(a.block_table, 4) || !aligned(a.q_seq, 4) || !aligned(row_lens, 4) ||
+       !aligned(a.prefix_lens, 4) || !aligned(a.doc_starts, 4) || !aligned(a.alibi, 4) || !aligned(a.mask, 4) ||
+       !aligned(a.status, 4)))
+    return fail(TQ_ERR_INVALID_ARG, "%s: misaligned pointer (pages need 16-byte alignment)", name);
+  const tq::AttnPlan plan = tq::plan_attn(a, current_device_sms());
+  if (a.num_rows > 0 && (workspace_bytes < plan.workspace_bytes || !a.workspace || !aligned(a.workspace, 256)))
+    return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be >= %zu bytes and 256-byte aligned (got %zu)", name,
+                plan.workspace_bytes, workspace_bytes);
+  if (plan.tc) {
+    a.k_alpha = fp16_scale_for(a.head_dim, a.k_bits);
+    a.v_alpha = fp16_scale_for(a.head_dim, a.v_bits);
+  }
+  return check_cuda(tq::launch_attn(a, plan, static_cast<cudaStream_t>(stream)), name);
 }
 
 
@@ -885,6 +952,167 @@ tq_status tq_paged_decode_recipe(const void* q, tq_dtype q_dtype, int batch, int
   a.status = status_dev;
   a.v_alpha = a.k_alpha = 1.0f;
   return check_cuda(tq::launch_decode_recipe(a, rc, plan, static_cast<cudaStream_t>(stream)), name);
+}
+
+tq_status tq_plan_step(const int32_t* seq_lens, const int32_t* new_lens, const int32_t* seq_blocks, int num_seqs,
+                       int32_t* block_table, int max_blocks_per_seq, int32_t* free_blocks, const int32_t* free_state,
+                       int64_t num_blocks, int block_size, int64_t max_rows, int64_t* slots, int32_t* q_seq,
+                       int32_t* q_len, int32_t* row_start, int32_t* seq_lens_out, int32_t* seq_blocks_out,
+                       int32_t* free_state_out, int32_t* status_dev, void* stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || num_blocks > 0x7fffffffLL || block_size < 1 ||
+      max_rows < 0 || max_rows > 0x7fffffffLL)
+    return fail(TQ_ERR_INVALID_ARG, "tq_plan_step: invalid sizes (seqs=%d, max_blocks=%d, blocks=%lld, block_size=%d, "
+                "max_rows=%lld)", num_seqs, max_blocks_per_seq, (long long)num_blocks, block_size, (long long)max_rows);
+  if (!free_state || !free_state_out || !row_start || (num_blocks > 0 && !free_blocks) ||
+      (num_seqs > 0 && (!seq_lens || !new_lens || !seq_blocks || !seq_lens_out || !seq_blocks_out ||
+                        (max_blocks_per_seq > 0 && !block_table))) ||
+      (max_rows > 0 && (!slots || !q_seq || !q_len)))
+    return fail(TQ_ERR_INVALID_ARG, "tq_plan_step: null pointer argument");
+  for (const void* p : {(const void*)seq_lens, (const void*)new_lens, (const void*)seq_blocks, (const void*)block_table,
+                        (const void*)free_blocks, (const void*)free_state, (const void*)q_seq, (const void*)q_len,
+                        (const void*)row_start, (const void*)seq_lens_out, (const void*)seq_blocks_out,
+                        (const void*)free_state_out, (const void*)status_dev})
+    if (!aligned(p, 4)) return fail(TQ_ERR_INVALID_ARG, "tq_plan_step: misaligned pointer");
+  if (!aligned(slots, 8)) return fail(TQ_ERR_INVALID_ARG, "tq_plan_step: misaligned slots");
+  tq::PlanArgs a{};
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.seq_blocks = seq_blocks;
+  a.num_seqs = num_seqs;
+  a.block_table = block_table;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.free_blocks = free_blocks;
+  a.free_state = free_state;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.max_rows = max_rows;
+  a.slots = slots;
+  a.q_seq = q_seq;
+  a.q_len = q_len;
+  a.row_start = row_start;
+  a.seq_lens_out = seq_lens_out;
+  a.seq_blocks_out = seq_blocks_out;
+  a.free_state_out = free_state_out;
+  a.status = status_dev;
+  return check_cuda(tq::launch_plan_step(a, static_cast<cudaStream_t>(stream)), "tq_plan_step");
+}
+
+tq_status tq_commit_tree(uint8_t* k_pages, int64_t k_row_bytes, uint8_t* v_pages, int64_t v_row_bytes,
+                         int64_t num_blocks, int block_size, int num_kv_heads, const int32_t* block_table,
+                         int num_seqs, int max_blocks_per_seq, const int32_t* ctx_lens, const int32_t* path,
+                         const int32_t* path_lens, int max_path, int32_t* seq_lens_out, int32_t* status_dev,
+                         void* stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || block_size < 1 || num_kv_heads < 1 || max_path < 0 ||
+      k_row_bytes < 0 || v_row_bytes < 0 || (k_pages && k_row_bytes < 1) || (v_pages && v_row_bytes < 1))
+    return fail(TQ_ERR_INVALID_ARG, "tq_commit_tree: invalid sizes (seqs=%d, max_blocks=%d, blocks=%lld, "
+                "block_size=%d, kv_heads=%d, max_path=%d, row_bytes=%lld/%lld)", num_seqs, max_blocks_per_seq,
+                (long long)num_blocks, block_size, num_kv_heads, max_path, (long long)k_row_bytes,
+                (long long)v_row_bytes);
+  if ((double)num_kv_heads * (double)std::max(k_row_bytes, v_row_bytes) > 16777216.0)
+    return fail(TQ_ERR_UNSUPPORTED, "tq_commit_tree: a token's rows of more than 16 MiB");
+  if (!k_pages && !v_pages) return fail(TQ_ERR_INVALID_ARG, "tq_commit_tree: no pages");
+  if (num_seqs > 0 && (!ctx_lens || !path_lens || !seq_lens_out || (max_path > 0 && !path) ||
+                       (max_blocks_per_seq > 0 && !block_table)))
+    return fail(TQ_ERR_INVALID_ARG, "tq_commit_tree: null pointer argument");
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) || !aligned(ctx_lens, 4) ||
+      !aligned(path, 4) || !aligned(path_lens, 4) || !aligned(seq_lens_out, 4) || !aligned(status_dev, 4))
+    return fail(TQ_ERR_INVALID_ARG, "tq_commit_tree: misaligned pointer (pages need 16-byte alignment)");
+  tq::CommitArgs a{};
+  a.k_pages = k_pages;
+  a.k_slab = k_pages ? (int)(num_kv_heads * k_row_bytes) : 0;
+  a.v_pages = v_pages;
+  a.v_slab = v_pages ? (int)(num_kv_heads * v_row_bytes) : 0;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.block_table = block_table;
+  a.num_seqs = num_seqs;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.ctx_lens = ctx_lens;
+  a.path = path;
+  a.path_lens = path_lens;
+  a.max_path = max_path;
+  a.seq_lens_out = seq_lens_out;
+  a.status = status_dev;
+  return check_cuda(tq::launch_commit_tree(a, static_cast<cudaStream_t>(stream)), "tq_commit_tree");
+}
+
+size_t tq_paged_tree_workspace(int num_q_rows, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (decode_shape_check(num_q_rows, num_q_heads, num_kv_heads, head_dim, 0, 1) != TQ_OK) return 0;
+  return attn_workspace_any(make_attn_args(num_q_rows, num_q_heads, num_kv_heads, head_dim, 0, 1),
+                            current_device_sms());
+}
+
+tq_status tq_paged_tree(const void* q, tq_dtype q_dtype, int num_q_rows, int num_q_heads, int num_kv_heads,
+                        int head_dim, const uint8_t* k_pages, int k_bits, const uint8_t* v_pages, int v_bits,
+                        int64_t num_blocks, int block_size, const int32_t* block_table, int num_seqs,
+                        int max_blocks_per_seq, const int32_t* q_seq, const int32_t* ctx_lens,
+                        const uint32_t* tree_mask, int mask_words, const float* signs, const float* k_centroids,
+                        const float* v_centroids, float scale, float softcap, void* out, tq_dtype out_dtype,
+                        void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  if (mask_words < 1 || mask_words > 1024)
+    return fail(TQ_ERR_INVALID_ARG, "tq_paged_tree: mask_words %d must be 1 .. 1024", mask_words);
+  if (num_q_rows > 0 && !tree_mask) return fail(TQ_ERR_INVALID_ARG, "tq_paged_tree: null pointer argument");
+  tq::AttnArgs a = make_attn_args(num_q_rows, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size);
+  a.q = q;
+  a.q_dtype = (int)q_dtype;
+  a.k_pages = k_pages;
+  a.k_bits = k_bits;
+  a.v_pages = v_pages;
+  a.v_bits = v_bits;
+  a.num_blocks = num_blocks;
+  a.block_table = block_table;
+  a.num_seqs = num_seqs;
+  a.q_seq = q_seq;
+  a.ctx_lens = ctx_lens;
+  a.mask = tree_mask;
+  a.mask_words = mask_words;
+  a.softcap = softcap;
+  a.scale = scale;
+  a.signs = signs;
+  a.k_centroids = k_centroids;
+  a.v_centroids = v_centroids;
+  a.out = out;
+  a.out_dtype = (int)out_dtype;
+  a.workspace = workspace;
+  a.status = status_dev;
+  return attn_impl("tq_paged_tree", a, workspace_bytes, ctx_lens, stream);
+}
+
+tq_status tq_paged_prefill_biased(const void* q, tq_dtype q_dtype, int num_q_rows, int num_q_heads, int num_kv_heads,
+                                  int head_dim, const uint8_t* k_pages, int k_bits, const uint8_t* v_pages, int v_bits,
+                                  int64_t num_blocks, int block_size, const int32_t* block_table, int num_seqs,
+                                  int max_blocks_per_seq, const int32_t* q_seq, const int32_t* q_len,
+                                  const int32_t* prefix_lens, const int32_t* doc_starts, int window,
+                                  const float* alibi_slopes, const float* signs, const float* k_centroids,
+                                  const float* v_centroids, float scale, float softcap, void* out, tq_dtype out_dtype,
+                                  void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  if (window < 0) return fail(TQ_ERR_INVALID_ARG, "tq_paged_prefill_biased: window %d < 0 (0: none)", window);
+  tq::AttnArgs a = make_attn_args(num_q_rows, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size);
+  a.q = q;
+  a.q_dtype = (int)q_dtype;
+  a.k_pages = k_pages;
+  a.k_bits = k_bits;
+  a.v_pages = v_pages;
+  a.v_bits = v_bits;
+  a.num_blocks = num_blocks;
+  a.block_table = block_table;
+  a.num_seqs = num_seqs;
+  a.q_seq = q_seq;
+  a.q_len = q_len;
+  a.prefix_lens = prefix_lens;
+  a.doc_starts = doc_starts;
+  a.window = window;
+  a.alibi = alibi_slopes;
+  a.softcap = softcap;
+  a.scale = scale;
+  a.signs = signs;
+  a.k_centroids = k_centroids;
+  a.v_centroids = v_centroids;
+  a.out = out;
+  a.out_dtype = (int)out_dtype;
+  a.workspace = workspace;
+  a.status = status_dev;
+  return attn_impl("tq_paged_prefill_biased", a, workspace_bytes, q_len, stream);
 }
 
 }  // extern "C"
