@@ -25,7 +25,7 @@ SOURCES = ["tq_api.cpp", "tq_write.cu", "tq_write_tc.cu", "tq_decode.cu", "tq_de
            "tq_decode_tc_b.cu", "tq_decode_tc_c.cu", "tq_decode_tc_d.cu", "tq_decode_tc_e.cu",
            "tq_decode_tc_f.cu", "tq_decode_tc_p.cu",
            "tq_decode_tc_q.cu", "tq_prefill_mq.cu",
-           "tq_dequant.cu", "tq_qjl.cu", "tq_recipe.cu", "tq_query.cu", "tq_step.cu", "tq_attn.cu",
+           "tq_dequant.cu", "tq_qjl.cu", "tq_recipe.cu", "tq_query.cu", "tq_step.cu", "tq_attn.cu", "tq_attn_tc.cu",
            "tq_small.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

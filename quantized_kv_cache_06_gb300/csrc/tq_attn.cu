@@ -439,10 +439,10 @@ cudaError_t launch_combine(const AttnArgs& a, const AttnWork& w, cudaStream_t st
 
 AttnPlan plan_attn(const AttnArgs& a, int num_sms) {
   AttnPlan p{};
-  p.tc = false;
-  p.cols = kSimtCols;
-  // SIMT: two CTAs an SM hide each other's barriers
-  const int ctas = 2 * num_sms;
+  p.tc = attn_tc_supported(a);
+  p.cols = p.tc ? attn_tc_cols(a) : kSimtCols;
+  // tensor cores: one CTA (all of TMEM) an SM; SIMT: two, which hide each other's barriers
+  const int ctas = p.tc ? num_sms : 2 * num_sms;
   p.parts = std::max(1, ctas / std::max(1, a.num_kv_heads));
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = (size_t)std::max(0, a.num_rows);
@@ -471,7 +471,9 @@ cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t strea
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   count_launches(1);
-  switch (a.head_dim) {
+  if (p.tc) {
+    err = launch_attn_tc(a, w, stream);
+  } else switch (a.head_dim) {
     case 16: err = launch_simt<16>(a, w, stream); break;
     case 32: err = launch_simt<32>(a, w, stream); break;
     case 64: err = launch_simt<64>(a, w, stream); break;

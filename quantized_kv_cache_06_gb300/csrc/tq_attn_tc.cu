@@ -1,0 +1,1142 @@
+// Tensor-core attention of query rows with a visible set of their own over packed TurboQuant
+// pages (sm_103a, tcgen05): drafted trees, biased prefill, single tokens.
+//
+// TurboQuant docs: "vLLM Usage" (Runtime Dispatch: the cache plus mixed prefill/decode reads
+// the packed cache) and "Architecture" (Diagnostic vs Serving Paths: keys consumed
+// compressed, values accumulated from packed indices).
+//
+// For a tile of 128 tokens of one kv head and the window's columns (query row, q head of the
+// group), both products are taken transposed, tokens (or dims) on the 128 lanes and the
+// columns on N, so that a window of any number of columns fills the tensor cores' M:
+//   S^T [tokens x cols] = Khat [tokens x D]  Q^T           A = Khat in TMEM, B = Q (K-major)
+//   O^T [dims x cols]  += Vhat^T [dims x tokens] P^T       A = Vhat, B = P^T, both stored as
+//                                                          they are produced (MN-major)
+// Khat = fp16(alpha_k c[idx]) never touches shared memory: the thread that owns a token
+// expands its packed row in registers and stores it to its own TMEM lane.  Vhat goes to
+// shared memory in 16-byte chunks, swizzled.  The norms are per token, so per lane: nu_k
+// multiplies the score, nu_v the weight.
+//
+// Precision.  fp16 outputs (SPLIT): Q = hi + lo 2^-12 and P' = hi + lo 2^-11 in fp16, the lo
+// parts as further columns of the same MMAs, so what is left is the rounding of the centroids
+// (alpha puts them near fp16 grid points).  bf16 outputs: one fp16 part each, eight times
+// finer than the output's own rounding.  The window's queries are scaled by one power of two,
+// and the weights p nu_v by another (moved when a larger norm arrives), so neither large
+// queries nor large norms leave the fp16 range.  Sums, maxima and both products are fp32.
+//
+// Softmax in base 2; the running max of a column moves only when a score passes it by 2^6, so
+// most tiles rescale nothing; when one does, the softmax warps scale O^T in TMEM themselves
+// (the product before has completed by then).
+//
+// Roles of the 18 warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, two
+// sets that take alternate groups of eight columns), 16 copies, 17 MMA issue.  Packed rows
+// arrive by TMA: the pages seen as a 2-D byte tensor [slots][H row_bytes], a box of up to 128
+// rows x the 16-byte aligned span around the head's bytes, so a block of a page is one copy.
+// Rows whose slab is not a multiple of 16 bytes (H not a multiple of 4) come by 4-byte
+// cp.async.  All waits are bounded: one that runs out records the timeout, every role leaves
+// its loop, copies and MMAs in flight are drained and TMEM is freed.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "tq_attn.h"
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+constexpr float kLog2eA = 1.4426950408889634f;
+constexpr int kTok = kAttnTile;  // tokens per tile = MMA lanes
+constexpr int kKeyWarps = 4, kValWarps = 4, kSoftWarps = 8;
+constexpr int kCopyWarp = kKeyWarps + kValWarps + kSoftWarps;
+constexpr int kMmaWarp = kCopyWarp + 1;
+constexpr int kTcThreads = 32 * (kMmaWarp + 1);
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kMaxRing = 6;
+constexpr float kSlack = 6.0f;            // log2 units the running max may lag
+constexpr float kLoQ = 4096.0f;           // scale of the fp16 remainders of Q
+constexpr float kLoP = 2048.0f;           // and of P'
+constexpr int kBarSoft = 1;               // named barrier of the softmax warps
+
+template <int D, bool SPLIT>
+struct Tc {
+  static constexpr int kN = D == 256 ? 64 : 128;         // MMA columns at most
+  static constexpr int kCols = SPLIT ? kN / 2 : kN;      // window columns at most
+  static constexpr int kGroups = kCols / 16;             // groups of 8 columns per softmax thread
+  static constexpr int kHalves = D == 256 ? 2 : 1;       // 128-dim halves of O^T
+  static constexpr int kKCols = D / 2;                   // TMEM columns of a key tile
+  static constexpr int kVBufs = D == 256 ? 1 : 2;
+  // TMEM columns
+  static constexpr int kS = 0;
+  static constexpr int kO = 2 * kN;
+  static constexpr int kK = kO + kHalves * kN;
+  static_assert(kK + 2 * kKCols <= 512, "TMEM columns");
+  // shared memory (offsets from a 1024-byte aligned base)
+  static constexpr int kQBytes = kN * D * 2;
+  static constexpr int kVBytes = kTok * D * 2;
+  static constexpr int kPBytes = kTok * kN * 2 < 16384 ? 16384 : kTok * kN * 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffV = kOffQ + kQBytes;
+  static constexpr int kOffP = kOffV + kVBufs * kVBytes;
+  static constexpr int kOffRows = kOffP + kPBytes;                 // RowView[kCols]
+  static constexpr int kOffCol = kOffRows + kCols * (int)sizeof(RowView);  // float m[kN], slope[kN], part[4][kN]
+  static constexpr int kOffTab = kOffCol + 6 * kN * 4;              // 5-bit tables, 2 x 32 x 32 words
+  static constexpr int kOffMeta = kOffTab + 2 * 32 * 32 * 4;        // uint32 valid[kMaxRing][4]
+  static constexpr int kOffRing = (kOffMeta + kMaxRing * 16 + 127) / 128 * 128;
+  static constexpr int kStageCols = kPBytes / (D * 4);              // output columns staged at a time
+};
+
+// Bytes of a packed row's span in the ring: the 16-byte aligned span that holds a row wherever
+// it starts (a multiple of 4), rounded to an odd number of 16-byte units, which keeps 16-byte
+// reads of neighbouring rows in different banks.
+__host__ __device__ constexpr int span_bytes(int d, int bits) {
+  int s = (d * bits / 8 + 4 + 12 + 15) / 16 * 16;
+  return (s / 16) % 2 ? s : s + 16;
+}
+
+struct TcAttnArgs {
+  AttnArgs a;
+  AttnWork w;
+  int ring;        // stages
+  int sub;         // tokens per copy: the largest power of two that divides the block size, at most 128
+  int tma;         // rows arrive by TMA (else cp.async)
+  uint32_t tries;  // of a bounded wait
+};
+
+// ---------------------------------------------------------------- primitives
+
+__device__ __forceinline__ uint32_t smem_a(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+// D (+)= A B, kind::f16, A in TMEM or in shared memory, B in shared memory; one thread.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
+                   "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::
+                   "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+               : "memory");
+}
+// Shared-memory operand in the 128-byte swizzle: rows (K-major) or k-lines (MN-major) of 128
+// bytes, groups of eight of them `sbo` apart; `lbo` apart the next 64 elements of an MN-major
+// operand.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// f16 x f16 -> f32, M 128; `mn`: both operands MN-major.
+__device__ __forceinline__ uint32_t mma_idesc(int n, bool mn) {
+  return (1u << 4) | (mn ? (1u << 15) | (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void st_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_s32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ex2a(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcpa(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;\n" ::"n"(kBarSoft), "n"(kSoftThreads) : "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(kBarSoft), "n"(kSoftThreads)
+      : "memory");
+  return r != 0;
+}
+// Order-preserving map of floats to ints and back (for integer maxima over a warp).
+__device__ __forceinline__ int ord_int(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float ord_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+// Exponent of a power of two near x > 0 (finite): floor(log2 x), -126 for zero and subnormals.
+__device__ __forceinline__ int exp_of(float x) { return max((int)((__float_as_uint(x) >> 23) & 0xffu) - 127, -126); }
+
+// ---------------------------------------------------------------- dequantisation
+
+// Centroids fp16(alpha c) as byte tables: the low and the high bytes of eight entries per
+// register pair.  A PRMT whose selector is four indices of three bits returns the bytes of four
+// coordinates, so no lookup leaves the registers; four bits take two of them and a select.
+template <int BITS>
+struct ByteTable {
+  static constexpr int kPairs = BITS == 4 ? 2 : 1;
+  uint32_t lo[2 * kPairs], hi[2 * kPairs];
+  __device__ __forceinline__ void load(const float* c, float alpha) {
+#pragma unroll
+    for (int r = 0; r < 2 * kPairs; ++r) {
+      lo[r] = hi[r] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = 4 * r + k;
+        if (e < (1 << BITS)) {
+          const uint32_t u = __half_as_ushort(__float2half_rn(__ldg(c + e) * alpha));
+          lo[r] |= (u & 255u) << (8 * k);
+          hi[r] |= (u >> 8) << (8 * k);
+        }
+      }
+    }
+  }
+};
+
+// Eight consecutive coordinates (group g of the row's words) as four fp16 pairs.
+template <int BITS>
+__device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTable<BITS>& t, uint32_t (&out)[4]) {
+  uint32_t sel;  // eight selector nibbles
+  uint32_t x;
+  if constexpr (BITS == 4) {
+    x = w[g];
+    sel = x & 0x77777777u;
+  } else if constexpr (BITS == 3) {
+    const int bit = 24 * g, i = bit >> 5, sh = bit & 31;
+    x = sh <= 8 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh);
+    x = (x & 0x00000fffu) | ((x << 4) & 0x0fff0000u);
+    x = (x & 0x003f003fu) | ((x << 2) & 0x3f003f00u);
+    sel = (x & 0x07070707u) | ((x << 1) & 0x70707070u);
+  } else {
+    x = g & 1 ? w[g >> 1] >> 16 : w[g >> 1] & 0xffffu;
+    x = (x | (x << 8)) & 0x00ff00ffu;
+    x = (x | (x << 4)) & 0x0f0f0f0fu;
+    sel = (x | (x << 2)) & 0x33333333u;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t s = k ? sel >> 16 : sel;
+    uint32_t lo = __byte_perm(t.lo[0], t.lo[1], s), hi = __byte_perm(t.hi[0], t.hi[1], s);
+    if constexpr (BITS == 4) {
+      // bytes 0xff where bit 3 of the index is set (the sign-replicating selector form)
+      const uint32_t y = k ? x >> 16 : x;
+      uint32_t m;
+      asm("prmt.b32 %0, %1, %2, 0xd9c8;\n" : "=r"(m) : "r"(y << 4), "r"(y));
+      lo = (lo & ~m) | (__byte_perm(t.lo[2], t.lo[3], s) & m);
+      hi = (hi & ~m) | (__byte_perm(t.hi[2], t.hi[3], s) & m);
+    }
+    out[2 * k] = __byte_perm(lo, hi, 0x5140);
+    out[2 * k + 1] = __byte_perm(lo, hi, 0x7362);
+  }
+}
+
+// 5-bit rows: one shared-memory lookup per coordinate, the 32 entries replicated per lane.
+__device__ __forceinline__ void expand8_5(const uint32_t* w, int g, uint32_t tab_lane, uint32_t (&out)[4]) {
+  uint32_t v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int bit = 40 * g + 5 * k, i = bit >> 5, sh = bit & 31;
+    const uint32_t f = (sh <= 27 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh)) & 31u;
+    v[k] = ld_s32(tab_lane + f * 128u);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) out[k] = __byte_perm(v[2 * k], v[2 * k + 1], 0x5410);
+}
+
+// The row of this thread's token in the ring: SPAN bytes, of which the row starts `skip` words in.
+template <int D, int BITS>
+__device__ __forceinline__ void load_row(uint32_t addr, int skip, uint32_t (&w)[D * BITS / 32 + 1]) {
+  constexpr int SPAN = span_bytes(D, BITS), NW = D * BITS / 32;
+  constexpr int NV = (NW + 3 + 3) / 4 < SPAN / 16 ? (NW + 3 + 3) / 4 : SPAN / 16;
+  uint32_t r[4 * NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint4 v = ld_v4(addr + 16 * i);
+    r[4 * i] = v.x;
+    r[4 * i + 1] = v.y;
+    r[4 * i + 2] = v.z;
+    r[4 * i + 3] = v.w;
+  }
+  const bool s1 = skip & 1, s2 = skip & 2;
+#pragma unroll
+  for (int i = 0; i < 4 * NV; ++i) r[i] = s1 && i + 1 < 4 * NV ? r[i + 1 < 4 * NV ? i + 1 : i] : r[i];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) w[i] = s2 ? r[i + 2 < 4 * NV ? i + 2 : i] : r[i];
+  w[NW] = 0;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tc_kernel(const __grid_constant__ TcAttnArgs p, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap) {
+  using C = Tc<D, SPLIT>;
+  const AttnArgs& a = p.a;
+  const AttnWork& w = p.w;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxRing + 16];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int dead, fail[2];
+  __shared__ int full_lo, full_hi, pre_lo, pre_hi, q_exp;
+  unsigned char* smem = smem_raw + ((1024u - (smem_a(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_a(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int H = a.num_kv_heads, G = a.num_q_heads / H;
+  const int h = blockIdx.x % H, part = blockIdx.x / H;
+  const int rbk = D * a.k_bits / 8 + 4, rbv = D * a.v_bits / 8 + 4;
+  const int spk = span_bytes(D, a.k_bits), spv = span_bytes(D, a.v_bits);
+  const int skip_k = p.tma ? (h * rbk) % 16 : 0, skip_v = p.tma ? (h * rbv) % 16 : 0;
+  const int stage_bytes = kTok * (spk + spv);
+  const uint32_t ring = base + C::kOffRing;
+
+  auto bar = [&](int i) -> uint32_t { return smem_a(bars) + 8u * i; };
+  auto raw_full = [&](int s) { return bar(s); };
+  auto raw_empty = [&](int s) { return bar(kMaxRing + s); };
+  const int B0 = 2 * kMaxRing;
+  auto k_full = [&](int b) { return bar(B0 + b); };
+  auto k_empty = [&](int b) { return bar(B0 + 2 + b); };
+  auto s_full = [&](int b) { return bar(B0 + 4 + b); };
+  auto s_empty = [&](int b) { return bar(B0 + 6 + b); };
+  auto v_full = [&](int b) { return bar(B0 + 8 + b); };
+  auto v_empty = [&](int b) { return bar(B0 + 10 + b); };
+  const uint32_t p_full = bar(B0 + 12), p_empty = bar(B0 + 13), q_full = bar(B0 + 14), drained = bar(B0 + 15);
+  volatile int* dead_v = &dead;
+
+  // A bounded wait of one thread; a role that has seen another give up leaves too.
+  auto wait1 = [&](uint32_t b, uint32_t parity) -> bool {
+    for (uint32_t i = 0; i < p.tries; ++i) {
+      if (bar_try(b, parity)) return true;
+      if ((i & 255u) == 255u && *dead_v) return false;
+    }
+    if (!*dead_v) {
+      *dead_v = 1;
+      if (a.status) atomicMax(a.status, (int32_t)kTimeout);
+    }
+    return false;
+  };
+  // The same by a whole warp, with one answer.
+  auto wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(kFullMask, wait1(b, parity)); };
+
+  if (tid == 0) {
+    dead = 0;
+    fail[0] = fail[1] = 0;
+    for (int s = 0; s < kMaxRing; ++s) {
+      bar_init(raw_full(s), p.tma ? 1 : 33);  // cp.async: every lane's copies and one arrival
+      bar_init(raw_empty(s), kKeyWarps + kValWarps + kSoftWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(k_full(b), kKeyWarps);
+      bar_init(k_empty(b), 1);
+      bar_init(s_full(b), 1);
+      bar_init(s_empty(b), kSoftWarps);
+      bar_init(v_full(b), kValWarps);
+      bar_init(v_empty(b), 1);
+    }
+    bar_init(p_full, kSoftWarps);
+    bar_init(p_empty, 1);
+    bar_init(q_full, kSoftWarps);
+    bar_init(drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_a(&tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  // 5-bit tables: entry e of lane l at e * 128 + 4 l
+  if (a.k_bits == 5 || a.v_bits == 5)
+    for (int i = tid; i < 2 * 32 * 32; i += kTcThreads) {
+      const int comp = i >> 10, e = (i >> 5) & 31;
+      const int bits = comp ? a.v_bits : a.k_bits;
+      const float c = e < (1 << bits) ? __ldg((comp ? a.v_centroids : a.k_centroids) + e) : 0.f;
+      reinterpret_cast<uint32_t*>(smem + C::kOffTab)[i] =
+          __half_as_ushort(__float2half_rn(c * (comp ? a.v_alpha : a.k_alpha)));
+    }
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+
+  const int total = w.head->total_tiles;
+  const int parts = live_parts(w, total);
+  const int g0 = part < parts ? part_begin(total, part, parts) : 0;
+  const int g1 = part < parts ? part_begin(total, part + 1, parts) : 0;
+  // Calls f(window, first tile, end tile) for every window with tiles in this part.
+  auto for_windows = [&](auto f) {
+    if (g0 >= g1) return;
+    for (int g = g0, wi = window_of(w, g0); g < g1; ++wi) {
+      const AttnWindow win = w.win[wi];
+      const int first = g - win.tile_base, last = min(win.nA + win.nB, first + (g1 - g));
+      if (last <= first) continue;
+      g += last - first;
+      if (!f(win, first, last)) return;
+    }
+  };
+  auto tile_token = [&](const AttnWindow& win, int tile) -> int {
+    return (tile < win.nA ? win.tA0 + tile : win.tB0 + tile - win.nA) * kTok;
+  };
+  auto pad_cols = [&](const AttnWindow& win) -> int { return (win.nrows * G + 15) / 16 * 16; };
+
+  if (warp < kKeyWarps) {
+    // ------------------------------------------------ keys: packed row -> this lane of TMEM
+    auto keys = [&](auto bits_tag) {
+      constexpr int BITS = decltype(bits_tag)::value;
+      constexpr int SPAN = span_bytes(D, BITS);
+      ByteTable<BITS == 5 ? 2 : BITS> table;
+      if constexpr (BITS != 5) table.load(a.k_centroids, a.k_alpha);
+      const uint32_t tab = base + C::kOffTab + lane * 4;
+      const uint32_t row = ring + (uint32_t)((warp * 32 + lane) * SPAN);
+      const uint32_t dst = tmem + ((uint32_t)(32 * warp) << 16) + C::kK;
+      int st = 0, ph = 0, it = 0;
+      for_windows([&](const AttnWindow&, int first, int last) -> bool {
+        for (int t = first; t < last; ++t, ++it) {
+          if (!wait(raw_full(st), ph)) return false;
+          uint32_t wd[D * BITS / 32 + 1];
+          load_row<D, BITS>(row + st * stage_bytes, skip_k >> 2, wd);
+          __syncwarp();
+          if (lane == 0) bar_arrive(raw_empty(st));
+          if (++st == p.ring) st = 0, ph ^= 1;
+          const int b = it & 1;
+          if (!wait(k_empty(b), ((it >> 1) & 1) ^ 1)) return false;
+          tc_after();
+#pragma unroll
+          for (int g = 0; g < D / 32; ++g) {
+            uint32_t o[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x[4];
+              if constexpr (BITS == 5) expand8_5(wd, 4 * g + e, tab, x);
+              else expand8<BITS>(wd, 4 * g + e, table, x);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[4 * e + k] = x[k];
+            }
+            tm_st16(dst + b * C::kKCols + 16 * g, o);
+          }
+          tm_wait_st();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(k_full(b));
+        }
+        return true;
+      });
+    };
+    if (a.k_bits == 4) keys(std::integral_constant<int, 4>{});
+    else if (a.k_bits == 3) keys(std::integral_constant<int, 3>{});
+    else if (a.k_bits == 2) keys(std::integral_constant<int, 2>{});
+    else keys(std::integral_constant<int, 5>{});
+  } else if (warp < kKeyWarps + kValWarps) {
+    // ------------------------------------------------ values: packed row -> swizzled k-line
+    auto values = [&](auto bits_tag) {
+      constexpr int BITS = decltype(bits_tag)::value;
+      constexpr int SPAN = span_bytes(D, BITS);
+      ByteTable<BITS == 5 ? 2 : BITS> table;
+      if constexpr (BITS != 5) table.load(a.v_centroids, a.v_alpha);
+      const uint32_t tab = base + C::kOffTab + 32 * 32 * 4 + lane * 4;
+      const int t = (warp - kKeyWarps) * 32 + lane;
+      const uint32_t row = ring + (uint32_t)(kTok * spk + t * SPAN);
+      const uint32_t line = base + C::kOffV + (uint32_t)((t >> 3) * 1024 + (t & 7) * 128);
+      int st = 0, ph = 0, it = 0;
+      for_windows([&](const AttnWindow&, int first, int last) -> bool {
+        for (int k = first; k < last; ++k, ++it) {
+          if (!wait(raw_full(st), ph)) return false;
+          uint32_t wd[D * BITS / 32 + 1];
+          load_row<D, BITS>(row + st * stage_bytes, skip_v >> 2, wd);
+          __syncwarp();
+          if (lane == 0) bar_arrive(raw_empty(st));
+          if (++st == p.ring) st = 0, ph ^= 1;
+          const int b = it % C::kVBufs;
+          if (!wait(v_empty(b), ((it / C::kVBufs) & 1) ^ 1)) return false;
+          const uint32_t to = line + b * C::kVBytes;
+#pragma unroll
+          for (int g = 0; g < D / 8; ++g) {
+            uint32_t x[4];
+            if constexpr (BITS == 5) expand8_5(wd, g, tab, x);
+            else expand8<BITS>(wd, g, table, x);
+            st_v4(to + (g >> 3) * (kTok * 128) + (((g & 7) ^ (t & 7)) << 4), x[0], x[1], x[2], x[3]);
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(v_full(b));
+        }
+        return true;
+      });
+    };
+    if (a.v_bits == 4) values(std::integral_constant<int, 4>{});
+    else if (a.v_bits == 3) values(std::integral_constant<int, 3>{});
+    else if (a.v_bits == 2) values(std::integral_constant<int, 2>{});
+    else values(std::integral_constant<int, 5>{});
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------ copies of packed rows
+    const int bs = a.block_size, sub = p.sub;
+    const int cap = (int)min((int64_t)a.max_blocks_per_seq * bs, (int64_t)0x7fffff00);
+    uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::kOffMeta);
+    const uint32_t per_copy = (uint32_t)(sub * (spk + spv));
+    int st = 0, ph = 0;
+    int last_ph[kMaxRing];
+#pragma unroll
+    for (int s = 0; s < kMaxRing; ++s) last_ph[s] = -1;
+    for_windows([&](const AttnWindow& win, int first, int last) -> bool {
+      const int32_t* table = a.block_table + (int64_t)win.seq * a.max_blocks_per_seq;
+      const int hi = min(max(win.p_hi, win.w_hi), cap);
+      for (int t = first; t < last; ++t) {
+        const int t0 = tile_token(win, t);
+        if (!wait(raw_empty(st), ph ^ 1)) return false;
+        uint32_t* v = valid + 4 * st;
+        if (lane < 4) v[lane] = 0;
+        __syncwarp();
+        const uint32_t kdst = ring + st * stage_bytes, vdst = kdst + kTok * spk;
+        int live = 0;
+        for (int i0 = 0; i0 < kTok / sub; i0 += 32) {
+          const int i = i0 + lane, tok = t0 + i * sub;
+          int block = -1;
+          if (i < kTok / sub && tok < hi) {
+            block = __ldg(table + tok / bs);
+            if (block < 0 || block >= a.num_blocks) {
+              block = -1;
+              if (a.status) atomicMax(a.status, (int32_t)kBlockOutOfRange);
+            }
+          }
+          if (block >= 0) {
+            if (sub >= 32) {
+              for (int k = 0; k < sub / 32; ++k) v[i * (sub / 32) + k] = 0xffffffffu;
+            } else {
+              atomicOr(v + ((i * sub) >> 5), ((1u << sub) - 1u) << ((i * sub) & 31));
+            }
+          }
+          if (p.tma) {
+            const unsigned m = __ballot_sync(kFullMask, block >= 0);
+            live += __popc(m);
+            // the transactions of this round are announced before its copies start
+            if (lane == 0 && m) {
+              asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(raw_full(st)),
+                           "r"((uint32_t)__popc(m) * per_copy)
+                           : "memory");
+            }
+            __syncwarp();
+            if (block >= 0) {
+              const int y = (int)((int64_t)block * bs + tok % bs);
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+                  "[%4];\n" ::"r"(kdst + i * sub * spk),
+                  "l"(&kmap), "r"(h * rbk - skip_k), "r"(y), "r"(raw_full(st))
+                  : "memory");
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+                  "[%4];\n" ::"r"(vdst + i * sub * spv),
+                  "l"(&vmap), "r"(h * rbv - skip_v), "r"(y), "r"(raw_full(st))
+                  : "memory");
+            }
+          } else {
+            // word by word; the rows of a round's copies are taken one after another by the warp
+            for (int k = 0; k < min(32, kTok / sub - i0); ++k) {
+              const int bk = __shfl_sync(kFullMask, block, k);
+              if (bk < 0) continue;
+              const int tk = t0 + (i0 + k) * sub;
+              const int64_t slot = (int64_t)bk * bs + tk % bs;
+              const int wk = rbk / 4, wv = rbv / 4, per = wk + wv;
+              for (int x = lane; x < sub * per; x += 32) {
+                const int r = x / per, c = x % per;
+                const int64_t line = (slot + r) * H + h;
+                const uint8_t* src = c < wk ? a.k_pages + line * rbk + 4 * c : a.v_pages + line * rbv + 4 * (c - wk);
+                const uint32_t dst = c < wk ? kdst + ((i0 + k) * sub + r) * spk + 4 * c
+                                            : vdst + ((i0 + k) * sub + r) * spv + 4 * (c - wk);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (!p.tma) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(raw_full(st)) : "memory");
+        if (lane == 0) bar_arrive(raw_full(st));
+#pragma unroll
+        for (int s = 0; s < kMaxRing; ++s)
+          if (s == st) last_ph[s] = ph;
+        if (++st == p.ring) st = 0, ph ^= 1;
+      }
+      return true;
+    });
+    if (!p.tma) asm volatile("cp.async.wait_all;\n" ::: "memory");
+    // none of the copies outlives the loop
+#pragma unroll
+    for (int s = 0; s < kMaxRing; ++s)
+      if (last_ph[s] >= 0)
+        for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(raw_full(s), last_ph[s]); ++i) {
+        }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const uint32_t q_at = base + C::kOffQ, v_at = base + C::kOffV, p_at = base + C::kOffP;
+      int it = 0, unit = 0;
+      bool issued = false;
+      for_windows([&](const AttnWindow& win, int first, int last) -> bool {
+        const int n = SPLIT ? 2 * pad_cols(win) : pad_cols(win);
+        const uint32_t ids = mma_idesc(n, false), idp = mma_idesc(n, true);
+        if (!wait1(q_full, unit & 1)) return false;
+        ++unit;
+        auto weigh = [&](int j, bool acc) -> bool {  // O^T += V^T P^T of tile j
+          const int b = j % C::kVBufs;
+          if (!wait1(p_full, j & 1) || !wait1(v_full(b), (j / C::kVBufs) & 1)) return false;
+          tc_after();
+#pragma unroll
+          for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+            for (int ks = 0; ks < kTok / 16; ++ks)
+              mma_ss(tmem + C::kO + hf * C::kN,
+                     sw128_desc(v_at + b * C::kVBytes + hf * 2 * kTok * 128 + ks * 2048, D == 64 ? 0 : kTok * 128, 1024),
+                     sw128_desc(p_at + ks * 2048, kTok * 128, 1024), idp, acc || ks > 0);
+          tc_commit(v_empty(b));
+          tc_commit(p_empty);
+          return true;
+        };
+        for (int t = first; t < last; ++t, ++it) {
+          const int b = it & 1;
+          if (!wait1(k_full(b), (it >> 1) & 1) || !wait1(s_empty(b), ((it >> 1) & 1) ^ 1)) return false;
+          tc_after();
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ts(tmem + C::kS + b * C::kN, tmem + C::kK + b * C::kKCols + ks * 8,
+                   sw128_desc(q_at + (ks >> 2) * (C::kN * 128) + (ks & 3) * 32, 16, 1024), ids, ks > 0);
+          issued = true;
+          tc_commit(s_full(b));
+          tc_commit(k_empty(b));
+          if (t > first && !weigh(it - 1, t - 1 > first)) return false;
+        }
+        return weigh(it - 1, last - 1 > first);
+      });
+      if (issued) {  // every MMA has finished before TMEM is freed
+        tc_commit(drained);
+        for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(drained, 0); ++i) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ softmax, queries and outputs
+    const int sw = warp - kKeyWarps - kValWarps;  // softmax warp
+    const int quad = warp & 3, set = sw >> 2;
+    const int stid = tid - 32 * (kKeyWarps + kValWarps);
+    const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
+    RowView* rows = reinterpret_cast<RowView*>(smem + C::kOffRows);
+    float* m_s = reinterpret_cast<float*>(smem + C::kOffCol);
+    float* slope_s = m_s + C::kN;
+    float* part_s = slope_s + C::kN;  // [4][kN]
+    const uint32_t* valid = reinterpret_cast<const uint32_t*>(smem + C::kOffMeta);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t krow = ring + (uint32_t)(t_lane * spk + skip_k + rbk - 4);
+    const uint32_t vrow = ring + (uint32_t)(kTok * spk + t_lane * spv + skip_v + rbv - 4);
+    const uint32_t p_line = base + C::kOffP + (uint32_t)((t_lane >> 3) * 1024 + (t_lane & 7) * 128);
+    const float scale = a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)D);
+    const bool capped = a.softcap > 0.f, biased = a.alibi != nullptr;
+    // capped scores: tanh(s / cap) from 2^(2 log2(e) s / cap)
+    const float qmul = (capped ? 2.f * scale / a.softcap : scale) * kLog2eA / (sqrtf((float)D) * a.k_alpha);
+    const float cap2 = a.softcap * kLog2eA;
+    const float inv_av = 1.0f / a.v_alpha;
+    int st = 0, ph = 0, it = 0;
+
+    for_windows([&](const AttnWindow& win, int first, int last) -> bool {
+      const int cols = win.nrows * G, padded = pad_cols(win);
+      const int lo_col = SPLIT ? padded : 0;
+      // ---- queries of the window: one power of two for all of them, rotated, hi (and lo)
+      if (stid == 0) {
+        full_lo = pre_lo = 0;
+        full_hi = pre_hi = 0x7fffffff;
+        q_exp = -1000;
+      }
+      soft_sync();
+      if (stid < win.nrows) {
+        const RowView v = row_view(a, win.row0 + stid);
+        rows[stid] = v;
+        atomicMax(&full_lo, v.w0);
+        atomicMin(&full_hi, v.w1);
+        atomicMax(&pre_lo, v.p0);
+        atomicMin(&pre_hi, v.p1);
+      }
+      if (stid < C::kN) {
+        m_s[stid] = stid < cols ? -INFINITY : INFINITY;  // no column there: never a new max
+        slope_s[stid] = biased && stid < cols ? a.alibi[h * G + stid % G] * kLog2eA : 0.f;
+      }
+      auto q_row = [&](int col, float (&v)[D / 32]) {
+        const int64_t at = ((int64_t)(win.row0 + col / G) * a.num_q_heads + h * G + col % G) * D + lane * (D / 32);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) v[i] = load_as_f32(a.q, at + i, a.q_dtype);
+      };
+      float most = 0.f;
+      for (int col = sw; col < cols; col += kSoftWarps) {
+        float v[D / 32], ss = 0.f;
+        q_row(col, v);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) ss = fmaf(v[i] * qmul, v[i] * qmul, ss);
+        ss = warp_sum(ss);
+        if (ss < INFINITY) most = fmaxf(most, ss);
+      }
+      if (lane == 0) atomicMax(&q_exp, (exp_of(most) + 1) / 2);
+      soft_sync();
+      // the largest rotated coordinate is at most the norm times sqrt(D): to 2^11 or less
+      const int qe = q_exp + (D == 64 ? 3 : 4) - 10;
+      const float q_down = pow2i(max(-126, min(126, -qe))), q_up = pow2i(max(-126, min(126, qe)));
+      for (int col = sw; col < cols; col += kSoftWarps) {
+        float v[D / 32];
+        q_row(col, v);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) v[i] *= qmul * a.signs[lane * (D / 32) + i];
+        fwht_warp<D / 32>(v);
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) {
+          const int d = lane * (D / 32) + i;
+          const float x0 = v[i] * q_down, x1 = v[i + 1] * q_down;
+          const uint32_t hi = pack2(x0, x1);
+          const uint32_t at = (uint32_t)((d >> 6) * (C::kN * 128) + (((d & 63) * 2) & 15));
+          const uint32_t ch = (uint32_t)((d & 63) >> 3);
+          *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + col * 128 + ((ch ^ (col & 7)) << 4)) = hi;
+          if constexpr (SPLIT) {
+            const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
+            const int lc = col + lo_col;
+            *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + lc * 128 + ((ch ^ (lc & 7)) << 4)) =
+                pack2((x0 - __low2float(hh)) * kLoQ, (x1 - __high2float(hh)) * kLoQ);
+          }
+        }
+      }
+      fence_async();
+      soft_sync();
+      if (lane == 0) bar_arrive(q_full);
+
+      // ---- tiles
+      const int hi_tok = max(win.p_hi, win.w_hi);
+      float l[C::kGroups * 8];
+#pragma unroll
+      for (int i = 0; i < C::kGroups * 8; ++i) l[i] = 0.f;
+      int ve = -1000;  // P' = p nu_v 2^-ve (every thread holds the same)
+      for (int t = first; t < last; ++t, ++it) {
+        const int t0 = tile_token(win, t), tok = t0 + t_lane;
+        bool ok = wait(raw_full(st), ph);
+        const float kn = __uint_as_float(ld_s32(krow + st * stage_bytes)) * q_up;
+        const float vn = __uint_as_float(ld_s32(vrow + st * stage_bytes));
+        const uint32_t v0 = valid[4 * st], v1 = valid[4 * st + 1], v2 = valid[4 * st + 2], v3 = valid[4 * st + 3];
+        const uint32_t vq = quad == 0 ? v0 : quad == 1 ? v1 : quad == 2 ? v2 : v3;
+        const bool real = ((vq >> lane) & 1u) && tok < hi_tok;
+        const bool all = (v0 & v1 & v2 & v3) == 0xffffffffu && ((t0 >= full_lo && t0 + kTok <= full_hi) ||
+                                                                 (t0 >= pre_lo && t0 + kTok <= pre_hi));
+        __syncwarp();
+        if (lane == 0) bar_arrive(raw_empty(st));
+        if (++st == p.ring) st = 0, ph ^= 1;
+        // which of this thread's columns see its token (bit 8 g + i: column 16 g + 8 set + i)
+        uint64_t see = ~0ull;
+        if (!all) {
+          see = 0;
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = 16 * g + 8 * set;
+            if (c0 >= cols) continue;
+            const int r0 = c0 / G, step = min(G, 8);
+            for (int k = 0; k < 8 / step; ++k) {
+              const int r = r0 + k;
+              if (r >= win.nrows || !real) continue;
+              if (row_sees(rows[r], a.mask ? a.mask + (int64_t)(win.row0 + r) * a.mask_words : nullptr, tok))
+                see |= (uint64_t)((1u << step) - 1u) << (8 * g + k * step);
+            }
+          }
+        }
+        // a norm that counts for the weights' scale: of a token some column here sees (a stale
+        // row may hold any bits), finite
+        const float vf = real && see != 0 && fabsf(vn) < INFINITY ? fabsf(vn) : 0.f;
+        const int sb = it & 1;
+        ok = wait(s_full(sb), (it >> 1) & 1) && ok;
+        tc_after();
+        const uint32_t s_at = lanes + C::kS + sb * C::kN + 8 * set;
+        // scores of group g (log2 units), -inf where the token is not seen
+        auto scores = [&](int g, float (&x)[8]) {
+          uint32_t u[8], v[8];
+          tm_ld8(s_at + 16 * g, u);
+          if constexpr (SPLIT) tm_ld8(s_at + lo_col + 16 * g, v);
+          tm_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = __uint_as_float(u[i]);
+            if constexpr (SPLIT) x[i] = fmaf(__uint_as_float(v[i]), 1.0f / kLoQ, x[i]);
+            x[i] *= kn;
+            if (capped) x[i] = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i])), cap2);
+          }
+          if (biased) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = 16 * g + 8 * set + i;
+              if (c < cols) x[i] -= slope_s[c] * fabsf((float)(a.q_len[win.row0 + c / G] - 1 - tok));
+            }
+          }
+          if (!all) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (!((see >> (8 * g + i)) & 1u)) x[i] = -INFINITY;
+          }
+        };
+        // ---- does a column's max move by more than the slack, or the weights' scale?
+        float over = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+          const int c0 = 16 * g + 8 * set;
+          if (c0 >= cols) continue;
+          float x[8];
+          scores(g, x);
+          const float4 ma = *reinterpret_cast<const float4*>(m_s + c0), mb = *reinterpret_cast<const float4*>(m_s + c0 + 4);
+          const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) over = fmaxf(over, x[i] - mm[i]);
+        }
+        const bool grow = vf > 0.f && exp_of(vf) - ve > 9;
+        ok = wait(p_empty, (it & 1) ^ 1) && ok;  // the product of the tile before is done: P and O are free
+        if (!ok) *(volatile int*)&fail[it & 1] = 1;
+        const bool move = soft_any(over > kSlack || grow);
+        if (*(volatile int*)&fail[it & 1]) return false;  // the same for all softmax warps
+        tc_after();
+        if (move) {
+          // new maxima per column over the four lane quadrants, then the scale of the values
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = 16 * g + 8 * set;
+            if (c0 >= cols) continue;
+            float x[8];
+            scores(g, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int top = __reduce_max_sync(kFullMask, ord_int(x[i]));
+              if (lane == 0) part_s[quad * C::kN + c0 + i] = ord_float(top);
+            }
+          }
+          const int vmax = __reduce_max_sync(kFullMask, __float_as_int(vf));
+          __shared__ int vpart[kSoftWarps];
+          if (lane == 0) vpart[sw] = vmax;
+          soft_sync();
+          int vall = 0;
+#pragma unroll
+          for (int k = 0; k < kSoftWarps; ++k) vall = max(vall, vpart[k]);
+          float vscale = 1.f;
+          if (vall > 0) {
+            const int e = exp_of(__int_as_float(vall));
+            if (e - ve > 9) {  // the largest norm so far to 2^6
+              const int ne = e - 6;
+              vscale = ve == -1000 ? 1.f : pow2i(max(-126, ve - ne));
+              ve = ne;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = 16 * g + 8 * set;
+            if (c0 >= cols) continue;
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float top = part_s[c0 + i];
+#pragma unroll
+              for (int k = 1; k < 4; ++k) top = fmaxf(top, part_s[k * C::kN + c0 + i]);
+              const float old = m_s[c0 + i];
+              const float corr = top > old + kSlack ? ex2a(old - top) : 1.f;
+              l[8 * g + i] *= corr;
+              f[i] = corr * vscale;
+            }
+            if (t > first) {
+#pragma unroll
+              for (int part2 = 0; part2 < (SPLIT ? 2 : 1) * C::kHalves; ++part2) {
+                const uint32_t at = lanes + C::kO + (part2 / (SPLIT ? 2 : 1)) * C::kN + (SPLIT && part2 % 2 ? lo_col : 0) + c0;
+                uint32_t u[8];
+                tm_ld8(at, u);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f[i]);
+                tm_st8(at, u);
+              }
+              tm_wait_st();
+            }
+          }
+          soft_sync();
+          if (stid < cols) {
+            float top = part_s[stid];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) top = fmaxf(top, part_s[k * C::kN + stid]);
+            if (top > m_s[stid] + kSlack) m_s[stid] = top;
+          }
+          soft_sync();
+        }
+        // ---- weights
+        const float vs = vn * pow2i(max(-126, min(126, -ve)));
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+          const int c0 = 16 * g + 8 * set;
+          if (c0 >= cols) continue;
+          float x[8];
+          scores(g, x);
+          const float4 ma = *reinterpret_cast<const float4*>(m_s + c0), mb = *reinterpret_cast<const float4*>(m_s + c0 + 4);
+          const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float pr = ex2a(x[i] - (mm[i] == -INFINITY ? 0.f : mm[i]));
+            l[8 * g + i] += pr;
+            y[i] = all || pr != 0.f ? pr * vs : 0.f;
+          }
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = pack2(y[2 * i], y[2 * i + 1]);
+          const uint32_t sx = (uint32_t)(t_lane & 7);
+          st_v4(p_line + (c0 >> 6) * (kTok * 128) + ((((c0 & 63) >> 3) ^ sx) << 4), o[0], o[1], o[2], o[3]);
+          if constexpr (SPLIT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __half2 hh = *reinterpret_cast<const __half2*>(&o[i]);
+              o[i] = pack2((y[2 * i] - __low2float(hh)) * kLoP, (y[2 * i + 1] - __high2float(hh)) * kLoP);
+            }
+            const int c1 = c0 + lo_col;
+            st_v4(p_line + (c1 >> 6) * (kTok * 128) + ((((c1 & 63) >> 3) ^ sx) << 4), o[0], o[1], o[2], o[3]);
+          }
+        }
+        fence_async();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(s_empty(sb));
+          bar_arrive(p_full);
+        }
+      }
+
+      // ---- outputs of the window
+      const bool ok = wait(p_empty, (it - 1) & 1);
+      if (!ok) *(volatile int*)&fail[it & 1] = 1;
+      // sums over the 128 lanes
+#pragma unroll
+      for (int g = 0; g < C::kGroups; ++g) {
+        const int c0 = 16 * g + 8 * set;
+        if (c0 >= cols) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float s = warp_sum(l[8 * g + i]);
+          if (lane == 0) part_s[quad * C::kN + c0 + i] = s;
+        }
+      }
+      soft_sync();
+      if (*(volatile int*)&fail[it & 1]) return false;
+      tc_after();
+      const bool whole = first == 0 && last == win.nA + win.nB;
+      const float up = pow2i(max(-126, min(126, ve == -1000 ? 0 : ve))) * inv_av;
+      auto sum_of = [&](int c) -> float {
+        return (part_s[c] + part_s[C::kN + c]) + (part_s[2 * C::kN + c] + part_s[3 * C::kN + c]);
+      };
+      // this lane's dim of columns c0 .. c0 + 7 (half hf of the dims)
+      auto load_o = [&](int hf, int c0, float (&x)[8]) {
+        uint32_t u[8], v[8];
+        tm_ld8(lanes + C::kO + hf * C::kN + c0, u);
+        if constexpr (SPLIT) tm_ld8(lanes + C::kO + hf * C::kN + lo_col + c0, v);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = __uint_as_float(u[i]);
+          if constexpr (SPLIT) x[i] = fmaf(__uint_as_float(v[i]), 1.0f / kLoP, x[i]);
+          x[i] *= up;
+        }
+      };
+      const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * w.cols;
+      if (!whole) {
+        if (stid < cols) {
+          w.ml[2 * (slot0 + stid)] = m_s[stid];
+          w.ml[2 * (slot0 + stid) + 1] = sum_of(stid);
+        }
+        for (int c0 = 8 * set; c0 < cols; c0 += 16)
+#pragma unroll
+          for (int hf = 0; hf < C::kHalves; ++hf) {
+            float x[8];
+            load_o(hf, c0, x);
+            if (D == 64 && quad >= 2) continue;  // lanes 64.. repeat the 64 dims
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c0 + i < cols) w.acc[(slot0 + c0 + i) * D + hf * 128 + t_lane] = x[i];
+          }
+      } else {
+        float* stage = reinterpret_cast<float*>(smem + C::kOffP);  // [kStageCols][D]
+        for (int r0 = 0; r0 < cols; r0 += C::kStageCols) {
+          const int r1 = min(cols, r0 + C::kStageCols);
+          for (int c0 = r0 + 8 * set; c0 < r1; c0 += 16)
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf) {
+              float x[8];
+              load_o(hf, c0, x);
+              if (D == 64 && quad >= 2) continue;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c0 + i < r1) stage[(c0 + i - r0) * D + hf * 128 + t_lane] = x[i];
+            }
+          soft_sync();
+          for (int c = r0 + sw; c < r1; c += kSoftWarps) {
+            float v[D / 32];
+            const float s = sum_of(c);
+            const float inv = s != 0.f ? 1.f / (s * sqrtf((float)D)) : 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) v[i] = stage[(c - r0) * D + lane * (D / 32) + i] * inv;
+            fwht_warp<D / 32>(v);
+            const int64_t at = ((int64_t)(win.row0 + c / G) * a.num_q_heads + h * G + c % G) * D + lane * (D / 32);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              store_from_f32(a.out, at + i, a.out_dtype, v[i] * a.signs[lane * (D / 32) + i]);
+          }
+          soft_sync();
+        }
+      }
+      tc_before();
+      soft_sync();  // the arrays and O are free for the next window
+      return true;
+    });
+  }
+
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+}
+
+// ---------------------------------------------------------------- launch
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// The pages as a 2-D byte tensor [num_blocks * block_size][slab] with boxes of `sub` rows x `span`.
+bool page_map(CUtensorMap* map, const uint8_t* pages, int64_t rows, int64_t slab, int span, int sub) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)slab, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)slab};
+  const cuuint32_t box[2] = {(cuuint32_t)span, (cuuint32_t)sub};
+  const cuuint32_t step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pages), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
+  using C = Tc<D, SPLIT>;
+  TcAttnArgs t{};
+  t.a = a;
+  t.w = w;
+  t.tries = wait_tries();
+  int sub = 1;
+  while (sub < kTok && a.block_size % (2 * sub) == 0) sub *= 2;
+  t.sub = sub;
+  const int64_t ks = (int64_t)a.num_kv_heads * (D * a.k_bits / 8 + 4), vs = (int64_t)a.num_kv_heads * (D * a.v_bits / 8 + 4);
+  const int spk = span_bytes(D, a.k_bits), spv = span_bytes(D, a.v_bits);
+  const int64_t slots = a.num_blocks * a.block_size;
+  CUtensorMap km{}, vm{};
+  // TMA: slabs of whole 16 bytes, boxes that start on 128 bytes of the ring (8 rows of an odd
+  // number of 16 bytes), and slot numbers that a 32-bit coordinate holds
+  t.tma = sub >= 8 && ks % 16 == 0 && vs % 16 == 0 && slots > 0 && slots < 0x7fffffffLL &&
+          page_map(&km, a.k_pages, slots, ks, spk, sub) && page_map(&vm, a.v_pages, slots, vs, spv, sub);
+  constexpr int limit = 227 * 1024 - 2048;  // the static arrays take their part
+  const int stage = kTok * (spk + spv);
+  t.ring = std::min(kMaxRing, (limit - 1024 - C::kOffRing) / stage);
+  if (t.ring < 2) return cudaErrorInvalidValue;
+  const int smem = 1024 + C::kOffRing + t.ring * stage;
+  auto kern = attn_tc_kernel<D, SPLIT>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(w.parts * a.num_kv_heads);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, kern, t, km, vm);
+  if (err == cudaSuccess) count_launches(1);
+  return err;
+}
+
+}  // namespace
+
+bool attn_tc_supported(const AttnArgs& a) {
+  return (a.head_dim == 64 || a.head_dim == 128 || a.head_dim == 256) && (a.out_dtype == kF16 || a.out_dtype == kBF16);
+}
+
+int attn_tc_cols(const AttnArgs& a) {
+  const bool split = a.out_dtype == kF16;
+  if (a.head_dim == 64) return split ? Tc<64, true>::kCols : Tc<64, false>::kCols;
+  if (a.head_dim == 128) return split ? Tc<128, true>::kCols : Tc<128, false>::kCols;
+  return split ? Tc<256, true>::kCols : Tc<256, false>::kCols;
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
+  const bool split = a.out_dtype == kF16;
+  if (a.head_dim == 64) return split ? launch_tc<64, true>(a, w, stream) : launch_tc<64, false>(a, w, stream);
+  if (a.head_dim == 128) return split ? launch_tc<128, true>(a, w, stream) : launch_tc<128, false>(a, w, stream);
+  return split ? launch_tc<256, true>(a, w, stream) : launch_tc<256, false>(a, w, stream);
+}
+
+}  // namespace tq
