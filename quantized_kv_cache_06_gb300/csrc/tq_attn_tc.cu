@@ -28,7 +28,7 @@
 // (the product before has completed by then).
 //
 // Roles of the 18 warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, two
-// sets that take alternate groups of eight columns), 16 copies, 17 MMA issue.  Packed rows
+// sets that take alternate groups of 16 columns), 16 copies, 17 MMA issue.  Packed rows
 // arrive by TMA: the pages seen as a 2-D byte tensor [slots][H row_bytes], a box of up to 128
 // rows x the 16-byte aligned span around the head's bytes, so a block of a page is one copy.
 // Rows whose slab is not a multiple of 16 bytes (H not a multiple of 4) come by 4-byte
@@ -66,7 +66,7 @@ template <int D, bool SPLIT>
 struct Tc {
   static constexpr int kN = D == 256 ? 64 : 128;         // MMA columns at most
   static constexpr int kCols = SPLIT ? kN / 2 : kN;      // window columns at most
-  static constexpr int kGroups = kCols / 16;             // groups of 8 columns per softmax thread
+  static constexpr int kGroups = (kCols + 31) / 32;      // groups of 16 columns per softmax thread
   static constexpr int kHalves = D == 256 ? 2 : 1;       // 128-dim halves of O^T
   static constexpr int kKCols = D / 2;                   // TMEM columns of a key tile
   static constexpr int kVBufs = D == 256 ? 1 : 2;
@@ -83,8 +83,9 @@ struct Tc {
   static constexpr int kOffV = kOffQ + kQBytes;
   static constexpr int kOffP = kOffV + kVBufs * kVBytes;
   static constexpr int kOffRows = kOffP + kPBytes;                 // RowView[kCols]
-  static constexpr int kOffCol = kOffRows + kCols * (int)sizeof(RowView);  // float m[kN], slope[kN], part[4][kN]
-  static constexpr int kOffTab = kOffCol + 6 * kN * 4;              // 5-bit tables, 2 x 32 x 32 words
+  // floats: -max, max (0 while there is none), correction, slope [kN], part [4][kN]; int position [kN]
+  static constexpr int kOffCol = kOffRows + kCols * (int)sizeof(RowView);
+  static constexpr int kOffTab = kOffCol + 9 * kN * 4;              // 5-bit tables, 2 x 32 x 32 words
   static constexpr int kOffMeta = kOffTab + 2 * 32 * 32 * 4;        // uint32 valid[kMaxRing][4]
   static constexpr int kOffRing = (kOffMeta + kMaxRing * 16 + 127) / 128 * 128;
   static constexpr int kStageCols = kPBytes / (D * 4);              // output columns staged at a time
@@ -153,16 +154,13 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint
 __device__ __forceinline__ uint32_t mma_idesc(int n, bool mn) {
   return (1u << 4) | (mn ? (1u << 15) | (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-__device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&v)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(addr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -196,6 +194,31 @@ __device__ __forceinline__ float rcpa(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+// Pairs of fp32 in one instruction.
+union F2 {
+  float2 f;
+  uint64_t u;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  r.f = make_float2(x, y);
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -246,22 +269,20 @@ struct ByteTable {
   }
 };
 
-// Eight consecutive coordinates (group g of the row's words) as four fp16 pairs.
+// Eight consecutive coordinates (group g of the words) as four fp16 pairs.
 template <int BITS>
 __device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTable<BITS>& t, uint32_t (&out)[4]) {
   uint32_t sel;  // eight selector nibbles
-  uint32_t x;
   if constexpr (BITS == 4) {
-    x = w[g];
-    sel = x & 0x77777777u;
+    sel = w[g] & 0x77777777u;
   } else if constexpr (BITS == 3) {
     const int bit = 24 * g, i = bit >> 5, sh = bit & 31;
-    x = sh <= 8 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh);
+    uint32_t x = sh <= 8 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh);
     x = (x & 0x00000fffu) | ((x << 4) & 0x0fff0000u);
     x = (x & 0x003f003fu) | ((x << 2) & 0x3f003f00u);
     sel = (x & 0x07070707u) | ((x << 1) & 0x70707070u);
   } else {
-    x = g & 1 ? w[g >> 1] >> 16 : w[g >> 1] & 0xffffu;
+    uint32_t x = g & 1 ? w[g >> 1] >> 16 : w[g >> 1] & 0xffffu;
     x = (x | (x << 8)) & 0x00ff00ffu;
     x = (x | (x << 4)) & 0x0f0f0f0fu;
     sel = (x | (x << 2)) & 0x33333333u;
@@ -272,9 +293,10 @@ __device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTabl
     uint32_t lo = __byte_perm(t.lo[0], t.lo[1], s), hi = __byte_perm(t.hi[0], t.hi[1], s);
     if constexpr (BITS == 4) {
       // bytes 0xff where bit 3 of the index is set (the sign-replicating selector form)
-      const uint32_t y = k ? x >> 16 : x;
+      const uint32_t z = w[g] << 4;
       uint32_t m;
-      asm("prmt.b32 %0, %1, %2, 0xd9c8;\n" : "=r"(m) : "r"(y << 4), "r"(y));
+      if (k == 0) asm("prmt.b32 %0, %1, %2, 0xd9c8;\n" : "=r"(m) : "r"(z), "r"(w[g]));
+      else asm("prmt.b32 %0, %1, %2, 0xfbea;\n" : "=r"(m) : "r"(z), "r"(w[g]));
       lo = (lo & ~m) | (__byte_perm(t.lo[2], t.lo[3], s) & m);
       hi = (hi & ~m) | (__byte_perm(t.hi[2], t.hi[3], s) & m);
     }
@@ -294,6 +316,23 @@ __device__ __forceinline__ void expand8_5(const uint32_t* w, int g, uint32_t tab
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) out[k] = __byte_perm(v[2 * k], v[2 * k + 1], 0x5410);
+}
+
+// 32 consecutive coordinates from the first BITS words of w; the words move up, so that a loop
+// over a row stays rolled (the roles share the instruction cache) with the row in registers.
+template <int BITS, int NW>
+__device__ __forceinline__ void expand32(uint32_t (&w)[NW], const ByteTable<BITS == 5 ? 2 : BITS>& t, uint32_t tab_lane,
+                                         uint32_t (&out)[16]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t x[4];
+    if constexpr (BITS == 5) expand8_5(w, g, tab_lane, x);
+    else expand8<BITS>(w, g, t, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[4 * g + k] = x[k];
+  }
+#pragma unroll
+  for (int i = 0; i + BITS < NW; ++i) w[i] = w[i + BITS];
 }
 
 // The row of this thread's token in the ring: SPAN bytes, of which the row starts `skip` words in.
@@ -455,17 +494,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int b = it & 1;
           if (!wait(k_empty(b), ((it >> 1) & 1) ^ 1)) return false;
           tc_after();
-#pragma unroll
+#pragma unroll 1
           for (int g = 0; g < D / 32; ++g) {
             uint32_t o[16];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t x[4];
-              if constexpr (BITS == 5) expand8_5(wd, 4 * g + e, tab, x);
-              else expand8<BITS>(wd, 4 * g + e, table, x);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[4 * e + k] = x[k];
-            }
+            expand32<BITS>(wd, table, tab, o);
             tm_st16(dst + b * C::kKCols + 16 * g, o);
           }
           tm_wait_st();
@@ -503,12 +535,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int b = it % C::kVBufs;
           if (!wait(v_empty(b), ((it / C::kVBufs) & 1) ^ 1)) return false;
           const uint32_t to = line + b * C::kVBytes;
+#pragma unroll 1
+          for (int g = 0; g < D / 32; ++g) {
+            uint32_t o[16];
+            expand32<BITS>(wd, table, tab, o);
+            const uint32_t at = to + (g >> 1) * (kTok * 128) + (((uint32_t)(t & 7) ^ (uint32_t)(4 * (g & 1))) << 4);
 #pragma unroll
-          for (int g = 0; g < D / 8; ++g) {
-            uint32_t x[4];
-            if constexpr (BITS == 5) expand8_5(wd, g, tab, x);
-            else expand8<BITS>(wd, g, table, x);
-            st_v4(to + (g >> 3) * (kTok * 128) + (((g & 7) ^ (t & 7)) << 4), x[0], x[1], x[2], x[3]);
+            for (int e = 0; e < 4; ++e)
+              st_v4(at ^ (uint32_t)(e << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           fence_async();
           __syncwarp();
@@ -673,9 +707,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int stid = tid - 32 * (kKeyWarps + kValWarps);
     const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
     RowView* rows = reinterpret_cast<RowView*>(smem + C::kOffRows);
-    float* m_s = reinterpret_cast<float*>(smem + C::kOffCol);
-    float* slope_s = m_s + C::kN;
-    float* part_s = slope_s + C::kN;  // [4][kN]
+    float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -max; -inf where there is no column
+    float* mu_s = negm_s + C::kN;   // the same, 0 while a column has seen nothing
+    float* corr_s = mu_s + C::kN;
+    float* slope_s = corr_s + C::kN;
+    int* pos_s = reinterpret_cast<int*>(slope_s + C::kN);
+    float* part_s = slope_s + 2 * C::kN;  // [4][kN]
+    __shared__ int vpart[kSoftWarps];
     const uint32_t* valid = reinterpret_cast<const uint32_t*>(smem + C::kOffMeta);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t krow = ring + (uint32_t)(t_lane * spk + skip_k + rbk - 4);
@@ -708,8 +746,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         atomicMin(&pre_hi, v.p1);
       }
       if (stid < C::kN) {
-        m_s[stid] = stid < cols ? -INFINITY : INFINITY;  // no column there: never a new max
+        negm_s[stid] = stid < cols ? INFINITY : -INFINITY;  // no column there: never a new max
+        mu_s[stid] = stid < cols ? 0.f : -INFINITY;
         slope_s[stid] = biased && stid < cols ? a.alibi[h * G + stid % G] * kLog2eA : 0.f;
+        pos_s[stid] = a.q_len && stid < cols ? a.q_len[win.row0 + stid / G] - 1 : 0;
       }
       auto q_row = [&](int col, float (&v)[D / 32]) {
         const int64_t at = ((int64_t)(win.row0 + col / G) * a.num_q_heads + h * G + col % G) * D + lane * (D / 32);
@@ -758,85 +798,112 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
       // ---- tiles
       const int hi_tok = max(win.p_hi, win.w_hi);
-      float l[C::kGroups * 8];
+      F2 l[C::kGroups * 8];
 #pragma unroll
-      for (int i = 0; i < C::kGroups * 8; ++i) l[i] = 0.f;
+      for (int i = 0; i < C::kGroups * 8; ++i) l[i] = f2(0.f, 0.f);
       int ve = -1000;  // P' = p nu_v 2^-ve (every thread holds the same)
       for (int t = first; t < last; ++t, ++it) {
         const int t0 = tile_token(win, t), tok = t0 + t_lane;
         bool ok = wait(raw_full(st), ph);
-        const float kn = __uint_as_float(ld_s32(krow + st * stage_bytes)) * q_up;
+        float kn = __uint_as_float(ld_s32(krow + st * stage_bytes)) * q_up;
         const float vn = __uint_as_float(ld_s32(vrow + st * stage_bytes));
-        const uint32_t v0 = valid[4 * st], v1 = valid[4 * st + 1], v2 = valid[4 * st + 2], v3 = valid[4 * st + 3];
-        const uint32_t vq = quad == 0 ? v0 : quad == 1 ? v1 : quad == 2 ? v2 : v3;
+        const uint4 vv = *reinterpret_cast<const uint4*>(valid + 4 * st);
+        const uint32_t vq = quad == 0 ? vv.x : quad == 1 ? vv.y : quad == 2 ? vv.z : vv.w;
         const bool real = ((vq >> lane) & 1u) && tok < hi_tok;
-        const bool all = (v0 & v1 & v2 & v3) == 0xffffffffu && ((t0 >= full_lo && t0 + kTok <= full_hi) ||
-                                                                 (t0 >= pre_lo && t0 + kTok <= pre_hi));
+        const bool all = (vv.x & vv.y & vv.z & vv.w) == 0xffffffffu && ((t0 >= full_lo && t0 + kTok <= full_hi) ||
+                                                                         (t0 >= pre_lo && t0 + kTok <= pre_hi));
         __syncwarp();
         if (lane == 0) bar_arrive(raw_empty(st));
         if (++st == p.ring) st = 0, ph ^= 1;
-        // which of this thread's columns see its token (bit 8 g + i: column 16 g + 8 set + i)
-        uint64_t see = ~0ull;
-        if (!all) {
-          see = 0;
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const int c0 = 16 * g + 8 * set;
-            if (c0 >= cols) continue;
-            const int r0 = c0 / G, step = min(G, 8);
-            for (int k = 0; k < 8 / step; ++k) {
-              const int r = r0 + k;
-              if (r >= win.nrows || !real) continue;
-              if (row_sees(rows[r], a.mask ? a.mask + (int64_t)(win.row0 + r) * a.mask_words : nullptr, tok))
-                see |= (uint64_t)((1u << step) - 1u) << (8 * g + k * step);
-            }
-          }
-        }
-        // a norm that counts for the weights' scale: of a token some column here sees (a stale
-        // row may hold any bits), finite
-        const float vf = real && see != 0 && fabsf(vn) < INFINITY ? fabsf(vn) : 0.f;
         const int sb = it & 1;
+        const uint32_t s_at = lanes + C::kS + sb * C::kN;
         ok = wait(s_full(sb), (it >> 1) & 1) && ok;
         tc_after();
-        const uint32_t s_at = lanes + C::kS + sb * C::kN + 8 * set;
-        // scores of group g (log2 units), -inf where the token is not seen
-        auto scores = [&](int g, float (&x)[8]) {
-          uint32_t u[8], v[8];
-          tm_ld8(s_at + 16 * g, u);
-          if constexpr (SPLIT) tm_ld8(s_at + lo_col + 16 * g, v);
-          tm_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = __uint_as_float(u[i]);
-            if constexpr (SPLIT) x[i] = fmaf(__uint_as_float(v[i]), 1.0f / kLoQ, x[i]);
-            x[i] *= kn;
-            if (capped) x[i] = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i])), cap2);
-          }
-          if (biased) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int c = 16 * g + 8 * set + i;
-              if (c < cols) x[i] -= slope_s[c] * fabsf((float)(a.q_len[win.row0 + c / G] - 1 - tok));
+        bool seen = true;  // a column of this thread sees its token
+        if (!all || capped || biased) {
+          // Scores in place: nu_k, cap, distance, -inf where the token is not seen; the passes
+          // below then take them with a factor of one.
+          seen = false;
+#pragma unroll 1
+          for (int c0 = 16 * set; c0 < cols; c0 += 32) {
+            uint32_t see = 0xffffu;  // bit i: column c0 + i
+            if (!all) {
+              see = 0;
+              for (int c = c0; c < c0 + 16 && c < cols && real; c += G) {
+                const int r = c / G;
+                if (row_sees(rows[r], a.mask ? a.mask + (int64_t)(win.row0 + r) * a.mask_words : nullptr, tok))
+                  see |= ((1u << G) - 1u) << (c - c0);
+              }
             }
+            seen |= see != 0;
+            uint32_t u[16];
+            tm_ld16(s_at + c0, u);
+            if constexpr (SPLIT) {
+              uint32_t v[16];
+              tm_ld16(s_at + lo_col + c0, v);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                u[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), 1.0f / kLoQ, __uint_as_float(u[i])));
+                v[i] = 0u;
+              }
+              tm_st16(s_at + lo_col + c0, v);
+            } else {
+              tm_wait_ld();
+            }
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]) * kn;
+            if (capped) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i])), cap2);
+            }
+            if (biased) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] -= slope_s[c0 + i] * fabsf((float)(pos_s[c0 + i] - tok));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = (see >> i) & 1u ? __float_as_uint(x[i]) : 0xff800000u;
+            tm_st16(s_at + c0, u);
           }
-          if (!all) {
+          tm_wait_st();
+          kn = 1.f;
+        }
+        // a norm that counts for the weights' scale: finite, of a token some column here sees (a
+        // stale row may hold any bits)
+        const bool vfin = fabsf(vn) < INFINITY;
+        const float vf = seen && real && vfin ? fabsf(vn) : 0.f;
+        const F2 kn2 = f2(kn, kn);
+        auto load_s = [&](int c0, F2 (&x)[8]) {
+          uint32_t u[16];
+          tm_ld16(s_at + c0, u);
+          if constexpr (SPLIT) {
+            uint32_t v[16];
+            tm_ld16(s_at + lo_col + c0, v);
+            tm_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (!((see >> (8 * g + i)) & 1u)) x[i] = -INFINITY;
+              x[i] = fma2(f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2(1.0f / kLoQ, 1.0f / kLoQ),
+                          f2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
+          } else {
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = f2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
           }
         };
         // ---- does a column's max move by more than the slack, or the weights' scale?
         float over = -INFINITY;
+#pragma unroll 1
+        for (int c0 = 16 * set; c0 < cols; c0 += 32) {
+          F2 x[8];
+          load_s(c0, x);
 #pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
-          const int c0 = 16 * g + 8 * set;
-          if (c0 >= cols) continue;
-          float x[8];
-          scores(g, x);
-          const float4 ma = *reinterpret_cast<const float4*>(m_s + c0), mb = *reinterpret_cast<const float4*>(m_s + c0 + 4);
-          const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) over = fmaxf(over, x[i] - mm[i]);
+          for (int i = 0; i < 4; ++i) {
+            const float4 m4 = *reinterpret_cast<const float4*>(negm_s + c0 + 4 * i);
+            const F2 ya = fma2(x[2 * i], kn2, f2(m4.x, m4.y)), yb = fma2(x[2 * i + 1], kn2, f2(m4.z, m4.w));
+            over = fmaxf(over, fmaxf(ya.f.x, ya.f.y));
+            over = fmaxf(over, fmaxf(yb.f.x, yb.f.y));
+          }
         }
         const bool grow = vf > 0.f && exp_of(vf) - ve > 9;
         ok = wait(p_empty, (it & 1) ^ 1) && ok;  // the product of the tile before is done: P and O are free
@@ -846,20 +913,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_after();
         if (move) {
           // new maxima per column over the four lane quadrants, then the scale of the values
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const int c0 = 16 * g + 8 * set;
-            if (c0 >= cols) continue;
-            float x[8];
-            scores(g, x);
+#pragma unroll 1
+          for (int c0 = 16 * set; c0 < cols; c0 += 32) {
+            F2 x[8];
+            load_s(c0, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int top = __reduce_max_sync(kFullMask, ord_int(x[i]));
-              if (lane == 0) part_s[quad * C::kN + c0 + i] = ord_float(top);
+              const int ta = __reduce_max_sync(kFullMask, ord_int(x[i].f.x * kn));
+              const int tb = __reduce_max_sync(kFullMask, ord_int(x[i].f.y * kn));
+              if (lane == 0) {
+                part_s[quad * C::kN + c0 + 2 * i] = ord_float(ta);
+                part_s[quad * C::kN + c0 + 2 * i + 1] = ord_float(tb);
+              }
             }
           }
           const int vmax = __reduce_max_sync(kFullMask, __float_as_int(vf));
-          __shared__ int vpart[kSoftWarps];
           if (lane == 0) vpart[sw] = vmax;
           soft_sync();
           int vall = 0;
@@ -874,74 +942,96 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ve = ne;
             }
           }
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const int c0 = 16 * g + 8 * set;
-            if (c0 >= cols) continue;
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float top = part_s[c0 + i];
-#pragma unroll
-              for (int k = 1; k < 4; ++k) top = fmaxf(top, part_s[k * C::kN + c0 + i]);
-              const float old = m_s[c0 + i];
-              const float corr = top > old + kSlack ? ex2a(old - top) : 1.f;
-              l[8 * g + i] *= corr;
-              f[i] = corr * vscale;
-            }
-            if (t > first) {
-#pragma unroll
-              for (int part2 = 0; part2 < (SPLIT ? 2 : 1) * C::kHalves; ++part2) {
-                const uint32_t at = lanes + C::kO + (part2 / (SPLIT ? 2 : 1)) * C::kN + (SPLIT && part2 % 2 ? lo_col : 0) + c0;
-                uint32_t u[8];
-                tm_ld8(at, u);
-                tm_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f[i]);
-                tm_st8(at, u);
-              }
-              tm_wait_st();
-            }
-          }
-          soft_sync();
           if (stid < cols) {
             float top = part_s[stid];
 #pragma unroll
             for (int k = 1; k < 4; ++k) top = fmaxf(top, part_s[k * C::kN + stid]);
-            if (top > m_s[stid] + kSlack) m_s[stid] = top;
+            const float old = -negm_s[stid];
+            const bool up = top > old + kSlack;
+            corr_s[stid] = up ? ex2a(old - top) : 1.f;
+            if (up) {
+              negm_s[stid] = -top;
+              mu_s[stid] = -top;
+            }
           }
           soft_sync();
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = 16 * set + 32 * g;
+            if (c0 >= cols) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 f = *reinterpret_cast<const float2*>(corr_s + c0 + 2 * i);
+              l[8 * g + i] = mul2(l[8 * g + i], f2(f.x, f.y));
+            }
+          }
+          if (t > first) {
+#pragma unroll 1
+            for (int c0 = 16 * set; c0 < cols; c0 += 32) {
+#pragma unroll 1
+              for (int k = 0; k < (SPLIT ? 2 : 1) * C::kHalves; ++k) {
+                const uint32_t at = lanes + C::kO + (SPLIT ? k >> 1 : k) * C::kN + (SPLIT && (k & 1) ? lo_col : 0) + c0;
+                uint32_t u[16];
+                tm_ld16(at, u);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  u[i] = __float_as_uint(__uint_as_float(u[i]) * (corr_s[c0 + i] * vscale));
+                tm_st16(at, u);
+              }
+            }
+            tm_wait_st();
+          }
         }
         // ---- weights
-        const float vs = vn * pow2i(max(-126, min(126, -ve)));
+        const float vs = vfin && real && seen ? vn * pow2i(max(-126, min(126, -ve))) : 0.f;
+        const F2 vs2 = f2(vs, vs);
+        const uint32_t sx = (uint32_t)(t_lane & 7);
+        auto p_addr = [&](int c) -> uint32_t { return p_line + (c >> 6) * (kTok * 128) + ((((c & 63) >> 3) ^ sx) << 4); };
 #pragma unroll
         for (int g = 0; g < C::kGroups; ++g) {
-          const int c0 = 16 * g + 8 * set;
+          const int c0 = 16 * set + 32 * g;
           if (c0 >= cols) continue;
-          float x[8];
-          scores(g, x);
-          const float4 ma = *reinterpret_cast<const float4*>(m_s + c0), mb = *reinterpret_cast<const float4*>(m_s + c0 + 4);
-          const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
-          float y[8];
+          F2 x[8];
+          load_s(c0, x);
+          uint32_t o[8], r[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float pr = ex2a(x[i] - (mm[i] == -INFINITY ? 0.f : mm[i]));
-            l[8 * g + i] += pr;
-            y[i] = all || pr != 0.f ? pr * vs : 0.f;
-          }
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = pack2(y[2 * i], y[2 * i + 1]);
-          const uint32_t sx = (uint32_t)(t_lane & 7);
-          st_v4(p_line + (c0 >> 6) * (kTok * 128) + ((((c0 & 63) >> 3) ^ sx) << 4), o[0], o[1], o[2], o[3]);
-          if constexpr (SPLIT) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            const float2 m2 = *reinterpret_cast<const float2*>(mu_s + c0 + 2 * i);
+            x[i] = fma2(x[i], kn2, f2(m2.x, m2.y));
+            x[i].f.x = ex2a(x[i].f.x);
+            x[i].f.y = ex2a(x[i].f.y);
+            l[8 * g + i] = add2(l[8 * g + i], x[i]);
+            x[i] = mul2(x[i], vs2);
+            o[i] = pack2(x[i].f.x, x[i].f.y);
+            if constexpr (SPLIT) {
               const __half2 hh = *reinterpret_cast<const __half2*>(&o[i]);
-              o[i] = pack2((y[2 * i] - __low2float(hh)) * kLoP, (y[2 * i + 1] - __high2float(hh)) * kLoP);
+              r[i] = pack2((x[i].f.x - __low2float(hh)) * kLoP, (x[i].f.y - __high2float(hh)) * kLoP);
             }
-            const int c1 = c0 + lo_col;
-            st_v4(p_line + (c1 >> 6) * (kTok * 128) + ((((c1 & 63) >> 3) ^ sx) << 4), o[0], o[1], o[2], o[3]);
+          }
+          st_v4(p_addr(c0), o[0], o[1], o[2], o[3]);
+          st_v4(p_addr(c0 + 8), o[4], o[5], o[6], o[7]);
+          if constexpr (SPLIT) {
+            st_v4(p_addr(c0 + lo_col), r[0], r[1], r[2], r[3]);
+            st_v4(p_addr(c0 + lo_col + 8), r[4], r[5], r[6], r[7]);
+          }
+        }
+        if (__any_sync(kFullMask, real && seen && !vfin)) {
+          // a value norm that is infinite or NaN: where its token has weight, the output takes it
+          // (its weights above were zero)
+#pragma unroll 1
+          for (int c0 = 16 * set; c0 < cols; c0 += 32) {
+            F2 x[8];
+            load_s(c0, x);
+            if (!vfin && real && seen) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float y = (i & 1 ? x[i >> 1].f.y : x[i >> 1].f.x) * kn + mu_s[c0 + i];
+                const uint32_t at = p_addr(c0 + (i & 8)) + 2 * (i & 7);
+                const uint16_t v = !(ex2a(y) == 0.f) ? __half_as_ushort(__float2half_rn(vn)) : (uint16_t)0;
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(at), "h"(v) : "memory");
+              }
+            }
           }
         }
         fence_async();
@@ -959,12 +1049,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // sums over the 128 lanes
 #pragma unroll
       for (int g = 0; g < C::kGroups; ++g) {
-        const int c0 = 16 * g + 8 * set;
+        const int c0 = 16 * set + 32 * g;
         if (c0 >= cols) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float s = warp_sum(l[8 * g + i]);
-          if (lane == 0) part_s[quad * C::kN + c0 + i] = s;
+          const float sa = warp_sum(l[8 * g + i].f.x), sb2 = warp_sum(l[8 * g + i].f.y);
+          if (lane == 0) {
+            part_s[quad * C::kN + c0 + 2 * i] = sa;
+            part_s[quad * C::kN + c0 + 2 * i + 1] = sb2;
+          }
         }
       }
       soft_sync();
@@ -975,47 +1068,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto sum_of = [&](int c) -> float {
         return (part_s[c] + part_s[C::kN + c]) + (part_s[2 * C::kN + c] + part_s[3 * C::kN + c]);
       };
-      // this lane's dim of columns c0 .. c0 + 7 (half hf of the dims)
-      auto load_o = [&](int hf, int c0, float (&x)[8]) {
-        uint32_t u[8], v[8];
-        tm_ld8(lanes + C::kO + hf * C::kN + c0, u);
-        if constexpr (SPLIT) tm_ld8(lanes + C::kO + hf * C::kN + lo_col + c0, v);
-        tm_wait_ld();
+      // this lane's dim of columns c0 .. c0 + 15 (half hf of the dims)
+      auto load_o = [&](int hf, int c0, float (&x)[16]) {
+        uint32_t u[16];
+        tm_ld16(lanes + C::kO + hf * C::kN + c0, u);
+        if constexpr (SPLIT) {
+          uint32_t v[16];
+          tm_ld16(lanes + C::kO + hf * C::kN + lo_col + c0, v);
+          tm_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = __uint_as_float(u[i]);
-          if constexpr (SPLIT) x[i] = fmaf(__uint_as_float(v[i]), 1.0f / kLoP, x[i]);
-          x[i] *= up;
+          for (int i = 0; i < 16; ++i)
+            x[i] = fmaf(__uint_as_float(v[i]), 1.0f / kLoP, __uint_as_float(u[i])) * up;
+        } else {
+          tm_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]) * up;
         }
       };
       const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * w.cols;
       if (!whole) {
         if (stid < cols) {
-          w.ml[2 * (slot0 + stid)] = m_s[stid];
+          w.ml[2 * (slot0 + stid)] = -negm_s[stid];
           w.ml[2 * (slot0 + stid) + 1] = sum_of(stid);
         }
-        for (int c0 = 8 * set; c0 < cols; c0 += 16)
-#pragma unroll
+#pragma unroll 1
+        for (int c0 = 16 * set; c0 < cols; c0 += 32)
+#pragma unroll 1
           for (int hf = 0; hf < C::kHalves; ++hf) {
-            float x[8];
+            float x[16];
             load_o(hf, c0, x);
             if (D == 64 && quad >= 2) continue;  // lanes 64.. repeat the 64 dims
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 16; ++i)
               if (c0 + i < cols) w.acc[(slot0 + c0 + i) * D + hf * 128 + t_lane] = x[i];
           }
       } else {
         float* stage = reinterpret_cast<float*>(smem + C::kOffP);  // [kStageCols][D]
         for (int r0 = 0; r0 < cols; r0 += C::kStageCols) {
           const int r1 = min(cols, r0 + C::kStageCols);
-          for (int c0 = r0 + 8 * set; c0 < r1; c0 += 16)
-#pragma unroll
+#pragma unroll 1
+          for (int c0 = r0 + 16 * set; c0 < r1; c0 += 32)
+#pragma unroll 1
             for (int hf = 0; hf < C::kHalves; ++hf) {
-              float x[8];
+              float x[16];
               load_o(hf, c0, x);
               if (D == 64 && quad >= 2) continue;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < 16; ++i)
                 if (c0 + i < r1) stage[(c0 + i - r0) * D + hf * 128 + t_lane] = x[i];
             }
           soft_sync();
