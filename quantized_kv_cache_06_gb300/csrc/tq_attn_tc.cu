@@ -12,7 +12,7 @@
 //   O^T [dims x cols]  += Vhat^T [dims x tokens] P^T       A = Vhat, B = P^T, both stored as
 //                                                          they are produced (MN-major)
 // Khat = fp16(alpha_k c[idx]) never touches shared memory: the thread that owns a token
-// expands its packed row in registers and stores it to its own TMEM lane.  Vhat goes to
+// expands its packed row in registers and stores it to its own lane of TMEM.  Vhat goes to
 // shared memory in 16-byte chunks, swizzled.  The norms are per token, so per lane: nu_k
 // multiplies the score, nu_v the weight.
 //
@@ -27,8 +27,11 @@
 // most tiles rescale nothing; when one does, the softmax warps scale O^T in TMEM themselves
 // (the product before has completed by then).
 //
-// Roles of the 18 warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, two
-// sets that take alternate groups of 16 columns), 16 copies, 17 MMA issue.  Packed rows
+// Roles of the 18 warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, in two
+// sets), 16 copies, 17 MMA issue.  A window of more than half the MMA columns has both sets on
+// one tile, each with its groups of 16 columns; a smaller one makes two streams of one set that
+// take alternate tiles, each with its own maxima, sums and O^T, merged when the window ends:
+// the chain of waits, TMEM reads and votes of one tile then hides behind the other's.  Packed rows
 // arrive by TMA: the pages seen as a 2-D byte tensor [slots][H row_bytes], a box of up to 128
 // rows x the 16-byte aligned span around the head's bytes, so a block of a page is one copy.
 // Rows whose slab is not a multiple of 16 bytes (H not a multiple of 4) come by 4-byte
@@ -51,16 +54,22 @@ namespace {
 
 constexpr float kLog2eA = 1.4426950408889634f;
 constexpr int kTok = kAttnTile;  // tokens per tile = MMA lanes
-constexpr int kKeyWarps = 4, kValWarps = 4, kSoftWarps = 8;
+constexpr int kKeyWarps = 4, kValWarps = 4, kSoftSets = 2, kSoftWarps = 4 * kSoftSets;
 constexpr int kCopyWarp = kKeyWarps + kValWarps + kSoftWarps;
 constexpr int kMmaWarp = kCopyWarp + 1;
-constexpr int kTcThreads = 32 * (kMmaWarp + 1);
+constexpr int kTcThreads = 32 * (kCopyWarp + 4);  // whole warpgroups (two warps idle)
 constexpr int kSoftThreads = 32 * kSoftWarps;
+// Registers a thread: 96 at launch (640 threads); the softmax warps, which hold sums of up to 64
+// columns, take what the others leave (a spill there goes to L2: little L1 is left beside the
+// shared memory).  128 (dequant + dequant + issue) + 256 soft <= 640 * 96.
+constexpr int kRegsIssue = 64;
 constexpr int kMaxRing = 6;
 constexpr float kSlack = 6.0f;            // log2 units the running max may lag
+constexpr float kMaxWeight = 64.0f;       // 2^kSlack
 constexpr float kLoQ = 4096.0f;           // scale of the fp16 remainders of Q
 constexpr float kLoP = 2048.0f;           // and of P'
-constexpr int kBarSoft = 1;               // named barrier of the softmax warps
+constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
+constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
 
 template <int D, bool SPLIT>
 struct Tc {
@@ -69,7 +78,7 @@ struct Tc {
   static constexpr int kGroups = (kCols + 31) / 32;      // groups of 16 columns per softmax thread
   static constexpr int kHalves = D == 256 ? 2 : 1;       // 128-dim halves of O^T
   static constexpr int kKCols = D / 2;                   // TMEM columns of a key tile
-  static constexpr int kVBufs = D == 256 ? 1 : 2;
+  static constexpr int kVSlots = D == 256 ? 2 : D == 128 ? 3 : 4;  // slots of 64 tokens' values
   // TMEM columns
   static constexpr int kS = 0;
   static constexpr int kO = 2 * kN;
@@ -77,17 +86,18 @@ struct Tc {
   static_assert(kK + 2 * kKCols <= 512, "TMEM columns");
   // shared memory (offsets from a 1024-byte aligned base)
   static constexpr int kQBytes = kN * D * 2;
-  static constexpr int kVBytes = kTok * D * 2;
+  static constexpr int kVBytes = kTok / 2 * D * 2;
   static constexpr int kPBytes = kTok * kN * 2 < 16384 ? 16384 : kTok * kN * 2;
   static constexpr int kOffQ = 0;
   static constexpr int kOffV = kOffQ + kQBytes;
-  static constexpr int kOffP = kOffV + kVBufs * kVBytes;
+  static constexpr int kOffP = kOffV + kVSlots * kVBytes;
   static constexpr int kOffRows = kOffP + kPBytes;                 // RowView[kCols]
-  // floats: -max, max (0 while there is none), correction, slope [kN], part [4][kN]; int position [kN]
+  // floats [kN]: -max, correction, slope, (int) position, max and sum of the window; part [4][kN]
   static constexpr int kOffCol = kOffRows + kCols * (int)sizeof(RowView);
-  static constexpr int kOffTab = kOffCol + 9 * kN * 4;              // 5-bit tables, 2 x 32 x 32 words
-  static constexpr int kOffMeta = kOffTab + 2 * 32 * 32 * 4;        // uint32 valid[kMaxRing][4]
-  static constexpr int kOffRing = (kOffMeta + kMaxRing * 16 + 127) / 128 * 128;
+  static constexpr int kOffMeta = kOffCol + 10 * kN * 4;            // uint32 valid[kMaxRing][4]
+  static constexpr int kOffTab = (kOffMeta + kMaxRing * 16 + 127) / 128 * 128;  // key table, 5-bit value table, ring
+  static constexpr int kRegsDequant = D == 256 ? 96 : 64;
+  static constexpr int kRegsSoft = (640 * 96 - 128 * (2 * kRegsDequant + kRegsIssue)) / 256 / 8 * 8;
   static constexpr int kStageCols = kPBytes / (D * 4);              // output columns staged at a time
 };
 
@@ -98,6 +108,12 @@ __host__ __device__ constexpr int span_bytes(int d, int bits) {
   int s = (d * bits / 8 + 4 + 12 + 15) / 16 * 16;
   return (s / 16) % 2 ? s : s + 16;
 }
+
+// Lookup tables in shared memory: 4-byte entries, a copy for each lane (entry e of lane l at
+// e * 128 + 4 l), so no lookup meets another lane's bank.  Keys: pairs of centroids by the 2 b
+// bits of two neighbouring indices; 5 bits (keys and values): single centroids.
+__host__ __device__ constexpr int key_table_bytes(int bits) { return (bits == 5 ? 32 : 1 << (2 * bits)) * 128; }
+__host__ __device__ constexpr int value_table_bytes(int bits) { return bits == 5 ? 32 * 128 : 0; }
 
 struct TcAttnArgs {
   AttnArgs a;
@@ -117,6 +133,9 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void bar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(n) : "memory");
+}
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -133,22 +152,26 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 // D (+)= A B, kind::f16, A in TMEM or in shared memory, B in shared memory; one thread.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
-                   "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-               : "memory");
+// Descriptors come as their low words (address and leading offset); the high word is the same
+// for all: eight rows (K-major) or k-lines (MN-major) of 128 bytes, the next eight 1024 bytes on,
+// 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::
-                   "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-               : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 bd;\n setp.ne.b32 p, %4, 0;\n mov.b64 bd, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
+      : "memory");
 }
-// Shared-memory operand in the 128-byte swizzle: rows (K-major) or k-lines (MN-major) of 128
-// bytes, groups of eight of them `sbo` apart; `lbo` apart the next 64 elements of an MN-major
-// operand.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 ad, bd;\n setp.ne.b32 p, %4, 0;\n mov.b64 ad, {%1, %5};\n mov.b64 bd, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
+      : "memory");
 }
 // f16 x f16 -> f32, M 128; `mn`: both operands MN-major.
 __device__ __forceinline__ uint32_t mma_idesc(int n, bool mn) {
@@ -195,42 +218,18 @@ __device__ __forceinline__ float rcpa(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// Pairs of fp32 in one instruction.
-union F2 {
-  float2 f;
-  uint64_t u;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  r.f = make_float2(x, y);
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;\n" ::"n"(kBarSoft), "n"(kSoftThreads) : "memory"); }
-__device__ __forceinline__ bool soft_any(bool x) {
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool named_any(int id, int n, bool x) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)x), "n"(kBarSoft), "n"(kSoftThreads)
+      : "r"((uint32_t)x), "r"(id), "r"(n)
       : "memory");
   return r != 0;
 }
@@ -245,12 +244,44 @@ __device__ __forceinline__ int exp_of(float x) { return max((int)((__float_as_ui
 
 // ---------------------------------------------------------------- dequantisation
 
-// Centroids fp16(alpha c) as byte tables: the low and the high bytes of eight entries per
-// register pair.  A PRMT whose selector is four indices of three bits returns the bytes of four
-// coordinates, so no lookup leaves the registers; four bits take two of them and a select.
+// Keys: 32 consecutive coordinates from the first BITS words of w, two per lookup (5 bits: one).
 template <int BITS>
+__device__ __forceinline__ void expand32_table(const uint32_t* w, uint32_t tab_lane, uint32_t (&out)[16]) {
+  if constexpr (BITS == 5) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t v[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int bit = 5 * (2 * i + k), j = bit >> 5, sh = bit & 31;
+        const uint32_t f = (sh <= 27 ? w[j] >> sh : __funnelshift_r(w[j], w[j + 1], sh)) & 31u;
+        v[k] = ld_s32(tab_lane + f * 128u);
+      }
+      out[i] = __byte_perm(v[0], v[1], 0x5410);
+    }
+  } else {
+    constexpr int W = 2 * BITS;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int bit = W * i, j = bit >> 5, sh = bit & 31;
+      uint32_t f;
+      if constexpr (BITS == 4) f = __byte_perm(w[j], 0, 0x4440 + (sh >> 3));
+      else f = (sh <= 32 - W ? w[j] >> sh : __funnelshift_r(w[j], w[j + 1], sh)) & ((1u << W) - 1u);
+      out[i] = ld_s32(tab_lane + f * 128u);
+    }
+  }
+}
+
+// Values: centroids fp16(alpha c) as byte tables in registers, the low and the high bytes of
+// eight entries per register pair.  A PRMT whose selector is four indices of three bits returns
+// the bytes of four coordinates.  Two units then share the work: the keys' lookups load the
+// shared-memory pipe, the values' the integer pipe (whose bytes have to go to shared memory
+// besides).  Four bits: the codebook is odd (c[15 - i] = -c[i]), so eight magnitudes and a sign
+// do; SYM false takes 16 entries.
+template <int BITS, bool SYM>
 struct ByteTable {
-  static constexpr int kPairs = BITS == 4 ? 2 : 1;
+  static constexpr int kPairs = BITS == 4 && !SYM ? 2 : 1;
+  static constexpr int kFirst = BITS == 4 && SYM ? 8 : 0;
   uint32_t lo[2 * kPairs], hi[2 * kPairs];
   __device__ __forceinline__ void load(const float* c, float alpha) {
 #pragma unroll
@@ -258,7 +289,7 @@ struct ByteTable {
       lo[r] = hi[r] = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int e = 4 * r + k;
+        const int e = kFirst + 4 * r + k;
         if (e < (1 << BITS)) {
           const uint32_t u = __half_as_ushort(__float2half_rn(__ldg(c + e) * alpha));
           lo[r] |= (u & 255u) << (8 * k);
@@ -270,10 +301,13 @@ struct ByteTable {
 };
 
 // Eight consecutive coordinates (group g of the words) as four fp16 pairs.
-template <int BITS>
-__device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTable<BITS>& t, uint32_t (&out)[4]) {
+template <int BITS, bool SYM>
+__device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTable<BITS, SYM>& t, uint32_t (&out)[4]) {
   uint32_t sel;  // eight selector nibbles
-  if constexpr (BITS == 4) {
+  if constexpr (BITS == 4 && SYM) {
+    const uint32_t n = ~w[g] & 0x88888888u;  // negative: index 7 - k is -c[8 + k]
+    sel = (w[g] ^ ((n >> 3) * 7u)) & 0x77777777u;
+  } else if constexpr (BITS == 4) {
     sel = w[g] & 0x77777777u;
   } else if constexpr (BITS == 3) {
     const int bit = 24 * g, i = bit >> 5, sh = bit & 31;
@@ -287,52 +321,26 @@ __device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTabl
     x = (x | (x << 4)) & 0x0f0f0f0fu;
     sel = (x | (x << 2)) & 0x33333333u;
   }
+  const uint32_t z = BITS == 4 ? w[g] << 4 : 0u;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const uint32_t s = k ? sel >> 16 : sel;
     uint32_t lo = __byte_perm(t.lo[0], t.lo[1], s), hi = __byte_perm(t.hi[0], t.hi[1], s);
     if constexpr (BITS == 4) {
       // bytes 0xff where bit 3 of the index is set (the sign-replicating selector form)
-      const uint32_t z = w[g] << 4;
       uint32_t m;
       if (k == 0) asm("prmt.b32 %0, %1, %2, 0xd9c8;\n" : "=r"(m) : "r"(z), "r"(w[g]));
       else asm("prmt.b32 %0, %1, %2, 0xfbea;\n" : "=r"(m) : "r"(z), "r"(w[g]));
-      lo = (lo & ~m) | (__byte_perm(t.lo[2], t.lo[3], s) & m);
-      hi = (hi & ~m) | (__byte_perm(t.hi[2], t.hi[3], s) & m);
+      if constexpr (SYM) {
+        hi |= ~m & 0x80808080u;
+      } else {
+        lo = (lo & ~m) | (__byte_perm(t.lo[2], t.lo[3], s) & m);
+        hi = (hi & ~m) | (__byte_perm(t.hi[2], t.hi[3], s) & m);
+      }
     }
     out[2 * k] = __byte_perm(lo, hi, 0x5140);
     out[2 * k + 1] = __byte_perm(lo, hi, 0x7362);
   }
-}
-
-// 5-bit rows: one shared-memory lookup per coordinate, the 32 entries replicated per lane.
-__device__ __forceinline__ void expand8_5(const uint32_t* w, int g, uint32_t tab_lane, uint32_t (&out)[4]) {
-  uint32_t v[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int bit = 40 * g + 5 * k, i = bit >> 5, sh = bit & 31;
-    const uint32_t f = (sh <= 27 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh)) & 31u;
-    v[k] = ld_s32(tab_lane + f * 128u);
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) out[k] = __byte_perm(v[2 * k], v[2 * k + 1], 0x5410);
-}
-
-// 32 consecutive coordinates from the first BITS words of w; the words move up, so that a loop
-// over a row stays rolled (the roles share the instruction cache) with the row in registers.
-template <int BITS, int NW>
-__device__ __forceinline__ void expand32(uint32_t (&w)[NW], const ByteTable<BITS == 5 ? 2 : BITS>& t, uint32_t tab_lane,
-                                         uint32_t (&out)[16]) {
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint32_t x[4];
-    if constexpr (BITS == 5) expand8_5(w, g, tab_lane, x);
-    else expand8<BITS>(w, g, t, x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) out[4 * g + k] = x[k];
-  }
-#pragma unroll
-  for (int i = 0; i + BITS < NW; ++i) w[i] = w[i + BITS];
 }
 
 // The row of this thread's token in the ring: SPAN bytes, of which the row starts `skip` words in.
@@ -349,12 +357,64 @@ __device__ __forceinline__ void load_row(uint32_t addr, int skip, uint32_t (&w)[
     r[4 * i + 2] = v.z;
     r[4 * i + 3] = v.w;
   }
-  const bool s1 = skip & 1, s2 = skip & 2;
+  auto take = [&](auto tag) {
+    constexpr int K = decltype(tag)::value;
 #pragma unroll
-  for (int i = 0; i < 4 * NV; ++i) r[i] = s1 && i + 1 < 4 * NV ? r[i + 1 < 4 * NV ? i + 1 : i] : r[i];
-#pragma unroll
-  for (int i = 0; i < NW; ++i) w[i] = s2 ? r[i + 2 < 4 * NV ? i + 2 : i] : r[i];
+    for (int i = 0; i < NW; ++i) w[i] = r[i + K < 4 * NV ? i + K : 0];
+  };
+  if (skip == 0) take(std::integral_constant<int, 0>{});
+  else if (skip == 1) take(std::integral_constant<int, 1>{});
+  else if (skip == 2) take(std::integral_constant<int, 2>{});
+  else take(std::integral_constant<int, 3>{});
   w[NW] = 0;
+}
+
+// Drops the first N words: a loop over a row stays rolled (the roles share the instruction
+// cache) with the row in registers.
+template <int N, int NW>
+__device__ __forceinline__ void drop_words(uint32_t (&w)[NW]) {
+#pragma unroll
+  for (int i = 0; i + N < NW; ++i) w[i] = w[i + N];
+}
+
+// ---------------------------------------------------------------- queries and outputs
+
+// E consecutive query elements from element `at` (a multiple of E); `vec`: the tensor starts on 16 bytes.
+template <int E>
+__device__ __forceinline__ void load_query(const void* q, int64_t at, int dtype, bool vec, float (&v)[E]) {
+  if (vec && dtype == kF32) {
+    load_chunk<float, E>(static_cast<const float*>(q) + at, v);
+  } else if (vec && dtype == kF16) {
+    load_chunk<__half, E>(static_cast<const __half*>(q) + at, v);
+  } else if (vec) {
+    load_chunk<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(q) + at, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = load_as_f32(q, at + i, dtype);
+  }
+}
+// E consecutive output elements (fp16 for SPLIT, else bf16).
+template <int E, bool SPLIT>
+__device__ __forceinline__ void store_row(void* out, int64_t at, bool vec, const float (&v)[E]) {
+  uint32_t u[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    if constexpr (SPLIT) {
+      u[i] = pack2(v[2 * i], v[2 * i + 1]);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  uint16_t* to = static_cast<uint16_t*>(out) + at;
+  if (vec) {
+    if constexpr (E == 8) *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+    else if constexpr (E == 4) *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
+    else *reinterpret_cast<uint32_t*>(to) = u[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) to[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+  }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -367,9 +427,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const AttnArgs& a = p.a;
   const AttnWork& w = p.w;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxRing + 16];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxRing + 26];
   __shared__ uint32_t tmem_slot;
-  __shared__ int dead, fail[2];
+  __shared__ int dead, fail[2][2], fail_all;
   __shared__ int full_lo, full_hi, pre_lo, pre_hi, q_exp;
   unsigned char* smem = smem_raw + ((1024u - (smem_a(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_a(smem);
@@ -380,7 +440,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int spk = span_bytes(D, a.k_bits), spv = span_bytes(D, a.v_bits);
   const int skip_k = p.tma ? (h * rbk) % 16 : 0, skip_v = p.tma ? (h * rbv) % 16 : 0;
   const int stage_bytes = kTok * (spk + spv);
-  const uint32_t ring = base + C::kOffRing;
+  const uint32_t ktab = base + C::kOffTab, vtab = ktab + key_table_bytes(a.k_bits);
+  const uint32_t ring = vtab + value_table_bytes(a.v_bits);
 
   auto bar = [&](int i) -> uint32_t { return smem_a(bars) + 8u * i; };
   auto raw_full = [&](int s) { return bar(s); };
@@ -388,11 +449,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int B0 = 2 * kMaxRing;
   auto k_full = [&](int b) { return bar(B0 + b); };
   auto k_empty = [&](int b) { return bar(B0 + 2 + b); };
-  auto s_full = [&](int b) { return bar(B0 + 4 + b); };
-  auto s_empty = [&](int b) { return bar(B0 + 6 + b); };
-  auto v_full = [&](int b) { return bar(B0 + 8 + b); };
-  auto v_empty = [&](int b) { return bar(B0 + 10 + b); };
-  const uint32_t p_full = bar(B0 + 12), p_empty = bar(B0 + 13), q_full = bar(B0 + 14), drained = bar(B0 + 15);
+  auto v_full = [&](int b) { return bar(B0 + 4 + b); };  // one per value slot
+  auto v_empty = [&](int b) { return bar(B0 + 8 + b); };
+  auto s_full = [&](int b) { return bar(B0 + 12 + b); };  // two per stream
+  auto s_empty = [&](int b) { return bar(B0 + 16 + b); };
+  auto p_full = [&](int s) { return bar(B0 + 20 + s); };  // one per stream
+  auto p_empty = [&](int s) { return bar(B0 + 22 + s); };
+  const uint32_t q_full = bar(B0 + 24), drained = bar(B0 + 25);
   volatile int* dead_v = &dead;
 
   // A bounded wait of one thread; a role that has seen another give up leaves too.
@@ -412,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (tid == 0) {
     dead = 0;
-    fail[0] = fail[1] = 0;
+    fail[0][0] = fail[0][1] = fail[1][0] = fail[1][1] = fail_all = 0;
     for (int s = 0; s < kMaxRing; ++s) {
       bar_init(raw_full(s), p.tma ? 1 : 33);  // cp.async: every lane's copies and one arrival
       bar_init(raw_empty(s), kKeyWarps + kValWarps + kSoftWarps);
@@ -420,13 +483,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int b = 0; b < 2; ++b) {
       bar_init(k_full(b), kKeyWarps);
       bar_init(k_empty(b), 1);
+      bar_init(p_full(b), kSoftWarps);
+      bar_init(p_empty(b), 1);
+    }
+    for (int b = 0; b < 4; ++b) {
+      bar_init(v_full(b), kValWarps / 2);
+      bar_init(v_empty(b), 1);
       bar_init(s_full(b), 1);
       bar_init(s_empty(b), kSoftWarps);
-      bar_init(v_full(b), kValWarps);
-      bar_init(v_empty(b), 1);
     }
-    bar_init(p_full, kSoftWarps);
-    bar_init(p_empty, 1);
     bar_init(q_full, kSoftWarps);
     bar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -436,15 +501,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
-  // 5-bit tables: entry e of lane l at e * 128 + 4 l
-  if (a.k_bits == 5 || a.v_bits == 5)
-    for (int i = tid; i < 2 * 32 * 32; i += kTcThreads) {
-      const int comp = i >> 10, e = (i >> 5) & 31;
-      const int bits = comp ? a.v_bits : a.k_bits;
-      const float c = e < (1 << bits) ? __ldg((comp ? a.v_centroids : a.k_centroids) + e) : 0.f;
-      reinterpret_cast<uint32_t*>(smem + C::kOffTab)[i] =
-          __half_as_ushort(__float2half_rn(c * (comp ? a.v_alpha : a.k_alpha)));
-    }
+  {
+    auto entry = [&](const float* c, float alpha, int e) -> uint32_t {
+      return (uint32_t)__half_as_ushort(__float2half_rn(__ldg(c + e) * alpha));
+    };
+    const int kw = key_table_bytes(a.k_bits) / 4, vw = value_table_bytes(a.v_bits) / 4;
+    uint32_t* t = reinterpret_cast<uint32_t*>(smem + C::kOffTab);
+    const int mask = (1 << a.k_bits) - 1;
+    for (int e = warp; e < kw / 32; e += kTcThreads / 32)
+      t[e * 32 + lane] = a.k_bits == 5 ? entry(a.k_centroids, a.k_alpha, e)
+                                       : entry(a.k_centroids, a.k_alpha, e & mask) |
+                                             entry(a.k_centroids, a.k_alpha, e >> a.k_bits) << 16;
+    for (int e = warp; e < vw / 32; e += kTcThreads / 32) t[kw + e * 32 + lane] = entry(a.v_centroids, a.v_alpha, e);
+  }
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   tc_before();
   __syncthreads();
@@ -471,15 +540,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return (tile < win.nA ? win.tA0 + tile : win.tB0 + tile - win.nA) * kTok;
   };
   auto pad_cols = [&](const AttnWindow& win) -> int { return (win.nrows * G + 15) / 16 * 16; };
+  // Two streams of tiles when the window's MMA columns fit half of the TMEM regions.
+  auto streams_of = [&](int padded) -> int { return (SPLIT ? 2 * padded : padded) <= C::kN / 2 ? 2 : 1; };
 
   if (warp < kKeyWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsDequant));
     // ------------------------------------------------ keys: packed row -> this lane of TMEM
     auto keys = [&](auto bits_tag) {
       constexpr int BITS = decltype(bits_tag)::value;
       constexpr int SPAN = span_bytes(D, BITS);
-      ByteTable<BITS == 5 ? 2 : BITS> table;
-      if constexpr (BITS != 5) table.load(a.k_centroids, a.k_alpha);
-      const uint32_t tab = base + C::kOffTab + lane * 4;
+      const uint32_t tab = ktab + lane * 4;
       const uint32_t row = ring + (uint32_t)((warp * 32 + lane) * SPAN);
       const uint32_t dst = tmem + ((uint32_t)(32 * warp) << 16) + C::kK;
       int st = 0, ph = 0, it = 0;
@@ -497,7 +567,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
           for (int g = 0; g < D / 32; ++g) {
             uint32_t o[16];
-            expand32<BITS>(wd, table, tab, o);
+            expand32_table<BITS>(wd, tab, o);
+            drop_words<BITS>(wd);
             tm_st16(dst + b * C::kKCols + 16 * g, o);
           }
           tm_wait_st();
@@ -513,58 +584,570 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     else if (a.k_bits == 2) keys(std::integral_constant<int, 2>{});
     else keys(std::integral_constant<int, 5>{});
   } else if (warp < kKeyWarps + kValWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsDequant));
     // ------------------------------------------------ values: packed row -> swizzled k-line
-    auto values = [&](auto bits_tag) {
+    auto values = [&](auto bits_tag, auto sym_tag) {
       constexpr int BITS = decltype(bits_tag)::value;
+      constexpr bool SYM = decltype(sym_tag)::value;
       constexpr int SPAN = span_bytes(D, BITS);
-      ByteTable<BITS == 5 ? 2 : BITS> table;
+      ByteTable<BITS == 5 ? 2 : BITS, SYM> table;
       if constexpr (BITS != 5) table.load(a.v_centroids, a.v_alpha);
-      const uint32_t tab = base + C::kOffTab + 32 * 32 * 4 + lane * 4;
-      const int t = (warp - kKeyWarps) * 32 + lane;
-      const uint32_t row = ring + (uint32_t)(kTok * spk + t * SPAN);
+      const uint32_t tab = vtab + lane * 4;
+      const int half = (warp - kKeyWarps) >> 1, t = ((warp - kKeyWarps) & 1) * 32 + lane;  // token t of 64
+      const uint32_t row = ring + (uint32_t)(kTok * spk + (64 * half + t) * SPAN);
       const uint32_t line = base + C::kOffV + (uint32_t)((t >> 3) * 1024 + (t & 7) * 128);
-      int st = 0, ph = 0, it = 0;
+      int st = 0, ph = 0;
+      int slot = half % C::kVSlots, vph = 1;  // slot 2 it + half, round by round
       for_windows([&](const AttnWindow&, int first, int last) -> bool {
-        for (int k = first; k < last; ++k, ++it) {
+        for (int k = first; k < last; ++k) {
           if (!wait(raw_full(st), ph)) return false;
           uint32_t wd[D * BITS / 32 + 1];
           load_row<D, BITS>(row + st * stage_bytes, skip_v >> 2, wd);
           __syncwarp();
           if (lane == 0) bar_arrive(raw_empty(st));
           if (++st == p.ring) st = 0, ph ^= 1;
-          const int b = it % C::kVBufs;
-          if (!wait(v_empty(b), ((it / C::kVBufs) & 1) ^ 1)) return false;
-          const uint32_t to = line + b * C::kVBytes;
+          if (!wait(v_empty(slot), vph)) return false;
+          const uint32_t to = line + slot * C::kVBytes;
 #pragma unroll 1
           for (int g = 0; g < D / 32; ++g) {
             uint32_t o[16];
-            expand32<BITS>(wd, table, tab, o);
-            const uint32_t at = to + (g >> 1) * (kTok * 128) + (((uint32_t)(t & 7) ^ (uint32_t)(4 * (g & 1))) << 4);
+            if constexpr (BITS == 5) {
+              expand32_table<5>(wd, tab, o);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t x[4];
+                expand8<BITS, SYM>(wd, e, table, x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[4 * e + i] = x[i];
+              }
+            }
+            drop_words<BITS>(wd);
+            const uint32_t at = to + (g >> 1) * (64 * 128) + (((uint32_t)(t & 7) ^ (uint32_t)(4 * (g & 1))) << 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               st_v4(at ^ (uint32_t)(e << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           fence_async();
           __syncwarp();
-          if (lane == 0) bar_arrive(v_full(b));
+          if (lane == 0) bar_arrive(v_full(slot));
+          slot += 2;
+          if (slot >= C::kVSlots) slot -= C::kVSlots, vph ^= 1;
         }
         return true;
       });
     };
-    if (a.v_bits == 4) values(std::integral_constant<int, 4>{});
-    else if (a.v_bits == 3) values(std::integral_constant<int, 3>{});
-    else if (a.v_bits == 2) values(std::integral_constant<int, 2>{});
-    else values(std::integral_constant<int, 5>{});
-  } else if (warp == kCopyWarp) {
+    using No = std::integral_constant<bool, false>;
+    if (a.v_bits == 4) {
+      bool odd = true;  // the codebook's halves mirror each other
+      for (int e = 0; e < 8; ++e) odd = odd && __ldg(a.v_centroids + e) == -__ldg(a.v_centroids + 15 - e);
+      if (odd) values(std::integral_constant<int, 4>{}, std::integral_constant<bool, true>{});
+      else values(std::integral_constant<int, 4>{}, No{});
+    } else if (a.v_bits == 3) values(std::integral_constant<int, 3>{}, No{});
+    else if (a.v_bits == 2) values(std::integral_constant<int, 2>{}, No{});
+    else values(std::integral_constant<int, 5>{}, No{});
+  } else if (warp < kCopyWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoft));
+    // ------------------------------------------------ softmax, queries and outputs
+    const int sw = warp - kKeyWarps - kValWarps;  // softmax warp
+    const int quad = warp & 3, set = sw >> 2;
+    const int stid = tid - 32 * (kKeyWarps + kValWarps);
+    const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
+    RowView* rows = reinterpret_cast<RowView*>(smem + C::kOffRows);
+    float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -max; -inf where there is no column
+    float* corr_s = negm_s + C::kN;
+    float* slope_s = corr_s + C::kN;
+    int* pos_s = reinterpret_cast<int*>(slope_s + C::kN);
+    float* top_s = slope_s + 2 * C::kN;  // max and sum of the window's columns over the streams
+    float* sum_s = top_s + C::kN;
+    float* part_s = sum_s + C::kN;  // [4][kN]
+    __shared__ int vpart[kSoftWarps], ve_s[2];
+    const uint32_t* valid = reinterpret_cast<const uint32_t*>(smem + C::kOffMeta);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t krow = ring + (uint32_t)(t_lane * spk + skip_k + rbk - 4);
+    const uint32_t vrow = ring + (uint32_t)(kTok * spk + t_lane * spv + skip_v + rbv - 4);
+    const uint32_t p_line = base + C::kOffP + (uint32_t)((t_lane >> 3) * 1024 + (t_lane & 7) * 128);
+    const float scale = a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)D);
+    const bool capped = a.softcap > 0.f, biased = a.alibi != nullptr;
+    // capped scores: tanh(s / cap) from 2^(2 log2(e) s / cap)
+    const float qmul = (capped ? 2.f * scale / a.softcap : scale) * kLog2eA / (sqrtf((float)D) * a.k_alpha);
+    const float cap2 = a.softcap * kLog2eA;
+    const float inv_av = 1.0f / a.v_alpha;
+    const bool q_vec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0, o_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+    float sgn[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) sgn[i] = __ldg(a.signs + lane * (D / 32) + i);
+    int st = 0, ph = 0;
+    uint32_t sph = 0, pph = 0;
+
+    for_windows([&](const AttnWindow& win, int first, int last) -> bool {
+      const int cols = win.nrows * G, padded = pad_cols(win);
+      const int lo_col = SPLIT ? padded : 0;
+      const int streams = streams_of(padded), pitch = C::kN / streams;
+      const int sets = kSoftSets / streams, stream = set / sets;
+      const int c_first = 16 * (set % sets), c_step = 16 * sets;  // this thread's groups of columns
+      const int col0 = stream * pitch;                             // the stream's part of the column arrays
+      const int bar_id = kBarSoft + 1 + stream, bar_n = 128 * sets;
+      const uint32_t weight = (uint32_t)streams;  // arrivals of this warp where all softmax warps count
+      // ---- queries of the window: one power of two for all of them, rotated, hi (and lo)
+      if (stid == 0) {
+        full_lo = pre_lo = 0;
+        full_hi = pre_hi = 0x7fffffff;
+        q_exp = -1000;
+      }
+      soft_sync();
+      if (stid < win.nrows) {
+        const RowView v = row_view(a, win.row0 + stid);
+        rows[stid] = v;
+        atomicMax(&full_lo, v.w0);
+        atomicMin(&full_hi, v.w1);
+        atomicMax(&pre_lo, v.p0);
+        atomicMin(&pre_hi, v.p1);
+      }
+      if (stid < C::kN) {
+        const int c = stid & (pitch - 1);
+        negm_s[stid] = c < cols ? -kNoMax : -INFINITY;  // no column there: never a new max
+        slope_s[stid] = biased && stid < cols ? a.alibi[h * G + stid % G] * kLog2eA : 0.f;
+        pos_s[stid] = a.q_len && stid < cols ? a.q_len[win.row0 + stid / G] - 1 : 0;
+      }
+      // this lane's D / 32 coordinates of a column's query; kAhead columns are loaded together
+      constexpr int kAhead = 4;
+      auto q_rows = [&](int col, float (&v)[kAhead][D / 32]) {
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          const int c = min(col + e * kSoftWarps, cols - 1);
+          const int64_t at = ((int64_t)(win.row0 + c / G) * a.num_q_heads + h * G + c % G) * D + lane * (D / 32);
+          load_query<D / 32>(a.q, at, a.q_dtype, q_vec, v[e]);
+        }
+      };
+      float most = 0.f;
+      for (int col = sw; col < cols; col += kAhead * kSoftWarps) {
+        float v[kAhead][D / 32];
+        q_rows(col, v);
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          float ss = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) ss = fmaf(v[e][i] * qmul, v[e][i] * qmul, ss);
+          ss = warp_sum(ss);
+          if (ss < INFINITY) most = fmaxf(most, ss);
+        }
+      }
+      if (lane == 0) atomicMax(&q_exp, (exp_of(most) + 1) / 2);
+      soft_sync();
+      // the largest rotated coordinate is at most the norm times sqrt(D): to 2^10 or less
+      const int qe = q_exp + (D == 64 ? 3 : 4) - 10;
+      const float q_down = pow2i(max(-126, min(126, -qe))), q_up = pow2i(max(-126, min(126, qe)));
+      for (int col4 = sw; col4 < cols; col4 += kAhead * kSoftWarps) {
+        float v[kAhead][D / 32];
+        q_rows(col4, v);
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          const int col = col4 + e * kSoftWarps;
+          if (col >= cols) continue;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) v[e][i] *= qmul * sgn[i];
+          fwht_warp<D / 32>(v[e]);
+#pragma unroll
+          for (int i = 0; i < D / 32; i += 2) {
+            const int d = lane * (D / 32) + i;
+            const float x0 = v[e][i] * q_down, x1 = v[e][i + 1] * q_down;
+            const uint32_t hi = pack2(x0, x1);
+            const uint32_t at = (uint32_t)((d >> 6) * (C::kN * 128) + (((d & 63) * 2) & 15));
+            const uint32_t ch = (uint32_t)((d & 63) >> 3);
+            *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + col * 128 + ((ch ^ (col & 7)) << 4)) = hi;
+            if constexpr (SPLIT) {
+              const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
+              const int lc = col + lo_col;
+              *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + lc * 128 + ((ch ^ (lc & 7)) << 4)) =
+                  pack2((x0 - __low2float(hh)) * kLoQ, (x1 - __high2float(hh)) * kLoQ);
+            }
+          }
+        }
+      }
+      fence_async();
+      soft_sync();
+      if (lane == 0) bar_arrive(q_full);
+
+      // ---- tiles
+      const int hi_tok = max(win.p_hi, win.w_hi), tiles = last - first;
+      float2 l[C::kGroups * 8];
+#pragma unroll
+      for (int i = 0; i < C::kGroups * 8; ++i) l[i] = make_float2(0.f, 0.f);
+      int ve = -1000;  // P' = p nu_v 2^-ve (every thread of the stream holds the same)
+      bool broken = false;
+      for (int k = 0; k < tiles; ++k) {
+        const int sb = k & (2 * streams - 1);
+        const int this_st = st, this_ph = ph;
+        const uint32_t this_s = (sph >> sb) & 1, this_p = (pph >> (k & (streams - 1))) & 1;
+        if (++st == p.ring) st = 0, ph ^= 1;
+        sph ^= 1u << sb;
+        pph ^= 1u << (k & (streams - 1));
+        if ((k & (streams - 1)) != stream || broken) continue;
+        const int t0 = tile_token(win, first + k), tok = t0 + t_lane;
+        const uint32_t s_at = lanes + C::kS + sb * pitch;
+        bool ok = wait(raw_full(this_st), this_ph);
+        float kn = __uint_as_float(ld_s32(krow + this_st * stage_bytes)) * q_up;
+        const float vn = __uint_as_float(ld_s32(vrow + this_st * stage_bytes));
+        const uint4 vv = *reinterpret_cast<const uint4*>(valid + 4 * this_st);
+        ok = wait(s_full(sb), this_s) && ok;
+        tc_after();
+        const bool real = (((quad == 0 ? vv.x : quad == 1 ? vv.y : quad == 2 ? vv.z : vv.w) >> lane) & 1u) && tok < hi_tok;
+        const bool all = (vv.x & vv.y & vv.z & vv.w) == 0xffffffffu && ((t0 >= full_lo && t0 + kTok <= full_hi) ||
+                                                                         (t0 >= pre_lo && t0 + kTok <= pre_hi));
+        __syncwarp();
+        if (lane == 0) bar_arrive_n(raw_empty(this_st), weight);
+        // Scores of columns c0 .. c0 + 15 from their accumulators (the two parts added).
+        auto fetch = [&](int c0, float2 (&x)[8]) {
+          uint32_t u[16];
+          tm_ld16(s_at + c0, u);
+          if constexpr (SPLIT) {
+            uint32_t v[16];
+            tm_ld16(s_at + lo_col + c0, v);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              x[i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                make_float2(1.0f / kLoQ, 1.0f / kLoQ),
+                                make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
+          } else {
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+          }
+        };
+        bool seen = true;  // a column of this thread sees its token
+        if (!all || capped || biased) {
+          // Scores in place: nu_k, cap, distance, -inf where the token is not seen; what follows
+          // takes them with a factor of one.  (A loop apart, so that plain tiles keep their code
+          // together in the instruction cache.)
+          seen = false;
+#pragma unroll 1
+          for (int c0 = c_first; c0 < cols; c0 += c_step) {
+            float2 x[8];
+            fetch(c0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], make_float2(kn, kn));
+            if (capped) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                x[i].x = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i].x)), cap2);
+                x[i].y = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i].y)), cap2);
+              }
+            }
+            if (biased) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                x[i].x -= slope_s[c0 + 2 * i] * fabsf((float)(pos_s[c0 + 2 * i] - tok));
+                x[i].y -= slope_s[c0 + 2 * i + 1] * fabsf((float)(pos_s[c0 + 2 * i + 1] - tok));
+              }
+            }
+            uint32_t see = 0xffffu;  // bit i: column c0 + i
+            if (!all) {
+              see = 0;
+              for (int c = c0; c < c0 + 16 && c < cols && real; c += G) {
+                const int r = c / G;
+                if (row_sees(rows[r], a.mask ? a.mask + (int64_t)(win.row0 + r) * a.mask_words : nullptr, tok))
+                  see |= ((1u << G) - 1u) << (c - c0);
+              }
+            }
+            seen |= see != 0;
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              u[i] = (see >> i) & 1u ? __float_as_uint(i & 1 ? x[i >> 1].y : x[i >> 1].x) : 0xff800000u;
+            tm_st16(s_at + c0, u);
+            if constexpr (SPLIT) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) u[i] = 0u;
+              tm_st16(s_at + lo_col + c0, u);
+            }
+          }
+          tm_wait_st();
+          kn = 1.f;
+        }
+        const float2 kn2 = make_float2(kn, kn);
+        const bool vfin = fabsf(vn) < INFINITY;
+        // a norm that counts for the weights' scale: finite, of a token some column here sees (a
+        // stale row may hold any bits)
+        const float vf = seen && real && vfin ? fabsf(vn) : 0.f;
+        const uint32_t sx = (uint32_t)(t_lane & 7);
+        auto p_addr = [&](int c) -> uint32_t { return p_line + (c >> 6) * (kTok * 128) + ((((c & 63) >> 3) ^ sx) << 4); };
+        volatile int* fl = &fail[stream][(k / streams) & 1];
+
+        // Weights with the running maxima as they are; when a column's has to move (or the values'
+        // scale), the tile is taken once more with the new ones.
+        for (bool again = false;; again = true) {
+          const float vs = vf > 0.f ? vn * pow2i(max(-126, min(126, -ve))) : 0.f;
+          const float2 vs2 = make_float2(vs, vs);
+          float over = 0.f;  // largest weight
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = c_first + c_step * g;
+            if (c0 >= cols) continue;
+            float2 x[8];
+            fetch(c0, x);
+            uint32_t o[8], r[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 m4 = *reinterpret_cast<const float4*>(negm_s + col0 + c0 + 4 * i);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float2 y = __ffma2_rn(x[2 * i + e], kn2, e ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
+                y.x = ex2a(y.x);
+                y.y = ex2a(y.y);
+                over = fmaxf(over, fmaxf(y.x, y.y));
+                l[8 * g + 2 * i + e] = __fadd2_rn(l[8 * g + 2 * i + e], y);
+                y = __fmul2_rn(y, vs2);
+                o[2 * i + e] = pack2(y.x, y.y);
+                if constexpr (SPLIT) {
+                  const __half2 hh = *reinterpret_cast<const __half2*>(&o[2 * i + e]);
+                  r[2 * i + e] = pack2((y.x - __low2float(hh)) * kLoP, (y.y - __high2float(hh)) * kLoP);
+                }
+              }
+            }
+            if (g == 0 && !again) {  // the stream's product before is done: P and O are free
+              ok = wait(p_empty(stream), this_p ^ 1) && ok;
+              if (!ok) *fl = 1;
+            }
+            st_v4(p_addr(col0 + c0), o[0], o[1], o[2], o[3]);
+            st_v4(p_addr(col0 + c0 + 8), o[4], o[5], o[6], o[7]);
+            if constexpr (SPLIT) {
+              st_v4(p_addr(col0 + lo_col + c0), r[0], r[1], r[2], r[3]);
+              st_v4(p_addr(col0 + lo_col + c0 + 8), r[4], r[5], r[6], r[7]);
+            }
+          }
+          if (again) break;
+          const bool grow = vf > 0.f && exp_of(vf) - ve > 9;
+          if (!named_any(bar_id, bar_n, over > kMaxWeight || grow || !ok)) break;
+          if (*fl) {  // the same for all warps of the stream
+            broken = true;
+            break;
+          }
+          // Take the tile's weights back out of the sums (a weight that moves a maximum leaves a
+          // rounding of itself, scaled away with it; an infinite one would leave nothing of the
+          // sum either), and find the columns' maxima over the four lane quadrants.
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = c_first + c_step * g;
+            if (c0 >= cols) continue;
+            float2 x[8];
+            fetch(c0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 m2 = *reinterpret_cast<const float2*>(negm_s + col0 + c0 + 2 * i);
+              const float2 y = __ffma2_rn(x[i], kn2, m2);
+              float2& li = l[8 * g + i];
+              li.x = li.x == INFINITY ? 0.f : li.x - ex2a(y.x);
+              li.y = li.y == INFINITY ? 0.f : li.y - ex2a(y.y);
+              const int ta = __reduce_max_sync(kFullMask, ord_int(x[i].x * kn));
+              const int tb = __reduce_max_sync(kFullMask, ord_int(x[i].y * kn));
+              if (lane == 0) {
+                part_s[quad * C::kN + col0 + c0 + 2 * i] = ord_float(ta);
+                part_s[quad * C::kN + col0 + c0 + 2 * i + 1] = ord_float(tb);
+              }
+            }
+          }
+          const int vmax = __reduce_max_sync(kFullMask, __float_as_int(vf));
+          if (lane == 0) vpart[sw] = vmax;
+          named_sync(bar_id, bar_n);
+          int vall = 0;
+          for (int i = 0; i < 4 * sets; ++i) vall = max(vall, vpart[4 * sets * stream + i]);
+          float vscale = 1.f;
+          if (vall > 0) {
+            const int e = exp_of(__int_as_float(vall));
+            if (e - ve > 9) {  // the largest norm so far to 2^6
+              const int ne = e - 6;
+              vscale = ve == -1000 ? 1.f : pow2i(max(-126, ve - ne));
+              ve = ne;
+            }
+          }
+          const int c = stid - 128 * sets * stream;  // a column for each thread of the stream
+          if (c < cols) {
+            float top = part_s[col0 + c];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) top = fmaxf(top, part_s[i * C::kN + col0 + c]);
+            const float old = -negm_s[col0 + c];
+            const bool up = top > old + kSlack;
+            corr_s[col0 + c] = up ? ex2a(old - top) : 1.f;
+            if (up) negm_s[col0 + c] = -top;
+          }
+          named_sync(bar_id, bar_n);
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = c_first + c_step * g;
+            if (c0 >= cols) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              l[8 * g + i] = __fmul2_rn(l[8 * g + i], *reinterpret_cast<const float2*>(corr_s + col0 + c0 + 2 * i));
+          }
+          if (k >= streams) {
+            tc_after();
+#pragma unroll 1
+            for (int c0 = c_first; c0 < cols; c0 += c_step) {
+#pragma unroll 1
+              for (int i2 = 0; i2 < (SPLIT ? 2 : 1) * C::kHalves; ++i2) {
+                const uint32_t at = lanes + C::kO + (SPLIT ? i2 >> 1 : i2) * C::kN + col0 +
+                                    (SPLIT && (i2 & 1) ? lo_col : 0) + c0;
+                uint32_t u[16];
+                tm_ld16(at, u);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  u[i] = __float_as_uint(__uint_as_float(u[i]) * (corr_s[col0 + c0 + i] * vscale));
+                tm_st16(at, u);
+              }
+            }
+            tm_wait_st();
+          }
+        }
+        if (broken) continue;
+        if (__any_sync(kFullMask, real && seen && !vfin)) {
+          // a value norm that is infinite or NaN: where its token has weight, the output takes it
+          // (its weights above were zero)
+#pragma unroll 1
+          for (int c0 = c_first; c0 < cols; c0 += c_step) {
+            float2 x[8];
+            fetch(c0, x);
+            if (!vfin && real && seen) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float y = (i & 1 ? x[i >> 1].y : x[i >> 1].x) * kn + negm_s[col0 + c0 + i];
+                const uint32_t at = p_addr(col0 + c0 + (i & 8)) + 2 * (i & 7);
+                const uint16_t v = !(ex2a(y) == 0.f) ? __half_as_ushort(__float2half_rn(vn)) : (uint16_t)0;
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(at), "h"(v) : "memory");
+              }
+            }
+          }
+        }
+        fence_async();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive_n(s_empty(sb), weight);
+          bar_arrive_n(p_full(stream), weight);
+        }
+      }
+
+      // ---- outputs of the window
+      const int live = min(streams, tiles);  // streams that took a tile
+      if (stream < live && !broken && !wait(p_empty(stream), ((pph >> stream) & 1) ^ 1)) broken = true;
+      if (broken) *(volatile int*)&fail_all = 1;
+      // sums over the 128 lanes
+#pragma unroll
+      for (int g = 0; g < C::kGroups; ++g) {
+        const int c0 = c_first + c_step * g;
+        if (c0 >= cols) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float sa = warp_sum(l[8 * g + i].x), sc = warp_sum(l[8 * g + i].y);
+          if (lane == 0) {
+            part_s[quad * C::kN + col0 + c0 + 2 * i] = sa;
+            part_s[quad * C::kN + col0 + c0 + 2 * i + 1] = sc;
+          }
+        }
+      }
+      if (lane == 0 && (sw % (4 * sets)) == 0) ve_s[stream] = ve == -1000 ? 0 : ve;
+      soft_sync();
+      if (*(volatile int*)&fail_all) return false;
+      tc_after();
+      if (stid < cols) {  // streams -> window: factors of their O^T
+        const float ma = -negm_s[stid], mb = live > 1 ? -negm_s[pitch + stid] : kNoMax;
+        const float top = fmaxf(ma, mb);
+        const float fa = ex2a(ma - top), fb = live > 1 ? ex2a(mb - top) : 0.f;
+        auto sum4 = [&](int c) -> float {
+          return (part_s[c] + part_s[C::kN + c]) + (part_s[2 * C::kN + c] + part_s[3 * C::kN + c]);
+        };
+        top_s[stid] = top;
+        sum_s[stid] = fa * sum4(stid) + (live > 1 ? fb * sum4(pitch + stid) : 0.f);
+        corr_s[stid] = fa * inv_av * pow2i(max(-126, min(126, ve_s[0])));
+        if (live > 1) corr_s[pitch + stid] = fb * inv_av * pow2i(max(-126, min(126, ve_s[1])));
+      }
+      soft_sync();
+      const bool whole = first == 0 && last == win.nA + win.nB;
+      // this lane's dim of columns c0 .. c0 + 15 (half hf of the dims)
+      auto load_o = [&](int hf, int c0, float (&x)[16]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+#pragma unroll 1
+        for (int s = 0; s < live; ++s) {
+          uint32_t u[16];
+          tm_ld16(lanes + C::kO + hf * C::kN + s * pitch + c0, u);
+          if constexpr (SPLIT) {
+            uint32_t v[16];
+            tm_ld16(lanes + C::kO + hf * C::kN + s * pitch + lo_col + c0, v);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              u[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), 1.0f / kLoP, __uint_as_float(u[i])));
+          } else {
+            tm_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(u[i]), corr_s[s * pitch + c0 + i], x[i]);
+        }
+      };
+      const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * w.cols;
+      if (!whole) {
+        if (stid < cols) {
+          w.ml[2 * (slot0 + stid)] = top_s[stid];
+          w.ml[2 * (slot0 + stid) + 1] = sum_s[stid];
+        }
+#pragma unroll 1
+        for (int c0 = 16 * set; c0 < cols; c0 += 16 * kSoftSets)
+#pragma unroll 1
+          for (int hf = 0; hf < C::kHalves; ++hf) {
+            float x[16];
+            load_o(hf, c0, x);
+            if (D == 64 && quad >= 2) continue;  // lanes 64.. repeat the 64 dims
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c0 + i < cols) w.acc[(slot0 + c0 + i) * D + hf * 128 + t_lane] = x[i];
+          }
+      } else {
+        float* stage = reinterpret_cast<float*>(smem + C::kOffP);  // [kStageCols][D]
+        for (int r0 = 0; r0 < cols; r0 += C::kStageCols) {
+          const int r1 = min(cols, r0 + C::kStageCols);
+#pragma unroll 1
+          for (int c0 = r0 + 16 * set; c0 < r1; c0 += 16 * kSoftSets)
+#pragma unroll 1
+            for (int hf = 0; hf < C::kHalves; ++hf) {
+              float x[16];
+              load_o(hf, c0, x);
+              if (D == 64 && quad >= 2) continue;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (c0 + i < r1) stage[(c0 + i - r0) * D + hf * 128 + t_lane] = x[i];
+            }
+          soft_sync();
+          for (int c = r0 + sw; c < r1; c += kSoftWarps) {
+            float v[D / 32];
+            const float s = sum_s[c];
+            const float inv = s != 0.f ? 1.f / (s * sqrtf((float)D)) : 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) v[i] = stage[(c - r0) * D + lane * (D / 32) + i] * inv;
+            fwht_warp<D / 32>(v);
+            const int64_t at = ((int64_t)(win.row0 + c / G) * a.num_q_heads + h * G + c % G) * D + lane * (D / 32);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) v[i] *= sgn[i];
+            store_row<D / 32, SPLIT>(a.out, at, o_vec, v);
+          }
+          soft_sync();
+        }
+      }
+      tc_before();
+      soft_sync();  // the arrays and O are free for the next window
+      return true;
+    });
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsIssue));
+    if (warp == kCopyWarp) {
     // ------------------------------------------------ copies of packed rows
     const int bs = a.block_size, sub = p.sub;
     const int cap = (int)min((int64_t)a.max_blocks_per_seq * bs, (int64_t)0x7fffff00);
     uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::kOffMeta);
     const uint32_t per_copy = (uint32_t)(sub * (spk + spv));
-    int st = 0, ph = 0;
-    int last_ph[kMaxRing];
-#pragma unroll
-    for (int s = 0; s < kMaxRing; ++s) last_ph[s] = -1;
+    int st = 0, ph = 0, issued = 0;
     for_windows([&](const AttnWindow& win, int first, int last) -> bool {
       const int32_t* table = a.block_table + (int64_t)win.seq * a.max_blocks_per_seq;
       const int hi = min(max(win.p_hi, win.w_hi), cap);
@@ -638,60 +1221,70 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (!p.tma) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(raw_full(st)) : "memory");
         if (lane == 0) bar_arrive(raw_full(st));
-#pragma unroll
-        for (int s = 0; s < kMaxRing; ++s)
-          if (s == st) last_ph[s] = ph;
+        ++issued;
         if (++st == p.ring) st = 0, ph ^= 1;
       }
       return true;
     });
     if (!p.tma) asm volatile("cp.async.wait_all;\n" ::: "memory");
     // none of the copies outlives the loop
-#pragma unroll
-    for (int s = 0; s < kMaxRing; ++s)
-      if (last_ph[s] >= 0)
-        for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(raw_full(s), last_ph[s]); ++i) {
-        }
-  } else if (warp == kMmaWarp) {
+    for (int n = max(0, issued - p.ring); n < issued; ++n)
+      for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(raw_full(n % p.ring), (n / p.ring) & 1); ++i) {
+      }
+    } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issue
     if (lane == 0) {
-      const uint32_t q_at = base + C::kOffQ, v_at = base + C::kOffV, p_at = base + C::kOffP;
-      int it = 0, unit = 0;
+      // (offsets are added to the low words in units of 16 bytes: no carry leaves the address)
+      const uint32_t q_at = desc_low(base + C::kOffQ, 16), v_at = desc_low(base + C::kOffV, D == 64 ? 0 : 64 * 128);
+      const uint32_t p_at = desc_low(base + C::kOffP, kTok * 128);
+      int it = 0, unit = 0, vslot = 0, vph = 0;
+      uint32_t sph = 0, pph = 0;  // phases of the score buffers and of the streams' weights
       bool issued = false;
       for_windows([&](const AttnWindow& win, int first, int last) -> bool {
-        const int n = SPLIT ? 2 * pad_cols(win) : pad_cols(win);
+        const int padded = pad_cols(win), n = SPLIT ? 2 * padded : padded;
+        const int streams = streams_of(padded), pitch = C::kN / streams, tiles = last - first;
         const uint32_t ids = mma_idesc(n, false), idp = mma_idesc(n, true);
         if (!wait1(q_full, unit & 1)) return false;
         ++unit;
-        auto weigh = [&](int j, bool acc) -> bool {  // O^T += V^T P^T of tile j
-          const int b = j % C::kVBufs;
-          if (!wait1(p_full, j & 1) || !wait1(v_full(b), (j / C::kVBufs) & 1)) return false;
-          tc_after();
+        auto weigh = [&](int k) -> bool {  // O^T of its stream += V^T P^T of the window's tile k
+          const int s = k & (streams - 1);
+          if (!wait1(p_full(s), (pph >> s) & 1)) return false;
+          pph ^= 1u << s;
+          const uint32_t p_s = p_at + (uint32_t)((((s * pitch) >> 6) * (kTok * 128) + ((s * pitch) & 63) * 2) >> 4);
+          const uint32_t o_s = tmem + C::kO + s * pitch;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (!wait1(v_full(vslot), vph)) return false;
+            tc_after();
 #pragma unroll
-          for (int hf = 0; hf < C::kHalves; ++hf)
+            for (int hf = 0; hf < C::kHalves; ++hf)
 #pragma unroll
-            for (int ks = 0; ks < kTok / 16; ++ks)
-              mma_ss(tmem + C::kO + hf * C::kN,
-                     sw128_desc(v_at + b * C::kVBytes + hf * 2 * kTok * 128 + ks * 2048, D == 64 ? 0 : kTok * 128, 1024),
-                     sw128_desc(p_at + ks * 2048, kTok * 128, 1024), idp, acc || ks > 0);
-          tc_commit(v_empty(b));
-          tc_commit(p_empty);
+              for (int ks = 0; ks < kTok / 32; ++ks)
+                mma_ss(o_s + hf * C::kN, v_at + ((vslot * C::kVBytes + hf * 2 * 64 * 128 + ks * 2048) >> 4),
+                       p_s + ((half * (kTok / 2 * 128) + ks * 2048) >> 4), idp, k >= streams || half > 0 || ks > 0);
+            tc_commit(v_empty(vslot));
+            if (++vslot == C::kVSlots) vslot = 0, vph ^= 1;
+          }
+          tc_commit(p_empty(s));
           return true;
         };
-        for (int t = first; t < last; ++t, ++it) {
-          const int b = it & 1;
-          if (!wait1(k_full(b), (it >> 1) & 1) || !wait1(s_empty(b), ((it >> 1) & 1) ^ 1)) return false;
+        for (int k = 0; k < tiles; ++k, ++it) {
+          const int b = it & 1, sb = k & (2 * streams - 1);
+          if (!wait1(k_full(b), (it >> 1) & 1) || !wait1(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
+          sph ^= 1u << sb;
           tc_after();
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_ts(tmem + C::kS + b * C::kN, tmem + C::kK + b * C::kKCols + ks * 8,
-                   sw128_desc(q_at + (ks >> 2) * (C::kN * 128) + (ks & 3) * 32, 16, 1024), ids, ks > 0);
+            mma_ts(tmem + C::kS + sb * pitch, tmem + C::kK + b * C::kKCols + ks * 8,
+                   q_at + (((ks >> 2) * (C::kN * 128) + (ks & 3) * 32) >> 4), ids, ks > 0);
           issued = true;
-          tc_commit(s_full(b));
+          tc_commit(s_full(sb));
           tc_commit(k_empty(b));
-          if (t > first && !weigh(it - 1, t - 1 > first)) return false;
+          if (k >= streams && !weigh(k - streams)) return false;
         }
-        return weigh(it - 1, last - 1 > first);
+        for (int k = max(0, tiles - streams); k < tiles; ++k)
+          if (!weigh(k)) return false;
+        return true;
       });
       if (issued) {  // every MMA has finished before TMEM is freed
         tc_commit(drained);
@@ -700,443 +1293,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------ softmax, queries and outputs
-    const int sw = warp - kKeyWarps - kValWarps;  // softmax warp
-    const int quad = warp & 3, set = sw >> 2;
-    const int stid = tid - 32 * (kKeyWarps + kValWarps);
-    const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
-    RowView* rows = reinterpret_cast<RowView*>(smem + C::kOffRows);
-    float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -max; -inf where there is no column
-    float* mu_s = negm_s + C::kN;   // the same, 0 while a column has seen nothing
-    float* corr_s = mu_s + C::kN;
-    float* slope_s = corr_s + C::kN;
-    int* pos_s = reinterpret_cast<int*>(slope_s + C::kN);
-    float* part_s = slope_s + 2 * C::kN;  // [4][kN]
-    __shared__ int vpart[kSoftWarps];
-    const uint32_t* valid = reinterpret_cast<const uint32_t*>(smem + C::kOffMeta);
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    const uint32_t krow = ring + (uint32_t)(t_lane * spk + skip_k + rbk - 4);
-    const uint32_t vrow = ring + (uint32_t)(kTok * spk + t_lane * spv + skip_v + rbv - 4);
-    const uint32_t p_line = base + C::kOffP + (uint32_t)((t_lane >> 3) * 1024 + (t_lane & 7) * 128);
-    const float scale = a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)D);
-    const bool capped = a.softcap > 0.f, biased = a.alibi != nullptr;
-    // capped scores: tanh(s / cap) from 2^(2 log2(e) s / cap)
-    const float qmul = (capped ? 2.f * scale / a.softcap : scale) * kLog2eA / (sqrtf((float)D) * a.k_alpha);
-    const float cap2 = a.softcap * kLog2eA;
-    const float inv_av = 1.0f / a.v_alpha;
-    int st = 0, ph = 0, it = 0;
-
-    for_windows([&](const AttnWindow& win, int first, int last) -> bool {
-      const int cols = win.nrows * G, padded = pad_cols(win);
-      const int lo_col = SPLIT ? padded : 0;
-      // ---- queries of the window: one power of two for all of them, rotated, hi (and lo)
-      if (stid == 0) {
-        full_lo = pre_lo = 0;
-        full_hi = pre_hi = 0x7fffffff;
-        q_exp = -1000;
-      }
-      soft_sync();
-      if (stid < win.nrows) {
-        const RowView v = row_view(a, win.row0 + stid);
-        rows[stid] = v;
-        atomicMax(&full_lo, v.w0);
-        atomicMin(&full_hi, v.w1);
-        atomicMax(&pre_lo, v.p0);
-        atomicMin(&pre_hi, v.p1);
-      }
-      if (stid < C::kN) {
-        negm_s[stid] = stid < cols ? INFINITY : -INFINITY;  // no column there: never a new max
-        mu_s[stid] = stid < cols ? 0.f : -INFINITY;
-        slope_s[stid] = biased && stid < cols ? a.alibi[h * G + stid % G] * kLog2eA : 0.f;
-        pos_s[stid] = a.q_len && stid < cols ? a.q_len[win.row0 + stid / G] - 1 : 0;
-      }
-      auto q_row = [&](int col, float (&v)[D / 32]) {
-        const int64_t at = ((int64_t)(win.row0 + col / G) * a.num_q_heads + h * G + col % G) * D + lane * (D / 32);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[i] = load_as_f32(a.q, at + i, a.q_dtype);
-      };
-      float most = 0.f;
-      for (int col = sw; col < cols; col += kSoftWarps) {
-        float v[D / 32], ss = 0.f;
-        q_row(col, v);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) ss = fmaf(v[i] * qmul, v[i] * qmul, ss);
-        ss = warp_sum(ss);
-        if (ss < INFINITY) most = fmaxf(most, ss);
-      }
-      if (lane == 0) atomicMax(&q_exp, (exp_of(most) + 1) / 2);
-      soft_sync();
-      // the largest rotated coordinate is at most the norm times sqrt(D): to 2^11 or less
-      const int qe = q_exp + (D == 64 ? 3 : 4) - 10;
-      const float q_down = pow2i(max(-126, min(126, -qe))), q_up = pow2i(max(-126, min(126, qe)));
-      for (int col = sw; col < cols; col += kSoftWarps) {
-        float v[D / 32];
-        q_row(col, v);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) v[i] *= qmul * a.signs[lane * (D / 32) + i];
-        fwht_warp<D / 32>(v);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-          const int d = lane * (D / 32) + i;
-          const float x0 = v[i] * q_down, x1 = v[i + 1] * q_down;
-          const uint32_t hi = pack2(x0, x1);
-          const uint32_t at = (uint32_t)((d >> 6) * (C::kN * 128) + (((d & 63) * 2) & 15));
-          const uint32_t ch = (uint32_t)((d & 63) >> 3);
-          *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + col * 128 + ((ch ^ (col & 7)) << 4)) = hi;
-          if constexpr (SPLIT) {
-            const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
-            const int lc = col + lo_col;
-            *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + lc * 128 + ((ch ^ (lc & 7)) << 4)) =
-                pack2((x0 - __low2float(hh)) * kLoQ, (x1 - __high2float(hh)) * kLoQ);
-          }
-        }
-      }
-      fence_async();
-      soft_sync();
-      if (lane == 0) bar_arrive(q_full);
-
-      // ---- tiles
-      const int hi_tok = max(win.p_hi, win.w_hi);
-      F2 l[C::kGroups * 8];
-#pragma unroll
-      for (int i = 0; i < C::kGroups * 8; ++i) l[i] = f2(0.f, 0.f);
-      int ve = -1000;  // P' = p nu_v 2^-ve (every thread holds the same)
-      for (int t = first; t < last; ++t, ++it) {
-        const int t0 = tile_token(win, t), tok = t0 + t_lane;
-        bool ok = wait(raw_full(st), ph);
-        float kn = __uint_as_float(ld_s32(krow + st * stage_bytes)) * q_up;
-        const float vn = __uint_as_float(ld_s32(vrow + st * stage_bytes));
-        const uint4 vv = *reinterpret_cast<const uint4*>(valid + 4 * st);
-        const uint32_t vq = quad == 0 ? vv.x : quad == 1 ? vv.y : quad == 2 ? vv.z : vv.w;
-        const bool real = ((vq >> lane) & 1u) && tok < hi_tok;
-        const bool all = (vv.x & vv.y & vv.z & vv.w) == 0xffffffffu && ((t0 >= full_lo && t0 + kTok <= full_hi) ||
-                                                                         (t0 >= pre_lo && t0 + kTok <= pre_hi));
-        __syncwarp();
-        if (lane == 0) bar_arrive(raw_empty(st));
-        if (++st == p.ring) st = 0, ph ^= 1;
-        const int sb = it & 1;
-        const uint32_t s_at = lanes + C::kS + sb * C::kN;
-        ok = wait(s_full(sb), (it >> 1) & 1) && ok;
-        tc_after();
-        bool seen = true;  // a column of this thread sees its token
-        if (!all || capped || biased) {
-          // Scores in place: nu_k, cap, distance, -inf where the token is not seen; the passes
-          // below then take them with a factor of one.
-          seen = false;
-#pragma unroll 1
-          for (int c0 = 16 * set; c0 < cols; c0 += 32) {
-            uint32_t see = 0xffffu;  // bit i: column c0 + i
-            if (!all) {
-              see = 0;
-              for (int c = c0; c < c0 + 16 && c < cols && real; c += G) {
-                const int r = c / G;
-                if (row_sees(rows[r], a.mask ? a.mask + (int64_t)(win.row0 + r) * a.mask_words : nullptr, tok))
-                  see |= ((1u << G) - 1u) << (c - c0);
-              }
-            }
-            seen |= see != 0;
-            uint32_t u[16];
-            tm_ld16(s_at + c0, u);
-            if constexpr (SPLIT) {
-              uint32_t v[16];
-              tm_ld16(s_at + lo_col + c0, v);
-              tm_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                u[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), 1.0f / kLoQ, __uint_as_float(u[i])));
-                v[i] = 0u;
-              }
-              tm_st16(s_at + lo_col + c0, v);
-            } else {
-              tm_wait_ld();
-            }
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]) * kn;
-            if (capped) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i])), cap2);
-            }
-            if (biased) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] -= slope_s[c0 + i] * fabsf((float)(pos_s[c0 + i] - tok));
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = (see >> i) & 1u ? __float_as_uint(x[i]) : 0xff800000u;
-            tm_st16(s_at + c0, u);
-          }
-          tm_wait_st();
-          kn = 1.f;
-        }
-        // a norm that counts for the weights' scale: finite, of a token some column here sees (a
-        // stale row may hold any bits)
-        const bool vfin = fabsf(vn) < INFINITY;
-        const float vf = seen && real && vfin ? fabsf(vn) : 0.f;
-        const F2 kn2 = f2(kn, kn);
-        auto load_s = [&](int c0, F2 (&x)[8]) {
-          uint32_t u[16];
-          tm_ld16(s_at + c0, u);
-          if constexpr (SPLIT) {
-            uint32_t v[16];
-            tm_ld16(s_at + lo_col + c0, v);
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              x[i] = fma2(f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2(1.0f / kLoQ, 1.0f / kLoQ),
-                          f2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
-          } else {
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = f2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-          }
-        };
-        // ---- does a column's max move by more than the slack, or the weights' scale?
-        float over = -INFINITY;
-#pragma unroll 1
-        for (int c0 = 16 * set; c0 < cols; c0 += 32) {
-          F2 x[8];
-          load_s(c0, x);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 m4 = *reinterpret_cast<const float4*>(negm_s + c0 + 4 * i);
-            const F2 ya = fma2(x[2 * i], kn2, f2(m4.x, m4.y)), yb = fma2(x[2 * i + 1], kn2, f2(m4.z, m4.w));
-            over = fmaxf(over, fmaxf(ya.f.x, ya.f.y));
-            over = fmaxf(over, fmaxf(yb.f.x, yb.f.y));
-          }
-        }
-        const bool grow = vf > 0.f && exp_of(vf) - ve > 9;
-        ok = wait(p_empty, (it & 1) ^ 1) && ok;  // the product of the tile before is done: P and O are free
-        if (!ok) *(volatile int*)&fail[it & 1] = 1;
-        const bool move = soft_any(over > kSlack || grow);
-        if (*(volatile int*)&fail[it & 1]) return false;  // the same for all softmax warps
-        tc_after();
-        if (move) {
-          // new maxima per column over the four lane quadrants, then the scale of the values
-#pragma unroll 1
-          for (int c0 = 16 * set; c0 < cols; c0 += 32) {
-            F2 x[8];
-            load_s(c0, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int ta = __reduce_max_sync(kFullMask, ord_int(x[i].f.x * kn));
-              const int tb = __reduce_max_sync(kFullMask, ord_int(x[i].f.y * kn));
-              if (lane == 0) {
-                part_s[quad * C::kN + c0 + 2 * i] = ord_float(ta);
-                part_s[quad * C::kN + c0 + 2 * i + 1] = ord_float(tb);
-              }
-            }
-          }
-          const int vmax = __reduce_max_sync(kFullMask, __float_as_int(vf));
-          if (lane == 0) vpart[sw] = vmax;
-          soft_sync();
-          int vall = 0;
-#pragma unroll
-          for (int k = 0; k < kSoftWarps; ++k) vall = max(vall, vpart[k]);
-          float vscale = 1.f;
-          if (vall > 0) {
-            const int e = exp_of(__int_as_float(vall));
-            if (e - ve > 9) {  // the largest norm so far to 2^6
-              const int ne = e - 6;
-              vscale = ve == -1000 ? 1.f : pow2i(max(-126, ve - ne));
-              ve = ne;
-            }
-          }
-          if (stid < cols) {
-            float top = part_s[stid];
-#pragma unroll
-            for (int k = 1; k < 4; ++k) top = fmaxf(top, part_s[k * C::kN + stid]);
-            const float old = -negm_s[stid];
-            const bool up = top > old + kSlack;
-            corr_s[stid] = up ? ex2a(old - top) : 1.f;
-            if (up) {
-              negm_s[stid] = -top;
-              mu_s[stid] = -top;
-            }
-          }
-          soft_sync();
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const int c0 = 16 * set + 32 * g;
-            if (c0 >= cols) continue;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = *reinterpret_cast<const float2*>(corr_s + c0 + 2 * i);
-              l[8 * g + i] = mul2(l[8 * g + i], f2(f.x, f.y));
-            }
-          }
-          if (t > first) {
-#pragma unroll 1
-            for (int c0 = 16 * set; c0 < cols; c0 += 32) {
-#pragma unroll 1
-              for (int k = 0; k < (SPLIT ? 2 : 1) * C::kHalves; ++k) {
-                const uint32_t at = lanes + C::kO + (SPLIT ? k >> 1 : k) * C::kN + (SPLIT && (k & 1) ? lo_col : 0) + c0;
-                uint32_t u[16];
-                tm_ld16(at, u);
-                tm_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  u[i] = __float_as_uint(__uint_as_float(u[i]) * (corr_s[c0 + i] * vscale));
-                tm_st16(at, u);
-              }
-            }
-            tm_wait_st();
-          }
-        }
-        // ---- weights
-        const float vs = vfin && real && seen ? vn * pow2i(max(-126, min(126, -ve))) : 0.f;
-        const F2 vs2 = f2(vs, vs);
-        const uint32_t sx = (uint32_t)(t_lane & 7);
-        auto p_addr = [&](int c) -> uint32_t { return p_line + (c >> 6) * (kTok * 128) + ((((c & 63) >> 3) ^ sx) << 4); };
-#pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
-          const int c0 = 16 * set + 32 * g;
-          if (c0 >= cols) continue;
-          F2 x[8];
-          load_s(c0, x);
-          uint32_t o[8], r[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 m2 = *reinterpret_cast<const float2*>(mu_s + c0 + 2 * i);
-            x[i] = fma2(x[i], kn2, f2(m2.x, m2.y));
-            x[i].f.x = ex2a(x[i].f.x);
-            x[i].f.y = ex2a(x[i].f.y);
-            l[8 * g + i] = add2(l[8 * g + i], x[i]);
-            x[i] = mul2(x[i], vs2);
-            o[i] = pack2(x[i].f.x, x[i].f.y);
-            if constexpr (SPLIT) {
-              const __half2 hh = *reinterpret_cast<const __half2*>(&o[i]);
-              r[i] = pack2((x[i].f.x - __low2float(hh)) * kLoP, (x[i].f.y - __high2float(hh)) * kLoP);
-            }
-          }
-          st_v4(p_addr(c0), o[0], o[1], o[2], o[3]);
-          st_v4(p_addr(c0 + 8), o[4], o[5], o[6], o[7]);
-          if constexpr (SPLIT) {
-            st_v4(p_addr(c0 + lo_col), r[0], r[1], r[2], r[3]);
-            st_v4(p_addr(c0 + lo_col + 8), r[4], r[5], r[6], r[7]);
-          }
-        }
-        if (__any_sync(kFullMask, real && seen && !vfin)) {
-          // a value norm that is infinite or NaN: where its token has weight, the output takes it
-          // (its weights above were zero)
-#pragma unroll 1
-          for (int c0 = 16 * set; c0 < cols; c0 += 32) {
-            F2 x[8];
-            load_s(c0, x);
-            if (!vfin && real && seen) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float y = (i & 1 ? x[i >> 1].f.y : x[i >> 1].f.x) * kn + mu_s[c0 + i];
-                const uint32_t at = p_addr(c0 + (i & 8)) + 2 * (i & 7);
-                const uint16_t v = !(ex2a(y) == 0.f) ? __half_as_ushort(__float2half_rn(vn)) : (uint16_t)0;
-                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(at), "h"(v) : "memory");
-              }
-            }
-          }
-        }
-        fence_async();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(s_empty(sb));
-          bar_arrive(p_full);
-        }
-      }
-
-      // ---- outputs of the window
-      const bool ok = wait(p_empty, (it - 1) & 1);
-      if (!ok) *(volatile int*)&fail[it & 1] = 1;
-      // sums over the 128 lanes
-#pragma unroll
-      for (int g = 0; g < C::kGroups; ++g) {
-        const int c0 = 16 * set + 32 * g;
-        if (c0 >= cols) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float sa = warp_sum(l[8 * g + i].f.x), sb2 = warp_sum(l[8 * g + i].f.y);
-          if (lane == 0) {
-            part_s[quad * C::kN + c0 + 2 * i] = sa;
-            part_s[quad * C::kN + c0 + 2 * i + 1] = sb2;
-          }
-        }
-      }
-      soft_sync();
-      if (*(volatile int*)&fail[it & 1]) return false;
-      tc_after();
-      const bool whole = first == 0 && last == win.nA + win.nB;
-      const float up = pow2i(max(-126, min(126, ve == -1000 ? 0 : ve))) * inv_av;
-      auto sum_of = [&](int c) -> float {
-        return (part_s[c] + part_s[C::kN + c]) + (part_s[2 * C::kN + c] + part_s[3 * C::kN + c]);
-      };
-      // this lane's dim of columns c0 .. c0 + 15 (half hf of the dims)
-      auto load_o = [&](int hf, int c0, float (&x)[16]) {
-        uint32_t u[16];
-        tm_ld16(lanes + C::kO + hf * C::kN + c0, u);
-        if constexpr (SPLIT) {
-          uint32_t v[16];
-          tm_ld16(lanes + C::kO + hf * C::kN + lo_col + c0, v);
-          tm_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            x[i] = fmaf(__uint_as_float(v[i]), 1.0f / kLoP, __uint_as_float(u[i])) * up;
-        } else {
-          tm_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]) * up;
-        }
-      };
-      const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * w.cols;
-      if (!whole) {
-        if (stid < cols) {
-          w.ml[2 * (slot0 + stid)] = -negm_s[stid];
-          w.ml[2 * (slot0 + stid) + 1] = sum_of(stid);
-        }
-#pragma unroll 1
-        for (int c0 = 16 * set; c0 < cols; c0 += 32)
-#pragma unroll 1
-          for (int hf = 0; hf < C::kHalves; ++hf) {
-            float x[16];
-            load_o(hf, c0, x);
-            if (D == 64 && quad >= 2) continue;  // lanes 64.. repeat the 64 dims
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c0 + i < cols) w.acc[(slot0 + c0 + i) * D + hf * 128 + t_lane] = x[i];
-          }
-      } else {
-        float* stage = reinterpret_cast<float*>(smem + C::kOffP);  // [kStageCols][D]
-        for (int r0 = 0; r0 < cols; r0 += C::kStageCols) {
-          const int r1 = min(cols, r0 + C::kStageCols);
-#pragma unroll 1
-          for (int c0 = r0 + 16 * set; c0 < r1; c0 += 32)
-#pragma unroll 1
-            for (int hf = 0; hf < C::kHalves; ++hf) {
-              float x[16];
-              load_o(hf, c0, x);
-              if (D == 64 && quad >= 2) continue;
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (c0 + i < r1) stage[(c0 + i - r0) * D + hf * 128 + t_lane] = x[i];
-            }
-          soft_sync();
-          for (int c = r0 + sw; c < r1; c += kSoftWarps) {
-            float v[D / 32];
-            const float s = sum_of(c);
-            const float inv = s != 0.f ? 1.f / (s * sqrtf((float)D)) : 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) v[i] = stage[(c - r0) * D + lane * (D / 32) + i] * inv;
-            fwht_warp<D / 32>(v);
-            const int64_t at = ((int64_t)(win.row0 + c / G) * a.num_q_heads + h * G + c % G) * D + lane * (D / 32);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              store_from_f32(a.out, at + i, a.out_dtype, v[i] * a.signs[lane * (D / 32) + i]);
-          }
-          soft_sync();
-        }
-      }
-      tc_before();
-      soft_sync();  // the arrays and O are free for the next window
-      return true;
-    });
+    }
   }
 
   tc_before();
@@ -1195,11 +1352,12 @@ cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream)
   // number of 16 bytes), and slot numbers that a 32-bit coordinate holds
   t.tma = sub >= 8 && ks % 16 == 0 && vs % 16 == 0 && slots > 0 && slots < 0x7fffffffLL &&
           page_map(&km, a.k_pages, slots, ks, spk, sub) && page_map(&vm, a.v_pages, slots, vs, spv, sub);
-  constexpr int limit = 227 * 1024 - 2048;  // the static arrays take their part
+  constexpr int limit = 227 * 1024 - 1024;  // the static arrays take their part
   const int stage = kTok * (spk + spv);
-  t.ring = std::min(kMaxRing, (limit - 1024 - C::kOffRing) / stage);
+  const int fixed = 1024 + C::kOffTab + key_table_bytes(a.k_bits) + value_table_bytes(a.v_bits);
+  t.ring = std::min(kMaxRing, (limit - fixed) / stage);
   if (t.ring < 2) return cudaErrorInvalidValue;
-  const int smem = 1024 + C::kOffRing + t.ring * stage;
+  const int smem = fixed + t.ring * stage;
   auto kern = attn_tc_kernel<D, SPLIT>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
