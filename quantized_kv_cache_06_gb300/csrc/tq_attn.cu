@@ -66,8 +66,43 @@ __device__ __forceinline__ int block_scan(int v, int* tmp) {
   return v;
 }
 
-// One CTA: windows, their visible tiles and the tile prefix.
+// CTA 0: windows, their visible tiles and the tile prefix.  The others (tensor-core kernel; D its
+// head dim, else 0): the queries rotated, one warp per (row, q head).
+template <int D>
 __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(AttnArgs a, AttnWork w) {
+  if constexpr (D > 0) {
+    if (blockIdx.x > 0) {
+      constexpr int E = D / 32;
+      const int lane = threadIdx.x & 31;
+      const int64_t id = (int64_t)(blockIdx.x - 1) * (kSchedThreads / 32) + (threadIdx.x >> 5);
+      pdl_launch();
+      if (id >= (int64_t)a.num_rows * a.num_q_heads) return;
+      float v[E];
+      const int64_t at = id * D + lane * E;
+      if (reinterpret_cast<uintptr_t>(a.q) % 16 != 0) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = load_as_f32(a.q, at + i, a.q_dtype);
+      } else if (a.q_dtype == kF32) {
+        load_chunk<float, E>(static_cast<const float*>(a.q) + at, v);
+      } else if (a.q_dtype == kF16) {
+        load_chunk<__half, E>(static_cast<const __half*>(a.q) + at, v);
+      } else {
+        load_chunk<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(a.q) + at, v);
+      }
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        v[i] *= w.q_mul * __ldg(a.signs + lane * E + i);
+        ss = fmaf(v[i], v[i], ss);
+      }
+      fwht_warp<E>(v);
+#pragma unroll
+      for (int i = 0; i < E; ++i) w.q_rot[at + i] = v[i];
+      ss = warp_sum(ss);
+      if (lane == 0) w.q_norm2[id] = ss;
+      return;
+    }
+  }
   __shared__ int tmp[33];
   __shared__ int carry_start, carry_win, carry_tiles;
   const int tid = threadIdx.x, T = a.num_rows;
@@ -351,8 +386,9 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
 constexpr int kCombineWarps = 8;
 
 // One warp per (row, q head): merges the pieces of a window that several parts hold, and
-// zeroes the rows that see nothing.
-template <int D>
+// zeroes the rows that see nothing.  Rows of the tensor-core kernel are rotated back here, those
+// of the SIMT kernel that one CTA finished are done.
+template <int D, bool TC>
 __global__ void __launch_bounds__(kCombineWarps * 32) attn_combine_kernel(AttnArgs a, AttnWork w) {
   constexpr int E = (D + 31) / 32;
   __shared__ float buf_s[kCombineWarps][D];
@@ -371,7 +407,17 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attn_combine_kernel(AttnAr
   const int total = w.head->total_tiles, base = win->tile_base;
   const int parts = live_parts(w, total);
   const int c0 = part_of(total, base, parts), c1 = part_of(total, base + n - 1, parts);
-  if (c0 == c1) return;
+  if (c0 == c1) {
+    if constexpr (TC) {
+      float v[E];
+      load_floats<E>(w.q_rot + id * D + lane * E, v);
+      fwht_warp<E>(v);
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        store_from_f32(a.out, id * D + lane * E + i, a.out_dtype, v[i] * __ldg(a.signs + lane * E + i));
+    }
+    return;
+  }
   const int col = (row - win->row0) * G + qh % G;
   auto slot_of = [&](int c) -> int64_t { return (((int64_t)c * H + h) * 2 + (c == c0 ? 1 : 0)) * w.cols + col; };
   float top = -INFINITY;
@@ -390,7 +436,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) attn_combine_kernel(AttnAr
     for (int e = 0; e < E; ++e)
       if (D >= 32 || lane < D) o[e] = fmaf(f, w.acc[s * D + lane + 32 * e], o[e]);
   }
-  const float inv = sum != 0.f ? 1.f / (sum * sqrtf((float)D)) : 0.f;
+  // (the tensor-core kernel's pieces hold 1 / sqrt(D) already)
+  const float inv = sum != 0.f ? (TC ? 1.f / sum : 1.f / (sum * sqrtf((float)D))) : 0.f;
   float* buf = buf_s[warp];
 #pragma unroll
   for (int e = 0; e < E; ++e)
@@ -427,12 +474,12 @@ cudaError_t launch_simt(const AttnArgs& a, const AttnWork& w, cudaStream_t strea
   return launch_after(attn_simt_kernel<D>, w.parts * a.num_kv_heads, kSimtWarps * 32, smem, stream, a, w);
 }
 
-template <int D>
+template <int D, bool TC = false>
 cudaError_t launch_combine(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
   const int64_t warps = (int64_t)a.num_rows * a.num_q_heads;
   const int64_t grid = (warps + kCombineWarps - 1) / kCombineWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_after(attn_combine_kernel<D>, (int)grid, kCombineWarps * 32, 0, stream, a, w);
+  return launch_after(attn_combine_kernel<D, TC>, (int)grid, kCombineWarps * 32, 0, stream, a, w);
 }
 
 }  // namespace
@@ -451,7 +498,10 @@ AttnPlan plan_attn(const AttnArgs& a, int num_sms) {
   p.off_acc = up(p.off_row_window + rows * sizeof(int));
   const size_t slots = (size_t)p.parts * a.num_kv_heads * 2 * p.cols;
   p.off_ml = up(p.off_acc + slots * a.head_dim * sizeof(float));
-  p.workspace_bytes = up(p.off_ml + slots * 2 * sizeof(float));
+  p.off_rot = up(p.off_ml + slots * 2 * sizeof(float));
+  const size_t qs = p.tc ? rows * a.num_q_heads : 0;
+  p.off_norm2 = up(p.off_rot + qs * a.head_dim * sizeof(float));
+  p.workspace_bytes = up(p.off_norm2 + qs * sizeof(float));
   return p;
 }
 
@@ -467,13 +517,32 @@ cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t strea
   w.cols = p.cols;
   w.parts = p.parts;
   w.rows_per_window = p.cols / (a.num_q_heads / a.num_kv_heads);
-  attn_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, w);
+  w.q_rot = reinterpret_cast<float*>(ws + p.off_rot);
+  w.q_norm2 = reinterpret_cast<float*>(ws + p.off_norm2);
+  if (p.tc) {
+    // scale, log2 e, the rotation's 1 / sqrt(D) and the keys' alpha in one factor; capped scores
+    // are taken as 2 log2(e) s / cap, whose power of two gives the tanh
+    const float scale = a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)a.head_dim);
+    w.q_mul = (a.softcap > 0.f ? 2.f * scale / a.softcap : scale) * kAttnLog2e / (sqrtf((float)a.head_dim) * a.k_alpha);
+    const int64_t ctas = ((int64_t)a.num_rows * a.num_q_heads + kSchedThreads / 32 - 1) / (kSchedThreads / 32) + 1;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (a.head_dim == 64) attn_schedule_kernel<64><<<(int)ctas, kSchedThreads, 0, stream>>>(a, w);
+    else if (a.head_dim == 128) attn_schedule_kernel<128><<<(int)ctas, kSchedThreads, 0, stream>>>(a, w);
+    else attn_schedule_kernel<256><<<(int)ctas, kSchedThreads, 0, stream>>>(a, w);
+  } else {
+    attn_schedule_kernel<0><<<1, kSchedThreads, 0, stream>>>(a, w);
+  }
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   count_launches(1);
   if (p.tc) {
     err = launch_attn_tc(a, w, stream);
-  } else switch (a.head_dim) {
+    if (err != cudaSuccess) return err;
+    if (a.head_dim == 64) return launch_combine<64, true>(a, w, stream);
+    if (a.head_dim == 128) return launch_combine<128, true>(a, w, stream);
+    return launch_combine<256, true>(a, w, stream);
+  }
+  switch (a.head_dim) {
     case 16: err = launch_simt<16>(a, w, stream); break;
     case 32: err = launch_simt<32>(a, w, stream); break;
     case 64: err = launch_simt<64>(a, w, stream); break;

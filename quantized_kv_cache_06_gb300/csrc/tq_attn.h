@@ -71,7 +71,7 @@ struct AttnPlan {
   bool tc;          // tensor-core kernel (else the SIMT kernel)
   int cols;         // (row, q head of the group) columns per CTA
   int parts;        // partitions of the tile list; grid = parts * kv heads
-  size_t off_windows, off_row_window, off_acc, off_ml;
+  size_t off_windows, off_row_window, off_acc, off_ml, off_rot, off_norm2;
   size_t workspace_bytes;
 };
 
@@ -86,6 +86,11 @@ struct AttnWork {
   int* row_window;
   float* acc;  // [grid][2][cols][D]: piece 0 continues a window, piece 1 starts one that goes on
   float* ml;   // [grid][2][cols][2]
+  // tensor-core kernel: rotated queries R q * q_mul and their squared norms, [rows][q heads]; the
+  // rows of windows that one CTA finishes come back in their place, in rotated space
+  float* q_rot;
+  float* q_norm2;
+  float q_mul;
   int cols, parts, rows_per_window;
 };
 
@@ -94,16 +99,19 @@ int attn_tc_cols(const AttnArgs& a);
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream);
 
 #ifdef __CUDACC__
-// The tokens a query row sees: [p0, p1), [w0, w1) and base + j for the set bits j of its mask.
-struct RowView {
+// The tokens a query row sees: [p0, p1), [w0, w1) and base + j for the set bits j of its mask
+// (bits: the highest set bit + 1; without a mask base is the row's position).
+struct RowSees {
+  int p0, p1, w0, w1, base, bits;
+};
+struct RowView : RowSees {
   int seq;  // -1: none
-  int p0, p1, w0, w1;
-  int base, bits;  // bits: highest set bit + 1
   bool bad;
 };
 
 __device__ __forceinline__ RowView row_view(const AttnArgs& a, int i) {
-  RowView v{-1, 0, 0, 0, 0, 0, 0, false};
+  RowView v{};
+  v.seq = -1;
   const int seq = a.q_seq[i];
   if (seq < 0 || seq >= a.num_seqs) {
     v.bad = seq != -1;  // -1 is a padding row
@@ -114,6 +122,7 @@ __device__ __forceinline__ RowView row_view(const AttnArgs& a, int i) {
   if (a.q_len) {
     int len = a.q_len[i];
     v.bad = len < 0 || len > cap;
+    v.base = len - 1;
     len = min(max(len, 0), cap);
     const int doc = a.doc_starts ? max(a.doc_starts[i], 0) : 0;
     v.w1 = len;
@@ -148,7 +157,7 @@ __device__ __forceinline__ RowView row_view(const AttnArgs& a, int i) {
 }
 
 // Whether a row sees token t.
-__device__ __forceinline__ bool row_sees(const RowView& v, const uint32_t* mask, int t) {
+__device__ __forceinline__ bool row_sees(const RowSees& v, const uint32_t* mask, int t) {
   bool s = (t >= v.w0 && t < v.w1) || (t >= v.p0 && t < v.p1);
   const int j = t - v.base;
   if (v.bits > 0 && j >= 0 && j < v.bits) s |= (mask[j >> 5] >> (j & 31)) & 1u;
@@ -158,6 +167,25 @@ __device__ __forceinline__ bool row_sees(const RowView& v, const uint32_t* mask,
 // Parts that hold tiles: with fewer tiles than parts, one tile each (the combine walks every
 // part between a window's first and last, so none of them may be empty).
 __device__ __forceinline__ int live_parts(const AttnWork& w, int total) { return min(w.parts, total); }
+// E consecutive floats another kernel of the call wrote (aligned to 4 E bytes; plain loads: the
+// memory is written again within the call).
+template <int E>
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[E]) {
+  if constexpr (E == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x;
+    v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + i);
+      v[i] = x.x;
+      v[i + 1] = x.y;
+      v[i + 2] = x.z;
+      v[i + 3] = x.w;
+    }
+  }
+}
 // The first tile of partition p of `parts` over `total` tiles.
 __device__ __forceinline__ int part_begin(int total, int p, int parts) { return (int)((int64_t)total * p / parts); }
 // The partition that holds tile g.

@@ -64,6 +64,7 @@ constexpr int kSoftThreads = 32 * kSoftWarps;
 // shared memory).  128 (dequant + dequant + issue) + 256 soft <= 640 * 96.
 constexpr int kRegsIssue = 64;
 constexpr int kMaxRing = 6;
+constexpr int kNorms = 6;  // tiles whose norms are kept: keys run at most five tiles ahead of the softmax
 constexpr float kSlack = 6.0f;            // log2 units the running max may lag
 constexpr float kMaxWeight = 64.0f;       // 2^kSlack
 constexpr float kLoQ = 4096.0f;           // scale of the fp16 remainders of Q
@@ -91,14 +92,14 @@ struct Tc {
   static constexpr int kOffQ = 0;
   static constexpr int kOffV = kOffQ + kQBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVBytes;
-  static constexpr int kOffRows = kOffP + kPBytes;                 // RowView[kCols]
-  // floats [kN]: -max, correction, slope, (int) position, max and sum of the window; part [4][kN]
-  static constexpr int kOffCol = kOffRows + kCols * (int)sizeof(RowView);
-  static constexpr int kOffMeta = kOffCol + 10 * kN * 4;            // uint32 valid[kMaxRing][4]
-  static constexpr int kOffTab = (kOffMeta + kMaxRing * 16 + 127) / 128 * 128;  // key table, 5-bit value table, ring
+  static constexpr int kOffRows = kOffP + kPBytes;                 // RowSees[kCols]
+  // floats [kN]: -max, correction, slope; part [4][kN]
+  static constexpr int kOffCol = kOffRows + (kCols * (int)sizeof(RowSees) + 15) / 16 * 16;
+  static constexpr int kOffMeta = kOffCol + 7 * kN * 4;            // uint32 valid[kMaxRing][4], of tiles [kNorms][4]
+  static constexpr int kOffNorm = kOffMeta + (kMaxRing + kNorms) * 16;  // float2 (nu_k, nu_v) [kNorms][128]
+  static constexpr int kOffTab = (kOffNorm + kNorms * kTok * 8 + 127) / 128 * 128;  // key table, 5-bit value table, ring
   static constexpr int kRegsDequant = D == 256 ? 96 : 64;
   static constexpr int kRegsSoft = (640 * 96 - 128 * (2 * kRegsDequant + kRegsIssue)) / 256 / 8 * 8;
-  static constexpr int kStageCols = kPBytes / (D * 4);              // output columns staged at a time
 };
 
 // Bytes of a packed row's span in the ring: the 16-byte aligned span that holds a row wherever
@@ -145,13 +146,26 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {  // never suspends
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t bar) {  // by a whole warp, one elected lane
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
 }
-// D (+)= A B, kind::f16, A in TMEM or in shared memory, B in shared memory; one thread.
+// D (+)= A B, kind::f16, A in TMEM or in shared memory, B in shared memory; called by a whole warp,
+// issued by one elected lane (the operands stay in uniform registers that way).
 // Descriptors come as their low words (address and leading offset); the high word is the same
 // for all: eight rows (K-major) or k-lines (MN-major) of 128 bytes, the next eight 1024 bytes on,
 // 128-byte swizzle.
@@ -161,15 +175,16 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 bd;\n setp.ne.b32 p, %4, 0;\n mov.b64 bd, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n .reg .b64 bd;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 bd, {%2, %5};\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 ad, bd;\n setp.ne.b32 p, %4, 0;\n mov.b64 ad, {%1, %5};\n mov.b64 bd, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n .reg .b64 ad, bd;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 ad, {%1, %5};\n mov.b64 bd, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
       : "memory");
 }
@@ -343,11 +358,12 @@ __device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTabl
   }
 }
 
-// The row of this thread's token in the ring: SPAN bytes, of which the row starts `skip` words in.
+// The row of this thread's token in the ring, indices and norm: SPAN bytes, of which the row
+// starts `skip` words in.
 template <int D, int BITS>
 __device__ __forceinline__ void load_row(uint32_t addr, int skip, uint32_t (&w)[D * BITS / 32 + 1]) {
   constexpr int SPAN = span_bytes(D, BITS), NW = D * BITS / 32;
-  constexpr int NV = (NW + 3 + 3) / 4 < SPAN / 16 ? (NW + 3 + 3) / 4 : SPAN / 16;
+  constexpr int NV = (NW + 4 + 3) / 4 < SPAN / 16 ? (NW + 4 + 3) / 4 : SPAN / 16;
   uint32_t r[4 * NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -360,13 +376,12 @@ __device__ __forceinline__ void load_row(uint32_t addr, int skip, uint32_t (&w)[
   auto take = [&](auto tag) {
     constexpr int K = decltype(tag)::value;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = r[i + K < 4 * NV ? i + K : 0];
+    for (int i = 0; i <= NW; ++i) w[i] = r[i + K < 4 * NV ? i + K : 0];
   };
   if (skip == 0) take(std::integral_constant<int, 0>{});
   else if (skip == 1) take(std::integral_constant<int, 1>{});
   else if (skip == 2) take(std::integral_constant<int, 2>{});
   else take(std::integral_constant<int, 3>{});
-  w[NW] = 0;
 }
 
 // Drops the first N words: a loop over a row stays rolled (the roles share the instruction
@@ -375,46 +390,6 @@ template <int N, int NW>
 __device__ __forceinline__ void drop_words(uint32_t (&w)[NW]) {
 #pragma unroll
   for (int i = 0; i + N < NW; ++i) w[i] = w[i + N];
-}
-
-// ---------------------------------------------------------------- queries and outputs
-
-// E consecutive query elements from element `at` (a multiple of E); `vec`: the tensor starts on 16 bytes.
-template <int E>
-__device__ __forceinline__ void load_query(const void* q, int64_t at, int dtype, bool vec, float (&v)[E]) {
-  if (vec && dtype == kF32) {
-    load_chunk<float, E>(static_cast<const float*>(q) + at, v);
-  } else if (vec && dtype == kF16) {
-    load_chunk<__half, E>(static_cast<const __half*>(q) + at, v);
-  } else if (vec) {
-    load_chunk<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(q) + at, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = load_as_f32(q, at + i, dtype);
-  }
-}
-// E consecutive output elements (fp16 for SPLIT, else bf16).
-template <int E, bool SPLIT>
-__device__ __forceinline__ void store_row(void* out, int64_t at, bool vec, const float (&v)[E]) {
-  uint32_t u[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    if constexpr (SPLIT) {
-      u[i] = pack2(v[2 * i], v[2 * i + 1]);
-    } else {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-  }
-  uint16_t* to = static_cast<uint16_t*>(out) + at;
-  if (vec) {
-    if constexpr (E == 8) *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
-    else if constexpr (E == 4) *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
-    else *reinterpret_cast<uint32_t*>(to) = u[0];
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) to[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
-  }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -430,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(8) uint64_t bars[2 * kMaxRing + 26];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead, fail[2][2], fail_all;
-  __shared__ int full_lo, full_hi, pre_lo, pre_hi, q_exp;
+  __shared__ int full_lo_s, full_hi_s, pre_lo_s, pre_hi_s, q_exp;
   unsigned char* smem = smem_raw + ((1024u - (smem_a(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_a(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -478,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     fail[0][0] = fail[0][1] = fail[1][0] = fail[1][1] = fail_all = 0;
     for (int s = 0; s < kMaxRing; ++s) {
       bar_init(raw_full(s), p.tma ? 1 : 33);  // cp.async: every lane's copies and one arrival
-      bar_init(raw_empty(s), kKeyWarps + kValWarps + kSoftWarps);
+      bar_init(raw_empty(s), kKeyWarps + kValWarps);
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(k_full(b), kKeyWarps);
@@ -536,6 +511,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!f(win, first, last)) return;
     }
   };
+  // Queries come rotated (q_rot, with the softmax scale), outputs leave in rotated space.
   auto tile_token = [&](const AttnWindow& win, int tile) -> int {
     return (tile < win.nA ? win.tA0 + tile : win.tB0 + tile - win.nA) * kTok;
   };
@@ -552,12 +528,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t tab = ktab + lane * 4;
       const uint32_t row = ring + (uint32_t)((warp * 32 + lane) * SPAN);
       const uint32_t dst = tmem + ((uint32_t)(32 * warp) << 16) + C::kK;
+      const uint32_t vnorm = ring + (uint32_t)(kTok * spk + (warp * 32 + lane) * spv + skip_v + rbv - 4);
+      float2* norms = reinterpret_cast<float2*>(smem + C::kOffNorm);
+      uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::kOffMeta);
       int st = 0, ph = 0, it = 0;
       for_windows([&](const AttnWindow&, int first, int last) -> bool {
         for (int t = first; t < last; ++t, ++it) {
           if (!wait(raw_full(st), ph)) return false;
           uint32_t wd[D * BITS / 32 + 1];
           load_row<D, BITS>(row + st * stage_bytes, skip_k >> 2, wd);
+          // the token's norms go on to the softmax warps (what they say is ordered by k_full,
+          // the product and its completion)
+          const float vn = __uint_as_float(ld_s32(vnorm + st * stage_bytes));
+          norms[(it % kNorms) * kTok + warp * 32 + lane] = make_float2(__uint_as_float(wd[D * BITS / 32]), vn);
+          if (lane == 0) valid[4 * (kMaxRing + it % kNorms) + warp] = valid[4 * st + warp];
           __syncwarp();
           if (lane == 0) bar_arrive(raw_empty(st));
           if (++st == p.ring) st = 0, ph ^= 1;
@@ -653,31 +637,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int quad = warp & 3, set = sw >> 2;
     const int stid = tid - 32 * (kKeyWarps + kValWarps);
     const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
-    RowView* rows = reinterpret_cast<RowView*>(smem + C::kOffRows);
+    RowSees* rows = reinterpret_cast<RowSees*>(smem + C::kOffRows);
     float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -max; -inf where there is no column
     float* corr_s = negm_s + C::kN;
     float* slope_s = corr_s + C::kN;
-    int* pos_s = reinterpret_cast<int*>(slope_s + C::kN);
-    float* top_s = slope_s + 2 * C::kN;  // max and sum of the window's columns over the streams
-    float* sum_s = top_s + C::kN;
-    float* part_s = sum_s + C::kN;  // [4][kN]
+    float* part_s = slope_s + C::kN;  // [4][kN]
     __shared__ int vpart[kSoftWarps], ve_s[2];
     const uint32_t* valid = reinterpret_cast<const uint32_t*>(smem + C::kOffMeta);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    const uint32_t krow = ring + (uint32_t)(t_lane * spk + skip_k + rbk - 4);
-    const uint32_t vrow = ring + (uint32_t)(kTok * spk + t_lane * spv + skip_v + rbv - 4);
+    const float2* norms = reinterpret_cast<const float2*>(smem + C::kOffNorm);
     const uint32_t p_line = base + C::kOffP + (uint32_t)((t_lane >> 3) * 1024 + (t_lane & 7) * 128);
-    const float scale = a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)D);
     const bool capped = a.softcap > 0.f, biased = a.alibi != nullptr;
-    // capped scores: tanh(s / cap) from 2^(2 log2(e) s / cap)
-    const float qmul = (capped ? 2.f * scale / a.softcap : scale) * kLog2eA / (sqrtf((float)D) * a.k_alpha);
     const float cap2 = a.softcap * kLog2eA;
-    const float inv_av = 1.0f / a.v_alpha;
-    const bool q_vec = reinterpret_cast<uintptr_t>(a.q) % 16 == 0, o_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
-    float sgn[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) sgn[i] = __ldg(a.signs + lane * (D / 32) + i);
-    int st = 0, ph = 0;
+    const float inv_av = 1.0f / (a.v_alpha * sqrtf((float)D));
+    int it = 0;
     uint32_t sph = 0, pph = 0;
 
     for_windows([&](const AttnWindow& win, int first, int last) -> bool {
@@ -689,65 +662,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int col0 = stream * pitch;                             // the stream's part of the column arrays
       const int bar_id = kBarSoft + 1 + stream, bar_n = 128 * sets;
       const uint32_t weight = (uint32_t)streams;  // arrivals of this warp where all softmax warps count
-      // ---- queries of the window: one power of two for all of them, rotated, hi (and lo)
+      // ---- queries of the window, rotated already: one power of two for all of them, hi (and lo)
       if (stid == 0) {
-        full_lo = pre_lo = 0;
-        full_hi = pre_hi = 0x7fffffff;
+        full_lo_s = pre_lo_s = 0;
+        full_hi_s = pre_hi_s = 0x7fffffff;
         q_exp = -1000;
       }
       soft_sync();
       if (stid < win.nrows) {
         const RowView v = row_view(a, win.row0 + stid);
         rows[stid] = v;
-        atomicMax(&full_lo, v.w0);
-        atomicMin(&full_hi, v.w1);
-        atomicMax(&pre_lo, v.p0);
-        atomicMin(&pre_hi, v.p1);
+        atomicMax(&full_lo_s, v.w0);
+        atomicMin(&full_hi_s, v.w1);
+        atomicMax(&pre_lo_s, v.p0);
+        atomicMin(&pre_hi_s, v.p1);
       }
+      const int64_t q_first = (int64_t)win.row0 * a.num_q_heads + h * G;  // (row, q head) of column 0
+      auto q_index = [&](int c) -> int64_t { return q_first + (int64_t)(c / G) * a.num_q_heads + c % G; };
       if (stid < C::kN) {
         const int c = stid & (pitch - 1);
         negm_s[stid] = c < cols ? -kNoMax : -INFINITY;  // no column there: never a new max
         slope_s[stid] = biased && stid < cols ? a.alibi[h * G + stid % G] * kLog2eA : 0.f;
-        pos_s[stid] = a.q_len && stid < cols ? a.q_len[win.row0 + stid / G] - 1 : 0;
+        const float n2 = stid < cols ? w.q_norm2[q_index(stid)] : 0.f;
+        const int e = __reduce_max_sync(kFullMask, n2 < INFINITY ? (exp_of(n2) + 1) / 2 : -1000);
+        if (lane == 0) atomicMax(&q_exp, e);
       }
-      // this lane's D / 32 coordinates of a column's query; kAhead columns are loaded together
-      constexpr int kAhead = 4;
-      auto q_rows = [&](int col, float (&v)[kAhead][D / 32]) {
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-          const int c = min(col + e * kSoftWarps, cols - 1);
-          const int64_t at = ((int64_t)(win.row0 + c / G) * a.num_q_heads + h * G + c % G) * D + lane * (D / 32);
-          load_query<D / 32>(a.q, at, a.q_dtype, q_vec, v[e]);
-        }
-      };
-      float most = 0.f;
-      for (int col = sw; col < cols; col += kAhead * kSoftWarps) {
-        float v[kAhead][D / 32];
-        q_rows(col, v);
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) ss = fmaf(v[e][i] * qmul, v[e][i] * qmul, ss);
-          ss = warp_sum(ss);
-          if (ss < INFINITY) most = fmaxf(most, ss);
-        }
-      }
-      if (lane == 0) atomicMax(&q_exp, (exp_of(most) + 1) / 2);
       soft_sync();
       // the largest rotated coordinate is at most the norm times sqrt(D): to 2^10 or less
       const int qe = q_exp + (D == 64 ? 3 : 4) - 10;
       const float q_down = pow2i(max(-126, min(126, -qe))), q_up = pow2i(max(-126, min(126, qe)));
+      const int full_lo = full_lo_s, full_hi = full_hi_s, pre_lo = pre_lo_s, pre_hi = pre_hi_s;
+      constexpr int kAhead = 4;  // columns loaded together
       for (int col4 = sw; col4 < cols; col4 += kAhead * kSoftWarps) {
         float v[kAhead][D / 32];
-        q_rows(col4, v);
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          load_floats<D / 32>(w.q_rot + q_index(min(col4 + e * kSoftWarps, cols - 1)) * D + lane * (D / 32), v[e]);
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
-          const int col = col4 + e * kSoftWarps;
+          const int col = col4 + e * kSoftWarps, lc = col + lo_col;
           if (col >= cols) continue;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) v[e][i] *= qmul * sgn[i];
-          fwht_warp<D / 32>(v[e]);
 #pragma unroll
           for (int i = 0; i < D / 32; i += 2) {
             const int d = lane * (D / 32) + i;
@@ -758,7 +712,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + col * 128 + ((ch ^ (col & 7)) << 4)) = hi;
             if constexpr (SPLIT) {
               const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
-              const int lc = col + lo_col;
               *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + lc * 128 + ((ch ^ (lc & 7)) << 4)) =
                   pack2((x0 - __low2float(hh)) * kLoQ, (x1 - __high2float(hh)) * kLoQ);
             }
@@ -777,26 +730,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int ve = -1000;  // P' = p nu_v 2^-ve (every thread of the stream holds the same)
       bool broken = false;
       for (int k = 0; k < tiles; ++k) {
-        const int sb = k & (2 * streams - 1);
-        const int this_st = st, this_ph = ph;
+        const int sb = k & (2 * streams - 1), slot = it++ % kNorms;
         const uint32_t this_s = (sph >> sb) & 1, this_p = (pph >> (k & (streams - 1))) & 1;
-        if (++st == p.ring) st = 0, ph ^= 1;
         sph ^= 1u << sb;
         pph ^= 1u << (k & (streams - 1));
         if ((k & (streams - 1)) != stream || broken) continue;
         const int t0 = tile_token(win, first + k), tok = t0 + t_lane;
         const uint32_t s_at = lanes + C::kS + sb * pitch;
-        bool ok = wait(raw_full(this_st), this_ph);
-        float kn = __uint_as_float(ld_s32(krow + this_st * stage_bytes)) * q_up;
-        const float vn = __uint_as_float(ld_s32(vrow + this_st * stage_bytes));
-        const uint4 vv = *reinterpret_cast<const uint4*>(valid + 4 * this_st);
-        ok = wait(s_full(sb), this_s) && ok;
+        bool ok = wait(s_full(sb), this_s);
         tc_after();
+        const float2 kv = norms[slot * kTok + t_lane];
+        const uint4 vv = *reinterpret_cast<const uint4*>(valid + 4 * (kMaxRing + slot));
+        const bool p_free = bar_test(p_empty(stream), this_p ^ 1);  // asked now, needed at the first store
+        float kn = kv.x * q_up;
+        const float vn = kv.y;
         const bool real = (((quad == 0 ? vv.x : quad == 1 ? vv.y : quad == 2 ? vv.z : vv.w) >> lane) & 1u) && tok < hi_tok;
         const bool all = (vv.x & vv.y & vv.z & vv.w) == 0xffffffffu && ((t0 >= full_lo && t0 + kTok <= full_hi) ||
                                                                          (t0 >= pre_lo && t0 + kTok <= pre_hi));
-        __syncwarp();
-        if (lane == 0) bar_arrive_n(raw_empty(this_st), weight);
         // Scores of columns c0 .. c0 + 15 from their accumulators (the two parts added).
         auto fetch = [&](int c0, float2 (&x)[8]) {
           uint32_t u[16];
@@ -838,8 +788,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (biased) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                x[i].x -= slope_s[c0 + 2 * i] * fabsf((float)(pos_s[c0 + 2 * i] - tok));
-                x[i].y -= slope_s[c0 + 2 * i + 1] * fabsf((float)(pos_s[c0 + 2 * i + 1] - tok));
+                x[i].x -= slope_s[c0 + 2 * i] * fabsf((float)(rows[(c0 + 2 * i) / G].base - tok));
+                x[i].y -= slope_s[c0 + 2 * i + 1] * fabsf((float)(rows[(c0 + 2 * i + 1) / G].base - tok));
               }
             }
             uint32_t see = 0xffffu;  // bit i: column c0 + i
@@ -907,7 +857,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
             if (g == 0 && !again) {  // the stream's product before is done: P and O are free
-              ok = wait(p_empty(stream), this_p ^ 1) && ok;
+              if (!__all_sync(kFullMask, p_free)) ok = wait(p_empty(stream), this_p ^ 1) && ok;
               if (!ok) *fl = 1;
             }
             st_v4(p_addr(col0 + c0), o[0], o[1], o[2], o[3]);
@@ -1051,6 +1001,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       soft_sync();
       if (*(volatile int*)&fail_all) return false;
       tc_after();
+      const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * w.cols;
+      const bool whole = first == 0 && last == win.nA + win.nB;
       if (stid < cols) {  // streams -> window: factors of their O^T
         const float ma = -negm_s[stid], mb = live > 1 ? -negm_s[pitch + stid] : kNoMax;
         const float top = fmaxf(ma, mb);
@@ -1058,13 +1010,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto sum4 = [&](int c) -> float {
           return (part_s[c] + part_s[C::kN + c]) + (part_s[2 * C::kN + c] + part_s[3 * C::kN + c]);
         };
-        top_s[stid] = top;
-        sum_s[stid] = fa * sum4(stid) + (live > 1 ? fb * sum4(pitch + stid) : 0.f);
-        corr_s[stid] = fa * inv_av * pow2i(max(-126, min(126, ve_s[0])));
-        if (live > 1) corr_s[pitch + stid] = fb * inv_av * pow2i(max(-126, min(126, ve_s[1])));
+        const float sum = fa * sum4(stid) + (live > 1 ? fb * sum4(pitch + stid) : 0.f);
+        const float f = !whole ? inv_av : sum != 0.f ? inv_av / sum : 0.f;
+        corr_s[stid] = fa * f * pow2i(max(-126, min(126, ve_s[0])));
+        if (live > 1) corr_s[pitch + stid] = fb * f * pow2i(max(-126, min(126, ve_s[1])));
+        if (!whole) {
+          w.ml[2 * (slot0 + stid)] = top;
+          w.ml[2 * (slot0 + stid) + 1] = sum;
+        }
       }
       soft_sync();
-      const bool whole = first == 0 && last == win.nA + win.nB;
       // this lane's dim of columns c0 .. c0 + 15 (half hf of the dims)
       auto load_o = [&](int hf, int c0, float (&x)[16]) {
 #pragma unroll
@@ -1087,54 +1042,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(u[i]), corr_s[s * pitch + c0 + i], x[i]);
         }
       };
-      const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * w.cols;
-      if (!whole) {
-        if (stid < cols) {
-          w.ml[2 * (slot0 + stid)] = top_s[stid];
-          w.ml[2 * (slot0 + stid) + 1] = sum_s[stid];
+      // a whole window's rows take the place of its queries, a piece goes to its slot; the
+      // combine rotates them back
+#pragma unroll 1
+      for (int c0 = 16 * set; c0 < cols; c0 += 16 * kSoftSets)
+#pragma unroll 1
+        for (int hf = 0; hf < C::kHalves; ++hf) {
+          float x[16];
+          load_o(hf, c0, x);
+          if (D == 64 && quad >= 2) continue;  // lanes 64.. repeat the 64 dims
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c0 + i < cols)
+              (whole ? w.q_rot + q_index(c0 + i) * D : w.acc + (slot0 + c0 + i) * D)[hf * 128 + t_lane] = x[i];
         }
-#pragma unroll 1
-        for (int c0 = 16 * set; c0 < cols; c0 += 16 * kSoftSets)
-#pragma unroll 1
-          for (int hf = 0; hf < C::kHalves; ++hf) {
-            float x[16];
-            load_o(hf, c0, x);
-            if (D == 64 && quad >= 2) continue;  // lanes 64.. repeat the 64 dims
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c0 + i < cols) w.acc[(slot0 + c0 + i) * D + hf * 128 + t_lane] = x[i];
-          }
-      } else {
-        float* stage = reinterpret_cast<float*>(smem + C::kOffP);  // [kStageCols][D]
-        for (int r0 = 0; r0 < cols; r0 += C::kStageCols) {
-          const int r1 = min(cols, r0 + C::kStageCols);
-#pragma unroll 1
-          for (int c0 = r0 + 16 * set; c0 < r1; c0 += 16 * kSoftSets)
-#pragma unroll 1
-            for (int hf = 0; hf < C::kHalves; ++hf) {
-              float x[16];
-              load_o(hf, c0, x);
-              if (D == 64 && quad >= 2) continue;
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (c0 + i < r1) stage[(c0 + i - r0) * D + hf * 128 + t_lane] = x[i];
-            }
-          soft_sync();
-          for (int c = r0 + sw; c < r1; c += kSoftWarps) {
-            float v[D / 32];
-            const float s = sum_s[c];
-            const float inv = s != 0.f ? 1.f / (s * sqrtf((float)D)) : 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) v[i] = stage[(c - r0) * D + lane * (D / 32) + i] * inv;
-            fwht_warp<D / 32>(v);
-            const int64_t at = ((int64_t)(win.row0 + c / G) * a.num_q_heads + h * G + c % G) * D + lane * (D / 32);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) v[i] *= sgn[i];
-            store_row<D / 32, SPLIT>(a.out, at, o_vec, v);
-          }
-          soft_sync();
-        }
-      }
       tc_before();
       soft_sync();  // the arrays and O are free for the next window
       return true;
@@ -1233,7 +1154,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issue
-    if (lane == 0) {
+    {
       // (offsets are added to the low words in units of 16 bytes: no carry leaves the address)
       const uint32_t q_at = desc_low(base + C::kOffQ, 16), v_at = desc_low(base + C::kOffV, D == 64 ? 0 : 64 * 128);
       const uint32_t p_at = desc_low(base + C::kOffP, kTok * 128);
@@ -1241,20 +1162,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t sph = 0, pph = 0;  // phases of the score buffers and of the streams' weights
       bool issued = false;
       for_windows([&](const AttnWindow& win, int first, int last) -> bool {
-        const int padded = pad_cols(win), n = SPLIT ? 2 * padded : padded;
-        const int streams = streams_of(padded), pitch = C::kN / streams, tiles = last - first;
+        // (the shuffles tell the compiler that the warp agrees)
+        const int padded = __shfl_sync(kFullMask, pad_cols(win), 0), n = SPLIT ? 2 * padded : padded;
+        const int tiles = __shfl_sync(kFullMask, last - first, 0);
+        const int streams = streams_of(padded), pitch = C::kN / streams;
         const uint32_t ids = mma_idesc(n, false), idp = mma_idesc(n, true);
-        if (!wait1(q_full, unit & 1)) return false;
+        if (!wait(q_full, unit & 1)) return false;
         ++unit;
         auto weigh = [&](int k) -> bool {  // O^T of its stream += V^T P^T of the window's tile k
           const int s = k & (streams - 1);
-          if (!wait1(p_full(s), (pph >> s) & 1)) return false;
+          if (!wait(p_full(s), (pph >> s) & 1)) return false;
           pph ^= 1u << s;
           const uint32_t p_s = p_at + (uint32_t)((((s * pitch) >> 6) * (kTok * 128) + ((s * pitch) & 63) * 2) >> 4);
           const uint32_t o_s = tmem + C::kO + s * pitch;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            if (!wait1(v_full(vslot), vph)) return false;
+            if (!wait(v_full(vslot), vph)) return false;
             tc_after();
 #pragma unroll
             for (int hf = 0; hf < C::kHalves; ++hf)
@@ -1270,7 +1193,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         for (int k = 0; k < tiles; ++k, ++it) {
           const int b = it & 1, sb = k & (2 * streams - 1);
-          if (!wait1(k_full(b), (it >> 1) & 1) || !wait1(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
+          if (!wait(k_full(b), (it >> 1) & 1) || !wait(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
           sph ^= 1u << sb;
           tc_after();
 #pragma unroll
@@ -1352,7 +1275,7 @@ cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream)
   // number of 16 bytes), and slot numbers that a 32-bit coordinate holds
   t.tma = sub >= 8 && ks % 16 == 0 && vs % 16 == 0 && slots > 0 && slots < 0x7fffffffLL &&
           page_map(&km, a.k_pages, slots, ks, spk, sub) && page_map(&vm, a.v_pages, slots, vs, spv, sub);
-  constexpr int limit = 227 * 1024 - 1024;  // the static arrays take their part
+  constexpr int limit = 227 * 1024 - 448;  // the static arrays take their part
   const int stage = kTok * (spk + spv);
   const int fixed = 1024 + C::kOffTab + key_table_bytes(a.k_bits) + value_table_bytes(a.v_bits);
   t.ring = std::min(kMaxRing, (limit - fixed) / stage);
