@@ -724,26 +724,28 @@ class StepPlan(NamedTuple):
     free_state: torch.Tensor  # int32 [2]
 
 
-def _need_like(name: str, dev: torch.device, **want) -> None:
-    """Every named (tensor, dtype, shape) is a contiguous tensor of that dtype and shape on `dev`."""
-    index = dev.index
+def _need_like(name: str, index: int, **want) -> None:
+    """Every named (tensor, dtype, shape) is a contiguous tensor of that dtype and shape on CUDA
+    device `index`."""
     for what, (t, dtype, shape) in want.items():
-        if t.get_device() != index or dev.type != "cuda":
+        if t.get_device() != index or index < 0:
             raise ValueError(f"{name}: all tensors must be on the same CUDA device ({what} is on {t.device})")
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: {what} must be a contiguous {dtype} {list(shape)}, got {t.dtype} "
                              f"{list(t.shape)}")
 
 
-def _call(dev: torch.device, fn, *args) -> None:
-    """One library call on the current stream of `dev`, with that device current."""
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    if status != TQ_OK:
-        _check(status)
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(index: int):
+    """Makes device `index` current for a call (nothing to do where it is)."""
+    return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _stream_ptr(index: int) -> int:
+    """The current stream of device `index`, as the library takes it."""
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 def tq_plan_step(seq_lens: torch.Tensor, new_lens: torch.Tensor, seq_blocks: torch.Tensor, block_table: torch.Tensor,
@@ -756,7 +758,7 @@ def tq_plan_step(seq_lens: torch.Tensor, new_lens: torch.Tensor, seq_blocks: tor
     inputs themselves (pass them in `out`).  With check=True the call synchronises and raises
     TQError(TQ_ERR_OUT_OF_BLOCKS / TQ_ERR_INVALID_ARG), with nothing planned."""
     name = "tq_plan_step"
-    dev, i32 = seq_lens.device, torch.int32
+    dev, i32, index = seq_lens.device, torch.int32, seq_lens.get_device()
     if block_table.dim() != 2 or free_blocks.dim() != 1:
         raise ValueError(f"{name}: block_table [S, W] and free_blocks [NB] expected")
     s, w = block_table.shape
@@ -764,27 +766,32 @@ def tq_plan_step(seq_lens: torch.Tensor, new_lens: torch.Tensor, seq_blocks: tor
     if max_rows < 0:
         raise ValueError(f"{name}: max_rows {max_rows} < 0")
     if out is None:
-        if dev.type != "cuda":
+        if index < 0:
             raise ValueError(f"{name}: all tensors must be on the same CUDA device (seq_lens is on {dev})")
-        rows = torch.empty(4, max_rows, dtype=i32, device=dev)  # slots, q_seq, q_len
-        ints = torch.empty(3 * s + 3, dtype=i32, device=dev)
-        out = StepPlan(rows[:2].view(-1).view(torch.int64), rows[2], rows[3], ints[:s + 1], ints[s + 1:2 * s + 1],
-                       ints[2 * s + 1:3 * s + 1], ints[3 * s + 1:])
-    _need_like(name, dev, seq_lens=(seq_lens, i32, (s,)), new_lens=(new_lens, i32, (s,)),
+        slots = torch.empty(max_rows, dtype=torch.int64, device=dev)
+        q_seq, q_len, row_start, lens, blocks, state = torch.empty(2 * max_rows + 3 * s + 3, dtype=i32, device=dev).split(
+            [max_rows, max_rows, s + 1, s, s, 2])
+        out = StepPlan(slots, q_seq, q_len, row_start, lens, blocks, state)
+    else:
+        _need_like(name, index, slots=(out.slots, torch.int64, (max_rows,)), q_seq=(out.q_seq, i32, (max_rows,)),
+                   q_len=(out.q_len, i32, (max_rows,)), row_start=(out.row_start, i32, (s + 1,)),
+                   seq_lens_out=(out.seq_lens, i32, (s,)), seq_blocks_out=(out.seq_blocks, i32, (s,)),
+                   free_state_out=(out.free_state, i32, (2,)))
+    _need_like(name, index, seq_lens=(seq_lens, i32, (s,)), new_lens=(new_lens, i32, (s,)),
                seq_blocks=(seq_blocks, i32, (s,)), block_table=(block_table, i32, (s, w)),
-               free_blocks=(free_blocks, i32, (free_blocks.numel(),)), free_state=(free_state, i32, (2,)),
-               slots=(out.slots, torch.int64, (max_rows,)), q_seq=(out.q_seq, i32, (max_rows,)),
-               q_len=(out.q_len, i32, (max_rows,)), row_start=(out.row_start, i32, (s + 1,)),
-               seq_lens_out=(out.seq_lens, i32, (s,)), seq_blocks_out=(out.seq_blocks, i32, (s,)),
-               free_state_out=(out.free_state, i32, (2,)))
+               free_blocks=(free_blocks, i32, (free_blocks.numel(),)), free_state=(free_state, i32, (2,)))
     _need_status(name, status, dev)
     if status is None and check:
         status = _status_buffer(dev)
-    _call(dev, lib().tq_plan_step, seq_lens.data_ptr(), new_lens.data_ptr(), seq_blocks.data_ptr(), s,
-          block_table.data_ptr(), w, free_blocks.data_ptr(), free_state.data_ptr(), free_blocks.numel(),
-          int(block_size), max_rows, out.slots.data_ptr(), out.q_seq.data_ptr(), out.q_len.data_ptr(),
-          out.row_start.data_ptr(), out.seq_lens.data_ptr(), out.seq_blocks.data_ptr(), out.free_state.data_ptr(),
-          _ptr(status))
+    with _on(index):
+        code = lib().tq_plan_step(seq_lens.data_ptr(), new_lens.data_ptr(), seq_blocks.data_ptr(), s,
+                                  block_table.data_ptr(), w, free_blocks.data_ptr(), free_state.data_ptr(),
+                                  free_blocks.numel(), int(block_size), max_rows, out.slots.data_ptr(),
+                                  out.q_seq.data_ptr(), out.q_len.data_ptr(), out.row_start.data_ptr(),
+                                  out.seq_lens.data_ptr(), out.seq_blocks.data_ptr(), out.free_state.data_ptr(),
+                                  _ptr(status), _stream_ptr(index))
+    if code != TQ_OK:
+        _check(code)
     if check:
         raise_for_device_status(status)
     return out
@@ -803,22 +810,25 @@ def tq_commit_tree(k_pages: torch.Tensor | None, v_pages: torch.Tensor | None, b
         raise ValueError(f"{name}: pages [NB, bs, H, RB], block_table [S, W] and path [S, P] expected")
     nb, bs, h, _ = pages.shape
     s, w = block_table.shape
-    dev, i32 = pages.device, torch.int32
+    dev, i32, index = pages.device, torch.int32, pages.get_device()
     if seq_lens is None:
         seq_lens = torch.empty(s, dtype=i32, device=dev)
     rb = [0, 0]
     for i, (what, t) in enumerate((("k_pages", k_pages), ("v_pages", v_pages))):
         if t is not None:
             rb[i] = t.shape[-1]
-            _need_like(name, dev, **{what: (t, torch.uint8, (nb, bs, h, rb[i]))})
-    _need_like(name, dev, block_table=(block_table, i32, (s, w)), ctx_lens=(ctx_lens, i32, (s,)),
+            _need_like(name, index, **{what: (t, torch.uint8, (nb, bs, h, rb[i]))})
+    _need_like(name, index, block_table=(block_table, i32, (s, w)), ctx_lens=(ctx_lens, i32, (s,)),
                path=(path, i32, (s, path.shape[1])), path_lens=(path_lens, i32, (s,)), seq_lens=(seq_lens, i32, (s,)))
     _need_status(name, status, dev)
     if status is None and check:
         status = _status_buffer(dev)
-    _call(dev, lib().tq_commit_tree, _ptr(k_pages), rb[0], _ptr(v_pages), rb[1], nb, bs, h, block_table.data_ptr(), s,
-          w, ctx_lens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), path.shape[1], seq_lens.data_ptr(),
-          _ptr(status))
+    with _on(index):
+        code = lib().tq_commit_tree(_ptr(k_pages), rb[0], _ptr(v_pages), rb[1], nb, bs, h, block_table.data_ptr(), s, w,
+                                    ctx_lens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), path.shape[1],
+                                    seq_lens.data_ptr(), _ptr(status), _stream_ptr(index))
+    if code != TQ_OK:
+        _check(code)
     if check:
         raise_for_device_status(status)
     return seq_lens
@@ -851,42 +861,38 @@ def _attn_call(name: str, q, q_seq, k_pages, v_pages, block_table, signs, k_cent
     nb, bs, h, rbk = k_pages.shape
     rbv = v_pages.shape[3]
     s, w = block_table.shape
-    dev, i32 = q.device, torch.int32
+    dev, i32, f32, u8, index = q.device, torch.int32, torch.float32, torch.uint8, q.get_device()
     kb, vb = _bits_from_centroids(k_centroids), _bits_from_centroids(v_centroids)
-    if rbk != tq_row_bytes(d, kb) or rbv != tq_row_bytes(d, vb):
+    if rbk * 8 != d * kb + 32 or rbv * 8 != d * vb + 32:  # head dims are multiples of 16
         raise ValueError(f"{name}: page rows of {rbk} / {rbv} bytes do not match head_dim {d} at {kb} / {vb} bits")
     if out is None:
         out = torch.empty((t, hq, d), dtype=out_dtype or q.dtype, device=dev)
     elif out.dtype not in _DTYPES:
         raise ValueError(f"{name}: out must be f32/f16/bf16, got {out.dtype}")
-    _need_like(name, dev, q=(q, q.dtype, (t, hq, d)), k_pages=(k_pages, torch.uint8, (nb, bs, h, rbk)),
-               v_pages=(v_pages, torch.uint8, (nb, bs, h, rbv)), block_table=(block_table, i32, (s, w)),
-               q_seq=(q_seq, i32, (t,)), signs=(signs, torch.float32, (d,)),
-               k_centroids=(k_centroids, torch.float32, (1 << kb,)),
-               v_centroids=(v_centroids, torch.float32, (1 << vb,)), out=(out, out.dtype, (t, hq, d)),
-               **more(t, hq, s, i32))
+    else:
+        _need_like(name, index, out=(out, out.dtype, (t, hq, d)))
+    _need_like(name, index, q=(q, q.dtype, (t, hq, d)), k_pages=(k_pages, u8, (nb, bs, h, rbk)),
+               v_pages=(v_pages, u8, (nb, bs, h, rbv)), block_table=(block_table, i32, (s, w)), q_seq=(q_seq, i32, (t,)),
+               signs=(signs, f32, (d,)), k_centroids=(k_centroids, f32, (1 << kb,)),
+               v_centroids=(v_centroids, f32, (1 << vb,)), **more(t, hq, s, i32))
     _need_status(name, status, dev)
-    with torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else _NO_SWITCH:
+    with _on(index):
         need = tq_paged_tree_workspace(t, hq, h, d)
         if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        elif workspace.get_device() != dev.index or not workspace.is_contiguous():
+            workspace = torch.empty(max(need, 256), dtype=u8, device=dev)
+        elif workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"{name}: workspace must be contiguous on {dev}")
         if status is None and check:
             status = _status_buffer(dev)
         code = fn(q.data_ptr(), _DTYPES[q.dtype], t, hq, h, d, k_pages.data_ptr(), kb, v_pages.data_ptr(), vb, nb, bs,
                   block_table.data_ptr(), s, w, q_seq.data_ptr(), *middle, signs.data_ptr(), k_centroids.data_ptr(),
                   v_centroids.data_ptr(), *tail, out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(),
-                  workspace.numel() * workspace.element_size(), _ptr(status),
-                  torch.cuda.current_stream(dev).cuda_stream)
+                  workspace.numel() * workspace.element_size(), _ptr(status), _stream_ptr(index))
     if code != TQ_OK:
         _check(code)
     if check:
         raise_for_device_status(status)
     return out
-
-
-_NO_SWITCH = contextlib.nullcontext()
 
 
 def tq_paged_tree(q: torch.Tensor, q_seq: torch.Tensor, ctx_lens: torch.Tensor, tree_mask: torch.Tensor,

@@ -28,7 +28,7 @@
 // (the product before has completed by then).
 //
 // Roles of the 18 warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, in two
-// sets), 16 copies, 17 MMA issue.  A window of more than half the MMA columns has both sets on
+// sets), 16 copies, 17 and 18 MMA issue.  A window of more than half the MMA columns has both sets on
 // one tile, each with its groups of 16 columns; a smaller one makes two streams of one set that
 // take alternate tiles, each with its own maxima, sums and O^T, merged when the window ends:
 // the chain of waits, TMEM reads and votes of one tile then hides behind the other's.  Packed rows
@@ -402,14 +402,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const AttnArgs& a = p.a;
   const AttnWork& w = p.w;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxRing + 26];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxRing + 27];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead, fail[2][2], fail_all;
   __shared__ int full_lo_s, full_hi_s, pre_lo_s, pre_hi_s, q_exp;
   unsigned char* smem = smem_raw + ((1024u - (smem_a(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_a(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int H = a.num_kv_heads, G = a.num_q_heads / H;
+  const int H = a.num_kv_heads, G = a.num_q_heads / H, g_log = 31 - __clz(G);  // G: a power of two
   const int h = blockIdx.x % H, part = blockIdx.x / H;
   const int rbk = D * a.k_bits / 8 + 4, rbv = D * a.v_bits / 8 + 4;
   const int spk = span_bytes(D, a.k_bits), spv = span_bytes(D, a.v_bits);
@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     bar_init(q_full, kSoftWarps);
     bar_init(drained, 1);
+    bar_init(drained + 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -519,6 +520,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Two streams of tiles when the window's MMA columns fit half of the TMEM regions.
   auto streams_of = [&](int padded) -> int { return (SPLIT ? 2 * padded : padded) <= C::kN / 2 ? 2 : 1; };
 
+  // Every MMA of an issuing warp has finished before TMEM is freed.
+  auto drain = [&]() {
+    const uint32_t b = drained + (warp == kMmaWarp ? 0 : 8);
+    tc_commit(b);
+    for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(b, 0); ++i) {
+    }
+    __syncwarp();
+  };
   if (warp < kKeyWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsDequant));
     // ------------------------------------------------ keys: packed row -> this lane of TMEM
@@ -678,11 +687,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         atomicMin(&pre_hi_s, v.p1);
       }
       const int64_t q_first = (int64_t)win.row0 * a.num_q_heads + h * G;  // (row, q head) of column 0
-      auto q_index = [&](int c) -> int64_t { return q_first + (int64_t)(c / G) * a.num_q_heads + c % G; };
+      auto q_index = [&](int c) -> int64_t { return q_first + (int64_t)(c >> g_log) * a.num_q_heads + (c & (G - 1)); };
       if (stid < C::kN) {
         const int c = stid & (pitch - 1);
         negm_s[stid] = c < cols ? -kNoMax : -INFINITY;  // no column there: never a new max
-        slope_s[stid] = biased && stid < cols ? a.alibi[h * G + stid % G] * kLog2eA : 0.f;
+        slope_s[stid] = biased && stid < cols ? a.alibi[h * G + (stid & (G - 1))] * kLog2eA : 0.f;
         const float n2 = stid < cols ? w.q_norm2[q_index(stid)] : 0.f;
         const int e = __reduce_max_sync(kFullMask, n2 < INFINITY ? (exp_of(n2) + 1) / 2 : -1000);
         if (lane == 0) atomicMax(&q_exp, e);
@@ -788,15 +797,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (biased) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                x[i].x -= slope_s[c0 + 2 * i] * fabsf((float)(rows[(c0 + 2 * i) / G].base - tok));
-                x[i].y -= slope_s[c0 + 2 * i + 1] * fabsf((float)(rows[(c0 + 2 * i + 1) / G].base - tok));
+                x[i].x -= slope_s[c0 + 2 * i] * fabsf((float)(rows[(c0 + 2 * i) >> g_log].base - tok));
+                x[i].y -= slope_s[c0 + 2 * i + 1] * fabsf((float)(rows[(c0 + 2 * i + 1) >> g_log].base - tok));
               }
             }
             uint32_t see = 0xffffu;  // bit i: column c0 + i
             if (!all) {
               see = 0;
               for (int c = c0; c < c0 + 16 && c < cols && real; c += G) {
-                const int r = c / G;
+                const int r = c >> g_log;
                 if (row_sees(rows[r], a.mask ? a.mask + (int64_t)(win.row0 + r) * a.mask_words : nullptr, tok))
                   see |= ((1u << G) - 1u) << (c - c0);
               }
@@ -988,14 +997,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int g = 0; g < C::kGroups; ++g) {
         const int c0 = c_first + c_step * g;
         if (c0 >= cols) continue;
+        // 16 columns over 32 lanes: halves of the columns exchanged four times, 16 shuffles in all
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float sa = warp_sum(l[8 * g + i].x), sc = warp_sum(l[8 * g + i].y);
-          if (lane == 0) {
-            part_s[quad * C::kN + col0 + c0 + 2 * i] = sa;
-            part_s[quad * C::kN + col0 + c0 + 2 * i + 1] = sc;
+        for (int i = 0; i < 8; ++i) v[2 * i] = l[8 * g + i].x, v[2 * i + 1] = l[8 * g + i].y;
+#pragma unroll
+        for (int m = 8; m >= 1; m >>= 1)
+#pragma unroll
+          for (int i = 0; i < m; ++i) {
+            const float keep = lane & m ? v[i + m] : v[i], give = lane & m ? v[i] : v[i + m];
+            v[i] = keep + __shfl_xor_sync(kFullMask, give, m);
           }
-        }
+        v[0] += __shfl_xor_sync(kFullMask, v[0], 16);
+        if (lane < 16) part_s[quad * C::kN + col0 + c0 + lane] = v[0];
       }
       if (lane == 0 && (sw % (4 * sets)) == 0) ve_s[stream] = ve == -1000 ? 0 : ve;
       soft_sync();
@@ -1153,69 +1167,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(raw_full(n % p.ring), (n / p.ring) & 1); ++i) {
       }
     } else if (warp == kMmaWarp) {
-    // ------------------------------------------------ MMA issue
-    {
-      // (offsets are added to the low words in units of 16 bytes: no carry leaves the address)
-      const uint32_t q_at = desc_low(base + C::kOffQ, 16), v_at = desc_low(base + C::kOffV, D == 64 ? 0 : 64 * 128);
-      const uint32_t p_at = desc_low(base + C::kOffP, kTok * 128);
-      int it = 0, unit = 0, vslot = 0, vph = 0;
-      uint32_t sph = 0, pph = 0;  // phases of the score buffers and of the streams' weights
-      bool issued = false;
-      for_windows([&](const AttnWindow& win, int first, int last) -> bool {
-        // (the shuffles tell the compiler that the warp agrees)
-        const int padded = __shfl_sync(kFullMask, pad_cols(win), 0), n = SPLIT ? 2 * padded : padded;
-        const int tiles = __shfl_sync(kFullMask, last - first, 0);
-        const int streams = streams_of(padded), pitch = C::kN / streams;
-        const uint32_t ids = mma_idesc(n, false), idp = mma_idesc(n, true);
-        if (!wait(q_full, unit & 1)) return false;
-        ++unit;
-        auto weigh = [&](int k) -> bool {  // O^T of its stream += V^T P^T of the window's tile k
-          const int s = k & (streams - 1);
-          if (!wait(p_full(s), (pph >> s) & 1)) return false;
-          pph ^= 1u << s;
-          const uint32_t p_s = p_at + (uint32_t)((((s * pitch) >> 6) * (kTok * 128) + ((s * pitch) & 63) * 2) >> 4);
-          const uint32_t o_s = tmem + C::kO + s * pitch;
+    // ------------------------------------------------ MMA issue: scores
+    // (the shuffles tell the compiler that the warp agrees; offsets are added to the low words of
+    // the descriptors in units of 16 bytes: no carry leaves the address)
+    const uint32_t q_at = desc_low(base + C::kOffQ, 16);
+    int it = 0, unit = 0;
+    uint32_t sph = 0;  // phases of the score buffers
+    for_windows([&](const AttnWindow& win, int first, int last) -> bool {
+      const int padded = __shfl_sync(kFullMask, pad_cols(win), 0), n = SPLIT ? 2 * padded : padded;
+      const int tiles = __shfl_sync(kFullMask, last - first, 0);
+      const int streams = streams_of(padded), pitch = C::kN / streams;
+      const uint32_t ids = mma_idesc(n, false);
+      if (!wait(q_full, unit & 1)) return false;
+      ++unit;
+      for (int k = 0; k < tiles; ++k, ++it) {
+        const int b = it & 1, sb = k & (2 * streams - 1);
+        if (!wait(k_full(b), (it >> 1) & 1) || !wait(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
+        sph ^= 1u << sb;
+        tc_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ts(tmem + C::kS + sb * pitch, tmem + C::kK + b * C::kKCols + ks * 8,
+                 q_at + (((ks >> 2) * (C::kN * 128) + (ks & 3) * 32) >> 4), ids, ks > 0);
+        tc_commit(s_full(sb));
+        tc_commit(k_empty(b));
+      }
+      return true;
+    });
+    drain();
+    } else if (warp == kMmaWarp + 1) {
+    // ------------------------------------------------ MMA issue: values
+    const uint32_t v_at = desc_low(base + C::kOffV, D == 64 ? 0 : 64 * 128), p_at = desc_low(base + C::kOffP, kTok * 128);
+    int vslot = 0, vph = 0;
+    uint32_t pph = 0;  // phases of the streams' weights
+    for_windows([&](const AttnWindow& win, int first, int last) -> bool {
+      const int padded = __shfl_sync(kFullMask, pad_cols(win), 0), n = SPLIT ? 2 * padded : padded;
+      const int tiles = __shfl_sync(kFullMask, last - first, 0);
+      const int streams = streams_of(padded), pitch = C::kN / streams;
+      const uint32_t idp = mma_idesc(n, true);
+      for (int k = 0; k < tiles; ++k) {  // O^T of its stream += V^T P^T
+        const int s = k & (streams - 1);
+        const uint32_t p_s = p_at + (uint32_t)((((s * pitch) >> 6) * (kTok * 128) + ((s * pitch) & 63) * 2) >> 4);
+        const uint32_t o_s = tmem + C::kO + s * pitch;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            if (!wait(v_full(vslot), vph)) return false;
-            tc_after();
-#pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-#pragma unroll
-              for (int ks = 0; ks < kTok / 32; ++ks)
-                mma_ss(o_s + hf * C::kN, v_at + ((vslot * C::kVBytes + hf * 2 * 64 * 128 + ks * 2048) >> 4),
-                       p_s + ((half * (kTok / 2 * 128) + ks * 2048) >> 4), idp, k >= streams || half > 0 || ks > 0);
-            tc_commit(v_empty(vslot));
-            if (++vslot == C::kVSlots) vslot = 0, vph ^= 1;
-          }
-          tc_commit(p_empty(s));
-          return true;
-        };
-        for (int k = 0; k < tiles; ++k, ++it) {
-          const int b = it & 1, sb = k & (2 * streams - 1);
-          if (!wait(k_full(b), (it >> 1) & 1) || !wait(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
-          sph ^= 1u << sb;
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(v_full(vslot), vph)) return false;
+          if (half == 0 && !wait(p_full(s), (pph >> s) & 1)) return false;
           tc_after();
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            mma_ts(tmem + C::kS + sb * pitch, tmem + C::kK + b * C::kKCols + ks * 8,
-                   q_at + (((ks >> 2) * (C::kN * 128) + (ks & 3) * 32) >> 4), ids, ks > 0);
-          issued = true;
-          tc_commit(s_full(sb));
-          tc_commit(k_empty(b));
-          if (k >= streams && !weigh(k - streams)) return false;
+          for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+            for (int ks = 0; ks < kTok / 32; ++ks)
+              mma_ss(o_s + hf * C::kN, v_at + ((vslot * C::kVBytes + hf * 2 * 64 * 128 + ks * 2048) >> 4),
+                     p_s + ((half * (kTok / 2 * 128) + ks * 2048) >> 4), idp, k >= streams || half > 0 || ks > 0);
+          tc_commit(v_empty(vslot));
+          if (++vslot == C::kVSlots) vslot = 0, vph ^= 1;
         }
-        for (int k = max(0, tiles - streams); k < tiles; ++k)
-          if (!weigh(k)) return false;
-        return true;
-      });
-      if (issued) {  // every MMA has finished before TMEM is freed
-        tc_commit(drained);
-        for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(drained, 0); ++i) {
-        }
+        pph ^= 1u << s;
+        tc_commit(p_empty(s));
       }
-    }
-    __syncwarp();
+      return true;
+    });
+    drain();
     }
   }
 
