@@ -26,6 +26,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tq_attn.h"
 #include "tq_device.cuh"
@@ -203,15 +204,15 @@ constexpr int simt_smem_bytes() {
   return (kSimtCols * D + kSimtTok * (D + 1) + kSimtTok * D + 2 * kSimtTok + 64) * 4 + kSimtCols * (int)sizeof(RowView);
 }
 
-// Walsh-Hadamard transform of D values in shared memory by one warp.
-template <int D>
+// Walsh-Hadamard transform of N vectors of D values in shared memory by one warp.
+template <int D, int N = 1>
 __device__ __forceinline__ void fwht_shared(float* v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int h = 1; h < D; h <<= 1) {
     __syncwarp();
 #pragma unroll
-    for (int p = lane; p < D / 2; p += 32) {
+    for (int p = lane; p < N * D / 2; p += 32) {  // (pairs of one vector follow those of the one before)
       const int i = (p / h) * 2 * h + p % h;
       const float x = v[i], y = v[i + h];
       v[i] = x + y;
@@ -258,16 +259,25 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
     if (t_first >= t_last) continue;
     const int cols = win.nrows * G;
     __syncthreads();
-    // rotated queries
+    // rotated queries, the four columns' loads and stages together
+    constexpr int R = (D + 31) / 32;
+    float qv[kSimtPer][R];
+#pragma unroll
     for (int m = 0; m < kSimtPer; ++m) {
-      const int col = warp * kSimtPer + m;
-      if (col >= cols) break;
-      const int row = win.row0 + col / G;
-      const int64_t at = ((int64_t)row * a.num_q_heads + h * G + col % G) * D;
-      for (int j = lane; j < D; j += 32) q_s[col * D + j] = load_as_f32(a.q, at + j, a.q_dtype) * a.signs[j] * qmul;
-      fwht_shared<D>(q_s + col * D);
-      if (lane == 0) view[col] = row_view(a, row);
+      const int col = min(warp * kSimtPer + m, cols - 1);
+      const int64_t at = ((int64_t)(win.row0 + col / G) * a.num_q_heads + h * G + col % G) * D;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (D >= 32 || lane < D) qv[m][i] = load_as_f32(a.q, at + lane + 32 * i, a.q_dtype) * a.signs[lane + 32 * i] * qmul;
     }
+    if (lane < kSimtPer && warp * kSimtPer + lane < cols)
+      view[warp * kSimtPer + lane] = row_view(a, win.row0 + (warp * kSimtPer + lane) / G);
+#pragma unroll
+    for (int m = 0; m < kSimtPer; ++m)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (D >= 32 || lane < D) q_s[(warp * kSimtPer + m) * D + lane + 32 * i] = qv[m][i];
+    fwht_shared<D, kSimtPer>(q_s + warp * kSimtPer * D);
     __syncwarp();
     float o[kSimtPer][E], mx[kSimtPer], sum[kSimtPer];
 #pragma unroll
@@ -287,48 +297,80 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
       const int hi = max(win.p_hi, win.w_hi);
       if (t0 >= hi) continue;
       __syncthreads();
-      // dequantise 32 tokens
-      for (int i = tid; i < 2 * kSimtTok * D; i += kSimtWarps * 32) {
-        const int comp = i / (kSimtTok * D), t = i / D % kSimtTok, j = i % D;
+      // dequantise 32 tokens; a task is a run of coordinates of one row (32 of them in whole words;
+      // D = 16: the row, whose bytes may start anywhere)
+      constexpr int kRun = D < 32 ? D : 32, kRuns = D / kRun;
+      for (int i = tid; i < 2 * kSimtTok * kRuns; i += kSimtWarps * 32) {
+        const int comp = i / (kSimtTok * kRuns), t = i / kRuns % kSimtTok, run = i % kRuns;
         const int tok = t0 + t;
-        const int block = tok < hi && tok < cap ? table[tok / bs] : -1;
+        const bool there = tok < hi && tok < cap;
+        const int block = there ? table[tok / bs] : -1;
         const bool ok = block >= 0 && block < a.num_blocks;
-        if (tok < hi && tok < cap && !ok && j == 0 && comp == 0 && a.status)
-          atomicMax(a.status, (int32_t)kBlockOutOfRange);
-        float x = 0.f;
         const int bits = comp ? a.v_bits : a.k_bits, rb = comp ? rbv : rbk;
+        const uint8_t* row = (comp ? a.v_pages : a.k_pages) + (((int64_t)max(block, 0) * bs + tok % bs) * H + h) * rb;
+        uint32_t words[6] = {0, 0, 0, 0, 0, 0}, norm = 0;
         if (ok) {
-          const uint8_t* row = (comp ? a.v_pages : a.k_pages) + (((int64_t)block * bs + tok % bs) * H + h) * rb;
-          const int bit = j * bits;
-          uint32_t f = row[bit >> 3];
-          if ((bit & 7) + bits > 8) f |= (uint32_t)row[(bit >> 3) + 1] << 8;
-          x = cb_s[comp * 32 + ((f >> (bit & 7)) & ((1u << bits) - 1u))];
-          if (j == 0) {
-            const uint8_t* p = row + rb - 4;
-            const uint32_t u = p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16 | (uint32_t)p[3] << 24;
-            (comp ? vn_s : kn_s)[t] = __uint_as_float(u);
+          if constexpr (D >= 32) {
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+              if (k < bits) words[k] = __ldg(reinterpret_cast<const uint32_t*>(row) + run * bits + k);
+            norm = __ldg(reinterpret_cast<const uint32_t*>(row) + (rb - 4) / 4);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 10; ++k)
+              if (k < 2 * bits) words[k >> 2] |= (uint32_t)row[k] << (8 * (k & 3));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) norm |= (uint32_t)row[rb - 4 + k] << (8 * k);
           }
+        } else if (there && run == 0 && comp == 0 && a.status) {
+          atomicMax(a.status, (int32_t)kBlockOutOfRange);
         }
-        if (j == 0 && comp == 0) ok_s[t] = ok;
-        if (comp) v_s[t * D + j] = x;
-        else k_s[t * (D + 1) + j] = x;
+        if (run == 0) {
+          (comp ? vn_s : kn_s)[t] = __uint_as_float(norm);
+          if (comp == 0) ok_s[t] = ok;
+        }
+        float* to = comp ? v_s + t * D + run * kRun : k_s + t * (D + 1) + run * kRun;
+        auto expand = [&](auto tag) {
+          constexpr int B = decltype(tag)::value;
+#pragma unroll
+          for (int j = 0; j < kRun; ++j) {
+            const int w0 = j * B / 32, sh = j * B % 32;
+            const uint32_t f = sh + B <= 32 ? words[w0] >> sh : __funnelshift_r(words[w0], words[w0 + 1], sh);
+            to[j] = cb_s[comp * 32 + (f & ((1u << B) - 1u))];
+          }
+        };
+        if (bits == 4) expand(std::integral_constant<int, 4>{});
+        else if (bits == 3) expand(std::integral_constant<int, 3>{});
+        else if (bits == 2) expand(std::integral_constant<int, 2>{});
+        else expand(std::integral_constant<int, 5>{});
       }
       __syncthreads();
       const int tok = t0 + lane;
       const bool ok = ok_s[lane] != 0;
+      // the warp's four columns together: a key or value element read once serves all of them
+      const int first_col = warp * kSimtPer;
+      if (first_col >= cols) continue;  // (no barrier follows before the next step's)
+      float dot[kSimtPer];
+#pragma unroll
+      for (int m = 0; m < kSimtPer; ++m) dot[m] = 0.f;
+      const float* key = k_s + lane * (D + 1);
+#pragma unroll 8
+      for (int j = 0; j < D; ++j) {
+        const float x = key[j];
+#pragma unroll
+        for (int m = 0; m < kSimtPer; ++m) dot[m] = fmaf(q_s[(first_col + m) * D + j], x, dot[m]);
+      }
+      float pv[kSimtPer];
 #pragma unroll
       for (int m = 0; m < kSimtPer; ++m) {
-        const int col = warp * kSimtPer + m;
+        const int col = first_col + m;
+        pv[m] = 0.f;
         if (col >= cols) continue;
         const int row = win.row0 + col / G;
-        const RowView& v = view[col];
-        const bool see = ok && row_sees(v, a.mask ? a.mask + (int64_t)row * a.mask_words : nullptr, tok);
+        const bool see = ok && row_sees(view[col], a.mask ? a.mask + (int64_t)row * a.mask_words : nullptr, tok);
         float x = -INFINITY;
         if (see) {
-          float dot = 0.f;
-#pragma unroll 8
-          for (int j = 0; j < D; ++j) dot = fmaf(q_s[col * D + j], k_s[lane * (D + 1) + j], dot);
-          x = dot * kn_s[lane];
+          x = dot[m] * kn_s[lane];
           if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
           if (a.alibi) x -= a.alibi[h * G + col % G] * fabsf((float)(a.q_len[row] - 1 - tok));
           x *= kAttnLog2e;
@@ -343,12 +385,18 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
         sum[m] = sum[m] * corr + warp_sum(p);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[m][e] *= corr;
-        const float pv = p != 0.f ? p * vn_s[lane] : 0.f;
-        for (int t = 0; t < kSimtTok; ++t) {
-          const float pt = __shfl_sync(kFullMask, pv, t);
+        pv[m] = p != 0.f ? p * vn_s[lane] : 0.f;
+      }
+#pragma unroll 4
+      for (int t = 0; t < kSimtTok; ++t) {
+        float val[E];
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (D >= 32 || lane < D) o[m][e] = fmaf(pt, v_s[t * D + (D >= 32 ? lane + 32 * e : lane)], o[m][e]);
+        for (int e = 0; e < E; ++e) val[e] = v_s[t * D + (D >= 32 ? lane + 32 * e : lane & (D - 1))];
+#pragma unroll
+        for (int m = 0; m < kSimtPer; ++m) {
+          const float pt = __shfl_sync(kFullMask, pv[m], t);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[m][e] = fmaf(pt, val[e], o[m][e]);
         }
       }
     }
