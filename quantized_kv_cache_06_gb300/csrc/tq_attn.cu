@@ -354,11 +354,17 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
 #pragma unroll
       for (int m = 0; m < kSimtPer; ++m) dot[m] = 0.f;
       const float* key = k_s + lane * (D + 1);
-#pragma unroll 8
-      for (int j = 0; j < D; ++j) {
-        const float x = key[j];
+#pragma unroll 4
+      for (int j = 0; j < D; j += 4) {
+        const float x0 = key[j], x1 = key[j + 1], x2 = key[j + 2], x3 = key[j + 3];
 #pragma unroll
-        for (int m = 0; m < kSimtPer; ++m) dot[m] = fmaf(q_s[(first_col + m) * D + j], x, dot[m]);
+        for (int m = 0; m < kSimtPer; ++m) {
+          const float4 qq = *reinterpret_cast<const float4*>(q_s + (first_col + m) * D + j);
+          dot[m] = fmaf(qq.x, x0, dot[m]);
+          dot[m] = fmaf(qq.y, x1, dot[m]);
+          dot[m] = fmaf(qq.z, x2, dot[m]);
+          dot[m] = fmaf(qq.w, x3, dot[m]);
+        }
       }
       float pv[kSimtPer];
 #pragma unroll
