@@ -111,10 +111,13 @@ __host__ __device__ constexpr int span_bytes(int d, int bits) {
 }
 
 // Lookup tables in shared memory: 4-byte entries, a copy for each lane (entry e of lane l at
-// e * 128 + 4 l), so no lookup meets another lane's bank.  Keys: pairs of centroids by the 2 b
-// bits of two neighbouring indices; 5 bits (keys and values): single centroids.
+// e * 128 + 4 l), so no lookup meets another lane's bank: pairs of centroids by the 2 b bits of
+// two neighbouring indices, 5 bits single centroids.  4-bit values take none: 32 KB more would
+// leave too little for the ring, and sharing the keys' table was slower than byte permutes (64 x
+// 8192 tokens, K4/V4: tree 818 against 780 us, single tokens 322 against 306 us): the lookups load
+// the shared-memory pipe, the permutes the integer pipe.
 __host__ __device__ constexpr int key_table_bytes(int bits) { return (bits == 5 ? 32 : 1 << (2 * bits)) * 128; }
-__host__ __device__ constexpr int value_table_bytes(int bits) { return bits == 5 ? 32 * 128 : 0; }
+__host__ __device__ constexpr int value_table_bytes(int bits) { return bits == 4 ? 0 : key_table_bytes(bits); }
 
 struct TcAttnArgs {
   AttnArgs a;
@@ -259,7 +262,7 @@ __device__ __forceinline__ int exp_of(float x) { return max((int)((__float_as_ui
 
 // ---------------------------------------------------------------- dequantisation
 
-// Keys: 32 consecutive coordinates from the first BITS words of w, two per lookup (5 bits: one).
+// 32 consecutive coordinates from the first BITS words of w, two per lookup (5 bits: one).
 template <int BITS>
 __device__ __forceinline__ void expand32_table(const uint32_t* w, uint32_t tab_lane, uint32_t (&out)[16]) {
   if constexpr (BITS == 5) {
@@ -287,71 +290,46 @@ __device__ __forceinline__ void expand32_table(const uint32_t* w, uint32_t tab_l
   }
 }
 
-// Values: centroids fp16(alpha c) as byte tables in registers, the low and the high bytes of
+// 4-bit values: centroids fp16(alpha c) as byte tables in registers, the low and the high bytes of
 // eight entries per register pair.  A PRMT whose selector is four indices of three bits returns
-// the bytes of four coordinates.  Two units then share the work: the keys' lookups load the
-// shared-memory pipe, the values' the integer pipe (whose bytes have to go to shared memory
-// besides).  Four bits: the codebook is odd (c[15 - i] = -c[i]), so eight magnitudes and a sign
-// do; SYM false takes 16 entries.
-template <int BITS, bool SYM>
+// the bytes of four coordinates.  The codebook is odd (c[15 - i] = -c[i]), so eight magnitudes and
+// a sign do; ODD false takes all 16 entries and a select by the fourth bit.
+template <bool ODD>
 struct ByteTable {
-  static constexpr int kPairs = BITS == 4 && !SYM ? 2 : 1;
-  static constexpr int kFirst = BITS == 4 && SYM ? 8 : 0;
-  uint32_t lo[2 * kPairs], hi[2 * kPairs];
+  uint32_t lo[ODD ? 2 : 4], hi[ODD ? 2 : 4];
   __device__ __forceinline__ void load(const float* c, float alpha) {
 #pragma unroll
-    for (int r = 0; r < 2 * kPairs; ++r) {
+    for (int r = 0; r < (ODD ? 2 : 4); ++r) {
       lo[r] = hi[r] = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int e = kFirst + 4 * r + k;
-        if (e < (1 << BITS)) {
-          const uint32_t u = __half_as_ushort(__float2half_rn(__ldg(c + e) * alpha));
-          lo[r] |= (u & 255u) << (8 * k);
-          hi[r] |= (u >> 8) << (8 * k);
-        }
+        const uint32_t u = __half_as_ushort(__float2half_rn(__ldg(c + (ODD ? 8 : 0) + 4 * r + k) * alpha));
+        lo[r] |= (u & 255u) << (8 * k);
+        hi[r] |= (u >> 8) << (8 * k);
       }
     }
   }
 };
 
-// Eight consecutive coordinates (group g of the words) as four fp16 pairs.
-template <int BITS, bool SYM>
-__device__ __forceinline__ void expand8(const uint32_t* w, int g, const ByteTable<BITS, SYM>& t, uint32_t (&out)[4]) {
-  uint32_t sel;  // eight selector nibbles
-  if constexpr (BITS == 4 && SYM) {
-    const uint32_t n = ~w[g] & 0x88888888u;  // negative: index 7 - k is -c[8 + k]
-    sel = (w[g] ^ ((n >> 3) * 7u)) & 0x77777777u;
-  } else if constexpr (BITS == 4) {
-    sel = w[g] & 0x77777777u;
-  } else if constexpr (BITS == 3) {
-    const int bit = 24 * g, i = bit >> 5, sh = bit & 31;
-    uint32_t x = sh <= 8 ? w[i] >> sh : __funnelshift_r(w[i], w[i + 1], sh);
-    x = (x & 0x00000fffu) | ((x << 4) & 0x0fff0000u);
-    x = (x & 0x003f003fu) | ((x << 2) & 0x3f003f00u);
-    sel = (x & 0x07070707u) | ((x << 1) & 0x70707070u);
-  } else {
-    uint32_t x = g & 1 ? w[g >> 1] >> 16 : w[g >> 1] & 0xffffu;
-    x = (x | (x << 8)) & 0x00ff00ffu;
-    x = (x | (x << 4)) & 0x0f0f0f0fu;
-    sel = (x | (x << 2)) & 0x33333333u;
-  }
-  const uint32_t z = BITS == 4 ? w[g] << 4 : 0u;
+// Eight consecutive coordinates (a word) as four fp16 pairs.
+template <bool ODD>
+__device__ __forceinline__ void expand8(uint32_t w, const ByteTable<ODD>& t, uint32_t (&out)[4]) {
+  uint32_t sel = w;
+  if constexpr (ODD) sel ^= ((~w & 0x88888888u) >> 3) * 7u;  // index 7 - k is -c[8 + k]
+  sel &= 0x77777777u;
+  const uint32_t z = w << 4;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const uint32_t s = k ? sel >> 16 : sel;
+    uint32_t m;  // bytes 0xff where bit 3 of the index is set (the sign-replicating selector form)
+    if (k == 0) asm("prmt.b32 %0, %1, %2, 0xd9c8;\n" : "=r"(m) : "r"(z), "r"(w));
+    else asm("prmt.b32 %0, %1, %2, 0xfbea;\n" : "=r"(m) : "r"(z), "r"(w));
     uint32_t lo = __byte_perm(t.lo[0], t.lo[1], s), hi = __byte_perm(t.hi[0], t.hi[1], s);
-    if constexpr (BITS == 4) {
-      // bytes 0xff where bit 3 of the index is set (the sign-replicating selector form)
-      uint32_t m;
-      if (k == 0) asm("prmt.b32 %0, %1, %2, 0xd9c8;\n" : "=r"(m) : "r"(z), "r"(w[g]));
-      else asm("prmt.b32 %0, %1, %2, 0xfbea;\n" : "=r"(m) : "r"(z), "r"(w[g]));
-      if constexpr (SYM) {
-        hi |= ~m & 0x80808080u;
-      } else {
-        lo = (lo & ~m) | (__byte_perm(t.lo[2], t.lo[3], s) & m);
-        hi = (hi & ~m) | (__byte_perm(t.hi[2], t.hi[3], s) & m);
-      }
+    if constexpr (ODD) {
+      hi |= ~m & 0x80808080u;
+    } else {
+      lo = (lo & ~m) | (__byte_perm(t.lo[2], t.lo[3], s) & m);
+      hi = (hi & ~m) | (__byte_perm(t.hi[2], t.hi[3], s) & m);
     }
     out[2 * k] = __byte_perm(lo, hi, 0x5140);
     out[2 * k + 1] = __byte_perm(lo, hi, 0x7362);
@@ -488,7 +466,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       t[e * 32 + lane] = a.k_bits == 5 ? entry(a.k_centroids, a.k_alpha, e)
                                        : entry(a.k_centroids, a.k_alpha, e & mask) |
                                              entry(a.k_centroids, a.k_alpha, e >> a.k_bits) << 16;
-    for (int e = warp; e < vw / 32; e += kTcThreads / 32) t[kw + e * 32 + lane] = entry(a.v_centroids, a.v_alpha, e);
+    const int vmask = (1 << a.v_bits) - 1;
+    for (int e = warp; e < vw / 32; e += kTcThreads / 32)
+      t[kw + e * 32 + lane] = a.v_bits == 5 ? entry(a.v_centroids, a.v_alpha, e)
+                                            : entry(a.v_centroids, a.v_alpha, e & vmask) |
+                                                  entry(a.v_centroids, a.v_alpha, e >> a.v_bits) << 16;
   }
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   tc_before();
@@ -579,12 +561,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp < kKeyWarps + kValWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsDequant));
     // ------------------------------------------------ values: packed row -> swizzled k-line
-    auto values = [&](auto bits_tag, auto sym_tag) {
+    auto values = [&](auto bits_tag, auto odd_tag) {
       constexpr int BITS = decltype(bits_tag)::value;
-      constexpr bool SYM = decltype(sym_tag)::value;
       constexpr int SPAN = span_bytes(D, BITS);
-      ByteTable<BITS == 5 ? 2 : BITS, SYM> table;
-      if constexpr (BITS != 5) table.load(a.v_centroids, a.v_alpha);
+      ByteTable<decltype(odd_tag)::value> table;
+      if constexpr (BITS == 4) table.load(a.v_centroids, a.v_alpha);
       const uint32_t tab = vtab + lane * 4;
       const int half = (warp - kKeyWarps) >> 1, t = ((warp - kKeyWarps) & 1) * 32 + lane;  // token t of 64
       const uint32_t row = ring + (uint32_t)(kTok * spk + (64 * half + t) * SPAN);
@@ -604,16 +585,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
           for (int g = 0; g < D / 32; ++g) {
             uint32_t o[16];
-            if constexpr (BITS == 5) {
-              expand32_table<5>(wd, tab, o);
-            } else {
+            if constexpr (BITS == 4) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t x[4];
-                expand8<BITS, SYM>(wd, e, table, x);
+                expand8(wd[e], table, x);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[4 * e + i] = x[i];
               }
+            } else {
+              expand32_table<BITS>(wd, tab, o);
             }
             drop_words<BITS>(wd);
             const uint32_t at = to + (g >> 1) * (64 * 128) + (((uint32_t)(t & 7) ^ (uint32_t)(4 * (g & 1))) << 4);
@@ -1292,7 +1273,8 @@ cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream)
   const int stage = kTok * (spk + spv);
   const int fixed = 1024 + C::kOffTab + key_table_bytes(a.k_bits) + value_table_bytes(a.v_bits);
   t.ring = std::min(kMaxRing, (limit - fixed) / stage);
-  if (t.ring < 2) return cudaErrorInvalidValue;
+  // (one stage is left for 4-bit keys and 5-bit values of 256 channels, two or more otherwise)
+  if (t.ring < 1) return cudaErrorInvalidValue;
   const int smem = fixed + t.ring * stage;
   auto kern = attn_tc_kernel<D, SPLIT>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -136,6 +136,11 @@ TREE_CASES = [
     (256, 4, 4, 8, 1, 16, [130, 31], [9, 70]),
     (256, 5, 5, 32, 8, 16, [77], [3]),
     (256, 3, 2, 8, 4, 5, [200, 1], [6, 1]),
+    (256, 4, 5, 8, 4, 16, [300, 20], [40, 2]),
+    (256, 4, 3, 4, 4, 16, [300, 20], [40, 2]),
+    (256, 5, 4, 8, 4, 16, [300, 20], [4, 2]),
+    (128, 4, 5, 16, 4, 16, [700], [20]),
+    (64, 5, 5, 16, 4, 16, [700], [20]),
     (32, 4, 3, 8, 2, 16, [70], [12]),
     (16, 3, 5, 8, 2, 16, [70, 3], [12, 1]),
 ]
@@ -372,6 +377,21 @@ def test_pages_beyond_32_bit_offsets(dtype):
     q = torch.from_numpy(rng.standard_normal((2, 4, 128)).astype(np.float32)).cuda().to(DT[dtype])
     q_seq, q_len = np.zeros(2, dtype=int), np.array([199, 200])
     out = tq.tq_paged_prefill_biased(q, _i32(q_seq), _i32(q_len), **dv)
+    want, reach = c.oracle(q.float().cpu().numpy(), q_seq, so.biased_visible(q_seq, q_len, c.cap, 1))
+    _close(out, want, reach, dtype, 128)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+def test_codebooks_that_are_not_odd(dtype):
+    # the calls take any ascending centroids; the library's own are odd, which the values' expansion uses
+    tq = _tq()
+    rng = np.random.default_rng(31)
+    c = Cache(rng, [200], 128, 4, 4, 4)
+    c.vc = np.sort(c.vc + rng.uniform(0.0, 0.01, 16).astype(np.float32)).astype(np.float32)
+    c.kc = np.sort(c.kc + rng.uniform(0.0, 0.01, 16).astype(np.float32)).astype(np.float32)
+    q = torch.from_numpy(rng.standard_normal((5, 8, 128)).astype(np.float32)).cuda().to(DT[dtype])
+    q_seq, q_len = np.zeros(5, dtype=int), np.array([200, 3, 130, 77, 199])
+    out = tq.tq_paged_prefill_biased(q, _i32(q_seq), _i32(q_len), **c.dev())
     want, reach = c.oracle(q.float().cpu().numpy(), q_seq, so.biased_visible(q_seq, q_len, c.cap, 1))
     _close(out, want, reach, dtype, 128)
 
