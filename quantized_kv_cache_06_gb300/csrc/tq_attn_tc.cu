@@ -37,7 +37,6 @@
 // Rows whose slab is not a multiple of 16 bytes (H not a multiple of 4) come by 4-byte
 // cp.async.  All waits are bounded: one that runs out records the timeout, every role leaves
 // its loop, copies and MMAs in flight are drained and TMEM is freed.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -55,21 +54,21 @@ namespace {
 constexpr float kLog2eA = 1.4426950408889634f;
 constexpr int kTok = kAttnTile;  // tokens per tile = MMA lanes
 constexpr int kKeyWarps = 4, kValWarps = 4, kSoftSets = 2, kSoftWarps = 4 * kSoftSets;
-constexpr int kCopyWarp = kKeyWarps + kValWarps + kSoftWarps;
-constexpr int kMmaWarp = kCopyWarp + 1;
-constexpr int kTcThreads = 32 * (kCopyWarp + 4);  // whole warpgroups (two warps idle)
+constexpr int kMmaWarp = kKeyWarps + kValWarps + kSoftWarps;
+constexpr int kTcThreads = 32 * (kMmaWarp + 4);  // whole warpgroups (two warps idle)
 constexpr int kSoftThreads = 32 * kSoftWarps;
 // Registers a thread: 96 at launch (640 threads); the softmax warps, which hold sums of up to 64
 // columns, take what the others leave (a spill there goes to L2: little L1 is left beside the
 // shared memory).  128 (dequant + dequant + issue) + 256 soft <= 640 * 96.
 constexpr int kRegsIssue = 64;
 constexpr int kMaxRing = 6;
-constexpr int kNorms = 6;  // tiles whose norms are kept: keys run at most five tiles ahead of the softmax
+constexpr int kNorms = 6;  // tiles whose norms are kept: keys and values run at most five tiles ahead of the softmax
 constexpr float kSlack = 6.0f;            // log2 units the running max may lag
 constexpr float kMaxWeight = 64.0f;       // 2^kSlack
 constexpr float kLoQ = 4096.0f;           // scale of the fp16 remainders of Q
 constexpr float kLoP = 2048.0f;           // and of P'
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
+constexpr int kNoToken = -0x7fffffff - 1;  // a table entry that no token asks for
 constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
 
 template <int D, bool SPLIT>
@@ -95,8 +94,8 @@ struct Tc {
   static constexpr int kOffRows = kOffP + kPBytes;                 // RowSees[kCols]
   // floats [kN]: -max, correction, slope; part [4][kN]
   static constexpr int kOffCol = kOffRows + (kCols * (int)sizeof(RowSees) + 15) / 16 * 16;
-  static constexpr int kOffMeta = kOffCol + 7 * kN * 4;            // uint32 valid[kMaxRing][4], of tiles [kNorms][4]
-  static constexpr int kOffNorm = kOffMeta + (kMaxRing + kNorms) * 16;  // float2 (nu_k, nu_v) [kNorms][128]
+  static constexpr int kOffMeta = kOffCol + 7 * kN * 4;            // uint32 valid[kNorms][4], a bit per token
+  static constexpr int kOffNorm = kOffMeta + kNorms * 16;  // float2 (nu_k, nu_v) [kNorms][128]
   static constexpr int kOffTab = (kOffNorm + kNorms * kTok * 8 + 127) / 128 * 128;  // key table, 5-bit value table, ring
   static constexpr int kRegsDequant = D == 256 ? 96 : 64;
   static constexpr int kRegsSoft = (640 * 96 - 128 * (2 * kRegsDequant + kRegsIssue)) / 256 / 8 * 8;
@@ -122,9 +121,9 @@ __host__ __device__ constexpr int value_table_bytes(int bits) { return bits == 4
 struct TcAttnArgs {
   AttnArgs a;
   AttnWork w;
-  int ring;        // stages
-  int sub;         // tokens per copy: the largest power of two that divides the block size, at most 128
-  int tma;         // rows arrive by TMA (else cp.async)
+  int ring;        // stages of packed rows, 1 .. kMaxRing
+  int wide;        // slabs are whole 16 bytes: rows come in 16-byte copies (else by words)
+  int bs_log;      // log2 of the block size, -1 if it is not a power of two
   uint32_t tries;  // of a bounded wait
 };
 
@@ -336,51 +335,16 @@ __device__ __forceinline__ void expand8(uint32_t w, const ByteTable<ODD>& t, uin
   }
 }
 
-// The row of this thread's token in the ring, indices and norm: SPAN bytes, of which the row
-// starts `skip` words in.
-template <int D, int BITS>
-__device__ __forceinline__ void load_row(uint32_t addr, int skip, uint32_t (&w)[D * BITS / 32 + 1]) {
-  constexpr int SPAN = span_bytes(D, BITS), NW = D * BITS / 32;
-  constexpr int NV = (NW + 4 + 3) / 4 < SPAN / 16 ? (NW + 4 + 3) / 4 : SPAN / 16;
-  uint32_t r[4 * NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint4 v = ld_v4(addr + 16 * i);
-    r[4 * i] = v.x;
-    r[4 * i + 1] = v.y;
-    r[4 * i + 2] = v.z;
-    r[4 * i + 3] = v.w;
-  }
-  auto take = [&](auto tag) {
-    constexpr int K = decltype(tag)::value;
-#pragma unroll
-    for (int i = 0; i <= NW; ++i) w[i] = r[i + K < 4 * NV ? i + K : 0];
-  };
-  if (skip == 0) take(std::integral_constant<int, 0>{});
-  else if (skip == 1) take(std::integral_constant<int, 1>{});
-  else if (skip == 2) take(std::integral_constant<int, 2>{});
-  else take(std::integral_constant<int, 3>{});
-}
-
-// Drops the first N words: a loop over a row stays rolled (the roles share the instruction
-// cache) with the row in registers.
-template <int N, int NW>
-__device__ __forceinline__ void drop_words(uint32_t (&w)[NW]) {
-#pragma unroll
-  for (int i = 0; i + N < NW; ++i) w[i] = w[i + N];
-}
-
 // ---------------------------------------------------------------- the kernel
 
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    attn_tc_kernel(const __grid_constant__ TcAttnArgs p, const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap) {
+    attn_tc_kernel(const __grid_constant__ TcAttnArgs p) {
   using C = Tc<D, SPLIT>;
   const AttnArgs& a = p.a;
   const AttnWork& w = p.w;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxRing + 27];
+  __shared__ __align__(8) uint64_t bars[kNorms + 27];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead, fail[2][2], fail_all;
   __shared__ int full_lo_s, full_hi_s, pre_lo_s, pre_hi_s, q_exp;
@@ -391,15 +355,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int h = blockIdx.x % H, part = blockIdx.x / H;
   const int rbk = D * a.k_bits / 8 + 4, rbv = D * a.v_bits / 8 + 4;
   const int spk = span_bytes(D, a.k_bits), spv = span_bytes(D, a.v_bits);
-  const int skip_k = p.tma ? (h * rbk) % 16 : 0, skip_v = p.tma ? (h * rbv) % 16 : 0;
+  const int skip_k = p.wide ? (h * rbk) % 16 : 0, skip_v = p.wide ? (h * rbv) % 16 : 0;
   const int stage_bytes = kTok * (spk + spv);
   const uint32_t ktab = base + C::kOffTab, vtab = ktab + key_table_bytes(a.k_bits);
   const uint32_t ring = vtab + value_table_bytes(a.v_bits);
 
   auto bar = [&](int i) -> uint32_t { return smem_a(bars) + 8u * i; };
-  auto raw_full = [&](int s) { return bar(s); };
-  auto raw_empty = [&](int s) { return bar(kMaxRing + s); };
-  const int B0 = 2 * kMaxRing;
+  const int B0 = kNorms;
+  auto n_full = [&](int b) { return bar(b); };  // values' norms of a tile
   auto k_full = [&](int b) { return bar(B0 + b); };
   auto k_empty = [&](int b) { return bar(B0 + 2 + b); };
   auto v_full = [&](int b) { return bar(B0 + 4 + b); };  // one per value slot
@@ -414,13 +377,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // A bounded wait of one thread; a role that has seen another give up leaves too.
   auto wait1 = [&](uint32_t b, uint32_t parity) -> bool {
     for (uint32_t i = 0; i < p.tries; ++i) {
-      if (bar_try(b, parity)) return true;
-      if ((i & 255u) == 255u && *dead_v) return false;
+      if (__builtin_expect(bar_try(b, parity), 1)) return true;
+      if (*dead_v) break;
     }
-    if (!*dead_v) {
-      *dead_v = 1;
-      if (a.status) atomicMax(a.status, (int32_t)kTimeout);
-    }
+    *dead_v = 1;  // reported at the end
     return false;
   };
   // The same by a whole warp, with one answer.
@@ -429,10 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     dead = 0;
     fail[0][0] = fail[0][1] = fail[1][0] = fail[1][1] = fail_all = 0;
-    for (int s = 0; s < kMaxRing; ++s) {
-      bar_init(raw_full(s), p.tma ? 1 : 33);  // cp.async: every lane's copies and one arrival
-      bar_init(raw_empty(s), kKeyWarps + kValWarps);
-    }
+    for (int b = 0; b < kNorms; ++b) bar_init(n_full(b), kValWarps);
     for (int b = 0; b < 2; ++b) {
       bar_init(k_full(b), kKeyWarps);
       bar_init(k_empty(b), 1);
@@ -502,6 +459,65 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Two streams of tiles when the window's MMA columns fit half of the TMEM regions.
   auto streams_of = [&](int padded) -> int { return (SPLIT ? 2 * padded : padded) <= C::kN / 2 ? 2 : 1; };
 
+  // Packed rows: a lane copies the rows of its token itself, `ring` tiles deep, so no other thread
+  // waits for them.  A cursor walks the part's tiles ahead of their use.
+  struct Cursor {
+    int g, wi, end, n_a, t_a, t_b, hi;  // tile, window, first tile behind it; its intervals, last token + 1
+    const int32_t* table;
+  };
+  const int cap = (int)min((int64_t)a.max_blocks_per_seq * a.block_size, (int64_t)0x7fffff00);
+  auto enter = [&](Cursor& c) {  // the window of tile c.g (c.g < g1), from c.wi on
+    for (;; ++c.wi) {
+      const AttnWindow win = w.win[c.wi];
+      c.end = win.tile_base + win.nA + win.nB;
+      if (c.g >= c.end) continue;
+      c.n_a = win.tile_base + win.nA;
+      c.t_a = win.tA0 - win.tile_base;
+      c.t_b = win.tB0 - c.n_a;
+      c.hi = min(max(win.p_hi, win.w_hi), cap);
+      c.table = a.block_table + (int64_t)win.seq * a.max_blocks_per_seq;
+      return;
+    }
+  };
+  // the table entry of token `lane_tok` of tile c.g (kNoToken: none there); then on to the next tile
+  auto next_entry = [&](Cursor& c, int lane_tok, int& off) -> int {
+    off = 0;
+    if (c.g >= g1) return kNoToken;
+    if (c.g >= c.end) enter(c);
+    const int tok = (c.g + (c.g < c.n_a ? c.t_a : c.t_b)) * kTok + lane_tok;
+    ++c.g;
+    if (tok >= c.hi) return kNoToken;
+    const int col = p.bs_log >= 0 ? tok >> p.bs_log : tok / a.block_size;
+    off = tok - col * a.block_size;
+    return __ldg(c.table + col);
+  };
+  // Starts the copies of the row at (block, off) to `dst`; whether there is one.
+  auto copy_row = [&](const uint8_t* from, int slab, int skip, int rb, uint32_t dst, int block, int off) -> bool {
+    const bool ok = block >= 0 && block < a.num_blocks;
+    if (ok) {
+      const uint8_t* src = from + ((int64_t)block * a.block_size + off) * slab;
+      if (p.wide) {
+        for (int c = 0; c < skip + rb; c += 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst + c), "l"(src + c) : "memory");
+      } else {
+        for (int c = 0; c < rb; c += 4)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst + c), "l"(src + c) : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    return ok;
+  };
+  // All but the newest ring - 1 groups of this thread have landed.
+  auto landed = [&]() {
+    switch (p.ring) {
+      case 1: asm volatile("cp.async.wait_group 0;\n" ::: "memory"); break;
+      case 2: asm volatile("cp.async.wait_group 1;\n" ::: "memory"); break;
+      case 3: asm volatile("cp.async.wait_group 2;\n" ::: "memory"); break;
+      case 4: asm volatile("cp.async.wait_group 3;\n" ::: "memory"); break;
+      case 5: asm volatile("cp.async.wait_group 4;\n" ::: "memory"); break;
+      default: asm volatile("cp.async.wait_group 5;\n" ::: "memory"); break;
+    }
+  };
   // Every MMA of an issuing warp has finished before TMEM is freed.
   auto drain = [&]() {
     const uint32_t b = drained + (warp == kMmaWarp ? 0 : 8);
@@ -517,33 +533,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr int BITS = decltype(bits_tag)::value;
       constexpr int SPAN = span_bytes(D, BITS);
       const uint32_t tab = ktab + lane * 4;
-      const uint32_t row = ring + (uint32_t)((warp * 32 + lane) * SPAN);
+      const int t_lane = warp * 32 + lane;
+      const uint32_t row = ring + (uint32_t)(t_lane * SPAN);
       const uint32_t dst = tmem + ((uint32_t)(32 * warp) << 16) + C::kK;
-      const uint32_t vnorm = ring + (uint32_t)(kTok * spk + (warp * 32 + lane) * spv + skip_v + rbv - 4);
       float2* norms = reinterpret_cast<float2*>(smem + C::kOffNorm);
       uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::kOffMeta);
-      int st = 0, ph = 0, it = 0;
-      for_windows([&](const AttnWindow&, int first, int last) -> bool {
-        for (int t = first; t < last; ++t, ++it) {
-          if (!wait(raw_full(st), ph)) return false;
-          uint32_t wd[D * BITS / 32 + 1];
-          load_row<D, BITS>(row + st * stage_bytes, skip_k >> 2, wd);
-          // the token's norms go on to the softmax warps (what they say is ordered by k_full,
-          // the product and its completion)
-          const float vn = __uint_as_float(ld_s32(vnorm + st * stage_bytes));
-          norms[(it % kNorms) * kTok + warp * 32 + lane] = make_float2(__uint_as_float(wd[D * BITS / 32]), vn);
-          if (lane == 0) valid[4 * (kMaxRing + it % kNorms) + warp] = valid[4 * st + warp];
-          __syncwarp();
-          if (lane == 0) bar_arrive(raw_empty(st));
-          if (++st == p.ring) st = 0, ph ^= 1;
+      const uint8_t* from = a.k_pages + h * rbk - skip_k;
+      Cursor cur{g0, g0 < g1 ? window_of(w, g0) : 0, g0, 0, 0, 0, 0, nullptr};  // (entered by the first entry)
+      uint32_t there = 0;  // bit s: stage s holds a row
+      int next_off, next = next_entry(cur, t_lane, next_off);  // entries are loaded a tile before their copies
+      int st = 0;
+      // (rounds before tile 0 only fill the ring)
+#pragma unroll 1
+      for (int it = -p.ring; it < g1 - g0; ++it) {
+        if (it >= 0) {
+          landed();
+          const uint32_t here = row + st * stage_bytes + skip_k;
+          const bool ok = (there >> st) & 1u;
+          // norms and validity go on to the softmax warps (what they say is ordered by k_full,
+          // n_full, the product and its completion)
+          const int slot = it % kNorms;
+          norms[slot * kTok + t_lane].x = __uint_as_float(ld_s32(here + D * BITS / 8));
+          const uint32_t m = __ballot_sync(kFullMask, ok);
+          if (lane == 0) valid[4 * slot + warp] = m;
           const int b = it & 1;
-          if (!wait(k_empty(b), ((it >> 1) & 1) ^ 1)) return false;
+          if (!wait(k_empty(b), ((it >> 1) & 1) ^ 1)) break;
           tc_after();
 #pragma unroll 1
           for (int g = 0; g < D / 32; ++g) {
             uint32_t o[16];
+            uint32_t wd[BITS + 1];
+#pragma unroll
+            for (int i = 0; i < BITS; ++i) wd[i] = ld_s32(here + 4 * (BITS * g + i));
+            wd[BITS] = 0;
             expand32_table<BITS>(wd, tab, o);
-            drop_words<BITS>(wd);
             tm_st16(dst + b * C::kKCols + 16 * g, o);
           }
           tm_wait_st();
@@ -551,13 +574,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
           if (lane == 0) bar_arrive(k_full(b));
         }
-        return true;
-      });
+        // the stage's row has been read: the row `ring` tiles on
+        const int block = next, off = next_off;
+        next = next_entry(cur, t_lane, next_off);
+        const bool copied = copy_row(from, H * rbk, skip_k, rbk, row + st * stage_bytes, block, off);
+        there = copied ? there | (1u << st) : there & ~(1u << st);
+        if (++st == p.ring) st = 0;
+      }
     };
     if (a.k_bits == 4) keys(std::integral_constant<int, 4>{});
     else if (a.k_bits == 3) keys(std::integral_constant<int, 3>{});
     else if (a.k_bits == 2) keys(std::integral_constant<int, 2>{});
     else keys(std::integral_constant<int, 5>{});
+    asm volatile("cp.async.wait_all;\n" ::: "memory");  // no copy outlives its use
   } else if (warp < kKeyWarps + kValWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsDequant));
     // ------------------------------------------------ values: packed row -> swizzled k-line
@@ -568,23 +597,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if constexpr (BITS == 4) table.load(a.v_centroids, a.v_alpha);
       const uint32_t tab = vtab + lane * 4;
       const int half = (warp - kKeyWarps) >> 1, t = ((warp - kKeyWarps) & 1) * 32 + lane;  // token t of 64
-      const uint32_t row = ring + (uint32_t)(kTok * spk + (64 * half + t) * SPAN);
+      const int t_lane = 64 * half + t;
+      const uint32_t row = ring + (uint32_t)(kTok * spk + t_lane * SPAN);
       const uint32_t line = base + C::kOffV + (uint32_t)((t >> 3) * 1024 + (t & 7) * 128);
-      int st = 0, ph = 0;
+      float2* norms = reinterpret_cast<float2*>(smem + C::kOffNorm);
+      const uint8_t* from = a.v_pages + h * rbv - skip_v;
+      Cursor cur{g0, g0 < g1 ? window_of(w, g0) : 0, g0, 0, 0, 0, 0, nullptr};  // (entered by the first entry)
+      int next_off, next = next_entry(cur, t_lane, next_off);
+      int st = 0;
       int slot = half % C::kVSlots, vph = 1;  // slot 2 it + half, round by round
-      for_windows([&](const AttnWindow&, int first, int last) -> bool {
-        for (int k = first; k < last; ++k) {
-          if (!wait(raw_full(st), ph)) return false;
-          uint32_t wd[D * BITS / 32 + 1];
-          load_row<D, BITS>(row + st * stage_bytes, skip_v >> 2, wd);
+#pragma unroll 1
+      for (int it = -p.ring; it < g1 - g0; ++it) {
+        if (it >= 0) {
+          landed();
+          const uint32_t here = row + st * stage_bytes + skip_v;
+          norms[(it % kNorms) * kTok + t_lane].y = __uint_as_float(ld_s32(here + D * BITS / 8));
           __syncwarp();
-          if (lane == 0) bar_arrive(raw_empty(st));
-          if (++st == p.ring) st = 0, ph ^= 1;
-          if (!wait(v_empty(slot), vph)) return false;
+          if (lane == 0) bar_arrive(n_full(it % kNorms));
+          if (!wait(v_empty(slot), vph)) break;
           const uint32_t to = line + slot * C::kVBytes;
 #pragma unroll 1
           for (int g = 0; g < D / 32; ++g) {
-            uint32_t o[16];
+            uint32_t o[16], wd[BITS + 1];
+#pragma unroll
+            for (int i = 0; i < BITS; ++i) wd[i] = ld_s32(here + 4 * (BITS * g + i));
+            wd[BITS] = 0;
             if constexpr (BITS == 4) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -596,7 +633,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             } else {
               expand32_table<BITS>(wd, tab, o);
             }
-            drop_words<BITS>(wd);
             const uint32_t at = to + (g >> 1) * (64 * 128) + (((uint32_t)(t & 7) ^ (uint32_t)(4 * (g & 1))) << 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -608,8 +644,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           slot += 2;
           if (slot >= C::kVSlots) slot -= C::kVSlots, vph ^= 1;
         }
-        return true;
-      });
+        const int block = next, off = next_off;
+        next = next_entry(cur, t_lane, next_off);
+        copy_row(from, H * rbv, skip_v, rbv, row + st * stage_bytes, block, off);
+        // (the values' warps report an entry out of range; the keys' leave its token out)
+        if (block != kNoToken && (block < 0 || block >= a.num_blocks) && a.status)
+          atomicMax(a.status, (int32_t)kBlockOutOfRange);
+        if (++st == p.ring) st = 0;
+      }
     };
     using No = std::integral_constant<bool, false>;
     if (a.v_bits == 4) {
@@ -620,7 +662,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (a.v_bits == 3) values(std::integral_constant<int, 3>{}, No{});
     else if (a.v_bits == 2) values(std::integral_constant<int, 2>{}, No{});
     else values(std::integral_constant<int, 5>{}, No{});
-  } else if (warp < kCopyWarp) {
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+  } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoft));
     // ------------------------------------------------ softmax, queries and outputs
     const int sw = warp - kKeyWarps - kValWarps;  // softmax warp
@@ -730,7 +773,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = wait(s_full(sb), this_s);
         tc_after();
         const float2 kv = norms[slot * kTok + t_lane];
-        const uint4 vv = *reinterpret_cast<const uint4*>(valid + 4 * (kMaxRing + slot));
+        const uint4 vv = *reinterpret_cast<const uint4*>(valid + 4 * slot);
         const bool p_free = bar_test(p_empty(stream), this_p ^ 1);  // asked now, needed at the first store
         float kn = kv.x * q_up;
         const float vn = kv.y;
@@ -757,7 +800,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         };
         bool seen = true;  // a column of this thread sees its token
-        if (!all || capped || biased) {
+        if (__builtin_expect(!all || capped || biased, 0)) {
           // Scores in place: nu_k, cap, distance, -inf where the token is not seen; what follows
           // takes them with a factor of one.  (A loop apart, so that plain tiles keep their code
           // together in the instruction cache.)
@@ -859,7 +902,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (again) break;
           const bool grow = vf > 0.f && exp_of(vf) - ve > 9;
-          if (!named_any(bar_id, bar_n, over > kMaxWeight || grow || !ok)) break;
+          if (__builtin_expect(!named_any(bar_id, bar_n, over > kMaxWeight || grow || !ok), 1)) break;
           if (*fl) {  // the same for all warps of the stream
             broken = true;
             break;
@@ -942,7 +985,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         if (broken) continue;
-        if (__any_sync(kFullMask, real && seen && !vfin)) {
+        if (__builtin_expect(__any_sync(kFullMask, real && seen && !vfin), 0)) {
           // a value norm that is infinite or NaN: where its token has weight, the output takes it
           // (its weights above were zero)
 #pragma unroll 1
@@ -1057,97 +1100,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     });
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsIssue));
-    if (warp == kCopyWarp) {
-    // ------------------------------------------------ copies of packed rows
-    const int bs = a.block_size, sub = p.sub;
-    const int cap = (int)min((int64_t)a.max_blocks_per_seq * bs, (int64_t)0x7fffff00);
-    uint32_t* valid = reinterpret_cast<uint32_t*>(smem + C::kOffMeta);
-    const uint32_t per_copy = (uint32_t)(sub * (spk + spv));
-    int st = 0, ph = 0, issued = 0;
-    for_windows([&](const AttnWindow& win, int first, int last) -> bool {
-      const int32_t* table = a.block_table + (int64_t)win.seq * a.max_blocks_per_seq;
-      const int hi = min(max(win.p_hi, win.w_hi), cap);
-      for (int t = first; t < last; ++t) {
-        const int t0 = tile_token(win, t);
-        if (!wait(raw_empty(st), ph ^ 1)) return false;
-        uint32_t* v = valid + 4 * st;
-        if (lane < 4) v[lane] = 0;
-        __syncwarp();
-        const uint32_t kdst = ring + st * stage_bytes, vdst = kdst + kTok * spk;
-        int live = 0;
-        for (int i0 = 0; i0 < kTok / sub; i0 += 32) {
-          const int i = i0 + lane, tok = t0 + i * sub;
-          int block = -1;
-          if (i < kTok / sub && tok < hi) {
-            block = __ldg(table + tok / bs);
-            if (block < 0 || block >= a.num_blocks) {
-              block = -1;
-              if (a.status) atomicMax(a.status, (int32_t)kBlockOutOfRange);
-            }
-          }
-          if (block >= 0) {
-            if (sub >= 32) {
-              for (int k = 0; k < sub / 32; ++k) v[i * (sub / 32) + k] = 0xffffffffu;
-            } else {
-              atomicOr(v + ((i * sub) >> 5), ((1u << sub) - 1u) << ((i * sub) & 31));
-            }
-          }
-          if (p.tma) {
-            const unsigned m = __ballot_sync(kFullMask, block >= 0);
-            live += __popc(m);
-            // the transactions of this round are announced before its copies start
-            if (lane == 0 && m) {
-              asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(raw_full(st)),
-                           "r"((uint32_t)__popc(m) * per_copy)
-                           : "memory");
-            }
-            __syncwarp();
-            if (block >= 0) {
-              const int y = (int)((int64_t)block * bs + tok % bs);
-              asm volatile(
-                  "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-                  "[%4];\n" ::"r"(kdst + i * sub * spk),
-                  "l"(&kmap), "r"(h * rbk - skip_k), "r"(y), "r"(raw_full(st))
-                  : "memory");
-              asm volatile(
-                  "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-                  "[%4];\n" ::"r"(vdst + i * sub * spv),
-                  "l"(&vmap), "r"(h * rbv - skip_v), "r"(y), "r"(raw_full(st))
-                  : "memory");
-            }
-          } else {
-            // word by word; the rows of a round's copies are taken one after another by the warp
-            for (int k = 0; k < min(32, kTok / sub - i0); ++k) {
-              const int bk = __shfl_sync(kFullMask, block, k);
-              if (bk < 0) continue;
-              const int tk = t0 + (i0 + k) * sub;
-              const int64_t slot = (int64_t)bk * bs + tk % bs;
-              const int wk = rbk / 4, wv = rbv / 4, per = wk + wv;
-              for (int x = lane; x < sub * per; x += 32) {
-                const int r = x / per, c = x % per;
-                const int64_t line = (slot + r) * H + h;
-                const uint8_t* src = c < wk ? a.k_pages + line * rbk + 4 * c : a.v_pages + line * rbv + 4 * (c - wk);
-                const uint32_t dst = c < wk ? kdst + ((i0 + k) * sub + r) * spk + 4 * c
-                                            : vdst + ((i0 + k) * sub + r) * spv + 4 * (c - wk);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (!p.tma) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(raw_full(st)) : "memory");
-        if (lane == 0) bar_arrive(raw_full(st));
-        ++issued;
-        if (++st == p.ring) st = 0, ph ^= 1;
-      }
-      return true;
-    });
-    if (!p.tma) asm volatile("cp.async.wait_all;\n" ::: "memory");
-    // none of the copies outlives the loop
-    for (int n = max(0, issued - p.ring); n < issued; ++n)
-      for (uint32_t i = 0; i < kDefaultWaitTries && !bar_try(raw_full(n % p.ring), (n / p.ring) & 1); ++i) {
-      }
-    } else if (warp == kMmaWarp) {
+    if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issue: scores
     // (the shuffles tell the compiler that the warp agrees; offsets are added to the low words of
     // the descriptors in units of 16 bytes: no carry leaves the address)
@@ -1163,7 +1116,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ++unit;
       for (int k = 0; k < tiles; ++k, ++it) {
         const int b = it & 1, sb = k & (2 * streams - 1);
-        if (!wait(k_full(b), (it >> 1) & 1) || !wait(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
+        if (!wait(k_full(b), (it >> 1) & 1) || !wait(n_full(it % kNorms), (it / kNorms) & 1) || !wait(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
         sph ^= 1u << sb;
         tc_after();
 #pragma unroll
@@ -1216,40 +1169,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
+  if (tid == 0 && dead && a.status) atomicMax(a.status, (int32_t)kTimeout);
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
 }
 
 // ---------------------------------------------------------------- launch
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-
-// The pages as a 2-D byte tensor [num_blocks * block_size][slab] with boxes of `sub` rows x `span`.
-bool page_map(CUtensorMap* map, const uint8_t* pages, int64_t rows, int64_t slab, int span, int sub) {
-  const EncodeTiled fn = encode_tiled();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)slab, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)slab};
-  const cuuint32_t box[2] = {(cuuint32_t)span, (cuuint32_t)sub};
-  const cuuint32_t step[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pages), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int D, bool SPLIT>
 cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
@@ -1258,17 +1183,12 @@ cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream)
   t.a = a;
   t.w = w;
   t.tries = wait_tries();
-  int sub = 1;
-  while (sub < kTok && a.block_size % (2 * sub) == 0) sub *= 2;
-  t.sub = sub;
-  const int64_t ks = (int64_t)a.num_kv_heads * (D * a.k_bits / 8 + 4), vs = (int64_t)a.num_kv_heads * (D * a.v_bits / 8 + 4);
+  t.bs_log = -1;
+  for (int k = 0; k < 31; ++k)
+    if (a.block_size == (1 << k)) t.bs_log = k;
+  const int rk = a.num_kv_heads * (D * a.k_bits / 8 + 4), rv = a.num_kv_heads * (D * a.v_bits / 8 + 4);
   const int spk = span_bytes(D, a.k_bits), spv = span_bytes(D, a.v_bits);
-  const int64_t slots = a.num_blocks * a.block_size;
-  CUtensorMap km{}, vm{};
-  // TMA: slabs of whole 16 bytes, boxes that start on 128 bytes of the ring (8 rows of an odd
-  // number of 16 bytes), and slot numbers that a 32-bit coordinate holds
-  t.tma = sub >= 8 && ks % 16 == 0 && vs % 16 == 0 && slots > 0 && slots < 0x7fffffffLL &&
-          page_map(&km, a.k_pages, slots, ks, spk, sub) && page_map(&vm, a.v_pages, slots, vs, spv, sub);
+  t.wide = rk % 16 == 0 && rv % 16 == 0;
   constexpr int limit = 227 * 1024 - 448;  // the static arrays take their part
   const int stage = kTok * (spk + spv);
   const int fixed = 1024 + C::kOffTab + key_table_bytes(a.k_bits) + value_table_bytes(a.v_bits);
@@ -1289,7 +1209,7 @@ cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, kern, t, km, vm);
+  err = cudaLaunchKernelEx(&cfg, kern, t);
   if (err == cudaSuccess) count_launches(1);
   return err;
 }
