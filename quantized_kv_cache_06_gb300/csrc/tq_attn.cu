@@ -19,8 +19,14 @@
 // finished there; the pieces of the others are merged by the combine, in tile order, so the
 // result does not depend on timing.
 //
-// The SIMT kernel below is the fp32 form: head dims and dtypes the tensor-core kernel does not
-// take.  A warp owns four columns; lane = token for the scores, lane = coordinate for values.
+// Three launches, the later two as programmatic dependents: the schedule (one CTA; for the
+// tensor-core kernel the other CTAs rotate the queries, one warp a row, which costs the attention
+// CTAs 130 instructions a column less), the attention, the combine (rotates back).
+//
+// The SIMT kernel below is the fp32 form: fp32 outputs, and head dims 16 and 32.  A warp owns four
+// columns; lane = token for the scores, lane = coordinate for the values.  It is bound by the
+// issue of its FMAs and shared-memory reads (64 tokens, 8 drafted, 16 / 2 heads: 41 us, most of it
+// the latency of one CTA's three steps of 32 tokens).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>

@@ -27,16 +27,28 @@
 // most tiles rescale nothing; when one does, the softmax warps scale O^T in TMEM themselves
 // (the product before has completed by then).
 //
-// Roles of the 18 warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, in two
-// sets), 16 copies, 17 and 18 MMA issue.  A window of more than half the MMA columns has both sets on
-// one tile, each with its groups of 16 columns; a smaller one makes two streams of one set that
-// take alternate tiles, each with its own maxima, sums and O^T, merged when the window ends:
-// the chain of waits, TMEM reads and votes of one tile then hides behind the other's.  Packed rows
-// arrive by TMA: the pages seen as a 2-D byte tensor [slots][H row_bytes], a box of up to 128
-// rows x the 16-byte aligned span around the head's bytes, so a block of a page is one copy.
-// Rows whose slab is not a multiple of 16 bytes (H not a multiple of 4) come by 4-byte
-// cp.async.  All waits are bounded: one that runs out records the timeout, every role leaves
-// its loop, copies and MMAs in flight are drained and TMEM is freed.
+// Roles of the warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, in two
+// sets), 16 and 17 MMA issue (scores, values).  A window of more than half the MMA columns has
+// both sets on one tile, each with its groups of 16 columns; a smaller one makes two streams of
+// one set that take alternate tiles, each with its own maxima, sums and O^T, merged when the
+// window ends: the chain of waits, TMEM reads and votes of one tile then hides behind the
+// other's.
+//
+// Packed rows: a dequantising lane copies the rows of its own token with 16-byte cp.async (the
+// aligned span around the head's bytes; by words where a slab is not whole 16 bytes, H not a
+// multiple of 4), up to six tiles deep, so no thread waits for another's copy.  TMA boxes of 16
+// rows x 80 bytes took ten cycles a row, 2700 a tile.
+//
+// What bounds it: not memory (64 x 8192 tokens: single tokens 0.28 ms, 1.0 TB/s; tree of 32 nodes
+// 0.71 ms, 0.39 PFLOP/s).  The tensor pipe is busy an eighth of the time; a tile's chain -- keys
+// expanded, scores, weights, product -- is a sequence of dependent instructions of few warps, and
+// five programs share the instruction cache.  Hence the rolled loops, the paths apart for changed
+// scores and moved maxima, and the short waits: unrolling the two dequantisation loops costs a
+// quarter (tree 0.84 -> 1.03 ms), reading rows word by word from shared memory instead of holding
+// them in registers saved a tenth, one copy of each loop's start another.
+//
+// All waits are bounded: one that runs out records the timeout, every role leaves its loop, the
+// copies and MMAs in flight are waited for and TMEM is freed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -91,19 +103,19 @@ struct Tc {
   static constexpr int kOffQ = 0;
   static constexpr int kOffV = kOffQ + kQBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVBytes;
-  static constexpr int kOffRows = kOffP + kPBytes;                 // RowSees[kCols]
+  static constexpr int kOffRows = kOffP + kPBytes;                 // int4 (p0, p1, w0, w1)[kCols], int2 (base, bits)[kCols]
   // floats [kN]: -max, correction, slope; part [4][kN]
   static constexpr int kOffCol = kOffRows + (kCols * (int)sizeof(RowSees) + 15) / 16 * 16;
   static constexpr int kOffMeta = kOffCol + 7 * kN * 4;            // uint32 valid[kNorms][4], a bit per token
   static constexpr int kOffNorm = kOffMeta + kNorms * 16;  // float2 (nu_k, nu_v) [kNorms][128]
-  static constexpr int kOffTab = (kOffNorm + kNorms * kTok * 8 + 127) / 128 * 128;  // key table, 5-bit value table, ring
+  static constexpr int kOffTab = (kOffNorm + kNorms * kTok * 8 + 127) / 128 * 128;  // key and value tables, ring
   static constexpr int kRegsDequant = D == 256 ? 96 : 64;
   static constexpr int kRegsSoft = (640 * 96 - 128 * (2 * kRegsDequant + kRegsIssue)) / 256 / 8 * 8;
 };
 
 // Bytes of a packed row's span in the ring: the 16-byte aligned span that holds a row wherever
-// it starts (a multiple of 4), rounded to an odd number of 16-byte units, which keeps 16-byte
-// reads of neighbouring rows in different banks.
+// it starts (a multiple of 4), rounded to an odd number of 16-byte units: the words of 32 rows
+// then meet four to a bank, no more.
 __host__ __device__ constexpr int span_bytes(int d, int bits) {
   int s = (d * bits / 8 + 4 + 12 + 15) / 16 * 16;
   return (s / 16) % 2 ? s : s + 16;
@@ -214,11 +226,6 @@ __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sy
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void st_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint4 ld_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
 }
 __device__ __forceinline__ uint32_t ld_s32(uint32_t addr) {
   uint32_t v;
@@ -670,7 +677,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int quad = warp & 3, set = sw >> 2;
     const int stid = tid - 32 * (kKeyWarps + kValWarps);
     const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
-    RowSees* rows = reinterpret_cast<RowSees*>(smem + C::kOffRows);
+    int4* row_spans = reinterpret_cast<int4*>(smem + C::kOffRows);             // p0, p1, w0, w1
+    int2* row_bits = reinterpret_cast<int2*>(smem + C::kOffRows + C::kCols * 16);  // base, bits
     float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -max; -inf where there is no column
     float* corr_s = negm_s + C::kN;
     float* slope_s = corr_s + C::kN;
@@ -704,7 +712,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       soft_sync();
       if (stid < win.nrows) {
         const RowView v = row_view(a, win.row0 + stid);
-        rows[stid] = v;
+        row_spans[stid] = make_int4(v.p0, v.p1, v.w0, v.w1);
+        row_bits[stid] = make_int2(v.base, v.bits);
         atomicMax(&full_lo_s, v.w0);
         atomicMin(&full_hi_s, v.w1);
         atomicMax(&pre_lo_s, v.p0);
@@ -821,8 +830,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (biased) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                x[i].x -= slope_s[c0 + 2 * i] * fabsf((float)(rows[(c0 + 2 * i) >> g_log].base - tok));
-                x[i].y -= slope_s[c0 + 2 * i + 1] * fabsf((float)(rows[(c0 + 2 * i + 1) >> g_log].base - tok));
+                x[i].x -= slope_s[c0 + 2 * i] * fabsf((float)(row_bits[(c0 + 2 * i) >> g_log].x - tok));
+                x[i].y -= slope_s[c0 + 2 * i + 1] * fabsf((float)(row_bits[(c0 + 2 * i + 1) >> g_log].x - tok));
               }
             }
             uint32_t see = 0xffffu;  // bit i: column c0 + i
@@ -830,8 +839,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               see = 0;
               for (int c = c0; c < c0 + 16 && c < cols && real; c += G) {
                 const int r = c >> g_log;
-                if (row_sees(rows[r], a.mask ? a.mask + (int64_t)(win.row0 + r) * a.mask_words : nullptr, tok))
-                  see |= ((1u << G) - 1u) << (c - c0);
+                const int4 v = row_spans[r];
+                bool s = (tok >= v.z && tok < v.w) || (tok >= v.x && tok < v.y);
+                if (a.mask) {
+                  const int2 b = row_bits[r];
+                  const int j = tok - b.x;
+                  if (j >= 0 && j < b.y)
+                    s |= (__ldg(a.mask + (int64_t)(win.row0 + r) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u;
+                }
+                if (s) see |= ((1u << G) - 1u) << (c - c0);
               }
             }
             seen |= see != 0;

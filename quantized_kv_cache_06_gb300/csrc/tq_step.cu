@@ -13,12 +13,14 @@
 // which scans all the sequences (a few KB out of L2), then writes its share of the rows.  A
 // cluster barrier between reading and writing lets every output be its own input (lengths,
 // block counts, ring state).  A row finds its sequence by binary search of the prefix in
-// shared memory.  Bound: latency for a decode step (a launch, one pass over the inputs, a
-// scan, one barrier), store bandwidth of the few SMs for a long prompt.
+// shared memory.  Bound: latency for a decode step (a launch, one pass over the inputs, a scan,
+// one barrier: 64 requests 6 us on the device), for a long prompt the latency of table reads on
+// eight SMs (131072 rows of 1024 requests 23 us, 2.1 MB).
 //
 // Commit.  Accepted node j of a sequence moves from token ctx + path[j] to ctx + j, path
 // strictly ascending, so path[j] >= j: a later source is never an earlier destination, and
-// one thread per 16-byte column that takes the rows in order needs no buffer and no barrier.
+// one thread per 16-byte column that takes the rows in order needs no buffer and no barrier; it
+// keeps eight rows in flight.  Bound: latency (1024 requests, 4096 rows moved, 9 MB: 6 us).
 #include <cooperative_groups.h>
 #include <stdint.h>
 
