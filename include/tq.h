@@ -477,7 +477,8 @@ tq_status tq_paged_decode_recipe(const void* q, tq_dtype q_dtype, int batch, int
  *   status_dev   device int32 or NULL: 0; TQ_ERR_OUT_OF_BLOCKS when the ring holds too few
  *                blocks; TQ_ERR_INVALID_ARG when a length is negative or beyond its blocks, a
  *                sequence would pass max_blocks_per_seq, the rows pass max_rows, or free_state
- *                is inconsistent.  In these cases nothing is planned: the state comes out as it
+ *                is inconsistent (the free and the returned blocks pass num_blocks among
+ *                others).  In these cases nothing is planned: the state comes out as it
  *                was, every row is a padding row.  TQ_ERR_BLOCK_OUT_OF_RANGE when a block id
  *                taken from the table or the ring lies outside [0, num_blocks): that token's
  *                slot is -1.

@@ -51,7 +51,7 @@ def plan_step(seq_lens, new_lens, seq_blocks, block_table, free_blocks, free_sta
         raise PlanError("arg")
     if need_all > count:
         raise PlanError("blocks")
-    if count - need_all + back_all > nb:
+    if count + back_all > nb:
         raise PlanError("arg")
     slots, q_seq, q_len, starts = [], [], [], []
     taken = 0

@@ -20,7 +20,8 @@
 // Commit.  Accepted node j of a sequence moves from token ctx + path[j] to ctx + j, path
 // strictly ascending, so path[j] >= j: a later source is never an earlier destination, and
 // one thread per 16-byte column that takes the rows in order needs no buffer and no barrier; it
-// keeps eight rows in flight.  Bound: latency (1024 requests, 4096 rows moved, 9 MB: 6 us).
+// keeps eight rows in flight.  One CTA takes a sequence's columns: its context length may be
+// overwritten by the same call.  Bound: latency (1024 requests, 4096 rows moved, 9 MB: 6 us).
 #include <cooperative_groups.h>
 #include <stdint.h>
 
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(PlanArgs a) {
   if (bad_any || rows > a.max_rows || head < 0 || count < 0 || count > NB || (NB > 0 ? head >= NB : head != 0))
     code = kInvalidArg;
   else if (fresh > count) code = kOutOfBlocks;
-  else if (count - fresh + back > NB) code = kInvalidArg;
+  else if (count + back > NB) code = kInvalidArg;  // returned entries would meet those being taken
   if (rank == 0 && tid == 0 && a.status) *a.status = code;
   if (code != kOk) rows = fresh = back = 0;
 
@@ -248,14 +249,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(PlanArgs a) {
 
 // ---------------------------------------------------------------- commit
 
-constexpr int kCommitThreads = 128;
+constexpr int kCommitMaxThreads = 1024;
 constexpr int kCommitChunk = 64;  // path entries staged at a time
 constexpr int kCommitBatch = 8;   // rows in flight per thread
 
 template <typename V>
-__global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(CommitArgs a) {
+__global__ void __launch_bounds__(kCommitMaxThreads) commit_tree_kernel(CommitArgs a) {
   __shared__ int64_t src[kCommitChunk], dst[kCommitChunk];  // flat slots; -1: nothing to move
-  const int s = blockIdx.x, tid = threadIdx.x, bs = a.block_size;
+  const int s = blockIdx.x, tid = threadIdx.x, bs = a.block_size, threads = blockDim.x;
   const int64_t cap = (int64_t)a.max_blocks_per_seq * bs;
   const int kcols = a.k_slab / (int)sizeof(V), vcols = a.v_slab / (int)sizeof(V);
   const int64_t ctx = a.ctx_lens[s];
@@ -263,25 +264,15 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(CommitArgs 
   const int32_t* path = a.path + (int64_t)s * a.max_path;
   int bad = ctx < 0 || ctx > cap || n < 0 || n > a.max_path;
   if (bad) n = 0;
-  for (int j = tid; j < n; j += kCommitThreads) {
+  for (int j = tid; j < n; j += threads) {
     const int p = path[j];
     bad |= p < 0 || ctx + p >= cap || (j > 0 && path[j - 1] >= p);
   }
   bad = __syncthreads_or(bad);
   if (bad) n = 0;
-  if (blockIdx.y == 0 && tid == 0) {
+  if (tid == 0) {
     a.seq_lens_out[s] = (int32_t)(ctx + n);
     if (bad && a.status) atomicMax(a.status, (int32_t)kInvalidArg);
-  }
-  const int col = blockIdx.y * kCommitThreads + tid;
-  V* base = nullptr;
-  int64_t stride = 0;
-  if (col < kcols) {
-    base = reinterpret_cast<V*>(a.k_pages) + col;
-    stride = kcols;
-  } else if (col < kcols + vcols) {
-    base = reinterpret_cast<V*>(a.v_pages) + (col - kcols);
-    stride = vcols;
   }
   const int32_t* table = a.block_table + (int64_t)s * a.max_blocks_per_seq;
   for (int j0 = 0; j0 < n; j0 += kCommitChunk) {
@@ -291,30 +282,35 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(CommitArgs 
       const int64_t from = ctx + path[j0 + tid], to = ctx + j0 + tid;
       const int64_t fb = table[from / bs], tb = table[to / bs];
       const bool ok = fb >= 0 && fb < a.num_blocks && tb >= 0 && tb < a.num_blocks;
-      if (!ok && blockIdx.y == 0 && a.status) atomicMax(a.status, (int32_t)kBlockOutOfRange);
+      if (!ok && a.status) atomicMax(a.status, (int32_t)kBlockOutOfRange);
       src[tid] = ok && from != to ? fb * bs + from % bs : -1;
       dst[tid] = tb * bs + to % bs;
     }
     __syncthreads();
-    if (!base) continue;
-    for (int j = 0; j < m; j += kCommitBatch) {
-      V v[kCommitBatch];
+    for (int col = tid; col < kcols + vcols; col += threads) {
+      const bool key = col < kcols;
+      V* base = reinterpret_cast<V*>(key ? a.k_pages : a.v_pages) + (key ? col : col - kcols);
+      const int64_t stride = key ? kcols : vcols;
+      for (int j = 0; j < m; j += kCommitBatch) {
+        V v[kCommitBatch];
 #pragma unroll
-      for (int u = 0; u < kCommitBatch; ++u)
-        if (j + u < m && src[j + u] >= 0) v[u] = base[src[j + u] * stride];
+        for (int u = 0; u < kCommitBatch; ++u)
+          if (j + u < m && src[j + u] >= 0) v[u] = base[src[j + u] * stride];
 #pragma unroll
-      for (int u = 0; u < kCommitBatch; ++u)
-        if (j + u < m && src[j + u] >= 0) base[dst[j + u] * stride] = v[u];
+        for (int u = 0; u < kCommitBatch; ++u)
+          if (j + u < m && src[j + u] >= 0) base[dst[j + u] * stride] = v[u];
+      }
     }
   }
 }
 
 template <typename V>
 cudaError_t launch_commit_as(const CommitArgs& a, cudaStream_t stream) {
+  // a thread per column, at least as many as path entries are staged at a time
   const int cols = (a.k_slab + a.v_slab) / (int)sizeof(V);
-  const int gy = std::max(1, (cols + kCommitThreads - 1) / kCommitThreads);
-  if (gy > 65535) return cudaErrorInvalidValue;
-  commit_tree_kernel<V><<<dim3(a.num_seqs, gy), kCommitThreads, 0, stream>>>(a);
+  const int threads = std::min(kCommitMaxThreads, std::max(128, (cols + 31) / 32 * 32));
+  static_assert(kCommitChunk <= 128, "entries are staged one a thread");
+  commit_tree_kernel<V><<<a.num_seqs, threads, 0, stream>>>(a);
   const cudaError_t err = cudaGetLastError();
   if (err == cudaSuccess) count_launches(1);
   return err;

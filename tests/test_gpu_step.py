@@ -132,6 +132,20 @@ def test_plan_refusals_change_nothing(change, code):
              16, st["rows"], check=True)
 
 
+def test_plan_refuses_a_ring_that_meets_its_returned_blocks():
+    # six blocks, all said to be free, one of them in use and returned
+    tq = _tq()
+    table, ring = np.array([[0, 1, -1], [2, -1, -1]]), np.arange(6)
+    args = np.array([30, 3]), np.array([3, -1]), np.array([2, 1])
+    p, t, r, code = _run(tq, *args, table, ring, np.array([0, 6]), 16, 3)
+    assert code == tq.TQ_ERR_INVALID_ARG and p.free_state.tolist() == [0, 6]
+    assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(r.cpu().numpy(), ring)
+    # the same with one less: the ring is full afterwards but for the block taken
+    p, t, r, code = _run(tq, *args, table, ring, np.array([0, 5]), 16, 3)
+    assert code == tq.TQ_OK and p.free_state.tolist() == [1, 5]
+    assert t.tolist()[0] == [0, 1, 0] and r.tolist() == [0, 1, 2, 3, 4, 2]
+
+
 def test_plan_reports_bad_block_ids():
     tq = _tq()
     # the partly filled block of sequence 0 and a ring entry lie outside the pages
@@ -186,6 +200,21 @@ def test_commit_one_component_in_place_lengths_and_whole_path():
     assert tq.tq_commit_tree(None, k, _dev(table), lens, _dev(path), _dev(count), seq_lens=lens) is lens
     want, want_lens = so.commit_tree(pages[0], table, ctx, path, count)
     assert np.array_equal(k.cpu().numpy(), want) and np.array_equal(lens.cpu().numpy(), want_lens)
+
+
+@pytest.mark.parametrize("h,rbs", [(16, (132, 132)), (5, (133, 259)), (64, (164, 164))])
+def test_commit_of_wide_tokens_with_lengths_in_place(h, rbs):
+    # more 16-byte (or 1-byte) columns than a CTA has threads
+    tq = _tq()
+    rng = np.random.default_rng(h)
+    ctx, table, path, count, pages = _commit_case(rng, 40, 4, h, rbs, 9, 6, 20)
+    dev = [torch.from_numpy(p).cuda() for p in pages]
+    lens = _dev(ctx)
+    assert tq.tq_commit_tree(dev[0], dev[1], _dev(table), lens, _dev(path), _dev(count), seq_lens=lens) is lens
+    for got, p in zip(dev, pages):
+        want, want_lens = so.commit_tree(p, table, ctx, path, count)
+        assert np.array_equal(got.cpu().numpy(), want)
+    assert np.array_equal(lens.cpu().numpy(), want_lens)
 
 
 def test_commit_bad_paths_move_nothing():
