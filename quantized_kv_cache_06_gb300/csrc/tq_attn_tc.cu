@@ -16,12 +16,14 @@
 // shared memory in 16-byte chunks, swizzled.  The norms are per token, so per lane: nu_k
 // multiplies the score, nu_v the weight.
 //
-// Precision.  fp16 outputs (SPLIT): Q = hi + lo 2^-12 and P' = hi + lo 2^-11 in fp16, the lo
-// parts as further columns of the same MMAs, so what is left is the rounding of the centroids
-// (alpha puts them near fp16 grid points).  bf16 outputs: one fp16 part each, eight times
-// finer than the output's own rounding.  The window's queries are scaled by one power of two,
-// and the weights p nu_v by another (moved when a larger norm arrives), so neither large
-// queries nor large norms leave the fp16 range.  Sums, maxima and both products are fp32.
+// Precision.  fp16 outputs (SPLIT): Q = hi + lo in fp16, the lo parts as further k-steps into the
+// same accumulators, so that scores are off by the rounding of the centroids alone (alpha puts
+// them near fp16 grid points) however large they are.  bf16 outputs: one fp16 part, eight times
+// finer than the output's own rounding.  A weight p nu_v is one fp16 value, half a step of the
+// output's type at most from its own (as a second pair of parts, 4e-5 of an output nearer, it took
+// half of the columns).  The window's queries are scaled by one power of two, and the weights by
+// another (moved when a larger norm arrives), so neither large queries nor large norms leave the
+// fp16 range.  Sums, maxima and both products are fp32.
 //
 // Softmax in base 2; the running max of a column moves only when a score passes it by 2^6, so
 // most tiles rescale nothing; when one does, the softmax warps scale O^T in TMEM themselves
@@ -77,17 +79,14 @@ constexpr int kMaxRing = 6;
 constexpr int kNorms = 6;  // tiles whose norms are kept: keys and values run at most five tiles ahead of the softmax
 constexpr float kSlack = 6.0f;            // log2 units the running max may lag
 constexpr float kMaxWeight = 64.0f;       // 2^kSlack
-constexpr float kLoQ = 4096.0f;           // scale of the fp16 remainders of Q
-constexpr float kLoP = 2048.0f;           // and of P'
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
 constexpr int kNoToken = -0x7fffffff - 1;  // a table entry that no token asks for
 constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
 
 template <int D, bool SPLIT>
 struct Tc {
-  static constexpr int kN = D == 256 ? 64 : 128;         // MMA columns at most
-  static constexpr int kCols = SPLIT ? kN / 2 : kN;      // window columns at most
-  static constexpr int kGroups = (kCols + 31) / 32;      // groups of 16 columns per softmax thread
+  static constexpr int kN = D < 256 ? 128 : SPLIT ? 32 : 64;  // MMA columns, window columns at most
+  static constexpr int kGroups = (kN + 31) / 32;      // groups of 16 columns per softmax thread
   static constexpr int kHalves = D == 256 ? 2 : 1;       // 128-dim halves of O^T
   static constexpr int kKCols = D / 2;                   // TMEM columns of a key tile
   static constexpr int kVSlots = D == 256 ? 2 : D == 128 ? 3 : 4;  // slots of 64 tokens' values
@@ -97,15 +96,16 @@ struct Tc {
   static constexpr int kK = kO + kHalves * kN;
   static_assert(kK + 2 * kKCols <= 512, "TMEM columns");
   // shared memory (offsets from a 1024-byte aligned base)
-  static constexpr int kQBytes = kN * D * 2;
+  static constexpr int kQPart = kN * D * 2;  // a part of the queries
+  static constexpr int kQBytes = (SPLIT ? 2 : 1) * kQPart;
   static constexpr int kVBytes = kTok / 2 * D * 2;
   static constexpr int kPBytes = kTok * kN * 2 < 16384 ? 16384 : kTok * kN * 2;
   static constexpr int kOffQ = 0;
   static constexpr int kOffV = kOffQ + kQBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVBytes;
-  static constexpr int kOffRows = kOffP + kPBytes;                 // int4 (p0, p1, w0, w1)[kCols], int2 (base, bits)[kCols]
+  static constexpr int kOffRows = kOffP + kPBytes;                 // int4 (p0, p1, w0, w1)[kN], int2 (base, bits)[kN]
   // floats [kN]: -max, correction, slope; part [4][kN]
-  static constexpr int kOffCol = kOffRows + (kCols * (int)sizeof(RowSees) + 15) / 16 * 16;
+  static constexpr int kOffCol = kOffRows + (kN * (int)sizeof(RowSees) + 15) / 16 * 16;
   static constexpr int kOffMeta = kOffCol + 7 * kN * 4;            // uint32 valid[kNorms][4], a bit per token
   static constexpr int kOffNorm = kOffMeta + kNorms * 16;  // float2 (nu_k, nu_v) [kNorms][128]
   static constexpr int kOffTab = (kOffNorm + kNorms * kTok * 8 + 127) / 128 * 128;  // key and value tables, ring
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   auto pad_cols = [&](const AttnWindow& win) -> int { return (win.nrows * G + 15) / 16 * 16; };
   // Two streams of tiles when the window's MMA columns fit half of the TMEM regions.
-  auto streams_of = [&](int padded) -> int { return (SPLIT ? 2 * padded : padded) <= C::kN / 2 ? 2 : 1; };
+  auto streams_of = [&](int padded) -> int { return padded <= C::kN / 2 ? 2 : 1; };
 
   // Packed rows: a lane copies the rows of its token itself, `ring` tiles deep, so no other thread
   // waits for them.  A cursor walks the part's tiles ahead of their use.
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int stid = tid - 32 * (kKeyWarps + kValWarps);
     const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
     int4* row_spans = reinterpret_cast<int4*>(smem + C::kOffRows);             // p0, p1, w0, w1
-    int2* row_bits = reinterpret_cast<int2*>(smem + C::kOffRows + C::kCols * 16);  // base, bits
+    int2* row_bits = reinterpret_cast<int2*>(smem + C::kOffRows + C::kN * 16);  // base, bits
     float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -max; -inf where there is no column
     float* corr_s = negm_s + C::kN;
     float* slope_s = corr_s + C::kN;
@@ -696,7 +696,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     for_windows([&](const AttnWindow& win, int first, int last) -> bool {
       const int cols = win.nrows * G, padded = pad_cols(win);
-      const int lo_col = SPLIT ? padded : 0;
       const int streams = streams_of(padded), pitch = C::kN / streams;
       const int sets = kSoftSets / streams, stream = set / sets;
       const int c_first = 16 * (set % sets), c_step = 16 * sets;  // this thread's groups of columns
@@ -742,7 +741,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           load_floats<D / 32>(w.q_rot + q_index(min(col4 + e * kSoftWarps, cols - 1)) * D + lane * (D / 32), v[e]);
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
-          const int col = col4 + e * kSoftWarps, lc = col + lo_col;
+          const int col = col4 + e * kSoftWarps;
           if (col >= cols) continue;
 #pragma unroll
           for (int i = 0; i < D / 32; i += 2) {
@@ -751,11 +750,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint32_t hi = pack2(x0, x1);
             const uint32_t at = (uint32_t)((d >> 6) * (C::kN * 128) + (((d & 63) * 2) & 15));
             const uint32_t ch = (uint32_t)((d & 63) >> 3);
-            *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + col * 128 + ((ch ^ (col & 7)) << 4)) = hi;
+            unsigned char* to = smem + C::kOffQ + at + col * 128 + ((ch ^ (col & 7)) << 4);
+            *reinterpret_cast<uint32_t*>(to) = hi;
             if constexpr (SPLIT) {
               const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
-              *reinterpret_cast<uint32_t*>(smem + C::kOffQ + at + lc * 128 + ((ch ^ (lc & 7)) << 4)) =
-                  pack2((x0 - __low2float(hh)) * kLoQ, (x1 - __high2float(hh)) * kLoQ);
+              *reinterpret_cast<uint32_t*>(to + C::kQPart) = pack2(x0 - __low2float(hh), x1 - __high2float(hh));
             }
           }
         }
@@ -789,24 +788,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool real = (((quad == 0 ? vv.x : quad == 1 ? vv.y : quad == 2 ? vv.z : vv.w) >> lane) & 1u) && tok < hi_tok;
         const bool all = (vv.x & vv.y & vv.z & vv.w) == 0xffffffffu && ((t0 >= full_lo && t0 + kTok <= full_hi) ||
                                                                          (t0 >= pre_lo && t0 + kTok <= pre_hi));
-        // Scores of columns c0 .. c0 + 15 from their accumulators (the two parts added).
+        // Scores of columns c0 .. c0 + 15.
         auto fetch = [&](int c0, float2 (&x)[8]) {
           uint32_t u[16];
           tm_ld16(s_at + c0, u);
-          if constexpr (SPLIT) {
-            uint32_t v[16];
-            tm_ld16(s_at + lo_col + c0, v);
-            tm_wait_ld();
+          tm_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              x[i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                make_float2(1.0f / kLoQ, 1.0f / kLoQ),
-                                make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
-          } else {
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-          }
+          for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
         };
         bool seen = true;  // a column of this thread sees its token
         if (__builtin_expect(!all || capped || biased, 0)) {
@@ -856,11 +844,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int i = 0; i < 16; ++i)
               u[i] = (see >> i) & 1u ? __float_as_uint(i & 1 ? x[i >> 1].y : x[i >> 1].x) : 0xff800000u;
             tm_st16(s_at + c0, u);
-            if constexpr (SPLIT) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = 0u;
-              tm_st16(s_at + lo_col + c0, u);
-            }
           }
           tm_wait_st();
           kn = 1.f;
@@ -886,7 +869,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (c0 >= cols) continue;
             float2 x[8];
             fetch(c0, x);
-            uint32_t o[8], r[8];
+            uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float4 m4 = *reinterpret_cast<const float4*>(negm_s + col0 + c0 + 4 * i);
@@ -899,10 +882,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 l[8 * g + 2 * i + e] = __fadd2_rn(l[8 * g + 2 * i + e], y);
                 y = __fmul2_rn(y, vs2);
                 o[2 * i + e] = pack2(y.x, y.y);
-                if constexpr (SPLIT) {
-                  const __half2 hh = *reinterpret_cast<const __half2*>(&o[2 * i + e]);
-                  r[2 * i + e] = pack2((y.x - __low2float(hh)) * kLoP, (y.y - __high2float(hh)) * kLoP);
-                }
               }
             }
             if (g == 0 && !again) {  // the stream's product before is done: P and O are free
@@ -911,10 +890,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             st_v4(p_addr(col0 + c0), o[0], o[1], o[2], o[3]);
             st_v4(p_addr(col0 + c0 + 8), o[4], o[5], o[6], o[7]);
-            if constexpr (SPLIT) {
-              st_v4(p_addr(col0 + lo_col + c0), r[0], r[1], r[2], r[3]);
-              st_v4(p_addr(col0 + lo_col + c0 + 8), r[4], r[5], r[6], r[7]);
-            }
           }
           if (again) break;
           const bool grow = vf > 0.f && exp_of(vf) - ve > 9;
@@ -985,9 +960,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (int c0 = c_first; c0 < cols; c0 += c_step) {
 #pragma unroll 1
-              for (int i2 = 0; i2 < (SPLIT ? 2 : 1) * C::kHalves; ++i2) {
-                const uint32_t at = lanes + C::kO + (SPLIT ? i2 >> 1 : i2) * C::kN + col0 +
-                                    (SPLIT && (i2 & 1) ? lo_col : 0) + c0;
+              for (int hf = 0; hf < C::kHalves; ++hf) {
+                const uint32_t at = lanes + C::kO + hf * C::kN + col0 + c0;
                 uint32_t u[16];
                 tm_ld16(at, u);
                 tm_wait_ld();
@@ -1082,16 +1056,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int s = 0; s < live; ++s) {
           uint32_t u[16];
           tm_ld16(lanes + C::kO + hf * C::kN + s * pitch + c0, u);
-          if constexpr (SPLIT) {
-            uint32_t v[16];
-            tm_ld16(lanes + C::kO + hf * C::kN + s * pitch + lo_col + c0, v);
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              u[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), 1.0f / kLoP, __uint_as_float(u[i])));
-          } else {
-            tm_wait_ld();
-          }
+          tm_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(u[i]), corr_s[s * pitch + c0 + i], x[i]);
         }
@@ -1124,10 +1089,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int it = 0, unit = 0;
     uint32_t sph = 0;  // phases of the score buffers
     for_windows([&](const AttnWindow& win, int first, int last) -> bool {
-      const int padded = __shfl_sync(kFullMask, pad_cols(win), 0), n = SPLIT ? 2 * padded : padded;
+      const int padded = __shfl_sync(kFullMask, pad_cols(win), 0);
       const int tiles = __shfl_sync(kFullMask, last - first, 0);
       const int streams = streams_of(padded), pitch = C::kN / streams;
-      const uint32_t ids = mma_idesc(n, false);
+      const uint32_t ids = mma_idesc(padded, false);
       if (!wait(q_full, unit & 1)) return false;
       ++unit;
       for (int k = 0; k < tiles; ++k, ++it) {
@@ -1135,10 +1100,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!wait(k_full(b), (it >> 1) & 1) || !wait(n_full(it % kNorms), (it / kNorms) & 1) || !wait(s_empty(sb), ((sph >> sb) & 1) ^ 1)) return false;
         sph ^= 1u << sb;
         tc_after();
+#pragma unroll 1
+        for (int lo = 0; lo < (SPLIT ? 2 : 1); ++lo)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ts(tmem + C::kS + sb * pitch, tmem + C::kK + b * C::kKCols + ks * 8,
-                 q_at + (((ks >> 2) * (C::kN * 128) + (ks & 3) * 32) >> 4), ids, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ts(tmem + C::kS + sb * pitch, tmem + C::kK + b * C::kKCols + ks * 8,
+                   q_at + ((lo * C::kQPart + (ks >> 2) * (C::kN * 128) + (ks & 3) * 32) >> 4), ids, lo > 0 || ks > 0);
         tc_commit(s_full(sb));
         tc_commit(k_empty(b));
       }
@@ -1151,10 +1118,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int vslot = 0, vph = 0;
     uint32_t pph = 0;  // phases of the streams' weights
     for_windows([&](const AttnWindow& win, int first, int last) -> bool {
-      const int padded = __shfl_sync(kFullMask, pad_cols(win), 0), n = SPLIT ? 2 * padded : padded;
+      const int padded = __shfl_sync(kFullMask, pad_cols(win), 0);
       const int tiles = __shfl_sync(kFullMask, last - first, 0);
       const int streams = streams_of(padded), pitch = C::kN / streams;
-      const uint32_t idp = mma_idesc(n, true);
+      const uint32_t idp = mma_idesc(padded, true);
       for (int k = 0; k < tiles; ++k) {  // O^T of its stream += V^T P^T
         const int s = k & (streams - 1);
         const uint32_t p_s = p_at + (uint32_t)((((s * pitch) >> 6) * (kTok * 128) + ((s * pitch) & 63) * 2) >> 4);
@@ -1237,10 +1204,8 @@ bool attn_tc_supported(const AttnArgs& a) {
 }
 
 int attn_tc_cols(const AttnArgs& a) {
-  const bool split = a.out_dtype == kF16;
-  if (a.head_dim == 64) return split ? Tc<64, true>::kCols : Tc<64, false>::kCols;
-  if (a.head_dim == 128) return split ? Tc<128, true>::kCols : Tc<128, false>::kCols;
-  return split ? Tc<256, true>::kCols : Tc<256, false>::kCols;
+  if (a.head_dim < 256) return Tc<128, false>::kN;
+  return a.out_dtype == kF16 ? Tc<256, true>::kN : Tc<256, false>::kN;
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
