@@ -83,9 +83,9 @@ constexpr int kBarSoft = 1;               // named barrier of all softmax warps;
 constexpr int kNoToken = -0x7fffffff - 1;  // a table entry that no token asks for
 constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, int N>
 struct Tc {
-  static constexpr int kN = D < 256 ? 128 : SPLIT ? 32 : 64;  // MMA columns, window columns at most
+  static constexpr int kN = N;                           // MMA columns, window columns at most
   static constexpr int kGroups = (kN + 31) / 32;      // groups of 16 columns per softmax thread
   static constexpr int kHalves = D == 256 ? 2 : 1;       // 128-dim halves of O^T
   static constexpr int kKCols = D / 2;                   // TMEM columns of a key tile
@@ -344,10 +344,10 @@ __device__ __forceinline__ void expand8(uint32_t w, const ByteTable<ODD>& t, uin
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcAttnArgs p) {
-  using C = Tc<D, SPLIT>;
+  using C = Tc<D, SPLIT, N>;
   const AttnArgs& a = p.a;
   const AttnWork& w = p.w;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -1159,9 +1159,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---------------------------------------------------------------- launch
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, int N>
 cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
-  using C = Tc<D, SPLIT>;
+  using C = Tc<D, SPLIT, N>;
   TcAttnArgs t{};
   t.a = a;
   t.w = w;
@@ -1179,7 +1179,7 @@ cudaError_t launch_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream)
   // (one stage is left for 4-bit keys and 5-bit values of 256 channels, two or more otherwise)
   if (t.ring < 1) return cudaErrorInvalidValue;
   const int smem = fixed + t.ring * stage;
-  auto kern = attn_tc_kernel<D, SPLIT>;
+  auto kern = attn_tc_kernel<D, SPLIT, N>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
@@ -1203,16 +1203,25 @@ bool attn_tc_supported(const AttnArgs& a) {
   return (a.head_dim == 64 || a.head_dim == 128 || a.head_dim == 256) && (a.out_dtype == kF16 || a.out_dtype == kBF16);
 }
 
+// Columns of a window: as many as shared memory and TMEM allow, or a quarter where the sequences'
+// rows fill no more on average (single tokens, short trees).
 int attn_tc_cols(const AttnArgs& a) {
-  if (a.head_dim < 256) return Tc<128, false>::kN;
-  return a.out_dtype == kF16 ? Tc<256, true>::kN : Tc<256, false>::kN;
+  const int most = a.head_dim < 256 ? 128 : a.out_dtype == kF16 ? 32 : 64, few = 32;
+  const int64_t cols = (int64_t)a.num_rows * (a.num_q_heads / a.num_kv_heads);
+  return a.num_seqs > 0 && cols <= (int64_t)few * a.num_seqs ? few : most;
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
-  const bool split = a.out_dtype == kF16;
-  if (a.head_dim == 64) return split ? launch_tc<64, true>(a, w, stream) : launch_tc<64, false>(a, w, stream);
-  if (a.head_dim == 128) return split ? launch_tc<128, true>(a, w, stream) : launch_tc<128, false>(a, w, stream);
-  return split ? launch_tc<256, true>(a, w, stream) : launch_tc<256, false>(a, w, stream);
+  const bool split = a.out_dtype == kF16, few = w.cols == 32;
+  auto of = [&](auto dim, auto most) -> cudaError_t {
+    constexpr int D = decltype(dim)::value, N = decltype(most)::value;
+    if (split) return few ? launch_tc<D, true, 32>(a, w, stream) : launch_tc<D, true, D == 256 ? 32 : N>(a, w, stream);
+    return few ? launch_tc<D, false, 32>(a, w, stream) : launch_tc<D, false, N>(a, w, stream);
+  };
+  using std::integral_constant;
+  if (a.head_dim == 64) return of(integral_constant<int, 64>{}, integral_constant<int, 128>{});
+  if (a.head_dim == 128) return of(integral_constant<int, 128>{}, integral_constant<int, 128>{});
+  return of(integral_constant<int, 256>{}, integral_constant<int, 64>{});
 }
 
 }  // namespace tq
