@@ -257,12 +257,6 @@ __device__ __forceinline__ bool named_any(int id, int n, bool x) {
       : "memory");
   return r != 0;
 }
-// Order-preserving map of floats to ints and back (for integer maxima over a warp).
-__device__ __forceinline__ int ord_int(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float ord_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 // Exponent of a power of two near x > 0 (finite): floor(log2 x), -126 for zero and subnormals.
 __device__ __forceinline__ int exp_of(float x) { return max((int)((__float_as_uint(x) >> 23) & 0xffu) - 127, -126); }
 
@@ -691,6 +685,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const bool capped = a.softcap > 0.f, biased = a.alibi != nullptr;
     const float cap2 = a.softcap * kLog2eA;
     const float inv_av = 1.0f / (a.v_alpha * sqrtf((float)D));
+    // 16 values of every lane to lane i's v[0], over all lanes, of value i % 16: halves of the values
+    // exchanged four times, 16 shuffles in all.
+    auto over_lanes = [&](float (&v)[16], auto op) {
+#pragma unroll
+      for (int m = 8; m >= 1; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+          const float keep = lane & m ? v[i + m] : v[i], give = lane & m ? v[i] : v[i + m];
+          v[i] = op(keep, __shfl_xor_sync(kFullMask, give, m));
+        }
+      v[0] = op(v[0], __shfl_xor_sync(kFullMask, v[0], 16));
+    };
     int it = 0;
     uint32_t sph = 0, pph = 0;
 
@@ -825,17 +831,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t see = 0xffffu;  // bit i: column c0 + i
             if (!all) {
               see = 0;
-              for (int c = c0; c < c0 + 16 && c < cols && real; c += G) {
-                const int r = c >> g_log;
-                const int4 v = row_spans[r];
-                bool s = (tok >= v.z && tok < v.w) || (tok >= v.x && tok < v.y);
-                if (a.mask) {
-                  const int2 b = row_bits[r];
-                  const int j = tok - b.x;
-                  if (j >= 0 && j < b.y)
-                    s |= (__ldg(a.mask + (int64_t)(win.row0 + r) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u;
+              // (four rows together, so that their loads are)
+              const int r_end = min((c0 + 16) >> g_log, win.nrows);
+#pragma unroll 1
+              for (int r0 = c0 >> g_log; r0 < r_end; r0 += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int r = min(r0 + e, r_end - 1);
+                  const int4 v = row_spans[r];
+                  bool s = (tok >= v.z && tok < v.w) || (tok >= v.x && tok < v.y);
+                  if (a.mask) {
+                    const int2 b = row_bits[r];
+                    const int j = tok - b.x;
+                    const bool node = j >= 0 && j < b.y;
+                    const uint32_t word =
+                        __ldg(a.mask + (int64_t)(win.row0 + r) * a.mask_words + (node ? j >> 5 : 0));
+                    s |= node && ((word >> (j & 31)) & 1u);
+                  }
+                  if (s && real) see |= ((1u << G) - 1u) << ((r << g_log) - c0);
                 }
-                if (s) see |= ((1u << G) - 1u) << (c - c0);
               }
             }
             seen |= see != 0;
@@ -857,70 +871,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto p_addr = [&](int c) -> uint32_t { return p_line + (c >> 6) * (kTok * 128) + ((((c & 63) >> 3) ^ sx) << 4); };
         volatile int* fl = &fail[stream][(k / streams) & 1];
 
-        // Weights with the running maxima as they are; when a column's has to move (or the values'
-        // scale), the tile is taken once more with the new ones.
-        for (bool again = false;; again = true) {
-          const float vs = vf > 0.f ? vn * pow2i(max(-126, min(126, -ve))) : 0.f;
-          const float2 vs2 = make_float2(vs, vs);
-          float over = 0.f;  // largest weight
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const int c0 = c_first + c_step * g;
-            if (c0 >= cols) continue;
+        // The columns' maxima over the tile, and the scale of the weights by its largest norm; where
+        // `sums`, the tile's weights taken back out of the sums (a weight that moves a maximum
+        // leaves a rounding of itself, scaled away with it; an infinite one leaves nothing of the sum
+        // either), which go to the new maxima with O^T.  Little code, as it runs seldom and then
+        // comes from far: with a reduction per column and both passes unrolled it took 20 us a window.
+        auto move_maxima = [&](bool sums) {
+#pragma unroll 1
+          for (int c0 = c_first; c0 < cols; c0 += c_step) {
             float2 x[8];
-            fetch(c0, x);
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 m4 = *reinterpret_cast<const float4*>(negm_s + col0 + c0 + 4 * i);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float2 y = __ffma2_rn(x[2 * i + e], kn2, e ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
-                y.x = ex2a(y.x);
-                y.y = ex2a(y.y);
-                over = fmaxf(over, fmaxf(y.x, y.y));
-                l[8 * g + 2 * i + e] = __fadd2_rn(l[8 * g + 2 * i + e], y);
-                y = __fmul2_rn(y, vs2);
-                o[2 * i + e] = pack2(y.x, y.y);
-              }
-            }
-            if (g == 0 && !again) {  // the stream's product before is done: P and O are free
-              if (!__all_sync(kFullMask, p_free)) ok = wait(p_empty(stream), this_p ^ 1) && ok;
-              if (!ok) *fl = 1;
-            }
-            st_v4(p_addr(col0 + c0), o[0], o[1], o[2], o[3]);
-            st_v4(p_addr(col0 + c0 + 8), o[4], o[5], o[6], o[7]);
-          }
-          if (again) break;
-          const bool grow = vf > 0.f && exp_of(vf) - ve > 9;
-          if (__builtin_expect(!named_any(bar_id, bar_n, over > kMaxWeight || grow || !ok), 1)) break;
-          if (*fl) {  // the same for all warps of the stream
-            broken = true;
-            break;
-          }
-          // Take the tile's weights back out of the sums (a weight that moves a maximum leaves a
-          // rounding of itself, scaled away with it; an infinite one would leave nothing of the
-          // sum either), and find the columns' maxima over the four lane quadrants.
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const int c0 = c_first + c_step * g;
-            if (c0 >= cols) continue;
-            float2 x[8];
+            float v[16];
             fetch(c0, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 m2 = *reinterpret_cast<const float2*>(negm_s + col0 + c0 + 2 * i);
-              const float2 y = __ffma2_rn(x[i], kn2, m2);
-              float2& li = l[8 * g + i];
-              li.x = li.x == INFINITY ? 0.f : li.x - ex2a(y.x);
-              li.y = li.y == INFINITY ? 0.f : li.y - ex2a(y.y);
-              const int ta = __reduce_max_sync(kFullMask, ord_int(x[i].x * kn));
-              const int tb = __reduce_max_sync(kFullMask, ord_int(x[i].y * kn));
-              if (lane == 0) {
-                part_s[quad * C::kN + col0 + c0 + 2 * i] = ord_float(ta);
-                part_s[quad * C::kN + col0 + c0 + 2 * i + 1] = ord_float(tb);
-              }
-            }
+            for (int i = 0; i < 8; ++i) v[2 * i] = x[i].x * kn, v[2 * i + 1] = x[i].y * kn;
+            over_lanes(v, [](float m, float n) { return fmaxf(m, n); });
+            if (lane < 16) part_s[quad * C::kN + col0 + c0 + lane] = v[0];
           }
           const int vmax = __reduce_max_sync(kFullMask, __float_as_int(vf));
           if (lane == 0) vpart[sw] = vmax;
@@ -947,32 +912,86 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (up) negm_s[col0 + c] = -top;
           }
           named_sync(bar_id, bar_n);
+          if (!sums) return;
 #pragma unroll
           for (int g = 0; g < C::kGroups; ++g) {
             const int c0 = c_first + c_step * g;
             if (c0 >= cols) continue;
+            float2 x[8];
+            fetch(c0, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              l[8 * g + i] = __fmul2_rn(l[8 * g + i], *reinterpret_cast<const float2*>(corr_s + col0 + c0 + 2 * i));
+            for (int i = 0; i < 8; ++i) {
+              const float2 m2 = *reinterpret_cast<const float2*>(negm_s + col0 + c0 + 2 * i);
+              const float2 f2 = *reinterpret_cast<const float2*>(corr_s + col0 + c0 + 2 * i);
+              const float2 y = __ffma2_rn(x[i], kn2, m2);
+              float2& li = l[8 * g + i];
+              li.x = li.x == INFINITY ? 0.f : fmaf(li.x, f2.x, -ex2a(y.x));
+              li.y = li.y == INFINITY ? 0.f : fmaf(li.y, f2.y, -ex2a(y.y));
+            }
           }
-          if (k >= streams) {
-            tc_after();
+          tc_after();
 #pragma unroll 1
-            for (int c0 = c_first; c0 < cols; c0 += c_step) {
+          for (int c0 = c_first; c0 < cols; c0 += c_step) {
 #pragma unroll 1
-              for (int hf = 0; hf < C::kHalves; ++hf) {
-                const uint32_t at = lanes + C::kO + hf * C::kN + col0 + c0;
-                uint32_t u[16];
-                tm_ld16(at, u);
-                tm_wait_ld();
+            for (int hf = 0; hf < C::kHalves; ++hf) {
+              const uint32_t at = lanes + C::kO + hf * C::kN + col0 + c0;
+              uint32_t u[16];
+              tm_ld16(at, u);
+              tm_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  u[i] = __float_as_uint(__uint_as_float(u[i]) * (corr_s[col0 + c0 + i] * vscale));
-                tm_st16(at, u);
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * (corr_s[col0 + c0 + i] * vscale));
+              tm_st16(at, u);
+            }
+          }
+          tm_wait_st();
+        };
+
+        // Weights with the running maxima as they are; when a column's has to move (or the values'
+        // scale), the tile is taken once more with the new ones.  A first tile has none yet.
+        bool moved = k < streams, waited = false;
+        for (;;) {
+          if (__builtin_expect(moved, 0)) move_maxima(k >= streams);
+          const float vs = vf > 0.f ? vn * pow2i(max(-126, min(126, -ve))) : 0.f;
+          const float2 vs2 = make_float2(vs, vs);
+          float over = 0.f;  // largest weight
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int c0 = c_first + c_step * g;
+            if (c0 >= cols) continue;
+            float2 x[8];
+            fetch(c0, x);
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 m4 = *reinterpret_cast<const float4*>(negm_s + col0 + c0 + 4 * i);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float2 y = __ffma2_rn(x[2 * i + e], kn2, e ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
+                y.x = ex2a(y.x);
+                y.y = ex2a(y.y);
+                over = fmaxf(over, fmaxf(y.x, y.y));
+                l[8 * g + 2 * i + e] = __fadd2_rn(l[8 * g + 2 * i + e], y);
+                y = __fmul2_rn(y, vs2);
+                o[2 * i + e] = pack2(y.x, y.y);
               }
             }
-            tm_wait_st();
+            if (g == 0 && !waited) {  // the stream's product before is done: P and O are free
+              if (!__all_sync(kFullMask, p_free)) ok = wait(p_empty(stream), this_p ^ 1) && ok;
+              if (!ok) *fl = 1;
+            }
+            st_v4(p_addr(col0 + c0), o[0], o[1], o[2], o[3]);
+            st_v4(p_addr(col0 + c0 + 8), o[4], o[5], o[6], o[7]);
           }
+          const bool first_pass = !waited;
+          waited = true;
+          if (!first_pass) break;
+          const bool move = !moved && (over > kMaxWeight || (vf > 0.f && exp_of(vf) - ve > 9));
+          if (__builtin_expect(!named_any(bar_id, bar_n, move || !ok), 1)) break;
+          if (*fl) {  // the same for all warps of the stream
+            broken = true;
+            break;
+          }
+          moved = true;
         }
         if (broken) continue;
         if (__builtin_expect(__any_sync(kFullMask, real && seen && !vfin), 0)) {
@@ -1011,18 +1030,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int g = 0; g < C::kGroups; ++g) {
         const int c0 = c_first + c_step * g;
         if (c0 >= cols) continue;
-        // 16 columns over 32 lanes: halves of the columns exchanged four times, 16 shuffles in all
         float v[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[2 * i] = l[8 * g + i].x, v[2 * i + 1] = l[8 * g + i].y;
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1)
-#pragma unroll
-          for (int i = 0; i < m; ++i) {
-            const float keep = lane & m ? v[i + m] : v[i], give = lane & m ? v[i] : v[i + m];
-            v[i] = keep + __shfl_xor_sync(kFullMask, give, m);
-          }
-        v[0] += __shfl_xor_sync(kFullMask, v[0], 16);
+        over_lanes(v, [](float m, float n) { return m + n; });
         if (lane < 16) part_s[quad * C::kN + col0 + c0 + lane] = v[0];
       }
       if (lane == 0 && (sw % (4 * sets)) == 0) ve_s[stream] = ve == -1000 ? 0 : ve;
