@@ -20,8 +20,9 @@
 // same accumulators, so that scores are off by the rounding of the centroids alone (alpha puts
 // them near fp16 grid points) however large they are.  bf16 outputs: one fp16 part, eight times
 // finer than the output's own rounding.  A weight p nu_v is one fp16 value, half a step of the
-// output's type at most from its own (as a second pair of parts, 4e-5 of an output nearer, it took
-// half of the columns).  The window's queries are scaled by one power of two, and the weights by
+// output's type at most from its own (in two parts an output comes nearer by a
+// fifth of its own rounding, and a window holds half of the columns: tree 4 x 131072 1.28 against
+// 0.72 ms).  The window's queries are scaled by one power of two, and the weights by
 // another (moved when a larger norm arrives), so neither large queries nor large norms leave the
 // fp16 range.  Sums, maxima and both products are fp32.
 //
@@ -41,13 +42,15 @@
 // multiple of 4), up to six tiles deep, so no thread waits for another's copy.  TMA boxes of 16
 // rows x 80 bytes took ten cycles a row, 2700 a tile.
 //
-// What bounds it: not memory (64 x 8192 tokens: single tokens 0.28 ms, 1.0 TB/s; tree of 32 nodes
-// 0.71 ms, 0.39 PFLOP/s).  The tensor pipe is busy an eighth of the time; a tile's chain -- keys
-// expanded, scores, weights, product -- is a sequence of dependent instructions of few warps, and
-// five programs share the instruction cache.  Hence the rolled loops, the paths apart for changed
-// scores and moved maxima, and the short waits: unrolling the two dequantisation loops costs a
-// quarter (tree 0.84 -> 1.03 ms), reading rows word by word from shared memory instead of holding
-// them in registers saved a tenth, one copy of each loop's start another.
+// What bounds it: not memory (64 x 8192 tokens: single tokens 0.25 ms, 1.1 TB/s; tree of 32 nodes
+// 0.70 ms, 0.39 PFLOP/s), nor the tensor pipe (an eighth busy).  A tile takes the softmax warps
+// 4700 cycles, 2900 of them in the weights of 128 columns, whose instructions alone would issue in
+// about 1100; dequantisation and the products hide behind that.  A window adds 45000 cycles (its
+// queries, a first tile's maxima, sums and outputs).  Twice the softmax warps, or a product and a
+// vote for each half of the columns, change nothing of a tile; code size does: five programs
+// share the instruction cache, and unrolling the two dequantisation loops costs a quarter (tree
+// 0.84 -> 1.03 ms).  Hence the rolled loops, the paths apart for changed scores and moved maxima,
+// and rows read word by word from shared memory (a tenth against holding them in registers).
 //
 // All waits are bounded: one that runs out records the timeout, every role leaves its loop, the
 // copies and MMAs in flight are waited for and TMEM is freed.
@@ -1214,8 +1217,9 @@ bool attn_tc_supported(const AttnArgs& a) {
   return (a.head_dim == 64 || a.head_dim == 128 || a.head_dim == 256) && (a.out_dtype == kF16 || a.out_dtype == kBF16);
 }
 
-// Columns of a window: as many as shared memory and TMEM allow, or a quarter where the sequences'
-// rows fill no more on average (single tokens, short trees).
+// Columns of a window: as many as shared memory and TMEM allow, or 32 where the sequences' rows
+// fill no more on average (single tokens, short trees): less code and a deeper ring (single tokens
+// 64 x 8192 0.28 -> 0.25 ms, 64 columns 0.26; 16 rows of 64 channels 75 -> 60 us, 64 columns 67).
 int attn_tc_cols(const AttnArgs& a) {
   const int most = a.head_dim < 256 ? 128 : a.out_dtype == kF16 ? 32 : 64, few = 32;
   const int64_t cols = (int64_t)a.num_rows * (a.num_q_heads / a.num_kv_heads);

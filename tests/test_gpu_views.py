@@ -244,6 +244,23 @@ def test_decode_batches_and_padding_rows(dtype, rows):
     _close(out, want, reach, dtype, 128)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_one_long_sequence_among_single_tokens(d, dtype):
+    # few rows a sequence on average, so narrow windows; one sequence fills several of them
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    lens = [int(x) for x in rng.integers(1, 300, size=11)] + [350]
+    c = Cache(rng, lens, d, 2, 4, 3)
+    q_seq = np.concatenate([np.arange(11), np.full(50, 11)])
+    q_len = np.concatenate([lens[:11], np.arange(301, 351)])
+    q = rng.standard_normal((len(q_seq), 8, d)).astype(np.float32)
+    qd = torch.from_numpy(q).cuda().to(DT[dtype])
+    out = tq.tq_paged_prefill_biased(qd, _i32(q_seq), _i32(q_len), **c.dev(), window=170, check=True)
+    want, reach = c.oracle(qd.float().cpu().numpy(), q_seq, so.biased_visible(q_seq, q_len, c.cap, 12, window=170))
+    _close(out, want, reach, dtype, d)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "fp16"])
 def test_agrees_with_the_prefill_without_modifiers(dtype):
     tq = _tq()
