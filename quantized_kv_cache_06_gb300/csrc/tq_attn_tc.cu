@@ -16,15 +16,13 @@
 // shared memory in 16-byte chunks, swizzled.  The norms are per token, so per lane: nu_k
 // multiplies the score, nu_v the weight.
 //
-// Precision.  fp16 outputs (SPLIT): Q = hi + lo in fp16, the lo parts as further k-steps into the
-// same accumulators, so that scores are off by the rounding of the centroids alone (alpha puts
-// them near fp16 grid points) however large they are.  bf16 outputs: one fp16 part, eight times
-// finer than the output's own rounding.  A weight p nu_v is one fp16 value, half a step of the
-// output's type at most from its own (in two parts an output comes nearer by a
-// fifth of its own rounding, and a window holds half of the columns: tree 4 x 131072 1.28 against
-// 0.72 ms).  The window's queries are scaled by one power of two, and the weights by
-// another (moved when a larger norm arrives), so neither large queries nor large norms leave the
-// fp16 range.  Sums, maxima and both products are fp32.
+// Precision.  fp16 outputs (SPLIT): Q and P' = hi + lo in fp16, the lo parts as further k-steps
+// into the same accumulators, so what is left is the rounding of the centroids (alpha puts them
+// near fp16 grid points).  One part for P' would hold twice the columns (tree 4 x 131072 0.73 ms),
+// at an error of one and a half times the output's own rounding.  bf16 outputs: one fp16 part
+// each, eight times finer than the output's own rounding.  The window's queries are scaled by one
+// power of two, and the weights p nu_v by another (moved when a larger norm arrives), so neither
+// large queries nor large norms leave the fp16 range.  Sums, maxima and both products are fp32.
 //
 // Softmax in base 2; the running max of a column moves only when a score passes it by 2^6, so
 // most tiles rescale nothing; when one does, the softmax warps scale O^T in TMEM themselves
@@ -43,7 +41,7 @@
 // rows x 80 bytes took ten cycles a row, 2700 a tile.
 //
 // What bounds it: not memory (64 x 8192 tokens: single tokens 0.25 ms, 1.1 TB/s; tree of 32 nodes
-// 0.70 ms, 0.39 PFLOP/s), nor the tensor pipe (an eighth busy).  A tile takes the softmax warps
+// 0.71 ms, 0.39 PFLOP/s), nor the tensor pipe (an eighth busy).  A tile takes the softmax warps
 // 4700 cycles, 2900 of them in the weights of 128 columns, whose instructions alone would issue in
 // about 1100; dequantisation and the products hide behind that.  A window adds 45000 cycles (its
 // queries, a first tile's maxima, sums and outputs).  Twice the softmax warps, or a product and a
@@ -102,7 +100,8 @@ struct Tc {
   static constexpr int kQPart = kN * D * 2;  // a part of the queries
   static constexpr int kQBytes = (SPLIT ? 2 : 1) * kQPart;
   static constexpr int kVBytes = kTok / 2 * D * 2;
-  static constexpr int kPBytes = kTok * kN * 2 < 16384 ? 16384 : kTok * kN * 2;
+  static constexpr int kPCols = (SPLIT ? 2 : 1) * kN;    // columns of P: the lo parts behind all hi parts
+  static constexpr int kPBytes = kTok * (kPCols < 64 ? 64 : kPCols) * 2;
   static constexpr int kOffQ = 0;
   static constexpr int kOffV = kOffQ + kQBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVBytes;
@@ -928,8 +927,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const float2 f2 = *reinterpret_cast<const float2*>(corr_s + col0 + c0 + 2 * i);
               const float2 y = __ffma2_rn(x[i], kn2, m2);
               float2& li = l[8 * g + i];
-              li.x = li.x == INFINITY ? 0.f : fmaf(li.x, f2.x, -ex2a(y.x));
-              li.y = li.y == INFINITY ? 0.f : fmaf(li.y, f2.y, -ex2a(y.y));
+              // (a factor that underflows leaves nothing either)
+              li.x = li.x == INFINITY || f2.x == 0.f ? 0.f : fmaf(li.x, f2.x, -ex2a(y.x));
+              li.y = li.y == INFINITY || f2.y == 0.f ? 0.f : fmaf(li.y, f2.y, -ex2a(y.y));
             }
           }
           tc_after();
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (c0 >= cols) continue;
             float2 x[8];
             fetch(c0, x);
-            uint32_t o[8];
+            uint32_t o[8], r[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float4 m4 = *reinterpret_cast<const float4*>(negm_s + col0 + c0 + 4 * i);
@@ -976,6 +976,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 l[8 * g + 2 * i + e] = __fadd2_rn(l[8 * g + 2 * i + e], y);
                 y = __fmul2_rn(y, vs2);
                 o[2 * i + e] = pack2(y.x, y.y);
+                if constexpr (SPLIT) {
+                  const __half2 hh = *reinterpret_cast<const __half2*>(&o[2 * i + e]);
+                  r[2 * i + e] = pack2(y.x - __low2float(hh), y.y - __high2float(hh));
+                }
               }
             }
             if (g == 0 && !waited) {  // the stream's product before is done: P and O are free
@@ -984,6 +988,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             st_v4(p_addr(col0 + c0), o[0], o[1], o[2], o[3]);
             st_v4(p_addr(col0 + c0 + 8), o[4], o[5], o[6], o[7]);
+            if constexpr (SPLIT) {
+              st_v4(p_addr(C::kN + col0 + c0), r[0], r[1], r[2], r[3]);
+              st_v4(p_addr(C::kN + col0 + c0 + 8), r[4], r[5], r[6], r[7]);
+            }
           }
           const bool first_pass = !waited;
           waited = true;
@@ -1138,7 +1146,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t idp = mma_idesc(padded, true);
       for (int k = 0; k < tiles; ++k) {  // O^T of its stream += V^T P^T
         const int s = k & (streams - 1);
-        const uint32_t p_s = p_at + (uint32_t)((((s * pitch) >> 6) * (kTok * 128) + ((s * pitch) & 63) * 2) >> 4);
+        auto p_of = [&](int c) -> uint32_t { return p_at + (uint32_t)(((c >> 6) * (kTok * 128) + (c & 63) * 2) >> 4); };
+        const uint32_t p_s = p_of(s * pitch), p_lo = p_of(C::kN + s * pitch);
         const uint32_t o_s = tmem + C::kO + s * pitch;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -1151,6 +1160,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int ks = 0; ks < kTok / 32; ++ks)
               mma_ss(o_s + hf * C::kN, v_at + ((vslot * C::kVBytes + hf * 2 * 64 * 128 + ks * 2048) >> 4),
                      p_s + ((half * (kTok / 2 * 128) + ks * 2048) >> 4), idp, k >= streams || half > 0 || ks > 0);
+          if constexpr (SPLIT)
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+              for (int ks = 0; ks < kTok / 32; ++ks)
+                mma_ss(o_s + hf * C::kN, v_at + ((vslot * C::kVBytes + hf * 2 * 64 * 128 + ks * 2048) >> 4),
+                       p_lo + ((half * (kTok / 2 * 128) + ks * 2048) >> 4), idp, true);
           tc_commit(v_empty(vslot));
           if (++vslot == C::kVSlots) vslot = 0, vph ^= 1;
         }
@@ -1219,24 +1235,29 @@ bool attn_tc_supported(const AttnArgs& a) {
 
 // Columns of a window: as many as shared memory and TMEM allow, or 32 where the sequences' rows
 // fill no more on average (single tokens, short trees): less code and a deeper ring (single tokens
-// 64 x 8192 0.28 -> 0.25 ms, 64 columns 0.26; 16 rows of 64 channels 75 -> 60 us, 64 columns 67).
+// 64 x 8192 0.28 -> 0.25 ms, with 64 columns 0.26).
+constexpr int kFewCols = 32;
+constexpr int most_cols(int d, bool split) { return d < 256 ? (split ? 64 : 128) : split ? 32 : 64; }
+
 int attn_tc_cols(const AttnArgs& a) {
-  const int most = a.head_dim < 256 ? 128 : a.out_dtype == kF16 ? 32 : 64, few = 32;
   const int64_t cols = (int64_t)a.num_rows * (a.num_q_heads / a.num_kv_heads);
-  return a.num_seqs > 0 && cols <= (int64_t)few * a.num_seqs ? few : most;
+  return a.num_seqs > 0 && cols <= (int64_t)kFewCols * a.num_seqs ? kFewCols : most_cols(a.head_dim, a.out_dtype == kF16);
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {
-  const bool split = a.out_dtype == kF16, few = w.cols == 32;
-  auto of = [&](auto dim, auto most) -> cudaError_t {
-    constexpr int D = decltype(dim)::value, N = decltype(most)::value;
-    if (split) return few ? launch_tc<D, true, 32>(a, w, stream) : launch_tc<D, true, D == 256 ? 32 : N>(a, w, stream);
-    return few ? launch_tc<D, false, 32>(a, w, stream) : launch_tc<D, false, N>(a, w, stream);
+  const bool few = w.cols == kFewCols;
+  auto of = [&](auto dim, auto split) -> cudaError_t {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool SPLIT = decltype(split)::value;
+    if (few) return launch_tc<D, SPLIT, kFewCols>(a, w, stream);
+    return launch_tc<D, SPLIT, most_cols(D, SPLIT)>(a, w, stream);
   };
-  using std::integral_constant;
-  if (a.head_dim == 64) return of(integral_constant<int, 64>{}, integral_constant<int, 128>{});
-  if (a.head_dim == 128) return of(integral_constant<int, 128>{}, integral_constant<int, 128>{});
-  return of(integral_constant<int, 256>{}, integral_constant<int, 64>{});
+  auto of_dim = [&](auto dim) -> cudaError_t {
+    return a.out_dtype == kF16 ? of(dim, std::integral_constant<bool, true>{}) : of(dim, std::integral_constant<bool, false>{});
+  };
+  if (a.head_dim == 64) return of_dim(std::integral_constant<int, 64>{});
+  if (a.head_dim == 128) return of_dim(std::integral_constant<int, 128>{});
+  return of_dim(std::integral_constant<int, 256>{});
 }
 
 }  // namespace tq

@@ -244,6 +244,28 @@ def test_decode_batches_and_padding_rows(dtype, rows):
     _close(out, want, reach, dtype, 128)
 
 
+@pytest.mark.parametrize("slope", [0.3, 0.65, 0.7, 1.0, 4.0])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_a_distance_bias_that_moves_every_maximum(d, dtype, slope):
+    # weights of one tile against the maximum of the one before: 2^55 to beyond the largest float
+    tq = _tq()
+    rng = np.random.default_rng(int(100 * slope) + d)
+    lens = [700, 900]
+    c = Cache(rng, lens, d, 2, 4, 4)
+    q_seq, q_len = np.array([0, 1, 1]), np.array([700, 900, 513])
+    q = rng.standard_normal((3, 4, d)).astype(np.float32)
+    qd = torch.from_numpy(q).cuda().to(DT[dtype])
+    slopes = np.array([slope, slope / 2, slope, 1.5 * slope])
+    out = tq.tq_paged_prefill_biased(qd, _i32(q_seq), _i32(q_len), **c.dev(), check=True,
+                                     alibi_slopes=torch.from_numpy(slopes).float().cuda())
+    see = so.biased_visible(q_seq, q_len, c.cap, 2)
+    want, reach = c.oracle(qd.float().cpu().numpy(), q_seq, see, slopes=slopes.astype(np.float32).astype(np.float64),
+                           q_pos=q_len - 1)
+    # (what has weight lies near the row: its bias, at most 30, is off by as many 2^-24)
+    _close(out, want, reach * (2 if dtype == "fp32" else 1), dtype, d)
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_one_long_sequence_among_single_tokens(d, dtype):
