@@ -42,8 +42,8 @@
 //
 // What bounds it: not memory (64 x 8192 tokens: single tokens 0.25 ms, 1.1 TB/s; tree of 32 nodes
 // 0.71 ms, 0.39 PFLOP/s), nor the tensor pipe (an eighth busy).  A tile takes the softmax warps
-// 4700 cycles, 2900 of them in the weights of 128 columns, whose instructions alone would issue in
-// about 1100; dequantisation and the products hide behind that.  A window adds 45000 cycles (its
+// 4700 cycles, 2900 of them in the weights of 128 columns; dequantisation and the products hide
+// behind that.  All roles together issue 11900 instructions a tile, half of the slots.  A window adds 45000 cycles (its
 // queries, a first tile's maxima, sums and outputs).  Twice the softmax warps, or a product and a
 // vote for each half of the columns, change nothing of a tile; code size does: five programs
 // share the instruction cache, and unrolling the two dequantisation loops costs a quarter (tree
