@@ -80,6 +80,9 @@ constexpr int kMaxRing = 6;
 constexpr int kNorms = 6;  // tiles whose norms are kept: keys and values run at most five tiles ahead of the softmax
 constexpr float kSlack = 6.0f;            // log2 units the running max may lag
 constexpr float kMaxWeight = 64.0f;       // 2^kSlack
+// Binades a scaled value norm may reach: a weight of up to 2^6 times a norm below 2^9 stays below
+// 2^15; with one more their product could pass 65520, which fp16 rounds to infinity.
+constexpr int kNormSlack = 8;
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
 constexpr int kNoToken = -0x7fffffff - 1;  // a table entry that no token asks for
 constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
@@ -897,7 +900,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float vscale = 1.f;
           if (vall > 0) {
             const int e = exp_of(__int_as_float(vall));
-            if (e - ve > 9) {  // the largest norm so far to 2^6
+            if (e - ve > kNormSlack) {  // the largest norm so far to 2^6
               const int ne = e - 6;
               vscale = ve == -1000 ? 1.f : pow2i(max(-126, ve - ne));
               ve = ne;
@@ -996,7 +999,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool first_pass = !waited;
           waited = true;
           if (!first_pass) break;
-          const bool move = !moved && (over > kMaxWeight || (vf > 0.f && exp_of(vf) - ve > 9));
+          const bool move = !moved && (over > kMaxWeight || (vf > 0.f && exp_of(vf) - ve > kNormSlack));
           if (__builtin_expect(!named_any(bar_id, bar_n, move || !ok), 1)) break;
           if (*fl) {  // the same for all warps of the stream
             broken = true;

@@ -1,0 +1,58 @@
+"""Attention views at the ends of their ranges: weights next to the largest fp16, caps and queries
+and norms of any size, blocks that no row sees, lengths beyond the table."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import views as w  # noqa: E402
+from oracle import step_oracle as so  # noqa: E402
+from oracle import tq_oracle as o  # noqa: E402
+from test_gpu_views import Cache  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def _tq():
+    import quantized_kv_cache_06_gb300 as tq
+
+    return tq
+
+
+def _set_norm(c, comp, seq, t, value):
+    c.pages[comp][c.bt[seq, t // c.bs], t % c.bs, :, -4:] = np.frombuffer(np.float32(value).tobytes(), dtype=np.uint8)
+
+
+def _sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_weight_times_norm_next_to_the_largest_fp16(dtype):
+    # one token of a third tile: its score up to 6 (in powers of two) above everything before it, its
+    # value norm a little under 16 times the others', so weight times norm stands at 2^16 times theirs
+    # / 2^6.  A kv head per SM, so that one CTA takes a sequence's three tiles in order.
+    tq = _tq()
+    rng = np.random.default_rng(41)
+    h, s, d, n, at = _sms(), 8, 128, 300, 270
+    c = Cache(rng, [n] * s, d, h, 4, 4)
+    q = torch.from_numpy(rng.standard_normal((s, h, d)).astype(np.float32)).cuda().to(w.DT[dtype])
+    rq = q.float().cpu().numpy().astype(np.float64) @ o.rotation_matrix(c.signs).T
+    target = np.linspace(5.999, 6.0003, s * h).reshape(s, h)  # log2 of the weight
+    for i in range(s):
+        blocks, off = c.bt[i, np.arange(n) // 16], np.arange(n) % 16
+        c.pages[0][blocks, off, :, -4:] = 0  # key norms: every score 0
+        idx = np.where(rq[i] > 0, 15, 0)
+        dot = (rq[i] * c.kc[idx]).sum(1) / math.sqrt(d)
+        c.pages[0][blocks[at], off[at]] = o.make_rows(idx, (target[i] * math.log(2) / dot).astype(np.float32), 4)
+        c.pages[1][blocks, off, :, -4:] = np.frombuffer(np.float32(1.0).tobytes(), dtype=np.uint8)
+        _set_norm(c, 1, i, at, 8 * 1.99999)
+    dv = c.dev()
+    zero = torch.zeros(s, 1, dtype=torch.int32, device="cuda")
+    out = tq.tq_paged_tree(q, w.i32(np.arange(s)), w.i32([n] * s), zero, **dv, check=True)
+    see = np.zeros((s, c.cap), dtype=bool)
+    see[:, :n] = True
+    w.close(out, w.exact(q, np.arange(s), see, **dv), dtype)
