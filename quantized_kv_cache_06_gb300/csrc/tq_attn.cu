@@ -580,10 +580,10 @@ cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t strea
   w.q_rot = reinterpret_cast<float*>(ws + p.off_rot);
   w.q_norm2 = reinterpret_cast<float*>(ws + p.off_norm2);
   if (p.tc) {
-    // scale, log2 e, the rotation's 1 / sqrt(D) and the keys' alpha in one factor; capped scores
-    // are taken as 2 log2(e) s / cap, whose power of two gives the tanh
+    // scale, log2 e, the rotation's 1 / sqrt(D) and the keys' alpha in one factor; scores with an
+    // ordinary cap are taken as 2 log2(e) s / cap, whose power of two gives the tanh
     const float scale = a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)a.head_dim);
-    w.q_mul = (a.softcap > 0.f ? 2.f * scale / a.softcap : scale) * kAttnLog2e / (sqrtf((float)a.head_dim) * a.k_alpha);
+    w.q_mul = (cap_folded(a.softcap) ? 2.f * scale / a.softcap : scale) * kAttnLog2e / (sqrtf((float)a.head_dim) * a.k_alpha);
     const int64_t ctas = ((int64_t)a.num_rows * a.num_q_heads + kSchedThreads / 32 - 1) / (kSchedThreads / 32) + 1;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (a.head_dim == 64) attn_schedule_kernel<64><<<(int)ctas, kSchedThreads, 0, stream>>>(a, w);

@@ -50,6 +50,12 @@ struct AttnArgs {
 
 constexpr int kAttnTile = 128;  // tokens per tile of the schedule
 
+// Whether the tensor-core kernel takes a cap as cap - 2 cap / (1 + e^(2 s / cap)), with 2 / cap in
+// the queries' factor: two instructions a score, off by 1.6e-7 of the cap (4e-5 at 256, a sixth
+// of the rounding of an fp16 weight; 0.09 at 1e6).  A cap below 2^-10 could take the queries' factor
+// out of range.  The others get the scores as they are and a form that holds anywhere.
+inline __host__ __device__ bool cap_folded(float c) { return c >= 0.0009765625f && c <= 256.f; }
+
 // A run of query rows of one sequence that a CTA takes together, and the tiles they see:
 // nA tiles from tA0 (the prefix interval), then nB tiles from tB0.
 struct AttnWindow {

@@ -56,3 +56,18 @@ def test_weight_times_norm_next_to_the_largest_fp16(dtype):
     see = np.zeros((s, c.cap), dtype=bool)
     see[:, :n] = True
     w.close(out, w.exact(q, np.arange(s), see, **dv), dtype)
+
+
+@pytest.mark.parametrize("cap", [1e-25, 1e-3, 200.0, 300.0, 1e4, 1e6, 1e8, 1e30, 3e38])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_caps_of_any_size(d, dtype, cap):
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [300, 77], d, 2, 4, 4)
+    q = torch.from_numpy(rng.standard_normal((5, 8, d)).astype(np.float32)).cuda().to(w.DT[dtype])
+    q_seq, q_len = np.array([0, 0, 0, 1, 1]), np.array([298, 299, 300, 1, 77])
+    dv = c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, softcap=cap, scale=0.3, check=True)
+    see = so.biased_visible(q_seq, q_len, c.cap, 2)
+    w.close(out, w.exact(q, q_seq, see, **dv, softcap=float(np.float32(cap)), scale=0.3), dtype)
