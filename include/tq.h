@@ -532,8 +532,9 @@ size_t tq_paged_tree_workspace(int num_q_rows, int num_q_heads, int num_kv_heads
  *   workspace  device, >= tq_paged_tree_workspace(...) bytes, 256-byte aligned
  *   status_dev device int32 or NULL: TQ_ERR_INVALID_ARG when a q_seq lies outside
  *              [-1, num_seqs) (zero row), or a context or node lies beyond the table row
- *              (clamped); TQ_ERR_BLOCK_OUT_OF_RANGE when a block id read lies outside
- *              [0, num_blocks) (its tokens are left out).
+ *              (clamped); TQ_ERR_BLOCK_OUT_OF_RANGE when the block id of a token that some
+ *              row sees lies outside [0, num_blocks) (the token is left out).  Entries of
+ *              blocks that no row sees (freed behind a window, say) may hold anything.
  * A row that sees nothing is zero.  Rows of one sequence should be neighbours: they share
  * every dequantised tile.  The other arguments are tq_paged_prefill's.  fp32 outputs are
  * computed in fp32 throughout; fp16 and bf16 outputs from fp16 products with fp32 sums.

@@ -328,8 +328,6 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
 #pragma unroll
             for (int k = 0; k < 4; ++k) norm |= (uint32_t)row[rb - 4 + k] << (8 * k);
           }
-        } else if (there && run == 0 && comp == 0 && a.status) {
-          atomicMax(a.status, (int32_t)kBlockOutOfRange);
         }
         if (run == 0) {
           (comp ? vn_s : kn_s)[t] = __uint_as_float(norm);
@@ -373,13 +371,16 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
         }
       }
       float pv[kSimtPer];
+      bool lost = false;  // a row sees this token, but its block lies outside the pages
 #pragma unroll
       for (int m = 0; m < kSimtPer; ++m) {
         const int col = first_col + m;
         pv[m] = 0.f;
         if (col >= cols) continue;
         const int row = win.row0 + col / G;
-        const bool see = ok && row_sees(view[col], a.mask ? a.mask + (int64_t)row * a.mask_words : nullptr, tok);
+        const bool asks = row_sees(view[col], a.mask ? a.mask + (int64_t)row * a.mask_words : nullptr, tok);
+        const bool see = asks && ok;
+        lost |= asks && !ok;
         float x = -INFINITY;
         if (see) {
           x = dot[m] * kn_s[lane];
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
         for (int e = 0; e < E; ++e) o[m][e] *= corr;
         pv[m] = p != 0.f ? p * vn_s[lane] : 0.f;
       }
+      if (lost && a.status) atomicMax(a.status, (int32_t)kBlockOutOfRange);
 #pragma unroll 4
       for (int t = 0; t < kSimtTok; ++t) {
         float val[E];

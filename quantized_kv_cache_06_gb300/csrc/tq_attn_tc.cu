@@ -84,7 +84,7 @@ constexpr float kMaxWeight = 64.0f;       // 2^kSlack
 // 2^15; with one more their product could pass 65520, which fp16 rounds to infinity.
 constexpr int kNormSlack = 8;
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
-constexpr int kNoToken = -0x7fffffff - 1;  // a table entry that no token asks for
+constexpr int kNoToken = -0x7fffffff - 1;  // the entry of a token that is not there: no block
 constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
 
 template <int D, bool SPLIT, int N>
@@ -663,9 +663,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int block = next, off = next_off;
         next = next_entry(cur, t_lane, next_off);
         copy_row(from, H * rbv, skip_v, rbv, row + st * stage_bytes, block, off);
-        // (the values' warps report an entry out of range; the keys' leave its token out)
-        if (block != kNoToken && (block < 0 || block >= a.num_blocks) && a.status)
-          atomicMax(a.status, (int32_t)kBlockOutOfRange);
         if (++st == p.ring) st = 0;
       }
     };
@@ -824,6 +821,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // takes them with a factor of one.  (A loop apart, so that plain tiles keep their code
           // together in the instruction cache.)
           seen = false;
+          bool lost = false;  // a row sees this token, but its block lies outside the pages
 #pragma unroll 1
           for (int c0 = c_first; c0 < cols; c0 += c_step) {
             float2 x[8];
@@ -870,6 +868,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         __ldg(a.mask + (int64_t)(win.row0 + r) * a.mask_words + (node ? j >> 5 : 0));
                     s |= node && ((word >> (j & 31)) & 1u);
                   }
+                  lost |= s && !real;
                   if (s && real) see |= ((1u << G) - 1u) << ((r << g_log) - c0);
                 }
               }
@@ -883,6 +882,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tm_wait_st();
           kn = 1.f;
+          if (lost && a.status) atomicMax(a.status, (int32_t)kBlockOutOfRange);
         }
         const float2 kn2 = make_float2(kn, kn);
         const bool vfin = fabsf(vn) < INFINITY;

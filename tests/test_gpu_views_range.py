@@ -71,3 +71,49 @@ def test_caps_of_any_size(d, dtype, cap):
     out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, softcap=cap, scale=0.3, check=True)
     see = so.biased_visible(q_seq, q_len, c.cap, 2)
     w.close(out, w.exact(q, q_seq, see, **dv, softcap=float(np.float32(cap)), scale=0.3), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_blocks_that_no_row_sees_may_be_gone(d, dtype):
+    # an engine that frees the blocks behind its window, between a prefix and the window, before the
+    # documents or under rejected nodes marks them -1 in the table
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    q = torch.from_numpy(rng.standard_normal((4, 8, d)).astype(np.float32)).cuda().to(w.DT[dtype])
+    q_seq, q_len = np.array([0, 0, 1, 2]), np.array([399, 400, 333, 20])
+    for kw in (dict(window=70), dict(window=9, prefix=[40, 17, 1]), dict(docs=np.array([300, 310, 200, 3])),
+               dict(docs=np.array([300, 310, 20, 3]), prefix=[350, 33, 17])):
+        c = Cache(rng, [400, 333, 20], d, 2, 4, 4)
+        docs, prefix = kw.get("docs"), kw.get("prefix")
+        see = so.biased_visible(q_seq, q_len, c.cap, 3, kw.get("window", 0), prefix, docs)
+        gone = 0
+        for s in range(3):
+            for b in range(c.width):
+                if not see[q_seq == s][:, b * 16:b * 16 + 16].any():
+                    c.bt[s, b] = [-1, c.nb, 10 ** 9, -2 ** 31][gone % 4]
+                    gone += 1
+        assert gone > 20
+        dv = c.dev()
+        out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, check=True, window=kw.get("window", 0),
+                                         doc_starts=None if docs is None else w.i32(docs),
+                                         prefix_lens=None if prefix is None else w.i32(prefix))
+        w.close(out, w.exact(q, q_seq, see, **dv), dtype)
+    c = Cache(rng, [80], d, 2, 4, 4)
+    c.bt[0, 3] = -1  # nodes 8 .. 23 of a context of 40 tokens
+    mask = np.array([[1 << 30, 1], [3, 255], [0x800000FF, 0], [0xFF, 0]], dtype=np.uint32)
+    see = so.tree_visible([0] * 4, [40], mask, c.cap)
+    dv = c.dev()
+    args = (q, w.i32([0] * 4), w.i32([40]), w.i32(mask.view(np.int32)))
+    w.close(tq.tq_paged_tree(*args, **dv, check=True), w.exact(q, np.zeros(4, int), see, **dv), dtype)
+    # and a seen one is still reported, whatever its entry
+    for bad in (-1, c.nb, -2 ** 31):
+        dv["block_table"][0, 4] = bad
+        with pytest.raises(tq.TQError) as err:
+            tq.tq_paged_tree(*args, **dv, check=True)
+        assert err.value.status == tq.TQ_ERR_BLOCK_OUT_OF_RANGE
+        dv["block_table"][0, 4] = 10 ** 6
+        see2 = so.tree_visible([0] * 4, [40], mask, c.cap)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        w.close(tq.tq_paged_tree(*args, **dv, status=status), w.exact(q, np.zeros(4, int), see2, **dv), dtype)
+        assert int(status.item()) == tq.TQ_ERR_BLOCK_OUT_OF_RANGE
