@@ -367,7 +367,7 @@ tq_status attn_impl(const char* name, tq::AttnArgs a, size_t workspace_bytes, co
   const int64_t cap = (int64_t)a.max_blocks_per_seq * a.block_size;
   if (cap > 0x7fffff00LL)
     return fail(TQ_ERR_UNSUPPORTED, "%s: a table row of %lld tokens (at most 2^31 - 256)", name, (long long)cap);
-  if ((double)a.num_rows * (double)(cap / tq::kAttnTile + 2) > 2147483647.0)
+  if ((double)a.num_rows * (double)(cap / tq::kAttnTile + 2 + tq::kAttnMaxLead) > 2147483647.0)
     return fail(TQ_ERR_UNSUPPORTED, "%s: %d rows of up to %lld tokens: pass fewer rows a call", name, a.num_rows,
                 (long long)cap);
   if (a.num_rows > 0 && (!a.q || !a.k_pages || !a.v_pages || !a.q_seq || !row_lens || !a.signs || !a.k_centroids ||

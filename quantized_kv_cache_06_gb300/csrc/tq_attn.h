@@ -57,11 +57,13 @@ constexpr int kAttnTile = 128;  // tokens per tile of the schedule
 inline __host__ __device__ bool cap_folded(float c) { return c >= 0.0009765625f && c <= 256.f; }
 
 // A run of query rows of one sequence that a CTA takes together, and the tiles they see:
-// nA tiles from tA0 (the prefix interval), then nB tiles from tB0.
+// nA tiles from tA0 (the prefix interval), then nB tiles from tB0.  The parts are cut from a line
+// of places, one a tile and `lead` before the first tile of each window, for its start and end.
 struct AttnWindow {
   int row0, nrows, seq;
   int tA0, nA, tB0, nB;
-  int tile_base;  // tiles of all windows before
+  int tile_base;     // place of the first tile
+  int tiles_before;  // tiles of all windows before
   // reductions over the rows, in tokens (schedule kernel)
   int p_lo, p_hi, w_lo, w_hi;
 };
@@ -69,8 +71,9 @@ struct AttnWindow {
 // Workspace: header, windows, window of each row, partial results of the CTAs.
 struct AttnHeader {
   int num_windows;
-  int total_tiles;
-  int pad[2];
+  int total;  // places
+  int lead;   // places before a window's first tile
+  int pad;
 };
 
 struct AttnPlan {
@@ -98,10 +101,13 @@ struct AttnWork {
   float* q_norm2;
   float q_mul;
   int cols, parts, rows_per_window;
+  int lead;  // where windows are many: places a window's start and end are worth
 };
+constexpr int kAttnMaxLead = 8;
 
 bool attn_tc_supported(const AttnArgs& a);
 int attn_tc_cols(const AttnArgs& a);
+int attn_tc_lead(int cols);
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream);
 
 #ifdef __CUDACC__
@@ -170,8 +176,8 @@ __device__ __forceinline__ bool row_sees(const RowSees& v, const uint32_t* mask,
   return s;
 }
 
-// Parts that hold tiles: with fewer tiles than parts, one tile each (the combine walks every
-// part between a window's first and last, so none of them may be empty).
+// Parts that hold places: with fewer places than parts, one each (the combine walks every part
+// between a window's first tile and its last, so none of them may be empty).
 __device__ __forceinline__ int live_parts(const AttnWork& w, int total) { return min(w.parts, total); }
 // E consecutive floats another kernel of the call wrote (aligned to 4 E bytes; plain loads: the
 // memory is written again within the call).
@@ -192,13 +198,14 @@ __device__ __forceinline__ void load_floats(const float* p, float (&v)[E]) {
     }
   }
 }
-// The first tile of partition p of `parts` over `total` tiles.
+// The first place of partition p of `parts` over `total` places.
 __device__ __forceinline__ int part_begin(int total, int p, int parts) { return (int)((int64_t)total * p / parts); }
-// The partition that holds tile g.
+// The partition that holds place g.
 __device__ __forceinline__ int part_of(int total, int g, int parts) {
   return (int)(((int64_t)(g + 1) * parts - 1) / total);
 }
-// The window that holds tile g (num_windows > 0, 0 <= g < total): the last one that starts at or before it.
+// The window that holds place g (num_windows > 0, 0 <= g <= total): the last one whose tiles start at
+// or before it, or the first.
 __device__ __forceinline__ int window_of(const AttnWork& w, int g) {
   int lo = 0, hi = w.head->num_windows;
   while (hi - lo > 1) {

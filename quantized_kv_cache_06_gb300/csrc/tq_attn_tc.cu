@@ -452,18 +452,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = tmem_slot;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
-  const int total = w.head->total_tiles;
+  const int4 head = *reinterpret_cast<const int4*>(w.head);
+  const int num_windows = head.x, total = head.y, lead = head.z;
   const int parts = live_parts(w, total);
   const int g0 = part < parts ? part_begin(total, part, parts) : 0;
   const int g1 = part < parts ? part_begin(total, part + 1, parts) : 0;
   // Calls f(window, first tile, end tile) for every window with tiles in this part.
   auto for_windows = [&](auto f) {
     if (g0 >= g1) return;
-    for (int g = g0, wi = window_of(w, g0); g < g1; ++wi) {
+    for (int g = g0, wi = window_of(w, g0); g < g1 && wi < num_windows; ++wi) {
       const AttnWindow win = w.win[wi];
-      const int first = g - win.tile_base, last = min(win.nA + win.nB, first + (g1 - g));
+      const int first = max(0, g - win.tile_base), last = min(win.nA + win.nB, g1 - win.tile_base);
       if (last <= first) continue;
-      g += last - first;
+      g = win.tile_base + last;
       if (!f(win, first, last)) return;
     }
   };
@@ -475,18 +476,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Two streams of tiles when the window's MMA columns fit half of the TMEM regions.
   auto streams_of = [&](int padded) -> int { return padded <= C::kN / 2 ? 2 : 1; };
 
+  // The part's tiles, from the window of its first place on.
+  auto part_tiles = [&](int wi) -> int {
+    if (lead == 0 || g0 >= g1) return g1 - g0;
+    auto before = [&](int g, const AttnWindow& win) -> int {
+      return win.tiles_before + max(0, min(win.nA + win.nB, g - win.tile_base));
+    };
+    return before(g1, w.win[window_of(w, g1)]) - before(g0, w.win[wi]);
+  };
+
   // Packed rows: a lane copies the rows of its token itself, `ring` tiles deep, so no other thread
   // waits for them.  A cursor walks the part's tiles ahead of their use.
   struct Cursor {
-    int g, wi, end, n_a, t_a, t_b, hi;  // tile, window, first tile behind it; its intervals, last token + 1
+    int g, wi, end, n_a, t_a, t_b, hi;  // place, window, place behind its tiles; its intervals, last token + 1
     const int32_t* table;
   };
   const int cap = (int)min((int64_t)a.max_blocks_per_seq * a.block_size, (int64_t)0x7fffff00);
-  auto enter = [&](Cursor& c) {  // the window of tile c.g (c.g < g1), from c.wi on
+  auto enter = [&](Cursor& c) {  // the window of the first tile at c.g (c.g < g1) or behind it, from c.wi on
     for (;; ++c.wi) {
+      if (c.wi >= num_windows) {
+        c.g = g1;
+        return;
+      }
       const AttnWindow win = w.win[c.wi];
       c.end = win.tile_base + win.nA + win.nB;
       if (c.g >= c.end) continue;
+      c.g = max(c.g, win.tile_base);
       c.n_a = win.tile_base + win.nA;
       c.t_a = win.tA0 - win.tile_base;
       c.t_b = win.tB0 - c.n_a;
@@ -499,7 +514,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto next_entry = [&](Cursor& c, int lane_tok, int& off) -> int {
     off = 0;
     if (c.g >= g1) return kNoToken;
-    if (c.g >= c.end) enter(c);
+    if (c.g >= c.end) {
+      enter(c);
+      if (c.g >= g1) return kNoToken;
+    }
     const int tok = (c.g + (c.g < c.n_a ? c.t_a : c.t_b)) * kTok + lane_tok;
     ++c.g;
     if (tok >= c.hi) return kNoToken;
@@ -557,11 +575,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint8_t* from = a.k_pages + h * rbk - skip_k;
       Cursor cur{g0, g0 < g1 ? window_of(w, g0) : 0, g0, 0, 0, 0, 0, nullptr};  // (entered by the first entry)
       uint32_t there = 0;  // bit s: stage s holds a row
+      const int n_tiles = part_tiles(cur.wi);
       int next_off, next = next_entry(cur, t_lane, next_off);  // entries are loaded a tile before their copies
       int st = 0;
       // (rounds before tile 0 only fill the ring)
 #pragma unroll 1
-      for (int it = -p.ring; it < g1 - g0; ++it) {
+      for (int it = -p.ring; it < n_tiles; ++it) {
         if (it >= 0) {
           landed();
           const uint32_t here = row + st * stage_bytes + skip_k;
@@ -619,11 +638,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float2* norms = reinterpret_cast<float2*>(smem + C::kOffNorm);
       const uint8_t* from = a.v_pages + h * rbv - skip_v;
       Cursor cur{g0, g0 < g1 ? window_of(w, g0) : 0, g0, 0, 0, 0, 0, nullptr};  // (entered by the first entry)
+      const int n_tiles = part_tiles(cur.wi);
       int next_off, next = next_entry(cur, t_lane, next_off);
       int st = 0;
       int slot = half % C::kVSlots, vph = 1;  // slot 2 it + half, round by round
 #pragma unroll 1
-      for (int it = -p.ring; it < g1 - g0; ++it) {
+      for (int it = -p.ring; it < n_tiles; ++it) {
         if (it >= 0) {
           landed();
           const uint32_t here = row + st * stage_bytes + skip_v;
@@ -1258,6 +1278,10 @@ bool attn_tc_supported(const AttnArgs& a) {
 // 64 x 8192 0.28 -> 0.25 ms, with 64 columns 0.26).
 constexpr int kFewCols = 32;
 constexpr int most_cols(int d, bool split) { return d < 256 ? (split ? 64 : 128) : split ? 32 : 64; }
+
+// A window's start and end in tiles: 45000 cycles beside 4700 a tile where it is wide, 5 us beside 2
+// us where it is narrow.
+int attn_tc_lead(int cols) { return cols == kFewCols ? 3 : kAttnMaxLead; }
 
 int attn_tc_cols(const AttnArgs& a) {
   const int64_t cols = (int64_t)a.num_rows * (a.num_q_heads / a.num_kv_heads);

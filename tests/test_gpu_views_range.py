@@ -117,3 +117,19 @@ def test_blocks_that_no_row_sees_may_be_gone(d, dtype):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         w.close(tq.tq_paged_tree(*args, **dv, status=status), w.exact(q, np.zeros(4, int), see2, **dv), dtype)
         assert int(status.item()) == tq.TQ_ERR_BLOCK_OUT_OF_RANGE
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_a_long_prompt_beside_many_single_tokens(dtype):
+    # many windows a part, of one tile to four: those of the prompt's first rows and of single tokens
+    tq = _tq()
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(1, 40, size=255)] + [400]
+    c = Cache(rng, lens, 64, 1, 4, 4)
+    q_seq = np.concatenate([np.arange(100), np.full(400, 255), np.arange(100, 255)])
+    q_len = np.concatenate([lens[:100], np.arange(1, 401), lens[100:255]])
+    q = torch.from_numpy(rng.standard_normal((len(q_seq), 4, 64)).astype(np.float32)).cuda().to(w.DT[dtype])
+    dv = c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, check=True)
+    see = so.biased_visible(q_seq, q_len, c.cap, 256)
+    w.close(out, w.exact(q, q_seq, see, **dv), dtype)
