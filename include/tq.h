@@ -536,7 +536,8 @@ size_t tq_paged_tree_workspace(int num_q_rows, int num_q_heads, int num_kv_heads
  *              row sees lies outside [0, num_blocks) (the token is left out).  Entries of
  *              blocks that no row sees (freed behind a window, say) may hold anything.
  * A row that sees nothing is zero.  Rows of one sequence should be neighbours: they share
- * every dequantised tile.  The other arguments are tq_paged_prefill's.  fp32 outputs are
+ * every dequantised tile.  num_seqs counts the table's rows, idle ones too: pass no more than
+ * are in use where that is easy, as rows per sequence choose between forms for few and for many.  The other arguments are tq_paged_prefill's.  fp32 outputs are
  * computed in fp32 throughout; fp16 and bf16 outputs from fp16 products with fp32 sums.
  * Asynchronous, graph-capturable (one workspace per call in flight); host-detected errors:
  * TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA. */

@@ -1274,9 +1274,14 @@ bool attn_tc_supported(const AttnArgs& a) {
 }
 
 // Columns of a window: as many as shared memory and TMEM allow, or 32 where the sequences' rows
-// fill no more on average (single tokens, short trees): less code and a deeper ring (single tokens
-// 64 x 8192 0.28 -> 0.25 ms, with 64 columns 0.26).
-constexpr int kFewCols = 32;
+// fill no more on average (single tokens, short trees): less code and a deeper ring (64 single
+// tokens of 2000: 133 against 151 us; eight rows each: 155 against 182).  That average counts the
+// table's idle rows too, and a long run of rows in narrow windows reads and expands every tile
+// again for each of them (4 x 1000 rows in a table of 512: 3078 against 1227 us).  So it decides
+// only where a wrong guess costs little, up to 2048 columns in all, and where the rows are no more
+// than the sequences, as single tokens are; else windows are wide (256 sequences of eight rows then
+// take 638 against 532 us).
+constexpr int kFewCols = 32, kFewTotal = 2048;
 constexpr int most_cols(int d, bool split) { return d < 256 ? (split ? 64 : 128) : split ? 32 : 64; }
 
 // A window's start and end in tiles: 45000 cycles beside 4700 a tile where it is wide, 5 us beside 2
@@ -1285,7 +1290,8 @@ int attn_tc_lead(int cols) { return cols == kFewCols ? 3 : kAttnMaxLead; }
 
 int attn_tc_cols(const AttnArgs& a) {
   const int64_t cols = (int64_t)a.num_rows * (a.num_q_heads / a.num_kv_heads);
-  return a.num_seqs > 0 && cols <= (int64_t)kFewCols * a.num_seqs ? kFewCols : most_cols(a.head_dim, a.out_dtype == kF16);
+  const bool few = cols <= (int64_t)kFewCols * a.num_seqs && (cols <= kFewTotal || a.num_rows <= a.num_seqs);
+  return few ? kFewCols : most_cols(a.head_dim, a.out_dtype == kF16);
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnWork& w, cudaStream_t stream) {

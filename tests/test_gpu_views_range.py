@@ -133,3 +133,18 @@ def test_a_long_prompt_beside_many_single_tokens(dtype):
     out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, check=True)
     see = so.biased_visible(q_seq, q_len, c.cap, 256)
     w.close(out, w.exact(q, q_seq, see, **dv), dtype)
+
+
+@pytest.mark.parametrize("slots", [5, 300])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prompts_in_a_table_of_mostly_idle_rows(dtype, slots):
+    tq = _tq()
+    rng = np.random.default_rng(4)
+    c = Cache(rng, [700, 300, 650], 128, 1, 4, 4)
+    c.bt = np.concatenate([c.bt, np.full((slots - 3, c.width), -1, dtype=np.int32)])
+    q_seq = np.repeat([2, 0, 1], [400, 500, 300])
+    q_len = np.concatenate([np.arange(251, 651), np.arange(201, 701), np.arange(1, 301)])
+    q = torch.from_numpy(rng.standard_normal((1200, 2, 128)).astype(np.float32)).cuda().to(w.DT[dtype])
+    dv = c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, check=True)
+    w.close(out, w.exact(q, q_seq, so.biased_visible(q_seq, q_len, c.cap, slots), **dv), dtype)
