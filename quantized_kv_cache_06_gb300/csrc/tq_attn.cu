@@ -98,17 +98,17 @@ __global__ void __launch_bounds__(kSchedThreads) attn_schedule_kernel(AttnArgs a
       } else {
         load_chunk<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(a.q) + at, v);
       }
-      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] *= w.q_mul * __ldg(a.signs + lane * E + i);
+      fwht_warp<E>(v);
+      float top = 0.f;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        v[i] *= w.q_mul * __ldg(a.signs + lane * E + i);
-        ss = fmaf(v[i], v[i], ss);
+        w.q_rot[at + i] = v[i];
+        top = fmaxf(top, fabsf(v[i]));
       }
-      fwht_warp<E>(v);
-#pragma unroll
-      for (int i = 0; i < E; ++i) w.q_rot[at + i] = v[i];
-      ss = warp_sum(ss);
-      if (lane == 0) w.q_norm2[id] = ss;
+      top = warp_max(top);
+      if (lane == 0) w.q_top[id] = top;
       return;
     }
   }
@@ -577,8 +577,8 @@ AttnPlan plan_attn(const AttnArgs& a, int num_sms) {
   p.off_ml = up(p.off_acc + slots * a.head_dim * sizeof(float));
   p.off_rot = up(p.off_ml + slots * 2 * sizeof(float));
   const size_t qs = p.tc ? rows * a.num_q_heads : 0;
-  p.off_norm2 = up(p.off_rot + qs * a.head_dim * sizeof(float));
-  p.workspace_bytes = up(p.off_norm2 + qs * sizeof(float));
+  p.off_top = up(p.off_rot + qs * a.head_dim * sizeof(float));
+  p.workspace_bytes = up(p.off_top + qs * sizeof(float));
   return p;
 }
 
@@ -596,7 +596,7 @@ cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, cudaStream_t strea
   w.parts = p.parts;
   w.rows_per_window = p.cols / (a.num_q_heads / a.num_kv_heads);
   w.q_rot = reinterpret_cast<float*>(ws + p.off_rot);
-  w.q_norm2 = reinterpret_cast<float*>(ws + p.off_norm2);
+  w.q_top = reinterpret_cast<float*>(ws + p.off_top);
   if (p.tc) {
     // scale, log2 e, the rotation's 1 / sqrt(D) and the keys' alpha in one factor; scores with an
     // ordinary cap are taken as 2 log2(e) s / cap, whose power of two gives the tanh

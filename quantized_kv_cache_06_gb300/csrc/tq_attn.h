@@ -80,7 +80,7 @@ struct AttnPlan {
   bool tc;          // tensor-core kernel (else the SIMT kernel)
   int cols;         // (row, q head of the group) columns per CTA
   int parts;        // partitions of the tile list; grid = parts * kv heads
-  size_t off_windows, off_row_window, off_acc, off_ml, off_rot, off_norm2;
+  size_t off_windows, off_row_window, off_acc, off_ml, off_rot, off_top;
   size_t workspace_bytes;
 };
 
@@ -95,10 +95,10 @@ struct AttnWork {
   int* row_window;
   float* acc;  // [grid][2][cols][D]: piece 0 continues a window, piece 1 starts one that goes on
   float* ml;   // [grid][2][cols][2]
-  // tensor-core kernel: rotated queries R q * q_mul and their squared norms, [rows][q heads]; the
-  // rows of windows that one CTA finishes come back in their place, in rotated space
+  // tensor-core kernel: rotated queries R q * q_mul and their largest coordinates, [rows][q heads];
+  // the rows of windows that one CTA finishes come back in their place, in rotated space
   float* q_rot;
-  float* q_norm2;
+  float* q_top;
   float q_mul;
   int cols, parts, rows_per_window;
   int lead;  // where windows are many: places a window's start and end are worth

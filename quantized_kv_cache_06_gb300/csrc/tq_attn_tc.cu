@@ -21,8 +21,9 @@
 // near fp16 grid points).  One part for P' would hold twice the columns (tree 4 x 131072 0.73 ms),
 // at an error of one and a half times the output's own rounding.  bf16 outputs: one fp16 part
 // each, eight times finer than the output's own rounding.  The window's queries are scaled by one
-// power of two, and the weights p nu_v by another (moved when a larger norm arrives), so neither
-// large queries nor large norms leave the fp16 range.  Sums, maxima and both products are fp32.
+// power of two (by one each where their sizes differ much: no row is the worse for its neighbours),
+// and the weights p nu_v by another (moved when a larger norm arrives), so neither large queries nor
+// large norms leave the fp16 range.  Sums, maxima and both products are fp32.
 //
 // Softmax in base 2; the running max of a column moves only when a score passes it by 2^6, so
 // most tiles rescale nothing; when one does, the softmax warps scale O^T in TMEM themselves
@@ -86,6 +87,10 @@ constexpr int kNormSlack = 8;
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
 constexpr int kNoToken = -0x7fffffff - 1;  // the entry of a token that is not there: no block
 constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
+constexpr int kNoQuery = -1000;           // exponent of a query that is zero, not finite, or sees nothing
+// Binades by which a window's queries may differ under one power of two: the smallest keeps its
+// largest coordinate above 2 in fp16, an absolute error of 2^-25 (lo part) against it.
+constexpr int kQuerySpread = 8;
 
 template <int D, bool SPLIT, int N>
 struct Tc {
@@ -111,7 +116,8 @@ struct Tc {
   static constexpr int kOffRows = kOffP + kPBytes;                 // int4 (p0, p1, w0, w1)[kN], int2 (base, bits)[kN]
   // floats [kN]: -max, correction, slope; part [4][kN]
   static constexpr int kOffCol = kOffRows + (kN * (int)sizeof(RowSees) + 15) / 16 * 16;
-  static constexpr int kOffMeta = kOffCol + 7 * kN * 4;            // uint32 valid[kNorms][4], a bit per token
+  static constexpr int kOffQExp = kOffCol + 7 * kN * 4;            // int16 [kN]: exponents of the queries
+  static constexpr int kOffMeta = kOffQExp + kN * 2;               // uint32 valid[kNorms][4], a bit per token
   static constexpr int kOffNorm = kOffMeta + kNorms * 16;  // float2 (nu_k, nu_v) [kNorms][128]
   static constexpr int kOffTab = (kOffNorm + kNorms * kTok * 8 + 127) / 128 * 128;  // key and value tables, ring
   static constexpr int kRegsDequant = D == 256 ? 96 : 64;
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(8) uint64_t bars[kNorms + 27];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead, fail[2][2], fail_all;
-  __shared__ int full_lo_s, full_hi_s, pre_lo_s, pre_hi_s, q_exp;
+  __shared__ int full_lo_s, full_hi_s, pre_lo_s, pre_hi_s, q_low, q_high;
   unsigned char* smem = smem_raw + ((1024u - (smem_a(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_a(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -709,13 +715,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     float* corr_s = negm_s + C::kN;
     float* slope_s = corr_s + C::kN;
     float* part_s = slope_s + C::kN;  // [4][kN]
+    short* q_exp_s = reinterpret_cast<short*>(smem + C::kOffQExp);
     __shared__ int vpart[kSoftWarps], ve_s[2];
     const uint32_t* valid = reinterpret_cast<const uint32_t*>(smem + C::kOffMeta);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const float2* norms = reinterpret_cast<const float2*>(smem + C::kOffNorm);
     const uint32_t p_line = base + C::kOffP + (uint32_t)((t_lane >> 3) * 1024 + (t_lane & 7) * 128);
-    const bool capped = a.softcap > 0.f, biased = a.alibi != nullptr;
-    const bool folded = cap_folded(a.softcap);
+    const bool capped = cap_folded(a.softcap), far = a.softcap > 0.f && !capped, biased = a.alibi != nullptr;
     const float cap2 = a.softcap * kLog2eA, inv_cap2 = fminf(1.f / cap2, 3e38f);
     const float inv_av = 1.0f / (a.v_alpha * sqrtf((float)D));
     // 16 values of every lane to lane i's v[0], over all lanes, of value i % 16: halves of the values
@@ -741,12 +747,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int col0 = stream * pitch;                             // the stream's part of the column arrays
       const int bar_id = kBarSoft + 1 + stream, bar_n = 128 * sets;
       const uint32_t weight = (uint32_t)streams;  // arrivals of this warp where all softmax warps count
-      // ---- queries of the window, rotated already: one power of two for all of them, hi (and lo)
+      // ---- queries of the window, rotated already: scaled by powers of two, hi (and lo)
       if (stid == 0) {
         full_lo_s = pre_lo_s = 0;
         full_hi_s = pre_hi_s = 0x7fffffff;
-        q_exp = -1000;
+        q_low = 1000;
+        q_high = kNoQuery;
       }
+      const int64_t q_first = (int64_t)win.row0 * a.num_q_heads + h * G;  // (row, q head) of column 0
+      auto q_index = [&](int c) -> int64_t { return q_first + (int64_t)(c >> g_log) * a.num_q_heads + (c & (G - 1)); };
+      const float top = stid < cols ? w.q_top[q_index(stid)] : 0.f;  // (on its way with the row's lengths)
       soft_sync();
       if (stid < win.nrows) {
         const RowView v = row_view(a, win.row0 + stid);
@@ -757,20 +767,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         atomicMax(&pre_lo_s, v.p0);
         atomicMin(&pre_hi_s, v.p1);
       }
-      const int64_t q_first = (int64_t)win.row0 * a.num_q_heads + h * G;  // (row, q head) of column 0
-      auto q_index = [&](int c) -> int64_t { return q_first + (int64_t)(c >> g_log) * a.num_q_heads + (c & (G - 1)); };
+      soft_sync();
       if (stid < C::kN) {
         const int c = stid & (pitch - 1);
         negm_s[stid] = c < cols ? -kNoMax : -INFINITY;  // no column there: never a new max
         slope_s[stid] = biased && stid < cols ? a.alibi[h * G + (stid & (G - 1))] * kLog2eA : 0.f;
-        const float n2 = stid < cols ? w.q_norm2[q_index(stid)] : 0.f;
-        const int e = __reduce_max_sync(kFullMask, n2 < INFINITY ? (exp_of(n2) + 1) / 2 : -1000);
-        if (lane == 0) atomicMax(&q_exp, e);
+        // the largest coordinate to below 2^10; not of rows that see nothing, which may hold any bits
+        int e = kNoQuery;
+        if (stid < cols) {
+          const int4 v = row_spans[stid >> g_log];
+          if ((v.y > v.x || v.w > v.z || row_bits[stid >> g_log].y > 0) && top > 0.f && top < INFINITY)
+            e = max(exp_of(top) - 9, -126);
+        }
+        q_exp_s[stid] = (short)e;
+        const int high = __reduce_max_sync(kFullMask, e), low = __reduce_min_sync(kFullMask, e == kNoQuery ? 1000 : e);
+        if (lane == 0) {
+          atomicMax(&q_high, high);
+          atomicMin(&q_low, low);
+        }
       }
       soft_sync();
-      // the largest rotated coordinate is at most the norm times sqrt(D): to 2^10 or less
-      const int qe = q_exp + (D == 64 ? 3 : 4) - 10;
-      const float q_down = pow2i(max(-126, min(126, -qe))), q_up = pow2i(max(-126, min(126, qe)));
+      // One power of two for all of them, which a token's factor takes back; where their sizes differ
+      // by more than 2^kQuerySpread, so that the small ones would lose bits, one for each column, taken
+      // back where scores are changed.
+      const bool mixed = q_high - q_low > kQuerySpread;
+      const int qe = q_high == kNoQuery ? 0 : q_high;
+      auto q_exp_of = [&](int c) -> int {
+        const int e = mixed ? q_exp_s[c] : kNoQuery;
+        return e == kNoQuery ? qe : e;
+      };
+      const float q_up = mixed ? 1.f : pow2i(qe);
       const int full_lo = full_lo_s, full_hi = full_hi_s, pre_lo = pre_lo_s, pre_hi = pre_hi_s;
       constexpr int kAhead = 4;  // columns loaded together
       for (int col4 = sw; col4 < cols; col4 += kAhead * kSoftWarps) {
@@ -782,6 +808,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int e = 0; e < kAhead; ++e) {
           const int col = col4 + e * kSoftWarps;
           if (col >= cols) continue;
+          const float q_down = pow2i(-q_exp_of(col));
 #pragma unroll
           for (int i = 0; i < D / 32; i += 2) {
             const int d = lane * (D / 32) + i;
@@ -835,6 +862,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
         };
+        if (__builtin_expect(mixed || far, 0)) {
+          // a query's own power of two, caps out of the ordinary; what follows finds the scores
+          // like the others (a pass of its own, so that no code of it is among what runs often)
+#pragma unroll 1
+          for (int c0 = c_first; c0 < cols; c0 += c_step) {
+            uint32_t u[16];
+            tm_ld16(s_at + c0, u);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = __uint_as_float(u[i]) * kn * (mixed ? pow2i(q_exp_of(c0 + i)) : 1.f);
+              u[i] = __float_as_uint(far ? far_cap(x, cap2, inv_cap2) : x);
+            }
+            tm_st16(s_at + c0, u);
+          }
+          tm_wait_st();
+          kn = 1.f;
+        }
         bool seen = true;  // a column of this thread sees its token
         if (__builtin_expect(!all || capped || biased, 0)) {
           // Scores in place: nu_k, cap, distance, -inf where the token is not seen; what follows
@@ -848,17 +893,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fetch(c0, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], make_float2(kn, kn));
-            if (capped && folded) {
+            if (capped) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 x[i].x = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i].x)), cap2);
                 x[i].y = fmaf(-2.f * cap2, rcpa(1.f + ex2a(x[i].y)), cap2);
-              }
-            } else if (capped) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                x[i].x = far_cap(x[i].x, cap2, inv_cap2);
-                x[i].y = far_cap(x[i].y, cap2, inv_cap2);
               }
             }
             if (biased) {

@@ -148,3 +148,50 @@ def test_prompts_in_a_table_of_mostly_idle_rows(dtype, slots):
     dv = c.dev()
     out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, check=True)
     w.close(out, w.exact(q, q_seq, so.biased_visible(q_seq, q_len, c.cap, slots), **dv), dtype)
+
+
+@pytest.mark.parametrize("kind", ["plain", "cap", "slopes", "blind"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_of_very_different_sizes_in_a_window(d, dtype, kind):
+    # rows beside one with a query 2^40 times theirs, beside a padded one whose query is any bits and
+    # which sees nothing, beside one of NaN: each as if it were alone
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [300], d, 2, 4, 4)
+    q = torch.from_numpy(rng.standard_normal((7, 8, d)).astype(np.float32)).cuda()
+    q_len = np.array([300, 299, 300, 0, 298, 300, 200])
+    q[2] *= 0 if kind == "blind" else 2.0 ** 40
+    q[3] = 1e37
+    q[4] = math.nan if kind != "blind" else 0.5
+    q[6] *= 2.0 ** -30
+    kw = dict(softcap=20.0) if kind == "cap" else {}
+    slopes = torch.from_numpy(rng.uniform(0.0, 0.2, 8).astype(np.float32)).cuda() if kind == "slopes" else None
+    q_seq, dv = np.zeros(7, int), c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, check=True, out_dtype=w.DT[dtype],
+                                     alibi_slopes=slopes, **kw)
+    see = so.biased_visible(q_seq, q_len, c.cap, 1)
+    ref = w.exact(q, q_seq, see, **dv, slopes=slopes, q_pos=q_len - 1, **kw)
+    for row in (0, 1, 5, 6):
+        w.close(out, ref, dtype, rows=[row])
+    assert torch.all(out[3] == 0) and bool(torch.isfinite(out[2].float()).all())
+    assert kind == "blind" or bool(torch.isnan(out[4].float()).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_queries_whose_square_leaves_fp32(d, dtype):
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [60], d, 2, 4, 4)
+    q = torch.from_numpy(rng.standard_normal((2, 8, d)).astype(np.float32)).cuda() * 1e25
+    q_seq, dv = np.zeros(2, int), c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32([60, 59]), **dv, check=True, out_dtype=w.DT[dtype])
+    see = so.biased_visible(q_seq, [60, 59], c.cap, 1)
+    # one token has all the weight where the scores of the first two differ by more than they are off
+    want = w.exact(q, q_seq, see, **dv)[0]
+    almost = w.exact(q * 1e-25 * 3000, q_seq, see, **dv)[0]
+    sure = np.abs(want - almost).max(-1) < 1e-9
+    assert sure.sum() >= 4
+    err = np.abs(out.float().cpu().numpy() - want)[sure]
+    assert np.all(err <= 2.0 ** -7 * np.abs(want[sure]) + 2.0 ** -9 * np.abs(want[sure]).max())
