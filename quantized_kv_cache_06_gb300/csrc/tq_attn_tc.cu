@@ -21,18 +21,19 @@
 // near fp16 grid points).  One part for P' would hold twice the columns (tree 4 x 131072 0.73 ms),
 // at an error of one and a half times the output's own rounding.  bf16 outputs: one fp16 part
 // each, eight times finer than the output's own rounding.  The window's queries are scaled by one
-// power of two (by one each where their sizes differ much: no row is the worse for its neighbours),
-// and the weights p nu_v by another (moved when a larger norm arrives), so neither large queries nor
-// large norms leave the fp16 range.  Sums, maxima and both products are fp32.
+// power of two, by one each where their sizes differ much.  The weights that fp16 holds are products
+// p nu_v, so a column is taken relative to the largest product it has seen, not the largest p: no
+// query and no norm leaves the fp16 range, and no row is the worse for its neighbours' or for a
+// giant norm that has no weight in it.  Sums, maxima and both products are fp32.
 //
-// Softmax in base 2; the running max of a column moves only when a score passes it by 2^6, so
+// Softmax in base 2; the reference of a column moves only when a product passes its place by 2^6, so
 // most tiles rescale nothing; when one does, the softmax warps scale O^T in TMEM themselves
 // (the product before has completed by then).
 //
 // Roles of the warps: 0-3 keys, 4-7 values, 8-15 softmax (lane quadrant = warp % 4, in two
 // sets), 16 and 17 MMA issue (scores, values).  A window of more than half the MMA columns has
 // both sets on one tile, each with its groups of 16 columns; a smaller one makes two streams of
-// one set that take alternate tiles, each with its own maxima, sums and O^T, merged when the
+// one set that take alternate tiles, each with its own references, sums and O^T, merged when the
 // window ends: the chain of waits, TMEM reads and votes of one tile then hides behind the
 // other's.
 //
@@ -45,10 +46,10 @@
 // 0.71 ms, 0.39 PFLOP/s), nor the tensor pipe (an eighth busy).  A tile takes the softmax warps
 // 4700 cycles, 2900 of them in the weights of 128 columns; dequantisation and the products hide
 // behind that.  All roles together issue 11900 instructions a tile, half of the slots.  A window adds 45000 cycles (its
-// queries, a first tile's maxima, sums and outputs).  Twice the softmax warps, or a product and a
+// queries, a first tile's references, sums and outputs).  Twice the softmax warps, or a product and a
 // vote for each half of the columns, change nothing of a tile; code size does: five programs
 // share the instruction cache, and unrolling the two dequantisation loops costs a quarter (tree
-// 0.84 -> 1.03 ms).  Hence the rolled loops, the paths apart for changed scores and moved maxima,
+// 0.84 -> 1.03 ms).  Hence the rolled loops, the paths apart for changed scores and moved references,
 // and rows read word by word from shared memory (a tenth against holding them in registers).
 //
 // All waits are bounded: one that runs out records the timeout, every role leaves its loop, the
@@ -79,14 +80,21 @@ constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kRegsIssue = 64;
 constexpr int kMaxRing = 6;
 constexpr int kNorms = 6;  // tiles whose norms are kept: keys and values run at most five tiles ahead of the softmax
-constexpr float kSlack = 6.0f;            // log2 units the running max may lag
-constexpr float kMaxWeight = 64.0f;       // 2^kSlack
-// Binades a scaled value norm may reach: a weight of up to 2^6 times a norm below 2^9 stays below
-// 2^15; with one more their product could pass 65520, which fp16 rounds to infinity.
-constexpr int kNormSlack = 8;
+// A column's reference r: its weights are 2^(x - r), its products 2^(x - r) nu_v 2^-8.  When it is
+// set, the largest product goes to 2^kProductExp; it moves when one passes that by 2^kSlack, so 2^14
+// at most is written, well inside fp16.  A scaled norm counts as kNormLow or more, so that tokens of no
+// value cannot make weights that overflow the sums.  (The 2^-8 keeps the weights of norms of up to
+// 2^127 above the smallest float.)
+constexpr float kSlack = 6.0f, kProductExp = 8.0f;
+constexpr float kMaxProduct = 16384.0f;  // 2^(kProductExp + kSlack)
+constexpr float kNormScale = 0.00390625f, kNormUnscale = 256.0f;
+constexpr float kNormLow = 3.552713678800501e-15f;  // 2^-48: a norm of 2^-40
+// Where a token's factor is above this, scores could pass 2^24 (|S| is 2^15 at most): r would no longer
+// hold a product's exponent beside them, nor x kn - r its own rounding.
+constexpr float kLargeFactor = 512.0f;
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
 constexpr int kNoToken = -0x7fffffff - 1;  // the entry of a token that is not there: no block
-constexpr float kNoMax = -1e30f;          // running max of a column that has seen nothing
+constexpr float kNoMax = -1e30f;          // reference of a column that has seen nothing
 constexpr int kNoQuery = -1000;           // exponent of a query that is zero, not finite, or sees nothing
 // Binades by which a window's queries may differ under one power of two: the smallest keeps its
 // largest coordinate above 2 in fp16, an absolute error of 2^-25 (lo part) against it.
@@ -711,19 +719,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int t_lane = 32 * quad + lane;  // token of the tile (dim of the output)
     int4* row_spans = reinterpret_cast<int4*>(smem + C::kOffRows);             // p0, p1, w0, w1
     int2* row_bits = reinterpret_cast<int2*>(smem + C::kOffRows + C::kN * 16);  // base, bits
-    float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -max; -inf where there is no column
+    float* negm_s = reinterpret_cast<float*>(smem + C::kOffCol);  // -reference; -inf where there is no column
     float* corr_s = negm_s + C::kN;
     float* slope_s = corr_s + C::kN;
     float* part_s = slope_s + C::kN;  // [4][kN]
     short* q_exp_s = reinterpret_cast<short*>(smem + C::kOffQExp);
-    __shared__ int vpart[kSoftWarps], ve_s[2];
     const uint32_t* valid = reinterpret_cast<const uint32_t*>(smem + C::kOffMeta);
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const float2* norms = reinterpret_cast<const float2*>(smem + C::kOffNorm);
     const uint32_t p_line = base + C::kOffP + (uint32_t)((t_lane >> 3) * 1024 + (t_lane & 7) * 128);
     const bool capped = cap_folded(a.softcap), far = a.softcap > 0.f && !capped, biased = a.alibi != nullptr;
     const float cap2 = a.softcap * kLog2eA, inv_cap2 = fminf(1.f / cap2, 3e38f);
-    const float inv_av = 1.0f / (a.v_alpha * sqrtf((float)D));
+    const float inv_av = kNormUnscale / (a.v_alpha * sqrtf((float)D));
     // 16 values of every lane to lane i's v[0], over all lanes, of value i % 16: halves of the values
     // exchanged four times, 16 shuffles in all.
     auto over_lanes = [&](float (&v)[16], auto op) {
@@ -834,7 +841,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float2 l[C::kGroups * 8];
 #pragma unroll
       for (int i = 0; i < C::kGroups * 8; ++i) l[i] = make_float2(0.f, 0.f);
-      int ve = -1000;  // P' = p nu_v 2^-ve (every thread of the stream holds the same)
       bool broken = false;
       for (int k = 0; k < tiles; ++k) {
         const int sb = k & (2 * streams - 1), slot = it++ % kNorms;
@@ -862,9 +868,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
         };
-        if (__builtin_expect(mixed || far, 0)) {
-          // a query's own power of two, caps out of the ordinary; what follows finds the scores
-          // like the others (a pass of its own, so that no code of it is among what runs often)
+        if (__builtin_expect(mixed || far || __any_sync(kFullMask, fabsf(kn) > kLargeFactor), 0)) {
+          // A query's own power of two, caps out of the ordinary, giant scores (rounded here, once, so
+          // that differences are exact); what follows finds the scores like the others (a pass of its own, so that no code of it is among what runs often)
 #pragma unroll 1
           for (int c0 = c_first; c0 < cols; c0 += c_step) {
             uint32_t u[16];
@@ -945,50 +951,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         const float2 kn2 = make_float2(kn, kn);
         const bool vfin = fabsf(vn) < INFINITY;
-        // a norm that counts for the weights' scale: finite, of a token some column here sees (a
-        // stale row may hold any bits)
-        const float vf = seen && real && vfin ? fabsf(vn) : 0.f;
+        const float vs = vfin ? vn * kNormScale : 0.f, vs_top = fmaxf(fabsf(vs), kNormLow);
         const uint32_t sx = (uint32_t)(t_lane & 7);
         auto p_addr = [&](int c) -> uint32_t { return p_line + (c >> 6) * (kTok * 128) + ((((c & 63) >> 3) ^ sx) << 4); };
         volatile int* fl = &fail[stream][(k / streams) & 1];
 
-        // The columns' maxima over the tile, and the scale of the weights by its largest norm; where
-        // `sums`, the tile's weights taken back out of the sums (a weight that moves a maximum
-        // leaves a rounding of itself, scaled away with it; an infinite one leaves nothing of the sum
-        // either), which go to the new maxima with O^T.  Little code, as it runs seldom and then
-        // comes from far: with a reduction per column and both passes unrolled it took 20 us a window.
-        auto move_maxima = [&](bool sums) {
+        // The columns' references by the tile's largest products; where `sums`, the tile's weights
+        // taken back out of the sums (a weight that moves a reference leaves a rounding of itself,
+        // scaled away with it; an infinite one leaves nothing of the sum either), which go to the
+        // new references with O^T.  Little code, as it runs seldom and then comes from far: with a
+        // reduction per column and both passes unrolled it took 20 us a window.
+        auto move_references = [&](bool sums) {
+          // (rounded up throughout: a product may come out smaller for it, never too large)
+          const float lv = __log2f(vs_top);
 #pragma unroll 1
           for (int c0 = c_first; c0 < cols; c0 += c_step) {
             float2 x[8];
             float v[16];
             fetch(c0, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[2 * i] = x[i].x * kn, v[2 * i + 1] = x[i].y * kn;
+            for (int i = 0; i < 8; ++i) v[2 * i] = __fmaf_ru(x[i].x, kn, lv), v[2 * i + 1] = __fmaf_ru(x[i].y, kn, lv);
             over_lanes(v, [](float m, float n) { return fmaxf(m, n); });
             if (lane < 16) part_s[quad * C::kN + col0 + c0 + lane] = v[0];
           }
-          const int vmax = __reduce_max_sync(kFullMask, __float_as_int(vf));
-          if (lane == 0) vpart[sw] = vmax;
           named_sync(bar_id, bar_n);
-          int vall = 0;
-          for (int i = 0; i < 4 * sets; ++i) vall = max(vall, vpart[4 * sets * stream + i]);
-          float vscale = 1.f;
-          if (vall > 0) {
-            const int e = exp_of(__int_as_float(vall));
-            if (e - ve > kNormSlack) {  // the largest norm so far to 2^6
-              const int ne = e - 6;
-              vscale = ve == -1000 ? 1.f : pow2i(max(-126, ve - ne));
-              ve = ne;
-            }
-          }
           const int c = stid - 128 * sets * stream;  // a column for each thread of the stream
           if (c < cols) {
             float top = part_s[col0 + c];
 #pragma unroll
             for (int i = 1; i < 4; ++i) top = fmaxf(top, part_s[i * C::kN + col0 + c]);
             const float old = -negm_s[col0 + c];
-            const bool up = top > old + kSlack;
+            top = __fadd_ru(top, -kProductExp);
+            const bool up = top - old > kSlack;
             corr_s[col0 + c] = up ? ex2a(old - top) : 1.f;
             if (up) negm_s[col0 + c] = -top;
           }
@@ -1021,19 +1015,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tm_ld16(at, u);
               tm_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * (corr_s[col0 + c0 + i] * vscale));
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * corr_s[col0 + c0 + i]);
               tm_st16(at, u);
             }
           }
           tm_wait_st();
         };
 
-        // Weights with the running maxima as they are; when a column's has to move (or the values'
-        // scale), the tile is taken once more with the new ones.  A first tile has none yet.
+        // Weights with the references as they are; when a column's has to move, the tile is taken
+        // once more with the new ones.  A first tile has none yet.
         bool moved = k < streams, waited = false;
         for (;;) {
-          if (__builtin_expect(moved, 0)) move_maxima(k >= streams);
-          const float vs = vf > 0.f ? vn * pow2i(max(-126, min(126, -ve))) : 0.f;
+          if (__builtin_expect(moved, 0)) move_references(k >= streams);
           const float2 vs2 = make_float2(vs, vs);
           float over = 0.f;  // largest weight
 #pragma unroll
@@ -1075,7 +1068,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool first_pass = !waited;
           waited = true;
           if (!first_pass) break;
-          const bool move = !moved && (over > kMaxWeight || (vf > 0.f && exp_of(vf) - ve > kNormSlack));
+          const bool move = !moved && over * vs_top > kMaxProduct;
           if (__builtin_expect(!named_any(bar_id, bar_n, move || !ok), 1)) break;
           if (*fl) {  // the same for all warps of the stream
             broken = true;
@@ -1126,7 +1119,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         over_lanes(v, [](float m, float n) { return m + n; });
         if (lane < 16) part_s[quad * C::kN + col0 + c0 + lane] = v[0];
       }
-      if (lane == 0 && (sw % (4 * sets)) == 0) ve_s[stream] = ve == -1000 ? 0 : ve;
       soft_sync();
       if (*(volatile int*)&fail_all) return false;
       tc_after();
@@ -1141,8 +1133,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         const float sum = fa * sum4(stid) + (live > 1 ? fb * sum4(pitch + stid) : 0.f);
         const float f = !whole ? inv_av : sum != 0.f ? inv_av / sum : 0.f;
-        corr_s[stid] = fa * f * pow2i(max(-126, min(126, ve_s[0])));
-        if (live > 1) corr_s[pitch + stid] = fb * f * pow2i(max(-126, min(126, ve_s[1])));
+        corr_s[stid] = fa * f;
+        if (live > 1) corr_s[pitch + stid] = fb * f;
         if (!whole) {
           w.ml[2 * (slot0 + stid)] = top;
           w.ml[2 * (slot0 + stid) + 1] = sum;

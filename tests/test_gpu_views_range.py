@@ -195,3 +195,67 @@ def test_queries_whose_square_leaves_fp32(d, dtype):
     assert sure.sum() >= 4
     err = np.abs(out.float().cpu().numpy() - want)[sure]
     assert np.all(err <= 2.0 ** -7 * np.abs(want[sure]) + 2.0 ** -9 * np.abs(want[sure]).max())
+
+
+@pytest.mark.parametrize("size", [3e5, 1e7, 1e8, 1e9, 1e12, 1e25])
+@pytest.mark.parametrize("n", [60, 300])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scores_of_any_size(d, dtype, n, size):
+    # from where fp32 still holds fractions of a score to where its steps pass any weight's exponent;
+    # masked tiles and whole ones
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [n], d, 2, 4, 4)
+    q = torch.from_numpy(rng.standard_normal((3, 8, d)).astype(np.float32)).cuda()
+    q_seq, q_len, dv = np.zeros(3, int), np.array([n, n - 1, n]), c.dev()
+    out = tq.tq_paged_prefill_biased(q * size, w.i32(q_seq), w.i32(q_len), **dv, check=True, out_dtype=w.DT[dtype])
+    # one token has all the weight where it leads by 30 / 300 of a unit query's scores: far more than the
+    # 6 * 2^-11 * 16 / sqrt(3 D) * 2 = 0.014 to 0.007 that roundings to fp16 take from them
+    see = so.biased_visible(q_seq, q_len, c.cap, 1)
+    want = w.exact(q * size, q_seq, see, **dv)[0]
+    sure = np.abs(want - w.exact(q * 300, q_seq, see, **dv)[0]).max(-1) < 1e-9
+    assert sure.sum() >= 8
+    got = out.float().cpu().numpy().astype(np.float64)[sure]
+    size = np.linalg.norm(want[sure], axis=-1, keepdims=True) / math.sqrt(d)
+    tol = w.HALF_STEP[dtype] * np.abs(want[sure]) + 6 * 2.0 ** -11 * size + 2.0 ** -11 * np.abs(want[sure])
+    assert np.all(np.isfinite(got)) and np.all(np.abs(got - want[sure]) <= tol)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("giant", [2.0 ** 25, 1e20, 1e30])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_beside_one_that_sees_a_giant_norm(d, giant, dtype):
+    # a drafted node with an enormous value norm that only its own row sees
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [150], d, 2, 4, 4)
+    _set_norm(c, 1, 0, 146, giant)
+    mask = np.array([[1], [2], [1 << 6], [5], [0]], dtype=np.uint32)
+    q = torch.from_numpy(rng.standard_normal((5, 8, d)).astype(np.float32)).cuda()
+    q_seq, dv = np.zeros(5, int), c.dev()
+    out = tq.tq_paged_tree(q, w.i32(q_seq), w.i32([140]), w.i32(mask.view(np.int32)), **dv, check=True,
+                           out_dtype=w.DT[dtype])
+    ref = w.exact(q, q_seq, so.tree_visible(q_seq, [140], mask, c.cap), **dv)
+    for row in (0, 1, 3, 4):
+        w.close(out, ref, dtype, rows=[row])
+    if dtype != "fp16":
+        w.close(out, ref, dtype, rows=[2])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("giant", [2.0 ** 25, 1e20, 1e30])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_giant_norm_without_weight(d, giant, dtype):
+    # the first token's value norm is enormous and its distance leaves it no weight
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [900], d, 2, 4, 4)
+    _set_norm(c, 1, 0, 0, giant)
+    q = torch.from_numpy(rng.standard_normal((2, 8, d)).astype(np.float32)).cuda()
+    slopes = torch.full((8,), 0.5, device="cuda")
+    q_seq, q_len, dv = np.zeros(2, int), np.array([899, 900]), c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, check=True, out_dtype=w.DT[dtype],
+                                     alibi_slopes=slopes)
+    see = so.biased_visible(q_seq, q_len, c.cap, 1)
+    w.close(out, w.exact(q, q_seq, see, **dv, slopes=slopes, q_pos=q_len - 1), dtype)
