@@ -89,8 +89,8 @@ constexpr float kSlack = 6.0f, kProductExp = 8.0f;
 constexpr float kMaxProduct = 16384.0f;  // 2^(kProductExp + kSlack)
 constexpr float kNormScale = 0.00390625f, kNormUnscale = 256.0f;
 constexpr float kNormLow = 3.552713678800501e-15f;  // 2^-48: a norm of 2^-40
-// Where a token's factor is above this, scores could pass 2^24 (|S| is 2^15 at most): r would no longer
-// hold a product's exponent beside them, nor x kn - r its own rounding.
+// Where a token's factor is above this, scores could pass 2^24 (|S| is 2^15 at most) and the rounding
+// of x kn a weight's exponent: such tiles are changed in place first, which rounds them once.
 constexpr float kLargeFactor = 512.0f;
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
 constexpr int kNoToken = -0x7fffffff - 1;  // the entry of a token that is not there: no block
@@ -804,6 +804,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return e == kNoQuery ? qe : e;
       };
       const float q_up = mixed ? 1.f : pow2i(qe);
+      const bool cold = mixed || far, always = capped || biased || cold;
       const int full_lo = full_lo_s, full_hi = full_hi_s, pre_lo = pre_lo_s, pre_hi = pre_hi_s;
       constexpr int kAhead = 4;  // columns loaded together
       for (int col4 = sw; col4 < cols; col4 += kAhead * kSoftWarps) {
@@ -868,26 +869,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
         };
-        if (__builtin_expect(mixed || far || __any_sync(kFullMask, fabsf(kn) > kLargeFactor), 0)) {
-          // A query's own power of two, caps out of the ordinary, giant scores (rounded here, once, so
-          // that differences are exact); what follows finds the scores like the others (a pass of its own, so that no code of it is among what runs often)
-#pragma unroll 1
-          for (int c0 = c_first; c0 < cols; c0 += c_step) {
-            uint32_t u[16];
-            tm_ld16(s_at + c0, u);
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x = __uint_as_float(u[i]) * kn * (mixed ? pow2i(q_exp_of(c0 + i)) : 1.f);
-              u[i] = __float_as_uint(far ? far_cap(x, cap2, inv_cap2) : x);
-            }
-            tm_st16(s_at + c0, u);
-          }
-          tm_wait_st();
-          kn = 1.f;
-        }
         bool seen = true;  // a column of this thread sees its token
-        if (__builtin_expect(!all || capped || biased, 0)) {
+        if (__builtin_expect(always || !all || __any_sync(kFullMask, fabsf(kn) > kLargeFactor), 0)) {
+          if (__builtin_expect(cold, 0)) {
+            // a query's own power of two, caps out of the ordinary; what follows finds the scores
+            // like the others (a pass of its own, so that no code of it is among what runs often)
+#pragma unroll 1
+            for (int c0 = c_first; c0 < cols; c0 += c_step) {
+              uint32_t u[16];
+              tm_ld16(s_at + c0, u);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float x = __uint_as_float(u[i]) * kn * (mixed ? pow2i(q_exp_of(c0 + i)) : 1.f);
+                u[i] = __float_as_uint(far ? far_cap(x, cap2, inv_cap2) : x);
+              }
+              tm_st16(s_at + c0, u);
+            }
+            tm_wait_st();
+            kn = 1.f;
+          }
           // Scores in place: nu_k, cap, distance, -inf where the token is not seen; what follows
           // takes them with a factor of one.  (A loop apart, so that plain tiles keep their code
           // together in the instruction cache.)
