@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) attn_simt_kernel(AttnArgs a, 
         if (see) {
           x = dot[m] * kn_s[lane];
           if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-          if (a.alibi) x -= a.alibi[h * G + col % G] * fabsf((float)(a.q_len[row] - 1 - tok));
+          if (a.alibi) x -= a.alibi[h * G + col % G] * fabsf((float)(view[col].base - tok));
           x *= kAttnLog2e;
         }
         if (!__any_sync(kFullMask, see)) continue;

@@ -134,8 +134,8 @@ __device__ __forceinline__ RowView row_view(const AttnArgs& a, int i) {
   if (a.q_len) {
     int len = a.q_len[i];
     v.bad = len < 0 || len > cap;
-    v.base = len - 1;
     len = min(max(len, 0), cap);
+    v.base = len - 1;
     const int doc = a.doc_starts ? max(a.doc_starts[i], 0) : 0;
     v.w1 = len;
     v.w0 = max(a.window > 0 ? max(0, len - a.window) : 0, doc);

@@ -259,3 +259,38 @@ def test_a_giant_norm_without_weight(d, giant, dtype):
                                      alibi_slopes=slopes)
     see = so.biased_visible(q_seq, q_len, c.cap, 1)
     w.close(out, w.exact(q, q_seq, see, **dv, slopes=slopes, q_pos=q_len - 1), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+def test_lengths_far_beyond_the_table_with_a_distance_bias(dtype):
+    # such a length is clamped to the table row, and so is the position that the bias counts from
+    tq = _tq()
+    rng = np.random.default_rng(8)
+    c = Cache(rng, [96, 96], 128, 2, 4, 4)
+    q = torch.from_numpy(rng.standard_normal((4, 8, 128)).astype(np.float32)).cuda().to(w.DT[dtype])
+    q_seq, q_len, prefix = np.array([0, 0, 1, 1]), np.array([2 ** 30, 96, 2 ** 31 - 1, -2 ** 31]), np.array([5, 60])
+    slopes = torch.from_numpy(rng.uniform(0.1, 0.4, 8).astype(np.float32)).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dv = c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, status=status, alibi_slopes=slopes,
+                                     prefix_lens=w.i32(prefix))
+    assert int(status.item()) == tq.TQ_ERR_INVALID_ARG
+    held = np.clip(q_len, 0, c.cap)
+    see = so.biased_visible(q_seq, held, c.cap, 2, prefix_lens=prefix)
+    w.close(out, w.exact(q, q_seq, see, **dv, slopes=slopes, q_pos=held - 1), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("d", [16, 64, 128, 256])
+def test_queries_and_outputs_at_any_element(d, dtype):
+    # views that start one element behind a 16-byte boundary, and nothing written beside the output
+    tq = _tq()
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [200, 90], d, 2, 4, 4)
+    flat = torch.from_numpy(rng.standard_normal(5 * 8 * d + 1).astype(np.float32)).cuda().to(w.DT[dtype])
+    q = flat[1:].view(5, 8, d)
+    hold = torch.full((5 * 8 * d + 2,), 7.0, device="cuda", dtype=w.DT[dtype])
+    q_seq, q_len, dv = np.array([0, 0, 1, 1, 1]), np.array([200, 3, 90, 89, 0]), c.dev()
+    out = tq.tq_paged_prefill_biased(q, w.i32(q_seq), w.i32(q_len), **dv, out=hold[1:-1].view(5, 8, d), check=True)
+    assert float(hold[0]) == 7 and float(hold[-1]) == 7
+    w.close(out, w.exact(q, q_seq, so.biased_visible(q_seq, q_len, c.cap, 2), **dv), dtype)
