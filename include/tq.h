@@ -501,7 +501,7 @@ tq_status tq_plan_step(const int32_t* seq_lens, const int32_t* new_lens, const i
  *                     the first path_lens[s] entries.
  *   seq_lens_out      device int32[num_seqs]; may be ctx_lens.
  *   status_dev        device int32 or NULL: 0; TQ_ERR_INVALID_ARG for a sequence whose path is
- *                     not ascending, or whose lengths leave the table or max_path (nothing of
+ *                     not ascending, or whose lengths leave the table, 2^31 - 1 or max_path (nothing of
  *                     it moves, its length stays ctx_lens[s]); TQ_ERR_BLOCK_OUT_OF_RANGE for a
  *                     block id outside [0, num_blocks) (that row does not move).
  *

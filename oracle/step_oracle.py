@@ -88,7 +88,7 @@ def commit_tree(pages, block_table, ctx_lens, path, path_lens):
     new lengths.  A sequence whose path is not ascending or leaves its table stays as it is."""
     out = np.array(pages)
     nb, bs = out.shape[:2]
-    cap = block_table.shape[1] * bs
+    cap = min(block_table.shape[1] * bs, 2 ** 31 - 1)
     lens = np.array(ctx_lens, dtype=np.int32)
     for s in range(len(lens)):
         ctx, n = int(ctx_lens[s]), int(path_lens[s])

@@ -257,7 +257,7 @@ template <typename V>
 __global__ void __launch_bounds__(kCommitMaxThreads) commit_tree_kernel(CommitArgs a) {
   __shared__ int64_t src[kCommitChunk], dst[kCommitChunk];  // flat slots; -1: nothing to move
   const int s = blockIdx.x, tid = threadIdx.x, bs = a.block_size, threads = blockDim.x;
-  const int64_t cap = (int64_t)a.max_blocks_per_seq * bs;
+  const int64_t cap = min((int64_t)a.max_blocks_per_seq * bs, (int64_t)0x7fffffff);  // lengths are int32
   const int kcols = a.k_slab / (int)sizeof(V), vcols = a.v_slab / (int)sizeof(V);
   const int64_t ctx = a.ctx_lens[s];
   int n = a.path_lens[s];
