@@ -94,7 +94,7 @@ constexpr float kNormLow = 3.552713678800501e-15f;  // 2^-48: a norm of 2^-40
 constexpr float kLargeFactor = 512.0f;
 constexpr int kBarSoft = 1;               // named barrier of all softmax warps; 2, 3: of a stream
 constexpr int kNoToken = -0x7fffffff - 1;  // the entry of a token that is not there: no block
-constexpr float kNoMax = -1e30f;          // reference of a column that has seen nothing
+constexpr float kNoMax = -3e38f;          // reference of a column that has seen nothing: below any score
 constexpr int kNoQuery = -1000;           // exponent of a query that is zero, not finite, or sees nothing
 // Binades by which a window's queries may differ under one power of two: the smallest keeps its
 // largest coordinate above 2 in fp16, an absolute error of 2^-25 (lo part) against it.

@@ -197,7 +197,7 @@ def test_queries_whose_square_leaves_fp32(d, dtype):
     assert np.all(err <= 2.0 ** -7 * np.abs(want[sure]) + 2.0 ** -9 * np.abs(want[sure]).max())
 
 
-@pytest.mark.parametrize("size", [3e5, 1e7, 1e8, 1e9, 1e12, 1e25])
+@pytest.mark.parametrize("size", [3e5, 1e7, 1e8, 1e9, 1e12, 1e25, 1e34])
 @pytest.mark.parametrize("n", [60, 300])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("d", [64, 128, 256])
