@@ -13,13 +13,12 @@
 // Work split.  The schedule cuts the rows into windows (runs of one sequence, up to the
 // columns a CTA holds) and lists the 128-token tiles any row of a window sees; the list of
 // all windows' tiles is cut into equal parts, and CTA (part, kv head) takes one of them.  So
-// every CTA has the same number of tiles whatever the lengths, tiles that no row sees (outside
+// every CTA has as much to do whatever the lengths, tiles that no row sees (outside
 // a window or a document) are never read, and the CTAs of one part read the interleaved rows
 // of all heads at the same time, which keeps them in L2.  Where a CTA takes several windows, their
 // starts and ends count too (a prompt's first windows have a tile or two each, single tokens among
-// them many).  A window that lies in one part is
-// finished there; the pieces of the others are merged by the combine, in tile order, so the
-// result does not depend on timing.
+// them many).  A window that lies in one part is finished there; the pieces of the others are merged
+// by the combine, in tile order, so the result does not depend on timing.
 //
 // Three launches, the later two as programmatic dependents: the schedule (one CTA; for the
 // tensor-core kernel the other CTAs rotate the queries, one warp a row, which costs the attention
@@ -27,8 +26,8 @@
 //
 // The SIMT kernel below is the fp32 form: fp32 outputs, and head dims 16 and 32.  A warp owns four
 // columns; lane = token for the scores, lane = coordinate for the values.  It is bound by the
-// issue of its FMAs and shared-memory reads (64 tokens, 8 drafted, 16 / 2 heads: 41 us, most of it
-// the latency of one CTA's three steps of 32 tokens).
+// issue of its FMAs and shared-memory reads (64 tokens, 8 drafted, 16 / 2 heads: 41 us on the device,
+// 40 of them here: the latency of a CTA's window of four rows, three steps of 32 tokens).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>

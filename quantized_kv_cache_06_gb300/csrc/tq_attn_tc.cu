@@ -42,14 +42,14 @@
 // multiple of 4), up to six tiles deep, so no thread waits for another's copy.  TMA boxes of 16
 // rows x 80 bytes took ten cycles a row, 2700 a tile.
 //
-// What bounds it: not memory (64 x 8192 tokens: single tokens 0.25 ms, 1.1 TB/s; tree of 32 nodes
-// 0.71 ms, 0.39 PFLOP/s), nor the tensor pipe (an eighth busy).  A tile takes the softmax warps
-// 4700 cycles, 2900 of them in the weights of 128 columns; dequantisation and the products hide
-// behind that.  All roles together issue 11900 instructions a tile, half of the slots.  A window adds 45000 cycles (its
-// queries, a first tile's references, sums and outputs).  Twice the softmax warps, or a product and a
-// vote for each half of the columns, change nothing of a tile; code size does: five programs
-// share the instruction cache, and unrolling the two dequantisation loops costs a quarter (tree
-// 0.84 -> 1.03 ms).  Hence the rolled loops, the paths apart for changed scores and moved references,
+// What bounds it: not memory (64 x 8192 tokens: single tokens 0.24 ms, 1.2 TB/s; tree of 32 nodes
+// 0.66 ms, 0.42 PFLOP/s), nor the tensor pipe (a sixth busy).  One more tile of 128 columns takes
+// 2.6 us, of single tokens 1.7, most of it the softmax warps' in the weights; dequantisation and the
+// products hide behind that.  All roles together issue 11700 instructions a tile, half of the slots.
+// One more window of as many tiles takes 29 us and 4.6 (its queries, a first tile's references, masked
+// tiles, sums and outputs).  Twice the softmax warps, or a product and a vote for each half of the
+// columns, change nothing of a tile; code size does: five programs share the instruction cache, and
+// unrolling the two dequantisation loops cost a quarter (tree 0.84 -> 1.03 ms).  Hence the rolled loops, the paths apart for changed scores and moved references,
 // and rows read word by word from shared memory (a tenth against holding them in registers).
 //
 // All waits are bounded: one that runs out records the timeout, every role leaves its loop, the
@@ -1316,8 +1316,8 @@ bool attn_tc_supported(const AttnArgs& a) {
 constexpr int kFewCols = 32, kFewTotal = 2048;
 constexpr int most_cols(int d, bool split) { return d < 256 ? (split ? 64 : 128) : split ? 32 : 64; }
 
-// A window's start and end in tiles: 45000 cycles beside 4700 a tile where it is wide, 5 us beside 2
-// us where it is narrow.
+// A window's start and end in tiles: 29 us beside 2.6 a tile at 128 columns (less where it holds
+// fewer), 4.6 beside 1.7 where it is narrow.
 int attn_tc_lead(int cols) { return cols == kFewCols ? 3 : kAttnMaxLead; }
 
 int attn_tc_cols(const AttnArgs& a) {
