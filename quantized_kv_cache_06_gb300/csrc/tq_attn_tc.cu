@@ -122,7 +122,7 @@ struct Tc {
   static constexpr int kOffV = kOffQ + kQBytes;
   static constexpr int kOffP = kOffV + kVSlots * kVBytes;
   static constexpr int kOffRows = kOffP + kPBytes;                 // int4 (p0, p1, w0, w1)[kN], int2 (base, bits)[kN]
-  // floats [kN]: -max, correction, slope; part [4][kN]
+  // floats [kN]: -reference, correction, slope; part [4][kN]
   static constexpr int kOffCol = kOffRows + (kN * (int)sizeof(RowSees) + 15) / 16 * 16;
   static constexpr int kOffQExp = kOffCol + 7 * kN * 4;            // int16 [kN]: exponents of the queries
   static constexpr int kOffMeta = kOffQExp + kN * 2;               // uint32 valid[kNorms][4], a bit per token
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       soft_sync();
       if (stid < C::kN) {
         const int c = stid & (pitch - 1);
-        negm_s[stid] = c < cols ? -kNoMax : -INFINITY;  // no column there: never a new max
+        negm_s[stid] = c < cols ? -kNoMax : -INFINITY;  // no column there: never a new reference
         slope_s[stid] = biased && stid < cols ? a.alibi[h * G + (stid & (G - 1))] * kLog2eA : 0.f;
         // the largest coordinate to below 2^10; not of rows that see nothing, which may hold any bits
         int e = kNoQuery;
