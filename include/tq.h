@@ -25,7 +25,11 @@
  *   tq_paged_decode_prod    over them ("vLLM Reference Audit", MSE and QJL codecs).
  *   tq_plan_step            a step's block tables, slot map and row list from request
  *                           lengths, on the device ("vLLM Usage", Slot Mapping).
+ *   tq_norm_rope            norms of query and key heads and their position rotation;
+ *   tq_append_kv            the same on the way into the pages, with the values ("vLLM Usage",
+ *                           TQ Packed Page Contract: write_tq4_kv of a step's K and V).
  *   tq_paged_tree           attention of drafted tokens (a tree per sequence) over the pages;
+ *   tq_verify_tree          drafted tokens kept or refused by the target's probabilities;
  *   tq_commit_tree          the accepted ones' rows moved behind their context.
  *   tq_paged_prefill_biased prefill / decode with capped scores, a distance bias, a sliding
  *                           window, a bidirectional prefix, packed documents.
@@ -449,8 +453,9 @@ tq_status tq_paged_decode_recipe(const void* q, tq_dtype q_dtype, int batch, int
  * The pages fix how a token is addressed ("vLLM Usage", Slot Mapping; "Architecture",
  * PackedPageCache) and leave who fills the tables to the host framework.  The calls below do
  * it on the device, for an engine that drafts several tokens a step: tq_plan_step lays out a
- * step's rows, tq_write_kv (or _prod, _recipe) writes them, tq_paged_tree verifies drafted
- * tokens, tq_commit_tree keeps the accepted ones. */
+ * step's rows, tq_append_kv (or tq_norm_rope and tq_write_kv, _prod, _recipe) writes them,
+ * tq_paged_tree attends to them, tq_verify_tree keeps or refuses drafted tokens, tq_commit_tree
+ * moves the kept ones. */
 
 /* Plans one step: appends new_lens[s] tokens to every sequence, taking new blocks from a ring
  * of free ones, and returns the blocks of finished sequences to it.
@@ -571,6 +576,115 @@ tq_status tq_paged_prefill_biased(const void* q, tq_dtype q_dtype, int num_q_row
                                   const float* alibi_slopes, const float* signs, const float* k_centroids,
                                   const float* v_centroids, float scale, float softcap, void* out, tq_dtype out_dtype,
                                   void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/* cos / sin table of the position rotation, host: row p holds cos(p f_i) for i < rot_dim / 2,
+ * then sin(p f_i), with f_i = inv_freq_host[i], or base^(-2 i / rot_dim) where that is NULL.
+ * Angles in fp64, rounded once.
+ *   rot_dim        even, 2 .. 256
+ *   cos_sin_host   host float[num_positions][rot_dim]
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (rot_dim). */
+tq_status tq_build_rope(int rot_dim, int64_t num_positions, double base, const double* inv_freq_host,
+                        float* cos_sin_host);
+
+/* Norm of each query and key head and the position rotation, one pass, in fp32, rounded once:
+ *   x <- w x / sqrt(mean(x^2) + eps) over the head's channels, then (a, b) <- (a cos - b sin,
+ *   b cos + a sin) for the pairs of its first rot_dim channels: (i, i + rot_dim / 2), or
+ *   (2 i, 2 i + 1) with `interleaved`.
+ *
+ *   q, k           device, dtype rows of [heads][head_dim], token t at element t * stride: slices
+ *                  of one projection's output will do.  Either may be NULL (its heads 0).
+ *   q_out, k_out   device, the same type and layout; may be q and k themselves, with their strides.
+ *                  No other overlap.
+ *   q_weight, k_weight  device float[head_dim], 16-byte aligned, or NULL: no norm for that side
+ *   eps            >= 0
+ *   positions      device int32[num_tokens]: token t stands at positions[t] + position_offset
+ *                  (tq_plan_step's q_len with offset -1).  A negative position is a padding row:
+ *                  nothing of it is read or written.  NULL where cos_sin is NULL: no padding rows.
+ *   cos_sin        device float[num_positions][rot_dim] (tq_build_rope), or NULL: no rotation
+ *   rot_dim        even, 2 .. head_dim; channels behind it are not rotated
+ *   status_dev     device int32 or NULL: 0, or TQ_ERR_INVALID_ARG for a position >= num_positions
+ *                  (nothing of that token is written)
+ * One launch, asynchronous, graph-capturable; 16-byte aligned rows are faster.  Host-detected
+ * errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim), TQ_ERR_CUDA. */
+tq_status tq_norm_rope(const void* q, int64_t q_stride, int num_q_heads, const void* k, int64_t k_stride,
+                       int num_k_heads, tq_dtype dtype, int64_t num_tokens, int head_dim, const int32_t* positions,
+                       int position_offset, const float* cos_sin, int64_t num_positions, int rot_dim, int interleaved,
+                       const float* q_weight, const float* k_weight, float eps, void* q_out, int64_t q_out_stride,
+                       void* k_out, int64_t k_out_stride, int32_t* status_dev, void* stream);
+
+/* Appends a step's keys and values to the packed pages, and rotates its queries: tq_norm_rope on
+ * q and k, with the fp32 rows of k (not rounded in between) and the rows of v encoded at their
+ * slots as tq_write_kv encodes them.  One launch.
+ *
+ *   q, q_out       as tq_norm_rope; q may be NULL
+ *   k, v           as tq_norm_rope's inputs, num_kv_heads heads; either may be NULL
+ *   slots          device int64[num_tokens]; a negative slot's K and V are not written (its q is)
+ *   k_pages, v_pages  device, uint8[num_blocks][block_size][num_kv_heads][RB], 16-byte aligned
+ *   signs, k_centroids, v_centroids  as tq_write_kv
+ *   positions .. eps  as tq_norm_rope
+ *   status_dev     device int32 or NULL: 0; TQ_ERR_INVALID_ARG as tq_norm_rope (nothing of the
+ *                  token is written); TQ_ERR_SLOT_OUT_OF_RANGE for a slot >= num_blocks *
+ *                  block_size: its K and V are not written, other tokens' are (tq_write_kv
+ *                  writes none: it looks at every slot in a launch of its own first).
+ * Duplicate slots: which row stays is unspecified.  Asynchronous, graph-capturable; host-detected
+ * errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA. */
+tq_status tq_append_kv(const void* q, int64_t q_stride, int num_q_heads, void* q_out, int64_t q_out_stride,
+                       const void* k, int64_t k_stride, const void* v, int64_t v_stride, tq_dtype dtype,
+                       int64_t num_tokens, int num_kv_heads, int head_dim, const int64_t* slots, uint8_t* k_pages,
+                       int k_bits, uint8_t* v_pages, int v_bits, int64_t num_blocks, int block_size,
+                       const float* signs, const float* k_centroids, const float* v_centroids,
+                       const int32_t* positions, int position_offset, const float* cos_sin, int64_t num_positions,
+                       int rot_dim, int interleaved, const float* q_weight, const float* k_weight, float eps,
+                       int32_t* status_dev, void* stream);
+
+/* Workspace bytes of tq_verify_tree; 0 when the arguments are invalid. */
+size_t tq_verify_tree_workspace(int num_rows, int vocab_size, int num_seqs);
+
+/* Keeps or refuses drafted tokens by the target's probabilities, from given random numbers, and
+ * draws the token that follows.  Rows row_start[s] .. row_start[s + 1] - 1 are the nodes of
+ * sequence s: node 0 is the last token of the sequence (always kept), the others are drafted, each
+ * behind an earlier node.  Row i's logits are the target's for the token behind node i, p their
+ * softmax at the sequence's temperature.  A token drawn with number u from weights w is the first
+ * i with w_0 + .. + w_i > u * (sum of w); at temperature 0 it is the first largest logit.
+ *
+ *   draft_probs NULL  a token is drawn from p with u_sample of the node's row; the walk goes on
+ *                     to the first child that carries it, or ends with that token.
+ *   draft_probs given q, row i: what the children of node i were drawn from, independently.  Child
+ *                     x, in node order, is kept when u_accept * q(x) < r(x), r = p at first; refused,
+ *                     r becomes max(r - q, 0) over its sum (left as it is where nothing remains).  All
+ *                     refused (or none there): a token is drawn from r with u_sample of the row.
+ *                     At temperature 0 a child is kept when it carries the first largest logit.
+ *
+ *   logits         device, logits_dtype rows of vocab_size, row i at element i * logits_stride.
+ *                  -inf and NaN have no probability.
+ *   draft_probs    device, draft_dtype rows as logits, or NULL; negative numbers and NaN count as 0
+ *   row_start      device int32[num_seqs + 1], ascending (tq_plan_step's); rows behind the last
+ *                  are not read.  A sequence may have none.
+ *   tokens         device int32[num_rows], tokens of the nodes (node 0's is not read).  One outside
+ *                  [0, vocab_size) is never kept, and nothing is subtracted for it.
+ *   parents        device int32[num_rows], the node (in its sequence) that node i is behind, less
+ *                  than i (node 0's is not read); NULL: node i is behind node i - 1
+ *   temperature    device float[num_seqs], 0 or in [2^-100, 2^100]; NULL: 1
+ *   u_accept       device float[num_rows], [0, 1), of the drafted nodes; only with draft_probs
+ *   u_sample       device float[num_rows], [0, 1)
+ *   path           device int32[num_seqs][max_path], max_path >= 1: the kept nodes, ascending, from
+ *                  node 0 (tq_commit_tree's path), then -1.  The walk ends at max_path nodes.
+ *   path_lens      device int32[num_seqs] (0 for a sequence without rows)
+ *   next_token     device int32[num_seqs]; -1 without rows, or without a distribution
+ *   workspace      device, >= tq_verify_tree_workspace(...) bytes, 256-byte aligned
+ *   status_dev     device int32 or NULL: 0, or TQ_ERR_INVALID_ARG for a temperature out of range
+ *                  (taken as 0), a parent that is no earlier node (the node is never kept), a
+ *                  row whose largest logit is not finite (the walk ends there, next_token -1), or a
+ *                  row_start that leaves [0, num_rows] or descends (taken as no rows).
+ * Sums that tokens are drawn by are 64-bit integers, weights fp32: the result does not depend on
+ * timing.  Two launches, asynchronous, graph-capturable (one workspace per call in flight);
+ * host-detected errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
+tq_status tq_verify_tree(const void* logits, tq_dtype logits_dtype, int64_t logits_stride, int num_rows,
+                         int vocab_size, const void* draft_probs, tq_dtype draft_dtype, int64_t draft_stride,
+                         const int32_t* row_start, int num_seqs, const int32_t* tokens, const int32_t* parents,
+                         const float* temperature, const float* u_accept, const float* u_sample, int32_t* path,
+                         int max_path, int32_t* path_lens, int32_t* next_token, void* workspace,
+                         size_t workspace_bytes, int32_t* status_dev, void* stream);
 
 #ifdef __cplusplus
 }

@@ -102,6 +102,15 @@ SIGNATURES = {
     "tq_paged_prefill_biased": (_c_int, [_c_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_p, _c_int, _c_p, _c_int,
                                          _c_i64, _c_int, _c_p, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p, _c_int, _c_p,
                                          _c_p, _c_p, _c_p, _c_f, _c_f, _c_p, _c_int, _c_p, _c_sz, _c_p, _c_p]),
+    "tq_build_rope": (_c_int, [_c_int, _c_i64, ctypes.c_double, _c_p, _c_p]),
+    "tq_norm_rope": (_c_int, [_c_p, _c_i64, _c_int, _c_p, _c_i64, _c_int, _c_int, _c_i64, _c_int, _c_p, _c_int, _c_p,
+                              _c_i64, _c_int, _c_int, _c_p, _c_p, _c_f, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p]),
+    "tq_append_kv": (_c_int, [_c_p, _c_i64, _c_int, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_int, _c_i64, _c_int,
+                              _c_int, _c_p, _c_p, _c_int, _c_p, _c_int, _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p, _c_int,
+                              _c_p, _c_i64, _c_int, _c_int, _c_p, _c_p, _c_f, _c_p, _c_p]),
+    "tq_verify_tree_workspace": (_c_sz, [_c_int, _c_int, _c_int]),
+    "tq_verify_tree": (_c_int, [_c_p, _c_int, _c_i64, _c_int, _c_int, _c_p, _c_int, _c_i64, _c_p, _c_int, _c_p, _c_p,
+                                _c_p, _c_p, _c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_sz, _c_p, _c_p]),
 }
 
 _lib = None
@@ -939,3 +948,236 @@ def tq_paged_prefill_biased(q: torch.Tensor, q_seq: torch.Tensor, q_len: torch.T
                       v_centroids, out, out_dtype, workspace, status, check, more,
                       (q_len.data_ptr(), _ptr(prefix_lens), _ptr(doc_starts), int(window), _ptr(alibi_slopes)),
                       (float(scale or 0.0), float(softcap)), lib().tq_paged_prefill_biased)
+
+
+# ---------------------------------------------------------------- norms, position rotation, append
+
+def tq_build_rope(rot_dim: int, num_positions: int, base: float = 10000.0, inv_freq: torch.Tensor | None = None,
+                  device=None) -> torch.Tensor:
+    """cos / sin table float32 [num_positions, rot_dim]: rot_dim / 2 cosines of position *
+    inv_freq[i] (base^(-2 i / rot_dim) by default), then the sines."""
+    if inv_freq is not None:
+        inv_freq = torch.as_tensor(inv_freq).to(torch.float64).contiguous().cpu()
+        if inv_freq.numel() * 2 != int(rot_dim):
+            raise ValueError(f"tq_build_rope: inv_freq must hold rot_dim / 2 = {int(rot_dim) // 2} values")
+    out = torch.empty(max(0, int(num_positions)), max(0, int(rot_dim)), dtype=torch.float32)
+    _check(lib().tq_build_rope(int(rot_dim), int(num_positions), float(base), _ptr(inv_freq), out.data_ptr()))
+    return out if device is None else out.to(device)
+
+
+def _head_rows(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, index: int, tokens: int, heads: int, d: int):
+    """(pointer, token stride) of head rows t[tokens, heads, d] whose heads are contiguous."""
+    if t.get_device() != index:
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device ({what} is on {t.device})")
+    if t.dtype is not dtype or t.shape != (tokens, heads, d):
+        raise ValueError(f"{name}: {what} must be {dtype} {[tokens, heads, d]}, got {t.dtype} {list(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError(f"{name}: the heads of a token of {what} must be contiguous")
+    return t.data_ptr(), (st[0] if tokens > 1 else heads * d)
+
+
+def _rope_args(name: str, index: int, tokens: int, d: int, positions, position_offset, cos_sin, interleaved, q_weight,
+               k_weight, eps):
+    f32, rows, rot = torch.float32, 0, 0
+    if positions is not None:
+        _need_like(name, index, positions=(positions, torch.int32, (tokens,)))
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions is None:
+            raise ValueError(f"{name}: cos_sin [P, rot_dim] comes with positions [T]")
+        rows, rot = cos_sin.shape
+        _need_like(name, index, cos_sin=(cos_sin, f32, (rows, rot)))
+    for what, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need_like(name, index, **{what: (w, f32, (d,))})
+    return (_ptr(positions), int(position_offset), _ptr(cos_sin), rows, rot, int(bool(interleaved)), _ptr(q_weight),
+            _ptr(k_weight), float(eps))
+
+
+def tq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
+                 cos_sin: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                 position_offset: int = 0, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None, check: bool = False):
+    """Norm (weights [D], or none) of every head of q[T, Hq, D] and k[T, H, D], then the rotation by
+    the table row of positions[t] + position_offset.  q and k may be slices of one projection's output
+    (any token stride), q_out and k_out q and k themselves.  A token at a negative position is left
+    out.  Returns (q_out, k_out)."""
+    name = "tq_norm_rope"
+    x = q if q is not None else k
+    if x is None or x.dim() != 3 or x.dtype not in _DTYPES:
+        raise ValueError(f"{name}: q [T, Hq, D] or k [T, H, D], f32/f16/bf16, expected")
+    t, _, d = x.shape
+    dev, dtype, index = x.device, x.dtype, x.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {dev})")
+    args = []
+    outs = []
+    for what, rows, out in (("q", q, q_out), ("k", k, k_out)):
+        if rows is None:
+            args.append((None, 0, 0, None, 0))
+            outs.append(None)
+            continue
+        if rows.dim() != 3:
+            raise ValueError(f"{name}: {what} [T, heads, D] expected")
+        h = rows.shape[1]
+        if out is None:
+            out = torch.empty((t, h, d), dtype=dtype, device=dev)
+        args.append((*_head_rows(name, what, rows, dtype, index, t, h, d), h,
+                     *_head_rows(name, what + "_out", out, dtype, index, t, h, d)))
+        outs.append(out)
+    rope = _rope_args(name, index, t, d, positions, position_offset, cos_sin, interleaved, q_weight, k_weight, eps)
+    _need_status(name, status, dev)
+    if status is None and check:
+        status = _status_buffer(dev)
+    (qp, qs, hq, qo, qos), (kp, ks, h, ko, kos) = args
+    with _on(index):
+        code = lib().tq_norm_rope(qp, qs, hq, kp, ks, h, _DTYPES[dtype], t, d, *rope, qo, qos, ko, kos, _ptr(status),
+                                  _stream_ptr(index))
+    if code != TQ_OK:
+        _check(code)
+    if check:
+        raise_for_device_status(status)
+    return outs[0], outs[1]
+
+
+def tq_append_kv(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
+                 k_pages: torch.Tensor | None, v_pages: torch.Tensor | None, slots: torch.Tensor, signs: torch.Tensor,
+                 k_centroids: torch.Tensor | None, v_centroids: torch.Tensor | None,
+                 positions: torch.Tensor | None = None, cos_sin: torch.Tensor | None = None,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, position_offset: int = 0, q_out: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None, check: bool = False) -> torch.Tensor | None:
+    """tq_norm_rope of q[T, Hq, D] and k[T, H, D] with the keys and the values v[T, H, D] encoded into
+    pages[NB, bs, H, RB] at slots[T] (negative: not written), one launch.  q, k or v may be None
+    (with its pages and centroids).  Returns q_out.  With check=True the call synchronises and raises
+    TQError for a slot or a position out of range (other tokens have been written)."""
+    name = "tq_append_kv"
+    x = q if q is not None else k if k is not None else v
+    if x is None or x.dim() != 3 or x.dtype not in _DTYPES:
+        raise ValueError(f"{name}: q [T, Hq, D], k, v [T, H, D], f32/f16/bf16, expected")
+    t, _, d = x.shape
+    dev, dtype, index = x.device, x.dtype, x.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {dev})")
+    _need_like(name, index, slots=(slots, torch.int64, (t,)), signs=(signs, torch.float32, (d,)))
+    qp, qs, hq, qo, qos = None, 0, 0, None, 0
+    if q is not None:
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((t, hq, d), dtype=dtype, device=dev)
+        qp, qs = _head_rows(name, "q", q, dtype, index, t, hq, d)
+        qo, qos = _head_rows(name, "q_out", q_out, dtype, index, t, hq, d)
+    shape = None
+    side = []
+    for what, rows, pages, cents in (("k", k, k_pages, k_centroids), ("v", v, v_pages, v_centroids)):
+        if rows is None:
+            side.append((None, 0, None, 0, None))
+            continue
+        if pages is None or cents is None or rows.dim() != 3 or pages.dim() != 4:
+            raise ValueError(f"{name}: {what} [T, H, D] comes with its pages [NB, bs, H, RB] and centroids")
+        bits = _bits_from_centroids(cents)
+        nb, bs, h, rb = pages.shape
+        if rb * 8 != d * bits + 32 or h != rows.shape[1] or (shape or (nb, bs, h)) != (nb, bs, h):  # D: a multiple of 16
+            raise ValueError(f"{name}: {what}_pages {list(pages.shape)} do not match {what} {list(rows.shape)} at {bits} bits")
+        shape = nb, bs, h
+        _need_like(name, index, **{what + "_pages": (pages, torch.uint8, (nb, bs, h, rb)),
+                                   what + "_centroids": (cents, torch.float32, (1 << bits,))})
+        side.append((*_head_rows(name, what, rows, dtype, index, t, h, d), pages.data_ptr(), bits, cents.data_ptr()))
+    nb, bs, h = shape or (0, 1, 1)
+    rope = _rope_args(name, index, t, d, positions, position_offset, cos_sin, interleaved, q_weight, k_weight, eps)
+    _need_status(name, status, dev)
+    if status is None and check:
+        status = _status_buffer(dev)
+    (kp, ks, kpg, kb, kc), (vp, vs, vpg, vb, vc) = side
+    with _on(index):
+        code = lib().tq_append_kv(qp, qs, hq, qo, qos, kp, ks, vp, vs, _DTYPES[dtype], t, h, d, slots.data_ptr(), kpg, kb,
+                                  vpg, vb, nb, bs, signs.data_ptr(), kc, vc, *rope, _ptr(status), _stream_ptr(index))
+    if code != TQ_OK:
+        _check(code)
+    if check:
+        raise_for_device_status(status)
+    return q_out
+
+
+# ---------------------------------------------------------------- verification of drafted tokens
+
+class Verified(NamedTuple):
+    """Outputs of tq_verify_tree."""
+    path: torch.Tensor        # int32 [S, max_path]: kept nodes, then -1
+    path_lens: torch.Tensor   # int32 [S]
+    next_token: torch.Tensor  # int32 [S]
+
+
+def tq_verify_tree_workspace(num_rows: int, vocab_size: int, num_seqs: int) -> int:
+    return int(lib().tq_verify_tree_workspace(num_rows, vocab_size, num_seqs))
+
+
+def _vocab_rows(name: str, what: str, t: torch.Tensor, index: int, shape: tuple):
+    """(pointer, row stride) of rows t[R, V] with contiguous elements."""
+    if t.get_device() != index:
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device ({what} is on {t.device})")
+    if t.dtype not in _DTYPES or t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: {what} must be f32/f16/bf16 rows {list(shape)} of contiguous elements, got {t.dtype} "
+                         f"{list(t.shape)}")
+    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
+
+
+def tq_verify_tree(logits: torch.Tensor, row_start: torch.Tensor, tokens: torch.Tensor, u_sample: torch.Tensor,
+                   max_path: int, parents: torch.Tensor | None = None, temperature: torch.Tensor | None = None,
+                   draft_probs: torch.Tensor | None = None, u_accept: torch.Tensor | None = None,
+                   out: Verified | None = None, workspace: torch.Tensor | None = None,
+                   status: torch.Tensor | None = None, check: bool = False) -> Verified:
+    """Keeps or refuses drafted tokens by the target's logits[R, V].  Rows row_start[s] ..
+    row_start[s + 1] - 1 are sequence s's nodes: node 0 its last token, the others drafted behind
+    parents (None: a chain).  temperature[S] 0: largest logits.  Without draft_probs a token is drawn
+    from every row with u_sample[R] and the path follows it; with draft_probs[R, V] (row i: what node
+    i's children were drawn from) a child is kept by u_accept[R], refused ones are subtracted.  The
+    result's path and path_lens are tq_commit_tree's; next_token follows the path."""
+    name = "tq_verify_tree"
+    if logits.dim() != 2 or row_start.dim() != 1 or row_start.numel() < 1:
+        raise ValueError(f"{name}: logits [R, V] and row_start [S + 1] expected")
+    r, vocab = logits.shape
+    s, max_path = row_start.numel() - 1, int(max_path)
+    dev, i32, f32, index = logits.device, torch.int32, torch.float32, logits.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {dev})")
+    if max_path < 1:
+        raise ValueError(f"{name}: max_path {max_path} < 1")
+    if (draft_probs is None) != (u_accept is None):
+        raise ValueError(f"{name}: draft_probs and u_accept come together")
+    lp, ls = _vocab_rows(name, "logits", logits, index, (r, vocab))
+    qp, qs, qt = None, 0, 0
+    if draft_probs is not None:
+        qp, qs = _vocab_rows(name, "draft_probs", draft_probs, index, (r, vocab))
+        qt = _DTYPES[draft_probs.dtype]
+        _need_like(name, index, u_accept=(u_accept, f32, (r,)))
+    _need_like(name, index, row_start=(row_start, i32, (s + 1,)), tokens=(tokens, i32, (r,)), u_sample=(u_sample, f32, (r,)))
+    if parents is not None:
+        _need_like(name, index, parents=(parents, i32, (r,)))
+    if temperature is not None:
+        _need_like(name, index, temperature=(temperature, f32, (s,)))
+    if out is None:
+        path, lens, after = torch.empty(s * (max_path + 2), dtype=i32, device=dev).split([s * max_path, s, s])
+        out = Verified(path.view(s, max_path), lens, after)
+    else:
+        _need_like(name, index, path=(out.path, i32, (s, max_path)), path_lens=(out.path_lens, i32, (s,)),
+                   next_token=(out.next_token, i32, (s,)))
+    _need_status(name, status, dev)
+    if status is None and check:
+        status = _status_buffer(dev)
+    with _on(index):
+        if workspace is None:
+            workspace = torch.empty(tq_verify_tree_workspace(r, vocab, s), dtype=torch.uint8, device=dev)
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"{name}: workspace must be contiguous on {dev}")
+        code = lib().tq_verify_tree(lp, _DTYPES[logits.dtype], ls, r, vocab, qp, qt, qs, row_start.data_ptr(), s,
+                                    tokens.data_ptr(), _ptr(parents), _ptr(temperature), _ptr(u_accept),
+                                    u_sample.data_ptr(), out.path.data_ptr(), max_path, out.path_lens.data_ptr(),
+                                    out.next_token.data_ptr(), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _ptr(status), _stream_ptr(index))
+    if code != TQ_OK:
+        _check(code)
+    if check:
+        raise_for_device_status(status)
+    return out

@@ -26,7 +26,7 @@ SOURCES = ["tq_api.cpp", "tq_write.cu", "tq_write_tc.cu", "tq_decode.cu", "tq_de
            "tq_decode_tc_f.cu", "tq_decode_tc_p.cu",
            "tq_decode_tc_q.cu", "tq_prefill_mq.cu",
            "tq_dequant.cu", "tq_qjl.cu", "tq_recipe.cu", "tq_query.cu", "tq_step.cu", "tq_attn.cu", "tq_attn_tc.cu",
-           "tq_small.cu"]
+           "tq_small.cu", "tq_append.cu", "tq_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

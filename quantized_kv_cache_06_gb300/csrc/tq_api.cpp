@@ -19,11 +19,13 @@
 #include <vector>
 
 #include "tq.h"
+#include "tq_append.h"
 #include "tq_attn.h"
 #include "tq_internal.h"
 #include "tq_qjl.h"
 #include "tq_recipe.h"
 #include "tq_step.h"
+#include "tq_verify.h"
 
 namespace {
 
@@ -416,6 +418,53 @@ tq_status write_with_own_status(const char* name, cudaStream_t stream, Launch la
     return fail(TQ_ERR_SLOT_OUT_OF_RANGE, "%s: a slot is >= num_blocks * block_size; no row was written", name);
   if (code != TQ_OK) return fail((tq_status)code, "%s: device status %d", name, (int)code);
   return ok();
+}
+
+// Shared by tq_norm_rope and tq_append_kv: types, positions, table and norms, into *out.
+tq_status rope_check(const char* name, tq_dtype dtype, int64_t num_tokens, int head_dim, const int32_t* positions,
+                     int position_offset, const float* cos_sin, int64_t num_positions, int rot_dim, int interleaved,
+                     const float* q_weight, const float* k_weight, float eps, tq::AppendArgs* out) {
+  if (num_tokens < 0 || num_positions < 0)
+    return fail(TQ_ERR_INVALID_ARG, "%s: invalid sizes (tokens=%lld, positions=%lld)", name, (long long)num_tokens,
+                (long long)num_positions);
+  if (!pow2_dim_ok(head_dim)) return fail(TQ_ERR_UNSUPPORTED, "head_dim %d: must be a power of two in [16, 256]", head_dim);
+  if (!dtype_ok(dtype)) return fail(TQ_ERR_INVALID_ARG, "%s: unknown dtype %d", name, (int)dtype);
+  if (cos_sin && (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2))
+    return fail(TQ_ERR_INVALID_ARG, "%s: rot_dim %d: must be even, 2 .. head_dim %d", name, rot_dim, head_dim);
+  if (cos_sin && !positions && num_tokens > 0) return fail(TQ_ERR_INVALID_ARG, "%s: a table needs positions", name);
+  if (!(eps >= 0.f && std::isfinite(eps))) return fail(TQ_ERR_INVALID_ARG, "%s: eps must be a number >= 0", name);
+  if (!aligned(positions, 4) || !aligned(cos_sin, 4) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return fail(TQ_ERR_INVALID_ARG, "%s: misaligned pointer (weights need 16-byte alignment)", name);
+  out->dtype = (int)dtype;
+  out->num_tokens = num_tokens;
+  out->head_dim = head_dim;
+  out->positions = positions;
+  out->position_offset = position_offset;
+  out->cos_sin = cos_sin;
+  out->num_positions = num_positions;
+  out->rot_dim = cos_sin ? rot_dim : 0;
+  out->interleaved = interleaved != 0;
+  out->q_weight = q_weight;
+  out->k_weight = k_weight;
+  out->eps = eps;
+  return TQ_OK;
+}
+
+// Dense rows of one side of tq_norm_rope (or the queries of tq_append_kv) and their output.
+tq_status rows_check(const char* name, const char* what, const void* in, int64_t stride, int heads, const void* out,
+                     int64_t out_stride, const tq::AppendArgs& a) {
+  if (heads < 0) return fail(TQ_ERR_INVALID_ARG, "%s: %s: %d heads", name, what, heads);
+  if (!in || heads == 0 || a.num_tokens == 0) return TQ_OK;
+  if (!out) return fail(TQ_ERR_INVALID_ARG, "%s: %s has no output", name, what);
+  const size_t size = dtype_size(a.dtype);
+  if (!aligned(in, size) || !aligned(out, size)) return fail(TQ_ERR_INVALID_ARG, "%s: %s: misaligned rows", name, what);
+  const int64_t row = (int64_t)heads * a.head_dim;
+  if (a.num_tokens > 1 && (stride < row || out_stride < row))
+    return fail(TQ_ERR_INVALID_ARG, "%s: %s: tokens %lld / %lld elements apart overlap", name, what, (long long)stride,
+                (long long)out_stride);
+  if (in == out && stride != out_stride && a.num_tokens > 1)
+    return fail(TQ_ERR_INVALID_ARG, "%s: %s in place needs one stride", name, what);
+  return TQ_OK;
 }
 
 }  // namespace
@@ -1113,6 +1162,174 @@ tq_status tq_paged_prefill_biased(const void* q, tq_dtype q_dtype, int num_q_row
   a.workspace = workspace;
   a.status = status_dev;
   return attn_impl("tq_paged_prefill_biased", a, workspace_bytes, q_len, stream);
+}
+
+tq_status tq_build_rope(int rot_dim, int64_t num_positions, double base, const double* inv_freq_host,
+                        float* cos_sin_host) {
+  if (num_positions < 0 || (num_positions > 0 && !cos_sin_host))
+    return fail(TQ_ERR_INVALID_ARG, "tq_build_rope: invalid table (%lld positions)", (long long)num_positions);
+  if (rot_dim < 2 || rot_dim > 256 || rot_dim % 2)
+    return fail(TQ_ERR_UNSUPPORTED, "tq_build_rope: rot_dim %d: must be even, 2 .. 256", rot_dim);
+  if (!inv_freq_host && !(base > 0.0 && std::isfinite(base)))
+    return fail(TQ_ERR_INVALID_ARG, "tq_build_rope: base must be a positive number");
+  const int half = rot_dim / 2;
+  double freq[128];
+  for (int i = 0; i < half; ++i) freq[i] = inv_freq_host ? inv_freq_host[i] : std::pow(base, -2.0 * i / rot_dim);
+  for (int64_t p = 0; p < num_positions; ++p) {
+    float* row = cos_sin_host + p * rot_dim;
+    for (int i = 0; i < half; ++i) {
+      row[i] = (float)std::cos((double)p * freq[i]);
+      row[half + i] = (float)std::sin((double)p * freq[i]);
+    }
+  }
+  return ok();
+}
+
+tq_status tq_norm_rope(const void* q, int64_t q_stride, int num_q_heads, const void* k, int64_t k_stride,
+                       int num_k_heads, tq_dtype dtype, int64_t num_tokens, int head_dim, const int32_t* positions,
+                       int position_offset, const float* cos_sin, int64_t num_positions, int rot_dim, int interleaved,
+                       const float* q_weight, const float* k_weight, float eps, void* q_out, int64_t q_out_stride,
+                       void* k_out, int64_t k_out_stride, int32_t* status_dev, void* stream) {
+  const char* name = "tq_norm_rope";
+  tq::AppendArgs a{};
+  tq_status st = rope_check(name, dtype, num_tokens, head_dim, positions, position_offset, cos_sin, num_positions,
+                            rot_dim, interleaved, q_weight, k_weight, eps, &a);
+  if (st != TQ_OK) return st;
+  st = rows_check(name, "q", q, q_stride, num_q_heads, q_out, q_out_stride, a);
+  if (st != TQ_OK) return st;
+  st = rows_check(name, "k", k, k_stride, num_k_heads, k_out, k_out_stride, a);
+  if (st != TQ_OK) return st;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.num_q_heads = q ? num_q_heads : 0;
+  a.q_out = q_out;
+  a.q_out_stride = q_out_stride;
+  a.k = k;
+  a.k_stride = k_stride;
+  a.num_k_heads = k ? num_k_heads : 0;
+  a.k_out = k_out;
+  a.k_out_stride = k_out_stride;
+  a.status = status_dev;
+  return check_cuda(tq::launch_append(a, static_cast<cudaStream_t>(stream)), name);
+}
+
+tq_status tq_append_kv(const void* q, int64_t q_stride, int num_q_heads, void* q_out, int64_t q_out_stride,
+                       const void* k, int64_t k_stride, const void* v, int64_t v_stride, tq_dtype dtype,
+                       int64_t num_tokens, int num_kv_heads, int head_dim, const int64_t* slots, uint8_t* k_pages,
+                       int k_bits, uint8_t* v_pages, int v_bits, int64_t num_blocks, int block_size,
+                       const float* signs, const float* k_centroids, const float* v_centroids,
+                       const int32_t* positions, int position_offset, const float* cos_sin, int64_t num_positions,
+                       int rot_dim, int interleaved, const float* q_weight, const float* k_weight, float eps,
+                       int32_t* status_dev, void* stream) {
+  const char* name = "tq_append_kv";
+  tq::AppendArgs a{};
+  tq_status st = rope_check(name, dtype, num_tokens, head_dim, positions, position_offset, cos_sin, num_positions,
+                            rot_dim, interleaved, q_weight, k_weight, eps, &a);
+  if (st != TQ_OK) return st;
+  st = rows_check(name, "q", q, q_stride, num_q_heads, q_out, q_out_stride, a);
+  if (st != TQ_OK) return st;
+  if (num_kv_heads < 1 || num_blocks < 0 || block_size < 1)
+    return fail(TQ_ERR_INVALID_ARG, "%s: invalid sizes (kv_heads=%d, blocks=%lld, block_size=%d)", name, num_kv_heads,
+                (long long)num_blocks, block_size);
+  struct Side {
+    const char* what;
+    const void* in;
+    int64_t stride;
+    uint8_t* pages;
+    int bits;
+    const float* centroids;
+  };
+  for (const Side& d : {Side{"k", k, k_stride, k_pages, k_bits, k_centroids}, Side{"v", v, v_stride, v_pages, v_bits, v_centroids}}) {
+    if (!d.in) continue;
+    if (!bits_ok(d.bits)) return fail(TQ_ERR_UNSUPPORTED, "%s: %s_bits %d: must be 2, 3, 4 or 5", name, d.what, d.bits);
+    if (num_tokens == 0) continue;
+    if (d.stride < (int64_t)num_kv_heads * head_dim && num_tokens > 1)
+      return fail(TQ_ERR_INVALID_ARG, "%s: %s: tokens %lld elements apart overlap", name, d.what, (long long)d.stride);
+    if (!slots || !d.pages || !signs || !d.centroids) return fail(TQ_ERR_INVALID_ARG, "%s: null pointer argument", name);
+    if (!aligned(d.in, dtype_size(dtype)) || !aligned(d.pages, 16) || !aligned(slots, 8) || !aligned(signs, 4) ||
+        !aligned(d.centroids, 4))
+      return fail(TQ_ERR_INVALID_ARG, "%s: misaligned pointer (pages need 16-byte alignment)", name);
+  }
+  a.q = q;
+  a.q_stride = q_stride;
+  a.num_q_heads = q ? num_q_heads : 0;
+  a.q_out = q_out;
+  a.q_out_stride = q_out_stride;
+  a.k = k;
+  a.k_stride = k_stride;
+  a.num_k_heads = k ? num_kv_heads : 0;
+  a.v = v;
+  a.v_stride = v_stride;
+  a.num_v_heads = v ? num_kv_heads : 0;
+  a.slots = slots;
+  a.num_slots = num_blocks * block_size;
+  a.k_pages = k ? k_pages : nullptr;
+  a.k_bits = k_bits;
+  a.v_pages = v ? v_pages : nullptr;
+  a.v_bits = v_bits;
+  a.signs = k || v ? signs : nullptr;
+  a.k_centroids = k_centroids;
+  a.v_centroids = v_centroids;
+  a.status = status_dev;
+  return check_cuda(tq::launch_append(a, static_cast<cudaStream_t>(stream)), name);
+}
+
+size_t tq_verify_tree_workspace(int num_rows, int vocab_size, int num_seqs) {
+  if (num_rows < 0 || vocab_size < 1 || num_seqs < 0) return 0;
+  return std::max<size_t>(256, tq::verify_workspace(num_rows, vocab_size, num_seqs));
+}
+
+tq_status tq_verify_tree(const void* logits, tq_dtype logits_dtype, int64_t logits_stride, int num_rows,
+                         int vocab_size, const void* draft_probs, tq_dtype draft_dtype, int64_t draft_stride,
+                         const int32_t* row_start, int num_seqs, const int32_t* tokens, const int32_t* parents,
+                         const float* temperature, const float* u_accept, const float* u_sample, int32_t* path,
+                         int max_path, int32_t* path_lens, int32_t* next_token, void* workspace,
+                         size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  const char* name = "tq_verify_tree";
+  if (num_rows < 0 || vocab_size < 1 || num_seqs < 0 || max_path < 1)
+    return fail(TQ_ERR_INVALID_ARG, "%s: invalid sizes (rows=%d, vocab=%d, seqs=%d, max_path=%d)", name, num_rows,
+                vocab_size, num_seqs, max_path);
+  if (!dtype_ok(logits_dtype) || (draft_probs && !dtype_ok(draft_dtype)))
+    return fail(TQ_ERR_INVALID_ARG, "%s: unknown dtype", name);
+  if (num_seqs > 0 && (!row_start || !path || !path_lens || !next_token ||
+                       (num_rows > 0 && (!logits || !tokens || !u_sample || (draft_probs && !u_accept)))))
+    return fail(TQ_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (num_rows > 1 && (logits_stride < vocab_size || (draft_probs && draft_stride < vocab_size)))
+    return fail(TQ_ERR_INVALID_ARG, "%s: rows overlap (strides %lld, %lld, vocab %d)", name, (long long)logits_stride,
+                (long long)draft_stride, vocab_size);
+  if (!aligned(logits, dtype_size(logits_dtype)) || (draft_probs && !aligned(draft_probs, dtype_size(draft_dtype))))
+    return fail(TQ_ERR_INVALID_ARG, "%s: misaligned rows", name);
+  for (const void* p : {(const void*)row_start, (const void*)tokens, (const void*)parents, (const void*)temperature,
+                        (const void*)u_accept, (const void*)u_sample, (const void*)path, (const void*)path_lens,
+                        (const void*)next_token, (const void*)status_dev})
+    if (!aligned(p, 4)) return fail(TQ_ERR_INVALID_ARG, "%s: misaligned pointer", name);
+  const size_t need = tq_verify_tree_workspace(num_rows, vocab_size, num_seqs);
+  if (num_seqs > 0 && (workspace_bytes < need || !workspace || !aligned(workspace, 256)))
+    return fail(TQ_ERR_INVALID_ARG, "%s: workspace must be >= %zu bytes and 256-byte aligned (got %zu)", name, need,
+                workspace_bytes);
+  tq::VerifyArgs a{};
+  a.logits = logits;
+  a.logits_dtype = (int)logits_dtype;
+  a.logits_stride = logits_stride;
+  a.num_rows = num_rows;
+  a.vocab = vocab_size;
+  a.draft = draft_probs;
+  a.draft_dtype = (int)draft_dtype;
+  a.draft_stride = draft_stride;
+  a.row_start = row_start;
+  a.num_seqs = num_seqs;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.temperature = temperature;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.path = path;
+  a.max_path = max_path;
+  a.path_lens = path_lens;
+  a.next_token = next_token;
+  a.workspace = workspace;
+  a.status = status_dev;
+  return check_cuda(tq::launch_verify(a, static_cast<cudaStream_t>(stream)), name);
 }
 
 }  // extern "C"

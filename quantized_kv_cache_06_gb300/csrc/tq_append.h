@@ -1,0 +1,52 @@
+// Head norms with position rotation, and the append into packed pages (tq_append.cu): internal
+// declarations.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace tq {
+
+struct AppendArgs {
+  // rows of head_dim elements, heads of a token contiguous, tokens `stride` elements apart
+  const void* q;
+  int64_t q_stride;
+  int num_q_heads;  // 0: no queries
+  const void* k;
+  int64_t k_stride;
+  int num_k_heads;
+  const void* v;
+  int64_t v_stride;
+  int num_v_heads;
+  int dtype;
+  int64_t num_tokens;
+  int head_dim;
+  void* q_out;  // dense, of the input type
+  int64_t q_out_stride;
+  void* k_out;  // dense keys (k_pages is then null)
+  int64_t k_out_stride;
+  // packed rows
+  const int64_t* slots;
+  int64_t num_slots;
+  uint8_t* k_pages;
+  int k_bits;
+  uint8_t* v_pages;
+  int v_bits;
+  const float* signs;
+  const float* k_centroids;
+  const float* v_centroids;
+  // norms (null: none) and position rotation (cos_sin null: none)
+  const float* q_weight;
+  const float* k_weight;
+  float eps;
+  const int32_t* positions;
+  int position_offset;
+  const float* cos_sin;
+  int64_t num_positions;
+  int rot_dim;
+  int interleaved;
+  int32_t* status;  // may be null
+};
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
+
+}  // namespace tq
