@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tq_append.h"
 #include "tq_device.cuh"
@@ -26,14 +27,15 @@ namespace tq {
 namespace {
 
 constexpr int kAppendWarps = 8;
+constexpr int kAppendCtas = 2;  // CTAs of an SM
 
 struct AppendPlan {
   AppendArgs a;
-  int q_groups, k_groups, v_groups;  // groups of 32 / (D / 16) heads of a token
-  int per_item;                      // groups a warp takes together
+  int per_item;         // groups of 32 / (D / 16) heads that a warp takes together
+  int items[3];         // items of a token's q, k, v
   int items_per_token;
-  int vec;        // inputs and dense outputs: 16-byte accesses
-  int table_vec;  // table rows: 16-byte loads
+  int vec;              // inputs and dense outputs: 16-byte accesses
+  int table_vec;        // table rows: 16-byte loads
 };
 
 // Sum over the LPR lanes of a row.
@@ -59,44 +61,59 @@ __device__ __forceinline__ float sum_squares(const float2 (&x)[8]) {
   return (s0.x + s0.y) + (s1.x + s1.y);
 }
 
-// Eight consecutive elements at p.
+// A lane's two chunks of eight elements, as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float2 (&v)[4]) {
-  if (vec) {
-    constexpr int W = 16 / (int)sizeof(T);  // elements of 16 bytes
+struct Raw {
+  static constexpr int N = 16 * (int)sizeof(T) / 16;
+  uint4 w[N];
+  // chunks at p and p + half; any alignment without `vec`
+  __device__ __forceinline__ void load(const T* p, int half, bool vec) {
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < 8 / W; ++i) {
-      const uint4 w = reinterpret_cast<const uint4*>(p)[i];
-      const T* e = reinterpret_cast<const T*>(&w);
+      for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(p + (i < N / 2 ? 0 : half))[i % (N / 2)];
+    } else {
+      T* e = reinterpret_cast<T*>(w);
 #pragma unroll
-      for (int j = 0; j < W; j += 2) v[(i * W + j) / 2] = make_float2(to_f32<T>(e[j]), to_f32<T>(e[j + 1]));
+      for (int j = 0; j < 16; ++j) e[j] = p[j < 8 ? j : half + j - 8];
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) v[j / 2] = make_float2(to_f32<T>(p[j]), to_f32<T>(p[j + 1]));
   }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, bool vec, const float2 (&v)[4]) {
+  __device__ __forceinline__ void store(T* p, int half, bool vec) const {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p + (i < N / 2 ? 0 : half))[i % (N / 2)] = w[i];
+    } else {
+      const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) p[j < 8 ? j : half + j - 8] = e[j];
+    }
+  }
+  __device__ __forceinline__ void get(float2 (&x)[8]) const {
+    const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = make_float2(to_f32<T>(e[2 * i]), to_f32<T>(e[2 * i + 1]));
+  }
+  __device__ __forceinline__ void set(const float2 (&x)[8]) {
+    T* e = reinterpret_cast<T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[2 * i] = from_f32<T>(x[i].x);
+      e[2 * i + 1] = from_f32<T>(x[i].y);
+    }
+  }
+};
+
+// Eight floats at p (16-byte aligned with `vec`).
+__device__ __forceinline__ void load8(const float* __restrict__ p, bool vec, float2 (&v)[4]) {
   if (vec) {
-    constexpr int W = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < 8 / W; ++i) {
-      uint4 w;
-      T* e = reinterpret_cast<T*>(&w);
-#pragma unroll
-      for (int j = 0; j < W; j += 2) {
-        e[j] = from_f32<T>(v[(i * W + j) / 2].x);
-        e[j + 1] = from_f32<T>(v[(i * W + j) / 2].y);
-      }
-      reinterpret_cast<uint4*>(p)[i] = w;
+    for (int i = 0; i < 2; ++i) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+      v[2 * i] = make_float2(f.x, f.y);
+      v[2 * i + 1] = make_float2(f.z, f.w);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      p[j] = from_f32<T>(v[j / 2].x);
-      p[j + 1] = from_f32<T>(v[j / 2].y);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__ldg(p + 2 * i), __ldg(p + 2 * i + 1));
   }
 }
 
@@ -113,9 +130,10 @@ __device__ __forceinline__ int row_exponent(const float2 (&x)[8]) {
   return ex;
 }
 
-// x <- w x / sqrt(mean x^2 + eps).  A row beyond the range of its squares is scaled first.
+// 1 / sqrt(mean x^2 + eps).  A row beyond the range of its squares is scaled by a power of two
+// first, x with it.
 template <int LPR>
-__device__ __forceinline__ void norm_row(float2 (&x)[8], const float* __restrict__ w, float eps, int l) {
+__device__ __forceinline__ float norm_factor(float2 (&x)[8], float eps) {
   constexpr int D = 16 * LPR;
   float ss = row_sum<LPR>(sum_squares(x));
   // squares that underflow count only where eps is as small
@@ -132,75 +150,125 @@ __device__ __forceinline__ void norm_row(float2 (&x)[8], const float* __restrict
     const float again = row_sum<LPR>(sum_squares(x));
     if (odd) ss = again;
   }
-  const float inv = rsqrtf(fmaf(ss, 1.0f / D, eps));
-  const float2 i2 = make_float2(inv, inv);
-  const float4* w4 = reinterpret_cast<const float4*>(w);
+  return rsqrtf(fmaf(ss, 1.0f / D, eps));
+}
+
+// What a token's rows are multiplied by: y[i] = x[i] p[i] + other(x)[i] s[i], weights, signs and
+// rotation in one.  `mode` says where the other channel of a pair lies.
+enum Mode { kPlain, kHalves, kPairs, kStaged };  // (no pair; slot i ^ 4; the same float2; by shared memory)
+struct Coef {
+  float2 p[8], s[8];
+};
+
+// Coefficients of a token: weights `w` (null: 1), signs `sg` (null: 1), the position's table row `cs`
+// (null: no rotation).  Channel e's other one is e +- rot / 2, or e ^ 1.
+template <int LPR>
+__device__ __forceinline__ void token_coef(Coef& f, int mode, const float* __restrict__ w, const float* __restrict__ sg,
+                                           const float* __restrict__ cs, int rot, bool tvec, int l) {
+  constexpr int D = 16 * LPR;
+  const int half = rot / 2;
+  const float2 one = make_float2(1.f, 1.f);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
+    const int e0 = c * (D / 2) + 8 * l;  // the chunk's first channel
+    float2 wv[4], cv[4], sv[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 g = __ldg(w4 + (c * (D / 2) + 8 * l) / 4 + h);
-      x[4 * c + 2 * h] = __fmul2_rn(__fmul2_rn(x[4 * c + 2 * h], i2), make_float2(g.x, g.y));
-      x[4 * c + 2 * h + 1] = __fmul2_rn(__fmul2_rn(x[4 * c + 2 * h + 1], i2), make_float2(g.z, g.w));
+    for (int i = 0; i < 4; ++i) wv[i] = cv[i] = one, sv[i] = make_float2(0.f, 0.f);
+    if (w) load8(w + e0, true, wv);
+    if (mode == kPairs) {
+      const int p0 = e0 / 2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p0 + i < half) {
+          const float a = __ldg(cs + p0 + i), b = __ldg(cs + half + p0 + i);
+          cv[i] = make_float2(a, a);
+          sv[i] = __fmul2_rn(make_float2(wv[i].y, wv[i].x), make_float2(-b, b));
+        }
+    } else if (mode == kHalves || (mode == kStaged && rot % 16 == 0)) {
+      if (e0 < rot) {  // the whole chunk is of one half
+        const bool first = e0 < half;
+        const int p0 = first ? e0 : e0 - half;
+        float2 ow[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ow[i] = one;
+        if (w) load8(w + (first ? e0 + half : p0), true, ow);
+        load8(cs + p0, tvec, cv);
+        load8(cs + half + p0, tvec, sv);
+        const float2 sign = first ? make_float2(-1.f, -1.f) : one;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sv[i] = __fmul2_rn(__fmul2_rn(sv[i], sign), ow[i]);
+      }
+    } else if (mode == kStaged) {
+      float* cf = reinterpret_cast<float*>(cv);
+      float* sf = reinterpret_cast<float*>(sv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = e0 + i;
+        if (e >= rot) continue;
+        const bool first = e < half;
+        const int p = first ? e : e - half;
+        const float ow = w ? __ldg(w + (first ? e + half : p)) : 1.f;
+        cf[i] = __ldg(cs + p);
+        sf[i] = (first ? -ow : ow) * __ldg(cs + half + p);
+      }
+    }
+    float2 g[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = one;
+    if (sg) load8(sg + e0, false, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.p[4 * c + i] = __fmul2_rn(__fmul2_rn(wv[i], cv[i]), g[i]);
+      f.s[4 * c + i] = __fmul2_rn(sv[i], g[i]);
     }
   }
 }
 
-// Position rotation of a row; `cs` is the position's table row (rot_dim / 2 cosines, then
-// sines).  `stage` is the warp's room for its rows (half style with rot_dim < D).
 template <int LPR>
-__device__ __forceinline__ void rotate_row(float2 (&x)[8], const float* __restrict__ cs, int rot, bool pairs, bool tvec,
-                                           int l, int row, float* stage) {
+__device__ __forceinline__ void apply_coef(float2 (&x)[8], const Coef& f, int mode, int rot, int l, float* mine) {
   constexpr int D = 16 * LPR;
-  const int half = rot / 2;
-  if (pairs) {
+  if (mode == kPlain) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f.p[i]);
+  } else if (mode == kHalves) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = x[i], b = x[4 + i];
+      x[i] = __ffma2_rn(a, f.p[i], __fmul2_rn(b, f.s[i]));
+      x[4 + i] = __ffma2_rn(b, f.p[4 + i], __fmul2_rn(a, f.s[4 + i]));
+    }
+  } else if (mode == kPairs) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __ffma2_rn(x[i], f.p[i], __fmul2_rn(make_float2(x[i].y, x[i].x), f.s[i]));
+  } else {
+    const int half = rot / 2;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      *reinterpret_cast<float4*>(mine + (i >> 2) * (D / 2) + 8 * l + 2 * (i & 3)) =
+          make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
+    __syncwarp();
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int p0 = (c * (D / 2) + 8 * l) / 2;  // first of the chunk's four pairs
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (p0 + j >= half) continue;
-        const float cv = __ldg(cs + p0 + j), sv = __ldg(cs + half + p0 + j);
-        const float2 v = x[4 * c + j];
-        x[4 * c + j] = make_float2(fmaf(v.x, cv, -v.y * sv), fmaf(v.y, cv, v.x * sv));
-      }
-    }
-  } else if (rot == D) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float2 cv, sv;
-      if (tvec) {
-        cv = __ldg(reinterpret_cast<const float2*>(cs + 8 * l) + j);
-        sv = __ldg(reinterpret_cast<const float2*>(cs + half + 8 * l) + j);
+      const int e0 = c * (D / 2) + 8 * l;
+      float2 other[4];
+      if (rot % 16 == 0) {
+        const float4* at = reinterpret_cast<const float4*>(mine + (e0 < half ? e0 + half : e0 < rot ? e0 - half : e0));
+        const float4 u = at[0], v = at[1];
+        other[0] = make_float2(u.x, u.y), other[1] = make_float2(u.z, u.w);
+        other[2] = make_float2(v.x, v.y), other[3] = make_float2(v.z, v.w);
       } else {
-        cv = make_float2(__ldg(cs + 8 * l + 2 * j), __ldg(cs + 8 * l + 2 * j + 1));
-        sv = make_float2(__ldg(cs + half + 8 * l + 2 * j), __ldg(cs + half + 8 * l + 2 * j + 1));
+        float* o = reinterpret_cast<float*>(other);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = e0 + i;
+          o[i] = mine[e < half ? e + half : e < rot ? e - half : e];
+        }
       }
-      const float2 a = x[j], b = x[4 + j];
-      const float2 ns = make_float2(-sv.x, -sv.y);
-      x[j] = __ffma2_rn(a, cv, __fmul2_rn(b, ns));
-      x[4 + j] = __ffma2_rn(b, cv, __fmul2_rn(a, sv));
-    }
-  } else {
-    float* mine = stage + row * D;
-    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<float2*>(mine + (i >> 2) * (D / 2) + 8 * l + 2 * (i & 3)) = x[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float* v = reinterpret_cast<float*>(&x[i]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int e = (i >> 2) * (D / 2) + 8 * l + 2 * (i & 3) + u;
-        if (e >= rot) continue;
-        const bool first = e < half;
-        const int p = first ? e : e - half;
-        const float cv = __ldg(cs + p), sv = __ldg(cs + half + p);
-        const float other = mine[first ? e + half : e - half];
-        v[u] = first ? fmaf(v[u], cv, -other * sv) : fmaf(v[u], cv, other * sv);
-      }
+      for (int i = 0; i < 4; ++i)
+        x[4 * c + i] = e0 + 2 * i < rot ? __ffma2_rn(x[4 * c + i], f.p[4 * c + i], __fmul2_rn(other[i], f.s[4 * c + i]))
+                                        : __fmul2_rn(x[4 * c + i], f.p[4 * c + i]);
     }
   }
 }
@@ -232,13 +300,54 @@ __device__ __forceinline__ void fwht_row(float2 (&x)[8], int l) {
   }
 }
 
-// Encodes a row (all lanes of the warp take part; `dst` null: nothing stored).
+// Quantiser of a codebook.  128 equal cells cover the decision points' span; a cell holds the
+// number of points in cells before it, so the index is that and one comparison for each point that
+// the cell itself may hold (`steps`, the most of any cell: 1 for a Lloyd-Max codebook).  Cells come
+// from one monotone function of u for points and coordinates alike, so its rounding does not
+// matter.  32 words of counts and at most 32 points: neither lookup has bank conflicts.
+struct Quant {
+  float point[32];      // decision points, then +inf
+  uint8_t below[128];   // 4 * (points in cells before this one)
+  float mul, add;       // span to [0, 1]
+  int steps;
+};
+// 127 times the clamped coordinate, as the bits of a subnormal: the cell's number
+__device__ __forceinline__ uint32_t cell_of(float u, float mul, float add) {
+  float t;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(t) : "f"(u), "f"(mul), "f"(add));  // NaN: 0
+  return __float_as_uint(t * 0x1.fcp-143f);  // 127 * 2^-149
+}
+// Set up by a warp from n = 2^bits ascending centroids (points: rounded midpoints).
+__device__ __forceinline__ void build_quant(Quant& q, const float* __restrict__ c, int n, int lane) {
+  const float pt = lane < n - 1 ? 0.5f * (__ldg(c + lane) + __ldg(c + lane + 1)) : __int_as_float(0x7f800000);
+  const float lo = __shfl_sync(kFullMask, pt, 0), hi = __shfl_sync(kFullMask, pt, n - 2);
+  const float mul = hi > lo ? 1.0f / (hi - lo) : 0.f, add = -lo * mul;
+  const int cell = lane < n - 1 ? (int)cell_of(pt, mul, add) : 128;
+  q.point[lane] = pt;
+  int most = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int below = 0, here = 0;
+    for (int k = 0; k < n - 1; ++k) {
+      const int ck = __shfl_sync(kFullMask, cell, k);
+      below += ck < lane + 32 * j;
+      here += ck == lane + 32 * j;
+    }
+    q.below[lane + 32 * j] = (uint8_t)(4 * below);
+    most = max(most, here);
+  }
+  most = __reduce_max_sync(kFullMask, most);
+  if (lane == 0) q.mul = mul, q.add = add, q.steps = most;
+}
+
+// Encodes rows of signed coordinates x, whose own norm is `factor` times theirs (all lanes of the
+// warp take part; `dst` null: nothing stored).
 template <int LPR, int B>
-__device__ __forceinline__ void encode_row(float2 (&x)[8], const float* __restrict__ bnd, const float2 (&sg)[8], int l,
-                                           uint8_t* dst) {
+__device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Quant& q, int l, uint8_t* dst) {
   constexpr int D = 16 * LPR, IB = D * B / 8;
   float ss = row_sum<LPR>(sum_squares(x));
   int ex = 0;
+  bool bad = false;
   const bool odd = !(ss <= 0x1p100f) || ss < 0x1p-100f;
   if (__any_sync(kFullMask, odd)) {
     const int e = row_exponent<LPR>(x);
@@ -249,39 +358,68 @@ __device__ __forceinline__ void encode_row(float2 (&x)[8], const float* __restri
     }
     const float again = row_sum<LPR>(sum_squares(x));
     if (odd) ss = again;
-  }
-  const bool bad = !(ss <= 3.402823466e38f);  // a NaN or infinite coordinate: a zero row's indices
-  const float rs = (ss > 0.f && !bad) ? rsqrtf(ss) : 0.f;
-  const float nu = bad ? ss : scale_pow2(ss * rs, ex);
+    bad = !(ss <= 3.402823466e38f);  // a NaN or infinite coordinate: a zero row's indices
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], sg[i]);
+    for (int i = 0; i < 8; ++i)
+      if (bad) x[i] = make_float2(0.f, 0.f);
+  }
+  const float rs = (ss > 0.f && !bad) ? rsqrtf(ss) : 0.f;
+  const float nu = bad ? ss : scale_pow2(ss * rs * factor, ex);
   fwht_row<LPR>(x, l);
   constexpr float kInvSqrtD = LPR == 1 ? 0.25f : LPR == 2 ? 0.17677669529663689f : LPR == 4 ? 0.125f
                               : LPR == 8 ? 0.088388347648318447f : 0.0625f;
   const float inv = rs * kInvSqrtD;
+  const float2 inv2 = make_float2(inv, inv);
+  const float mul = q.mul, add = q.add;
+  const int steps = q.steps;
+  const unsigned char* below = q.below;
+  const unsigned char* point = reinterpret_cast<const unsigned char*>(q.point);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], inv2);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    uint64_t word = 0;
+    using Word = typename std::conditional<(B > 4), uint64_t, uint32_t>::type;
+    Word word = 0;  // 4 times the indices
+    if (steps == 1) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 p = x[4 * c + j / 2];
-      const float u = bad ? 0.f : ((j & 1) ? p.y : p.x) * inv;
-      int idx = 0;  // #{k : boundary_k < u}, by halves
-#pragma unroll
-      for (int s = 1 << (B - 1); s > 0; s >>= 1)
-        if (u > bnd[idx + s - 1]) idx += s;
-      word |= (uint64_t)idx << (B * j);
-    }
-    if (dst) {
-      uint8_t* at = dst + c * (IB / 2) + B * l;
-      if constexpr (B == 4) {
-        *reinterpret_cast<uint32_t*>(at) = (uint32_t)word;
-      } else if constexpr (B == 2) {
-        *reinterpret_cast<uint16_t*>(at) = (uint16_t)word;
-      } else {
-#pragma unroll
-        for (int k = 0; k < B; ++k) at[k] = (uint8_t)(word >> (8 * k));
+      for (int j = 0; j < 8; ++j) {
+        const float u = (j & 1) ? x[4 * c + j / 2].y : x[4 * c + j / 2].x;
+        const uint32_t four = below[cell_of(u, mul, add)];
+        const bool up = u > *reinterpret_cast<const float*>(point + four);
+        if (j == 0) word = (four >> 2) + (up ? 1 : 0);
+        else word += ((Word)four << (B * j - 2)) + (up ? (Word)1 << (B * j) : 0);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = (j & 1) ? x[4 * c + j / 2].y : x[4 * c + j / 2].x;
+        uint32_t four = below[cell_of(u, mul, add)];
+        for (int k = 0; k < steps; ++k)
+          if (u > *reinterpret_cast<const float*>(point + four)) four += 4;
+        word |= (Word)(four >> 2) << (B * j);
+      }
+    }
+    // a chunk's B bytes: whole words where the lanes of a row's quad share them
+    uint8_t* at = dst + c * (IB / 2) + B * l;
+    if constexpr (B == 4) {
+      if (dst) *reinterpret_cast<uint32_t*>(at) = word;
+    } else if constexpr (B == 2 && LPR >= 2) {
+      const uint32_t next = __shfl_down_sync(kFullMask, word, 1);
+      if (dst && (l & 1) == 0) *reinterpret_cast<uint32_t*>(at) = word | next << 16;
+    } else if constexpr (B == 3 && LPR >= 4) {
+      const uint32_t next = __shfl_down_sync(kFullMask, word, 1);
+      const int k = l & 3;  // word k of three: 24 bits of lane k less 8 k, then lane k + 1's
+      if (dst && k < 3) *reinterpret_cast<uint32_t*>(at + k) = word >> (8 * k) | next << (24 - 8 * k);
+    } else if constexpr (B == 5 && LPR >= 4) {
+      const uint64_t before = __shfl_up_sync(kFullMask, word, 1);
+      const int k = l & 3;  // word k of five: the last 8 k bits of lane k - 1, then lane k's
+      if (dst) {
+        *reinterpret_cast<uint32_t*>(at - k) = (uint32_t)(word << (8 * k) | (k ? before >> (40 - 8 * k) : 0));
+        if (k == 3) *reinterpret_cast<uint32_t*>(at + 1) = (uint32_t)(word >> 8);
+      }
+    } else if (dst) {
+#pragma unroll
+      for (int k = 0; k < B; ++k) at[k] = (uint8_t)(word >> (8 * k));
     }
   }
   if (dst && l == 0) {
@@ -295,34 +433,36 @@ __device__ __forceinline__ void encode_row(float2 (&x)[8], const float* __restri
   }
 }
 
-template <typename T, int LPR>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendPlan p) {
+// PACK: some rows are packed (a dense call needs neither quantisers nor their code).
+template <typename T, int LPR, bool PACK>
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(AppendPlan p) {
   constexpr int D = 16 * LPR, RPW = 32 / LPR;
-  __shared__ float bnd[2][32];
+  __shared__ Quant quant[PACK ? 2 : 1];
   __shared__ __align__(16) float stage_all[kAppendWarps][RPW * D];
   const AppendArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LPR, row = lane / LPR;
-  if (threadIdx.x < 62) {
-    const int side = threadIdx.x >= 31, i = threadIdx.x - 31 * side;
-    const uint8_t* pages = side ? a.v_pages : a.k_pages;
-    const float* c = side ? a.v_centroids : a.k_centroids;
-    const int n = pages ? (1 << (side ? a.v_bits : a.k_bits)) - 1 : 0;
-    if (i < n) bnd[side][i] = 0.5f * (c[i] + c[i + 1]);
+  if constexpr (PACK) {
+    if (warp == 0 && a.k_pages) build_quant(quant[0], a.k_centroids, 1 << a.k_bits, lane);
+    if (warp == 1 && a.v_pages) build_quant(quant[1], a.v_centroids, 1 << a.v_bits, lane);
+    __syncthreads();
   }
-  __syncthreads();
-  float2 sg[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    sg[i] = make_float2(1.f, 1.f);
-    const int e = (i >> 2) * (D / 2) + 8 * l + 2 * (i & 3);
-    if (a.signs) sg[i] = make_float2(__ldg(a.signs + e), __ldg(a.signs + e + 1));
-  }
-  const int groups = p.q_groups + p.k_groups + p.v_groups;
   const int64_t items = a.num_tokens * p.items_per_token;
   for (int64_t item = (int64_t)blockIdx.x * kAppendWarps + warp; item < items; item += (int64_t)gridDim.x * kAppendWarps) {
     const int64_t t = item / p.items_per_token;
     const int part = (int)(item - t * p.items_per_token);
+    const int side = part < p.items[0] ? 0 : part < p.items[0] + p.items[1] ? 1 : 2;
+    const int first = (part - (side > 0 ? p.items[0] : 0) - (side > 1 ? p.items[1] : 0)) * p.per_item;
+    const int heads = side == 0 ? a.num_q_heads : side == 1 ? a.num_k_heads : a.num_v_heads;
+    const int end = min((heads + RPW - 1) / RPW, first + p.per_item);
+    const T* src = static_cast<const T*>(side == 0 ? a.q : side == 1 ? a.k : a.v) +
+                   t * (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) + 8 * l;
+    auto fetch = [&](Raw<T>& raw, int g) {
+      const int head = g * RPW + row;
+      raw.load(src + (head < heads ? head : 0) * D, D / 2, p.vec);
+    };
+    Raw<T> raw, next;
+    fetch(raw, first);
     const float* cs = nullptr;
     if (a.positions) {
       const int64_t pos = (int64_t)a.positions[t] + a.position_offset;
@@ -332,72 +472,72 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendPlan p)
           if (a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
           continue;
         }
-        cs = a.cos_sin + pos * a.rot_dim;
+        if (side < 2) cs = a.cos_sin + pos * a.rot_dim;
       }
     }
-    int64_t slot = -1;
-    if (a.slots) {
+    const bool dense = !PACK || side == 0;
+    int64_t slot = 0;
+    if (!dense) {
       slot = a.slots[t];
       if (slot >= a.num_slots) {
         if (a.status && lane == 0) atomicMax(a.status, (int32_t)kSlotOutOfRange);
-        slot = -1;
+        continue;
       }
+      if (slot < 0) continue;
     }
-    const int end = min(groups, (part + 1) * p.per_item);
-    for (int g = part * p.per_item; g < end; ++g) {
-      const int side = g < p.q_groups ? 0 : g < p.q_groups + p.k_groups ? 1 : 2;
-      const int heads = side == 0 ? a.num_q_heads : side == 1 ? a.num_k_heads : a.num_v_heads;
-      const int head = (g - (side == 0 ? 0 : side == 1 ? p.q_groups : p.q_groups + p.k_groups)) * RPW + row;
-      const bool dense = side == 0 || (side == 1 && a.k_out);
-      if (!dense && slot < 0) continue;
+    const float* w = side == 0 ? a.q_weight : side == 1 ? a.k_weight : nullptr;
+    const int mode = !cs ? kPlain : a.interleaved ? kPairs : a.rot_dim == D ? kHalves : kStaged;
+    Coef f;
+    token_coef<LPR>(f, mode, w, dense ? nullptr : a.signs, cs, a.rot_dim, p.table_vec, l);
+    for (int g = first; g < end; ++g) {
+      if (g + 1 < end) fetch(next, g + 1);
+      const int head = g * RPW + row;
       const bool live = head < heads;
-      const T* src = static_cast<const T*>(side == 0 ? a.q : side == 1 ? a.k : a.v) +
-                     t * (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) + (int64_t)(live ? head : 0) * D;
       float2 x[8];
-      {
-        float2 lo[4], hi[4];
-        load8<T>(src + 8 * l, p.vec, lo);
-        load8<T>(src + D / 2 + 8 * l, p.vec, hi);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
-      }
-      if (side < 2) {
-        const float* w = side == 0 ? a.q_weight : a.k_weight;
-        if (w) norm_row<LPR>(x, w, a.eps, l);
-        if (cs) rotate_row<LPR>(x, cs, a.rot_dim, a.interleaved, p.table_vec, l, row, stage_all[warp]);
-      }
+      raw.get(x);
+      float factor = 1.f;
+      if (w) factor = norm_factor<LPR>(x, a.eps);
+      apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage_all[warp] + row * D);
       if (dense) {
-        if (live) {
-          T* dst = static_cast<T*>(side == 0 ? a.q_out : a.k_out) + t * (side == 0 ? a.q_out_stride : a.k_out_stride) +
-                   (int64_t)head * D;
-          const float2 lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
-          store8<T>(dst + 8 * l, p.vec, lo);
-          store8<T>(dst + D / 2 + 8 * l, p.vec, hi);
+        const float2 f2 = make_float2(factor, factor);
+        if (w) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f2);
         }
-      } else {
+        Raw<T> out;
+        out.set(x);
+        T* dst = static_cast<T*>(side == 0 ? a.q_out : a.k_out) + t * (side == 0 ? a.q_out_stride : a.k_out_stride) +
+                 8 * l + head * D;
+        if (live) out.store(dst, D / 2, p.vec);
+      } else if constexpr (PACK) {
         const int bits = side == 1 ? a.k_bits : a.v_bits;
         uint8_t* dst = live ? (side == 1 ? a.k_pages : a.v_pages) + (slot * heads + head) * (int64_t)(D * bits / 8 + 4) : nullptr;
-        const float* b = bnd[side - 1];
+        const Quant& q = quant[side - 1];
         switch (bits) {
-          case 2: encode_row<LPR, 2>(x, b, sg, l, dst); break;
-          case 3: encode_row<LPR, 3>(x, b, sg, l, dst); break;
-          case 4: encode_row<LPR, 4>(x, b, sg, l, dst); break;
-          default: encode_row<LPR, 5>(x, b, sg, l, dst); break;
+          case 2: encode_row<LPR, 2>(x, factor, q, l, dst); break;
+          case 3: encode_row<LPR, 3>(x, factor, q, l, dst); break;
+          case 4: encode_row<LPR, 4>(x, factor, q, l, dst); break;
+          default: encode_row<LPR, 5>(x, factor, q, l, dst); break;
         }
       }
+      raw = next;
     }
   }
 }
 
+template <typename T, int LPR>
+void launch_append_as(const AppendPlan& p, int grid, cudaStream_t stream) {
+  if (p.a.k_pages || p.a.v_pages) append_kernel<T, LPR, true><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+  else append_kernel<T, LPR, false><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+}
 template <typename T>
 cudaError_t launch_append_typed(const AppendPlan& p, int grid, cudaStream_t stream) {
-  const int threads = kAppendWarps * 32;
   switch (p.a.head_dim) {
-    case 16: append_kernel<T, 1><<<grid, threads, 0, stream>>>(p); break;
-    case 32: append_kernel<T, 2><<<grid, threads, 0, stream>>>(p); break;
-    case 64: append_kernel<T, 4><<<grid, threads, 0, stream>>>(p); break;
-    case 128: append_kernel<T, 8><<<grid, threads, 0, stream>>>(p); break;
-    case 256: append_kernel<T, 16><<<grid, threads, 0, stream>>>(p); break;
+    case 16: launch_append_as<T, 1>(p, grid, stream); break;
+    case 32: launch_append_as<T, 2>(p, grid, stream); break;
+    case 64: launch_append_as<T, 4>(p, grid, stream); break;
+    case 128: launch_append_as<T, 8>(p, grid, stream); break;
+    case 256: launch_append_as<T, 16>(p, grid, stream); break;
     default: return cudaErrorInvalidValue;
   }
   const cudaError_t err = cudaGetLastError();
@@ -418,20 +558,20 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   }
   AppendPlan p{};
   p.a = a;
-  const int rpw = 32 / (a.head_dim / 16), size = a.dtype == kF32 ? 4 : 2;
-  auto groups = [&](int heads) { return (heads + rpw - 1) / rpw; };
-  p.q_groups = groups(a.num_q_heads);
-  p.k_groups = groups(a.num_k_heads);
-  p.v_groups = groups(a.num_v_heads);
-  const int total = p.q_groups + p.k_groups + p.v_groups;
+  const int rpw = 32 / (a.head_dim / 16), size = a.dtype == kF32 ? 4 : 2, sms = device_sms();
+  const int groups[3] = {(a.num_q_heads + rpw - 1) / rpw, (a.num_k_heads + rpw - 1) / rpw, (a.num_v_heads + rpw - 1) / rpw};
+  const int64_t total = (int64_t)groups[0] + groups[1] + groups[2];
   if (a.num_tokens == 0 || total == 0) return cudaSuccess;
   p.vec = vec_ok(a.q, a.q_stride, size) && vec_ok(a.k, a.k_stride, size) && vec_ok(a.v, a.v_stride, size) &&
           vec_ok(a.q_out, a.q_out_stride, size) && vec_ok(a.k_out, a.k_out_stride, size);
-  p.table_vec = vec_ok(a.cos_sin, a.rot_dim / 2, 4);
-  p.per_item = 1;
-  p.items_per_token = total;
+  p.table_vec = reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0 && a.rot_dim % 8 == 0;
+  // a token's coefficients serve up to eight groups of heads; fewer where that leaves warps idle
+  const int64_t warps = (int64_t)sms * kAppendCtas * kAppendWarps;
+  p.per_item = (int)std::max<int64_t>(1, std::min<int64_t>(8, a.num_tokens * total / (2 * warps)));
+  for (int i = 0; i < 3; ++i) p.items[i] = (groups[i] + p.per_item - 1) / p.per_item;
+  p.items_per_token = p.items[0] + p.items[1] + p.items[2];
   const int64_t ctas = (a.num_tokens * p.items_per_token + kAppendWarps - 1) / kAppendWarps;
-  const int grid = (int)std::min<int64_t>(ctas, (int64_t)device_sms() * 16);
+  const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * kAppendCtas);
   switch (a.dtype) {
     case kF32: return launch_append_typed<float>(p, grid, stream);
     case kF16: return launch_append_typed<__half>(p, grid, stream);
