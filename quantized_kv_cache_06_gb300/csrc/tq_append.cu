@@ -34,6 +34,8 @@ struct AppendPlan {
   int per_item;         // groups of 32 / (D / 16) heads that a warp takes together
   int items[3];         // items of a token's q, k, v
   int items_per_token;
+  int64_t step_t;       // tokens and items between two items of a warp
+  int step_part;
   int vec;              // inputs and dense outputs: 16-byte accesses
   int table_vec;        // table rows: 16-byte loads
 };
@@ -66,19 +68,15 @@ template <typename T>
 struct Raw {
   static constexpr int N = 16 * (int)sizeof(T) / 16;
   uint4 w[N];
-  // chunks at p and p + half; any alignment without `vec`
-  __device__ __forceinline__ void load(const T* p, int half, bool vec) {
-    if (vec) {
+  // chunks at p and p + half, at any alignment
+  __device__ __forceinline__ void load(const T* p, int half) {
+    T* e = reinterpret_cast<T*>(w);
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(p + (i < N / 2 ? 0 : half))[i % (N / 2)];
-    } else {
-      T* e = reinterpret_cast<T*>(w);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) e[j] = p[j < 8 ? j : half + j - 8];
-    }
+    for (int j = 0; j < 16; ++j) e[j] = p[j < 8 ? j : half + j - 8];
   }
-  __device__ __forceinline__ void store(T* p, int half, bool vec) const {
-    if (vec) {
+  template <bool VEC>
+  __device__ __forceinline__ void store(T* p, int half) const {
+    if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p + (i < N / 2 ? 0 : half))[i % (N / 2)] = w[i];
     } else {
@@ -433,71 +431,153 @@ __device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Q
   }
 }
 
-// PACK: some rows are packed (a dense call needs neither quantisers nor their code).
-template <typename T, int LPR, bool PACK>
+__device__ __forceinline__ uint32_t smem_address(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// Groups of rows in flight of a warp, 1 KB (16-bit types) or 2 KB each.
+template <typename T>
+__host__ __device__ constexpr int stages() {
+  return sizeof(T) == 2 ? 4 : 3;
+}
+// Dynamic shared memory: the copies in flight, and room to exchange pairs.
+template <typename T>
+__host__ __device__ constexpr int ring_bytes() {
+  return kAppendWarps * stages<T>() * 32 * 16 * (int)sizeof(T);
+}
+constexpr int kStageBytes = kAppendWarps * 512 * 4;
+
+// One side of a token, or some of its groups of heads.
+template <typename T, int LPR>
+struct Item {
+  int64_t t;
+  int part, side, heads, g, end;
+  const T* src;  // this lane's elements of group 0's first row
+  __device__ __forceinline__ void open(const AppendPlan& p, int l) {
+    constexpr int RPW = 32 / LPR;
+    const AppendArgs& a = p.a;
+    side = part < p.items[0] ? 0 : part < p.items[0] + p.items[1] ? 1 : 2;
+    g = (part - (side > 0 ? p.items[0] : 0) - (side > 1 ? p.items[1] : 0)) * p.per_item;
+    heads = side == 0 ? a.num_q_heads : side == 1 ? a.num_k_heads : a.num_v_heads;
+    end = min((heads + RPW - 1) / RPW, g + p.per_item);
+    src = static_cast<const T*>(side == 0 ? a.q : side == 1 ? a.k : a.v) +
+          t * (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) + 8 * l;
+  }
+  __device__ __forceinline__ void next(const AppendPlan& p) {
+    t += p.step_t;
+    part += p.step_part;
+    if (part >= p.items_per_token) part -= p.items_per_token, ++t;
+  }
+  // rows behind the last head are read as the first: they are not stored
+  __device__ __forceinline__ const T* rows(int group, int row) const {
+    const int head = group * (32 / LPR) + row;
+    return src + (head < heads ? head : 0) * (16 * LPR);
+  }
+};
+
+// PACK: some rows are packed (a dense call needs neither quantisers nor their code).  VEC: rows
+// are 16-byte aligned; their copies run ahead of the arithmetic, across items, each lane's own
+// elements through its own shared memory, so that nothing has to be waited for but the copies.
+template <typename T, int LPR, bool PACK, bool VEC>
 __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(AppendPlan p) {
-  constexpr int D = 16 * LPR, RPW = 32 / LPR;
+  constexpr int D = 16 * LPR, RPW = 32 / LPR, S = stages<T>(), N = Raw<T>::N;
   __shared__ Quant quant[PACK ? 2 : 1];
-  __shared__ __align__(16) float stage_all[kAppendWarps][RPW * D];
+  extern __shared__ __align__(16) unsigned char dynamic[];
   const AppendArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LPR, row = lane / LPR;
+  unsigned char* ring = dynamic + warp * (S * N * 512) + lane * 16;
+  float* stage = reinterpret_cast<float*>(dynamic + (VEC ? ring_bytes<T>() : 0)) + warp * 512 + row * D;
+  Item<T, LPR> it, ahead;
+  {
+    const uint32_t item = blockIdx.x * kAppendWarps + warp;
+    it.t = item / (uint32_t)p.items_per_token;
+    it.part = (int)(item - (uint32_t)it.t * (uint32_t)p.items_per_token);
+    ahead.t = it.t;
+    ahead.part = it.part;
+  }
+  int slot_in = 0, slot_out = 0;
+  if (VEC && ahead.t < a.num_tokens) ahead.open(p, l);
+  auto produce = [&] {
+    if (ahead.t < a.num_tokens) {
+      const T* from = ahead.rows(ahead.g, row);
+      const uint32_t to = smem_address(ring) + slot_in * (N * 512);
+#pragma unroll
+      for (int i = 0; i < N; ++i) copy16(to + i * 512, reinterpret_cast<const uint4*>(from + (i < N / 2 ? 0 : D / 2)) + i % (N / 2));
+      slot_in = slot_in + 1 == S ? 0 : slot_in + 1;
+      if (++ahead.g == ahead.end) {
+        ahead.next(p);
+        if (ahead.t < a.num_tokens) ahead.open(p, l);
+      }
+    }
+    copies_commit();
+  };
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) produce();
+  }
   if constexpr (PACK) {
     if (warp == 0 && a.k_pages) build_quant(quant[0], a.k_centroids, 1 << a.k_bits, lane);
     if (warp == 1 && a.v_pages) build_quant(quant[1], a.v_centroids, 1 << a.v_bits, lane);
     __syncthreads();
   }
-  const int64_t items = a.num_tokens * p.items_per_token;
-  for (int64_t item = (int64_t)blockIdx.x * kAppendWarps + warp; item < items; item += (int64_t)gridDim.x * kAppendWarps) {
-    const int64_t t = item / p.items_per_token;
-    const int part = (int)(item - t * p.items_per_token);
-    const int side = part < p.items[0] ? 0 : part < p.items[0] + p.items[1] ? 1 : 2;
-    const int first = (part - (side > 0 ? p.items[0] : 0) - (side > 1 ? p.items[1] : 0)) * p.per_item;
-    const int heads = side == 0 ? a.num_q_heads : side == 1 ? a.num_k_heads : a.num_v_heads;
-    const int end = min((heads + RPW - 1) / RPW, first + p.per_item);
-    const T* src = static_cast<const T*>(side == 0 ? a.q : side == 1 ? a.k : a.v) +
-                   t * (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) + 8 * l;
-    auto fetch = [&](Raw<T>& raw, int g) {
-      const int head = g * RPW + row;
-      raw.load(src + (head < heads ? head : 0) * D, D / 2, p.vec);
-    };
-    Raw<T> raw, next;
-    fetch(raw, first);
+  for (; it.t < a.num_tokens; it.next(p)) {
+    it.open(p, l);
+    const int64_t t = it.t;
+    bool skip = false;
     const float* cs = nullptr;
     if (a.positions) {
       const int64_t pos = (int64_t)a.positions[t] + a.position_offset;
-      if (pos < 0) continue;  // a padding row
-      if (a.cos_sin) {
+      if (pos < 0) {
+        skip = true;  // a padding row
+      } else if (a.cos_sin) {
         if (pos >= a.num_positions) {
           if (a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
-          continue;
+          skip = true;
+        } else if (it.side < 2) {
+          cs = a.cos_sin + pos * a.rot_dim;
         }
-        if (side < 2) cs = a.cos_sin + pos * a.rot_dim;
       }
     }
-    const bool dense = !PACK || side == 0;
+    const bool dense = !PACK || it.side == 0;
     int64_t slot = 0;
     if (!dense) {
       slot = a.slots[t];
-      if (slot >= a.num_slots) {
-        if (a.status && lane == 0) atomicMax(a.status, (int32_t)kSlotOutOfRange);
-        continue;
-      }
-      if (slot < 0) continue;
+      if (slot >= a.num_slots && !skip && a.status && lane == 0) atomicMax(a.status, (int32_t)kSlotOutOfRange);
+      skip |= slot < 0 || slot >= a.num_slots;
     }
-    const float* w = side == 0 ? a.q_weight : side == 1 ? a.k_weight : nullptr;
+    const float* w = it.side == 0 ? a.q_weight : it.side == 1 ? a.k_weight : nullptr;
     const int mode = !cs ? kPlain : a.interleaved ? kPairs : a.rot_dim == D ? kHalves : kStaged;
     Coef f;
-    token_coef<LPR>(f, mode, w, dense ? nullptr : a.signs, cs, a.rot_dim, p.table_vec, l);
-    for (int g = first; g < end; ++g) {
-      if (g + 1 < end) fetch(next, g + 1);
-      const int head = g * RPW + row;
-      const bool live = head < heads;
+    if (!skip) token_coef<LPR>(f, mode, w, dense ? nullptr : a.signs, cs, a.rot_dim, p.table_vec, l);
+    for (int g = it.g; g < it.end; ++g) {
+      Raw<T> raw;
+      if constexpr (VEC) {
+        copies_wait<S - 2>();
+        const unsigned char* from = ring + slot_out * (N * 512);
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw.w[i] = *reinterpret_cast<const uint4*>(from + i * 512);
+        slot_out = slot_out + 1 == S ? 0 : slot_out + 1;
+      } else {
+        raw.load(it.rows(g, row), D / 2);
+      }
       float2 x[8];
       raw.get(x);
+      if constexpr (VEC) produce();
+      if (skip) continue;
       float factor = 1.f;
       if (w) factor = norm_factor<LPR>(x, a.eps);
-      apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage_all[warp] + row * D);
+      apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage);
+      const int head = g * RPW + row;
+      const bool live = head < it.heads;
       if (dense) {
         const float2 f2 = make_float2(factor, factor);
         if (w) {
@@ -506,13 +586,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
         }
         Raw<T> out;
         out.set(x);
-        T* dst = static_cast<T*>(side == 0 ? a.q_out : a.k_out) + t * (side == 0 ? a.q_out_stride : a.k_out_stride) +
-                 8 * l + head * D;
-        if (live) out.store(dst, D / 2, p.vec);
+        T* dst = static_cast<T*>(it.side == 0 ? a.q_out : a.k_out) +
+                 t * (it.side == 0 ? a.q_out_stride : a.k_out_stride) + 8 * l + head * D;
+        if (live) out.template store<VEC>(dst, D / 2);
       } else if constexpr (PACK) {
-        const int bits = side == 1 ? a.k_bits : a.v_bits;
-        uint8_t* dst = live ? (side == 1 ? a.k_pages : a.v_pages) + (slot * heads + head) * (int64_t)(D * bits / 8 + 4) : nullptr;
-        const Quant& q = quant[side - 1];
+        const int bits = it.side == 1 ? a.k_bits : a.v_bits;
+        uint8_t* dst = live ? (it.side == 1 ? a.k_pages : a.v_pages) + (slot * it.heads + head) * (int64_t)(D * bits / 8 + 4)
+                            : nullptr;
+        const Quant& q = quant[it.side - 1];
         switch (bits) {
           case 2: encode_row<LPR, 2>(x, factor, q, l, dst); break;
           case 3: encode_row<LPR, 3>(x, factor, q, l, dst); break;
@@ -520,29 +601,43 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
           default: encode_row<LPR, 5>(x, factor, q, l, dst); break;
         }
       }
-      raw = next;
     }
   }
+  if constexpr (VEC) copies_wait<0>();
 }
 
+template <typename T, int LPR, bool PACK, bool VEC>
+cudaError_t launch_append_kernel(const AppendPlan& p, int grid, cudaStream_t stream) {
+  auto kern = append_kernel<T, LPR, PACK, VEC>;
+  const bool staged = p.a.cos_sin && !p.a.interleaved && p.a.rot_dim < p.a.head_dim;
+  const int smem = (VEC ? ring_bytes<T>() : 0) + (staged ? kStageBytes : 0);
+  if (smem > 46 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  kern<<<grid, kAppendWarps * 32, smem, stream>>>(p);
+  const cudaError_t err = cudaGetLastError();
+  if (err == cudaSuccess) count_launches(1);
+  return err;
+}
 template <typename T, int LPR>
-void launch_append_as(const AppendPlan& p, int grid, cudaStream_t stream) {
-  if (p.a.k_pages || p.a.v_pages) append_kernel<T, LPR, true><<<grid, kAppendWarps * 32, 0, stream>>>(p);
-  else append_kernel<T, LPR, false><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+cudaError_t launch_append_as(const AppendPlan& p, int grid, cudaStream_t stream) {
+  const bool pack = p.a.k_pages || p.a.v_pages;
+  if (p.vec) return pack ? launch_append_kernel<T, LPR, true, true>(p, grid, stream)
+                         : launch_append_kernel<T, LPR, false, true>(p, grid, stream);
+  return pack ? launch_append_kernel<T, LPR, true, false>(p, grid, stream)
+              : launch_append_kernel<T, LPR, false, false>(p, grid, stream);
 }
 template <typename T>
 cudaError_t launch_append_typed(const AppendPlan& p, int grid, cudaStream_t stream) {
   switch (p.a.head_dim) {
-    case 16: launch_append_as<T, 1>(p, grid, stream); break;
-    case 32: launch_append_as<T, 2>(p, grid, stream); break;
-    case 64: launch_append_as<T, 4>(p, grid, stream); break;
-    case 128: launch_append_as<T, 8>(p, grid, stream); break;
-    case 256: launch_append_as<T, 16>(p, grid, stream); break;
+    case 16: return launch_append_as<T, 1>(p, grid, stream);
+    case 32: return launch_append_as<T, 2>(p, grid, stream);
+    case 64: return launch_append_as<T, 4>(p, grid, stream);
+    case 128: return launch_append_as<T, 8>(p, grid, stream);
+    case 256: return launch_append_as<T, 16>(p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
-  const cudaError_t err = cudaGetLastError();
-  if (err == cudaSuccess) count_launches(1);
-  return err;
 }
 
 bool vec_ok(const void* p, int64_t stride, int size) {
@@ -572,6 +667,8 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   p.items_per_token = p.items[0] + p.items[1] + p.items[2];
   const int64_t ctas = (a.num_tokens * p.items_per_token + kAppendWarps - 1) / kAppendWarps;
   const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * kAppendCtas);
+  p.step_t = (int64_t)grid * kAppendWarps / p.items_per_token;
+  p.step_part = (int)((int64_t)grid * kAppendWarps % p.items_per_token);
   switch (a.dtype) {
     case kF32: return launch_append_typed<float>(p, grid, stream);
     case kF16: return launch_append_typed<__half>(p, grid, stream);
