@@ -26,7 +26,8 @@ SOURCES = ["tq_api.cpp", "tq_write.cu", "tq_write_tc.cu", "tq_decode.cu", "tq_de
            "tq_decode_tc_f.cu", "tq_decode_tc_p.cu",
            "tq_decode_tc_q.cu", "tq_prefill_mq.cu",
            "tq_dequant.cu", "tq_qjl.cu", "tq_recipe.cu", "tq_query.cu", "tq_step.cu", "tq_attn.cu", "tq_attn_tc.cu",
-           "tq_small.cu", "tq_append.cu", "tq_verify.cu"]
+           "tq_small.cu", "tq_append.cu", "tq_append_f32.cu", "tq_append_f16.cu", "tq_append_bf16.cu",
+           "tq_append_packed_f32.cu", "tq_append_packed_f16.cu", "tq_append_packed_bf16.cu", "tq_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,769 @@
+// Norms of each query and key head with the position rotation, one pass, and the same on the
+// way into the packed pages, sm_103a.
+//
+// TurboQuant docs: "vLLM Usage" (TQ Byte Layout, Slot Mapping: a token's row goes to its flat
+// slot; TQ Packed Page Contract: write_tq4_kv encodes K and V rows).
+//
+// Per head row x of D channels, in fp32:
+//   norm      x <- w x / sqrt(mean x^2 + eps)
+//   rotation  (a, b) <- (a cos - b sin, b cos + a sin), pairs (i, i + r/2) or (2i, 2i + 1)
+//   encoding  (K and V) nu = ||x||, y = H (s x) / (sqrt(D) nu), index = #{k : boundary_k < y},
+//             packed LSB first, nu appended
+// D / 16 lanes share a row.  Lane l holds channels 8 l .. 8 l + 7 and D / 2 + 8 l .. + 7: the
+// pairs of either style lie in one lane, 16-byte loads cover 16-bit types, the transform has four
+// stages inside a lane and log2(D / 16) by shuffles, and eight indices are `bits` whole bytes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "tq_append.h"
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+// Sum over the LPR lanes of a row.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int m = LPR / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(kFullMask, v, m);
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int m = LPR / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, m));
+  return v;
+}
+__device__ __forceinline__ float sum_squares(const float2 (&x)[8]) {
+  float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s0 = __ffma2_rn(x[i], x[i], s0);
+    s1 = __ffma2_rn(x[i + 4], x[i + 4], s1);
+  }
+  return (s0.x + s0.y) + (s1.x + s1.y);
+}
+
+// A lane's two chunks of eight elements, as they lie in memory.
+template <typename T>
+struct Raw {
+  static constexpr int N = 16 * (int)sizeof(T) / 16;
+  uint4 w[N];
+  // chunks at p and p + half; any alignment without `vec`
+  __device__ __forceinline__ void load(const T* p, int half, bool vec) {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(p + (i < N / 2 ? 0 : half))[i % (N / 2)];
+    } else {
+      T* e = reinterpret_cast<T*>(w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) e[j] = p[j < 8 ? j : half + j - 8];
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int half, bool vec) const {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p + (i < N / 2 ? 0 : half))[i % (N / 2)] = w[i];
+    } else {
+      const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) p[j < 8 ? j : half + j - 8] = e[j];
+    }
+  }
+  __device__ __forceinline__ void get(float2 (&x)[8]) const {
+    const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = make_float2(to_f32<T>(e[2 * i]), to_f32<T>(e[2 * i + 1]));
+  }
+  __device__ __forceinline__ void set(const float2 (&x)[8]) {
+    T* e = reinterpret_cast<T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[2 * i] = from_f32<T>(x[i].x);
+      e[2 * i + 1] = from_f32<T>(x[i].y);
+    }
+  }
+};
+
+// Eight floats at p (16-byte aligned with `vec`).
+__device__ __forceinline__ void load8(const float* __restrict__ p, bool vec, float2 (&v)[4]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+      v[2 * i] = make_float2(f.x, f.y);
+      v[2 * i + 1] = make_float2(f.z, f.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__ldg(p + 2 * i), __ldg(p + 2 * i + 1));
+  }
+}
+
+// ---- rows whose sum of squares leaves [2^-100, 2^100] (out of line: they are rare) -------------
+//
+// Such a row is scaled by 2^-ex, ex the exponent of its largest magnitude (0 where that is 0 or not
+// finite), which is exact.  `odd`: this lane's row is one.
+
+template <int LPR>
+__device__ __forceinline__ int row_exponent(const float2 (&x)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+  m = row_max<LPR>(m);
+  int ex = 0;
+  if (m > 0.f && m <= 3.402823466e38f) frexpf(m, &ex);
+  return ex;
+}
+// Scales x; returns the sum of squares (unchanged where the row is not odd); `eps`, the norm's, goes
+// with the row and bounds ex from below: in the row's units it stays below 2^100.
+template <int LPR>
+__device__ __noinline__ float scale_rows(float2 (&x)[8], float ss, bool odd, float* eps, int* ex_out) {
+  int ex = row_exponent<LPR>(x);
+  if (!odd) ex = 0;
+  if (eps && ex < 0 && *eps > 0.f) ex = max(ex, (ilogbf(*eps) - 100) / 2);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = make_float2(scale_pow2(x[i].x, -ex), scale_pow2(x[i].y, -ex));
+  const float again = row_sum<LPR>(sum_squares(x));
+  if (eps) *eps = ldexpf(*eps, -2 * ex);
+  *ex_out = ex;
+  return odd ? again : ss;
+}
+
+// 1 / sqrt(mean x^2 + eps).
+template <int LPR>
+__device__ __forceinline__ float norm_factor(float2 (&x)[8], float eps) {
+  constexpr int D = 16 * LPR;
+  float ss = row_sum<LPR>(sum_squares(x));
+  // squares that underflow count only where eps is as small
+  const bool odd = !(ss <= 0x1p100f) || (ss < 0x1p-100f && eps < 0x1p-80f);
+  if (__any_sync(kFullMask, odd)) {
+    float2 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+    int ex;
+    float e = eps;
+    ss = scale_rows<LPR>(y, ss, odd, &e, &ex);
+    eps = e;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = y[i];
+  }
+  return rsqrtf(fmaf(ss, 1.0f / D, eps));
+}
+
+__device__ __forceinline__ uint32_t smem_address(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint32_t shared_u8(uint32_t at) {
+  uint32_t v;
+  asm("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float shared_f32(uint32_t at) {
+  float v;
+  asm("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void add_if_greater(uint32_t& word, float u, float pt, uint32_t one) {
+  asm("{\n .reg .pred p;\n setp.gt.f32 p, %1, %2;\n @p add.u32 %0, %0, %3;\n}\n" : "+r"(word) : "f"(u), "f"(pt), "r"(one));
+}
+
+// ---- weights, signs and rotation: y[e] = x[e] p[e] + x[e'] s[e], e' the other channel of e's pair ----
+
+// Where it lies.  kAny: as the call has it.
+enum Mode { kPlain, kHalves, kPairs, kStaged, kAny };  // no pair; slot i ^ 4; same float2; by shared memory
+
+// A side's part of p and s that every token shares: p[e] = weight(e) sign(e), s[e] = -+ weight(e')
+// sign(e), 0 behind the rotated channels.  (Encoded sides carry the transform's signs.)
+struct Shared {
+  float p[256], s[256];
+};
+__device__ __forceinline__ void build_shared(Shared& f, int mode, int D, const float* __restrict__ w,
+                                             const float* __restrict__ sg, int rot, int first, int step) {
+  const int half = rot / 2;
+  for (int e = first; e < D; e += step) {
+    const float g = sg ? __ldg(sg + e) : 1.f;
+    f.p[e] = (w ? __ldg(w + e) : 1.f) * g;
+    float s = 0.f;
+    if (mode != kPlain && e < rot) {
+      const bool head = mode == kPairs ? (e & 1) == 0 : e < half;
+      const int other = mode == kPairs ? e ^ 1 : head ? e + half : e - half;
+      s = (w ? __ldg(w + other) : 1.f) * (head ? -g : g);
+    }
+    f.s[e] = s;
+  }
+}
+
+struct Coef {
+  float2 p[8], s[8];
+};
+__device__ __forceinline__ void shared8(const float* p, float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 f = reinterpret_cast<const float4*>(p)[i];
+    v[2 * i] = make_float2(f.x, f.y);
+    v[2 * i + 1] = make_float2(f.z, f.w);
+  }
+}
+template <int LPR>
+__device__ __forceinline__ void plain_coef(float2 (&p)[8], const Shared& f, int l) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float2 v[4];
+    shared8(f.p + c * 8 * LPR + 8 * l, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[4 * c + i] = v[i];
+  }
+}
+
+// A token's coefficients, `cs` its table row (rot / 2 cosines, then the sines).
+template <int LPR>
+__device__ __forceinline__ void token_coef(Coef& f, const Shared& sh, int mode, const float* __restrict__ cs, int rot,
+                                           bool tvec, int l) {
+  constexpr int D = 16 * LPR;
+  const int half = rot / 2;
+  float2 cv[4], nv[4];
+  if (mode == kHalves) {  // both chunks turn by the same angles
+    load8(cs + 8 * l, tvec, cv);
+    load8(cs + half + 8 * l, tvec, nv);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int e0 = c * (D / 2) + 8 * l;  // the chunk's first channel
+    float2 pv[4], sv[4];
+    shared8(sh.p + e0, pv);
+    shared8(sh.s + e0, sv);
+    if (mode == kPairs) {
+      const int p0 = e0 / 2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cv[i] = make_float2(1.f, 1.f), nv[i] = make_float2(0.f, 0.f);
+      if (tvec && p0 + 4 <= half) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(cs + p0));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + p0));
+        const float cf[4] = {a.x, a.y, a.z, a.w}, sf[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cv[i] = make_float2(cf[i], cf[i]), nv[i] = make_float2(sf[i], sf[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p0 + i < half) {
+            const float a = __ldg(cs + p0 + i), b = __ldg(cs + half + p0 + i);
+            cv[i] = make_float2(a, a), nv[i] = make_float2(b, b);
+          }
+      }
+    } else if (mode == kStaged) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cv[i] = make_float2(1.f, 1.f), nv[i] = make_float2(0.f, 0.f);
+      if (rot % 16 == 0) {  // the whole chunk is of one half
+        if (e0 < rot) {
+          load8(cs + (e0 < half ? e0 : e0 - half), tvec, cv);
+          load8(cs + (e0 < half ? e0 + half : e0), tvec, nv);
+        }
+      } else {
+        float* cf = reinterpret_cast<float*>(cv);
+        float* sf = reinterpret_cast<float*>(nv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = e0 + i, t = e < half ? e : e - half;
+          if (e < rot) cf[i] = __ldg(cs + t), sf[i] = __ldg(cs + half + t);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.p[4 * c + i] = __fmul2_rn(pv[i], cv[i]);
+      f.s[4 * c + i] = __fmul2_rn(sv[i], nv[i]);
+    }
+  }
+}
+
+template <int LPR>
+__device__ __forceinline__ void apply_coef(float2 (&x)[8], const Coef& f, int mode, int rot, int l, float* mine) {
+  constexpr int D = 16 * LPR;
+  if (mode == kHalves) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = x[i], b = x[4 + i];
+      x[i] = __ffma2_rn(a, f.p[i], __fmul2_rn(b, f.s[i]));
+      x[4 + i] = __ffma2_rn(b, f.p[4 + i], __fmul2_rn(a, f.s[4 + i]));
+    }
+  } else if (mode == kPairs) {
+    if (rot == D) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __ffma2_rn(x[i], f.p[i], __fmul2_rn(make_float2(x[i].y, x[i].x), f.s[i]));
+    } else {  // (the neighbour of a channel that stays may be infinite)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = (i >> 2) * (D / 2) + 8 * l + 2 * (i & 3) < rot;
+        const float2 other = in ? make_float2(x[i].y, x[i].x) : make_float2(0.f, 0.f);
+        x[i] = __ffma2_rn(x[i], f.p[i], __fmul2_rn(other, f.s[i]));
+      }
+    }
+  } else {
+    const int half = rot / 2;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      *reinterpret_cast<float4*>(mine + (i >> 2) * (D / 2) + 8 * l + 2 * (i & 3)) =
+          make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int e0 = c * (D / 2) + 8 * l;
+      float2 other[4];
+      if (rot % 16 == 0) {
+        const float4* at = reinterpret_cast<const float4*>(mine + (e0 < half ? e0 + half : e0 < rot ? e0 - half : e0));
+        const float4 u = at[0], v = at[1];
+        other[0] = make_float2(u.x, u.y), other[1] = make_float2(u.z, u.w);
+        other[2] = make_float2(v.x, v.y), other[3] = make_float2(v.z, v.w);
+        if (e0 >= rot) other[0] = other[1] = other[2] = other[3] = make_float2(0.f, 0.f);
+      } else {
+        float* o = reinterpret_cast<float*>(other);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = e0 + i;
+          o[i] = e < half ? mine[e + half] : e < rot ? mine[e - half] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[4 * c + i] = __ffma2_rn(x[4 * c + i], f.p[4 * c + i], __fmul2_rn(other[i], f.s[4 * c + i]));
+    }
+  }
+}
+
+// Unnormalised Walsh-Hadamard transform of a row (natural order; the stages commute).
+template <int LPR>
+__device__ __forceinline__ void fwht_row(float2 (&x)[8], int l) {
+  const float2 minus1 = make_float2(-1.f, -1.f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = make_float2(x[i].x + x[i].y, x[i].x - x[i].y);
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)  // h = 1, 2: inside a chunk; 4: between the two chunks
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & h) == 0) {
+        const float2 a = x[i], b = x[i + h];
+        x[i] = __fadd2_rn(a, b);
+        x[i + h] = __ffma2_rn(b, minus1, a);
+      }
+#pragma unroll
+  for (int m = 1; m < LPR; m <<= 1) {
+    const float sg = (l & m) ? -1.f : 1.f;
+    const float2 s2 = make_float2(sg, sg);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 p = make_float2(__shfl_xor_sync(kFullMask, x[i].x, m), __shfl_xor_sync(kFullMask, x[i].y, m));
+      x[i] = __ffma2_rn(x[i], s2, p);
+    }
+  }
+}
+
+// Quantiser of a codebook.  128 equal cells cover the decision points' span; a cell holds the
+// number of points in cells before it, so the index is that and one comparison for each point that
+// the cell itself may hold (`steps`, the most of any cell: 1 for a Lloyd-Max codebook).  Cells come
+// from one monotone function of u for points and coordinates alike, so its rounding does not
+// matter.  32 words of counts and at most 32 points: neither lookup has bank conflicts.
+struct Quant {
+  float point[32];      // decision points, then +inf
+  uint8_t below[128];   // 4 * (points in cells before this one)
+  float mul, add;       // span to [0, 1]
+  int steps;
+};
+// 127 times the clamped coordinate, as the bits of a subnormal: the cell's number
+__device__ __forceinline__ uint32_t cell_of(float u, float mul, float add) {
+  float t;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(t) : "f"(u), "f"(mul), "f"(add));  // NaN: 0
+  return __float_as_uint(t * 0x1.fcp-143f);  // 127 * 2^-149
+}
+// Set up by a warp from n = 2^bits ascending centroids (points: rounded midpoints).
+__device__ __forceinline__ void build_quant(Quant& q, const float* __restrict__ c, int n, int lane) {
+  const float pt = lane < n - 1 ? 0.5f * (__ldg(c + lane) + __ldg(c + lane + 1)) : __int_as_float(0x7f800000);
+  const float lo = __shfl_sync(kFullMask, pt, 0), hi = __shfl_sync(kFullMask, pt, n - 2);
+  const float mul = hi > lo ? 1.0f / (hi - lo) : 0.f, add = -lo * mul;
+  const int cell = lane < n - 1 ? (int)cell_of(pt, mul, add) : 128;
+  q.point[lane] = pt;
+  int most = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int below = 0, here = 0;
+    for (int k = 0; k < n - 1; ++k) {
+      const int ck = __shfl_sync(kFullMask, cell, k);
+      below += ck < lane + 32 * j;
+      here += ck == lane + 32 * j;
+    }
+    q.below[lane + 32 * j] = (uint8_t)(4 * below);
+    most = max(most, here);
+  }
+  most = __reduce_max_sync(kFullMask, most);
+  if (lane == 0) q.mul = mul, q.add = add, q.steps = most;
+}
+
+// Codebooks of which a cell holds several points (out of line; no Lloyd-Max codebook is one).
+template <int B>
+__device__ __noinline__ uint32_t four_indices_slow(float u0, float u1, float u2, float u3, uint32_t below, uint32_t point,
+                                                   float mul, float add, int steps) {
+  const float u[4] = {u0, u1, u2, u3};
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t four = shared_u8(below + cell_of(u[j], mul, add));
+    for (int k = 0; k < steps; ++k)
+      if (u[j] > shared_f32(point + four)) four += 4;
+    word += (four >> 2) << (B * j);
+  }
+  return word;
+}
+
+// Encodes rows of signed coordinates x, whose own norm is `factor` times theirs (all lanes of the
+// warp take part; `dst` null: nothing stored).
+template <int LPR, int B>
+__device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Quant& q, int l, uint8_t* dst) {
+  constexpr int D = 16 * LPR, IB = D * B / 8;
+  float ss = row_sum<LPR>(sum_squares(x));
+  int ex = 0;
+  bool bad = false;
+  const bool odd = !(ss <= 0x1p100f) || ss < 0x1p-100f;
+  if (__any_sync(kFullMask, odd)) {
+    float2 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+    int e;
+    ss = scale_rows<LPR>(y, ss, odd, nullptr, &e);
+    ex = e;
+    bad = !(ss <= 3.402823466e38f);  // a NaN or infinite coordinate: a zero row's indices
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = bad ? make_float2(0.f, 0.f) : y[i];
+  }
+  const float rs = (ss > 0.f && !bad) ? rsqrtf(ss) : 0.f;
+  const float nu = bad ? ss : scale_pow2(ss * rs * factor, ex);
+  fwht_row<LPR>(x, l);
+  constexpr float kInvSqrtD = LPR == 1 ? 0.25f : LPR == 2 ? 0.17677669529663689f : LPR == 4 ? 0.125f
+                              : LPR == 8 ? 0.088388347648318447f : 0.0625f;
+  const float inv = rs * kInvSqrtD;
+  const float2 inv2 = make_float2(inv, inv);
+  const float mul = q.mul, add = q.add;
+  const int steps = q.steps;
+  const uint32_t below = smem_address(q.below), point = smem_address(q.point);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], inv2);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    // the eight indices as two words of four (4 B bits each)
+    uint32_t half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t word = 0, lowest = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 pair = x[4 * c + 2 * h + j / 2];
+        const float u = (j & 1) ? pair.y : pair.x;
+        const uint32_t four = shared_u8(below + cell_of(u, mul, add));
+        const float pt = shared_f32(point + four);
+        if (j == 0) lowest = four >> 2;
+        else word += four * (1u << (B * j - 2));
+        add_if_greater(word, u, pt, 1u << (B * j));
+      }
+      half[h] = word + lowest;
+      if (steps > 1) {
+        const float2 u = x[4 * c + 2 * h], v = x[4 * c + 2 * h + 1];
+        half[h] = four_indices_slow<B>(u.x, u.y, v.x, v.y, below, point, mul, add, steps);
+      }
+    }
+    using Word = typename std::conditional<(B > 4), uint64_t, uint32_t>::type;
+    const Word word = (Word)half[0] | (Word)half[1] << (4 * B);
+    // a chunk's B bytes: whole words where the lanes of a row's quad share them
+    uint8_t* at = dst + c * (IB / 2) + B * l;
+    if constexpr (B == 4) {
+      if (dst) *reinterpret_cast<uint32_t*>(at) = word;
+    } else if constexpr (B == 2 && LPR >= 2) {
+      const uint32_t next = __shfl_down_sync(kFullMask, word, 1);
+      if (dst && (l & 1) == 0) *reinterpret_cast<uint32_t*>(at) = word | next << 16;
+    } else if constexpr (B == 3 && LPR >= 4) {
+      const uint32_t next = __shfl_down_sync(kFullMask, word, 1);
+      const int k = l & 3;  // word k of three: 24 bits of lane k less 8 k, then lane k + 1's
+      if (dst && k < 3) *reinterpret_cast<uint32_t*>(at + k) = word >> (8 * k) | next << (24 - 8 * k);
+    } else if constexpr (B == 5 && LPR >= 4) {
+      const uint64_t before = __shfl_up_sync(kFullMask, word, 1);
+      const int k = l & 3;  // word k of five: the last 8 k bits of lane k - 1, then lane k's
+      if (dst) {
+        *reinterpret_cast<uint32_t*>(at - k) = (uint32_t)(word << (8 * k) | (k ? before >> (40 - 8 * k) : 0));
+        if (k == 3) *reinterpret_cast<uint32_t*>(at + 1) = (uint32_t)(word >> 8);
+      }
+    } else if (dst) {
+#pragma unroll
+      for (int k = 0; k < B; ++k) at[k] = (uint8_t)(word >> (8 * k));
+    }
+  }
+  if (dst && l == 0) {
+    if constexpr (D == 16) {  // rows of 8 to 14 bytes: 2-byte aligned
+      const uint32_t w = __float_as_uint(nu);
+      *reinterpret_cast<uint16_t*>(dst + IB) = (uint16_t)w;
+      *reinterpret_cast<uint16_t*>(dst + IB + 2) = (uint16_t)(w >> 16);
+    } else {
+      *reinterpret_cast<float*>(dst + IB) = nu;
+    }
+  }
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// Groups of rows in flight of a warp, 1 KB (16-bit types) or 2 KB each.
+template <typename T>
+__host__ __device__ constexpr int stages() {
+  return sizeof(T) == 2 ? 4 : 3;
+}
+// Dynamic shared memory: the copies in flight, and room to exchange pairs.
+template <typename T>
+__host__ __device__ constexpr int ring_bytes() {
+  return kAppendWarps * stages<T>() * 32 * 16 * (int)sizeof(T);
+}
+constexpr int kStageBytes = kAppendWarps * 512 * 4;
+
+// A stretch of the groups of heads of one side (0: q, 1: k, 2: v) over a block of tokens, token by
+// token, and where a warp stands in it.
+struct Walk {
+  int64_t t;        // token
+  int block, part;  // which stretch
+  int side, groups;
+  int g, left;      // group of heads, groups left
+  __device__ __forceinline__ void open(const AppendPlan& p) {
+    side = part < p.items[0] ? 0 : part < p.items[0] + p.items[1] ? 1 : 2;
+    groups = side == 0 ? p.groups[0] : side == 1 ? p.groups[1] : p.groups[2];
+    const int u = (part - (side > 0 ? p.items[0] : 0) - (side > 1 ? p.items[1] : 0)) * p.per_item;
+    const int n = (int)((uint32_t)u / (uint32_t)groups);
+    t = (int64_t)block * p.block_tokens + n;
+    g = u - n * groups;
+    const int tokens = (int)min((int64_t)(p.block_tokens - n), p.a.num_tokens - t);
+    left = min(p.per_item, tokens * groups - g);  // (none in a stretch behind the last token)
+  }
+  __device__ __forceinline__ void next(const AppendPlan& p) {
+    block += p.step_block;
+    part += p.step_part;
+    if (part >= p.block_items) part -= p.block_items, ++block;
+  }
+  __device__ __forceinline__ void step() {
+    --left;
+    if (++g == groups) g = 0, ++t;
+  }
+};
+
+// PACK: some rows are packed (a dense call needs neither quantisers nor their code).  RING: rows are
+// 16-byte aligned; their copies run ahead of the arithmetic, across tokens, each lane's own elements
+// through its own shared memory, so that nothing has to be waited for but the copies.
+template <typename T, int LPR, int MODE, bool PACK, bool RING>
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(AppendPlan p) {
+  constexpr int D = 16 * LPR, RPW = 32 / LPR, S = stages<T>(), N = Raw<T>::N;
+  constexpr int kGroup = RPW * D * (int)sizeof(T);  // bytes of a group's rows
+  __shared__ Quant quant[PACK ? 2 : 1];
+  __shared__ __align__(16) Shared shared[3];
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  const AppendArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int l = lane % LPR, row = lane / LPR;
+  unsigned char* ring = dynamic + warp * (S * N * 512) + lane * 16;
+  float* stage = reinterpret_cast<float*>(dynamic + (RING ? ring_bytes<T>() : 0)) + warp * 512 + row * D;
+  Walk it, ahead;
+  {
+    const uint32_t item = blockIdx.x * kAppendWarps + warp;
+    it.block = item / (uint32_t)p.block_items;
+    it.part = (int)(item - (uint32_t)it.block * (uint32_t)p.block_items);
+    ahead.block = it.block;
+    ahead.part = it.part;
+    ahead.left = 0;
+  }
+  auto stride_of = [&](int side) { return (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) * (int64_t)sizeof(T); };
+  auto rows_of = [&](const Walk& w) {  // this lane's elements of the group's row
+    return static_cast<const unsigned char*>(w.side == 0 ? a.q : w.side == 1 ? a.k : a.v) + w.t * stride_of(w.side) +
+           w.g * kGroup + (row * D + 8 * l) * (int)sizeof(T);
+  };
+  auto heads_of = [&](int side) { return side == 0 ? p.heads[0] : side == 1 ? p.heads[1] : p.heads[2]; };
+  const unsigned char* from = nullptr;
+  uint32_t slot_in = smem_address(ring), slot_out = slot_in;
+  const uint32_t ring_end = slot_in + S * N * 512;
+  auto produce = [&] {
+    if (ahead.left <= 0) {
+      while (ahead.block < p.blocks) {
+        ahead.open(p);
+        if (ahead.left > 0) break;
+        ahead.next(p);
+      }
+      if (ahead.left > 0) from = rows_of(ahead);
+    }
+    if (ahead.left > 0) {
+      if (ahead.g * RPW + row < heads_of(ahead.side)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) copy16(slot_in + i * 512, from + (i < N / 2 ? 0 : D / 2 * (int)sizeof(T)) + i % (N / 2) * 16);
+      }
+      slot_in += N * 512;
+      if (slot_in == ring_end) slot_in -= S * N * 512;
+      const bool last = ahead.g + 1 == ahead.groups;
+      from += kGroup;
+      if (last) from += stride_of(ahead.side) - ahead.groups * kGroup;
+      ahead.step();
+      if (ahead.left == 0) ahead.next(p);
+    }
+    copies_commit();
+  };
+  if constexpr (RING) {
+    // lanes of rows behind a side's last head keep what they held: ones, to begin with
+#pragma unroll
+    for (int i = 0; i < S * N; ++i) *reinterpret_cast<uint4*>(ring + i * 512) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+#pragma unroll 1
+    for (int i = 0; i < S - 1; ++i) produce();
+  }
+  const int mode = MODE == kAny ? (!a.cos_sin ? kPlain : a.interleaved ? kPairs : a.rot_dim == D ? kHalves : kStaged) : MODE;
+  if constexpr (PACK) {
+    if (warp == 0 && a.k_pages) build_quant(quant[0], a.k_centroids, 1 << a.k_bits, lane);
+    if (warp == 1 && a.v_pages) build_quant(quant[1], a.v_centroids, 1 << a.v_bits, lane);
+  }
+  if (warp >= 2) {  // (six warps: two a side)
+    const int side = (warp - 2) >> 1;
+    build_shared(shared[side], side == 2 ? kPlain : mode, D, side == 0 ? a.q_weight : side == 1 ? a.k_weight : nullptr,
+                 PACK && side > 0 ? a.signs : nullptr, a.rot_dim, (warp & 1) * 32 + lane, 64);
+  }
+  __syncthreads();
+  for (; it.block < p.blocks; it.next(p)) {
+    it.open(p);
+    const int side = it.side, heads = heads_of(side);
+    const bool dense = !PACK || side == 0;
+    const bool normed = (side == 0 ? a.q_weight : side == 1 ? a.k_weight : nullptr) != nullptr;
+    Coef f;
+    if (side == 2 || mode == kPlain) plain_coef<LPR>(f.p, shared[side], l);
+    bool fresh = true, skip = false;
+    unsigned char* to = nullptr;  // this lane's place in the group's row
+    for (; it.left > 0; it.step()) {
+      if (fresh || it.g == 0) {  // a token's position, slot and coefficients
+        fresh = skip = false;
+        const int64_t pos = a.positions ? (int64_t)a.positions[it.t] + a.position_offset : 0;
+        if (dense) {
+          to = static_cast<unsigned char*>(side == 0 ? a.q_out : a.k_out) +
+               (it.t * (side == 0 ? a.q_out_stride : a.k_out_stride) + row * D + 8 * l) * (int64_t)sizeof(T) + it.g * kGroup;
+        } else {
+          const int64_t slot = a.slots[it.t];
+          if (slot >= a.num_slots && pos >= 0 && a.status && lane == 0) atomicMax(a.status, (int32_t)kSlotOutOfRange);
+          skip = slot < 0 || slot >= a.num_slots;
+          const int rb = D * (side == 1 ? a.k_bits : a.v_bits) / 8 + 4;
+          to = (side == 1 ? a.k_pages : a.v_pages) + (slot * heads + it.g * RPW + row) * rb;
+        }
+        skip |= pos < 0;  // a padding row
+        if (a.cos_sin && pos >= a.num_positions) {
+          if (a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
+          skip = true;
+        }
+        if (!skip && side < 2 && mode != kPlain)
+          token_coef<LPR>(f, shared[side], mode, a.cos_sin + pos * a.rot_dim, a.rot_dim, p.table_vec, l);
+      }
+      const bool live = it.g * RPW + row < heads;
+      Raw<T> raw;
+      if constexpr (RING) {
+        copies_wait<S - 2>();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(raw.w[i].x), "=r"(raw.w[i].y), "=r"(raw.w[i].z), "=r"(raw.w[i].w)
+                       : "r"(slot_out + i * 512)
+                       : "memory");
+        slot_out += N * 512;
+        if (slot_out == ring_end) slot_out -= S * N * 512;
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
+        if (live) raw.load(reinterpret_cast<const T*>(rows_of(it)), D / 2, p.vec);
+      }
+      float2 x[8];
+      raw.get(x);
+      if constexpr (RING) produce();
+      if (!skip) {
+        float factor = 1.f;
+        if (normed) factor = norm_factor<LPR>(x, a.eps);
+        if (side == 2 || mode == kPlain) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f.p[i]);
+        } else {
+          apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage);
+        }
+        if (dense) {
+          if (normed) {
+            const float2 f2 = make_float2(factor, factor);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f2);
+          }
+          Raw<T> out;
+          out.set(x);
+          if (live) out.store(reinterpret_cast<T*>(to), D / 2, RING || p.vec);
+          to += kGroup;
+        } else if constexpr (PACK) {
+          const int bits = side == 1 ? a.k_bits : a.v_bits;
+          uint8_t* dst = live ? to : nullptr;
+          const Quant& q = quant[side - 1];
+          switch (bits) {
+            case 2: encode_row<LPR, 2>(x, factor, q, l, dst); break;
+            case 3: encode_row<LPR, 3>(x, factor, q, l, dst); break;
+            case 4: encode_row<LPR, 4>(x, factor, q, l, dst); break;
+            default: encode_row<LPR, 5>(x, factor, q, l, dst); break;
+          }
+          to += RPW * (D * bits / 8 + 4);
+        }
+      }
+    }
+  }
+  if constexpr (RING) copies_wait<0>();
+}
+
+template <typename T, int LPR, int MODE, bool PACK, bool RING>
+cudaError_t launch_append_kernel(const AppendPlan& p, cudaStream_t stream) {
+  auto kern = append_kernel<T, LPR, MODE, PACK, RING>;
+  const bool staged = p.a.cos_sin && !p.a.interleaved && p.a.rot_dim < p.a.head_dim;
+  const int smem = (RING ? ring_bytes<T>() : 0) + (staged ? kStageBytes : 0);
+  if (smem > 46 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  kern<<<p.grid, kAppendWarps * 32, smem, stream>>>(p);
+  const cudaError_t err = cudaGetLastError();
+  if (err == cudaSuccess) count_launches(1);
+  return err;
+}
+
+// Head dims of 64 and more with aligned rows and a rotation take a kernel of their mode; the rest
+// one for any call.
+template <typename T, int LPR, bool PACK>
+cudaError_t launch_append_mode(const AppendPlan& p, cudaStream_t stream) {
+  if constexpr (LPR >= 4) {
+    if (p.vec && p.a.cos_sin) {
+      if (p.a.interleaved) return launch_append_kernel<T, LPR, kPairs, PACK, true>(p, stream);
+      if (p.a.rot_dim == p.a.head_dim) return launch_append_kernel<T, LPR, kHalves, PACK, true>(p, stream);
+      return launch_append_kernel<T, LPR, kStaged, PACK, true>(p, stream);
+    }
+  }
+  return launch_append_kernel<T, LPR, kAny, PACK, false>(p, stream);
+}
+template <typename T, bool PACK>
+cudaError_t launch_append_typed(const AppendPlan& p, cudaStream_t stream) {
+  switch (p.a.head_dim) {
+    case 16: return launch_append_mode<T, 1, PACK>(p, stream);
+    case 32: return launch_append_mode<T, 2, PACK>(p, stream);
+    case 64: return launch_append_mode<T, 4, PACK>(p, stream);
+    case 128: return launch_append_mode<T, 8, PACK>(p, stream);
+    case 256: return launch_append_mode<T, 16, PACK>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+}  // namespace tq

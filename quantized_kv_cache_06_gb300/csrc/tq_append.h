@@ -49,4 +49,28 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 
+constexpr int kAppendWarps = 8;
+constexpr int kAppendCtas = 2;  // CTAs of an SM
+
+// How a call is cut: blocks of tokens, each side's groups of 32 / (head_dim / 16) heads over a block
+// in stretches of `per_item`, a warp a stretch.
+struct AppendPlan {
+  AppendArgs a;
+  int block_tokens, blocks;
+  int per_item;
+  int heads[3], groups[3], items[3];  // of q, k, v
+  int block_items;
+  int step_block, step_part;  // from one stretch of a warp to its next
+  int grid;
+  int vec;                    // inputs and dense outputs: 16-byte accesses
+  int table_vec, signs_vec;   // table rows, signs: 16-byte loads
+};
+// By type, dense or packed (one translation unit each).
+cudaError_t launch_append_f32(const AppendPlan& p, cudaStream_t stream);
+cudaError_t launch_append_f16(const AppendPlan& p, cudaStream_t stream);
+cudaError_t launch_append_bf16(const AppendPlan& p, cudaStream_t stream);
+cudaError_t launch_append_packed_f32(const AppendPlan& p, cudaStream_t stream);
+cudaError_t launch_append_packed_f16(const AppendPlan& p, cudaStream_t stream);
+cudaError_t launch_append_packed_bf16(const AppendPlan& p, cudaStream_t stream);
+
 }  // namespace tq

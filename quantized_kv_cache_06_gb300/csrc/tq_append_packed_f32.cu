@@ -1,0 +1,10 @@
+// fp32 rows of the append into packed pages (tq_append.cuh).
+#include "tq_append.cuh"
+
+namespace tq {
+
+cudaError_t launch_append_packed_f32(const AppendPlan& p, cudaStream_t stream) {
+  return launch_append_typed<float, true>(p, stream);
+}
+
+}  // namespace tq

@@ -348,3 +348,15 @@ def test_another_stream_and_a_replayed_graph(tq):
         work()
         torch.cuda.synchronize()
         assert torch.equal(q_out, got[0]) and torch.equal(live(kp), got[1])
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("rot", [64, 40])
+def test_infinities_of_channels_that_stay(tq, rot, pairs):
+    # a channel behind the rotated ones stays what it is, and so do the others
+    x = Inputs(tq, 4, 3, 1, 128, F32, rot, False, pairs)
+    want = tq.tq_norm_rope(x.q, None, **x.kw_args())[0].clone()
+    for at in (rot, rot + 1, 127, rot + 16):
+        x.q[2, 1, at] = float("inf")
+        want[2, 1, at] = float("inf")
+    assert torch.equal(tq.tq_norm_rope(x.q, None, **x.kw_args())[0], want)
