@@ -38,14 +38,17 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   // Stretches of eight groups share a token's coefficients and hide the copies' latency; shorter ones
   // where they leave warps idle.
   const int64_t warps = (int64_t)sms * kAppendCtas * kAppendWarps;
-  p.per_item = (int)std::max<int64_t>(1, std::min<int64_t>(8, a.num_tokens * total / (2 * warps)));
+  const int want = (int)std::max<int64_t>(1, std::min<int64_t>(8, a.num_tokens * total / (2 * warps)));
+  const int most = size == 2 ? 4 : 2;  // run_groups
+  p.run = std::min(want, most);
+  p.chain = want / p.run;
   // Blocks of four tokens where a side's groups of one token are fewer than a stretch.
-  p.block_tokens = p.per_item > 1 ? 4 : 1;
+  p.block_tokens = want > 1 ? 4 : 1;
   const int64_t blocks = (a.num_tokens + p.block_tokens - 1) / p.block_tokens;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   p.blocks = (int)blocks;
   for (int i = 0; i < 3; ++i) {
-    p.items[i] = (p.groups[i] * p.block_tokens + p.per_item - 1) / p.per_item;
+    p.items[i] = (p.groups[i] * p.block_tokens + p.run * p.chain - 1) / (p.run * p.chain);
     p.block_items += p.items[i];
   }
   const int64_t ctas = (blocks * p.block_items + kAppendWarps - 1) / kAppendWarps;

@@ -472,7 +472,10 @@ __device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Q
         add_if_greater(word, u, pt, 1u << (B * j));
       }
       half[h] = word + lowest;
-      if (steps > 1) {
+    }
+    if (steps > 1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         const float2 u = x[4 * c + 2 * h], v = x[4 * c + 2 * h + 1];
         half[h] = four_indices_slow<B>(u.x, u.y, v.x, v.y, below, point, mul, add, steps);
       }
@@ -522,52 +525,55 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-// Groups of rows in flight of a warp, 1 KB (16-bit types) or 2 KB each.
+// Groups of rows (1 KB each, fp32 2 KB) that a warp takes together: their copies, positions and
+// slots are under way while it works on the ones before.
 template <typename T>
-__host__ __device__ constexpr int stages() {
-  return sizeof(T) == 2 ? 4 : 3;
+__host__ __device__ constexpr int run_groups() {
+  return sizeof(T) == 2 ? 4 : 2;
 }
-// Dynamic shared memory: the copies in flight, and room to exchange pairs.
-template <typename T>
-__host__ __device__ constexpr int ring_bytes() {
-  return kAppendWarps * stages<T>() * 32 * 16 * (int)sizeof(T);
-}
+// Dynamic shared memory: the rows of two runs a warp, and room to exchange pairs.
+constexpr int kRingBytes = kAppendWarps * 2 * 4 * 1024;
 constexpr int kStageBytes = kAppendWarps * 512 * 4;
 
-// A stretch of the groups of heads of one side (0: q, 1: k, 2: v) over a block of tokens, token by
-// token, and where a warp stands in it.
-struct Walk {
-  int64_t t;        // token
-  int block, part;  // which stretch
+// A run: consecutive groups of heads of one side (0: q, 1: k, 2: v) over a block of tokens, token by
+// token.  A warp takes p.chain runs in a row, which share a token's coefficients where they are of one.
+struct Run {
+  int block, part, link;  // stretch of p.chain runs, and which of them
   int side, groups;
-  int g, left;      // group of heads, groups left
+  int64_t t;              // token and group of the run's first group
+  int g, n;               // groups of the run
   __device__ __forceinline__ void open(const AppendPlan& p) {
     side = part < p.items[0] ? 0 : part < p.items[0] + p.items[1] ? 1 : 2;
     groups = side == 0 ? p.groups[0] : side == 1 ? p.groups[1] : p.groups[2];
-    const int u = (part - (side > 0 ? p.items[0] : 0) - (side > 1 ? p.items[1] : 0)) * p.per_item;
-    const int n = (int)((uint32_t)u / (uint32_t)groups);
-    t = (int64_t)block * p.block_tokens + n;
-    g = u - n * groups;
-    const int tokens = (int)min((int64_t)(p.block_tokens - n), p.a.num_tokens - t);
-    left = min(p.per_item, tokens * groups - g);  // (none in a stretch behind the last token)
+    const int u = ((part - (side > 0 ? p.items[0] : 0) - (side > 1 ? p.items[1] : 0)) * p.chain + link) * p.run;
+    const int k = (int)((uint32_t)u / (uint32_t)groups);
+    t = (int64_t)block * p.block_tokens + k;
+    g = u - k * groups;
+    const int tokens = (int)min((int64_t)(p.block_tokens - k), p.a.num_tokens - t);
+    n = max(0, min(p.run, tokens * groups - g));
   }
+  // to the next run that has groups; n = 0 behind the last
   __device__ __forceinline__ void next(const AppendPlan& p) {
-    block += p.step_block;
-    part += p.step_part;
-    if (part >= p.block_items) part -= p.block_items, ++block;
-  }
-  __device__ __forceinline__ void step() {
-    --left;
-    if (++g == groups) g = 0, ++t;
+    do {
+      if (++link == p.chain) {
+        link = 0;
+        block += p.step_block;
+        part += p.step_part;
+        if (part >= p.block_items) part -= p.block_items, ++block;
+      }
+      n = 0;
+      if (block >= p.blocks) return;
+      open(p);
+    } while (n == 0);
   }
 };
 
 // PACK: some rows are packed (a dense call needs neither quantisers nor their code).  RING: rows are
-// 16-byte aligned; their copies run ahead of the arithmetic, across tokens, each lane's own elements
-// through its own shared memory, so that nothing has to be waited for but the copies.
+// 16-byte aligned and copied ahead, each lane's own elements through its own shared memory, so that
+// nothing has to be waited for but the copies.
 template <typename T, int LPR, int MODE, bool PACK, bool RING>
 __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(AppendPlan p) {
-  constexpr int D = 16 * LPR, RPW = 32 / LPR, S = stages<T>(), N = Raw<T>::N;
+  constexpr int D = 16 * LPR, RPW = 32 / LPR, U = run_groups<T>(), N = Raw<T>::N;
   constexpr int kGroup = RPW * D * (int)sizeof(T);  // bytes of a group's rows
   __shared__ Quant quant[PACK ? 2 : 1];
   __shared__ __align__(16) Shared shared[3];
@@ -575,57 +581,63 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
   const AppendArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LPR, row = lane / LPR;
-  unsigned char* ring = dynamic + warp * (S * N * 512) + lane * 16;
-  float* stage = reinterpret_cast<float*>(dynamic + (RING ? ring_bytes<T>() : 0)) + warp * 512 + row * D;
-  Walk it, ahead;
+  unsigned char* ring = dynamic + warp * (2 * U * N * 512) + lane * 16;
+  float* stage = reinterpret_cast<float*>(dynamic + (RING ? kRingBytes : 0)) + warp * 512 + row * D;
+  const int mine = (row * D + 8 * l) * (int)sizeof(T);  // this lane's elements in a group's rows
+  Run it;
   {
     const uint32_t item = blockIdx.x * kAppendWarps + warp;
     it.block = item / (uint32_t)p.block_items;
     it.part = (int)(item - (uint32_t)it.block * (uint32_t)p.block_items);
-    ahead.block = it.block;
-    ahead.part = it.part;
-    ahead.left = 0;
+    it.link = -1;
+    it.next(p);
   }
-  auto stride_of = [&](int side) { return (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) * (int64_t)sizeof(T); };
-  auto rows_of = [&](const Walk& w) {  // this lane's elements of the group's row
-    return static_cast<const unsigned char*>(w.side == 0 ? a.q : w.side == 1 ? a.k : a.v) + w.t * stride_of(w.side) +
-           w.g * kGroup + (row * D + 8 * l) * (int)sizeof(T);
-  };
   auto heads_of = [&](int side) { return side == 0 ? p.heads[0] : side == 1 ? p.heads[1] : p.heads[2]; };
-  const unsigned char* from = nullptr;
-  uint32_t slot_in = smem_address(ring), slot_out = slot_in;
-  const uint32_t ring_end = slot_in + S * N * 512;
-  auto produce = [&] {
-    if (ahead.left <= 0) {
-      while (ahead.block < p.blocks) {
-        ahead.open(p);
-        if (ahead.left > 0) break;
-        ahead.next(p);
-      }
-      if (ahead.left > 0) from = rows_of(ahead);
+  auto rows_of = [&](const Run& w) {
+    const int64_t stride = w.side == 0 ? a.q_stride : w.side == 1 ? a.k_stride : a.v_stride;
+    return static_cast<const unsigned char*>(w.side == 0 ? a.q : w.side == 1 ? a.k : a.v) +
+           w.t * stride * (int64_t)sizeof(T) + w.g * kGroup + mine;
+  };
+  // Copies a run's rows, and loads the position and the slot of group j's token in lane j.
+  int32_t pos_in = 0;
+  int64_t slot_in = 0;
+  auto fetch = [&](const Run& w, int half) {
+    if (w.n == 0) return;
+    int g = w.g;
+    {
+      int64_t t = w.t;
+      int gg = w.g + min(lane, w.n - 1);
+      while (gg >= w.groups) gg -= w.groups, ++t;
+      if (a.positions) pos_in = __ldg(a.positions + t);
+      if (PACK && w.side > 0) slot_in = __ldg(a.slots + t);
     }
-    if (ahead.left > 0) {
-      if (ahead.g * RPW + row < heads_of(ahead.side)) {
+    if constexpr (RING) {
+      const unsigned char* from = rows_of(w);
+      const int64_t wrap = (w.side == 0 ? a.q_stride : w.side == 1 ? a.k_stride : a.v_stride) * (int64_t)sizeof(T) -
+                           (int64_t)w.groups * kGroup;
+      const int heads = heads_of(w.side);
+      uint32_t to = smem_address(ring) + half * (U * N * 512);
 #pragma unroll
-        for (int i = 0; i < N; ++i) copy16(slot_in + i * 512, from + (i < N / 2 ? 0 : D / 2 * (int)sizeof(T)) + i % (N / 2) * 16);
+      for (int j = 0; j < U; ++j) {
+        if (j >= w.n) break;
+        if (g * RPW + row < heads) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) copy16(to + i * 512, from + (i < N / 2 ? 0 : D / 2 * (int)sizeof(T)) + i % (N / 2) * 16);
+        }
+        to += N * 512;
+        from += kGroup;
+        if (++g == w.groups) g = 0, from += wrap;
       }
-      slot_in += N * 512;
-      if (slot_in == ring_end) slot_in -= S * N * 512;
-      const bool last = ahead.g + 1 == ahead.groups;
-      from += kGroup;
-      if (last) from += stride_of(ahead.side) - ahead.groups * kGroup;
-      ahead.step();
-      if (ahead.left == 0) ahead.next(p);
     }
-    copies_commit();
   };
   if constexpr (RING) {
     // lanes of rows behind a side's last head keep what they held: ones, to begin with
 #pragma unroll
-    for (int i = 0; i < S * N; ++i) *reinterpret_cast<uint4*>(ring + i * 512) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-#pragma unroll 1
-    for (int i = 0; i < S - 1; ++i) produce();
+    for (int i = 0; i < 2 * U * N; ++i)
+      *reinterpret_cast<uint4*>(ring + i * 512) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
   }
+  fetch(it, 0);
+  copies_commit();
   const int mode = MODE == kAny ? (!a.cos_sin ? kPlain : a.interleaved ? kPairs : a.rot_dim == D ? kHalves : kStaged) : MODE;
   if constexpr (PACK) {
     if (warp == 0 && a.k_pages) build_quant(quant[0], a.k_centroids, 1 << a.k_bits, lane);
@@ -637,90 +649,134 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
                  PACK && side > 0 ? a.signs : nullptr, a.rot_dim, (warp & 1) * 32 + lane, 64);
   }
   __syncthreads();
-  for (; it.block < p.blocks; it.next(p)) {
-    it.open(p);
-    const int side = it.side, heads = heads_of(side);
-    const bool dense = !PACK || side == 0;
+
+  Coef f;
+  int64_t coef_t = -1;  // whose token's coefficients f holds, and of which side
+  int coef_side = -1, half = 0;
+  // One run: `use(x, factor, to, live)` takes each group's rows.
+  auto take = [&](const Run& w, int32_t pos_all, int64_t slot_all, bool dense, int bits, auto use) {
+    const int side = w.side, heads = heads_of(side);
     const bool normed = (side == 0 ? a.q_weight : side == 1 ? a.k_weight : nullptr) != nullptr;
-    Coef f;
-    if (side == 2 || mode == kPlain) plain_coef<LPR>(f.p, shared[side], l);
+    const bool turned = side < 2 && mode != kPlain;
+    if (!turned && coef_side != side) plain_coef<LPR>(f.p, shared[side], l);
+    int64_t t = w.t;
+    int g = w.g;
     bool fresh = true, skip = false;
-    unsigned char* to = nullptr;  // this lane's place in the group's row
-    for (; it.left > 0; it.step()) {
-      if (fresh || it.g == 0) {  // a token's position, slot and coefficients
-        fresh = skip = false;
-        const int64_t pos = a.positions ? (int64_t)a.positions[it.t] + a.position_offset : 0;
+    unsigned char* to = nullptr;  // this lane's place in the group's rows
+    const int step = dense ? kGroup : RPW * (D * bits / 8 + 4);
+    uint32_t at = smem_address(ring) + half * (U * N * 512);
+    const unsigned char* from = RING ? nullptr : rows_of(w);
+#pragma unroll 1
+    for (int j = 0; j < w.n; ++j) {
+      if (fresh) {  // a token's place and coefficients
+        fresh = false;
+        const int64_t pos = a.positions ? (int64_t)__shfl_sync(kFullMask, pos_all, j) + a.position_offset : 0;
         if (dense) {
           to = static_cast<unsigned char*>(side == 0 ? a.q_out : a.k_out) +
-               (it.t * (side == 0 ? a.q_out_stride : a.k_out_stride) + row * D + 8 * l) * (int64_t)sizeof(T) + it.g * kGroup;
+               t * (side == 0 ? a.q_out_stride : a.k_out_stride) * (int64_t)sizeof(T) + mine + g * kGroup;
+          skip = false;
         } else {
-          const int64_t slot = a.slots[it.t];
-          if (slot >= a.num_slots && pos >= 0 && a.status && lane == 0) atomicMax(a.status, (int32_t)kSlotOutOfRange);
+          const int64_t slot = __shfl_sync(kFullMask, slot_all, j);
           skip = slot < 0 || slot >= a.num_slots;
-          const int rb = D * (side == 1 ? a.k_bits : a.v_bits) / 8 + 4;
-          to = (side == 1 ? a.k_pages : a.v_pages) + (slot * heads + it.g * RPW + row) * rb;
+          if (skip && slot >= 0 && pos >= 0 && a.status && lane == 0) atomicMax(a.status, (int32_t)kSlotOutOfRange);
+          to = (side == 1 ? a.k_pages : a.v_pages) + (slot * heads + g * RPW + row) * (D * bits / 8 + 4);
         }
         skip |= pos < 0;  // a padding row
         if (a.cos_sin && pos >= a.num_positions) {
           if (a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
           skip = true;
         }
-        if (!skip && side < 2 && mode != kPlain)
+        if (!skip && turned && !(coef_t == t && coef_side == side))
           token_coef<LPR>(f, shared[side], mode, a.cos_sin + pos * a.rot_dim, a.rot_dim, p.table_vec, l);
+        coef_t = skip ? -1 : t;
+        coef_side = side;
       }
-      const bool live = it.g * RPW + row < heads;
-      Raw<T> raw;
-      if constexpr (RING) {
-        copies_wait<S - 2>();
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(raw.w[i].x), "=r"(raw.w[i].y), "=r"(raw.w[i].z), "=r"(raw.w[i].w)
-                       : "r"(slot_out + i * 512)
-                       : "memory");
-        slot_out += N * 512;
-        if (slot_out == ring_end) slot_out -= S * N * 512;
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
-        if (live) raw.load(reinterpret_cast<const T*>(rows_of(it)), D / 2, p.vec);
-      }
-      float2 x[8];
-      raw.get(x);
-      if constexpr (RING) produce();
+      const bool live = g * RPW + row < heads;
       if (!skip) {
+        Raw<T> raw;
+        if constexpr (RING) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw.w[i].x), "=r"(raw.w[i].y), "=r"(raw.w[i].z), "=r"(raw.w[i].w)
+                         : "r"(at + i * 512)
+                         : "memory");
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
+          if (live) raw.load(reinterpret_cast<const T*>(from), D / 2, p.vec);
+        }
+        float2 x[8];
+        raw.get(x);
         float factor = 1.f;
         if (normed) factor = norm_factor<LPR>(x, a.eps);
-        if (side == 2 || mode == kPlain) {
+        if (turned) {
+          apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage);
+        } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f.p[i]);
-        } else {
-          apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage);
         }
-        if (dense) {
-          if (normed) {
-            const float2 f2 = make_float2(factor, factor);
+        use(x, factor, to, live, normed);
+      }
+      at += N * 512;
+      to += step;
+      if (!RING) from += kGroup;
+      if (++g == w.groups) {
+        g = 0;
+        ++t;
+        fresh = true;
+        if (!RING)
+          from += (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) * (int64_t)sizeof(T) - (int64_t)w.groups * kGroup;
+      }
+    }
+  };
+  while (it.n > 0) {
+    const int32_t pos_all = pos_in;
+    const int64_t slot_all = slot_in;
+    Run ahead = it;
+    ahead.next(p);
+    fetch(ahead, half ^ 1);
+    copies_commit();
+    if constexpr (RING) copies_wait<1>();
+    if (!PACK || it.side == 0) {
+      take(it, pos_all, slot_all, true, 0, [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool normed) {
+        if (normed) {
+          const float2 f2 = make_float2(factor, factor);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f2);
-          }
-          Raw<T> out;
-          out.set(x);
-          if (live) out.store(reinterpret_cast<T*>(to), D / 2, RING || p.vec);
-          to += kGroup;
-        } else if constexpr (PACK) {
-          const int bits = side == 1 ? a.k_bits : a.v_bits;
+          for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f2);
+        }
+        Raw<T> out;
+        out.set(x);
+        if (live) out.store(reinterpret_cast<T*>(to), D / 2, RING || p.vec);
+      });
+    } else if constexpr (PACK) {
+      const Quant& q = quant[it.side - 1];
+      auto packed = [&](auto tag) {
+        constexpr int B = decltype(tag)::value;
+        take(it, pos_all, slot_all, false, B, [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool) {
+          encode_row<LPR, B>(x, factor, q, l, live ? to : nullptr);
+        });
+      };
+      const int bits = it.side == 1 ? a.k_bits : a.v_bits;
+      if constexpr (MODE == kAny) {  // (one body for all widths: this form is not for speed)
+        take(it, pos_all, slot_all, false, bits, [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool) {
           uint8_t* dst = live ? to : nullptr;
-          const Quant& q = quant[side - 1];
           switch (bits) {
             case 2: encode_row<LPR, 2>(x, factor, q, l, dst); break;
             case 3: encode_row<LPR, 3>(x, factor, q, l, dst); break;
             case 4: encode_row<LPR, 4>(x, factor, q, l, dst); break;
             default: encode_row<LPR, 5>(x, factor, q, l, dst); break;
           }
-          to += RPW * (D * bits / 8 + 4);
-        }
+        });
+      } else switch (bits) {
+        case 2: packed(std::integral_constant<int, 2>{}); break;
+        case 3: packed(std::integral_constant<int, 3>{}); break;
+        case 4: packed(std::integral_constant<int, 4>{}); break;
+        default: packed(std::integral_constant<int, 5>{}); break;
       }
     }
+    it = ahead;
+    half ^= 1;
   }
   if constexpr (RING) copies_wait<0>();
 }
@@ -729,9 +785,9 @@ template <typename T, int LPR, int MODE, bool PACK, bool RING>
 cudaError_t launch_append_kernel(const AppendPlan& p, cudaStream_t stream) {
   auto kern = append_kernel<T, LPR, MODE, PACK, RING>;
   const bool staged = p.a.cos_sin && !p.a.interleaved && p.a.rot_dim < p.a.head_dim;
-  const int smem = (RING ? ring_bytes<T>() : 0) + (staged ? kStageBytes : 0);
-  if (smem > 46 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = (RING ? kRingBytes : 0) + (staged ? kStageBytes : 0);
+  if (RING) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + kStageBytes);
     if (err != cudaSuccess) return err;
   }
   kern<<<p.grid, kAppendWarps * 32, smem, stream>>>(p);

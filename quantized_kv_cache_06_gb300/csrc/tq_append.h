@@ -53,12 +53,12 @@ constexpr int kAppendWarps = 8;
 constexpr int kAppendCtas = 2;  // CTAs of an SM
 
 // How a call is cut: blocks of tokens, each side's groups of 32 / (head_dim / 16) heads over a block
-// in stretches of `per_item`, a warp a stretch.
+// in stretches of chain * run groups, a warp a stretch.
 struct AppendPlan {
   AppendArgs a;
   int block_tokens, blocks;
-  int per_item;
-  int heads[3], groups[3], items[3];  // of q, k, v
+  int run, chain;             // groups of a run, runs of a stretch
+  int heads[3], groups[3], items[3];  // of q, k, v; items: stretches of a block
   int block_items;
   int step_block, step_part;  // from one stretch of a warp to its next
   int grid;
