@@ -605,7 +605,7 @@ tq_status tq_build_rope(int rot_dim, int64_t num_positions, double base, const d
  *   status_dev     device int32 or NULL: 0, or TQ_ERR_INVALID_ARG for a position >= num_positions
  *                  (nothing of that token is written)
  * One launch, asynchronous, graph-capturable; 16-byte aligned rows are faster.  Host-detected
- * errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim), TQ_ERR_CUDA. */
+ * errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (head_dim; more than 16384 heads), TQ_ERR_CUDA. */
 tq_status tq_norm_rope(const void* q, int64_t q_stride, int num_q_heads, const void* k, int64_t k_stride,
                        int num_k_heads, tq_dtype dtype, int64_t num_tokens, int head_dim, const int32_t* positions,
                        int position_offset, const float* cos_sin, int64_t num_positions, int rot_dim, int interleaved,

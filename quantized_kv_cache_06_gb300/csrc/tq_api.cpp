@@ -420,11 +420,14 @@ tq_status write_with_own_status(const char* name, cudaStream_t stream, Launch la
   return ok();
 }
 
+// Heads of a side of tq_norm_rope and tq_append_kv (their groups are counted in 16 bits).
+constexpr int kMaxHeads = 16384;
+
 // Shared by tq_norm_rope and tq_append_kv: types, positions, table and norms, into *out.
 tq_status rope_check(const char* name, tq_dtype dtype, int64_t num_tokens, int head_dim, const int32_t* positions,
                      int position_offset, const float* cos_sin, int64_t num_positions, int rot_dim, int interleaved,
                      const float* q_weight, const float* k_weight, float eps, tq::AppendArgs* out) {
-  if (num_tokens < 0 || num_positions < 0)
+  if (num_tokens < 0 || num_tokens > 0x7fffffffLL || num_positions < 0)
     return fail(TQ_ERR_INVALID_ARG, "%s: invalid sizes (tokens=%lld, positions=%lld)", name, (long long)num_tokens,
                 (long long)num_positions);
   if (!pow2_dim_ok(head_dim)) return fail(TQ_ERR_UNSUPPORTED, "head_dim %d: must be a power of two in [16, 256]", head_dim);
@@ -454,6 +457,7 @@ tq_status rope_check(const char* name, tq_dtype dtype, int64_t num_tokens, int h
 tq_status rows_check(const char* name, const char* what, const void* in, int64_t stride, int heads, const void* out,
                      int64_t out_stride, const tq::AppendArgs& a) {
   if (heads < 0) return fail(TQ_ERR_INVALID_ARG, "%s: %s: %d heads", name, what, heads);
+  if (heads > kMaxHeads) return fail(TQ_ERR_UNSUPPORTED, "%s: %s: more than %d heads", name, what, kMaxHeads);
   if (!in || heads == 0 || a.num_tokens == 0) return TQ_OK;
   if (!out) return fail(TQ_ERR_INVALID_ARG, "%s: %s has no output", name, what);
   const size_t size = dtype_size(a.dtype);
@@ -1228,6 +1232,7 @@ tq_status tq_append_kv(const void* q, int64_t q_stride, int num_q_heads, void* q
   if (st != TQ_OK) return st;
   st = rows_check(name, "q", q, q_stride, num_q_heads, q_out, q_out_stride, a);
   if (st != TQ_OK) return st;
+  if (num_kv_heads > kMaxHeads) return fail(TQ_ERR_UNSUPPORTED, "%s: more than %d heads", name, kMaxHeads);
   if (num_kv_heads < 1 || num_blocks < 0 || block_size < 1)
     return fail(TQ_ERR_INVALID_ARG, "%s: invalid sizes (kv_heads=%d, blocks=%lld, block_size=%d)", name, num_kv_heads,
                 (long long)num_blocks, block_size);

@@ -22,14 +22,30 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   AppendPlan p{};
   p.a = a;
   const int rpw = 32 / (a.head_dim / 16), size = a.dtype == kF32 ? 4 : 2, sms = device_sms();
-  p.heads[0] = a.num_q_heads;
-  p.heads[1] = a.num_k_heads;
-  p.heads[2] = a.num_v_heads;
+  const int heads[3] = {a.num_q_heads, a.num_k_heads, a.num_v_heads};
+  const void* in[3] = {a.q, a.k, a.v};
+  const int64_t stride[3] = {a.q_stride, a.k_stride, a.v_stride};
   int64_t total = 0;
+  p.full = 1;
   for (int i = 0; i < 3; ++i) {
-    p.groups[i] = (p.heads[i] + rpw - 1) / rpw;
-    total += p.groups[i];
+    AppendSide& s = p.side[i];
+    s.in = static_cast<const unsigned char*>(in[i]);
+    s.in_step = stride[i] * size;
+    s.heads = heads[i];
+    s.groups = (heads[i] + rpw - 1) / rpw;
+    s.inv_groups = s.groups > 1 ? (uint32_t)((0x100000000ull + s.groups - 1) / s.groups) : 0;
+    s.normed = (i == 0 ? a.q_weight : i == 1 ? a.k_weight : nullptr) != nullptr;
+    p.full &= heads[i] % rpw == 0;
+    total += s.groups;
   }
+  auto packed_row = [&](int bits) { return (int64_t)a.head_dim * bits / 8 + 4; };
+  p.side[0].out = static_cast<unsigned char*>(a.q_out);
+  p.side[0].out_step = a.q_out_stride * size;
+  p.side[1].out = a.k_pages ? a.k_pages : static_cast<unsigned char*>(a.k_out);
+  p.side[1].out_step = a.k_pages ? packed_row(a.k_bits) : a.k_out_stride * size;
+  p.side[2].out = a.v_pages;
+  p.side[2].out_step = packed_row(a.v_bits);
+  for (int i = 1; i < 3; ++i) p.side[i].slot_step = p.side[i].out_step * heads[i];
   if (a.num_tokens == 0 || total == 0) return cudaSuccess;
   p.vec = vec_ok(a.q, a.q_stride, size) && vec_ok(a.k, a.k_stride, size) && vec_ok(a.v, a.v_stride, size) &&
           vec_ok(a.q_out, a.q_out_stride, size) && vec_ok(a.k_out, a.k_out_stride, size);
@@ -45,10 +61,10 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   // Blocks of four tokens where a side's groups of one token are fewer than a stretch.
   p.block_tokens = want > 1 ? 4 : 1;
   const int64_t blocks = (a.num_tokens + p.block_tokens - 1) / p.block_tokens;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   p.blocks = (int)blocks;
   for (int i = 0; i < 3; ++i) {
-    p.items[i] = (p.groups[i] * p.block_tokens + p.run * p.chain - 1) / (p.run * p.chain);
+    p.items[i] = (p.side[i].groups * p.block_tokens + p.run * p.chain - 1) / (p.run * p.chain);
+    p.side[i].first = p.block_items;
     p.block_items += p.items[i];
   }
   const int64_t ctas = (blocks * p.block_items + kAppendWarps - 1) / kAppendWarps;

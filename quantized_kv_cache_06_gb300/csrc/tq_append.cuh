@@ -166,13 +166,8 @@ __device__ __forceinline__ uint32_t shared_u8(uint32_t at) {
   asm("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
-__device__ __forceinline__ float shared_f32(uint32_t at) {
-  float v;
-  asm("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ void add_if_greater(uint32_t& word, float u, float pt, uint32_t one) {
-  asm("{\n .reg .pred p;\n setp.gt.f32 p, %1, %2;\n @p add.u32 %0, %0, %3;\n}\n" : "+r"(word) : "f"(u), "f"(pt), "r"(one));
+__device__ __forceinline__ void add_if_greater(uint32_t& v, float u, float pt, uint32_t one) {
+  asm("{\n .reg .pred p;\n setp.gt.f32 p, %1, %2;\n @p add.u32 %0, %0, %3;\n}\n" : "+r"(v) : "f"(u), "f"(pt), "r"(one));
 }
 
 // ---- weights, signs and rotation: y[e] = x[e] p[e] + x[e'] s[e], e' the other channel of e's pair ----
@@ -366,32 +361,40 @@ __device__ __forceinline__ void fwht_row(float2 (&x)[8], int l) {
   }
 }
 
-// Quantiser of a codebook.  128 equal cells cover the decision points' span; a cell holds the
-// number of points in cells before it, so the index is that and one comparison for each point that
-// the cell itself may hold (`steps`, the most of any cell: 1 for a Lloyd-Max codebook).  Cells come
-// from one monotone function of u for points and coordinates alike, so its rounding does not
-// matter.  32 words of counts and at most 32 points: neither lookup has bank conflicts.
-struct Quant {
-  float point[32];      // decision points, then +inf
-  uint8_t below[128];   // 4 * (points in cells before this one)
-  float mul, add;       // span to [0, 1]
-  int steps;
+// Quantisers of the two packed sides.  128 equal cells cover the span of a codebook's decision
+// points; a cell holds the number of points in cells before it, so the index is that and one
+// comparison for each point that the cell itself may hold (`steps`, the most of any cell: 1 for a
+// Lloyd-Max codebook).  Cells come from one monotone function of u for points and coordinates
+// alike, so its rounding does not matter.  32 words of counts and at most 32 points a side: neither
+// lookup has bank conflicts.
+struct Quants {
+  float point[2][32];      // a side's decision points, then +inf
+  uint8_t below[2][128];   // offset in `point` of the first point that is in no earlier cell
+  float mul[2], add[2];    // span to [0, 1]
+  int steps[2];
 };
-// 127 times the clamped coordinate, as the bits of a subnormal: the cell's number
-__device__ __forceinline__ uint32_t cell_of(float u, float mul, float add) {
+// base + 127 t for the clamped t = u mul + add, as the bits of a subnormal (base: one too)
+__device__ __forceinline__ uint32_t cell_of(float u, float mul, float add, float base) {
   float t;
   asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(t) : "f"(u), "f"(mul), "f"(add));  // NaN: 0
-  return __float_as_uint(t * 0x1.fcp-143f);  // 127 * 2^-149
+  return __float_as_uint(fmaf(t, 0x1.fcp-143f, base));  // 127 * 2^-149
+}
+__device__ __forceinline__ uint2 cells_of(float2 u, float mul, float add, float base) {
+  float2 t;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(t.x) : "f"(u.x), "f"(mul), "f"(add));
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(t.y) : "f"(u.y), "f"(mul), "f"(add));
+  const float2 c = __ffma2_rn(t, make_float2(0x1.fcp-143f, 0x1.fcp-143f), make_float2(base, base));
+  return make_uint2(__float_as_uint(c.x), __float_as_uint(c.y));
 }
 // Set up by a warp from n = 2^bits ascending centroids (points: rounded midpoints).
-__device__ __forceinline__ void build_quant(Quant& q, const float* __restrict__ c, int n, int lane) {
+__device__ __forceinline__ void build_quant(Quants& q, int side, const float* __restrict__ c, int n, int lane) {
   const float pt = lane < n - 1 ? 0.5f * (__ldg(c + lane) + __ldg(c + lane + 1)) : __int_as_float(0x7f800000);
   const float lo = __shfl_sync(kFullMask, pt, 0), hi = __shfl_sync(kFullMask, pt, n - 2);
   const float mul = hi > lo ? 1.0f / (hi - lo) : 0.f, add = -lo * mul;
-  const int cell = lane < n - 1 ? (int)cell_of(pt, mul, add) : 128;
-  q.point[lane] = pt;
+  const int cell = lane < n - 1 ? (int)cell_of(pt, mul, add, 0.f) : 128;
+  q.point[side][lane] = pt;
   int most = 0;
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < 4; ++j) {
     int below = 0, here = 0;
     for (int k = 0; k < n - 1; ++k) {
@@ -399,89 +402,102 @@ __device__ __forceinline__ void build_quant(Quant& q, const float* __restrict__ 
       below += ck < lane + 32 * j;
       here += ck == lane + 32 * j;
     }
-    q.below[lane + 32 * j] = (uint8_t)(4 * below);
+    q.below[side][lane + 32 * j] = (uint8_t)(4 * (below + 32 * side));
     most = max(most, here);
   }
   most = __reduce_max_sync(kFullMask, most);
-  if (lane == 0) q.mul = mul, q.add = add, q.steps = most;
+  if (lane == 0) q.mul[side] = mul, q.add[side] = add, q.steps[side] = most;
 }
+// A side's quantiser in registers.
+struct Quant {
+  float mul, add, base;
+  int steps, side;
+  __device__ __forceinline__ void open(const Quants& q, int s) {
+    mul = q.mul[s];
+    add = q.add[s];
+    base = __int_as_float((int)smem_address(q.below[s]));
+    steps = q.steps[s];
+    side = s;
+  }
+};
 
 // Codebooks of which a cell holds several points (out of line; no Lloyd-Max codebook is one).
 template <int B>
-__device__ __noinline__ uint32_t four_indices_slow(float u0, float u1, float u2, float u3, uint32_t below, uint32_t point,
-                                                   float mul, float add, int steps) {
-  const float u[4] = {u0, u1, u2, u3};
-  uint32_t word = 0;
-#pragma unroll
+__device__ __noinline__ uint32_t fours_slow(float2 u, float2 v, Quant q, const float* points) {
+  const float x[4] = {u.x, u.y, v.x, v.y};
+  uint32_t sum = 0;
   for (int j = 0; j < 4; ++j) {
-    uint32_t four = shared_u8(below + cell_of(u[j], mul, add));
-    for (int k = 0; k < steps; ++k)
-      if (u[j] > shared_f32(point + four)) four += 4;
-    word += (four >> 2) << (B * j);
+    uint32_t offset = shared_u8(cell_of(x[j], q.mul, q.add, q.base));
+    for (int k = 0; k < q.steps; ++k)
+      if (x[j] > points[offset / 4]) offset += 4;
+    sum += offset << (B * j);
   }
-  return word;
+  return sum;
 }
 
 // Encodes rows of signed coordinates x, whose own norm is `factor` times theirs (all lanes of the
 // warp take part; `dst` null: nothing stored).
 template <int LPR, int B>
-__device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Quant& q, int l, uint8_t* dst) {
+__device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Quant& q, const float* points, int l,
+                                           uint8_t* dst) {
   constexpr int D = 16 * LPR, IB = D * B / 8;
-  float ss = row_sum<LPR>(sum_squares(x));
-  int ex = 0;
-  bool bad = false;
+  float ss = row_sum<LPR>(sum_squares(x)), back = 1.f;
   const bool odd = !(ss <= 0x1p100f) || ss < 0x1p-100f;
   if (__any_sync(kFullMask, odd)) {
     float2 y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = x[i];
-    int e;
-    ss = scale_rows<LPR>(y, ss, odd, nullptr, &e);
-    ex = e;
-    bad = !(ss <= 3.402823466e38f);  // a NaN or infinite coordinate: a zero row's indices
+    int ex;
+    ss = scale_rows<LPR>(y, ss, odd, nullptr, &ex);
+    const bool bad = !(ss <= 3.402823466e38f);  // a NaN or infinite coordinate: a zero row's indices
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = bad ? make_float2(0.f, 0.f) : y[i];
+    // the norm is ss rsqrt(ss) factor 2^ex below; zero rows and rows that are not finite keep theirs
+    back = pow2i(ex / 2);
+    factor *= pow2i(ex - ex / 2);
+    if (bad) back = factor = 1.f;
+    if (ss == 0.f) ss = 0x1p-126f, factor = 0.f;
   }
-  const float rs = (ss > 0.f && !bad) ? rsqrtf(ss) : 0.f;
-  const float nu = bad ? ss : scale_pow2(ss * rs * factor, ex);
+  float rs;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(ss));  // ss in the normal range, or not finite
+  float nu = ss * rs * factor * back;
+  if (!(ss <= 3.402823466e38f)) nu = ss, rs = 0.f;
   fwht_row<LPR>(x, l);
   constexpr float kInvSqrtD = LPR == 1 ? 0.25f : LPR == 2 ? 0.17677669529663689f : LPR == 4 ? 0.125f
                               : LPR == 8 ? 0.088388347648318447f : 0.0625f;
   const float inv = rs * kInvSqrtD;
   const float2 inv2 = make_float2(inv, inv);
-  const float mul = q.mul, add = q.add;
-  const int steps = q.steps;
-  const uint32_t below = smem_address(q.below), point = smem_address(q.point);
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], inv2);
+  // offsets of a side's points start at 128 side: four of them, B bits apart
+  const uint32_t start = 0u - (uint32_t)q.side * 128u * (1u + (1u << B) + (1u << (2 * B)) + (1u << (3 * B)));
+  uint32_t fours[4];  // 4 times four indices, B bits apart
+  if (q.steps == 1) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      fours[h] = start;
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float2 u = x[2 * h + j / 2];
+        const uint2 cell = cells_of(u, q.mul, q.add, q.base);
+        uint32_t o0 = shared_u8(cell.x), o1 = shared_u8(cell.y);
+        const char* at = reinterpret_cast<const char*>(points);
+        add_if_greater(o0, u.x, *reinterpret_cast<const float*>(at + o0), 4u);
+        add_if_greater(o1, u.y, *reinterpret_cast<const float*>(at + o1), 4u);
+        fours[h] += o0 * (1u << (B * j));
+        fours[h] += o1 * (1u << (B * j + B));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      fours[h] = start + fours_slow<B>(x[2 * h], x[2 * h + 1], q, points);
+  }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    // the eight indices as two words of four (4 B bits each)
-    uint32_t half[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t word = 0, lowest = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 pair = x[4 * c + 2 * h + j / 2];
-        const float u = (j & 1) ? pair.y : pair.x;
-        const uint32_t four = shared_u8(below + cell_of(u, mul, add));
-        const float pt = shared_f32(point + four);
-        if (j == 0) lowest = four >> 2;
-        else word += four * (1u << (B * j - 2));
-        add_if_greater(word, u, pt, 1u << (B * j));
-      }
-      half[h] = word + lowest;
-    }
-    if (steps > 1) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float2 u = x[4 * c + 2 * h], v = x[4 * c + 2 * h + 1];
-        half[h] = four_indices_slow<B>(u.x, u.y, v.x, v.y, below, point, mul, add, steps);
-      }
-    }
+    const uint32_t half[2] = {fours[2 * c], fours[2 * c + 1]};
     using Word = typename std::conditional<(B > 4), uint64_t, uint32_t>::type;
-    const Word word = (Word)half[0] | (Word)half[1] << (4 * B);
+    const Word word = (Word)(half[0] >> 2) | (Word)(half[1] >> 2) << (4 * B);
     // a chunk's B bytes: whole words where the lanes of a row's quad share them
     uint8_t* at = dst + c * (IB / 2) + B * l;
     if constexpr (B == 4) {
@@ -539,28 +555,31 @@ constexpr int kStageBytes = kAppendWarps * 512 * 4;
 // token.  A warp takes p.chain runs in a row, which share a token's coefficients where they are of one.
 struct Run {
   int block, part, link;  // stretch of p.chain runs, and which of them
-  int side, groups;
-  int64_t t;              // token and group of the run's first group
-  int g, n;               // groups of the run
+  int side;
+  int t, g, n;            // token and group of the run's first group; groups of the run
   __device__ __forceinline__ void open(const AppendPlan& p) {
     side = part < p.items[0] ? 0 : part < p.items[0] + p.items[1] ? 1 : 2;
-    groups = side == 0 ? p.groups[0] : side == 1 ? p.groups[1] : p.groups[2];
-    const int u = ((part - (side > 0 ? p.items[0] : 0) - (side > 1 ? p.items[1] : 0)) * p.chain + link) * p.run;
-    const int k = (int)((uint32_t)u / (uint32_t)groups);
-    t = (int64_t)block * p.block_tokens + k;
+    const int groups = p.side[side].groups;
+    const int u = (part - p.side[side].first) * p.chain * p.run;
+    const int k = groups == 1 ? u : (int)__umulhi((uint32_t)u, p.side[side].inv_groups);
+    t = block * p.block_tokens + k;
     g = u - k * groups;
-    const int tokens = (int)min((int64_t)(p.block_tokens - k), p.a.num_tokens - t);
-    n = max(0, min(p.run, tokens * groups - g));
+    n = max(0, min(p.run, min(p.block_tokens - k, (int)p.a.num_tokens - t) * groups - g));
   }
   // to the next run that has groups; n = 0 behind the last
   __device__ __forceinline__ void next(const AppendPlan& p) {
+    if (++link < p.chain) {  // where this one ended
+      const int groups = p.side[side].groups, last = min((block + 1) * p.block_tokens, (int)p.a.num_tokens);
+      g += n;
+      while (g >= groups) g -= groups, ++t;
+      n = max(0, min(p.run, (last - t) * groups - g));
+      if (n > 0) return;
+    }
     do {
-      if (++link == p.chain) {
-        link = 0;
-        block += p.step_block;
-        part += p.step_part;
-        if (part >= p.block_items) part -= p.block_items, ++block;
-      }
+      link = 0;
+      block += p.step_block;
+      part += p.step_part;
+      if (part >= p.block_items) part -= p.block_items, ++block;
       n = 0;
       if (block >= p.blocks) return;
       open(p);
@@ -569,19 +588,18 @@ struct Run {
 };
 
 // PACK: some rows are packed (a dense call needs neither quantisers nor their code).  RING: rows are
-// 16-byte aligned and copied ahead, each lane's own elements through its own shared memory, so that
-// nothing has to be waited for but the copies.
+// 16-byte aligned and copied ahead, 512 consecutive bytes at a time.
 template <typename T, int LPR, int MODE, bool PACK, bool RING>
-__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(AppendPlan p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(const __grid_constant__ AppendPlan p) {
   constexpr int D = 16 * LPR, RPW = 32 / LPR, U = run_groups<T>(), N = Raw<T>::N;
-  constexpr int kGroup = RPW * D * (int)sizeof(T);  // bytes of a group's rows
-  __shared__ Quant quant[PACK ? 2 : 1];
+  constexpr int kGroup = RPW * D * (int)sizeof(T);  // bytes of a group's rows: N * 512
+  __shared__ Quants quants;
   __shared__ __align__(16) Shared shared[3];
   extern __shared__ __align__(16) unsigned char dynamic[];
   const AppendArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LPR, row = lane / LPR;
-  unsigned char* ring = dynamic + warp * (2 * U * N * 512) + lane * 16;
+  unsigned char* ring = dynamic + warp * (2 * U * kGroup);
   float* stage = reinterpret_cast<float*>(dynamic + (RING ? kRingBytes : 0)) + warp * 512 + row * D;
   const int mine = (row * D + 8 * l) * (int)sizeof(T);  // this lane's elements in a group's rows
   Run it;
@@ -589,59 +607,62 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
     const uint32_t item = blockIdx.x * kAppendWarps + warp;
     it.block = item / (uint32_t)p.block_items;
     it.part = (int)(item - (uint32_t)it.block * (uint32_t)p.block_items);
-    it.link = -1;
-    it.next(p);
+    it.link = 0;
+    it.n = 0;
+    if (it.block < p.blocks) it.open(p);
+    if (it.n == 0) it.link = p.chain, it.next(p);
   }
-  auto heads_of = [&](int side) { return side == 0 ? p.heads[0] : side == 1 ? p.heads[1] : p.heads[2]; };
-  auto rows_of = [&](const Run& w) {
-    const int64_t stride = w.side == 0 ? a.q_stride : w.side == 1 ? a.k_stride : a.v_stride;
-    return static_cast<const unsigned char*>(w.side == 0 ? a.q : w.side == 1 ? a.k : a.v) +
-           w.t * stride * (int64_t)sizeof(T) + w.g * kGroup + mine;
-  };
-  // Copies a run's rows, and loads the position and the slot of group j's token in lane j.
+  // Copies a run's rows, and loads the position and the slot of the j-th token of the run in lane j.
   int32_t pos_in = 0;
   int64_t slot_in = 0;
-  auto fetch = [&](const Run& w, int half) {
+  auto fetch = [&](const Run& w, uint32_t to) {
     if (w.n == 0) return;
-    int g = w.g;
-    {
-      int64_t t = w.t;
-      int gg = w.g + min(lane, w.n - 1);
-      while (gg >= w.groups) gg -= w.groups, ++t;
-      if (a.positions) pos_in = __ldg(a.positions + t);
-      if (PACK && w.side > 0) slot_in = __ldg(a.slots + t);
+    const AppendSide& sd = p.side[w.side];
+    if (lane < U && w.t + lane < (int)a.num_tokens) {
+      if (a.positions) pos_in = __ldg(a.positions + w.t + lane);
+      if (PACK && w.side > 0) slot_in = __ldg(a.slots + w.t + lane);
     }
     if constexpr (RING) {
-      const unsigned char* from = rows_of(w);
-      const int64_t wrap = (w.side == 0 ? a.q_stride : w.side == 1 ? a.k_stride : a.v_stride) * (int64_t)sizeof(T) -
-                           (int64_t)w.groups * kGroup;
-      const int heads = heads_of(w.side);
-      uint32_t to = smem_address(ring) + half * (U * N * 512);
+      const unsigned char* from = sd.in + (int64_t)w.t * sd.in_step + w.g * kGroup + lane * 16;
+      int left = w.n, m = min(left, sd.groups - w.g);
+      int bytes = sd.heads * (D * (int)sizeof(T)) - w.g * kGroup - lane * 16;  // what the token has for this lane
+#pragma unroll 1
+      while (true) {  // a token's groups, one after the other
+        if (p.full) {
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        if (j >= w.n) break;
-        if (g * RPW + row < heads) {
+          for (int j = 0; j < U; ++j)
+            if (j < m) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) copy16(to + i * 512, from + (i < N / 2 ? 0 : D / 2 * (int)sizeof(T)) + i % (N / 2) * 16);
+              for (int i = 0; i < N; ++i) copy16(to + (j * N + i) * 512, from + (j * N + i) * 512);
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < U * N; ++i)
+            if (i < m * N && i * 512 < bytes) copy16(to + i * 512, from + i * 512);
         }
-        to += N * 512;
-        from += kGroup;
-        if (++g == w.groups) g = 0, from += wrap;
+        left -= m;
+        if (left == 0) break;
+        to += m * kGroup;
+        from += sd.in_step - (sd.groups - m) * kGroup;  // (the first token may have begun behind its first group)
+        m = min(left, sd.groups);
+        bytes = sd.heads * (D * (int)sizeof(T)) - lane * 16;
       }
     }
   };
+  const uint32_t ring_at = smem_address(ring) + lane * 16;
   if constexpr (RING) {
-    // lanes of rows behind a side's last head keep what they held: ones, to begin with
+    // what lies behind a side's last head keeps what it held: ones, to begin with
 #pragma unroll
     for (int i = 0; i < 2 * U * N; ++i)
-      *reinterpret_cast<uint4*>(ring + i * 512) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+      *reinterpret_cast<uint4*>(ring + lane * 16 + i * 512) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    __syncwarp();
   }
-  fetch(it, 0);
+  fetch(it, ring_at);
   copies_commit();
   const int mode = MODE == kAny ? (!a.cos_sin ? kPlain : a.interleaved ? kPairs : a.rot_dim == D ? kHalves : kStaged) : MODE;
   if constexpr (PACK) {
-    if (warp == 0 && a.k_pages) build_quant(quant[0], a.k_centroids, 1 << a.k_bits, lane);
-    if (warp == 1 && a.v_pages) build_quant(quant[1], a.v_centroids, 1 << a.v_bits, lane);
+    if (warp == 0 && a.k_pages) build_quant(quants, 0, a.k_centroids, 1 << a.k_bits, lane);
+    if (warp == 1 && a.v_pages) build_quant(quants, 1, a.v_centroids, 1 << a.v_bits, lane);
   }
   if (warp >= 2) {  // (six warps: two a side)
     const int side = (warp - 2) >> 1;
@@ -651,83 +672,82 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
   __syncthreads();
 
   Coef f;
-  int64_t coef_t = -1;  // whose token's coefficients f holds, and of which side
-  int coef_side = -1, half = 0;
-  // One run: `use(x, factor, to, live)` takes each group's rows.
-  auto take = [&](const Run& w, int32_t pos_all, int64_t slot_all, bool dense, int bits, auto use) {
-    const int side = w.side, heads = heads_of(side);
-    const bool normed = (side == 0 ? a.q_weight : side == 1 ? a.k_weight : nullptr) != nullptr;
-    const bool turned = side < 2 && mode != kPlain;
+  int coef_t = -1, coef_side = -1;  // whose coefficients f holds
+  uint32_t half = 0;                // bytes: the ring's half of the run
+  // One run: `use(x, factor, to, live, normed)` takes each group's rows.  TURNS: 1 the side is rotated,
+  // 0 it is not, -1 as the run has it.
+  auto take = [&](const Run& w, int32_t pos_all, int64_t slot_all, auto dense_tag, auto turns_tag, int step, auto use) {
+    constexpr bool dense = decltype(dense_tag)::value;
+    constexpr int kTurns = decltype(turns_tag)::value;
+    const int side = w.side;
+    const AppendSide& sd = p.side[side];
+    const bool normed = sd.normed;
+    const bool turned = kTurns >= 0 ? kTurns != 0 : side < 2 && mode != kPlain;
     if (!turned && coef_side != side) plain_coef<LPR>(f.p, shared[side], l);
-    int64_t t = w.t;
-    int g = w.g;
-    bool fresh = true, skip = false;
-    unsigned char* to = nullptr;  // this lane's place in the group's rows
-    const int step = dense ? kGroup : RPW * (D * bits / 8 + 4);
-    uint32_t at = smem_address(ring) + half * (U * N * 512);
-    const unsigned char* from = RING ? nullptr : rows_of(w);
+    // every lane's token: its position and slot
+    const int64_t pos = a.positions ? (int64_t)pos_all + a.position_offset : 0;
+    const bool far = a.cos_sin && pos >= a.num_positions;
+    const bool astray = !dense && slot_all >= a.num_slots && pos >= 0;
+    const uint32_t good = __ballot_sync(kFullMask, pos >= 0 && !far && (dense || (uint64_t)slot_all < (uint64_t)a.num_slots));
+    if (__any_sync(kFullMask, far || astray)) {
+      if (a.status && lane < U && w.t + lane < (int)a.num_tokens) {
+        if (far) atomicMax(a.status, (int32_t)kInvalidArg);
+        if (astray) atomicMax(a.status, (int32_t)kSlotOutOfRange);
+      }
+    }
+    int k = 0, g = w.g, left = w.n;  // token of the run, group, groups left
+    uint32_t at = smem_address(ring) + half + mine;
 #pragma unroll 1
-    for (int j = 0; j < w.n; ++j) {
-      if (fresh) {  // a token's place and coefficients
-        fresh = false;
-        const int64_t pos = a.positions ? (int64_t)__shfl_sync(kFullMask, pos_all, j) + a.position_offset : 0;
-        if (dense) {
-          to = static_cast<unsigned char*>(side == 0 ? a.q_out : a.k_out) +
-               t * (side == 0 ? a.q_out_stride : a.k_out_stride) * (int64_t)sizeof(T) + mine + g * kGroup;
-          skip = false;
-        } else {
-          const int64_t slot = __shfl_sync(kFullMask, slot_all, j);
-          skip = slot < 0 || slot >= a.num_slots;
-          if (skip && slot >= 0 && pos >= 0 && a.status && lane == 0) atomicMax(a.status, (int32_t)kSlotOutOfRange);
-          to = (side == 1 ? a.k_pages : a.v_pages) + (slot * heads + g * RPW + row) * (D * bits / 8 + 4);
-        }
-        skip |= pos < 0;  // a padding row
-        if (a.cos_sin && pos >= a.num_positions) {
-          if (a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
-          skip = true;
-        }
-        if (!skip && turned && !(coef_t == t && coef_side == side))
-          token_coef<LPR>(f, shared[side], mode, a.cos_sin + pos * a.rot_dim, a.rot_dim, p.table_vec, l);
-        coef_t = skip ? -1 : t;
-        coef_side = side;
-      }
-      const bool live = g * RPW + row < heads;
+    while (true) {  // a token's groups
+      const int m = min(left, sd.groups - g), t = w.t + k;
+      const bool skip = !((good >> k) & 1u);
+      unsigned char* to;  // this lane's place in the group's rows
+      if constexpr (dense) to = sd.out + (int64_t)t * sd.out_step + g * kGroup + mine;
+      else to = sd.out + __shfl_sync(kFullMask, slot_all, k) * sd.slot_step + (g * RPW + row) * (int)sd.out_step;
       if (!skip) {
-        Raw<T> raw;
-        if constexpr (RING) {
+        if (turned && !(coef_t == t && coef_side == side))
+          token_coef<LPR>(f, shared[side], mode, a.cos_sin + (uint64_t)__shfl_sync(kFullMask, (uint32_t)pos, k) * (uint32_t)a.rot_dim,
+                          a.rot_dim, p.table_vec, l);
+        coef_t = t;
+        coef_side = side;
+#pragma unroll 1
+        for (int j = 0; j < m; ++j) {
+          const bool live = p.full || (g + j) * RPW + row < sd.heads;
+          Raw<T> raw;
+          if constexpr (RING) {
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(raw.w[i].x), "=r"(raw.w[i].y), "=r"(raw.w[i].z), "=r"(raw.w[i].w)
-                         : "r"(at + i * 512)
-                         : "memory");
-        } else {
+            for (int i = 0; i < N; ++i)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(raw.w[i].x), "=r"(raw.w[i].y), "=r"(raw.w[i].z), "=r"(raw.w[i].w)
+                           : "r"(at + (i < N / 2 ? 0 : D / 2 * (int)sizeof(T)) + i % (N / 2) * 16)
+                           : "memory");
+            at += kGroup;
+          } else {
 #pragma unroll
-          for (int i = 0; i < N; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
-          if (live) raw.load(reinterpret_cast<const T*>(from), D / 2, p.vec);
+            for (int i = 0; i < N; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
+            if (live)
+              raw.load(reinterpret_cast<const T*>(sd.in + (int64_t)t * sd.in_step + (g + j) * kGroup + mine), D / 2, p.vec);
+          }
+          float2 x[8];
+          raw.get(x);
+          float factor = 1.f;
+          if (normed) factor = norm_factor<LPR>(x, a.eps);
+          if (turned) {
+            apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f.p[i]);
+          }
+          use(x, factor, to, live, normed);
+          to += step;
         }
-        float2 x[8];
-        raw.get(x);
-        float factor = 1.f;
-        if (normed) factor = norm_factor<LPR>(x, a.eps);
-        if (turned) {
-          apply_coef<LPR>(x, f, mode, a.rot_dim, l, stage);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f.p[i]);
-        }
-        use(x, factor, to, live, normed);
+      } else {
+        at += m * kGroup;
       }
-      at += N * 512;
-      to += step;
-      if (!RING) from += kGroup;
-      if (++g == w.groups) {
-        g = 0;
-        ++t;
-        fresh = true;
-        if (!RING)
-          from += (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) * (int64_t)sizeof(T) - (int64_t)w.groups * kGroup;
-      }
+      left -= m;
+      if (left == 0) break;
+      g = 0;
+      ++k;
     }
   };
   while (it.n > 0) {
@@ -735,48 +755,62 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
     const int64_t slot_all = slot_in;
     Run ahead = it;
     ahead.next(p);
-    fetch(ahead, half ^ 1);
+    if constexpr (RING) __syncwarp();  // the half to be copied to has been read by all lanes
+    fetch(ahead, ring_at + (half ^ (uint32_t)(U * kGroup)));
     copies_commit();
-    if constexpr (RING) copies_wait<1>();
+    if constexpr (RING) {
+      copies_wait<1>();
+      __syncwarp();
+    }
+    using Any = std::integral_constant<int, -1>;
+    using No = std::integral_constant<int, 0>;
+    using Turns = std::integral_constant<int, MODE == kAny ? -1 : 1>;
     if (!PACK || it.side == 0) {
-      take(it, pos_all, slot_all, true, 0, [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool normed) {
-        if (normed) {
-          const float2 f2 = make_float2(factor, factor);
+      take(it, pos_all, slot_all, std::true_type{}, Turns{}, kGroup,
+           [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool normed) {
+             if (normed) {
+               const float2 f2 = make_float2(factor, factor);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f2);
-        }
-        Raw<T> out;
-        out.set(x);
-        if (live) out.store(reinterpret_cast<T*>(to), D / 2, RING || p.vec);
-      });
+               for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], f2);
+             }
+             Raw<T> out;
+             out.set(x);
+             if (live) out.store(reinterpret_cast<T*>(to), D / 2, RING || p.vec);
+           });
     } else if constexpr (PACK) {
-      const Quant& q = quant[it.side - 1];
-      auto packed = [&](auto tag) {
-        constexpr int B = decltype(tag)::value;
-        take(it, pos_all, slot_all, false, B, [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool) {
-          encode_row<LPR, B>(x, factor, q, l, live ? to : nullptr);
-        });
-      };
-      const int bits = it.side == 1 ? a.k_bits : a.v_bits;
+      Quant q;
+      q.open(quants, it.side - 1);
+      const int bits = it.side == 1 ? a.k_bits : a.v_bits, step = RPW * (D * bits / 8 + 4);
+      const float* points = &quants.point[0][0];
       if constexpr (MODE == kAny) {  // (one body for all widths: this form is not for speed)
-        take(it, pos_all, slot_all, false, bits, [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool) {
-          uint8_t* dst = live ? to : nullptr;
-          switch (bits) {
-            case 2: encode_row<LPR, 2>(x, factor, q, l, dst); break;
-            case 3: encode_row<LPR, 3>(x, factor, q, l, dst); break;
-            case 4: encode_row<LPR, 4>(x, factor, q, l, dst); break;
-            default: encode_row<LPR, 5>(x, factor, q, l, dst); break;
-          }
-        });
-      } else switch (bits) {
-        case 2: packed(std::integral_constant<int, 2>{}); break;
-        case 3: packed(std::integral_constant<int, 3>{}); break;
-        case 4: packed(std::integral_constant<int, 4>{}); break;
-        default: packed(std::integral_constant<int, 5>{}); break;
+        take(it, pos_all, slot_all, std::false_type{}, Any{}, step,
+             [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool) {
+               uint8_t* dst = live ? to : nullptr;
+               switch (bits) {
+                 case 2: encode_row<LPR, 2>(x, factor, q, points, l, dst); break;
+                 case 3: encode_row<LPR, 3>(x, factor, q, points, l, dst); break;
+                 case 4: encode_row<LPR, 4>(x, factor, q, points, l, dst); break;
+                 default: encode_row<LPR, 5>(x, factor, q, points, l, dst); break;
+               }
+             });
+      } else {
+        auto packed = [&](auto tag) {
+          constexpr int B = decltype(tag)::value;
+          take(it, pos_all, slot_all, std::false_type{}, Any{}, step,
+               [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool) {
+                 encode_row<LPR, B>(x, factor, q, points, l, live ? to : nullptr);
+               });
+        };
+        switch (bits) {
+          case 2: packed(std::integral_constant<int, 2>{}); break;
+          case 3: packed(std::integral_constant<int, 3>{}); break;
+          case 4: packed(std::integral_constant<int, 4>{}); break;
+          default: packed(std::integral_constant<int, 5>{}); break;
+        }
       }
     }
     it = ahead;
-    half ^= 1;
+    half ^= (uint32_t)(U * kGroup);
   }
   if constexpr (RING) copies_wait<0>();
 }

@@ -108,21 +108,21 @@ def _append(tq, **kw):
     return tq.lib().tq_append_kv(*a.values(), None, None)
 
 
-BOTH = [(dict(n=-1), 1), (dict(d=96), 2), (dict(d=512), 2), (dict(t=3), 1), (dict(rot=0), 1), (dict(rot=130), 1),
+BOTH = [(dict(n=-1), 1), (dict(n=1 << 31), 1), (dict(hq=20000, qs=1 << 23, qos=1 << 23), 2), (dict(d=96), 2), (dict(d=512), 2), (dict(t=3), 1), (dict(rot=0), 1), (dict(rot=130), 1),
         (dict(rot=7), 1), (dict(rows=-1), 1), (dict(pos=None), 1), (dict(pos=DUMMY + 2), 1), (dict(table=DUMMY + 1), 1),
         (dict(qw=DUMMY + 4), 1), (dict(kw=DUMMY + 8), 1), (dict(eps=-1e-6), 1), (dict(eps=float("nan")), 1),
         (dict(eps=float("inf")), 1), (dict(hq=-1), 1), (dict(qo=None), 1), (dict(q=DUMMY + 1), 1), (dict(qo=DUMMY + 1), 1),
         (dict(qs=4095), 1), (dict(qos=4095), 1), (dict(qo=DUMMY, qos=5000), 1)]
 
 
-@pytest.mark.parametrize("kw,code", BOTH + [(dict(h=-1), 1), (dict(ko=None), 1), (dict(ks=1023), 1), (dict(k=DUMMY + 1), 1)])
+@pytest.mark.parametrize("kw,code", BOTH + [(dict(h=-1), 1), (dict(h=20000, ks=1 << 23, kos=1 << 23), 2), (dict(ko=None), 1), (dict(ks=1023), 1), (dict(k=DUMMY + 1), 1)])
 def test_norm_rope_host_refusals(tq, kw, code):
     assert _rope(tq, **kw) == code
     assert tq.lib().tq_last_error().decode()
 
 
 @pytest.mark.parametrize("kw,code", BOTH + [
-    (dict(h=0), 1), (dict(nb=-1), 1), (dict(bs=0), 1), (dict(kb=1), 2), (dict(vb=6), 2), (dict(slots=None), 1),
+    (dict(h=0), 1), (dict(h=20000, ks=1 << 23, vs=1 << 23), 2), (dict(nb=-1), 1), (dict(bs=0), 1), (dict(kb=1), 2), (dict(vb=6), 2), (dict(slots=None), 1),
     (dict(slots=DUMMY + 4), 1), (dict(kp=None), 1), (dict(vp=DUMMY + 8), 1), (dict(signs=None), 1), (dict(vc=None), 1),
     (dict(ks=1023), 1), (dict(vs=1000), 1), (dict(v=DUMMY + 1), 1), (dict(kc=DUMMY + 2), 1)])
 def test_append_host_refusals(tq, kw, code):
