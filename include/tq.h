@@ -655,8 +655,8 @@ size_t tq_verify_tree_workspace(int num_rows, int vocab_size, int num_seqs);
  *                     refused (or none there): a token is drawn from r with u_sample of the row.
  *                     At temperature 0 a child is kept when it carries the first largest logit.
  *
- *   logits         device, logits_dtype rows of vocab_size, row i at element i * logits_stride.
- *                  -inf and NaN have no probability.
+ *   logits         device, logits_dtype rows of vocab_size (at most 2^30), row i at element i *
+ *                  logits_stride. *                  -inf and NaN have no probability.
  *   draft_probs    device, draft_dtype rows as logits, or NULL; negative numbers and NaN count as 0
  *   row_start      device int32[num_seqs + 1], ascending (tq_plan_step's); rows behind the last
  *                  are not read.  A sequence may have none.

@@ -420,6 +420,8 @@ tq_status write_with_own_status(const char* name, cudaStream_t stream, Launch la
   return ok();
 }
 
+// Largest vocabulary of tq_verify_tree (positions in a row are 32-bit, with room for a piece).
+constexpr int kMaxVocab = 1 << 30;
 // Heads of a side of tq_norm_rope and tq_append_kv (their groups are counted in 16 bits).
 constexpr int kMaxHeads = 16384;
 
@@ -1280,7 +1282,7 @@ tq_status tq_append_kv(const void* q, int64_t q_stride, int num_q_heads, void* q
 }
 
 size_t tq_verify_tree_workspace(int num_rows, int vocab_size, int num_seqs) {
-  if (num_rows < 0 || vocab_size < 1 || num_seqs < 0) return 0;
+  if (num_rows < 0 || vocab_size < 1 || vocab_size > kMaxVocab || num_seqs < 0) return 0;
   return std::max<size_t>(256, tq::verify_workspace(num_rows, vocab_size, num_seqs));
 }
 
@@ -1291,7 +1293,7 @@ tq_status tq_verify_tree(const void* logits, tq_dtype logits_dtype, int64_t logi
                          int max_path, int32_t* path_lens, int32_t* next_token, void* workspace,
                          size_t workspace_bytes, int32_t* status_dev, void* stream) {
   const char* name = "tq_verify_tree";
-  if (num_rows < 0 || vocab_size < 1 || num_seqs < 0 || max_path < 1)
+  if (num_rows < 0 || vocab_size < 1 || vocab_size > kMaxVocab || num_seqs < 0 || max_path < 1)
     return fail(TQ_ERR_INVALID_ARG, "%s: invalid sizes (rows=%d, vocab=%d, seqs=%d, max_path=%d)", name, num_rows,
                 vocab_size, num_seqs, max_path);
   if (!dtype_ok(logits_dtype) || (draft_probs && !dtype_ok(draft_dtype)))

@@ -34,6 +34,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -66,7 +67,8 @@ struct VerifyWork {
   int pieces;
 };
 
-__host__ __device__ inline int pieces_of(int vocab) { return (int)(((int64_t)vocab + 7 + kPiece - 1) / kPiece); }
+// pieces of a row that starts `shift` elements behind an aligned address
+inline int pieces_of(int vocab, int shift) { return (int)(((int64_t)vocab + shift + kPiece - 1) / kPiece); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -107,6 +109,18 @@ __device__ __forceinline__ int seq_of(const int32_t* row_start, int seqs, int ro
   return lo;
 }
 
+// Two elements of a 32-bit word.
+template <typename T>
+__device__ __forceinline__ float2 two(uint32_t w);
+template <>
+__device__ __forceinline__ float2 two<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 two<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 // A lane's 32 logits of a piece: register v * VEC + e holds element first(v) + e of the row.
 template <typename T>
 struct Piece {
@@ -114,18 +128,25 @@ struct Piece {
   const T* row;
   int vocab;
   int shift;  // elements between the aligned address and the row's start
-  __device__ __forceinline__ Piece(const VerifyArgs& a, int64_t r) {
+  __device__ __forceinline__ void open(const VerifyArgs& a, int64_t r) {
     row = static_cast<const T*>(a.logits) + r * a.logits_stride;
     vocab = a.vocab;
     shift = (int)((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % VEC);
   }
-  __device__ __forceinline__ int64_t first(int piece, int v, int lane) const {
-    return (int64_t)piece * kPiece + v * 32 * VEC + lane * VEC - shift;
+  __device__ __forceinline__ int first(int piece, int v, int lane) const {
+    return piece * kPiece + v * 32 * VEC + lane * VEC - shift;
   }
   __device__ __forceinline__ void load(int piece, int lane, uint4 (&raw)[NV]) const {
+    const int begin = piece * kPiece - shift;
+    if (begin >= 0 && begin + kPiece <= vocab) {
+      const uint4* at = reinterpret_cast<const uint4*>(row + begin) + lane;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) raw[v] = at[32 * v];
+      return;
+    }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t i = first(piece, v, lane);
+      const int i = first(piece, v, lane);
       if (i >= 0 && i + VEC <= vocab) {
         raw[v] = *reinterpret_cast<const uint4*>(row + i);
       } else {
@@ -135,50 +156,113 @@ struct Piece {
       }
     }
   }
+  // elements e and e + 1 (e even) of vector v
+  static __device__ __forceinline__ float2 pair(const uint4 (&raw)[NV], int v, int e) {
+    const uint32_t w[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+    else return two<T>(w[e / 2]);
+  }
   static __device__ __forceinline__ float at(const uint4 (&raw)[NV], int v, int e) {
-    return to_f32<T>(reinterpret_cast<const T*>(&raw[v])[e]);
+    const float2 p = pair(raw, v, e & ~1);
+    return (e & 1) ? p.y : p.x;
+  }
+  // the lane's largest element (NaN left out; -inf where there is none)
+  static __device__ __forceinline__ float largest(const uint4 (&raw)[NV]) {
+    if constexpr (sizeof(T) == 4) {
+      float m = -CUDART_INF_F;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        m = fmaxf(m, fmaxf(fmaxf(at(raw, v, 0), at(raw, v, 1)), fmaxf(at(raw, v, 2), at(raw, v, 3))));
+      return m;
+    } else {
+      using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      T2 m[4];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const uint32_t w[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const T2 x = *reinterpret_cast<const T2*>(&w[k]);
+          m[k] = v == 0 ? x : __hmax2(m[k], x);
+        }
+      }
+      const T2 all = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+      const float2 f = two<T>(*reinterpret_cast<const uint32_t*>(&all));
+      return fmaxf(fmaxf(f.x, f.y), -CUDART_INF_F);
+    }
   }
 };
 
+__device__ __forceinline__ float2 weights(float2 x, float m, const Scale& s) {
+  float2 t = __fadd2_rn(x, make_float2(-m, -m));
+  t.x = fmaxf(t.x, s.least);
+  t.y = fmaxf(t.y, s.least);
+  const float2 y = __ffma2_rn(t, make_float2(s.hi, s.hi), __fmul2_rn(t, make_float2(s.lo, s.lo)));
+  return make_float2(ex2(y.x), ex2(y.y));
+}
+
 // ---------------------------------------------------------------- pieces
 
+// A warp takes `per` consecutive pieces, the next one's logits under way while it works on one:
+// a row's temperature is looked up once.
 template <typename T>
-__global__ void __launch_bounds__(kStatWarps * 32) verify_stats_kernel(VerifyArgs a, VerifyWork w) {
+__global__ void __launch_bounds__(kStatWarps * 32, sizeof(T) == 4 ? 2 : 3)
+verify_stats_kernel(VerifyArgs a, VerifyWork w, int64_t per) {
   using P = Piece<T>;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = a.num_seqs > 0 ? min(a.num_rows, max(0, a.row_start[a.num_seqs])) : 0;
   const int64_t items = (int64_t)rows * w.pieces;
-  for (int64_t item = (int64_t)blockIdx.x * kStatWarps + warp; item < items; item += (int64_t)gridDim.x * kStatWarps) {
-    const int r = (int)(item / w.pieces), piece = (int)(item - (int64_t)r * w.pieces);
-    const P p(a, r);
+  int64_t item = ((int64_t)blockIdx.x * kStatWarps + warp) * per;
+  const int64_t end = min(items, item + per);
+  if (item >= end) return;
+  int r = (int)(item / w.pieces), piece = (int)(item - (int64_t)r * w.pieces);
+  P p;
+  p.open(a, r);
+  uint4 next[P::NV];
+  p.load(piece, lane, next);
+  bool fresh = true, greedy = false;
+  Scale s;
+#pragma unroll 1
+  for (; item < end; ++item) {
     uint4 raw[P::NV];
-    p.load(piece, lane, raw);
-    float temp = 1.f;
-    if (a.temperature) temp = __ldg(a.temperature + seq_of(a.row_start, a.num_seqs, r));
-    float m = -CUDART_INF_F;
 #pragma unroll
-    for (int v = 0; v < P::NV; ++v)
-#pragma unroll
-      for (int e = 0; e < P::VEC; ++e) m = fmaxf(m, P::at(raw, v, e));
-    m = warp_max(m);
+    for (int v = 0; v < P::NV; ++v) raw[v] = next[v];
+    const int here = r, first = p.first(piece, 0, lane);
+    if (++piece == w.pieces) {
+      piece = 0;
+      ++r;
+      if (item + 1 < end) p.open(a, r);
+    }
+    if (item + 1 < end) p.load(piece, lane, next);
+    if (fresh) {
+      const float temp = a.temperature ? __ldg(a.temperature + seq_of(a.row_start, a.num_seqs, here)) : 1.f;
+      greedy = is_greedy(temp);
+      s = scale_of(greedy ? 1.f : temp);
+    }
+    fresh = r != here;
+    const float m = warp_max(P::largest(raw));
     float2 st = make_float2(m, 0.f);
-    if (is_greedy(temp)) {
+    if (greedy) {
       unsigned best = 0x7fffffffu;
 #pragma unroll
       for (int v = P::NV - 1; v >= 0; --v)
 #pragma unroll
         for (int e = P::VEC - 1; e >= 0; --e)
-          if (P::at(raw, v, e) == m) best = (unsigned)(p.first(piece, v, lane) + e);
+          if (P::at(raw, v, e) == m) best = (unsigned)(first + v * 32 * P::VEC + e);
       st.y = __uint_as_float(__reduce_min_sync(kFullMask, best));
     } else {
-      const Scale s = scale_of(temp);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 sum[4];
 #pragma unroll
       for (int v = 0; v < P::NV; ++v)
 #pragma unroll
-        for (int e = 0; e < P::VEC; ++e) sum[e & 3] += weight(P::at(raw, v, e), m, s);
-      st.y = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        for (int e = 0; e < P::VEC; e += 2) {
+          const int k = (v * P::VEC + e) / 2;
+          const float2 x = weights(P::pair(raw, v, e), m, s);
+          sum[k & 3] = k < 4 ? x : __fadd2_rn(sum[k & 3], x);
+        }
+      const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+      st.y = warp_sum(all.x + all.y);
     }
     if (lane == 0) w.stats[item] = st;
   }
@@ -210,10 +294,10 @@ __device__ __forceinline__ u64 part_of(float u, u64 total) {
 // The first element e of a piece whose running sum of value(v, e) passes `target`, by a warp;
 // where rounding leaves none, the last with a value.  -1: the piece has none.
 template <typename T, typename F>
-__device__ __forceinline__ int64_t find_in_piece(const Piece<T>& p, int piece, int lane, u64 target, F value) {
+__device__ __forceinline__ int find_in_piece(const Piece<T>& p, int piece, int lane, u64 target, F value) {
   constexpr int VEC = Piece<T>::VEC, NV = Piece<T>::NV;
   u64 run = 0;
-  int64_t last = -1;
+  int last = -1;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     u64 part = 0;
@@ -274,6 +358,16 @@ __device__ __forceinline__ int find_piece(int pieces, int lane, float u, u64& ta
 
 __device__ __forceinline__ u64 fixed(float v, float unit) { return (u64)__float2ll_rn(v * unit); }
 
+// A row's pieces, in the warp's shared memory where they fit: they are gone through several times.
+constexpr int kHeld = 256;
+__device__ __forceinline__ const float2* hold_stats(const VerifyWork& w, int64_t r, float2* room, int lane) {
+  const float2* st = w.stats + r * w.pieces;
+  if (w.pieces > kHeld) return st;
+  __syncwarp();
+  for (int k = lane; k < w.pieces; k += 32) room[k] = __ldcg(st + k);
+  __syncwarp();
+  return room;
+}
 // Largest logit of a row, from its pieces.
 __device__ __forceinline__ float row_top(const float2* st, int pieces, int lane) {
   float m = -CUDART_INF_F;
@@ -295,17 +389,17 @@ __device__ __forceinline__ float row_unit(int vocab) { return pow2i(62 - (32 - _
 
 // A token from p, by a warp.
 template <typename T>
-__device__ __forceinline__ int draw_token(const VerifyArgs& a, const VerifyWork& w, int64_t r, float top, const Scale& s,
-                                          float u, int lane) {
-  const float2* st = w.stats + r * w.pieces;
+__device__ __forceinline__ int draw_token(const VerifyArgs& a, const VerifyWork& w, const float2* st, int64_t r, float top,
+                                          const Scale& s, float u, int lane) {
   const float unit = row_unit(a.vocab);
   u64 target;
   const int piece = find_piece(w.pieces, lane, u, target,
                                [&](int k) { return fixed(st[k].y * weight(st[k].x, top, s), unit); });
-  const Piece<T> p(a, r);
+  Piece<T> p;
+  p.open(a, r);
   uint4 raw[Piece<T>::NV];
   p.load(piece, lane, raw);
-  int64_t i = find_in_piece<T>(p, piece, lane, target,
+  int i = find_in_piece<T>(p, piece, lane, target,
                                [&](int v, int e) { return fixed(weight(Piece<T>::at(raw, v, e), top, s), unit); });
   if (i < 0) {  // weights too small for the unit one by one, not together: the piece's largest
     float m = -CUDART_INF_F;
@@ -319,9 +413,9 @@ __device__ __forceinline__ int draw_token(const VerifyArgs& a, const VerifyWork&
       }
     const float all = warp_max(m);
     if (m != all) best = 0x7fffffffu;
-    i = __reduce_min_sync(kFullMask, best);
+    i = (int)__reduce_min_sync(kFullMask, best);
   }
-  return (int)i;
+  return i;
 }
 
 // Rows [r0, r0 + n) of a sequence; none where row_start is not ascending inside [0, num_rows].
@@ -332,23 +426,38 @@ __device__ __forceinline__ int rows_of(const VerifyArgs& a, int s, int& r0) {
   if (!ok && a.status && threadIdx.x == 0) atomicMax(a.status, (int32_t)kInvalidArg);
   return ok ? r1 - r0 : 0;
 }
-__device__ __forceinline__ int parent_of(const VerifyArgs& a, int r0, int i) {
-  return a.parents ? __ldg(a.parents + r0 + i) : i - 1;
-}
-
-// First child i >= from of node c that `match` accepts (-1: none), by a warp.
-template <typename F>
-__device__ __forceinline__ int next_child(const VerifyArgs& a, int r0, int n, int c, int from, int lane, F match) {
-  if (!a.parents && from > c + 1) return -1;  // a chain: one child a node
-  for (int b = from; b < n; b += 32) {
-    const int i = b + lane;
-    const bool hit = i < n && parent_of(a, r0, i) == c && match(i);
-    const unsigned mask = __ballot_sync(kFullMask, hit);
-    if (mask) return b + __ffs(mask) - 1;
-    if (!a.parents) return -1;
+// A sequence's tokens and parents, in shared memory up to kNodes of them.
+constexpr int kNodes = 256;
+struct Nodes {
+  const int32_t* tokens;
+  const int32_t* parents;  // null: a chain
+  int n;
+  // by a CTA of `threads` threads (a barrier follows before they are read)
+  __device__ __forceinline__ void open(const VerifyArgs& a, int r0, int rows, int32_t (*room)[kNodes], int threads) {
+    n = rows;
+    tokens = a.tokens + r0;
+    parents = a.parents ? a.parents + r0 : nullptr;
+    if (n > kNodes) return;
+    for (int i = threadIdx.x; i < n; i += threads) {
+      room[0][i] = tokens[i];
+      if (parents) room[1][i] = parents[i];
+    }
+    tokens = room[0];
+    if (parents) parents = room[1];
   }
-  return -1;
-}
+  __device__ __forceinline__ int parent(int i) const { return parents ? parents[i] : i - 1; }
+  // First child i >= from of node c that `match` accepts (-1: none), by a warp.
+  template <typename F>
+  __device__ __forceinline__ int next_child(int c, int from, int lane, F match) const {
+    if (!parents) return from == c + 1 && from < n && match(from) ? from : -1;  // a chain: one child a node
+    for (int b = from; b < n; b += 32) {
+      const int i = b + lane;
+      const unsigned mask = __ballot_sync(kFullMask, i < n && parents[i] == c && match(i));
+      if (mask) return b + __ffs(mask) - 1;
+    }
+    return -1;
+  }
+};
 
 // Temperatures out of range and parents that are no earlier nodes are reported.
 __device__ __forceinline__ void check_sequence(const VerifyArgs& a, int s, int r0, int n, int first, int step) {
@@ -370,22 +479,28 @@ __device__ __forceinline__ void check_sequence(const VerifyArgs& a, int s, int r
 
 template <typename T>
 __global__ void __launch_bounds__(kPickWarps * 32) verify_pick_kernel(VerifyArgs a, VerifyWork w) {
+  extern __shared__ float2 held[];  // kHeld of every warp
+  __shared__ int32_t node_room[2][kNodes], pick_room[kNodes];
   const int s = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   int r0;
   const int n = rows_of(a, s, r0);
   check_sequence(a, s, r0, n, threadIdx.x, blockDim.x);
+  Nodes nodes;
+  nodes.open(a, r0, n, node_room, blockDim.x);
   const float temp = a.temperature ? a.temperature[s] : 1.f;
+  const bool greedy = is_greedy(temp);
+  const Scale sc = scale_of(greedy ? 1.f : temp);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   bool none = false;
   for (int i = warp; i < n; i += warps) {
     const int64_t r = r0 + i;
-    const float2* st = w.stats + r * w.pieces;
+    const float2* st = hold_stats(w, r, held + warp * kHeld, lane);
     const float top = row_top(st, w.pieces, lane);
     int pick = -1;
     if (!has_distribution(top)) none = true;
-    else if (is_greedy(temp)) pick = row_best(st, w.pieces, lane, top);
-    else pick = draw_token<T>(a, w, r, top, scale_of(temp), a.u_sample[r], lane);
-    if (lane == 0) w.rows[r].pick = pick;
+    else if (greedy) pick = row_best(st, w.pieces, lane, top);
+    else pick = draw_token<T>(a, w, st, r, top, sc, a.u_sample[r], lane);
+    if (lane == 0) (n <= kNodes ? pick_room[i] : w.rows[r].pick) = pick;
   }
   if (none && a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
   __syncthreads();
@@ -397,9 +512,9 @@ __global__ void __launch_bounds__(kPickWarps * 32) verify_pick_kernel(VerifyArgs
     while (true) {
       if (lane == 0) path[len] = c;
       ++len;
-      next = w.rows[r0 + c].pick;
+      next = n <= kNodes ? pick_room[c] : w.rows[r0 + c].pick;
       if (next < 0 || len == a.max_path) break;
-      const int child = next_child(a, r0, n, c, c + 1, lane, [&](int i) { return a.tokens[r0 + i] == next; });
+      const int child = nodes.next_child(c, c + 1, lane, [&](int i) { return nodes.tokens[i] == next; });
       if (child < 0) break;
       c = child;
     }
@@ -421,7 +536,7 @@ __device__ __forceinline__ void load_draft(const VerifyArgs& a, const Piece<T>& 
   const Q* row = static_cast<const Q*>(a.draft) + r * a.draft_stride;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int64_t i = p.first(piece, v, lane);
+    const int i = p.first(piece, v, lane);
     constexpr int bytes = VEC * (int)sizeof(Q);
     constexpr int step = bytes < 16 ? bytes : 16, per = step / (int)sizeof(Q);
     if (i >= 0 && i + VEC <= a.vocab && reinterpret_cast<uintptr_t>(row + i) % step == 0) {
@@ -443,91 +558,107 @@ __device__ __forceinline__ void load_draft(const VerifyArgs& a, const Piece<T>& 
 
 constexpr float kRestUnit = 0x1p60f;  // sums of max(a p - b q, 0) are at most 1
 
+// A sequence of up to kNodes nodes: every CTA of its cluster works out all rows and nodes for itself
+// (the same numbers), so that only passes over a row need the others.  Longer ones share the work.
 template <typename T, typename Q>
-__global__ void __launch_bounds__(kDraftWarps * 32) verify_draft_kernel(VerifyArgs a, VerifyWork w) {
+__global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_draft_kernel(VerifyArgs a, VerifyWork w) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int s = blockIdx.x / ranks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int threads = ranks * kDraftWarps * 32, gtid = rank * kDraftWarps * 32 + (int)threadIdx.x;
+  constexpr int threads = kDraftWarps * 32;
   const int warps = ranks * kDraftWarps, gwarp = rank * kDraftWarps + warp;
+  __shared__ float2 held[kDraftWarps][kHeld];
+  __shared__ int32_t node_room[2][kNodes];
+  __shared__ float4 row_room[kNodes];
+  __shared__ float2 pq_room[kNodes];
+  __shared__ u64 rest_room[kHeld];
   __shared__ int todo;  // what the walk needs next: -1 nothing, else the row to subtract from
   __shared__ float coef[2];
   int r0;
   const int n = rows_of(a, s, r0);
-  check_sequence(a, s, r0, n, gtid, threads);
+  check_sequence(a, s, r0, n, rank * threads + threadIdx.x, ranks * threads);
+  Nodes nodes;
+  nodes.open(a, r0, n, node_room, threads);
+  const bool local = n <= kNodes;
+  float4* const rows = local ? row_room : reinterpret_cast<float4*>(w.rows + r0);
+  float2* const pqs = local ? pq_room : w.pq + r0;
   const float temp = a.temperature ? a.temperature[s] : 1.f;
   const bool greedy = is_greedy(temp);
   const Scale sc = scale_of(greedy ? 1.f : temp);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  // rows' largest logits and sums
+  // rows' largest logits, sums (their inverses) and, greedy, first largest logits
   bool none = false;
-  for (int i = gwarp; i < n; i += warps) {
-    const int64_t r = r0 + i;
-    const float2* st = w.stats + r * w.pieces;
+  for (int i = local ? warp : gwarp; i < n; i += local ? kDraftWarps : warps) {
+    const float2* st = hold_stats(w, r0 + i, held[warp], lane);
     const float top = row_top(st, w.pieces, lane);
-    RowInfo info{top, 0.f, -1, 0};
+    float inv = 0.f;
+    int pick = -1;
     if (!has_distribution(top)) {
       none = true;
     } else if (greedy) {
-      info.pick = row_best(st, w.pieces, lane, top);
+      pick = row_best(st, w.pieces, lane, top);
     } else {
       const float unit = row_unit(a.vocab);
       u64 sum = 0;
       for (int k = lane; k < w.pieces; k += 32) sum += fixed(st[k].y * weight(st[k].x, top, sc), unit);
-      info.inv = unit / (float)warp_sum_u64(sum);
-      info.pick = 0;
+      inv = unit / (float)warp_sum_u64(sum);
+      pick = 0;
     }
-    if (lane == 0) w.rows[r] = info;
+    if (lane == 0) rows[i] = make_float4(top, inv, __int_as_float(pick), 0.f);
   }
   if (none && a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
-  cluster.sync();
   // p and q of every drafted token
-  for (int i = 1 + gtid; i < n; i += threads) {
-    const int up = parent_of(a, r0, i), tok = a.tokens[r0 + i];
+  auto settle = [&] {
+    if (local) __syncthreads();
+    else cluster.sync();
+  };
+  settle();
+  for (int i = 1 + (local ? (int)threadIdx.x : rank * threads + (int)threadIdx.x); i < n; i += local ? threads : ranks * threads) {
+    const int up = nodes.parent(i), tok = nodes.tokens[i];
     float2 pq = make_float2(-1.f, 0.f);  // never kept
     if (up >= 0 && up < i && tok >= 0 && tok < a.vocab) {
       const int64_t r = r0 + up;
-      const float4 info = __ldcg(reinterpret_cast<const float4*>(w.rows + r));
+      const float4 info = rows[up];
       const int pick = __float_as_int(info.z);
       if (greedy) {
         pq.x = pick == tok ? 1.f : -1.f;
       } else if (pick >= 0) {
         const float x = to_f32<T>(static_cast<const T*>(a.logits)[r * a.logits_stride + tok]);
-        pq.x = weight(x, info.x, sc) * info.y;
         pq.y = fmaxf(to_f32<Q>(static_cast<const Q*>(a.draft)[r * a.draft_stride + tok]), 0.f);
+        pq.x = weight(x, info.x, sc) * info.y;
       }
     }
-    w.pq[r0 + i] = pq;
+    pqs[i] = pq;
   }
-  cluster.sync();
+  settle();
   // the walk, by every CTA's first warp alike; all CTAs share the sums over a row
-  int c = 0, len = 0, from = 1, pass = 0;
+  int c = 0, from = 1, pass = 0;
   float ca = 1.f, cb = 0.f;      // r = max(ca p - cb q, 0) at node c
   float da = 1.f, db = 0.f;      // the coefficients whose sums the last pass took (db 0: none at c)
   bool again = false;
   int32_t* path = a.path + (int64_t)s * a.max_path;
-  float4 info = n > 0 ? __ldcg(reinterpret_cast<const float4*>(w.rows + r0)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 info = n > 0 ? rows[0] : make_float4(0.f, 0.f, 0.f, 0.f);
   if (rank == 0 && warp == 0 && lane == 0 && n > 0) path[0] = 0;
-  len = n > 0 ? 1 : 0;
+  int len = n > 0 ? 1 : 0;
   while (true) {
     if (warp == 0) {
       int need = -1;
       while (n > 0 && !again && __float_as_int(info.z) >= 0 && len < a.max_path) {
-        const int child = next_child(a, r0, n, c, from, lane, [](int) { return true; });
+        const int child = nodes.next_child(c, from, lane, [](int) { return true; });
         if (child < 0) break;
-        const float2 pq = __ldcg(w.pq + r0 + child);
+        const float2 pq = pqs[child];
         const float r = fmaf(ca, pq.x, -cb * pq.y);
         if (greedy ? pq.x > 0.f : (r > 0.f && a.u_accept[r0 + child] * pq.y < r)) {
           c = child;
           from = c + 1;
           ca = da = 1.f;
           cb = db = 0.f;
-          info = __ldcg(reinterpret_cast<const float4*>(w.rows + r0 + c));
+          info = rows[c];
           if (rank == 0 && lane == 0) path[len] = c;
           ++len;
         } else {
           from = child + 1;
-          const int tok = a.tokens[r0 + child];
+          const int tok = nodes.tokens[child];
           if (greedy || tok < 0 || tok >= a.vocab) continue;  // not drawn from q
           da = ca, db = cb + 1.f;
           need = c;
@@ -546,8 +677,9 @@ __global__ void __launch_bounds__(kDraftWarps * 32) verify_draft_kernel(VerifyAr
     if (row < 0) break;
     const float pa = coef[0], pb = coef[1];
     const int64_t r = r0 + row;
-    const float top = __ldcg(&w.rows[r].max);
-    const Piece<T> p(a, r);
+    const float top = rows[row].x;
+    Piece<T> p;
+    p.open(a, r);
     u64* rest = w.rest + ((int64_t)(pass & 1) * a.num_seqs + s) * w.pieces;
     for (int k = gwarp; k < w.pieces; k += warps) {
       uint4 raw[Piece<T>::NV];
@@ -567,7 +699,12 @@ __global__ void __launch_bounds__(kDraftWarps * 32) verify_draft_kernel(VerifyAr
     cluster.sync();
     if (warp == 0) {
       u64 sum = 0;
-      for (int k = lane; k < w.pieces; k += 32) sum += __ldcg(rest + k);
+      for (int k = lane; k < w.pieces; k += 32) {
+        const u64 x = __ldcg(rest + k);
+        if (w.pieces <= kHeld) rest_room[k] = x;
+        sum += x;
+      }
+      __syncwarp();
       sum = warp_sum_u64(sum);
       if (again) {
         again = false;
@@ -588,23 +725,27 @@ __global__ void __launch_bounds__(kDraftWarps * 32) verify_draft_kernel(VerifyAr
     const float u = a.u_sample[r];
     if (greedy) {
       next = __float_as_int(info.z);
-    } else if (db == 0.f) {
-      next = draw_token<T>(a, w, r, info.x, sc, u, lane);
     } else {
-      const u64* rest = w.rest + ((int64_t)((pass - 1) & 1) * a.num_seqs + s) * w.pieces;
-      u64 target;
-      const int piece = find_piece(w.pieces, lane, u, target, [&](int k) { return __ldcg(rest + k); });
-      const Piece<T> p(a, r);
-      uint4 raw[Piece<T>::NV];
-      float q[32];
-      p.load(piece, lane, raw);
-      load_draft<T, Q>(a, p, r, piece, lane, q);
-      const float pa = da * info.y;
-      const int64_t i = find_in_piece<T>(p, piece, lane, target, [&](int v, int e) {
-        return fixed(fmaxf(fmaf(pa, weight(Piece<T>::at(raw, v, e), info.x, sc), -db * q[v * Piece<T>::VEC + e]), 0.f),
-                     kRestUnit);
-      });
-      next = i >= 0 ? (int)i : draw_token<T>(a, w, r, info.x, sc, u, lane);  // (no weight above the unit)
+      int i = -1;
+      if (db > 0.f) {
+        const u64* rest = w.pieces <= kHeld ? rest_room : w.rest + ((int64_t)((pass - 1) & 1) * a.num_seqs + s) * w.pieces;
+        u64 target;
+        const int piece = find_piece(w.pieces, lane, u, target, [&](int k) { return rest[k]; });
+        Piece<T> p;
+        p.open(a, r);
+        uint4 raw[Piece<T>::NV];
+        float q[32];
+        p.load(piece, lane, raw);
+        load_draft<T, Q>(a, p, r, piece, lane, q);
+        const float pa = da * info.y;
+        i = find_in_piece<T>(p, piece, lane, target, [&](int v, int e) {
+          return fixed(fmaxf(fmaf(pa, weight(Piece<T>::at(raw, v, e), info.x, sc), -db * q[v * Piece<T>::VEC + e]), 0.f),
+                       kRestUnit);
+        });
+      }
+      // from p where nothing was refused (or no weight is above the unit)
+      if (i < 0) i = draw_token<T>(a, w, hold_stats(w, r, held[0], lane), r, info.x, sc, u, lane);
+      next = i;
     }
   }
   for (int j = len + lane; j < a.max_path; j += 32) path[j] = -1;
@@ -614,9 +755,10 @@ __global__ void __launch_bounds__(kDraftWarps * 32) verify_draft_kernel(VerifyAr
   }
 }
 
+// Laid out for rows at any address.
 VerifyWork layout(void* workspace, int rows, int vocab, int seqs, size_t* bytes) {
   VerifyWork w{};
-  w.pieces = pieces_of(vocab);
+  w.pieces = pieces_of(vocab, 7);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t first = at;
@@ -633,11 +775,12 @@ VerifyWork layout(void* workspace, int rows, int vocab, int seqs, size_t* bytes)
 
 // The second kernel is a programmatic dependent of the first: its set-up overlaps it.
 template <typename K>
-cudaError_t launch_after(K kern, int grid, int threads, int cluster, cudaStream_t stream, const VerifyArgs& a,
+cudaError_t launch_after(K kern, int grid, int threads, int cluster, int smem, cudaStream_t stream, const VerifyArgs& a,
                          const VerifyWork& w) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -654,26 +797,33 @@ cudaError_t launch_after(K kern, int grid, int threads, int cluster, cudaStream_
 }
 
 template <typename T>
-cudaError_t launch_verify_typed(const VerifyArgs& a, const VerifyWork& w, cudaStream_t stream) {
-  const int64_t ctas = ((int64_t)a.num_rows * w.pieces + kStatWarps - 1) / kStatWarps;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)device_sms() * 8));
-  verify_stats_kernel<T><<<grid, kStatWarps * 32, 0, stream>>>(a, w);
+cudaError_t launch_verify_typed(const VerifyArgs& a, VerifyWork w, cudaStream_t stream) {
+  const int sms = device_sms();
+  // rows that all start at 16-byte boundaries have no piece more
+  const bool even = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && (a.num_rows < 2 || a.logits_stride * sizeof(T) % 16 == 0);
+  w.pieces = pieces_of(a.vocab, even ? 0 : 16 / (int)sizeof(T) - 1);
+  const int64_t items = (int64_t)a.num_rows * w.pieces, resident = (int64_t)sms * (sizeof(T) == 4 ? 2 : 3) * kStatWarps;
+  const int64_t per = std::max<int64_t>(1, (items + resident - 1) / resident);
+  const int64_t ctas = ((items + per - 1) / per + kStatWarps - 1) / kStatWarps;
+  verify_stats_kernel<T><<<(int)std::max<int64_t>(1, ctas), kStatWarps * 32, 0, stream>>>(a, w, per);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   count_launches(1);
   if (!a.draft) {
-    // a warp a row of an average sequence
-    const int warps = std::max(1, std::min(kPickWarps, (a.num_rows + a.num_seqs - 1) / a.num_seqs));
-    return launch_after(verify_pick_kernel<T>, a.num_seqs, warps * 32, 1, stream, a, w);
+    // twice the warps of an average sequence's rows: ragged ones take one turn too
+    const int warps = std::max(1, std::min(kPickWarps, 2 * ((a.num_rows + a.num_seqs - 1) / a.num_seqs)));
+    return launch_after(verify_pick_kernel<T>, a.num_seqs, warps * 32, 1, warps * kHeld * (int)sizeof(float2), stream, a, w);
   }
-  // no more CTAs a sequence than its rows' pieces keep busy
+  // as many CTAs a sequence as run at once, and as its rows' pieces keep busy
   int ctas_seq = kDraftCtas;
-  while (ctas_seq > 1 && ctas_seq * kDraftWarps > 2 * w.pieces) ctas_seq /= 2;
-  const int dgrid = a.num_seqs * ctas_seq, threads = kDraftWarps * 32;
+  while (ctas_seq > 1 && ((int64_t)a.num_seqs * ctas_seq > 2 * sms || ctas_seq * kDraftWarps >= 2 * w.pieces)) ctas_seq /= 2;
+  const int64_t dgrid = (int64_t)a.num_seqs * ctas_seq;
+  if (dgrid > 0x7fffffff) return cudaErrorInvalidValue;
+  const int threads = kDraftWarps * 32;
   switch (a.draft_dtype) {
-    case kF32: return launch_after(verify_draft_kernel<T, float>, dgrid, threads, ctas_seq, stream, a, w);
-    case kF16: return launch_after(verify_draft_kernel<T, __half>, dgrid, threads, ctas_seq, stream, a, w);
-    case kBF16: return launch_after(verify_draft_kernel<T, __nv_bfloat16>, dgrid, threads, ctas_seq, stream, a, w);
+    case kF32: return launch_after(verify_draft_kernel<T, float>, (int)dgrid, threads, ctas_seq, 0, stream, a, w);
+    case kF16: return launch_after(verify_draft_kernel<T, __half>, (int)dgrid, threads, ctas_seq, 0, stream, a, w);
+    case kBF16: return launch_after(verify_draft_kernel<T, __nv_bfloat16>, (int)dgrid, threads, ctas_seq, 0, stream, a, w);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -84,7 +84,7 @@ def _verify(tq, **kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(r=-1), dict(v=0), dict(s=-1), dict(mp=0), dict(xt=3), dict(qt=-1), dict(x=None), dict(start=None), dict(tok=None),
+    dict(r=-1), dict(v=0), dict(v=(1 << 30) + 1, xs=1 << 31, qs=1 << 31), dict(s=-1), dict(mp=0), dict(xt=3), dict(qt=-1), dict(x=None), dict(start=None), dict(tok=None),
     dict(us=None), dict(ua=None), dict(path=None), dict(lens=None), dict(nxt=None), dict(xs=63), dict(qs=63),
     dict(x=DUMMY + 1), dict(q=DUMMY + 2), dict(start=DUMMY + 2), dict(up=DUMMY + 1), dict(temp=DUMMY + 3),
     dict(ua=DUMMY + 2), dict(path=DUMMY + 2), dict(wb=1000), dict(ws=None), dict(ws=DUMMY + 16)])
@@ -95,7 +95,7 @@ def test_verify_host_refusals(tq, kw):
 
 def test_workspace_query(tq):
     f = tq.tq_verify_tree_workspace
-    assert f(-1, 8, 1) == 0 and f(1, 0, 1) == 0 and f(1, 8, -1) == 0
+    assert f(1, (1 << 30) + 1, 1) == 0 and f(-1, 8, 1) == 0 and f(1, 0, 1) == 0 and f(1, 8, -1) == 0
     assert 256 <= f(0, 1, 0) <= f(1, 8, 1) <= f(64, 131072, 8)
 
 
