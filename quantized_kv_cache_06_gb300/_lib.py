@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -300,27 +301,36 @@ def tq_dequant_rows(pages: torch.Tensor, slots: torch.Tensor, signs: torch.Tenso
     nu * R^T c[idx] for slot >= 0, zeros for slot < 0.  pages [NB, bs, H, RB] uint8,
     slots [T] int64.  With check=True the call synchronises and raises
     TQError(TQ_ERR_SLOT_OUT_OF_RANGE) when a slot lies past the pages.  Returns `out`."""
-    dev = _need_cuda("tq_dequant_rows", pages, slots, signs, centroids)
-    if pages.dim() != 4 or slots.dim() != 1 or pages.dtype != torch.uint8 or slots.dtype != torch.int64:
+    index = pages.get_device()
+    if pages.dim() != 4 or slots.dim() != 1 or pages.dtype is not torch.uint8 or slots.dtype is not torch.int64:
         raise ValueError("tq_dequant_rows: pages uint8 [NB, bs, H, RB] and slots int64 [T] expected")
     nb, bs, h, rb = pages.shape
-    d = signs.numel()
+    d, t = signs.numel(), slots.numel()
     bits = _bits_from_centroids(centroids)
-    _need_f32("tq_dequant_rows", d, signs, centroids)
-    if rb != tq_row_bytes(d, bits):
-        raise ValueError(f"tq_dequant_rows: pages row bytes {rb} != RB({d}, {bits})")
-    t = slots.numel()
+    if not (index >= 0 and slots.get_device() == index and signs.get_device() == index and
+            centroids.get_device() == index and pages.is_contiguous() and slots.is_contiguous() and
+            signs.is_contiguous() and centroids.is_contiguous()):
+        _need_cuda("tq_dequant_rows", pages, slots, signs, centroids)
+    if signs.dtype is not torch.float32 or centroids.dtype is not torch.float32:
+        _need_f32("tq_dequant_rows", d, signs, centroids)
+    if d % 16 or rb * 8 != d * bits + 32 or not 2 <= bits <= 5:  # as tq_row_bytes has it for its head dims
+        if rb != tq_row_bytes(d, bits):
+            raise ValueError(f"tq_dequant_rows: pages row bytes {rb} != RB({d}, {bits})")
     if out is None:
-        out = torch.empty(t, h, d, dtype=out_dtype, device=dev)
-    if tuple(out.shape) != (t, h, d) or out.dtype not in _DTYPES:
+        out = torch.empty((t, h, d), dtype=out_dtype, device=pages.device)
+    if out.shape != (t, h, d) or out.dtype not in _DTYPES:
         raise ValueError(f"tq_dequant_rows: out must be [{t}, {h}, {d}] f32/f16/bf16")
-    _need_cuda("tq_dequant_rows", pages, out)
-    _need_status("tq_dequant_rows", status, dev)
-    if status is None:
-        status = _status_buffer(dev)
-    with torch.cuda.device(dev):
-        _check(lib().tq_dequant_rows(_ptr(pages), bits, nb, bs, h, d, _ptr(slots), t, _ptr(signs), _ptr(centroids),
-                                     _ptr(out), _DTYPES[out.dtype], _ptr(status), _stream(dev)))
+    if out.get_device() != index or not out.is_contiguous():
+        _need_cuda("tq_dequant_rows", pages, out)
+    _need_status("tq_dequant_rows", status, pages.device)
+    if status is None and check:
+        status = _status_buffer(pages.device)
+    with _on(index):
+        code = lib().tq_dequant_rows(pages.data_ptr(), bits, nb, bs, h, d, slots.data_ptr(), t, signs.data_ptr(),
+                                     centroids.data_ptr(), out.data_ptr(), _DTYPES[out.dtype], _ptr(status),
+                                     _stream_ptr(index))
+    if code != TQ_OK:
+        _check(code)
     if check:
         raise_for_device_status(status)
     return out
@@ -752,9 +762,15 @@ def _on(index: int):
     return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _stream_ptr(index: int) -> int:
-    """The current stream of device `index`, as the library takes it."""
-    return torch.cuda.current_stream(index).cuda_stream
+# The current stream of a device, as the library takes it (without the Stream object where torch
+# gives the pointer itself).
+_stream_ptr = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _plain(t: torch.Tensor, dtype: torch.dtype, shape: tuple, index: int) -> bool:
+    """Whether _need_like would let `t` pass."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
 def tq_plan_step(seq_lens: torch.Tensor, new_lens: torch.Tensor, seq_blocks: torch.Tensor, block_table: torch.Tensor,
@@ -980,16 +996,18 @@ def _head_rows(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, index:
 def _rope_args(name: str, index: int, tokens: int, d: int, positions, position_offset, cos_sin, interleaved, q_weight,
                k_weight, eps):
     f32, rows, rot = torch.float32, 0, 0
-    if positions is not None:
+    if positions is not None and not _plain(positions, torch.int32, (tokens,), index):
         _need_like(name, index, positions=(positions, torch.int32, (tokens,)))
     if cos_sin is not None:
         if cos_sin.dim() != 2 or positions is None:
             raise ValueError(f"{name}: cos_sin [P, rot_dim] comes with positions [T]")
         rows, rot = cos_sin.shape
-        _need_like(name, index, cos_sin=(cos_sin, f32, (rows, rot)))
-    for what, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _need_like(name, index, **{what: (w, f32, (d,))})
+        if not _plain(cos_sin, f32, (rows, rot), index):
+            _need_like(name, index, cos_sin=(cos_sin, f32, (rows, rot)))
+    if q_weight is not None and not _plain(q_weight, f32, (d,), index):
+        _need_like(name, index, q_weight=(q_weight, f32, (d,)))
+    if k_weight is not None and not _plain(k_weight, f32, (d,), index):
+        _need_like(name, index, k_weight=(k_weight, f32, (d,)))
     return (_ptr(positions), int(position_offset), _ptr(cos_sin), rows, rot, int(bool(interleaved)), _ptr(q_weight),
             _ptr(k_weight), float(eps))
 
@@ -1060,7 +1078,8 @@ def tq_append_kv(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor
     dev, dtype, index = x.device, x.dtype, x.get_device()
     if index < 0:
         raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {dev})")
-    _need_like(name, index, slots=(slots, torch.int64, (t,)), signs=(signs, torch.float32, (d,)))
+    if not (_plain(slots, torch.int64, (t,), index) and _plain(signs, torch.float32, (d,), index)):
+        _need_like(name, index, slots=(slots, torch.int64, (t,)), signs=(signs, torch.float32, (d,)))
     qp, qs, hq, qo, qos = None, 0, 0, None, 0
     if q is not None:
         hq = q.shape[1]
@@ -1081,8 +1100,9 @@ def tq_append_kv(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor
         if rb * 8 != d * bits + 32 or h != rows.shape[1] or (shape or (nb, bs, h)) != (nb, bs, h):  # D: a multiple of 16
             raise ValueError(f"{name}: {what}_pages {list(pages.shape)} do not match {what} {list(rows.shape)} at {bits} bits")
         shape = nb, bs, h
-        _need_like(name, index, **{what + "_pages": (pages, torch.uint8, (nb, bs, h, rb)),
-                                   what + "_centroids": (cents, torch.float32, (1 << bits,))})
+        if not (_plain(pages, torch.uint8, (nb, bs, h, rb), index) and _plain(cents, torch.float32, (1 << bits,), index)):
+            _need_like(name, index, **{what + "_pages": (pages, torch.uint8, (nb, bs, h, rb)),
+                                       what + "_centroids": (cents, torch.float32, (1 << bits,))})
         side.append((*_head_rows(name, what, rows, dtype, index, t, h, d), pages.data_ptr(), bits, cents.data_ptr()))
     nb, bs, h = shape or (0, 1, 1)
     rope = _rope_args(name, index, t, d, positions, position_offset, cos_sin, interleaved, q_weight, k_weight, eps)
@@ -1109,7 +1129,9 @@ class Verified(NamedTuple):
     next_token: torch.Tensor  # int32 [S]
 
 
+@functools.lru_cache(maxsize=4096)
 def tq_verify_tree_workspace(num_rows: int, vocab_size: int, num_seqs: int) -> int:
+    """Workspace bytes of tq_verify_tree."""
     return int(lib().tq_verify_tree_workspace(num_rows, vocab_size, num_seqs))
 
 
@@ -1151,15 +1173,19 @@ def tq_verify_tree(logits: torch.Tensor, row_start: torch.Tensor, tokens: torch.
     if draft_probs is not None:
         qp, qs = _vocab_rows(name, "draft_probs", draft_probs, index, (r, vocab))
         qt = _DTYPES[draft_probs.dtype]
-        _need_like(name, index, u_accept=(u_accept, f32, (r,)))
-    _need_like(name, index, row_start=(row_start, i32, (s + 1,)), tokens=(tokens, i32, (r,)), u_sample=(u_sample, f32, (r,)))
-    if parents is not None:
+        if not _plain(u_accept, f32, (r,), index):
+            _need_like(name, index, u_accept=(u_accept, f32, (r,)))
+    if not (_plain(row_start, i32, (s + 1,), index) and _plain(tokens, i32, (r,), index) and
+            _plain(u_sample, f32, (r,), index)):
+        _need_like(name, index, row_start=(row_start, i32, (s + 1,)), tokens=(tokens, i32, (r,)),
+                   u_sample=(u_sample, f32, (r,)))
+    if parents is not None and not _plain(parents, i32, (r,), index):
         _need_like(name, index, parents=(parents, i32, (r,)))
-    if temperature is not None:
+    if temperature is not None and not _plain(temperature, f32, (s,), index):
         _need_like(name, index, temperature=(temperature, f32, (s,)))
     if out is None:
-        path, lens, after = torch.empty(s * (max_path + 2), dtype=i32, device=dev).split([s * max_path, s, s])
-        out = Verified(path.view(s, max_path), lens, after)
+        out = Verified(torch.empty((s, max_path), dtype=i32, device=dev), torch.empty(s, dtype=i32, device=dev),
+                       torch.empty(s, dtype=i32, device=dev))
     else:
         _need_like(name, index, path=(out.path, i32, (s, max_path)), path_lens=(out.path_lens, i32, (s,)),
                    next_token=(out.next_token, i32, (s,)))
