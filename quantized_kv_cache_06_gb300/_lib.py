@@ -981,35 +981,52 @@ def tq_build_rope(rot_dim: int, num_positions: int, base: float = 10000.0, inv_f
     return out if device is None else out.to(device)
 
 
-def _head_rows(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, index: int, tokens: int, heads: int, d: int):
-    """(pointer, token stride) of head rows t[tokens, heads, d] whose heads are contiguous."""
-    if t.get_device() != index:
-        raise ValueError(f"{name}: all tensors must be on the same CUDA device ({what} is on {t.device})")
-    if t.dtype is not dtype or t.shape != (tokens, heads, d):
-        raise ValueError(f"{name}: {what} must be {dtype} {[tokens, heads, d]}, got {t.dtype} {list(t.shape)}")
+# Codebook sizes and their bits.
+_BITS = {4: 2, 8: 3, 16: 4, 32: 5}
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple, index: int) -> bool:
+    """Whether t is head rows [T, heads, D] whose heads are contiguous."""
     st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != d):
+    return t.dtype is dtype and t.shape == shape and st[2] == 1 and (st[1] == shape[2] or shape[1] == 1) and \
+        t.get_device() == index
+
+
+def _explain_rows(name: str, what: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, index: int) -> None:
+    """The error of a tensor that _rows does not let pass (none where it does)."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device ({what} is on {t.device})")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: {what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not _rows(t, dtype, shape, index):
         raise ValueError(f"{name}: the heads of a token of {what} must be contiguous")
-    return t.data_ptr(), (st[0] if tokens > 1 else heads * d)
 
 
 def _rope_args(name: str, index: int, tokens: int, d: int, positions, position_offset, cos_sin, interleaved, q_weight,
                k_weight, eps):
-    f32, rows, rot = torch.float32, 0, 0
-    if positions is not None and not _plain(positions, torch.int32, (tokens,), index):
-        _need_like(name, index, positions=(positions, torch.int32, (tokens,)))
+    """Checks and arguments of the position rotation and the norms."""
+    f32, rows, rot, pp, cp = torch.float32, 0, 0, None, None
+    if positions is not None:
+        if not _plain(positions, torch.int32, (tokens,), index):
+            _need_like(name, index, positions=(positions, torch.int32, (tokens,)))
+        pp = positions.data_ptr()
     if cos_sin is not None:
         if cos_sin.dim() != 2 or positions is None:
             raise ValueError(f"{name}: cos_sin [P, rot_dim] comes with positions [T]")
         rows, rot = cos_sin.shape
         if not _plain(cos_sin, f32, (rows, rot), index):
             _need_like(name, index, cos_sin=(cos_sin, f32, (rows, rot)))
-    if q_weight is not None and not _plain(q_weight, f32, (d,), index):
-        _need_like(name, index, q_weight=(q_weight, f32, (d,)))
-    if k_weight is not None and not _plain(k_weight, f32, (d,), index):
-        _need_like(name, index, k_weight=(k_weight, f32, (d,)))
-    return (_ptr(positions), int(position_offset), _ptr(cos_sin), rows, rot, int(bool(interleaved)), _ptr(q_weight),
-            _ptr(k_weight), float(eps))
+        cp = cos_sin.data_ptr()
+    qw = kw = None
+    if q_weight is not None:
+        if not _plain(q_weight, f32, (d,), index):
+            _need_like(name, index, q_weight=(q_weight, f32, (d,)))
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if not _plain(k_weight, f32, (d,), index):
+            _need_like(name, index, k_weight=(k_weight, f32, (d,)))
+        kw = k_weight.data_ptr()
+    return pp, int(position_offset), cp, rows, rot, 1 if interleaved else 0, qw, kw, float(eps)
 
 
 def tq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
@@ -1025,38 +1042,66 @@ def tq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     x = q if q is not None else k
     if x is None or x.dim() != 3 or x.dtype not in _DTYPES:
         raise ValueError(f"{name}: q [T, Hq, D] or k [T, H, D], f32/f16/bf16, expected")
-    t, _, d = x.shape
-    dev, dtype, index = x.device, x.dtype, x.get_device()
+    t, h, d = x.shape
+    dtype, index = x.dtype, x.get_device()
     if index < 0:
-        raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {dev})")
-    args = []
-    outs = []
-    for what, rows, out in (("q", q, q_out), ("k", k, k_out)):
-        if rows is None:
-            args.append((None, 0, 0, None, 0))
-            outs.append(None)
-            continue
-        if rows.dim() != 3:
-            raise ValueError(f"{name}: {what} [T, heads, D] expected")
-        h = rows.shape[1]
-        if out is None:
-            out = torch.empty((t, h, d), dtype=dtype, device=dev)
-        args.append((*_head_rows(name, what, rows, dtype, index, t, h, d), h,
-                     *_head_rows(name, what + "_out", out, dtype, index, t, h, d)))
-        outs.append(out)
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {x.device})")
+    qp = qo = kp = ko = None
+    qs = qos = ks = kos = hq = 0
+    if q is not None:
+        hq = h
+        shape = (t, hq, d)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        if not (_rows(q, dtype, shape, index) and _rows(q_out, dtype, shape, index)):
+            _explain_rows(name, "q", q, dtype, shape, index)
+            _explain_rows(name, "q_out", q_out, dtype, shape, index)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+        qs, qos = (q.stride(0), q_out.stride(0)) if t > 1 else (hq * d, hq * d)
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError(f"{name}: k [T, H, D] expected")
+        h = k.shape[1]
+        shape = (t, h, d)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=x.device)
+        if not (_rows(k, dtype, shape, index) and _rows(k_out, dtype, shape, index)):
+            _explain_rows(name, "k", k, dtype, shape, index)
+            _explain_rows(name, "k_out", k_out, dtype, shape, index)
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+        ks, kos = (k.stride(0), k_out.stride(0)) if t > 1 else (h * d, h * d)
     rope = _rope_args(name, index, t, d, positions, position_offset, cos_sin, interleaved, q_weight, k_weight, eps)
-    _need_status(name, status, dev)
-    if status is None and check:
-        status = _status_buffer(dev)
-    (qp, qs, hq, qo, qos), (kp, ks, h, ko, kos) = args
+    if status is not None:
+        _need_status(name, status, x.device)
+    elif check:
+        status = _status_buffer(x.device)
     with _on(index):
-        code = lib().tq_norm_rope(qp, qs, hq, kp, ks, h, _DTYPES[dtype], t, d, *rope, qo, qos, ko, kos, _ptr(status),
-                                  _stream_ptr(index))
+        code = lib().tq_norm_rope(qp, qs, hq, kp, ks, h if kp is not None else 0, _DTYPES[dtype], t, d, *rope, qo, qos, ko,
+                                  kos, None if status is None else status.data_ptr(), _stream_ptr(index))
     if code != TQ_OK:
         _check(code)
     if check:
         raise_for_device_status(status)
-    return outs[0], outs[1]
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+def _pages_like(name: str, what: str, rows: torch.Tensor, pages, cents, t: int, d: int, dtype: torch.dtype, index: int):
+    """(pointer, token stride, page pointer, bits, centroids pointer, (blocks, block size, heads)) of one
+    packed side, checked."""
+    if pages is None or cents is None or rows.dim() != 3 or pages.dim() != 4:
+        raise ValueError(f"{name}: {what} [T, H, D] comes with its pages [NB, bs, H, RB] and centroids")
+    nb, bs, h, rb = pages.shape
+    bits = _BITS.get(cents.numel(), 0)
+    if rb * 8 != d * bits + 32 or h != rows.shape[1]:  # head dims are multiples of 16
+        bits = _bits_from_centroids(cents)
+        raise ValueError(f"{name}: {what}_pages {list(pages.shape)} do not match {what} {list(rows.shape)} at {bits} bits")
+    if not (_rows(rows, dtype, (t, h, d), index) and pages.dtype is torch.uint8 and pages.get_device() == index and
+            pages.is_contiguous() and cents.dtype is torch.float32 and cents.get_device() == index and
+            cents.is_contiguous()):
+        _explain_rows(name, what, rows, dtype, (t, h, d), index)
+        _need_like(name, index, **{what + "_pages": (pages, torch.uint8, (nb, bs, h, rb)),
+                                   what + "_centroids": (cents, torch.float32, (1 << bits,))})
+    return rows.data_ptr(), (rows.stride(0) if t > 1 else h * d), pages.data_ptr(), bits, cents.data_ptr(), (nb, bs, h)
 
 
 def tq_append_kv(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
@@ -1074,45 +1119,43 @@ def tq_append_kv(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor
     x = q if q is not None else k if k is not None else v
     if x is None or x.dim() != 3 or x.dtype not in _DTYPES:
         raise ValueError(f"{name}: q [T, Hq, D], k, v [T, H, D], f32/f16/bf16, expected")
-    t, _, d = x.shape
-    dev, dtype, index = x.device, x.dtype, x.get_device()
+    t, hq, d = x.shape
+    dtype, index = x.dtype, x.get_device()
     if index < 0:
-        raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {dev})")
+        raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {x.device})")
     if not (_plain(slots, torch.int64, (t,), index) and _plain(signs, torch.float32, (d,), index)):
         _need_like(name, index, slots=(slots, torch.int64, (t,)), signs=(signs, torch.float32, (d,)))
-    qp, qs, hq, qo, qos = None, 0, 0, None, 0
     if q is not None:
-        hq = q.shape[1]
+        shape = (t, hq, d)
         if q_out is None:
-            q_out = torch.empty((t, hq, d), dtype=dtype, device=dev)
-        qp, qs = _head_rows(name, "q", q, dtype, index, t, hq, d)
-        qo, qos = _head_rows(name, "q_out", q_out, dtype, index, t, hq, d)
-    shape = None
-    side = []
-    for what, rows, pages, cents in (("k", k, k_pages, k_centroids), ("v", v, v_pages, v_centroids)):
-        if rows is None:
-            side.append((None, 0, None, 0, None))
-            continue
-        if pages is None or cents is None or rows.dim() != 3 or pages.dim() != 4:
-            raise ValueError(f"{name}: {what} [T, H, D] comes with its pages [NB, bs, H, RB] and centroids")
-        bits = _bits_from_centroids(cents)
-        nb, bs, h, rb = pages.shape
-        if rb * 8 != d * bits + 32 or h != rows.shape[1] or (shape or (nb, bs, h)) != (nb, bs, h):  # D: a multiple of 16
-            raise ValueError(f"{name}: {what}_pages {list(pages.shape)} do not match {what} {list(rows.shape)} at {bits} bits")
-        shape = nb, bs, h
-        if not (_plain(pages, torch.uint8, (nb, bs, h, rb), index) and _plain(cents, torch.float32, (1 << bits,), index)):
-            _need_like(name, index, **{what + "_pages": (pages, torch.uint8, (nb, bs, h, rb)),
-                                       what + "_centroids": (cents, torch.float32, (1 << bits,))})
-        side.append((*_head_rows(name, what, rows, dtype, index, t, h, d), pages.data_ptr(), bits, cents.data_ptr()))
+            q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        if not (_rows(q, dtype, shape, index) and _rows(q_out, dtype, shape, index)):
+            _explain_rows(name, "q", q, dtype, shape, index)
+            _explain_rows(name, "q_out", q_out, dtype, shape, index)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+        qs, qos = (q.stride(0), q_out.stride(0)) if t > 1 else (hq * d, hq * d)
+    else:
+        qp = qo = q_out = None
+        qs = qos = hq = 0
+    kp = kpg = kc = vp = vpg = vc = shape = None
+    ks = kb = vs = vb = 0
+    if k is not None:
+        kp, ks, kpg, kb, kc, shape = _pages_like(name, "k", k, k_pages, k_centroids, t, d, dtype, index)
+    if v is not None:
+        vp, vs, vpg, vb, vc, other = _pages_like(name, "v", v, v_pages, v_centroids, t, d, dtype, index)
+        if shape is not None and shape != other:
+            raise ValueError(f"{name}: k_pages {list(k_pages.shape)} and v_pages {list(v_pages.shape)} hold different tokens")
+        shape = other
     nb, bs, h = shape or (0, 1, 1)
     rope = _rope_args(name, index, t, d, positions, position_offset, cos_sin, interleaved, q_weight, k_weight, eps)
-    _need_status(name, status, dev)
-    if status is None and check:
-        status = _status_buffer(dev)
-    (kp, ks, kpg, kb, kc), (vp, vs, vpg, vb, vc) = side
+    if status is not None:
+        _need_status(name, status, x.device)
+    elif check:
+        status = _status_buffer(x.device)
     with _on(index):
         code = lib().tq_append_kv(qp, qs, hq, qo, qos, kp, ks, vp, vs, _DTYPES[dtype], t, h, d, slots.data_ptr(), kpg, kb,
-                                  vpg, vb, nb, bs, signs.data_ptr(), kc, vc, *rope, _ptr(status), _stream_ptr(index))
+                                  vpg, vb, nb, bs, signs.data_ptr(), kc, vc, *rope,
+                                  None if status is None else status.data_ptr(), _stream_ptr(index))
     if code != TQ_OK:
         _check(code)
     if check:

@@ -301,6 +301,16 @@ __device__ __forceinline__ void apply_coef(float2 (&x)[8], const Coef& f, int mo
         x[i] = __ffma2_rn(x[i], f.p[i], __fmul2_rn(other, f.s[i]));
       }
     }
+  } else if (rot <= D / 2 && rot % 16 == 0 && (rot & (rot - 1)) == 0) {
+    // a power of two of at least 16 in the first half: chunks of eight pair up between lanes (staged in
+    // shared memory they cost twice the time: 8200 tokens of rot 64, D 128)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 other = make_float2(__shfl_xor_sync(kFullMask, x[i].x, rot / 16), __shfl_xor_sync(kFullMask, x[i].y, rot / 16));
+      if (8 * l >= rot) other = make_float2(0.f, 0.f);
+      x[i] = __ffma2_rn(x[i], f.p[i], __fmul2_rn(other, f.s[i]));
+      x[4 + i] = __fmul2_rn(x[4 + i], f.p[4 + i]);
+    }
   } else {
     const int half = rot / 2;
     __syncwarp();
