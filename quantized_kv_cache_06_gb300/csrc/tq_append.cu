@@ -69,8 +69,19 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   }
   const int64_t ctas = (blocks * p.block_items + kAppendWarps - 1) / kAppendWarps;
   p.grid = (int)std::min<int64_t>(ctas, (int64_t)sms * kAppendCtas);
-  p.step_block = p.grid * kAppendWarps / p.block_items;
-  p.step_part = p.grid * kAppendWarps % p.block_items;
+  // Whole blocks a turn, and every warp one part further at each: stretches of packed rows take several
+  // times those of dense ones, and each warp gets its share of all.  (More parts than warps: as they come.)
+  p.warps = p.grid * kAppendWarps;
+  if (p.warps >= p.block_items) {
+    p.warps -= p.warps % p.block_items;
+    p.step_block = p.warps / p.block_items;
+    p.step_part = 1;
+    p.carry = 0;
+  } else {
+    p.step_block = 0;
+    p.step_part = p.warps;
+    p.carry = 1;
+  }
   const bool packed = a.k_pages || a.v_pages;
   switch (a.dtype) {
     case kF32: return packed ? launch_append_packed_f32(p, stream) : launch_append_f32(p, stream);

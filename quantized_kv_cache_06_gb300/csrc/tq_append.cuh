@@ -589,7 +589,7 @@ struct Run {
       link = 0;
       block += p.step_block;
       part += p.step_part;
-      if (part >= p.block_items) part -= p.block_items, ++block;
+      if (part >= p.block_items) part -= p.block_items, block += p.carry;
       n = 0;
       if (block >= p.blocks) return;
       open(p);
@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
     it.part = (int)(item - (uint32_t)it.block * (uint32_t)p.block_items);
     it.link = 0;
     it.n = 0;
+    if ((int)item >= p.warps) it.block = p.blocks;  // (a warp too many)
     if (it.block < p.blocks) it.open(p);
     if (it.n == 0) it.link = p.chain, it.next(p);
   }

@@ -50,7 +50,7 @@ struct AppendArgs {
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 
 constexpr int kAppendWarps = 8;
-constexpr int kAppendCtas = 2;  // CTAs of an SM
+constexpr int kAppendCtas = 3;  // CTAs of an SM
 
 // How a call is cut: blocks of tokens, each side's groups of 32 / (head_dim / 16) heads over a block
 // in stretches of chain * run groups, a warp a stretch.
@@ -71,7 +71,8 @@ struct AppendPlan {
   AppendSide side[3];         // q, k, v
   int items[3];               // stretches of a block
   int block_items;
-  int step_block, step_part;  // from one stretch of a warp to its next
+  int warps;                  // that take part
+  int step_block, step_part, carry;  // from one stretch of a warp to its next
   int grid;
   int full;                   // every side's heads fill its groups
   int vec;                    // inputs and dense outputs: 16-byte accesses
