@@ -51,25 +51,24 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
           vec_ok(a.q_out, a.q_out_stride, size) && vec_ok(a.k_out, a.k_out_stride, size);
   p.table_vec = reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0 && a.rot_dim % 8 == 0;
   p.signs_vec = reinterpret_cast<uintptr_t>(a.signs) % 16 == 0;
-  // Stretches of eight groups share a token's coefficients and hide the copies' latency; shorter ones
-  // where they leave warps idle.
+  // Runs of eight groups share a token's coefficients and hide the copies' latency; shorter ones where
+  // they leave warps idle.
   const int64_t warps = (int64_t)sms * kAppendCtas * kAppendWarps;
-  const int want = (int)std::max<int64_t>(1, std::min<int64_t>(8, a.num_tokens * total / (2 * warps)));
-  const int most = size == 2 ? 4 : 2;  // run_groups
-  p.run = std::min(want, most);
-  p.chain = want / p.run;
-  // Blocks of four tokens where a side's groups of one token are fewer than a stretch.
-  p.block_tokens = want > 1 ? 4 : 1;
+  const int most = size == 2 ? kRunGroups : kRunGroups / 2;
+  p.run = 1;
+  while (2 * p.run <= most && a.num_tokens * total / (2 * warps) >= 2 * p.run) p.run *= 2;
+  // Blocks of four tokens where a side's groups of one token are fewer than a run.
+  p.block_tokens = p.run > 1 ? 4 : 1;
   const int64_t blocks = (a.num_tokens + p.block_tokens - 1) / p.block_tokens;
   p.blocks = (int)blocks;
   for (int i = 0; i < 3; ++i) {
-    p.items[i] = (p.side[i].groups * p.block_tokens + p.run * p.chain - 1) / (p.run * p.chain);
+    p.items[i] = (p.side[i].groups * p.block_tokens + p.run - 1) / p.run;
     p.side[i].first = p.block_items;
     p.block_items += p.items[i];
   }
   const int64_t ctas = (blocks * p.block_items + kAppendWarps - 1) / kAppendWarps;
   p.grid = (int)std::min<int64_t>(ctas, (int64_t)sms * kAppendCtas);
-  // Whole blocks a turn, and every warp one part further at each: stretches of packed rows take several
+  // Whole blocks a turn, and every warp one part further at each: runs of packed rows take several
   // times those of dense ones, and each warp gets its share of all.  (More parts than warps: as they come.)
   p.warps = p.grid * kAppendWarps;
   if (p.warps >= p.block_items) {

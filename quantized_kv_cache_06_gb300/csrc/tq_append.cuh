@@ -551,26 +551,25 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-// Groups of rows (1 KB each, fp32 2 KB) that a warp takes together: their copies, positions and
-// slots are under way while it works on the ones before.
+// Groups of rows (1 KB each, fp32 2 KB) of a run, and as many copies in flight a warp.
 template <typename T>
 __host__ __device__ constexpr int run_groups() {
-  return sizeof(T) == 2 ? 4 : 2;
+  return sizeof(T) == 2 ? kRunGroups : kRunGroups / 2;
 }
-// Dynamic shared memory: the rows of two runs a warp, and room to exchange pairs.
-constexpr int kRingBytes = kAppendWarps * 2 * 4 * 1024;
+// Dynamic shared memory: the rows in flight, and room to exchange pairs.
+constexpr int kRingBytes = kAppendWarps * kRunGroups * 1024;
 constexpr int kStageBytes = kAppendWarps * 512 * 4;
 
 // A run: consecutive groups of heads of one side (0: q, 1: k, 2: v) over a block of tokens, token by
-// token.  A warp takes p.chain runs in a row, which share a token's coefficients where they are of one.
+// token; a warp's unit of work.
 struct Run {
-  int block, part, link;  // stretch of p.chain runs, and which of them
+  int block, part;  // which
   int side;
-  int t, g, n;            // token and group of the run's first group; groups of the run
+  int t, g, n;      // token and group of its first group; groups
   __device__ __forceinline__ void open(const AppendPlan& p) {
     side = part < p.items[0] ? 0 : part < p.items[0] + p.items[1] ? 1 : 2;
     const int groups = p.side[side].groups;
-    const int u = (part - p.side[side].first) * p.chain * p.run;
+    const int u = (part - p.side[side].first) * p.run;
     const int k = groups == 1 ? u : (int)__umulhi((uint32_t)u, p.side[side].inv_groups);
     t = block * p.block_tokens + k;
     g = u - k * groups;
@@ -578,15 +577,7 @@ struct Run {
   }
   // to the next run that has groups; n = 0 behind the last
   __device__ __forceinline__ void next(const AppendPlan& p) {
-    if (++link < p.chain) {  // where this one ended
-      const int groups = p.side[side].groups, last = min((block + 1) * p.block_tokens, (int)p.a.num_tokens);
-      g += n;
-      while (g >= groups) g -= groups, ++t;
-      n = max(0, min(p.run, (last - t) * groups - g));
-      if (n > 0) return;
-    }
     do {
-      link = 0;
       block += p.step_block;
       part += p.step_part;
       if (part >= p.block_items) part -= p.block_items, block += p.carry;
@@ -598,78 +589,83 @@ struct Run {
 };
 
 // PACK: some rows are packed (a dense call needs neither quantisers nor their code).  RING: rows are
-// 16-byte aligned and copied ahead, 512 consecutive bytes at a time.
+// 16-byte aligned; while a warp works on a run the next one's rows are copied, each into the place of
+// the group just read, each lane's own elements through its own shared memory: nothing has to be waited
+// for but the copies.
 template <typename T, int LPR, int MODE, bool PACK, bool RING>
 __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(const __grid_constant__ AppendPlan p) {
   constexpr int D = 16 * LPR, RPW = 32 / LPR, U = run_groups<T>(), N = Raw<T>::N;
-  constexpr int kGroup = RPW * D * (int)sizeof(T);  // bytes of a group's rows: N * 512
+  constexpr int kGroup = RPW * D * (int)sizeof(T);  // bytes of a group's rows
   __shared__ Quants quants;
   __shared__ __align__(16) Shared shared[3];
   extern __shared__ __align__(16) unsigned char dynamic[];
   const AppendArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LPR, row = lane / LPR;
-  unsigned char* ring = dynamic + warp * (2 * U * kGroup);
   float* stage = reinterpret_cast<float*>(dynamic + (RING ? kRingBytes : 0)) + warp * 512 + row * D;
   const int mine = (row * D + 8 * l) * (int)sizeof(T);  // this lane's elements in a group's rows
+  unsigned char* const ring = dynamic + warp * (kRunGroups * 1024) + lane * 16;
   Run it;
   {
     const uint32_t item = blockIdx.x * kAppendWarps + warp;
     it.block = item / (uint32_t)p.block_items;
     it.part = (int)(item - (uint32_t)it.block * (uint32_t)p.block_items);
-    it.link = 0;
     it.n = 0;
     if ((int)item >= p.warps) it.block = p.blocks;  // (a warp too many)
     if (it.block < p.blocks) it.open(p);
-    if (it.n == 0) it.link = p.chain, it.next(p);
+    if (it.n == 0) it.next(p);
   }
-  // Copies a run's rows, and loads the position and the slot of the j-th token of the run in lane j.
+  // The positions and slots of a run's tokens, the j-th token's in lane j.
   int32_t pos_in = 0;
   int64_t slot_in = 0;
-  auto fetch = [&](const Run& w, uint32_t to) {
-    if (w.n == 0) return;
-    const AppendSide& sd = p.side[w.side];
-    if (lane < U && w.t + lane < (int)a.num_tokens) {
+  auto look_up = [&](const Run& w) {
+    if (lane < U && w.n > 0 && w.t + lane < (int)a.num_tokens) {
       if (a.positions) pos_in = __ldg(a.positions + w.t + lane);
       if (PACK && w.side > 0) slot_in = __ldg(a.slots + w.t + lane);
     }
+  };
+  // The rows that are copied next: group c_g of c_groups of a token, c_left to go of the run.
+  const unsigned char* c_from = nullptr;
+  int64_t c_wrap = 0;
+  int c_g = 0, c_groups = 0, c_heads = 0, c_left = 0;
+  auto aim = [&](const Run& w) {
+    c_left = w.n;
+    if (w.n == 0) return;
+    const AppendSide& sd = p.side[w.side];
+    c_groups = sd.groups;
+    c_heads = sd.heads;
+    c_g = w.g;
+    c_from = sd.in + (int64_t)w.t * sd.in_step + w.g * kGroup + mine;
+    c_wrap = sd.in_step - (int64_t)sd.groups * kGroup;
+  };
+  auto copy_next = [&](uint32_t to) {
     if constexpr (RING) {
-      const unsigned char* from = sd.in + (int64_t)w.t * sd.in_step + w.g * kGroup + lane * 16;
-      int left = w.n, m = min(left, sd.groups - w.g);
-      int bytes = sd.heads * (D * (int)sizeof(T)) - w.g * kGroup - lane * 16;  // what the token has for this lane
-#pragma unroll 1
-      while (true) {  // a token's groups, one after the other
-        if (p.full) {
+      if (c_left > 0) {
+        if (p.full || c_g * RPW + row < c_heads) {
 #pragma unroll
-          for (int j = 0; j < U; ++j)
-            if (j < m) {
-#pragma unroll
-              for (int i = 0; i < N; ++i) copy16(to + (j * N + i) * 512, from + (j * N + i) * 512);
-            }
-        } else {
-#pragma unroll
-          for (int i = 0; i < U * N; ++i)
-            if (i < m * N && i * 512 < bytes) copy16(to + i * 512, from + i * 512);
+          for (int i = 0; i < N; ++i)
+            copy16(to + i * 512, c_from + (i < N / 2 ? 0 : D / 2 * (int)sizeof(T)) + i % (N / 2) * 16);
         }
-        left -= m;
-        if (left == 0) break;
-        to += m * kGroup;
-        from += sd.in_step - (sd.groups - m) * kGroup;  // (the first token may have begun behind its first group)
-        m = min(left, sd.groups);
-        bytes = sd.heads * (D * (int)sizeof(T)) - lane * 16;
+        --c_left;
+        c_from += kGroup;
+        if (++c_g == c_groups) c_g = 0, c_from += c_wrap;
       }
+      copies_commit();
     }
   };
-  const uint32_t ring_at = smem_address(ring) + lane * 16;
+  const uint32_t ring_at = smem_address(ring);
   if constexpr (RING) {
-    // what lies behind a side's last head keeps what it held: ones, to begin with
+    // lanes of rows behind a side's last head keep what they held: ones, to begin with
+    if (!p.full) {
 #pragma unroll
-    for (int i = 0; i < 2 * U * N; ++i)
-      *reinterpret_cast<uint4*>(ring + lane * 16 + i * 512) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    __syncwarp();
+      for (int i = 0; i < U * N; ++i)
+        *reinterpret_cast<uint4*>(ring + i * 512) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    }
   }
-  fetch(it, ring_at);
-  copies_commit();
+  look_up(it);
+  aim(it);
+#pragma unroll 1
+  for (int j = 0; j < U; ++j) copy_next(ring_at + j * (N * 512));
   const int mode = MODE == kAny ? (!a.cos_sin ? kPlain : a.interleaved ? kPairs : a.rot_dim == D ? kHalves : kStaged) : MODE;
   if constexpr (PACK) {
     if (warp == 0 && a.k_pages) build_quant(quants, 0, a.k_centroids, 1 << a.k_bits, lane);
@@ -683,10 +679,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
   __syncthreads();
 
   Coef f;
-  int coef_t = -1, coef_side = -1;  // whose coefficients f holds
-  uint32_t half = 0;                // bytes: the ring's half of the run
-  // One run: `use(x, factor, to, live, normed)` takes each group's rows.  TURNS: 1 the side is rotated,
-  // 0 it is not, -1 as the run has it.
+  int coef_side = -1;  // the side that is not rotated whose coefficients f holds
+  // One run: `use(x, factor, to, live, normed)` takes each group's rows.  turns_tag: 1 the side is
+  // rotated, 0 it is not, -1 as the run has it.
   auto take = [&](const Run& w, int32_t pos_all, int64_t slot_all, auto dense_tag, auto turns_tag, int step, auto use) {
     constexpr bool dense = decltype(dense_tag)::value;
     constexpr int kTurns = decltype(turns_tag)::value;
@@ -695,6 +690,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
     const bool normed = sd.normed;
     const bool turned = kTurns >= 0 ? kTurns != 0 : side < 2 && mode != kPlain;
     if (!turned && coef_side != side) plain_coef<LPR>(f.p, shared[side], l);
+    coef_side = turned ? -1 : side;
     // every lane's token: its position and slot
     const int64_t pos = a.positions ? (int64_t)pos_all + a.position_offset : 0;
     const bool far = a.cos_sin && pos >= a.num_positions;
@@ -706,41 +702,45 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
         if (astray) atomicMax(a.status, (int32_t)kSlotOutOfRange);
       }
     }
-    int k = 0, g = w.g, left = w.n;  // token of the run, group, groups left
-    uint32_t at = smem_address(ring) + half + mine;
+    // this lane's place in the first group's rows of its lane's token (k-th of the run)
+    int64_t place;
+    if constexpr (dense) place = (int64_t)(w.t + lane) * sd.out_step;
+    else place = slot_all * sd.slot_step;
+    int k = 0, left = w.n, m = min(left, sd.groups - w.g);  // token of the run, groups left, of the token
+    int head = w.g * RPW + row;
+    uint32_t at = ring_at;
 #pragma unroll 1
     while (true) {  // a token's groups
-      const int m = min(left, sd.groups - g), t = w.t + k;
-      const bool skip = !((good >> k) & 1u);
-      unsigned char* to;  // this lane's place in the group's rows
-      if constexpr (dense) to = sd.out + (int64_t)t * sd.out_step + g * kGroup + mine;
-      else to = sd.out + __shfl_sync(kFullMask, slot_all, k) * sd.slot_step + (g * RPW + row) * (int)sd.out_step;
-      if (!skip) {
-        if (turned && !(coef_t == t && coef_side == side))
+      if ((good >> k) & 1u) {
+        unsigned char* to = sd.out + __shfl_sync(kFullMask, place, k);
+        if constexpr (dense) to += (head - row) * (D * (int)sizeof(T)) + mine;
+        else to += head * (int)sd.out_step;
+        if (turned)
           token_coef<LPR>(f, shared[side], mode, a.cos_sin + (uint64_t)__shfl_sync(kFullMask, (uint32_t)pos, k) * (uint32_t)a.rot_dim,
                           a.rot_dim, p.table_vec, l);
-        coef_t = t;
-        coef_side = side;
 #pragma unroll 1
         for (int j = 0; j < m; ++j) {
-          const bool live = p.full || (g + j) * RPW + row < sd.heads;
+          const bool live = p.full || head < sd.heads;
           Raw<T> raw;
           if constexpr (RING) {
+            copies_wait<U - 1>();
 #pragma unroll
             for (int i = 0; i < N; ++i)
               asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(raw.w[i].x), "=r"(raw.w[i].y), "=r"(raw.w[i].z), "=r"(raw.w[i].w)
-                           : "r"(at + (i < N / 2 ? 0 : D / 2 * (int)sizeof(T)) + i % (N / 2) * 16)
+                           : "r"(at + i * 512)
                            : "memory");
-            at += kGroup;
           } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) raw.w[i] = make_uint4(0, 0, 0, 0);
             if (live)
-              raw.load(reinterpret_cast<const T*>(sd.in + (int64_t)t * sd.in_step + (g + j) * kGroup + mine), D / 2, p.vec);
+              raw.load(reinterpret_cast<const T*>(sd.in + (int64_t)(w.t + k) * sd.in_step + (head - row) * (D * (int)sizeof(T)) + mine),
+                       D / 2, p.vec);
           }
           float2 x[8];
           raw.get(x);
+          copy_next(at);
+          at += N * 512;
           float factor = 1.f;
           if (normed) factor = norm_factor<LPR>(x, a.eps);
           if (turned) {
@@ -751,14 +751,30 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
           }
           use(x, factor, to, live, normed);
           to += step;
+          head += RPW;
         }
       } else {
-        at += m * kGroup;
+        if constexpr (RING) {
+#pragma unroll 1
+          for (int j = 0; j < m; ++j) {
+            copies_wait<U - 1>();  // (what is on its way here has to be there before the next is sent)
+            copy_next(at);
+            at += N * 512;
+          }
+        }
       }
       left -= m;
       if (left == 0) break;
-      g = 0;
+      m = min(left, sd.groups);
+      head = row;
       ++k;
+    }
+    if constexpr (RING) {  // places that this run did not use
+#pragma unroll 1
+      for (int j = w.n; j < U; ++j) {
+        copy_next(at);
+        at += N * 512;
+      }
     }
   };
   while (it.n > 0) {
@@ -766,15 +782,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
     const int64_t slot_all = slot_in;
     Run ahead = it;
     ahead.next(p);
-    if constexpr (RING) __syncwarp();  // the half to be copied to has been read by all lanes
-    fetch(ahead, ring_at + (half ^ (uint32_t)(U * kGroup)));
-    copies_commit();
-    if constexpr (RING) {
-      copies_wait<1>();
-      __syncwarp();
-    }
+    look_up(ahead);
+    aim(ahead);
     using Any = std::integral_constant<int, -1>;
-    using No = std::integral_constant<int, 0>;
     using Turns = std::integral_constant<int, MODE == kAny ? -1 : 1>;
     if (!PACK || it.side == 0) {
       take(it, pos_all, slot_all, std::true_type{}, Turns{}, kGroup,
@@ -821,7 +831,6 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
       }
     }
     it = ahead;
-    half ^= (uint32_t)(U * kGroup);
   }
   if constexpr (RING) copies_wait<0>();
 }

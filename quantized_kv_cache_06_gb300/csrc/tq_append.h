@@ -50,29 +50,31 @@ struct AppendArgs {
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 
 constexpr int kAppendWarps = 8;
-constexpr int kAppendCtas = 3;  // CTAs of an SM
+constexpr int kAppendCtas = 2;  // CTAs of an SM
+
+constexpr int kRunGroups = 8;   // groups of a run (fp32: half as many)
 
 // How a call is cut: blocks of tokens, each side's groups of 32 / (head_dim / 16) heads over a block
-// in stretches of chain * run groups, a warp a stretch.
+// in runs of `run` groups, a warp a run.
 struct AppendSide {
   const unsigned char* in;
   int64_t in_step;            // bytes between tokens
   unsigned char* out;         // dense rows, or pages
   int64_t out_step;           // bytes between tokens, or of a packed row
   int64_t slot_step;          // bytes of a packed token
-  int heads, groups, first;   // first: of its stretches in a block
+  int heads, groups, first;   // first: of its runs in a block
   uint32_t inv_groups;        // ceil(2^32 / groups), groups 2 .. 2^14: u / groups = umulhi(u, inv_groups) for u < 8 groups
   int normed;
 };
 struct AppendPlan {
   AppendArgs a;
   int block_tokens, blocks;
-  int run, chain;             // groups of a run, runs of a stretch
+  int run;                    // groups of a run
   AppendSide side[3];         // q, k, v
-  int items[3];               // stretches of a block
+  int items[3];               // runs of a block
   int block_items;
   int warps;                  // that take part
-  int step_block, step_part, carry;  // from one stretch of a warp to its next
+  int step_block, step_part, carry;  // from one run of a warp to its next
   int grid;
   int full;                   // every side's heads fill its groups
   int vec;                    // inputs and dense outputs: 16-byte accesses
