@@ -595,11 +595,11 @@ tq_status tq_build_rope(int rot_dim, int64_t num_positions, double base, const d
  *                  of one projection's output will do.  Either may be NULL (its heads 0).
  *   q_out, k_out   device, the same type and layout; may be q and k themselves, with their strides.
  *                  No other overlap.
- *   q_weight, k_weight  device float[head_dim], 16-byte aligned, or NULL: no norm for that side
+ *   q_weight, k_weight  device float[head_dim], or NULL: no norm for that side
  *   eps            >= 0
  *   positions      device int32[num_tokens]: token t stands at positions[t] + position_offset
  *                  (tq_plan_step's q_len with offset -1).  A negative position is a padding row:
- *                  nothing of it is read or written.  NULL where cos_sin is NULL: no padding rows.
+ *                  nothing of it is written.  NULL where cos_sin is NULL: no padding rows.
  *   cos_sin        device float[num_positions][rot_dim] (tq_build_rope), or NULL: no rotation
  *   rot_dim        even, 2 .. head_dim; channels behind it are not rotated
  *   status_dev     device int32 or NULL: 0, or TQ_ERR_INVALID_ARG for a position >= num_positions

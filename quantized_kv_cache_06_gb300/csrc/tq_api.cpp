@@ -422,6 +422,8 @@ tq_status write_with_own_status(const char* name, cudaStream_t stream, Launch la
 
 // Largest vocabulary of tq_verify_tree (positions in a row are 32-bit, with room for a piece).
 constexpr int kMaxVocab = 1 << 30;
+// Tokens of a call of tq_norm_rope and tq_append_kv (counted in 32 bits, with room for a run).
+constexpr int64_t kMaxTokens = 0x7fff0000;
 // Heads of a side of tq_norm_rope and tq_append_kv (their groups are counted in 16 bits).
 constexpr int kMaxHeads = 16384;
 
@@ -429,7 +431,7 @@ constexpr int kMaxHeads = 16384;
 tq_status rope_check(const char* name, tq_dtype dtype, int64_t num_tokens, int head_dim, const int32_t* positions,
                      int position_offset, const float* cos_sin, int64_t num_positions, int rot_dim, int interleaved,
                      const float* q_weight, const float* k_weight, float eps, tq::AppendArgs* out) {
-  if (num_tokens < 0 || num_tokens > 0x7fffffffLL || num_positions < 0)
+  if (num_tokens < 0 || num_tokens > kMaxTokens || num_positions < 0)
     return fail(TQ_ERR_INVALID_ARG, "%s: invalid sizes (tokens=%lld, positions=%lld)", name, (long long)num_tokens,
                 (long long)num_positions);
   if (!pow2_dim_ok(head_dim)) return fail(TQ_ERR_UNSUPPORTED, "head_dim %d: must be a power of two in [16, 256]", head_dim);
@@ -438,8 +440,8 @@ tq_status rope_check(const char* name, tq_dtype dtype, int64_t num_tokens, int h
     return fail(TQ_ERR_INVALID_ARG, "%s: rot_dim %d: must be even, 2 .. head_dim %d", name, rot_dim, head_dim);
   if (cos_sin && !positions && num_tokens > 0) return fail(TQ_ERR_INVALID_ARG, "%s: a table needs positions", name);
   if (!(eps >= 0.f && std::isfinite(eps))) return fail(TQ_ERR_INVALID_ARG, "%s: eps must be a number >= 0", name);
-  if (!aligned(positions, 4) || !aligned(cos_sin, 4) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
-    return fail(TQ_ERR_INVALID_ARG, "%s: misaligned pointer (weights need 16-byte alignment)", name);
+  if (!aligned(positions, 4) || !aligned(cos_sin, 4) || !aligned(q_weight, 4) || !aligned(k_weight, 4))
+    return fail(TQ_ERR_INVALID_ARG, "%s: misaligned pointer", name);
   out->dtype = (int)dtype;
   out->num_tokens = num_tokens;
   out->head_dim = head_dim;

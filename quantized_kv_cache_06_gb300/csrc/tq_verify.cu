@@ -35,6 +35,7 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -63,7 +64,7 @@ struct VerifyWork {
   float2* stats;   // [rows][pieces]: largest logit, sum of weights (its bits: first largest)
   RowInfo* rows;   // [rows]
   float2* pq;      // [rows]: p and q of the row's token under its parent
-  u64* rest;       // [2][seqs][pieces]: sums of max(a p - b q, 0)
+  u64* rest;       // [seqs][pieces]: sums of max(a p - b q, 0)
   int pieces;
 };
 
@@ -558,92 +559,104 @@ __device__ __forceinline__ void load_draft(const VerifyArgs& a, const Piece<T>& 
 
 constexpr float kRestUnit = 0x1p60f;  // sums of max(a p - b q, 0) are at most 1
 
-// A sequence of up to kNodes nodes: every CTA of its cluster works out all rows and nodes for itself
-// (the same numbers), so that only passes over a row need the others.  Longer ones share the work.
+// The first CTA of a sequence's cluster works out the rows and walks; the others take their share of
+// the passes over a row, told by the first alone which row and with what coefficients, so that all
+// meet at the same barriers whatever the buffers hold.
 template <typename T, typename Q>
 __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_draft_kernel(VerifyArgs a, VerifyWork w) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int s = blockIdx.x / ranks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a CTA's shared memory may be written by another once it runs)
+  auto started = cluster.barrier_arrive();
   constexpr int threads = kDraftWarps * 32;
   const int warps = ranks * kDraftWarps, gwarp = rank * kDraftWarps + warp;
+  struct Pass {
+    int row;             // -1: no more
+    float a, b, top;     // max(a weight - b q, 0)
+  };
   __shared__ float2 held[kDraftWarps][kHeld];
   __shared__ int32_t node_room[2][kNodes];
   __shared__ float4 row_room[kNodes];
   __shared__ float2 pq_room[kNodes];
   __shared__ u64 rest_room[kHeld];
-  __shared__ int todo;  // what the walk needs next: -1 nothing, else the row to subtract from
-  __shared__ float coef[2];
-  int r0;
-  const int n = rows_of(a, s, r0);
-  check_sequence(a, s, r0, n, rank * threads + threadIdx.x, ranks * threads);
-  Nodes nodes;
-  nodes.open(a, r0, n, node_room, threads);
-  const bool local = n <= kNodes;
-  float4* const rows = local ? row_room : reinterpret_cast<float4*>(w.rows + r0);
-  float2* const pqs = local ? pq_room : w.pq + r0;
+  __shared__ Pass todo;
   const float temp = a.temperature ? a.temperature[s] : 1.f;
   const bool greedy = is_greedy(temp);
   const Scale sc = scale_of(greedy ? 1.f : temp);
+  int r0 = 0, n = 0;
+  Nodes nodes;
+  float4* rows = row_room;
+  float2* pqs = pq_room;
+  if (rank == 0) {
+    n = rows_of(a, s, r0);
+    check_sequence(a, s, r0, n, threadIdx.x, threads);
+    nodes.open(a, r0, n, node_room, threads);
+    if (n > kNodes) {
+      rows = reinterpret_cast<float4*>(w.rows + r0);
+      pqs = w.pq + r0;
+    }
+  }
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  // rows' largest logits, sums (their inverses) and, greedy, first largest logits
-  bool none = false;
-  for (int i = local ? warp : gwarp; i < n; i += local ? kDraftWarps : warps) {
-    const float2* st = hold_stats(w, r0 + i, held[warp], lane);
-    const float top = row_top(st, w.pieces, lane);
-    float inv = 0.f;
-    int pick = -1;
-    if (!has_distribution(top)) {
-      none = true;
-    } else if (greedy) {
-      pick = row_best(st, w.pieces, lane, top);
-    } else {
-      const float unit = row_unit(a.vocab);
-      u64 sum = 0;
-      for (int k = lane; k < w.pieces; k += 32) sum += fixed(st[k].y * weight(st[k].x, top, sc), unit);
-      inv = unit / (float)warp_sum_u64(sum);
-      pick = 0;
-    }
-    if (lane == 0) rows[i] = make_float4(top, inv, __int_as_float(pick), 0.f);
-  }
-  if (none && a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
-  // p and q of every drafted token
-  auto settle = [&] {
-    if (local) __syncthreads();
-    else cluster.sync();
-  };
-  settle();
-  for (int i = 1 + (local ? (int)threadIdx.x : rank * threads + (int)threadIdx.x); i < n; i += local ? threads : ranks * threads) {
-    const int up = nodes.parent(i), tok = nodes.tokens[i];
-    float2 pq = make_float2(-1.f, 0.f);  // never kept
-    if (up >= 0 && up < i && tok >= 0 && tok < a.vocab) {
-      const int64_t r = r0 + up;
-      const float4 info = rows[up];
-      const int pick = __float_as_int(info.z);
-      if (greedy) {
-        pq.x = pick == tok ? 1.f : -1.f;
-      } else if (pick >= 0) {
-        const float x = to_f32<T>(static_cast<const T*>(a.logits)[r * a.logits_stride + tok]);
-        pq.y = fmaxf(to_f32<Q>(static_cast<const Q*>(a.draft)[r * a.draft_stride + tok]), 0.f);
-        pq.x = weight(x, info.x, sc) * info.y;
+  if (rank == 0) {
+    // rows' largest logits, sums (their inverses) and, greedy, first largest logits
+    bool none = false;
+    for (int i = warp; i < n; i += kDraftWarps) {
+      const float2* st = hold_stats(w, r0 + i, held[warp], lane);
+      const float top = row_top(st, w.pieces, lane);
+      float inv = 0.f;
+      int pick = -1;
+      if (!has_distribution(top)) {
+        none = true;
+      } else if (greedy) {
+        pick = row_best(st, w.pieces, lane, top);
+      } else {
+        const float unit = row_unit(a.vocab);
+        u64 sum = 0;
+        for (int k = lane; k < w.pieces; k += 32) sum += fixed(st[k].y * weight(st[k].x, top, sc), unit);
+        inv = unit / (float)warp_sum_u64(sum);
+        pick = 0;
       }
+      if (lane == 0) rows[i] = make_float4(top, inv, __int_as_float(pick), 0.f);
     }
-    pqs[i] = pq;
+    if (none && a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
+    __syncthreads();
+    // p and q of every drafted token
+    for (int i = 1 + (int)threadIdx.x; i < n; i += threads) {
+      const int up = nodes.parent(i), tok = nodes.tokens[i];
+      float2 pq = make_float2(-1.f, 0.f);  // never kept
+      if (up >= 0 && up < i && tok >= 0 && tok < a.vocab) {
+        const int64_t r = r0 + up;
+        const float4 info = rows[up];
+        const int pick = __float_as_int(info.z);
+        if (greedy) {
+          pq.x = pick == tok ? 1.f : -1.f;
+        } else if (pick >= 0) {
+          const float x = to_f32<T>(static_cast<const T*>(a.logits)[r * a.logits_stride + tok]);
+          pq.y = fmaxf(to_f32<Q>(static_cast<const Q*>(a.draft)[r * a.draft_stride + tok]), 0.f);
+          pq.x = weight(x, info.x, sc) * info.y;
+        }
+      }
+      pqs[i] = pq;
+    }
+    __syncthreads();
   }
-  settle();
-  // the walk, by every CTA's first warp alike; all CTAs share the sums over a row
-  int c = 0, from = 1, pass = 0;
+  // the walk, by the first CTA's first warp
+  const bool walks = rank == 0 && warp == 0;
+  cluster.barrier_wait(std::move(started));
+  int c = 0, from = 1;
   float ca = 1.f, cb = 0.f;      // r = max(ca p - cb q, 0) at node c
   float da = 1.f, db = 0.f;      // the coefficients whose sums the last pass took (db 0: none at c)
   bool again = false;
   int32_t* path = a.path + (int64_t)s * a.max_path;
-  float4 info = n > 0 ? rows[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-  if (rank == 0 && warp == 0 && lane == 0 && n > 0) path[0] = 0;
+  const float4 no_row = make_float4(0.f, 0.f, __int_as_float(-1), 0.f);
+  float4 info = walks && n > 0 ? rows[0] : no_row;
+  if (walks && lane == 0 && n > 0) path[0] = 0;
   int len = n > 0 ? 1 : 0;
   while (true) {
-    if (warp == 0) {
+    if (walks) {
       int need = -1;
-      while (n > 0 && !again && __float_as_int(info.z) >= 0 && len < a.max_path) {
+      while (!again && __float_as_int(info.z) >= 0 && len < a.max_path) {
         const int child = nodes.next_child(c, from, lane, [](int) { return true; });
         if (child < 0) break;
         const float2 pq = pqs[child];
@@ -654,7 +667,7 @@ __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_draft_kernel(Verif
           ca = da = 1.f;
           cb = db = 0.f;
           info = rows[c];
-          if (rank == 0 && lane == 0) path[len] = c;
+          if (lane == 0) path[len] = c;
           ++len;
         } else {
           from = child + 1;
@@ -666,38 +679,34 @@ __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_draft_kernel(Verif
         }
       }
       if (again) need = c;
-      if (lane == 0) {
-        todo = need;
-        coef[0] = da * info.y;
-        coef[1] = db;
-      }
+      const Pass next{need < 0 ? -1 : r0 + need, da * info.y, db, info.x};
+      if (lane < ranks) *cluster.map_shared_rank(&todo, lane) = next;
     }
-    __syncthreads();
-    const int row = todo;
-    if (row < 0) break;
-    const float pa = coef[0], pb = coef[1];
-    const int64_t r = r0 + row;
-    const float top = rows[row].x;
+    cluster.sync();
+    const Pass now = todo;
+    if (now.row < 0) break;
     Piece<T> p;
-    p.open(a, r);
-    u64* rest = w.rest + ((int64_t)(pass & 1) * a.num_seqs + s) * w.pieces;
+    p.open(a, now.row);
+    u64* rest = w.rest + (int64_t)s * w.pieces;
     for (int k = gwarp; k < w.pieces; k += warps) {
       uint4 raw[Piece<T>::NV];
       float q[32];
       p.load(k, lane, raw);
-      load_draft<T, Q>(a, p, r, k, lane, q);
+      load_draft<T, Q>(a, p, now.row, k, lane, q);
       float sum = 0.f;
 #pragma unroll
       for (int v = 0; v < Piece<T>::NV; ++v)
 #pragma unroll
-        for (int e = 0; e < Piece<T>::VEC; ++e)
-          sum += fmaxf(fmaf(pa, weight(Piece<T>::at(raw, v, e), top, sc), -pb * q[v * Piece<T>::VEC + e]), 0.f);
+        for (int e = 0; e < Piece<T>::VEC; e += 2) {
+          const float2 x = weights(Piece<T>::pair(raw, v, e), now.top, sc);
+          sum += fmaxf(fmaf(now.a, x.x, -now.b * q[v * Piece<T>::VEC + e]), 0.f);
+          sum += fmaxf(fmaf(now.a, x.y, -now.b * q[v * Piece<T>::VEC + e + 1]), 0.f);
+        }
       const u64 all = warp_sum_u64(fixed(sum, kRestUnit));
       if (lane == 0) __stcg(rest + k, all);
     }
-    ++pass;
     cluster.sync();
-    if (warp == 0) {
+    if (walks) {
       u64 sum = 0;
       for (int k = lane; k < w.pieces; k += 32) {
         const u64 x = __ldcg(rest + k);
@@ -718,9 +727,9 @@ __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_draft_kernel(Verif
       }
     }
   }
-  if (rank != 0 || warp != 0) return;
+  if (!walks) return;
   int next = -1;
-  if (n > 0 && __float_as_int(info.z) >= 0) {
+  if (__float_as_int(info.z) >= 0) {
     const int64_t r = r0 + c;
     const float u = a.u_sample[r];
     if (greedy) {
@@ -728,7 +737,7 @@ __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_draft_kernel(Verif
     } else {
       int i = -1;
       if (db > 0.f) {
-        const u64* rest = w.pieces <= kHeld ? rest_room : w.rest + ((int64_t)((pass - 1) & 1) * a.num_seqs + s) * w.pieces;
+        const u64* rest = w.pieces <= kHeld ? rest_room : w.rest + (int64_t)s * w.pieces;
         u64 target;
         const int piece = find_piece(w.pieces, lane, u, target, [&](int k) { return rest[k]; });
         Piece<T> p;
@@ -768,7 +777,7 @@ VerifyWork layout(void* workspace, int rows, int vocab, int seqs, size_t* bytes)
   w.stats = reinterpret_cast<float2*>(take((size_t)rows * w.pieces * sizeof(float2)));
   w.rows = reinterpret_cast<RowInfo*>(take((size_t)rows * sizeof(RowInfo)));
   w.pq = reinterpret_cast<float2*>(take((size_t)rows * sizeof(float2)));
-  w.rest = reinterpret_cast<u64*>(take((size_t)2 * seqs * w.pieces * sizeof(u64)));
+  w.rest = reinterpret_cast<u64*>(take((size_t)seqs * w.pieces * sizeof(u64)));
   *bytes = at;
   return w;
 }

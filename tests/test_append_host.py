@@ -110,7 +110,7 @@ def _append(tq, **kw):
 
 BOTH = [(dict(n=-1), 1), (dict(n=1 << 31), 1), (dict(hq=20000, qs=1 << 23, qos=1 << 23), 2), (dict(d=96), 2), (dict(d=512), 2), (dict(t=3), 1), (dict(rot=0), 1), (dict(rot=130), 1),
         (dict(rot=7), 1), (dict(rows=-1), 1), (dict(pos=None), 1), (dict(pos=DUMMY + 2), 1), (dict(table=DUMMY + 1), 1),
-        (dict(qw=DUMMY + 4), 1), (dict(kw=DUMMY + 8), 1), (dict(eps=-1e-6), 1), (dict(eps=float("nan")), 1),
+        (dict(qw=DUMMY + 2), 1), (dict(kw=DUMMY + 1), 1), (dict(eps=-1e-6), 1), (dict(eps=float("nan")), 1),
         (dict(eps=float("inf")), 1), (dict(hq=-1), 1), (dict(qo=None), 1), (dict(q=DUMMY + 1), 1), (dict(qo=DUMMY + 1), 1),
         (dict(qs=4095), 1), (dict(qos=4095), 1), (dict(qo=DUMMY, qos=5000), 1)]
 

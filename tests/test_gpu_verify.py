@@ -354,3 +354,21 @@ def test_refusals_of_the_binding(tq):
         args.update(bad)
         with pytest.raises(ValueError):
             tq.tq_verify_tree(**args)
+
+
+def test_long_sequences(tq):
+    # more nodes than are kept in shared memory, in chains and trees, with and without draft probabilities
+    for kind, draft in (("chain", None), ("tree", None), ("chain", F32), ("tree", BF16)):
+        d = Drafts([300, 700, 3], 400, F32, kind, draft, seed=30, kids=40)
+        if draft is not None and kind == "chain":  # long walks
+            d.draft = torch.softmax(d.logits.double() / torch.tensor(np.repeat(d.temp, [300, 700, 3]))[:, None].cuda(), 1).float()
+            d.ua = d.ua * np.float32(0.999)
+        same(d, d.call(tq, 700, check=True), d.want(700))
+
+
+def test_more_pieces_than_are_held(tq):
+    # a vocabulary of more pieces than shared memory has room for
+    d = Drafts([2, 3], 300001, BF16, "chain", F32, seed=31, spread=3.0)
+    same(d, d.call(tq, 3, check=True), d.want(3))
+    d.draft = None
+    same(d, d.call(tq, 3, check=True), d.want(3))
