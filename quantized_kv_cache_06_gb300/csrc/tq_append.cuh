@@ -122,6 +122,8 @@ __device__ __forceinline__ int row_exponent(const float2 (&x)[8]) {
   if (m > 0.f && m <= 3.402823466e38f) frexpf(m, &ex);
   return ex;
 }
+// Whether ss (>= 0 or NaN) lies outside [the float of bits `least`, 2^100].
+__device__ __forceinline__ bool outside(float ss, uint32_t least) { return __float_as_uint(ss) - least > 0x71800000u - least; }
 // Scales x; returns the sum of squares (unchanged where the row is not odd); `eps`, the norm's, goes
 // with the row and bounds ex from below: in the row's units it stays below 2^100.
 template <int LPR>
@@ -143,7 +145,8 @@ __device__ __forceinline__ float norm_factor(float2 (&x)[8], float eps) {
   constexpr int D = 16 * LPR;
   float ss = row_sum<LPR>(sum_squares(x));
   // squares that underflow count only where eps is as small
-  const bool odd = !(ss <= 0x1p100f) || (ss < 0x1p-100f && eps < 0x1p-80f);
+  const uint32_t least = eps < 0x1p-80f ? 0x0d800000u : 0u;  // the bits of 2^-100
+  const bool odd = outside(ss, least);
   if (__any_sync(kFullMask, odd)) {
     float2 y[8];
 #pragma unroll
@@ -452,7 +455,7 @@ __device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Q
                                            uint8_t* dst) {
   constexpr int D = 16 * LPR, IB = D * B / 8;
   float ss = row_sum<LPR>(sum_squares(x)), back = 1.f;
-  const bool odd = !(ss <= 0x1p100f) || ss < 0x1p-100f;
+  const bool odd = outside(ss, 0x0d800000u);
   if (__any_sync(kFullMask, odd)) {
     float2 y[8];
 #pragma unroll
@@ -671,7 +674,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
     if (warp == 0 && a.k_pages) build_quant(quants, 0, a.k_centroids, 1 << a.k_bits, lane);
     if (warp == 1 && a.v_pages) build_quant(quants, 1, a.v_centroids, 1 << a.v_bits, lane);
   }
-  if (warp >= 2) {  // (six warps: two a side)
+  static_assert(kAppendWarps == 8, "two warps for the quantisers, two a side for the shared parts");
+  if (warp >= 2) {
     const int side = (warp - 2) >> 1;
     build_shared(shared[side], side == 2 ? kPlain : mode, D, side == 0 ? a.q_weight : side == 1 ? a.k_weight : nullptr,
                  PACK && side > 0 ? a.signs : nullptr, a.rot_dim, (warp & 1) * 32 + lane, 64);
