@@ -12,6 +12,24 @@
 // D / 16 lanes share a row.  Lane l holds channels 8 l .. 8 l + 7 and D / 2 + 8 l .. + 7: the
 // pairs of either style lie in one lane, 16-byte loads cover 16-bit types, the transform has four
 // stages inside a lane and log2(D / 16) by shuffles, and eight indices are `bits` whole bytes.
+// Weights, the transform's signs and the rotation are one product and one sum a channel, y = x p +
+// x' s, with p and s worked out once for a token's heads.  A key's norm factor is not applied to its
+// coordinates: u is scale free, the stored norm takes it.
+//
+// A warp takes runs of up to eight groups of 32 / (D / 16) heads and copies the next run's rows by
+// cp.async while it works on one.  Packed sides cost it three to four times what dense ones do, so
+// each warp's runs go through all sides in turn.
+//
+// Bound (GB300, 32768 tokens, 32 / 8 heads, D 128, bf16, norms; copy bandwidth 6684 GB/s):
+//   tq_norm_rope, 688 MB     114 us, 90 % of that bandwidth
+//   tq_append_kv K4 / V4, 724 MB   151 us, 72 %: issue.  An encoded group takes 490 to 560 warp
+//     instructions (transform 116, quantiser 108, norm and store 70, the rest rows, places and loops),
+//     a dense one 175; 60 % of the issue slots are used, by 16 warps an SM (registers: the coefficients
+//     of a token take 32).
+// Measured and not kept: 24 warps of 80 registers (spills: 212 us), 20 of 96 not run for its spills;
+// one coordinate's index by halving the decision points in shared memory (12 instructions instead of
+// 6.5); staging partial rotations in shared memory where they pair up between lanes (80 -> 67 us for
+// 8200 tokens); runs that a warp's position alone gave to sides (165 -> 160 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -789,7 +807,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) append_kernel(
     look_up(ahead);
     aim(ahead);
     using Any = std::integral_constant<int, -1>;
-    using Turns = std::integral_constant<int, MODE == kAny ? -1 : 1>;
+    using Turns = std::integral_constant<int, MODE == kAny ? -1 : MODE != kPlain>;
     if (!PACK || it.side == 0) {
       take(it, pos_all, slot_all, std::true_type{}, Turns{}, kGroup,
            [&](float2 (&x)[8], float factor, unsigned char* to, bool live, bool normed) {
@@ -854,12 +872,13 @@ cudaError_t launch_append_kernel(const AppendPlan& p, cudaStream_t stream) {
   return err;
 }
 
-// Head dims of 64 and more with aligned rows and a rotation take a kernel of their mode; the rest
-// one for any call.
+// Head dims of 64 and more with aligned rows take a kernel of their mode (values alone, 32768 tokens of
+// 8 heads: 41 us, 70 in the one for any call); the rest one for any call.
 template <typename T, int LPR, bool PACK>
 cudaError_t launch_append_mode(const AppendPlan& p, cudaStream_t stream) {
   if constexpr (LPR >= 4) {
-    if (p.vec && p.a.cos_sin) {
+    if (p.vec) {
+      if (!p.a.cos_sin) return launch_append_kernel<T, LPR, kPlain, PACK, true>(p, stream);
       if (p.a.interleaved) return launch_append_kernel<T, LPR, kPairs, PACK, true>(p, stream);
       if (p.a.rot_dim == p.a.head_dim) return launch_append_kernel<T, LPR, kHalves, PACK, true>(p, stream);
       return launch_append_kernel<T, LPR, kStaged, PACK, true>(p, stream);
