@@ -626,7 +626,7 @@ tq_status tq_norm_rope(const void* q, int64_t q_stride, int num_q_heads, const v
  *                  token is written); TQ_ERR_SLOT_OUT_OF_RANGE for a slot >= num_blocks *
  *                  block_size: its K and V are not written, other tokens' are (tq_write_kv
  *                  writes none: it looks at every slot in a launch of its own first).
- * Duplicate slots: which row stays is unspecified.  Asynchronous, graph-capturable; host-detected
+ * Duplicate slots: what stays is unspecified, parts of both rows included.  Asynchronous, graph-capturable; host-detected
  * errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA. */
 tq_status tq_append_kv(const void* q, int64_t q_stride, int num_q_heads, void* q_out, int64_t q_out_stride,
                        const void* k, int64_t k_stride, const void* v, int64_t v_stride, tq_dtype dtype,

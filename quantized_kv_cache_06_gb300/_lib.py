@@ -1016,6 +1016,8 @@ def _rope_args(name: str, index: int, tokens: int, d: int, positions, position_o
         rows, rot = cos_sin.shape
         if not _plain(cos_sin, f32, (rows, rot), index):
             _need_like(name, index, cos_sin=(cos_sin, f32, (rows, rot)))
+        if rows * rot == 0:
+            raise ValueError(f"{name}: cos_sin {[rows, rot]} is empty")
         cp = cos_sin.data_ptr()
     qw = kw = None
     if q_weight is not None:

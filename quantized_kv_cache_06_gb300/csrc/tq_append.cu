@@ -50,7 +50,6 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   p.vec = vec_ok(a.q, a.q_stride, size) && vec_ok(a.k, a.k_stride, size) && vec_ok(a.v, a.v_stride, size) &&
           vec_ok(a.q_out, a.q_out_stride, size) && vec_ok(a.k_out, a.k_out_stride, size);
   p.table_vec = reinterpret_cast<uintptr_t>(a.cos_sin) % 16 == 0 && a.rot_dim % 8 == 0;
-  p.signs_vec = reinterpret_cast<uintptr_t>(a.signs) % 16 == 0;
   // Runs of eight groups share a token's coefficients and hide the copies' latency; shorter ones where
   // they leave warps idle.
   const int64_t warps = (int64_t)sms * kAppendCtas * kAppendWarps;

@@ -78,7 +78,7 @@ struct AppendPlan {
   int grid;
   int full;                   // every side's heads fill its groups
   int vec;                    // inputs and dense outputs: 16-byte accesses
-  int table_vec, signs_vec;   // table rows, signs: 16-byte loads
+  int table_vec;              // table rows: 16-byte loads
 };
 // By type, dense or packed (one translation unit each).
 cudaError_t launch_append_f32(const AppendPlan& p, cudaStream_t stream);

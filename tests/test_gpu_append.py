@@ -360,3 +360,48 @@ def test_infinities_of_channels_that_stay(tq, rot, pairs):
         x.q[2, 1, at] = float("inf")
         want[2, 1, at] = float("inf")
     assert torch.equal(tq.tq_norm_rope(x.q, None, **x.kw_args())[0], want)
+
+
+def test_more_runs_a_token_than_warps(tq):
+    # 16384 heads of 256: 8192 groups a token, more runs in a block than the GPU holds warps
+    for t in (1, 2, 7):
+        x = Inputs(tq, t, 16384, 1, 256, BF16, 256, True, seed=t)
+        q, k = tq.tq_norm_rope(x.q, x.k, **x.kw_args())
+        for lo in range(0, 16384, 4096):
+            near(q[:, lo:lo + 4096], *x.want(x.q[:, lo:lo + 4096], x.qw), BF16)
+        near(k, *x.want(x.k, x.kw), BF16)
+
+
+@pytest.mark.parametrize("t", [1, 3, 4, 5, 150, 1217, 4099])
+@pytest.mark.parametrize("hq,h", [(32, 8), (5, 3)])
+def test_every_token_whatever_the_cut(tq, t, hq, h):
+    # runs of one to eight groups, blocks of one and four tokens, cut off at the last
+    x = Inputs(tq, t, hq, h, 64, BF16, 64, True, seed=t)
+    kp, vp, signs, kc, vc = pages_of(tq, x, -(-t // 16), 16, 4, 3)
+    slots = torch.randperm(kp.shape[0] * 16, device="cuda")[:t]
+    q = tq.tq_append_kv(x.q, x.k, x.v, kp, vp, slots, signs, kc, vc, check=True, **x.kw_args())
+    near(q, *x.want(x.q, x.qw), BF16)
+    packed_near(tq, kp, slots, x.want(x.k, x.kw)[0], signs, kc, 4)
+    packed_near(tq, vp, slots, x.v.double().cpu().numpy(), signs, vc, 3)
+
+
+def test_refusals_of_the_bindings(tq):
+    x = Inputs(tq, 6, 4, 2, 64, F16, 64)
+    kp, vp, signs, kc, vc = pages_of(tq, x, 2, 8, 4, 4)
+    slots = torch.arange(6, device="cuda")
+    rope = x.kw_args()
+    for bad in (dict(q=x.q.transpose(1, 2)), dict(q=x.q.float()), dict(k=x.k[:5]), dict(q=x.q[:, ::2]), dict(q_out=x.q[:, :3]),
+                dict(positions=rope["positions"].long()), dict(positions=rope["positions"][:5]), dict(positions=None),
+                dict(cos_sin=x.table.double()), dict(cos_sin=x.table[:0]), dict(q_weight=x.qw[:63]), dict(k_weight=x.kw.half()),
+                dict(k=x.k.cpu()), dict(status=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            tq.tq_norm_rope(**{**dict(q=x.q, k=x.k), **rope, **bad})
+    args = dict(q=x.q, k=x.k, v=x.v, k_pages=kp, v_pages=vp, slots=slots, signs=signs, k_centroids=kc, v_centroids=vc, **rope)
+    for bad in (dict(slots=slots.int()), dict(slots=slots[:5]), dict(signs=signs[:32]), dict(k_pages=kp[..., :-4]), dict(v_pages=vp[:1]),
+                dict(k_centroids=kc[:5]), dict(v_centroids=vc.double()), dict(v=x.v[:, :1]), dict(k_pages=None), dict(v_centroids=None),
+                dict(k_pages=kp.to(torch.int8)), dict(v=x.v.float())):
+        with pytest.raises(ValueError):
+            tq.tq_append_kv(**{**args, **bad})
+    with pytest.raises(tq.TQError) as e:  # a table wider than the heads
+        tq.tq_norm_rope(x.q, x.k, rope["positions"], tq.tq_build_rope(128, 10, device="cuda"))
+    assert e.value.status == tq.TQ_ERR_INVALID_ARG

@@ -372,3 +372,13 @@ def test_more_pieces_than_are_held(tq):
     same(d, d.call(tq, 3, check=True), d.want(3))
     d.draft = None
     same(d, d.call(tq, 3, check=True), d.want(3))
+
+
+def test_rows_beyond_32_bit_offsets(tq):
+    d = Drafts([2, 1], 1200, BF16, "chain", F32, seed=32)
+    want = d.call(tq, 2, check=True)
+    far = torch.empty(3, (1 << 31) + 64, dtype=BF16, device="cuda")[:, 8:1208]
+    far.copy_(d.logits)
+    d.logits = far
+    got = d.call(tq, 2, check=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
