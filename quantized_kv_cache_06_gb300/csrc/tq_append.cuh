@@ -26,10 +26,11 @@
 //     instructions (transform 116, quantiser 108, norm and store 70, the rest rows, places and loops),
 //     a dense one 175; 60 % of the issue slots are used, by 16 warps an SM (registers: the coefficients
 //     of a token take 32).
-// Measured and not kept: 24 warps of 80 registers (spills: 212 us), 20 of 96 not run for its spills;
-// one coordinate's index by halving the decision points in shared memory (12 instructions instead of
-// 6.5); staging partial rotations in shared memory where they pair up between lanes (80 -> 67 us for
-// 8200 tokens); runs that a warp's position alone gave to sides (165 -> 160 us).
+// Measured and not kept: 24 warps of 80 registers (spills: 212 us) or 20 of 96 (193 us); values in tiles
+// of 16 rows with the transform on mma.sync (fewer instructions, but 64 accumulators beside the runs'
+// state: 203 us, values alone 41 -> 45 us); an index by halving the decision points in shared memory (12
+// instructions instead of 6.5); partial rotations through shared memory where they pair up between lanes
+// (80 -> 67 us for 8200 tokens); runs that a warp's position alone gave to sides (165 -> 160 us).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -405,3 +405,50 @@ def test_refusals_of_the_bindings(tq):
     with pytest.raises(tq.TQError) as e:  # a table wider than the heads
         tq.tq_norm_rope(x.q, x.k, rope["positions"], tq.tq_build_rope(128, 10, device="cuda"))
     assert e.value.status == tq.TQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("h", [4, 8, 12, 16])
+def test_values_of_many_tokens(tq, dtype, bits, h):
+    # enough tokens for whole runs of values; among them skipped slots, padding rows, zero rows, rows beyond
+    # fp32's squares and rows that are not finite
+    t = 9001
+    x = Inputs(tq, t, 2 * h, h, 128, dtype, 128, True, seed=h)
+    v = x.v.clone()
+    v[7::501] = 0
+    if dtype is BF16:
+        v[8::503] *= 2.0 ** 70
+        v[9::505] *= 2.0 ** -80
+    x.qkv[:, 3 * h * 128:].unflatten(1, (h, 128)).copy_(v)
+    kp, vp, signs, kc, vc = pages_of(tq, x, -(-t // 16) + 1, 16, 4, bits)
+    slots = torch.randperm(vp.shape[0] * 16, device="cuda")[:t]
+    slots[3::7] = -1
+    pos = torch.from_numpy(x.pos).cuda()
+    pos[5::97] = -1
+    args = dict(x.kw_args(), positions=pos)
+    before = vp.clone()
+    tq.tq_append_kv(x.q, x.k, x.v, kp, vp, slots, signs, kc, vc, check=True, **args)
+    live = (slots >= 0) & (pos >= 0)
+    packed_near(tq, vp, slots[live], x.v[live].double().cpu().numpy(), signs, vc, bits)
+    packed_near(tq, kp, slots[live], x.want(x.k, x.kw)[0][live.cpu().numpy()], signs, kc, 4)
+    rest = torch.ones(vp.shape[0] * 16, dtype=torch.bool, device="cuda")
+    rest[slots[live]] = False
+    assert torch.equal(vp.view(-1, h * vp.shape[3])[rest], before.view(-1, h * vp.shape[3])[rest])
+    bad = torch.tensor([100, 5000, 9000], device="cuda")
+    unused = torch.ones(vp.shape[0] * 16, dtype=torch.bool, device="cuda")
+    unused[slots[slots >= 0]] = False
+    slots[bad], pos[bad] = torch.nonzero(unused)[:3, 0], 1
+    x.v[100, 1, 9], x.v[5000, h - 1, 100], x.v[9000, 2, 0] = float("nan"), float("inf"), float("-inf")
+    tq.tq_append_kv(x.q, x.k, x.v, kp, vp, slots, signs, kc, vc, **dict(args, positions=pos))
+    zeros = torch.zeros(1, 16, h, vp.shape[3], dtype=torch.uint8, device="cuda")
+    tq.tq_append_kv(None, None, torch.zeros(1, h, 128, dtype=dtype, device="cuda"), None, zeros, slots[:1] * 0, signs, None, vc)
+    rows = vp.view(-1, h, vp.shape[3])
+    for i, head in ((100, 1), (5000, h - 1), (9000, 2)):
+        row = rows[slots[i], head]
+        assert torch.equal(row[:-4], zeros[0, 0, head, :-4]) and not torch.isfinite(row[-4:].clone().view(F32)).any()
+        other = x.v[i:i + 1].clone()
+        other[0, head] = 0
+        got = rows[slots[i]].clone()
+        got[head] = zeros[0, 0, head]
+        packed_near(tq, got[None, None], torch.zeros(1, dtype=torch.int64, device="cuda"), other.double().cpu().numpy(), signs, vc, bits)
