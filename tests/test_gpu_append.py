@@ -407,13 +407,11 @@ def test_refusals_of_the_bindings(tq):
     assert e.value.status == tq.TQ_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("bits", [2, 4])
-@pytest.mark.parametrize("h", [4, 8, 12, 16])
+@pytest.mark.parametrize("dtype,bits,h", [(BF16, 4, 8), (F16, 2, 8), (BF16, 2, 12), (F16, 4, 4)])
 def test_values_of_many_tokens(tq, dtype, bits, h):
     # enough tokens for whole runs of values; among them skipped slots, padding rows, zero rows, rows beyond
     # fp32's squares and rows that are not finite
-    t = 9001
+    t = 5201
     x = Inputs(tq, t, 2 * h, h, 128, dtype, 128, True, seed=h)
     v = x.v.clone()
     v[7::501] = 0
@@ -435,16 +433,16 @@ def test_values_of_many_tokens(tq, dtype, bits, h):
     rest = torch.ones(vp.shape[0] * 16, dtype=torch.bool, device="cuda")
     rest[slots[live]] = False
     assert torch.equal(vp.view(-1, h * vp.shape[3])[rest], before.view(-1, h * vp.shape[3])[rest])
-    bad = torch.tensor([100, 5000, 9000], device="cuda")
+    bad = torch.tensor([100, 5000, 5200], device="cuda")
     unused = torch.ones(vp.shape[0] * 16, dtype=torch.bool, device="cuda")
     unused[slots[slots >= 0]] = False
     slots[bad], pos[bad] = torch.nonzero(unused)[:3, 0], 1
-    x.v[100, 1, 9], x.v[5000, h - 1, 100], x.v[9000, 2, 0] = float("nan"), float("inf"), float("-inf")
+    x.v[100, 1, 9], x.v[5000, h - 1, 100], x.v[5200, 2, 0] = float("nan"), float("inf"), float("-inf")
     tq.tq_append_kv(x.q, x.k, x.v, kp, vp, slots, signs, kc, vc, **dict(args, positions=pos))
     zeros = torch.zeros(1, 16, h, vp.shape[3], dtype=torch.uint8, device="cuda")
     tq.tq_append_kv(None, None, torch.zeros(1, h, 128, dtype=dtype, device="cuda"), None, zeros, slots[:1] * 0, signs, None, vc)
     rows = vp.view(-1, h, vp.shape[3])
-    for i, head in ((100, 1), (5000, h - 1), (9000, 2)):
+    for i, head in ((100, 1), (5000, h - 1), (5200, 2)):
         row = rows[slots[i], head]
         assert torch.equal(row[:-4], zeros[0, 0, head, :-4]) and not torch.isfinite(row[-4:].clone().view(F32)).any()
         other = x.v[i:i + 1].clone()
