@@ -198,33 +198,42 @@ __device__ __forceinline__ void add_if_greater(uint32_t& v, float u, float pt, u
 enum Mode { kPlain, kHalves, kPairs, kStaged, kAny };  // no pair; slot i ^ 4; same float2; by shared memory
 
 // A side's part of p and s that every token shares: p[e] = weight(e) sign(e), s[e] = -+ weight(e')
-// sign(e), 0 behind the rotated channels.  (Encoded sides carry the transform's signs.)
+// sign(e), 0 behind the rotated channels.  (Encoded sides carry the transform's signs.)  In the order
+// that lanes read them, four channels each: lane after lane, for the first and the second half of a
+// lane's eight channels.
 struct Shared {
   float p[256], s[256];
 };
+__device__ __forceinline__ int shared_place(int e, int D) {
+  const int half = e >= D / 2, in = e - half * (D / 2);
+  return ((2 * half + ((in >> 2) & 1)) * (D / 16) + (in >> 3)) * 4 + (in & 3);
+}
 __device__ __forceinline__ void build_shared(Shared& f, int mode, int D, const float* __restrict__ w,
                                              const float* __restrict__ sg, int rot, int first, int step) {
   const int half = rot / 2;
   for (int e = first; e < D; e += step) {
     const float g = sg ? __ldg(sg + e) : 1.f;
-    f.p[e] = (w ? __ldg(w + e) : 1.f) * g;
+    const int at = shared_place(e, D);
+    f.p[at] = (w ? __ldg(w + e) : 1.f) * g;
     float s = 0.f;
     if (mode != kPlain && e < rot) {
       const bool head = mode == kPairs ? (e & 1) == 0 : e < half;
       const int other = mode == kPairs ? e ^ 1 : head ? e + half : e - half;
       s = (w ? __ldg(w + other) : 1.f) * (head ? -g : g);
     }
-    f.s[e] = s;
+    f.s[at] = s;
   }
 }
 
 struct Coef {
   float2 p[8], s[8];
 };
-__device__ __forceinline__ void shared8(const float* p, float2 (&v)[4]) {
+// a lane's eight channels of half c
+template <int LPR>
+__device__ __forceinline__ void shared8(const float* p, int c, int l, float2 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 f = reinterpret_cast<const float4*>(p)[i];
+    const float4 f = reinterpret_cast<const float4*>(p)[(2 * c + i) * LPR + l];
     v[2 * i] = make_float2(f.x, f.y);
     v[2 * i + 1] = make_float2(f.z, f.w);
   }
@@ -234,7 +243,7 @@ __device__ __forceinline__ void plain_coef(float2 (&p)[8], const Shared& f, int 
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     float2 v[4];
-    shared8(f.p + c * 8 * LPR + 8 * l, v);
+    shared8<LPR>(f.p, c, l, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[4 * c + i] = v[i];
   }
@@ -255,8 +264,8 @@ __device__ __forceinline__ void token_coef(Coef& f, const Shared& sh, int mode, 
   for (int c = 0; c < 2; ++c) {
     const int e0 = c * (D / 2) + 8 * l;  // the chunk's first channel
     float2 pv[4], sv[4];
-    shared8(sh.p + e0, pv);
-    shared8(sh.s + e0, sv);
+    shared8<LPR>(sh.p, c, l, pv);
+    shared8<LPR>(sh.s, c, l, sv);
     if (mode == kPairs) {
       const int p0 = e0 / 2;
 #pragma unroll
