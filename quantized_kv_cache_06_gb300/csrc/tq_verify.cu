@@ -85,6 +85,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Largest of a warp's numbers, none of them NaN.
+__device__ __forceinline__ float largest_of_warp(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Scale of a row: c = log2(e) / temperature in two parts, and the difference below which a
 // weight is zero (NaN differences, of NaN logits or where all are -inf, go there too).
 struct Scale {
@@ -250,7 +257,7 @@ verify_stats_kernel(VerifyArgs a, VerifyWork w, int64_t per) {
       s = scale_of(greedy ? 1.f : temp);
     }
     fresh = r != here;
-    const float m = warp_max(P::largest(raw));
+    const float m = largest_of_warp(P::largest(raw));
     float2 st = make_float2(m, 0.f);
     if (greedy) {
       unsigned best = 0x7fffffffu;
@@ -381,7 +388,7 @@ __device__ __forceinline__ const float2* hold_stats(const VerifyWork& w, int64_t
 __device__ __forceinline__ float row_top(const float2* st, int pieces, int lane) {
   float m = -CUDART_INF_F;
   for (int k = lane; k < pieces; k += 32) m = fmaxf(m, st[k].x);
-  return warp_max(m);
+  return largest_of_warp(m);
 }
 __device__ __forceinline__ bool has_distribution(float top) { return fabsf(top) < CUDART_INF_F; }
 
