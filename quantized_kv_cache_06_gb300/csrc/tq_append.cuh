@@ -22,9 +22,9 @@
 //
 // Bound (GB300, 32768 tokens, 32 / 8 heads, D 128, bf16, norms; copy bandwidth 6684 GB/s):
 //   tq_norm_rope, 688 MB     114 us, 90 % of that bandwidth
-//   tq_append_kv K4 / V4, 724 MB   151 us, 72 %: issue.  An encoded group takes 490 to 560 warp
+//   tq_append_kv K4 / V4, 724 MB   146 us, 74 %: issue.  An encoded group takes 490 to 560 warp
 //     instructions (transform 116, quantiser 108, norm and store 70, the rest rows, places and loops),
-//     a dense one 175; 60 % of the issue slots are used, by 16 warps an SM (registers: the coefficients
+//     a dense one 175; 62 % of the issue slots are used, by 16 warps an SM (registers: the coefficients
 //     of a token take 32).
 // Measured and not kept: 24 warps of 80 registers (spills: 212 us) or 20 of 96 (193 us); values in tiles
 // of 16 rows with the transform on mma.sync (fewer instructions, but 64 accumulators beside the runs'

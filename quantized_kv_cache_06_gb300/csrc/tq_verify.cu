@@ -25,9 +25,9 @@
 // token are read again, and with draft probabilities the rows of refused tokens once per refusal.
 //
 // Bound (GB300): of the first launch the logits' bytes (256 trees, 1153 rows of 131072 bf16, 303 MB
-// read once: 56 us, 81 % of the copy bandwidth; 262 warp instructions a piece, 65 % of the issue slots,
+// read once: 55 us, 82 % of the copy bandwidth; 253 warp instructions a piece, 64 % of the issue slots,
 // the exponentials' pipe as busy); of the second latency (10 us behind it; with draft probabilities 20 us,
-// of which the refused rows' 50 MB of logits and probabilities take 8).  Whole calls: 65 us, and 38 us for
+// of which the refused rows' 50 MB of logits and probabilities take 8).  Whole calls: 64 us, and 37 us for
 // 64 chains of 5 rows.  Measured and not kept: pieces dealt out one by one, a row's temperature looked up
 // for each (256 trees 131 us); every CTA of a cluster walking for itself (the same time, and barriers that
 // would hang on buffers that change under the call).
