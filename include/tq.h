@@ -676,8 +676,10 @@ size_t tq_verify_tree_workspace(int num_rows, int vocab_size, int num_seqs);
  *                  (taken as 0), a parent that is no earlier node (the node is never kept), a
  *                  row whose largest logit is not finite (the walk ends there, next_token -1), or a
  *                  row_start that leaves [0, num_rows] or descends (taken as no rows).
- * Sums that tokens are drawn by are 64-bit integers, weights fp32: the result does not depend on
- * timing.  Two launches, asynchronous, graph-capturable (one workspace per call in flight);
+ * Decisions are those of the definition wherever what they compare is further apart than 2^-40 of a
+ * row's whole weight (after refusals: of the weight that is left, times p's share in it); sums are
+ * integers, so the result does not depend on timing.  Two launches, three for many sequences without
+ * draft probabilities, asynchronous, graph-capturable (one workspace per call in flight);
  * host-detected errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA. */
 tq_status tq_verify_tree(const void* logits, tq_dtype logits_dtype, int64_t logits_stride, int num_rows,
                          int vocab_size, const void* draft_probs, tq_dtype draft_dtype, int64_t draft_stride,

@@ -9,28 +9,30 @@
 // from weights w_0, w_1, ... is the first i whose running sum passes u times the whole sum.
 //   * No draft probabilities (drafted tokens are fixed): a token is drawn from p at every row; the
 //     walk goes on to the child that carries it.
-//   * Draft probabilities q (children drawn from q): child x is kept when u q(x) < r(x) with
-//     r = max(a p - b q, 0), at first (a, b) = (1, 0).  A refusal subtracts q once more:
-//     Z = sum max(a p - (b + 1) q, 0), (a, b) <- (a, b + 1) / Z, as max(max(x, 0) - q, 0) =
-//     max(x - q, 0) for q >= 0.  All refused: a token from r.
+//   * Draft probabilities q (children drawn from q): child x is kept when u q(x) < r(x), r = p at first;
+//     refused, r becomes max(r - q, 0) over its sum.  All refused: a token from r.
 //
-// Weights are 2^((x - m) c), c = log2(e) / temperature in two parts, m the row's largest logit.
-// Sums that decide which token is drawn are 64-bit integers (fixed point), so they do not depend
-// on any order, and their error is that of the weights (about 1e-7 each, independent).
+// Two levels of precision.  fp32 weights 2^((x - m) c), c = log2(e) / temperature in two parts, m the
+// piece's largest logit, give every border of a row's running sum to about 10^-6 of the whole, and a
+// derived bound of that.  A vocabulary of 131072 has tokens no wider than that, so a number that lies
+// within the bound of its token's borders (2 to 15 % of the draws at that size), and every refusal, is
+// decided by a pass over the row with weights of two floats, to 2^-40 of the whole.  Sums are integers at
+// both levels: results do not depend on any order.
 //
-// Two launches.  1. Every warp takes consecutive pieces of 1024 logits, the next one's under way, and
+// Launches.  1. Every warp takes consecutive pieces of 1024 logits, the next one's under way, and
 // leaves each piece's largest logit and its sum of weights (or its first largest, where the temperature
-// is 0).  2. One CTA takes a sequence (a cluster with draft probabilities, of which one CTA decides and
-// all share the passes over a row): rows' sums from the pieces, then only the pieces that hold a drawn
-// token are read again, and with draft probabilities the rows of refused tokens once per refusal.
+// is 0).  2. A cluster takes a sequence: one CTA decides and all share the passes over a row.  Many
+// sequences without draft probabilities have a CTA each instead, and 3. clusters for those that need a pass.
 //
 // Bound (GB300): of the first launch the logits' bytes (256 trees, 1153 rows of 131072 bf16, 303 MB
 // read once: 55 us, 82 % of the copy bandwidth; 253 warp instructions a piece, 64 % of the issue slots,
-// the exponentials' pipe as busy); of the second latency (10 us behind it; with draft probabilities 20 us,
-// of which the refused rows' 50 MB of logits and probabilities take 8).  Whole calls: 64 us, and 37 us for
-// 64 chains of 5 rows.  Measured and not kept: pieces dealt out one by one, a row's temperature looked up
-// for each (256 trees 131 us); every CTA of a cluster walking for itself (the same time, and barriers that
-// would hang on buffers that change under the call).
+// the exponentials' pipe as busy); of the others latency, and in a pass the fp32 pipe (40 operations an
+// element: 64 refused rows of 131072 take 15 us for their sums and 26 us for what refusals leave).  Whole
+// calls: 95 us, and 87 us for 64 chains of 5 rows with draft probabilities.  Measured and not kept:
+// pieces dealt out one by one, a row's temperature looked up for each (256 trees 131 us); every CTA of a
+// cluster walking for itself (the same time, and barriers that would hang on buffers that change under the
+// call); passes by 12 or 16 warps a CTA (the same time: they wait for the fp32 pipe); 64-bit conversions
+// of every element in a pass (64 chains 116 us).
 //
 // Rows may start at any multiple of their element's size: pieces are laid out from the aligned
 // address at or before the row's start, so all but a row's first and last 16 bytes are loaded 16
@@ -38,6 +40,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <float.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -63,16 +66,19 @@ constexpr int kDraftCtas = 8;     // CTAs of a sequence's cluster (with draft pr
 using u64 = unsigned long long;
 
 struct RowInfo {
-  float max, inv;  // largest logit; 1 / sum of weights
-  int32_t pick;    // token drawn (no draft probabilities, or temperature 0); -1: no distribution
+  float max, sum;  // largest logit; sum of weights
+  int32_t pick;    // token drawn (no draft probabilities, or temperature 0), or one of the two below
   int32_t pad;
 };
+constexpr int kNoPick = -1;      // no distribution
+constexpr int kUnsure = -2;      // fp32 weights do not tell
 
 struct VerifyWork {
   float2* stats;   // [rows][pieces]: largest logit, sum of weights (its bits: first largest)
   RowInfo* rows;   // [rows]
-  float2* pq;      // [rows]: p and q of the row's token under its parent
-  u64* rest;       // [seqs][pieces]: sums of max(a p - b q, 0)
+  float2* pq;      // [rows]: weight and q of the row's token under its parent
+  u64* rest;       // [clusters][pieces][vectors of a piece]: sums of max(W - G q, 0)
+  int32_t* list;   // [1 + seqs]: how many sequences the second launch left to the third, and which
   int pieces;
 };
 
@@ -172,14 +178,26 @@ struct Piece {
       }
     }
   }
+  // vector v of a piece
+  __device__ __forceinline__ uint4 load_one(int piece, int v, int lane) const {
+    const int i = first(piece, v, lane);
+    if (i >= 0 && i + VEC <= vocab) return *reinterpret_cast<const uint4*>(row + i);
+    uint4 raw;
+    T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) e[k] = i + k >= 0 && i + k < vocab ? row[i + k] : from_f32<T>(-CUDART_INF_F);
+    return raw;
+  }
   // elements e and e + 1 (e even) of vector v
-  static __device__ __forceinline__ float2 pair(const uint4 (&raw)[NV], int v, int e) {
-    const uint32_t w[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+  static __device__ __forceinline__ float2 pair(const uint4 (&raw)[NV], int v, int e) { return pair_of(raw[v], e); }
+  static __device__ __forceinline__ float2 pair_of(const uint4& raw, int e) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
     else return two<T>(w[e / 2]);
   }
-  static __device__ __forceinline__ float at(const uint4 (&raw)[NV], int v, int e) {
-    const float2 p = pair(raw, v, e & ~1);
+  static __device__ __forceinline__ float at(const uint4 (&raw)[NV], int v, int e) { return one(raw[v], e); }
+  static __device__ __forceinline__ float one(const uint4& raw, int e) {
+    const float2 p = pair_of(raw, e & ~1);
     return (e & 1) ? p.y : p.x;
   }
   // the lane's largest element (NaN left out; -inf where there is none)
@@ -227,6 +245,7 @@ verify_stats_kernel(VerifyArgs a, VerifyWork w, int64_t per) {
   using P = Piece<T>;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 0) w.list[0] = 0;
   const int rows = a.num_seqs > 0 ? min(a.num_rows, max(0, a.row_start[a.num_seqs])) : 0;
   const int64_t items = (int64_t)rows * w.pieces;
   int64_t item = ((int64_t)blockIdx.x * kStatWarps + warp) * per;
@@ -307,34 +326,45 @@ __device__ __forceinline__ u64 part_of(float u, u64 total) {
   return min((u64)((double)u * (double)total), total - 1);
 }
 
-// The first element e of a piece whose running sum of value(v, e) passes `target`, by a warp;
-// where rounding leaves none, the last with a value.  -1: the piece has none.
+// The first element of a piece whose running sum of value(x) passes `target`, by a warp, and the running
+// sums before and behind it; where rounding leaves none, the last with a value (-1: there is none), and
+// `target` for both.  (Rolled: a warp comes here once, and waits longer for instructions than for their
+// results.)
 template <typename T, typename F>
-__device__ __forceinline__ int find_in_piece(const Piece<T>& p, int piece, int lane, u64 target, F value) {
+__device__ __forceinline__ int find_in_piece(const Piece<T>& p, int piece, int lane, u64 target, u64& before, u64& behind,
+                                             F value) {
   constexpr int VEC = Piece<T>::VEC, NV = Piece<T>::NV;
+  uint4 raw[NV];
+  p.load(piece, lane, raw);
   u64 run = 0;
   int last = -1;
-#pragma unroll
+#pragma unroll 1
   for (int v = 0; v < NV; ++v) {
-    u64 part = 0;
+    const uint4 now = raw[0];
+#pragma unroll
+    for (int k = 0; k + 1 < NV; ++k) raw[k] = raw[k + 1];
+    u64 values[VEC], part = 0;
     int tail = -1;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const u64 x = value(v, e);
-      part += x;
-      if (x) tail = e;
+      values[e] = value(Piece<T>::one(now, e));
+      part += values[e];
+      if (values[e]) tail = e;
     }
     const u64 incl = warp_scan_u64(part, lane);
     const unsigned hit = __ballot_sync(kFullMask, run + incl > target);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      u64 at = run + incl - part;
+      u64 at = run + incl - part, lo = 0, hi = 0;
       int found = -1;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        at += value(v, e);
-        if (found < 0 && at > target) found = e;
+        const u64 next = at + values[e];
+        if (found < 0 && next > target) found = e, lo = at, hi = next;
+        at = next;
       }
+      before = shfl_u64(lo, src);
+      behind = shfl_u64(hi, src);
       return p.first(piece, v, src) + __shfl_sync(kFullMask, found, src);
     }
     const unsigned some = __ballot_sync(kFullMask, tail >= 0);
@@ -344,18 +374,20 @@ __device__ __forceinline__ int find_in_piece(const Piece<T>& p, int piece, int l
     }
     run += shfl_u64(incl, 31);
   }
+  before = behind = target;
   return last;
 }
 
-// The piece in which the running sum of sums(k), k < pieces, passes u times the whole, by a
-// warp; `target` becomes the rest inside it.
+// The piece in which the running sum of sums(k), k < pieces, passes u times the whole (`goal` of
+// `total`), by a warp; `target` becomes the rest inside it.
 template <typename F>
-__device__ __forceinline__ int find_piece(int pieces, int lane, float u, u64& target, F sums) {
+__device__ __forceinline__ int find_piece(int pieces, int lane, float u, u64& total, u64& goal, u64& target, F sums) {
   const int per = (pieces + 31) / 32;
   u64 part = 0;
   for (int k = lane * per; k < min(pieces, (lane + 1) * per); ++k) part += sums(k);
   const u64 incl = warp_scan_u64(part, lane);
-  const u64 goal = part_of(u, shfl_u64(incl, 31));
+  total = shfl_u64(incl, 31);
+  goal = part_of(u, total);
   const unsigned hit = __ballot_sync(kFullMask, incl > goal);
   const int src = hit ? __ffs(hit) - 1 : 31;
   u64 rest = goal - (incl - part);
@@ -403,35 +435,35 @@ __device__ __forceinline__ int row_best(const float2* st, int pieces, int lane, 
 // Fixed-point unit of a row's weights: at most `vocab` of them, at most 1 each.
 __device__ __forceinline__ float row_unit(int vocab) { return pow2i(62 - (32 - __clz(vocab))); }
 
-// A token from p, by a warp.
+// How far fp32 weights 2^y may be off, relative to themselves:
+//   kPowError |y|  the exponent's roundings: one of x - m, one of the product, 2^-24 |y| each, times ln 2;
+//   kSumError      ex2's error, below 2^-22 (2^-22.7 over every fp32 in [-126, 0]), of a weight within its piece and of the piece's within the row, and
+//                  12 roundings of 2^-24 in sums (three of a lane's accumulators, three joins, five
+//                  exchanges) and the product of the two.
+// The mean of |y| over a row's tokens, weighted, is its entropy less log2 of the weights' sum, which is
+// at least 1: below log2 of the vocabulary.
+constexpr float kPowError = 0.7f * 0x1p-23f, kSumError = 0x1p-21f + 13 * 0x1p-24f;
+
+// A token from p, by a warp: kUnsure where the borders of the token found are nearer to the number than
+// they may be off.  With errors d_i of the weights, a running sum P of the whole S is off u S by
+// (1 - u) times the errors behind it less u times those in front: at most 2 u (1 - u) S where all are
+// bounded alike, max(u, 1 - u) S where their mean is.
 template <typename T>
-__device__ __forceinline__ int draw_token(const VerifyArgs& a, const VerifyWork& w, const float2* st, int64_t r, float top,
+__device__ __noinline__ int draw_token(const VerifyArgs& a, const VerifyWork& w, const float2* st, int64_t r, float top,
                                           const Scale& s, float u, int lane) {
   const float unit = row_unit(a.vocab);
-  u64 target;
-  const int piece = find_piece(w.pieces, lane, u, target,
+  u64 total, goal, target, before, behind;
+  const int piece = find_piece(w.pieces, lane, u, total, goal, target,
                                [&](int k) { return fixed(st[k].y * weight(st[k].x, top, s), unit); });
   Piece<T> p;
   p.open(a, r);
-  uint4 raw[Piece<T>::NV];
-  p.load(piece, lane, raw);
-  int i = find_in_piece<T>(p, piece, lane, target,
-                               [&](int v, int e) { return fixed(weight(Piece<T>::at(raw, v, e), top, s), unit); });
-  if (i < 0) {  // weights too small for the unit one by one, not together: the piece's largest
-    float m = -CUDART_INF_F;
-    unsigned best = 0x7fffffffu;
-#pragma unroll
-    for (int v = 0; v < Piece<T>::NV; ++v)
-#pragma unroll
-      for (int e = 0; e < Piece<T>::VEC; ++e) {
-        const float x = Piece<T>::at(raw, v, e);
-        if (x > m) m = x, best = (unsigned)(p.first(piece, v, lane) + e);
-      }
-    const float all = warp_max(m);
-    if (m != all) best = 0x7fffffffu;
-    i = (int)__reduce_min_sync(kFullMask, best);
-  }
-  return i;
+  const int i = find_in_piece<T>(p, piece, lane, target, before, behind,
+                                 [&](float x) { return fixed(weight(x, top, s), unit); });
+  const float whole = (float)total, share = (float)goal / whole;
+  const float near = whole * (kSumError * 2.f * share * (1.f - share) +
+                              kPowError * (float)(32 - __clz(a.vocab)) * fmaxf(share, 1.f - share)) * 1.001f +
+                     (float)(w.pieces + kPiece);  // roundings to the unit
+  return (float)(target - before) > near && (float)(behind - target) > near ? i : kUnsure;
 }
 
 // Rows [r0, r0 + n) of a sequence; none where row_start is not ascending inside [0, num_rows].
@@ -506,6 +538,7 @@ __global__ void __launch_bounds__(kPickWarps * 32) verify_pick_kernel(VerifyArgs
   const float temp = a.temperature ? a.temperature[s] : 1.f;
   const bool greedy = is_greedy(temp);
   const Scale sc = scale_of(greedy ? 1.f : temp);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   bool none = false;
   for (int i = warp; i < n; i += warps) {
@@ -535,6 +568,15 @@ __global__ void __launch_bounds__(kPickWarps * 32) verify_pick_kernel(VerifyArgs
       c = child;
     }
   }
+  if (next == kUnsure) {  // left to verify_walk_kernel
+    if (n <= kNodes)
+      for (int i = lane; i < n; i += 32) w.rows[r0 + i].pick = pick_room[i];
+    if (lane == 0) {
+      const int at = atomicAdd(w.list, 1);
+      if (at >= 0 && at < a.num_seqs) w.list[1 + at] = s;  // (always, but in a workspace that another call uses)
+    }
+    return;
+  }
   for (int j = len + lane; j < a.max_path; j += 32) path[j] = -1;
   if (lane == 0) {
     a.path_lens[s] = len;
@@ -542,240 +584,566 @@ __global__ void __launch_bounds__(kPickWarps * 32) verify_pick_kernel(VerifyArgs
   }
 }
 
-// ---------------------------------------------------------------- draft probabilities
+// ---------------------------------------------------------------- weights beyond fp32
+//
+// W = 2^54 2^y, y = (x - m) c, as two floats: x - m is exact as a sum of two, its product with the two
+// parts of c too but for parts below 2^-46 |y|, and with y = k / 1024 + g
+//   2^y = 2^(k div 1024) T (1 + z + z^2 / 2 + z^3 / 6), z = g ln 2, |z| < 2^-11.5,
+// T = 2^((k mod 1024) / 1024) from a table of two floats, the head of T z by an exact product.  W is off by
+// less than 2^-45 (1 + |y|) of itself (20 million logits and temperatures against 64-bit significands).  A
+// lane adds a vector's weights with exact sums of the heads and rounds once to a whole number; a vector's
+// sum of those fits 64 bits, a row's takes 128.
+// (37 fp32 operations an element, 8 others and a lookup: this GPU's fp64 would take many times that.)
 
-// A lane's 32 draft probabilities beside a Piece<T>.
-template <typename T, typename Q>
-__device__ __forceinline__ void load_draft(const VerifyArgs& a, const Piece<T>& p, int64_t r, int piece, int lane,
-                                           float (&q)[32]) {
-  constexpr int VEC = Piece<T>::VEC, NV = Piece<T>::NV;
-  const Q* row = static_cast<const Q*>(a.draft) + r * a.draft_stride;
+struct HiLo {
+  float h, l;
+};
+constexpr int kCells = 1024;
+struct Pow2Table {
+  HiLo e[kCells];
+};
+constexpr Pow2Table make_pow2() {
+  Pow2Table t{};
+  for (int j = 0; j < kCells; ++j) {
+    const double z = 0.69314718055994530942 * j / kCells;
+    double sum = 0;
+    for (int n = 20; n >= 1; --n) sum = z / n * (1.0 + sum);  // e^z - 1
+    const float h = (float)(1.0 + sum);
+    t.e[j].h = h;
+    t.e[j].l = (float)(1.0 - (double)h + sum);
+  }
+  return t;
+}
+__device__ const Pow2Table kPow2 = make_pow2();
+
+constexpr int kUnitBits = 54;
+
+struct Exact {
+  float top, hi, lo;  // m; c
+  float least;        // weights of logits below are 0
+};
+__device__ __forceinline__ Exact exact_of(float top, const Scale& s) {
+  return {top, s.hi, s.lo, fmaxf(top - 100.0f / s.hi, -FLT_MAX)};
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 less(float2 a, float2 b) { return __ffma2_rn(b, both(-1.f), a); }
+
+// W of two logits (NaN and -inf: 0), `table` kPow2's entries.
+__device__ __forceinline__ void exact_weights(float2 at, const Exact& s, const HiLo* table, float2& h, float2& l) {
+  const float2 x = make_float2(fmaxf(at.x, s.least), fmaxf(at.y, s.least)), nm = both(-s.top);
+  const float2 t = __fadd2_rn(x, nm), b = less(t, x);
+  const float2 tl = __fadd2_rn(less(x, less(t, b)), less(nm, b));
+  const float2 y = __fmul2_rn(t, both(s.hi));
+  float2 yl = __ffma2_rn(t, both(s.hi), make_float2(-y.x, -y.y));
+  yl = __ffma2_rn(t, both(s.lo), yl);
+  yl = __ffma2_rn(tl, both(s.hi), yl);
+  constexpr float kRound = 12288.0f;  // 1.5 * 2^13: neighbours are 1 / 1024 apart
+  const float2 k = __fadd2_rn(y, both(kRound));
+  const float2 g = less(y, __fadd2_rn(k, both(-kRound)));
+  const uint32_t kx = __float_as_uint(k.x), ky = __float_as_uint(k.y);
+  const HiLo tx = table[kx % kCells], ty = table[ky % kCells];
+  // k div 1024 + kUnitBits as an exponent
+  constexpr uint32_t kBias = ((uint32_t)(127 + kUnitBits) * kCells - 0x46400000u) << 13;
+  const uint32_t ux = (kx * 8192u + kBias) & 0xff800000u, uy = (ky * 8192u + kBias) & 0xff800000u;
+  const float2 unit = make_float2(__uint_as_float(at.x >= s.least ? ux : 0u), __uint_as_float(at.y >= s.least ? uy : 0u));
+  constexpr double kLn2 = 0.69314718055994530942;
+  constexpr float kLnHi = (float)kLn2, kLnLo = (float)(kLn2 - (double)kLnHi);
+  const float2 z = __fmul2_rn(g, both(kLnHi));
+  float2 zl = __ffma2_rn(g, both(kLnHi), make_float2(-z.x, -z.y));
+  zl = __ffma2_rn(g, both(kLnLo), zl);
+  zl = __ffma2_rn(yl, both(kLnHi), zl);
+  const float2 e = __fadd2_rn(z, zl);
+  zl = __ffma2_rn(__fmul2_rn(e, e), __ffma2_rn(e, both(1.0f / 6), both(0.5f)), zl);  // e^(z + zl) - 1 - z
+  const float2 th = make_float2(tx.h, ty.h), tt = make_float2(tx.l, ty.l);
+  const float2 p = __fmul2_rn(th, z);
+  float2 rest = __fadd2_rn(__ffma2_rn(th, z, make_float2(-p.x, -p.y)), tt);
+  rest = __ffma2_rn(tt, z, rest);
+  rest = __ffma2_rn(th, zl, rest);
+  h = __fadd2_rn(th, p);
+  l = __fadd2_rn(less(p, less(h, th)), rest);
+  h = __fmul2_rn(h, unit);
+  l = __fmul2_rn(l, unit);
+}
+// max(W - G q, 0), G in two parts.
+__device__ __forceinline__ void exact_rest(float2& h, float2& l, float2 q, float gh, float gl) {
+  const float2 p = __fmul2_rn(q, both(gh));
+  const float2 pl = __ffma2_rn(q, both(gl), __ffma2_rn(q, both(gh), make_float2(-p.x, -p.y)));
+  const float2 d = less(h, p);
+  const float2 e = less(less(h, d), p);  // exact wherever the rest may be above zero
+  l = __fadd2_rn(e, less(l, pl));
+  h = d;
+  if (!(h.x + l.x > 0.f)) h.x = l.x = 0.f;  // (an infinite q too)
+  if (!(h.y + l.y > 0.f)) h.y = l.y = 0.f;
+}
+// Nearest whole number, by its bits (below 2^63; a conversion to 64 bits takes 64 cycles of a warp).
+__device__ __forceinline__ int64_t nearest(float x) {
+  const int32_t bits = __float_as_int(x), up = ((bits >> 23) & 255) - 150;
+  const uint32_t digits = ((uint32_t)bits & 0x7fffffu) | 0x800000u;
+  const uint64_t v = up >= 0 ? (uint64_t)digits << up : up > -25 ? (uint64_t)((digits + (1u << (-up - 1))) >> -up) : 0;
+  return bits < 0 ? -(int64_t)v : (int64_t)v;
+}
+__device__ __forceinline__ u64 whole(float h, float l) { return (u64)max((int64_t)0, nearest(h) + nearest(l)); }
+// (h, l) += (x, xl), by an exact sum of the heads
+__device__ __forceinline__ void add_exact(float2& h, float2& l, float2 x, float2 xl) {
+  const float2 s = __fadd2_rn(h, x), b = less(s, h);
+  l = __fadd2_rn(__fadd2_rn(l, xl), __fadd2_rn(less(h, less(s, b)), less(x, b)));
+  h = s;
+}
+
+using u128 = unsigned __int128;
+__device__ __forceinline__ u128 make_u128(u64 hi, u64 lo) { return (u128)hi << 64 | lo; }
+__device__ __forceinline__ double to_double(u128 v) { return (double)(u64)(v >> 64) * 0x1p64 + (double)(u64)v; }
+__device__ __forceinline__ u128 warp_scan_u128(u128 v, int lane) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int i = p.first(piece, v, lane);
-    constexpr int bytes = VEC * (int)sizeof(Q);
-    constexpr int step = bytes < 16 ? bytes : 16, per = step / (int)sizeof(Q);
-    if (i >= 0 && i + VEC <= a.vocab && reinterpret_cast<uintptr_t>(row + i) % step == 0) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const u128 u = make_u128(__shfl_up_sync(kFullMask, (u64)(v >> 64), o), __shfl_up_sync(kFullMask, (u64)v, o));
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ u128 shfl_u128(u128 v, int lane) {
+  return make_u128(shfl_u64((u64)(v >> 64), lane), shfl_u64((u64)v, lane));
+}
+// The whole part of u times a sum (numbers outside [0, 1), and NaN, go to the nearest end).
+__device__ __forceinline__ u128 part_of_u128(float u, u128 total) {
+  if (!(u > 0.f) || total == 0) return 0;
+  if (u >= 1.f) return total - 1;
+  const uint32_t bits = __float_as_uint(u), ex = bits >> 23;
+  const uint32_t digits = ex ? (bits & 0x7fffffu) | 0x800000u : bits;  // u = digits 2^-down
+  const uint32_t down = 150u - max(ex, 1u);
+  return down < 128u ? (u128)digits * total >> down : 0;
+}
+
+// Draft probabilities beside a vector of logits, the first at element i of the row.
+template <typename Q, int VEC>
+__device__ __forceinline__ void load_draft(const Q* row, int vocab, int i, float (&q)[VEC]) {
+  constexpr int bytes = VEC * (int)sizeof(Q);
+  constexpr int step = bytes < 16 ? bytes : 16, per = step / (int)sizeof(Q);
+  if (i >= 0 && i + VEC <= vocab && reinterpret_cast<uintptr_t>(row + i) % step == 0) {
 #pragma unroll
-      for (int k = 0; k < bytes / step; ++k) {
-        alignas(16) Q e[per];
-        if constexpr (step == 16) *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(row + i)[k];
-        else *reinterpret_cast<uint2*>(e) = reinterpret_cast<const uint2*>(row + i)[k];
+    for (int k = 0; k < bytes / step; ++k) {
+      alignas(16) Q e[per];
+      if constexpr (step == 16) *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(row + i)[k];
+      else *reinterpret_cast<uint2*>(e) = reinterpret_cast<const uint2*>(row + i)[k];
 #pragma unroll
-        for (int u = 0; u < per; ++u) q[v * VEC + k * per + u] = fmaxf(to_f32<Q>(e[u]), 0.f);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        q[v * VEC + k] = i + k >= 0 && i + k < a.vocab ? fmaxf(to_f32<Q>(row[i + k]), 0.f) : 0.f;
+      for (int u = 0; u < per; ++u) q[k * per + u] = fmaxf(to_f32<Q>(e[u]), 0.f);
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) q[k] = i + k >= 0 && i + k < vocab ? fmaxf(to_f32<Q>(row[i + k]), 0.f) : 0.f;
   }
 }
 
-constexpr float kRestUnit = 0x1p60f;  // sums of max(a p - b q, 0) are at most 1
+// A pass over a row by a cluster: sums of max(W - G q, 0), a vector of a piece each.
+struct Pass {
+  int row;        // -1: no more
+  float top;
+  float gh, gl;   // G; 0: sums of W
+};
 
-// The first CTA of a sequence's cluster works out the rows and walks; the others take their share of
-// the passes over a row, told by the first alone which row and with what coefficients, so that all
-// meet at the same barriers whatever the buffers hold.
-template <typename T, typename Q>
-__global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_draft_kernel(VerifyArgs a, VerifyWork w) {
+// The numbers of one vector, by a warp.  REST: G is not 0.  (No branch among its pairs: they run side by side.)
+template <typename T, typename Q, bool REST>
+struct Vector {
+  static constexpr int VEC = Piece<T>::VEC, NV = Piece<T>::NV;
+  uint4 raw;
+  float q[VEC];
+  __device__ __forceinline__ void load(const VerifyArgs& a, const Piece<T>& p, const Pass& now, int k, int lane) {
+    raw = p.load_one(k / NV, k % NV, lane);
+    if constexpr (REST)
+      load_draft<Q, VEC>(static_cast<const Q*>(a.draft) + now.row * a.draft_stride, a.vocab, p.first(k / NV, k % NV, lane), q);
+  }
+  // elements e and e + 1
+  __device__ __forceinline__ void pair(const Pass& now, const Exact& ex, const HiLo* table, int e, float2& h, float2& l) const {
+    exact_weights(Piece<T>::pair_of(raw, e), ex, table, h, l);
+    if constexpr (REST) exact_rest(h, l, make_float2(q[e], q[e + 1]), now.gh, now.gl);
+  }
+  // the lane's sum
+  __device__ __forceinline__ u64 sum(const Pass& now, const Exact& ex, const HiLo* table) const {
+    float2 h, l;
+    pair(now, ex, table, 0, h, l);
+#pragma unroll
+    for (int e = 2; e < VEC; e += 2) {
+      float2 x, xl;
+      pair(now, ex, table, e, x, xl);
+      add_exact(h, l, x, xl);
+    }
+    const float s = h.x + h.y, b = s - h.x;
+    return whole(s, (l.x + l.y) + ((h.x - (s - b)) + (h.y - b)));
+  }
+};
+
+// A pass by the warps of a cluster: warp i takes vectors i * share .. and leaves their sums in `rest`;
+// its own is returned.  (A function of its own: the walk's state would take the registers of its loop.)
+template <typename T, typename Q, bool REST>
+__device__ __noinline__ u128 pass_over(const VerifyArgs& a, const Pass now, const Exact ex, u64* rest, int vectors, int share,
+                                       int gwarp, const HiLo* table, int lane) {
+  using V = Vector<T, Q, REST>;
+  const int end = min(vectors, (gwarp + 1) * share);
+  Piece<T> p;
+  p.open(a, now.row);
+  V v;
+  u128 all = 0;
+  int k = gwarp * share;
+  if (k < end) v.load(a, p, now, k, lane);
+#pragma unroll 1
+  for (; k < end; ++k) {
+    const V here = v;
+    if (k + 1 < end) v.load(a, p, now, k + 1, lane);
+    const u64 sum = warp_sum_u64(here.sum(now, ex, table));
+    if (lane == 0) __stcg(rest + k, sum);
+    all += sum;
+  }
+  return all;
+}
+
+constexpr int kMaxWarps = kDraftCtas * kDraftWarps;  // of a cluster
+struct WarpSum {
+  u64 hi, lo;
+};
+__device__ __forceinline__ u128 sum_of(const WarpSum& x) { return make_u128(x.hi, x.lo); }
+
+// The first of n numbers whose running sum passes `left`, by a warp (there is one); `left` becomes the rest
+// in it.
+template <typename F>
+__device__ __forceinline__ int find_sum(int n, int lane, u128& left, F number) {
+  const int per = (n + 31) / 32;
+  u128 part = 0;
+  for (int k = lane * per; k < min(n, (lane + 1) * per); ++k) part += number(k);
+  const u128 incl = warp_scan_u128(part, lane);
+  const unsigned hit = __ballot_sync(kFullMask, incl > left);
+  const int src = hit ? __ffs(hit) - 1 : 31;
+  u128 rest = left - (incl - part);
+  int found = 0;
+  if (lane == src) {
+    for (int k = lane * per; k < min(n, (lane + 1) * per); ++k) {
+      const u128 x = number(k);
+      found = k;
+      if (x > rest) break;
+      rest -= x;
+    }
+  }
+  left = shfl_u128(rest, src);
+  return __shfl_sync(kFullMask, found, src);
+}
+
+// The first token whose running sum passes u times the whole `total`, by a warp, from the sums of a pass.
+template <typename T, typename Q, bool REST>
+__device__ __noinline__ int draw_exact(const VerifyArgs& a, const Pass& now, const Scale& s, const WarpSum* warp_sums, int warps,
+                                       const u64* rest, int vectors, int share, u128 total, float u, const HiLo* table,
+                                       int lane) {
+  using V = Vector<T, Q, REST>;
+  if (total == 0) return kNoPick;
+  u128 left = part_of_u128(u, total);
+  const int first = share * find_sum(warps, lane, left, [&](int i) { return sum_of(warp_sums[i]); });
+  const int k = first + find_sum(min(share, vectors - first), lane, left, [&](int i) { return (u128)__ldcg(rest + first + i); });
+  const u64 target = (u64)left;
+  Piece<T> p;
+  p.open(a, now.row);
+  V v;
+  v.load(a, p, now, k, lane);
+  const Exact ex = exact_of(now.top, s);
+  u64 values[V::VEC], sum = 0;
+  int tail = -1;
+#pragma unroll
+  for (int e = 0; e < V::VEC; e += 2) {
+    float2 h, l;
+    v.pair(now, ex, table, e, h, l);
+    values[e] = (u64)max(0ll, __float2ll_rn(h.x) + __float2ll_rn(l.x));
+    values[e + 1] = (u64)max(0ll, __float2ll_rn(h.y) + __float2ll_rn(l.y));
+    sum += values[e] + values[e + 1];
+    if (values[e]) tail = e;
+    if (values[e + 1]) tail = e + 1;
+  }
+  const u64 upto = warp_scan_u64(sum, lane);
+  const unsigned hit = __ballot_sync(kFullMask, upto > target), some = __ballot_sync(kFullMask, tail >= 0);
+  if ((hit | some) == 0) return kNoPick;  // (logits that changed under the call)
+  // where the sum's rounding leaves no token: the last with a weight
+  const int who = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+  u64 at = upto - sum;
+  int which = -1;
+#pragma unroll
+  for (int e = 0; e < V::VEC; ++e) {
+    at += values[e];
+    if (which < 0 && at > target) which = e;
+  }
+  if (which < 0) which = tail;
+  return p.first(k / V::NV, k % V::NV, who) + __shfl_sync(kFullMask, which, who);
+}
+
+// ---------------------------------------------------------------- the walk by clusters
+
+constexpr int kMaxClusters = 1024;     // of a launch (each has its sums in the workspace)
+// fp32 tells that a drafted token is kept where u q S is below W by more than this share: S is off by
+// less than 2^-17 (see kSumError, kPowError: 30 2^-23), W by 2^-22 + 0.7 2^-23 |y|, |y| < 150.
+constexpr float kKeptNear = 0x1p-15f;
+
+// A cluster takes sequences in turn: all of them, or (`listed`) those that verify_pick_kernel left.
+//
+// With draft probabilities, in whole numbers: W the weights of node c, N their sum and G = 0 at first.
+// Child x is kept when u q(x) N < W_x - G q(x); refused, G becomes G + N and N the sum of max(W - G q,
+// 0) (both stay where that is 0): r = max(W - G q, 0) / N, as max(max(x, 0) - q, 0) = max(x - q, 0) for
+// q >= 0.  fp32 sums of the first launch decide where they can: on children kept, and on the token that
+// follows a node of which no child was refused.
+//
+// The first CTA of a cluster works out the rows and walks; the others take their share of the passes over
+// a row, told by the first alone which sequence, which row and with what G, so that all meet at the same
+// barriers whatever the buffers hold.
+template <typename T, typename Q, bool DRAFT>
+__global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_walk_kernel(const __grid_constant__ VerifyArgs a, const __grid_constant__ VerifyWork w, int listed) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int s = blockIdx.x / ranks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (a CTA's shared memory may be written by another once it runs)
   auto started = cluster.barrier_arrive();
   constexpr int threads = kDraftWarps * 32;
-  const int warps = ranks * kDraftWarps, gwarp = rank * kDraftWarps + warp;
-  struct Pass {
-    int row;             // -1: no more
-    float a, b, top;     // max(a weight - b q, 0)
-  };
+  const int warps = ranks * kDraftWarps, gwarp = rank * kDraftWarps + warp, vectors = w.pieces * Piece<T>::NV;
+  const int share = (vectors + warps - 1) / warps;  // vectors of a warp
+  __shared__ __align__(16) HiLo table[kCells];
   __shared__ float2 held[kDraftWarps][kHeld];
-  __shared__ int32_t node_room[2][kNodes];
+  __shared__ int32_t node_room[2][kNodes], pick_room[kNodes];
   __shared__ float4 row_room[kNodes];
   __shared__ float2 pq_room[kNodes];
-  __shared__ u64 rest_room[kHeld];
   __shared__ Pass todo;
-  const float temp = a.temperature ? a.temperature[s] : 1.f;
-  const bool greedy = is_greedy(temp);
-  const Scale sc = scale_of(greedy ? 1.f : temp);
-  int r0 = 0, n = 0;
-  Nodes nodes;
-  float4* rows = row_room;
-  float2* pqs = pq_room;
-  if (rank == 0) {
-    n = rows_of(a, s, r0);
-    check_sequence(a, s, r0, n, threadIdx.x, threads);
-    nodes.open(a, r0, n, node_room, threads);
-    if (n > kNodes) {
-      rows = reinterpret_cast<float4*>(w.rows + r0);
-      pqs = w.pq + r0;
-    }
-  }
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  if (rank == 0) {
-    // rows' largest logits, sums (their inverses) and, greedy, first largest logits
-    bool none = false;
-    for (int i = warp; i < n; i += kDraftWarps) {
-      const float2* st = hold_stats(w, r0 + i, held[warp], lane);
-      const float top = row_top(st, w.pieces, lane);
-      float inv = 0.f;
-      int pick = -1;
-      if (!has_distribution(top)) {
-        none = true;
-      } else if (greedy) {
-        pick = row_best(st, w.pieces, lane, top);
-      } else {
-        const float unit = row_unit(a.vocab);
-        u64 sum = 0;
-        for (int k = lane; k < w.pieces; k += 32) sum += fixed(st[k].y * weight(st[k].x, top, sc), unit);
-        inv = unit / (float)warp_sum_u64(sum);
-        pick = 0;
+  __shared__ int turn;
+  __shared__ WarpSum warp_sums[kMaxWarps];
+  for (int i = threadIdx.x; i < kCells / 2; i += threads)
+    reinterpret_cast<float4*>(table)[i] = __ldg(reinterpret_cast<const float4*>(&kPow2) + i);
+  const bool walks = rank == 0 && warp == 0;
+  u64* rest = w.rest + (int64_t)(blockIdx.x / ranks) * vectors;
+  const float near = kKeptNear + (float)w.pieces / row_unit(a.vocab);  // (roundings to the unit)
+  cluster.barrier_wait(std::move(started));
+  if (listed) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+
+  for (int at = blockIdx.x / ranks; at < a.num_seqs; at += gridDim.x / ranks) {
+    int s = at;
+    if (listed) {
+      if (walks) {
+        s = at < __ldcg(w.list) ? __ldcg(w.list + 1 + at) : -1;
+        if (s >= a.num_seqs) s = -1;
+        if (lane < ranks) *cluster.map_shared_rank(&turn, lane) = s;
       }
-      if (lane == 0) rows[i] = make_float4(top, inv, __int_as_float(pick), 0.f);
+      cluster.sync();
+      s = turn;
+      if (s < 0) break;
+    }
+    const float temp = a.temperature ? a.temperature[s] : 1.f;
+    const bool greedy = is_greedy(temp);
+    const Scale sc = scale_of(greedy ? 1.f : temp);
+    int r0 = 0, n = 0;
+    Nodes nodes;
+    float4* rows = row_room;
+    float2* pqs = pq_room;
+    if (rank == 0 || (!DRAFT && !listed)) n = rows_of(a, s, r0);
+    if (rank == 0) {
+      if (!listed) check_sequence(a, s, r0, n, threadIdx.x, threads);
+      nodes.open(a, r0, n, node_room, threads);
+      if (n > kNodes) {
+        rows = reinterpret_cast<float4*>(w.rows + r0);
+        pqs = w.pq + r0;
+      }
+    }
+    if (!listed) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    bool none = false;
+    if constexpr (!DRAFT) {
+      if (listed) {
+        if (rank == 0 && n <= kNodes)
+          for (int i = threadIdx.x; i < n; i += threads) pick_room[i] = __ldcg(&w.rows[r0 + i].pick);
+      } else {
+        for (int i = gwarp; i < n; i += warps) {
+          const int64_t r = r0 + i;
+          const float2* st = hold_stats(w, r, held[warp], lane);
+          const float top = row_top(st, w.pieces, lane);
+          int pick = kNoPick;
+          if (!has_distribution(top)) none = true;
+          else if (greedy) pick = row_best(st, w.pieces, lane, top);
+          else pick = draw_token<T>(a, w, st, r, top, sc, a.u_sample[r], lane);
+          if (lane == 0) {
+            if (n <= kNodes) *cluster.map_shared_rank(&pick_room[i], 0) = pick;
+            else __stcg(&w.rows[r].pick, pick);
+          }
+        }
+      }
+      cluster.sync();
+    } else if (rank == 0) {
+      // rows' largest logits, sums and, greedy, first largest logits
+      for (int i = warp; i < n; i += kDraftWarps) {
+        const float2* st = hold_stats(w, r0 + i, held[warp], lane);
+        const float top = row_top(st, w.pieces, lane);
+        float all = 0.f;
+        int pick = kNoPick;
+        if (!has_distribution(top)) {
+          none = true;
+        } else if (greedy) {
+          pick = row_best(st, w.pieces, lane, top);
+        } else {
+          const float unit = row_unit(a.vocab);
+          u64 sum = 0;
+          for (int k = lane; k < w.pieces; k += 32) sum += fixed(st[k].y * weight(st[k].x, top, sc), unit);
+          all = (float)warp_sum_u64(sum) / unit;
+          pick = 0;
+        }
+        if (lane == 0) rows[i] = make_float4(top, all, __int_as_float(pick), 0.f);
+      }
+      __syncthreads();
+      // weight and q of every drafted token
+      for (int i = 1 + (int)threadIdx.x; i < n; i += threads) {
+        const int up = nodes.parent(i), tok = nodes.tokens[i];
+        float2 pq = make_float2(-1.f, 0.f);  // never kept
+        if (up >= 0 && up < i && tok >= 0 && tok < a.vocab) {
+          const int64_t r = r0 + up;
+          const float4 info = rows[up];
+          const int pick = __float_as_int(info.z);
+          if (greedy) {
+            pq.x = pick == tok ? 1.f : -1.f;
+          } else if (pick >= 0) {
+            const float x = to_f32<T>(static_cast<const T*>(a.logits)[r * a.logits_stride + tok]);
+            pq.y = fmaxf(to_f32<Q>(static_cast<const Q*>(a.draft)[r * a.draft_stride + tok]), 0.f);
+            pq.x = weight(x, info.x, sc);
+          }
+        }
+        pqs[i] = pq;
+      }
+      __syncthreads();
     }
     if (none && a.status && lane == 0) atomicMax(a.status, (int32_t)kInvalidArg);
-    __syncthreads();
-    // p and q of every drafted token
-    for (int i = 1 + (int)threadIdx.x; i < n; i += threads) {
-      const int up = nodes.parent(i), tok = nodes.tokens[i];
-      float2 pq = make_float2(-1.f, 0.f);  // never kept
-      if (up >= 0 && up < i && tok >= 0 && tok < a.vocab) {
-        const int64_t r = r0 + up;
-        const float4 info = rows[up];
-        const int pick = __float_as_int(info.z);
-        if (greedy) {
-          pq.x = pick == tok ? 1.f : -1.f;
-        } else if (pick >= 0) {
-          const float x = to_f32<T>(static_cast<const T*>(a.logits)[r * a.logits_stride + tok]);
-          pq.y = fmaxf(to_f32<Q>(static_cast<const Q*>(a.draft)[r * a.draft_stride + tok]), 0.f);
-          pq.x = weight(x, info.x, sc) * info.y;
-        }
-      }
-      pqs[i] = pq;
+
+    // The walk, by the first CTA's first warp.
+    int32_t* path = a.path + (int64_t)s * a.max_path;
+    int c = 0, from = 1, len = 0, next = kNoPick;
+    bool exact = false, holds = false;  // N is; the sums of the last pass are those of G at node c
+    double G = 0.0, N = 0.0;
+    u128 total = 0;  // of the last pass
+    float4 info = make_float4(0.f, 0.f, __int_as_float(kNoPick), 0.f);
+    if (walks && n > 0) {
+      if (lane == 0) path[0] = 0;
+      len = 1;
+      if constexpr (DRAFT) info = rows[0];
     }
-    __syncthreads();
-  }
-  // the walk, by the first CTA's first warp
-  const bool walks = rank == 0 && warp == 0;
-  cluster.barrier_wait(std::move(started));
-  int c = 0, from = 1;
-  float ca = 1.f, cb = 0.f;      // r = max(ca p - cb q, 0) at node c
-  float da = 1.f, db = 0.f;      // the coefficients whose sums the last pass took (db 0: none at c)
-  bool again = false;
-  int32_t* path = a.path + (int64_t)s * a.max_path;
-  const float4 no_row = make_float4(0.f, 0.f, __int_as_float(-1), 0.f);
-  float4 info = walks && n > 0 ? rows[0] : no_row;
-  if (walks && lane == 0 && n > 0) path[0] = 0;
-  int len = n > 0 ? 1 : 0;
-  while (true) {
-    if (walks) {
-      int need = -1;
-      while (!again && __float_as_int(info.z) >= 0 && len < a.max_path) {
-        const int child = nodes.next_child(c, from, lane, [](int) { return true; });
-        if (child < 0) break;
-        const float2 pq = pqs[child];
-        const float r = fmaf(ca, pq.x, -cb * pq.y);
-        if (greedy ? pq.x > 0.f : (r > 0.f && a.u_accept[r0 + child] * pq.y < r)) {
+    auto pass_of = [&](double g) {
+      const float gh = (float)g;
+      return Pass{r0 + c, info.x, gh, (float)(g - (double)gh)};
+    };
+    auto drawn = [&] {
+      const Pass now = pass_of(G);
+      const float u = a.u_sample[r0 + c];
+      if constexpr (DRAFT) {
+        if (G > 0.0) return draw_exact<T, Q, true>(a, now, sc, warp_sums, warps, rest, vectors, share, total, u, table, lane);
+      }
+      return draw_exact<T, Q, false>(a, now, sc, warp_sums, warps, rest, vectors, share, total, u, table, lane);
+    };
+    // Goes on as far as it can: the G of the pass that it needs, -1 at the end.
+    auto walk = [&]() -> double {
+      if (n == 0) return -1.0;
+      if constexpr (!DRAFT) {
+        while (true) {
+          next = n <= kNodes ? pick_room[c] : __ldcg(&w.rows[r0 + c].pick);
+          if (next == kUnsure) {
+            if (!holds) {
+              info.x = row_top(hold_stats(w, r0 + c, held[0], lane), w.pieces, lane);
+              return 0.0;
+            }
+            next = drawn();
+          }
+          if (next < 0 || len == a.max_path) return -1.0;
+          const int child = nodes.next_child(c, c + 1, lane, [&](int i) { return nodes.tokens[i] == next; });
+          if (child < 0) return -1.0;
           c = child;
-          from = c + 1;
-          ca = da = 1.f;
-          cb = db = 0.f;
-          info = rows[c];
+          holds = false;
           if (lane == 0) path[len] = c;
           ++len;
+        }
+      } else {
+        while (__float_as_int(info.z) >= 0 && len < a.max_path) {
+          const int child = nodes.next_child(c, from, lane, [](int) { return true; });
+          if (child < 0) break;
+          const float2 pq = pqs[child];
+          bool kept;
+          if (greedy) {
+            kept = pq.x > 0.f;
+          } else {
+            const int tok = nodes.tokens[child];
+            if (tok < 0 || tok >= a.vocab) {  // not drawn from q
+              from = child + 1;
+              continue;
+            }
+            const float u = a.u_accept[r0 + child];
+            if (!exact) {
+              kept = pq.x * (1.f - near) - u * pq.y * info.y > 0x1p-110f;
+              if (!kept) return 0.0;
+            } else {
+              const float x = to_f32<T>(static_cast<const T*>(a.logits)[(int64_t)(r0 + c) * a.logits_stride + tok]);
+              float2 h, l;
+              exact_weights(both(x), exact_of(info.x, sc), table, h, l);
+              const double r = (double)h.x + (double)l.x - (G > 0.0 ? G * pq.y : 0.0);
+              kept = r > 0.0 && (double)u * pq.y * N < r;
+            }
+          }
+          if (kept) {
+            c = child;
+            from = c + 1;
+            exact = holds = false;
+            G = N = 0.0;
+            info = rows[c];
+            if (lane == 0) path[len] = c;
+            ++len;
+          } else {
+            from = child + 1;
+            if (!greedy) return G + N;
+          }
+        }
+        if (__float_as_int(info.z) < 0 || greedy) {
+          next = __float_as_int(info.z);
+        } else if (!exact) {
+          const int64_t r = r0 + c;
+          next = draw_token<T>(a, w, hold_stats(w, r, held[0], lane), r, info.x, sc, a.u_sample[r], lane);
+          if (next == kUnsure) return 0.0;
         } else {
-          from = child + 1;
-          const int tok = nodes.tokens[child];
-          if (greedy || tok < 0 || tok >= a.vocab) continue;  // not drawn from q
-          da = ca, db = cb + 1.f;
-          need = c;
-          break;
+          if (!holds) return G;
+          next = drawn();
+        }
+        return -1.0;
+      }
+    };
+    while (true) {
+      double g = -1.0;
+      if (walks) {
+        g = walk();
+        Pass ask = pass_of(g);
+        if (g < 0.0) ask.row = -1;
+        if (lane < ranks) *cluster.map_shared_rank(&todo, lane) = ask;
+      }
+      cluster.sync();
+      const Pass now = todo;
+      if (now.row < 0) break;
+      u128 mine;
+      if (DRAFT && now.gh > 0.f) mine = pass_over<T, Q, DRAFT>(a, now, exact_of(now.top, sc), rest, vectors, share, gwarp, table, lane);
+      else mine = pass_over<T, Q, false>(a, now, exact_of(now.top, sc), rest, vectors, share, gwarp, table, lane);
+      if (lane == 0) *cluster.map_shared_rank(&warp_sums[gwarp], 0) = WarpSum{(u64)(mine >> 64), (u64)mine};
+      cluster.sync();
+      if (walks) {
+        u128 part = 0;
+        for (int i = lane; i < warps; i += 32) part += sum_of(warp_sums[i]);
+        total = shfl_u128(warp_scan_u128(part, lane), 31);
+        const double sum = to_double(total);
+        holds = true;
+        if (!exact) {
+          exact = true;
+          N = sum;
+        } else if (g > G) {
+          if (sum > 0.0) G = g, N = sum;
+          else holds = false;  // nothing is left: the distribution before the subtraction stays
         }
       }
-      if (again) need = c;
-      const Pass next{need < 0 ? -1 : r0 + need, da * info.y, db, info.x};
-      if (lane < ranks) *cluster.map_shared_rank(&todo, lane) = next;
     }
-    cluster.sync();
-    const Pass now = todo;
-    if (now.row < 0) break;
-    Piece<T> p;
-    p.open(a, now.row);
-    u64* rest = w.rest + (int64_t)s * w.pieces;
-    for (int k = gwarp; k < w.pieces; k += warps) {
-      uint4 raw[Piece<T>::NV];
-      float q[32];
-      p.load(k, lane, raw);
-      load_draft<T, Q>(a, p, now.row, k, lane, q);
-      float sum = 0.f;
-#pragma unroll
-      for (int v = 0; v < Piece<T>::NV; ++v)
-#pragma unroll
-        for (int e = 0; e < Piece<T>::VEC; e += 2) {
-          const float2 x = weights(Piece<T>::pair(raw, v, e), now.top, sc);
-          sum += fmaxf(fmaf(now.a, x.x, -now.b * q[v * Piece<T>::VEC + e]), 0.f);
-          sum += fmaxf(fmaf(now.a, x.y, -now.b * q[v * Piece<T>::VEC + e + 1]), 0.f);
-        }
-      const u64 all = warp_sum_u64(fixed(sum, kRestUnit));
-      if (lane == 0) __stcg(rest + k, all);
-    }
-    cluster.sync();
     if (walks) {
-      u64 sum = 0;
-      for (int k = lane; k < w.pieces; k += 32) {
-        const u64 x = __ldcg(rest + k);
-        if (w.pieces <= kHeld) rest_room[k] = x;
-        sum += x;
-      }
-      __syncwarp();
-      sum = warp_sum_u64(sum);
-      if (again) {
-        again = false;
-      } else if (sum > 0) {
-        const float z = (float)sum / kRestUnit;
-        ca = da / z;
-        cb = db / z;
-      } else {  // nothing is left: the distribution before the subtraction stays
-        da = ca, db = cb;
-        again = db > 0.f;
+      for (int j = len + lane; j < a.max_path; j += 32) path[j] = -1;
+      if (lane == 0) {
+        a.path_lens[s] = len;
+        a.next_token[s] = next;
       }
     }
-  }
-  if (!walks) return;
-  int next = -1;
-  if (__float_as_int(info.z) >= 0) {
-    const int64_t r = r0 + c;
-    const float u = a.u_sample[r];
-    if (greedy) {
-      next = __float_as_int(info.z);
-    } else {
-      int i = -1;
-      if (db > 0.f) {
-        const u64* rest = w.pieces <= kHeld ? rest_room : w.rest + (int64_t)s * w.pieces;
-        u64 target;
-        const int piece = find_piece(w.pieces, lane, u, target, [&](int k) { return rest[k]; });
-        Piece<T> p;
-        p.open(a, r);
-        uint4 raw[Piece<T>::NV];
-        float q[32];
-        p.load(piece, lane, raw);
-        load_draft<T, Q>(a, p, r, piece, lane, q);
-        const float pa = da * info.y;
-        i = find_in_piece<T>(p, piece, lane, target, [&](int v, int e) {
-          return fixed(fmaxf(fmaf(pa, weight(Piece<T>::at(raw, v, e), info.x, sc), -db * q[v * Piece<T>::VEC + e]), 0.f),
-                       kRestUnit);
-        });
-      }
-      // from p where nothing was refused (or no weight is above the unit)
-      if (i < 0) i = draw_token<T>(a, w, hold_stats(w, r, held[0], lane), r, info.x, sc, u, lane);
-      next = i;
-    }
-  }
-  for (int j = len + lane; j < a.max_path; j += 32) path[j] = -1;
-  if (lane == 0) {
-    a.path_lens[s] = len;
-    a.next_token[s] = next;
+    if (at + (int)(gridDim.x / ranks) < a.num_seqs) cluster.sync();
   }
 }
 
@@ -792,15 +1160,15 @@ VerifyWork layout(void* workspace, int rows, int vocab, int seqs, size_t* bytes)
   w.stats = reinterpret_cast<float2*>(take((size_t)rows * w.pieces * sizeof(float2)));
   w.rows = reinterpret_cast<RowInfo*>(take((size_t)rows * sizeof(RowInfo)));
   w.pq = reinterpret_cast<float2*>(take((size_t)rows * sizeof(float2)));
-  w.rest = reinterpret_cast<u64*>(take((size_t)seqs * w.pieces * sizeof(u64)));
+  w.rest = reinterpret_cast<u64*>(take((size_t)std::min(seqs, kMaxClusters) * w.pieces * 8 * sizeof(u64)));
+  w.list = reinterpret_cast<int32_t*>(take(((size_t)seqs + 1) * sizeof(int32_t)));
   *bytes = at;
   return w;
 }
 
-// The second kernel is a programmatic dependent of the first: its set-up overlaps it.
-template <typename K>
-cudaError_t launch_after(K kern, int grid, int threads, int cluster, int smem, cudaStream_t stream, const VerifyArgs& a,
-                         const VerifyWork& w) {
+// A kernel is a programmatic dependent of the one before: its set-up overlaps it.
+template <typename K, typename... Args>
+cudaError_t launch_after(K kern, int grid, int threads, int cluster, int smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -815,7 +1183,7 @@ cudaError_t launch_after(K kern, int grid, int threads, int cluster, int smem, c
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, w);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, args...);
   if (err == cudaSuccess) count_launches(1);
   return err;
 }
@@ -833,21 +1201,27 @@ cudaError_t launch_verify_typed(const VerifyArgs& a, VerifyWork w, cudaStream_t 
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   count_launches(1);
-  if (!a.draft) {
-    // twice the warps of an average sequence's rows: ragged ones take one turn too
-    const int warps = std::max(1, std::min(kPickWarps, 2 * ((a.num_rows + a.num_seqs - 1) / a.num_seqs)));
-    return launch_after(verify_pick_kernel<T>, a.num_seqs, warps * 32, 1, warps * kHeld * (int)sizeof(float2), stream, a, w);
-  }
-  // as many CTAs a sequence as run at once, and as its rows' pieces keep busy
+  // as many CTAs a sequence as run at once, and as its rows' vectors keep busy
+  const int vectors = w.pieces * Piece<T>::NV, threads = kDraftWarps * 32;
   int ctas_seq = kDraftCtas;
-  while (ctas_seq > 1 && ((int64_t)a.num_seqs * ctas_seq > 2 * sms || ctas_seq * kDraftWarps >= 2 * w.pieces)) ctas_seq /= 2;
-  const int64_t dgrid = (int64_t)a.num_seqs * ctas_seq;
-  if (dgrid > 0x7fffffff) return cudaErrorInvalidValue;
-  const int threads = kDraftWarps * 32;
+  while (ctas_seq > 1 && ctas_seq * kDraftWarps >= 2 * vectors) ctas_seq /= 2;
+  int clusters = std::min(a.num_seqs, kMaxClusters);
+  if (!a.draft && (int64_t)a.num_seqs * ctas_seq > 2 * sms) {
+    // many sequences: a CTA each, with twice the warps of an average one's rows (ragged ones take one turn
+    // too), and clusters for those that it leaves
+    const int warps = std::max(1, std::min(kPickWarps, 2 * ((a.num_rows + a.num_seqs - 1) / a.num_seqs)));
+    err = launch_after(verify_pick_kernel<T>, a.num_seqs, warps * 32, 1, warps * kHeld * (int)sizeof(float2), stream, a, w);
+    if (err != cudaSuccess) return err;
+    clusters = std::min(clusters, std::max(1, 2 * sms / ctas_seq));
+    return launch_after(verify_walk_kernel<T, float, false>, clusters * ctas_seq, threads, ctas_seq, 0, stream, a, w, 1);
+  }
+  while (ctas_seq > 1 && (int64_t)a.num_seqs * ctas_seq > 2 * sms) ctas_seq /= 2;
+  const int grid = clusters * ctas_seq;
+  if (!a.draft) return launch_after(verify_walk_kernel<T, float, false>, grid, threads, ctas_seq, 0, stream, a, w, 0);
   switch (a.draft_dtype) {
-    case kF32: return launch_after(verify_draft_kernel<T, float>, (int)dgrid, threads, ctas_seq, 0, stream, a, w);
-    case kF16: return launch_after(verify_draft_kernel<T, __half>, (int)dgrid, threads, ctas_seq, 0, stream, a, w);
-    case kBF16: return launch_after(verify_draft_kernel<T, __nv_bfloat16>, (int)dgrid, threads, ctas_seq, 0, stream, a, w);
+    case kF32: return launch_after(verify_walk_kernel<T, float, true>, grid, threads, ctas_seq, 0, stream, a, w, 0);
+    case kF16: return launch_after(verify_walk_kernel<T, __half, true>, grid, threads, ctas_seq, 0, stream, a, w, 0);
+    case kBF16: return launch_after(verify_walk_kernel<T, __nv_bfloat16, true>, grid, threads, ctas_seq, 0, stream, a, w, 0);
     default: return cudaErrorInvalidValue;
   }
 }
