@@ -675,7 +675,9 @@ size_t tq_verify_tree_workspace(int num_rows, int vocab_size, int num_seqs);
  *   status_dev     device int32 or NULL: 0, or TQ_ERR_INVALID_ARG for a temperature out of range
  *                  (taken as 0), a parent that is no earlier node (the node is never kept), a
  *                  row whose largest logit is not finite (the walk ends there, next_token -1), or a
- *                  row_start that leaves [0, num_rows] or descends (taken as no rows).
+ *                  row_start that leaves [0, num_rows], descends or passes its last entry (taken as no
+ *                  rows; a row that others claim as well is one sequence's, and has no distribution
+ *                  for another).
  * Decisions are those of the definition wherever what they compare is further apart than 2^-40 of a
  * row's whole weight (after refusals: of the weight that is left, times p's share in it); sums are
  * integers, so the result does not depend on timing.  Two launches, three for many sequences without

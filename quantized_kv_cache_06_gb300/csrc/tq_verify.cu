@@ -68,7 +68,7 @@ using u64 = unsigned long long;
 struct RowInfo {
   float max, sum;  // largest logit; sum of weights
   int32_t pick;    // token drawn (no draft probabilities, or temperature 0), or one of the two below
-  int32_t pad;
+  int32_t seq;     // whose temperature the row's pieces are of
 };
 constexpr int kNoPick = -1;      // no distribution
 constexpr int kUnsure = -2;      // fp32 weights do not tell
@@ -264,6 +264,7 @@ verify_stats_kernel(VerifyArgs a, VerifyWork w, int64_t per) {
 #pragma unroll
     for (int v = 0; v < P::NV; ++v) raw[v] = next[v];
     const int here = r, first = p.first(piece, 0, lane);
+    const bool begins = piece == 0;
     if (++piece == w.pieces) {
       piece = 0;
       ++r;
@@ -271,7 +272,9 @@ verify_stats_kernel(VerifyArgs a, VerifyWork w, int64_t per) {
     }
     if (item + 1 < end) p.load(piece, lane, next);
     if (fresh) {
-      const float temp = a.temperature ? __ldg(a.temperature + seq_of(a.row_start, a.num_seqs, here)) : 1.f;
+      const int seq = seq_of(a.row_start, a.num_seqs, here);
+      if (begins && lane == 0) w.rows[here].seq = seq;
+      const float temp = a.temperature ? __ldg(a.temperature + seq) : 1.f;
       greedy = is_greedy(temp);
       s = scale_of(greedy ? 1.f : temp);
     }
@@ -422,7 +425,10 @@ __device__ __forceinline__ float row_top(const float2* st, int pieces, int lane)
   for (int k = lane; k < pieces; k += 32) m = fmaxf(m, st[k].x);
   return largest_of_warp(m);
 }
-__device__ __forceinline__ bool has_distribution(float top) { return fabsf(top) < CUDART_INF_F; }
+// (a row that two sequences of a descending row_start claim is one's alone)
+__device__ __forceinline__ bool has_distribution(const VerifyWork& w, int64_t r, int s, float top) {
+  return fabsf(top) < CUDART_INF_F && __ldcg(&w.rows[r].seq) == s;
+}
 
 // First largest logit of a row with largest logit `top`.
 __device__ __forceinline__ int row_best(const float2* st, int pieces, int lane, float top) {
@@ -466,11 +472,12 @@ __device__ __noinline__ int draw_token(const VerifyArgs& a, const VerifyWork& w,
   return (float)(target - before) > near && (float)(behind - target) > near ? i : kUnsure;
 }
 
-// Rows [r0, r0 + n) of a sequence; none where row_start is not ascending inside [0, num_rows].
+// Rows [r0, r0 + n) of a sequence; none where row_start is not ascending inside [0, num_rows], or
+// passes its last entry: the first launch takes no rows behind that.
 __device__ __forceinline__ int rows_of(const VerifyArgs& a, int s, int& r0) {
   r0 = a.row_start[s];
   const int r1 = a.row_start[s + 1];
-  const bool ok = r0 >= 0 && r1 >= r0 && r1 <= a.num_rows;
+  const bool ok = r0 >= 0 && r1 >= r0 && r1 <= min(a.num_rows, a.row_start[a.num_seqs]);
   if (!ok && a.status && threadIdx.x == 0) atomicMax(a.status, (int32_t)kInvalidArg);
   return ok ? r1 - r0 : 0;
 }
@@ -546,7 +553,7 @@ __global__ void __launch_bounds__(kPickWarps * 32) verify_pick_kernel(VerifyArgs
     const float2* st = hold_stats(w, r, held + warp * kHeld, lane);
     const float top = row_top(st, w.pieces, lane);
     int pick = -1;
-    if (!has_distribution(top)) none = true;
+    if (!has_distribution(w, r, s, top)) none = true;
     else if (greedy) pick = row_best(st, w.pieces, lane, top);
     else pick = draw_token<T>(a, w, st, r, top, sc, a.u_sample[r], lane);
     if (lane == 0) (n <= kNodes ? pick_room[i] : w.rows[r].pick) = pick;
@@ -955,7 +962,7 @@ __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_walk_kernel(const 
           const float2* st = hold_stats(w, r, held[warp], lane);
           const float top = row_top(st, w.pieces, lane);
           int pick = kNoPick;
-          if (!has_distribution(top)) none = true;
+          if (!has_distribution(w, r, s, top)) none = true;
           else if (greedy) pick = row_best(st, w.pieces, lane, top);
           else pick = draw_token<T>(a, w, st, r, top, sc, a.u_sample[r], lane);
           if (lane == 0) {
@@ -972,7 +979,7 @@ __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_walk_kernel(const 
         const float top = row_top(st, w.pieces, lane);
         float all = 0.f;
         int pick = kNoPick;
-        if (!has_distribution(top)) {
+        if (!has_distribution(w, r0 + i, s, top)) {
           none = true;
         } else if (greedy) {
           pick = row_best(st, w.pieces, lane, top);
