@@ -493,7 +493,7 @@ __device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Q
     const bool bad = !(ss <= 3.402823466e38f);  // a NaN or infinite coordinate: a zero row's indices
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = bad ? make_float2(0.f, 0.f) : y[i];
-    // the norm is ss rsqrt(ss) factor 2^ex below; zero rows and rows that are not finite keep theirs
+    // the norm is sqrt(ss) factor 2^ex below; zero rows and rows that are not finite keep theirs
     back = pow2i(ex / 2);
     factor *= pow2i(ex - ex / 2);
     if (bad) back = factor = 1.f;
@@ -501,8 +501,11 @@ __device__ __forceinline__ void encode_row(float2 (&x)[8], float factor, const Q
   }
   float rs;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(ss));  // ss in the normal range, or not finite
-  float nu = ss * rs * factor * back;
-  if (!(ss <= 3.402823466e38f)) nu = ss, rs = 0.f;
+  // (the norm that is stored is correctly rounded, as the writer's; the coordinates' own factor needs
+  // fewer bits: its error, below 2^-22, is as that of the transform's sums)
+  const bool finite = ss <= 3.402823466e38f;
+  const float nu = finite ? sqrtf(ss) * factor * back : ss;
+  if (!finite) rs = 0.f;
   fwht_row<LPR>(x, l);
   constexpr float kInvSqrtD = LPR == 1 ? 0.25f : LPR == 2 ? 0.17677669529663689f : LPR == 4 ? 0.125f
                               : LPR == 8 ? 0.088388347648318447f : 0.0625f;
