@@ -976,9 +976,18 @@ def tq_build_rope(rot_dim: int, num_positions: int, base: float = 10000.0, inv_f
         inv_freq = torch.as_tensor(inv_freq).to(torch.float64).contiguous().cpu()
         if inv_freq.numel() * 2 != int(rot_dim):
             raise ValueError(f"tq_build_rope: inv_freq must hold rot_dim / 2 = {int(rot_dim) // 2} values")
-    out = torch.empty(max(0, int(num_positions)), max(0, int(rot_dim)), dtype=torch.float32)
-    _check(lib().tq_build_rope(int(rot_dim), int(num_positions), float(base), _ptr(inv_freq), out.data_ptr()))
+    rot_dim = _i32("tq_build_rope", "rot_dim", rot_dim)
+    out = torch.empty(max(0, int(num_positions)), max(0, rot_dim), dtype=torch.float32)
+    _check(lib().tq_build_rope(rot_dim, int(num_positions), float(base), _ptr(inv_freq), out.data_ptr()))
     return out if device is None else out.to(device)
+
+
+def _i32(name: str, what: str, value: int) -> int:
+    """A number that the library takes in 32 bits (ctypes would cut it off)."""
+    value = int(value)
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name}: {what} {value} does not fit 32 bits")
+    return value
 
 
 # Codebook sizes and their bits.
@@ -1028,7 +1037,7 @@ def _rope_args(name: str, index: int, tokens: int, d: int, positions, position_o
         if not _plain(k_weight, f32, (d,), index):
             _need_like(name, index, k_weight=(k_weight, f32, (d,)))
         kw = k_weight.data_ptr()
-    return pp, int(position_offset), cp, rows, rot, 1 if interleaved else 0, qw, kw, float(eps)
+    return pp, _i32(name, "position_offset", position_offset), cp, rows, rot, 1 if interleaved else 0, qw, kw, float(eps)
 
 
 def tq_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
@@ -1176,7 +1185,9 @@ class Verified(NamedTuple):
 
 @functools.lru_cache(maxsize=4096)
 def tq_verify_tree_workspace(num_rows: int, vocab_size: int, num_seqs: int) -> int:
-    """Workspace bytes of tq_verify_tree."""
+    """Workspace bytes of tq_verify_tree; 0 when the arguments are invalid."""
+    if max(num_rows, vocab_size, num_seqs) >= 1 << 31:
+        return 0
     return int(lib().tq_verify_tree_workspace(num_rows, vocab_size, num_seqs))
 
 
@@ -1205,12 +1216,14 @@ def tq_verify_tree(logits: torch.Tensor, row_start: torch.Tensor, tokens: torch.
     if logits.dim() != 2 or row_start.dim() != 1 or row_start.numel() < 1:
         raise ValueError(f"{name}: logits [R, V] and row_start [S + 1] expected")
     r, vocab = logits.shape
-    s, max_path = row_start.numel() - 1, int(max_path)
+    s, max_path = row_start.numel() - 1, _i32(name, "max_path", max_path)
     dev, i32, f32, index = logits.device, torch.int32, torch.float32, logits.get_device()
     if index < 0:
         raise ValueError(f"{name}: all tensors must be on the same CUDA device (got {dev})")
     if max_path < 1:
         raise ValueError(f"{name}: max_path {max_path} < 1")
+    if max(r, vocab, s) >= 1 << 31:
+        raise ValueError(f"{name}: logits {[r, vocab]} of {s} sequences: counts of 2^31 and more are not taken")
     if (draft_probs is None) != (u_accept is None):
         raise ValueError(f"{name}: draft_probs and u_accept come together")
     lp, ls = _vocab_rows(name, "logits", logits, index, (r, vocab))
