@@ -614,7 +614,9 @@ tq_status tq_norm_rope(const void* q, int64_t q_stride, int num_q_heads, const v
 
 /* Appends a step's keys and values to the packed pages, and rotates its queries: tq_norm_rope on
  * q and k, with the fp32 rows of k (not rounded in between) and the rows of v encoded at their
- * slots as tq_write_kv encodes them.  One launch.
+ * slots as tq_write_kv encodes them.  (An index may be the neighbour of tq_write_kv's where the
+ * coordinate lies within 2^-18 of a decision point, and a norm differ in its last bits: the two sum in
+ * different orders.)  One launch.
  *
  *   q, q_out       as tq_norm_rope; q may be NULL
  *   k, v           as tq_norm_rope's inputs, num_kv_heads heads; either may be NULL
@@ -656,7 +658,7 @@ size_t tq_verify_tree_workspace(int num_rows, int vocab_size, int num_seqs);
  *                     At temperature 0 a child is kept when it carries the first largest logit.
  *
  *   logits         device, logits_dtype rows of vocab_size (at most 2^30), row i at element i *
- *                  logits_stride. *                  -inf and NaN have no probability.
+ *                  logits_stride.  -inf and NaN have no probability.
  *   draft_probs    device, draft_dtype rows as logits, or NULL; negative numbers and NaN count as 0
  *   row_start      device int32[num_seqs + 1], ascending (tq_plan_step's); rows behind the last
  *                  are not read.  A sequence may have none.

@@ -126,7 +126,8 @@ __device__ __forceinline__ void load8(const float* __restrict__ p, bool vec, flo
   }
 }
 
-// ---- rows whose sum of squares leaves [2^-100, 2^100] (out of line: they are rare) -------------
+// ---- rows whose sum of squares leaves [2^-100, 2^100] (out of line: they are rare, but in the kernel
+// for any call, where the lanes behind a side's last head hold zero rows) ------------------------
 //
 // Such a row is scaled by 2^-ex, ex the exponent of its largest magnitude (0 where that is 0 or not
 // finite), which is exact.  `odd`: this lane's row is one.

@@ -15,7 +15,7 @@
 // Two levels of precision.  fp32 weights 2^((x - m) c), c = log2(e) / temperature in two parts, m the
 // piece's largest logit, give every border of a row's running sum to about 10^-6 of the whole, and a
 // derived bound of that.  A vocabulary of 131072 has tokens no wider than that, so a number that lies
-// within the bound of its token's borders (2 to 15 % of the draws at that size), and every refusal, is
+// within the bound of its token's borders (about a tenth of the draws at that size), and every refusal, is
 // decided by a pass over the row with weights of two floats, to 2^-40 of the whole.  Sums are integers at
 // both levels: results do not depend on any order.
 //
@@ -28,7 +28,7 @@
 // read once: 55 us, 82 % of the copy bandwidth; 253 warp instructions a piece, 64 % of the issue slots,
 // the exponentials' pipe as busy); of the others latency, and in a pass the fp32 pipe (40 operations an
 // element: 64 refused rows of 131072 take 15 us for their sums and 26 us for what refusals leave).  Whole
-// calls: 95 us, and 87 us for 64 chains of 5 rows with draft probabilities.  Measured and not kept:
+// calls: 89 us, and 88 us for 64 chains of 5 rows with draft probabilities.  Measured and not kept:
 // pieces dealt out one by one, a row's temperature looked up for each (256 trees 131 us); every CTA of a
 // cluster walking for itself (the same time, and barriers that would hang on buffers that change under the
 // call); passes by 12 or 16 warps a CTA (the same time: they wait for the fp32 pipe); 64-bit conversions
@@ -60,15 +60,15 @@ namespace {
 constexpr int kPiece = 1024;      // logits of a piece
 constexpr int kStatWarps = 8;
 constexpr int kPickWarps = 16;    // most warps of a sequence's CTA
-constexpr int kDraftWarps = 8;
-constexpr int kDraftCtas = 8;     // CTAs of a sequence's cluster (with draft probabilities)
+constexpr int kWalkWarps = 8;    // of a CTA of a cluster
+constexpr int kWalkCtas = 8;     // most CTAs of a cluster
 
 using u64 = unsigned long long;
 
 struct RowInfo {
   float max, sum;  // largest logit; sum of weights
   int32_t pick;    // token drawn (no draft probabilities, or temperature 0), or one of the two below
-  int32_t seq;     // whose temperature the row's pieces are of
+  int32_t seq;     // whose temperature the row's pieces are of (0 once a walk holds the row)
 };
 constexpr int kNoPick = -1;      // no distribution
 constexpr int kUnsure = -2;      // fp32 weights do not tell
@@ -443,9 +443,9 @@ __device__ __forceinline__ float row_unit(int vocab) { return pow2i(62 - (32 - _
 
 // How far fp32 weights 2^y may be off, relative to themselves:
 //   kPowError |y|  the exponent's roundings: one of x - m, one of the product, 2^-24 |y| each, times ln 2;
-//   kSumError      ex2's error, below 2^-22 (2^-22.7 over every fp32 in [-126, 0]), of a weight within its piece and of the piece's within the row, and
-//                  12 roundings of 2^-24 in sums (three of a lane's accumulators, three joins, five
-//                  exchanges) and the product of the two.
+//   kSumError      ex2's error, below 2^-22 (2^-22.7 over every fp32 in [-126, 0]), of a weight within its
+//                  piece and of the piece's within the row, and 12 roundings of 2^-24 in sums (three of a
+//                  lane's accumulators, three joins, five exchanges) and the product of the two.
 // The mean of |y| over a row's tokens, weighted, is its entropy less log2 of the weights' sum, which is
 // at least 1: below log2 of the vocabulary.
 constexpr float kPowError = 0.7f * 0x1p-23f, kSumError = 0x1p-21f + 13 * 0x1p-24f;
@@ -804,7 +804,7 @@ __device__ __noinline__ u128 pass_over(const VerifyArgs& a, const Pass now, cons
   return all;
 }
 
-constexpr int kMaxWarps = kDraftCtas * kDraftWarps;  // of a cluster
+constexpr int kMaxWarps = kWalkCtas * kWalkWarps;  // of a cluster
 struct WarpSum {
   u64 hi, lo;
 };
@@ -897,17 +897,17 @@ constexpr float kKeptNear = 0x1p-15f;
 // a row, told by the first alone which sequence, which row and with what G, so that all meet at the same
 // barriers whatever the buffers hold.
 template <typename T, typename Q, bool DRAFT>
-__global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_walk_kernel(const __grid_constant__ VerifyArgs a, const __grid_constant__ VerifyWork w, int listed) {
+__global__ void __launch_bounds__(kWalkWarps * 32, 2) verify_walk_kernel(const __grid_constant__ VerifyArgs a, const __grid_constant__ VerifyWork w, int listed) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (a CTA's shared memory may be written by another once it runs)
   auto started = cluster.barrier_arrive();
-  constexpr int threads = kDraftWarps * 32;
-  const int warps = ranks * kDraftWarps, gwarp = rank * kDraftWarps + warp, vectors = w.pieces * Piece<T>::NV;
+  constexpr int threads = kWalkWarps * 32;
+  const int warps = ranks * kWalkWarps, gwarp = rank * kWalkWarps + warp, vectors = w.pieces * Piece<T>::NV;
   const int share = (vectors + warps - 1) / warps;  // vectors of a warp
   __shared__ __align__(16) HiLo table[kCells];
-  __shared__ float2 held[kDraftWarps][kHeld];
+  __shared__ float2 held[kWalkWarps][kHeld];
   __shared__ int32_t node_room[2][kNodes], pick_room[kNodes];
   __shared__ float4 row_room[kNodes];
   __shared__ float2 pq_room[kNodes];
@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(kDraftWarps * 32, 2) verify_walk_kernel(const 
       cluster.sync();
     } else if (rank == 0) {
       // rows' largest logits, sums and, greedy, first largest logits
-      for (int i = warp; i < n; i += kDraftWarps) {
+      for (int i = warp; i < n; i += kWalkWarps) {
         const float2* st = hold_stats(w, r0 + i, held[warp], lane);
         const float top = row_top(st, w.pieces, lane);
         float all = 0.f;
@@ -1209,9 +1209,9 @@ cudaError_t launch_verify_typed(const VerifyArgs& a, VerifyWork w, cudaStream_t 
   if (err != cudaSuccess) return err;
   count_launches(1);
   // as many CTAs a sequence as run at once, and as its rows' vectors keep busy
-  const int vectors = w.pieces * Piece<T>::NV, threads = kDraftWarps * 32;
-  int ctas_seq = kDraftCtas;
-  while (ctas_seq > 1 && ctas_seq * kDraftWarps >= 2 * vectors) ctas_seq /= 2;
+  const int vectors = w.pieces * Piece<T>::NV, threads = kWalkWarps * 32;
+  int ctas_seq = kWalkCtas;
+  while (ctas_seq > 1 && ctas_seq * kWalkWarps >= 2 * vectors) ctas_seq /= 2;
   int clusters = std::min(a.num_seqs, kMaxClusters);
   if (!a.draft && (int64_t)a.num_seqs * ctas_seq > 2 * sms) {
     // many sequences: a CTA each, with twice the warps of an average one's rows (ragged ones take one turn
