@@ -606,7 +606,7 @@ struct HiLo {
   float h, l;
 };
 constexpr int kCells = 1024;
-struct Pow2Table {
+struct alignas(16) Pow2Table {
   HiLo e[kCells];
 };
 constexpr Pow2Table make_pow2() {
