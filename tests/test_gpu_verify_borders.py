@@ -226,6 +226,24 @@ def test_children_kept_or_refused_next_to_the_border(tq, dtype, vocab, seqs):
             assert torch.equal(seen.path[far, 1], node[far].to(I32))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_vocabularies_of_millions(tq, dtype):
+    # 20000 pieces a row, 80000 or 160000 vectors; drawn and refused
+    seqs, vocab = 4, 20_000_003
+    logits, temp, gen = language(seqs, vocab, dtype, 11)
+    cum = weights(logits, temp).cumsum_(1)
+    start, tokens = start_of(seqs, 1), torch.zeros(seqs, dtype=I32, device=DEV)
+    for turn in range(6):
+        u = torch.rand(seqs, generator=gen, device=DEV)
+        equal(tq.tq_verify_tree(logits, start, tokens, u, 1, temperature=temp, check=True).next_token, *drawn(cum, u))
+    logits, temp, q, tokens, parents, ua, cum, z, gen = refused(2, 1, vocab, dtype, BF16, seed=12)
+    for turn in range(6):
+        us = torch.rand(4, generator=gen, device=DEV)
+        seen = tq.tq_verify_tree(logits, start_of(2, 2), tokens, us, 2, parents=parents, temperature=temp, draft_probs=q, u_accept=ua)
+        i, d = drawn(cum, us[::2])
+        equal(seen.next_token, i, d * z)
+
+
 def test_a_captured_call_follows_its_inputs(tq):
     # sequences that need more than fp32 in one replay and not in the next
     seqs, vocab = 100, 33001
